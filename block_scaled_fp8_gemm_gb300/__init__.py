@@ -58,12 +58,16 @@ GEMMAR_SERIAL_REDUCE = 1 << 7
 GEMMAR_FUSE_QUANTIZE = 1 << 8
 GEMMAR_MAX_P = 8
 GEMMAR_NOALLOC_MAX_PARTIALS = 8 * 1024 * 1024
+GEMMAR_NORM_MAX_N = 16384
+GEMMAR_LORA_MAX_ADAPTERS = 1024
+GEMMAR_LORA_MAX_RANK = 128
 
 # ---- signatures ----------------------------------------------------------------
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _U32 = ctypes.c_uint32
+_F = ctypes.c_float
 _PP = ctypes.POINTER(ctypes.c_void_p)
 
 _SIGS = {
@@ -86,6 +90,14 @@ _SIGS = {
     "fused_gemm_reduce": (_I, [_P, _I, _PP, _PP, _PP, _PP, _I, _I64, _I64, _I64, _I, _U32, _P, _P]),
     "fused_gemm_reduce_noalloc": (_I, [_I, _PP, _PP, _PP, _PP, _I64, _I64, _I64, _I, _P, _P]),
     "fused_gemm_reduce_noalloc_status": (_I, [ctypes.POINTER(_I)]),
+    "norm_gate_residual": (_I, [_P, _P, _I, _I64, _P, _I, _I64, _P, _P, _P, _I64, _F, _F, _F, _I64, _I64,
+                                _P, _P, _P, _P, _P, _P]),
+    "norm_gate_residual_bwd": (_I, [_P, _P, _I, _I64, _P, _I, _I64, _P, _P, _P, _P, _I64, _F, _F, _I64, _I64,
+                                    _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P]),
+    "lora_plan": (_I, [_P, _P, _I64, _I, _P, _P, _P]),
+    "lora_apply": (_I, [_P, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _P, _I64, _P, _I64, _P, _P]),
+    "lora_apply_bwd": (_I, [_P, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I,
+                            _P, _I64, _P, _I64, _P, _P, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -347,3 +359,140 @@ def fused_gemm_reduce_noalloc_status():
     d = ctypes.c_int(0)
     code = int(_lib.fused_gemm_reduce_noalloc_status(ctypes.byref(d)))
     return code, int(d.value)
+
+
+# ---- the residual stream after wo_b, and adapters beside it --------------------------
+
+def _shaped(t: torch.Tensor, shape, name: str) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows(t: torch.Tensor, shape, name: str, dtype=None):
+    """(pointer, row stride) of a [rows, cols] matrix with contiguous rows, which may be a view."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    _shaped(t, shape, name)
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _dense(t, shape, name: str, dtype):
+    """Pointer of a contiguous tensor of that shape and type; None stays None."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    p = _ptr(t, name)
+    _shaped(t, shape, name)
+    return p
+
+
+def _gate(gate, M: int, N: int):
+    """(pointer, row stride) of a gate: [N] (stride 0) or [M, N]."""
+    if gate is None:
+        return None, 0
+    if isinstance(gate, torch.Tensor) and gate.dim() == 1:
+        return _dense(gate, (N,), "gate", torch.bfloat16), 0
+    ptr, stride = _rows(gate, (M, N), "gate", torch.bfloat16)
+    if stride == 0:
+        raise ValueError("gate: pass one row for all rows as a tensor of shape [N]")
+    return ptr, stride
+
+
+def norm_gate_residual(ctx: Context, y, h, w_pre, t, w_post=None, gate=None, alpha: float = 1.0, beta: float = 1.0,
+                       eps: float = 1e-6, u=None, q=None, scales=None, rstd=None, stream=None) -> None:
+    """t = alpha*h + beta*gate*norm(y)*w_post and the next block's input norm(t)*w_pre, as bf16 rows u
+    and/or e4m3 codes q with fp32 scales per 1x128 (gemm_blockscale_fp8's A operand).  w_post None: no
+    post norm; w_pre None: t only; gate bf16 [N] or [M, N]; rstd fp32 [M, 2] for the backward pass."""
+    M, N = y.shape
+    yp, ys = _rows(y, (M, N), "y")
+    hp, hs = _rows(h, (M, N), "h")
+    gp, gs = _gate(gate, M, N)
+    f32, bf16 = torch.float32, torch.bfloat16
+    if q is not None:
+        _shaped(q, (M, N), "q")
+    _check(_lib.norm_gate_residual(ctx.handle, yp, _xdtype(y), ys, hp, _xdtype(h), hs,
+                                   _dense(w_post, (N,), "w_post", f32), _dense(w_pre, (N,), "w_pre", f32), gp, gs,
+                                   alpha, beta, eps, M, N, _dense(t, (M, N), "t", h.dtype),
+                                   _dense(u, (M, N), "u", bf16), None if q is None else _u8(q, "q"),
+                                   _dense(scales, (M, N // 128), "scales", f32), _dense(rstd, (M, 2), "rstd", f32),
+                                   _stream(stream)),
+           "norm_gate_residual")
+
+
+def norm_gate_residual_bwd(ctx: Context, y, h, rstd, dt, dy, dh, w_post=None, w_pre=None, gate=None,
+                           alpha: float = 1.0, beta: float = 1.0, du=None, dw_post=None, dw_pre=None, dgate=None,
+                           stream=None) -> None:
+    """Gradients of norm_gate_residual from dt (of t; None: zero) and du (of the normed rows), given its
+    inputs and rstd.  dw_post, dw_pre fp32 [N]; dgate fp32 [N] for a gate row, bf16 [M, N] per token."""
+    M, N = y.shape
+    yp, ys = _rows(y, (M, N), "y")
+    hp, hs = _rows(h, (M, N), "h")
+    gp, gs = _gate(gate, M, N)
+    tp, ts = (None, 0) if dt is None else _rows(dt, (M, N), "dt", h.dtype)
+    up, us = (None, 0) if du is None else _rows(du, (M, N), "du", torch.bfloat16)
+    f32 = torch.float32
+    dg = _dense(dgate, (N,), "dgate", f32) if gs == 0 else _dense(dgate, (M, N), "dgate", torch.bfloat16)
+    _check(_lib.norm_gate_residual_bwd(ctx.handle, yp, _xdtype(y), ys, hp, _xdtype(h), hs,
+                                       _dense(rstd, (M, 2), "rstd", f32), _dense(w_post, (N,), "w_post", f32),
+                                       _dense(w_pre, (N,), "w_pre", f32), gp, gs, alpha, beta, M, N, tp, ts, up, us,
+                                       _dense(dy, (M, N), "dy", y.dtype), _dense(dh, (M, N), "dh", h.dtype),
+                                       _dense(dw_post, (N,), "dw_post", f32), _dense(dw_pre, (N,), "dw_pre", f32), dg,
+                                       _stream(stream)),
+           "norm_gate_residual_bwd")
+
+
+def lora_plan(ctx: Context, adapter_ids, order, offsets, stream=None) -> None:
+    """Sort a batch's tokens by adapter: order int32 [T] and offsets int32 [R+1] from adapter_ids int32 [T]
+    (an id outside [0, R) is a token without one).  One plan serves every layer of the batch."""
+    T, R = adapter_ids.numel(), offsets.numel() - 1
+    i32 = torch.int32
+    _check(_lib.lora_plan(ctx.handle, _dense(adapter_ids, (T,), "adapter_ids", i32), T, R,
+                          _dense(order, (T,), "order", i32), _dense(offsets, (R + 1,), "offsets", i32),
+                          _stream(stream)),
+           "lora_plan")
+
+
+def _lora_operands(x, order, offsets, A, B, scales, ranks):
+    T, K = x.shape
+    R, r, _ = A.shape
+    N = B.shape[2]
+    i32, bf16 = torch.int32, torch.bfloat16
+    return (T, K, N, R, r), (_dense(order, (T,), "order", i32), _dense(offsets, (R + 1,), "offsets", i32),
+                             _dense(A, (R, r, K), "A", bf16), _dense(B, (R, r, N), "B", bf16),
+                             _dense(scales, (R,), "scales", torch.float32), _dense(ranks, (R,), "ranks", i32))
+
+
+def lora_apply(ctx: Context, x, order, offsets, A, B, scales, ranks, out, y=None, v=None, stream=None) -> None:
+    """out = y + the tokens' adapters applied to x: scales[a] * (x[t] A[a]^T) B[a], A [R, r, K] and B [R, r, N]
+    bf16, ranks int32 [R] or None.  y None: zero; y may be out.  v fp32 [T, r]: kept for the backward pass."""
+    (T, K, N, R, r), ptrs = _lora_operands(x, order, offsets, A, B, scales, ranks)
+    bf16 = torch.bfloat16
+    xp, xs = _rows(x, (T, K), "x", bf16)
+    yp, ys = (None, 0) if y is None else _rows(y, (T, N), "y", bf16)
+    op, os_ = _rows(out, (T, N), "out", bf16)
+    _check(_lib.lora_apply(ctx.handle, xp, xs, *ptrs, T, K, N, R, r, yp, ys, op, os_,
+                           _dense(v, (T, r), "v", torch.float32), _stream(stream)),
+           "lora_apply")
+
+
+def lora_apply_bwd(ctx: Context, x, dy, order, offsets, A, B, scales, ranks, v, dx, dA, dB, dx0=None,
+                   stream=None) -> None:
+    """Gradients of lora_apply: dx = dx0 + the adapters' part (dx0 None: zero; may be dx), dA and dB of A's
+    and B's shapes, from dy, the forward pass's x and its v."""
+    (T, K, N, R, r), ptrs = _lora_operands(x, order, offsets, A, B, scales, ranks)
+    bf16 = torch.bfloat16
+    xp, xs = _rows(x, (T, K), "x", bf16)
+    yp, ys = _rows(dy, (T, N), "dy", bf16)
+    bp, bs = (None, 0) if dx0 is None else _rows(dx0, (T, K), "dx0", bf16)
+    dp, ds = _rows(dx, (T, K), "dx", bf16)
+    _check(_lib.lora_apply_bwd(ctx.handle, xp, xs, yp, ys, *ptrs, _dense(v, (T, r), "v", torch.float32),
+                               T, K, N, R, r, bp, bs, dp, ds, _dense(dA, (R, r, K), "dA", bf16),
+                               _dense(dB, (R, r, N), "dB", bf16), _stream(stream)),
+           "lora_apply_bwd")

@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -609,6 +610,181 @@ GEMMAR_API int gemmar_phase_times(gemmar_ctx *ctx, float *ms, int *calls)
     if (calls)
         *calls = ctx->recorded;
     ctx->recorded = 0;
+    return GEMMAR_OK;
+}
+
+// ---------------------------------------------------------------- residual stream and adapters
+
+namespace {
+
+bool known_dtype(int d) { return d == GEMMAR_DTYPE_F32 || d == GEMMAR_DTYPE_BF16; }
+
+// A matrix of rows at a stride: 0 (one row for all) or at least the row's length.
+int check_rows(const void *p, int64_t stride, int64_t cols, int elem_bytes, bool written = false)
+{
+    if (stride < 0 || (stride != 0 && stride < cols) || (written && stride == 0))
+        return GEMMAR_ERR_ARG;
+    if (!aligned16(p) || (stride * elem_bytes) % 16 != 0)
+        return GEMMAR_ERR_ALIGN;
+    return GEMMAR_OK;
+}
+
+int norm_shape(int64_t M, int64_t N)
+{
+    if (M < 1 || N < 1)
+        return GEMMAR_ERR_ARG;
+    if (N % 8 != 0 || N > GEMMAR_NORM_MAX_N || M > (int64_t(1) << 24))
+        return GEMMAR_ERR_SHAPE;
+    return GEMMAR_OK;
+}
+
+// What lora_apply and lora_apply_bwd share.
+int check_lora(const int32_t *order, const int32_t *offsets, const uint16_t *A, const uint16_t *B, const float *scales,
+               const int32_t *ranks, int64_t T, int64_t K, int64_t N, int R, int r)
+{
+    if (!order || !offsets || !A || !B || !scales || T < 1 || K < 1 || N < 1 || R < 1 || r < 1)
+        return GEMMAR_ERR_ARG;
+    if (K % 8 != 0 || N % 8 != 0 || K > 65536 || N > 65536 || T > (int64_t(1) << 24) ||
+        R > GEMMAR_LORA_MAX_ADAPTERS || r > GEMMAR_LORA_MAX_RANK)
+        return GEMMAR_ERR_SHAPE;
+    if (!aligned16(order) || !aligned16(offsets) || !aligned16(A) || !aligned16(B) || !aligned16(scales) ||
+        !aligned16(ranks))
+        return GEMMAR_ERR_ALIGN;
+    return GEMMAR_OK;
+}
+
+}  // namespace
+
+GEMMAR_API int norm_gate_residual(gemmar_ctx *ctx, const void *y, int y_dtype, int64_t y_stride, const void *h,
+                                  int h_dtype, int64_t h_stride, const float *w_post, const float *w_pre,
+                                  const uint16_t *gate, int64_t gate_stride, float alpha, float beta, float eps,
+                                  int64_t M, int64_t N, void *t, uint16_t *u, uint8_t *q, float *scales, float *rstd,
+                                  void *stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc)
+        return rc;
+    if (!y || !h || !t || !known_dtype(y_dtype) || !known_dtype(h_dtype) || (!w_pre && (u || q)) || (!q) != (!scales) ||
+        !std::isfinite(alpha) || !std::isfinite(beta) || !std::isfinite(eps) || eps < 0.0f)
+        return GEMMAR_ERR_ARG;
+    if ((rc = norm_shape(M, N)))
+        return rc;
+    if (q && N % 128 != 0)
+        return GEMMAR_ERR_SHAPE;
+    if ((rc = check_rows(y, y_stride, N, y_dtype == GEMMAR_DTYPE_BF16 ? 2 : 4)) ||
+        (rc = check_rows(h, h_stride, N, h_dtype == GEMMAR_DTYPE_BF16 ? 2 : 4)) ||
+        (gate && (rc = check_rows(gate, gate_stride, N, 2))))
+        return rc;
+    if (!aligned16(w_post) || !aligned16(w_pre) || !aligned16(t) || !aligned16(u) || !aligned16(q) ||
+        !aligned16(scales) || !aligned16(rstd))
+        return GEMMAR_ERR_ALIGN;
+    NormArgs a{y, h, y_dtype == GEMMAR_DTYPE_BF16, h_dtype == GEMMAR_DTYPE_BF16, y_stride, h_stride, w_post, w_pre,
+               gate, gate_stride, alpha, beta, eps, M, (int)N, t, u, q, scales, rstd};
+    CUDA_OK(launch_norm(a, ctx->num_sms, as_stream(stream)));
+    return GEMMAR_OK;
+}
+
+GEMMAR_API int norm_gate_residual_bwd(gemmar_ctx *ctx, const void *y, int y_dtype, int64_t y_stride, const void *h,
+                                      int h_dtype, int64_t h_stride, const float *rstd, const float *w_post,
+                                      const float *w_pre, const uint16_t *gate, int64_t gate_stride, float alpha,
+                                      float beta, int64_t M, int64_t N, const void *dt, int64_t dt_stride,
+                                      const uint16_t *du, int64_t du_stride, void *dy, void *dh, float *dw_post,
+                                      float *dw_pre, void *dgate, void *stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc)
+        return rc;
+    if (!y || !h || !rstd || !dy || !dh || !known_dtype(y_dtype) || !known_dtype(h_dtype) || (w_pre && !du) ||
+        (dw_post && !w_post) || (dw_pre && !w_pre) || (dgate && !gate) || !std::isfinite(alpha) ||
+        !std::isfinite(beta))
+        return GEMMAR_ERR_ARG;
+    if ((rc = norm_shape(M, N)))
+        return rc;
+    const int yb = y_dtype == GEMMAR_DTYPE_BF16 ? 2 : 4, hb = h_dtype == GEMMAR_DTYPE_BF16 ? 2 : 4;
+    if ((rc = check_rows(y, y_stride, N, yb)) || (rc = check_rows(h, h_stride, N, hb)) ||
+        (gate && (rc = check_rows(gate, gate_stride, N, 2))) || (dt && (rc = check_rows(dt, dt_stride, N, hb))) ||
+        (w_pre && (rc = check_rows(du, du_stride, N, 2))))
+        return rc;
+    if (!aligned16(rstd) || !aligned16(w_post) || !aligned16(w_pre) || !aligned16(dy) || !aligned16(dh) ||
+        !aligned16(dw_post) || !aligned16(dw_pre) || !aligned16(dgate))
+        return GEMMAR_ERR_ALIGN;
+    if (norm_bwd_ws_floats(M, (int)N, ctx->num_sms) > ctx->W_floats)
+        return GEMMAR_ERR_WORKSPACE;
+    NormBwdArgs a{y, h, yb == 2, hb == 2, y_stride, h_stride, rstd, w_post, w_pre, gate, gate_stride, alpha, beta, M,
+                  (int)N, dt, dt_stride, w_pre ? du : nullptr, du_stride, dy, dh, dw_post, dw_pre, dgate};
+    CUDA_OK(launch_norm_bwd(a, ctx->W, ctx->num_sms, as_stream(stream)));
+    return GEMMAR_OK;
+}
+
+GEMMAR_API int lora_plan(gemmar_ctx *ctx, const int32_t *adapter_ids, int64_t T, int R, int32_t *order,
+                         int32_t *offsets, void *stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc)
+        return rc;
+    if (!adapter_ids || !order || !offsets || T < 1 || R < 1)
+        return GEMMAR_ERR_ARG;
+    if (T > (int64_t(1) << 24) || R > GEMMAR_LORA_MAX_ADAPTERS)
+        return GEMMAR_ERR_SHAPE;
+    if (!aligned16(adapter_ids) || !aligned16(order) || !aligned16(offsets))
+        return GEMMAR_ERR_ALIGN;
+    CUDA_OK(launch_lora_plan(adapter_ids, T, R, order, offsets, as_stream(stream)));
+    return GEMMAR_OK;
+}
+
+GEMMAR_API int lora_apply(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, const int32_t *order,
+                          const int32_t *offsets, const uint16_t *A, const uint16_t *B, const float *scales,
+                          const int32_t *ranks, int64_t T, int64_t K, int64_t N, int R, int r, const uint16_t *y,
+                          int64_t y_stride, uint16_t *out, int64_t out_stride, float *v, void *stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc)
+        return rc;
+    if (!x || !out)
+        return GEMMAR_ERR_ARG;
+    if ((rc = check_lora(order, offsets, A, B, scales, ranks, T, K, N, R, r)) || (rc = check_rows(x, x_stride, K, 2)) ||
+        (y && (rc = check_rows(y, y_stride, N, 2))) || (rc = check_rows(out, out_stride, N, 2, true)))
+        return rc;
+    if (!aligned16(v))
+        return GEMMAR_ERR_ALIGN;
+    if (T * r + lora_ws_floats(T, r) > ctx->W_floats)
+        return GEMMAR_ERR_WORKSPACE;
+    cudaStream_t st = as_stream(stream);
+    const LoraArgs l{order, offsets, ranks, scales, T, R, r};
+    float *ws = ctx->W + (T * r + 3) / 4 * 4;
+    if (v == nullptr)
+        v = ctx->W;
+    CUDA_OK(launch_lora_down(l, x, x_stride, A, (int)K, false, v, ws, ctx->num_sms, st));
+    CUDA_OK(launch_lora_up(l, v, B, (int)N, true, y, y_stride, out, out_stride, ws, ctx->num_sms, st));
+    return GEMMAR_OK;
+}
+
+GEMMAR_API int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, const uint16_t *dy,
+                              int64_t dy_stride, const int32_t *order, const int32_t *offsets, const uint16_t *A,
+                              const uint16_t *B, const float *scales, const int32_t *ranks, const float *v, int64_t T,
+                              int64_t K, int64_t N, int R, int r, const uint16_t *dx0, int64_t dx0_stride,
+                              uint16_t *dx, int64_t dx_stride, uint16_t *dA, uint16_t *dB, void *stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc)
+        return rc;
+    if (!x || !dy || !v || !dx || !dA || !dB)
+        return GEMMAR_ERR_ARG;
+    if ((rc = check_lora(order, offsets, A, B, scales, ranks, T, K, N, R, r)) || (rc = check_rows(x, x_stride, K, 2)) ||
+        (rc = check_rows(dy, dy_stride, N, 2)) || (dx0 && (rc = check_rows(dx0, dx0_stride, K, 2))) ||
+        (rc = check_rows(dx, dx_stride, K, 2, true)))
+        return rc;
+    if (!aligned16(v) || !aligned16(dA) || !aligned16(dB))
+        return GEMMAR_ERR_ALIGN;
+    if (T * r + lora_ws_floats(T, r) > ctx->W_floats)
+        return GEMMAR_ERR_WORKSPACE;
+    cudaStream_t st = as_stream(stream);
+    const LoraArgs l{order, offsets, ranks, scales, T, R, r};
+    float *w = ctx->W, *ws = ctx->W + (T * r + 3) / 4 * 4;
+    CUDA_OK(launch_lora_down(l, dy, dy_stride, B, (int)N, true, w, ws, ctx->num_sms, st));
+    CUDA_OK(launch_lora_up(l, w, A, (int)K, false, dx0, dx0_stride, dx, dx_stride, ws, ctx->num_sms, st));
+    CUDA_OK(launch_lora_grad(l, w, x, x_stride, (int)K, false, dA, ws, ctx->num_sms, st));
+    CUDA_OK(launch_lora_grad(l, v, dy, dy_stride, (int)N, true, dB, ws, ctx->num_sms, st));
     return GEMMAR_OK;
 }
 

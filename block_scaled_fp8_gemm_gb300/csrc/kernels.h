@@ -153,4 +153,63 @@ cudaError_t launch_quant_blockscale(const void *x, int x_is_bf16, int64_t R, int
 cudaError_t launch_quant_mx(const void *x, int x_is_bf16, int64_t R, int64_t C, uint8_t *q, uint8_t *e8, int num_sms,
                             cudaStream_t st);
 
+// norm_gate_residual and its backward pass (residual.cu).  Strides in elements; a
+// gate with stride 0 is one row for every row.
+struct NormArgs {
+    const void *y, *h;
+    int y_bf16, h_bf16;
+    int64_t ys, hs;
+    const float *w1, *w2;      // post- and pre-norm weights, nullptr: none
+    const uint16_t *gate;
+    int64_t gs;
+    float alpha, beta, eps;
+    int64_t M;
+    int N;
+    void *t;                   // of h's type
+    uint16_t *u;
+    uint8_t *q;
+    float *scales, *rstd;
+};
+struct NormBwdArgs {
+    const void *y, *h;
+    int y_bf16, h_bf16;
+    int64_t ys, hs;
+    const float *rstd, *w1, *w2;
+    const uint16_t *gate;
+    int64_t gs;
+    float alpha, beta;
+    int64_t M;
+    int N;
+    const void *dt;            // of h's type
+    int64_t dts;
+    const uint16_t *du;
+    int64_t dus;
+    void *dy, *dh;
+    float *dw1, *dw2;
+    void *dgate;               // bf16 [M,N], or fp32 [N] when gs == 0
+};
+int64_t norm_bwd_ws_floats(int64_t M, int N, int num_sms);
+cudaError_t launch_norm(const NormArgs &a, int num_sms, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormBwdArgs &a, float *ws, int num_sms, cudaStream_t st);
+
+// Low-rank adapters (lora.cu).
+struct LoraArgs {
+    const int32_t *order, *offsets, *ranks;
+    const float *scales;
+    int64_t T;
+    int R, r;
+};
+cudaError_t launch_lora_plan(const int32_t *ids, int64_t T, int R, int32_t *order, int32_t *offsets, cudaStream_t st);
+// v[i,j] = f sum_c x[order[i],c] W[a,j,c], f = scales[a] if scaled, else 1
+int64_t lora_ws_floats(int64_t T, int r);
+cudaError_t launch_lora_down(const LoraArgs &l, const uint16_t *x, int64_t xs, const uint16_t *W, int C, bool scaled,
+                             float *v, float *ws, int num_sms, cudaStream_t st);
+// out[t,c] = base[t,c] + f sum_j v[i,j] W[a,j,c]; rows without an adapter: base
+cudaError_t launch_lora_up(const LoraArgs &l, const float *v, const uint16_t *W, int C, bool scaled,
+                           const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *ws, int num_sms,
+                           cudaStream_t st);
+// G[a,j,c] = f sum_{tokens of a} p[i,j] x[order[i],c]
+cudaError_t launch_lora_grad(const LoraArgs &l, const float *p, const uint16_t *x, int64_t xs, int C, bool scaled,
+                             uint16_t *G, float *ws, int num_sms, cudaStream_t st);
+
 }  // namespace gemmar

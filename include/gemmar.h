@@ -399,6 +399,130 @@ int fused_gemm_reduce_noalloc(int P, const uint8_t *const *A, const float *const
  */
 int fused_gemm_reduce_noalloc_status(int *detail);
 
+/*
+ * ---- The residual stream after wo_b -----------------------------------------
+ *
+ * The pages end at wo_b's bf16 rows; the operators from here on are additions
+ * of this library: what a transformer block does to those rows next (norms,
+ * gate and residual, codes for the next block-scaled GEMM), and the low-rank
+ * adapters that requests bring beside the shared projection.
+ *
+ * Their matrices may be views: a row stride (in elements) follows each pointer
+ * that has one, stride * element size a multiple of 16 bytes (else
+ * GEMMAR_ERR_ALIGN), 0 for one row read for all rows.  Everything else is
+ * contiguous.  They use the context's partial-sum workspace as scratch
+ * (GEMMAR_ERR_WORKSPACE when it is too small; a context made for the layer's
+ * max_M and N is large enough), so the rule on stream order above holds.
+ */
+
+/* Widest row and smallest column granule of norm_gate_residual. */
+#define GEMMAR_NORM_MAX_N 16384
+
+/*
+ * norm_gate_residual -- a block's output y joins the residual stream h, and the
+ * next block's input is formed from the sum; per row, with w1 = w_post,
+ * w2 = w_pre and the gate g,
+ *   r1 = 1 / sqrt(mean(y^2) + eps),  z = y * r1 * w1     (w_post NULL: z = y, r1 = 1)
+ *   t  = alpha * h + beta * g * z                        (gate NULL: g = 1)
+ *   r2 = 1 / sqrt(mean(t^2) + eps),  x = t * r2 * w2     (w_pre NULL: t only)
+ * t goes out in h's type, x as bf16 rows u and/or as the A operand of
+ * gemm_blockscale_fp8: e4m3 codes q [M,N] with fp32 scales [M, N/128], by the rule
+ * of quant_blockscale_e4m3 applied to the fp32 x (not to its bf16 rounding).
+ * All arithmetic is fp32 and every output is rounded once; x is formed from the
+ * fp32 t, not from its rounding to h's type.  Rows are independent: a row with a
+ * NaN or an infinity leaves the others alone.  |y| or |t| above 1.8e19 overflows
+ * its sum of squares.
+ *   y [M,N] of y_dtype, h [M,N] of h_dtype (GEMMAR_DTYPE_F32 or _BF16), row
+ *   strides y_stride, h_stride; w_post, w_pre fp32 [N] or NULL; gate bf16:
+ *   gate_stride 0 is one row [N] for every row, else [M,N].
+ *   t [M,N] of h_dtype (may be h itself when h is contiguous); u bf16 [M,N], q,
+ *   scales, rstd fp32 [M,2] (r1, r2; r2 is 1 without w_pre): NULL to leave out.
+ *   u may be y itself when y is contiguous bf16.
+ * N % 8 == 0, N <= GEMMAR_NORM_MAX_N; with q N % 128 == 0 (else
+ * GEMMAR_ERR_SHAPE).  eps >= 0, alpha, beta and eps finite.
+ */
+int norm_gate_residual(gemmar_ctx *ctx, const void *y, int y_dtype, int64_t y_stride,
+                       const void *h, int h_dtype, int64_t h_stride,
+                       const float *w_post, const float *w_pre, const uint16_t *gate, int64_t gate_stride,
+                       float alpha, float beta, float eps, int64_t M, int64_t N,
+                       void *t, uint16_t *u, uint8_t *q, float *scales, float *rstd, void *stream);
+
+/*
+ * norm_gate_residual_bwd -- its gradients, from dt (of t, type h_dtype; NULL: 0) and
+ * du (of x, bf16; required with w_pre, else ignored), given the forward pass's y,
+ * h and rstd; t is recomputed in fp32.  With n = y r1 and that = t r2:
+ *   d    = dt + r2 (du w2 - that mean(du w2 that))      (w_pre NULL: d = dt)
+ *   dh   = alpha d,   e = beta g d w1
+ *   dy   = r1 (e - n mean(e n))                         (w_post NULL: dy = beta g d)
+ *   dw_pre = sum_rows du that,   dw_post = sum_rows beta g d n
+ *   dgate  = beta n w1 d per token (bf16 [M,N]), or its sum over the rows when
+ *            the gate is one row (fp32 [N])
+ * dy [M,N] has y_dtype, dh [M,N] h_dtype (may be dt itself when dt is contiguous);
+ * dw_post, dw_pre fp32 [N] are overwritten and NULL leaves one out; dgate NULL
+ * likewise.  The sums over rows run in fp32 in an order fixed by M, N and the GPU:
+ * two calls give the same bits.
+ */
+int norm_gate_residual_bwd(gemmar_ctx *ctx, const void *y, int y_dtype, int64_t y_stride,
+                           const void *h, int h_dtype, int64_t h_stride, const float *rstd,
+                           const float *w_post, const float *w_pre, const uint16_t *gate, int64_t gate_stride,
+                           float alpha, float beta, int64_t M, int64_t N,
+                           const void *dt, int64_t dt_stride, const uint16_t *du, int64_t du_stride,
+                           void *dy, void *dh, float *dw_post, float *dw_pre, void *dgate, void *stream);
+
+/* Limits of the adapters: how many one call takes, and their largest rank. */
+#define GEMMAR_LORA_MAX_ADAPTERS 1024
+#define GEMMAR_LORA_MAX_RANK 128
+
+/*
+ * lora_plan -- the tokens of a batch in the order of their adapters: order[T] holds
+ * the tokens of adapter 0 in ascending order, then those of adapter 1, ..., then
+ * those without one (an id outside [0, R)); adapter a's are
+ * order[offsets[a] .. offsets[a+1]).  One batch's plan serves every layer.
+ *   adapter_ids int32 [T]; order int32 [T]; offsets int32 [R+1].
+ * 1 <= R <= GEMMAR_LORA_MAX_ADAPTERS, T <= 2^24.
+ */
+int lora_plan(gemmar_ctx *ctx, const int32_t *adapter_ids, int64_t T, int R, int32_t *order, int32_t *offsets,
+              void *stream);
+
+/*
+ * lora_apply -- low-rank adapters of many requests beside a shared projection: for
+ * token t with adapter a,
+ *   v[t,j]   = sum_k x[t,k] A[a,j,k]
+ *   out[t,n] = y[t,n] + scales[a] sum_{j < ranks[a]} v[t,j] B[a,j,n]
+ * and out[t] = y[t] for a token without one.  Both factors are stored rank-major
+ * (B is the transpose of an [N, r] up-projection), so a rank of any size keeps its
+ * rows on 16 bytes.  v is fp32 and enters the second product as two bf16 parts
+ * (its rounding error is below 2^-16); out is rounded once.
+ *   x bf16 [T,K], y bf16 [T,N] (NULL: 0) and out bf16 [T,N] with row strides; y may
+ *   be out itself.  order, offsets: lora_plan's form (entries outside [0,T) are
+ *   skipped).  A bf16 [R,r,K], B bf16 [R,r,N], scales fp32 [R], ranks int32 [R] (NULL:
+ *   r for all; rows beyond ranks[a] are not used).  v: NULL, or fp32 [T,r] for the
+ *   backward pass: row i belongs to token order[i]; rows past offsets[R] are left
+ *   alone, columns past ranks[a] are 0.
+ * K % 8 == 0, N % 8 == 0 (else GEMMAR_ERR_SHAPE), K, N <= 65536, T <= 2^24,
+ * 1 <= r <= GEMMAR_LORA_MAX_RANK.
+ */
+int lora_apply(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, const int32_t *order, const int32_t *offsets,
+               const uint16_t *A, const uint16_t *B, const float *scales, const int32_t *ranks,
+               int64_t T, int64_t K, int64_t N, int R, int r, const uint16_t *y, int64_t y_stride,
+               uint16_t *out, int64_t out_stride, float *v, void *stream);
+
+/*
+ * lora_apply_bwd -- its gradients, from dy (of out) and the forward pass's x and v:
+ *   w[t,j]    = scales[a] sum_n dy[t,n] B[a,j,n]
+ *   dx[t,k]   = dx0[t,k] + sum_{j < ranks[a]} w[t,j] A[a,j,k]   (dx0[t] for a token without one)
+ *   dA[a,j,k] = sum_{t of a} w[t,j] x[t,k],   dB[a,j,n] = scales[a] sum_{t of a} v[t,j] dy[t,n]
+ * (the gradient of y is dy itself).  dx0 bf16 [T,K] (NULL: 0; may be dx itself) and
+ * dx bf16 [T,K] with row strides; dA, dB bf16, of A's and B's shapes, overwritten:
+ * 0 for an adapter without tokens and for rows past ranks[a].  Sums are fp32 in a
+ * fixed order, rounded once.  Other arguments and limits as lora_apply.
+ */
+int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, const uint16_t *dy, int64_t dy_stride,
+                   const int32_t *order, const int32_t *offsets, const uint16_t *A, const uint16_t *B,
+                   const float *scales, const int32_t *ranks, const float *v,
+                   int64_t T, int64_t K, int64_t N, int R, int r, const uint16_t *dx0, int64_t dx0_stride,
+                   uint16_t *dx, int64_t dx_stride, uint16_t *dA, uint16_t *dB, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
