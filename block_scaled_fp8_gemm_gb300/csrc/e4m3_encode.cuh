@@ -65,6 +65,26 @@ struct Enc {
             return enc4(a, b, c, d, s);
         return enc2_guarded(a, b, s, yl, yh) | (enc2_guarded(c, d, s, yl, yh) << 16);
     }
+    // The same codes for W values that come from fp32 arithmetic, where a quotient this
+    // near a midpoint is rare (2^-20 or so a value): one test for all of them, and the
+    // divisions for all where it fails.
+    template <int W>
+    __device__ __forceinline__ void codes(const float (&x)[W], uint32_t (&w)[W / 4]) const
+    {
+        uint32_t differ = fast ? 0u : 1u;
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) {
+            const float2 l0 = ptx::mul2(x[4 * i], x[4 * i + 1], yl, yl), l1 = ptx::mul2(x[4 * i + 2], x[4 * i + 3], yl, yl);
+            const float2 h0 = ptx::mul2(x[4 * i], x[4 * i + 1], yh, yh), h1 = ptx::mul2(x[4 * i + 2], x[4 * i + 3], yh, yh);
+            w[i] = ptx::e4m3x2_from_f32(l0.x, l0.y) | (ptx::e4m3x2_from_f32(l1.x, l1.y) << 16);
+            differ |= w[i] ^ (ptx::e4m3x2_from_f32(h0.x, h0.y) | (ptx::e4m3x2_from_f32(h1.x, h1.y) << 16));
+        }
+        if (differ != 0u) {
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i)
+                w[i] = enc4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], s);
+        }
+    }
 };
 
 }  // namespace gemmar

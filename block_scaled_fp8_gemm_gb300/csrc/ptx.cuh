@@ -535,6 +535,12 @@ __device__ __forceinline__ void cp_async_cg16(uint32_t dst, const void *src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// 8 bytes (through L1: the 8-byte form has no other).
+__device__ __forceinline__ void cp_async_ca8(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // wait until at most N of this thread's committed cp.async groups are pending

@@ -21,64 +21,216 @@ namespace {
 
 constexpr int kMaxSmem = 231424;   // of the 232448 a CTA may have; the rest is static
 
-__device__ __forceinline__ void unpack8(const uint4 &w, float (&v)[8])
+// Two fp32 lanes in one register pair: the packed instructions round each lane as
+// the scalar ones do and halve the issue slots, which bound these kernels before
+// HBM does (see the measured figures at the kernels).
+typedef uint64_t f2;
+
+__device__ __forceinline__ f2 pack2(uint32_t lo, uint32_t hi)
 {
-    v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
-    v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z); v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
+    f2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+__device__ __forceinline__ f2 pack2(float lo, float hi) { return pack2(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ f2 both(float v) { return pack2(v, v); }
+__device__ __forceinline__ float lo2(f2 v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2(f2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b)
+{
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
+{
+    f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
 }
 
-// Eight consecutive fp32 (weights: re-read every row, from L1) or bf16.
-__device__ __forceinline__ void ldg8(const float *p, float (&v)[8])
+__device__ __forceinline__ f2 add2(f2 a, f2 b)
 {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
-__device__ __forceinline__ void ldg8(const uint16_t *p, float (&v)[8])
+// W consecutive values of a row as pairs.  W is 8 where the row's matrices are all
+// bf16 and 4 where one of them is fp32: a thread's unit is then 16 bytes of the
+// wider type, so that a warp's accesses cover whole 32-byte sectors (units of 8
+// columns read and wrote fp32 rows in half sectors: 102 us instead of 66 at
+// 4096 x 7168 with an fp32 stream).
+template <int W>
+struct Vec {
+    f2 v[W / 2];
+};
+
+template <int W>
+__device__ __forceinline__ Vec<W> all_of(float x)
 {
-    unpack8(__ldg(reinterpret_cast<const uint4 *>(p)), v);
+    Vec<W> r;
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i)
+        r.v[i] = both(x);
+    return r;
 }
 
-template <bool BF>
-__device__ __forceinline__ void store8(void *p, int64_t i, const float (&v)[8])
+template <int W>
+__device__ __forceinline__ Vec<W> operator*(const Vec<W> &a, const Vec<W> &b)
 {
-    if constexpr (BF) {
-        uint4 w;
-        w.x = bf16x2_from_f32(v[0], v[1]);
-        w.y = bf16x2_from_f32(v[2], v[3]);
-        w.z = bf16x2_from_f32(v[4], v[5]);
-        w.w = bf16x2_from_f32(v[6], v[7]);
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) = w;
-    } else {
-        float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-        f[0] = make_float4(v[0], v[1], v[2], v[3]);
-        f[1] = make_float4(v[4], v[5], v[6], v[7]);
+    Vec<W> r;
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i)
+        r.v[i] = mul2(a.v[i], b.v[i]);
+    return r;
+}
+
+template <int W>
+__device__ __forceinline__ Vec<W> operator*(const Vec<W> &a, f2 b)
+{
+    Vec<W> r;
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i)
+        r.v[i] = mul2(a.v[i], b);
+    return r;
+}
+
+// a * b + c
+template <int W>
+__device__ __forceinline__ Vec<W> fma_of(const Vec<W> &a, f2 b, const Vec<W> &c)
+{
+    Vec<W> r;
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i)
+        r.v[i] = fma2(a.v[i], b, c.v[i]);
+    return r;
+}
+
+template <int W>
+__device__ __forceinline__ f2 dot_of(const Vec<W> &a, const Vec<W> &b, f2 s)
+{
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i)
+        s = fma2(a.v[i], b.v[i], s);
+    return s;
+}
+
+// A unit as it lies in memory: W * 2 or W * 4 bytes.
+template <int W, bool BF>
+struct Raw {
+    static constexpr int kWords = W * (BF ? 2 : 4) / 4;   // 2, 4 or 8
+    static constexpr int kBytes = kWords * 4;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ f2 pair(int i) const   // columns 2i, 2i + 1
+    {
+        if constexpr (BF)
+            return pack2(w[i] << 16, w[i] & 0xFFFF0000u);
+        else
+            return pack2(w[2 * i], w[2 * i + 1]);
     }
+    __device__ __forceinline__ Vec<W> vec() const
+    {
+        Vec<W> r;
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i)
+            r.v[i] = pair(i);
+        return r;
+    }
+    __device__ __forceinline__ void set(const Vec<W> &r)
+    {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+            if constexpr (BF) {
+                w[i] = bf16x2_from_f32(lo2(r.v[i]), hi2(r.v[i]));
+            } else {
+                w[2 * i] = (uint32_t)r.v[i];
+                w[2 * i + 1] = (uint32_t)(r.v[i] >> 32);
+            }
+        }
+    }
+    // from a shared-memory slot, or through the read-only cache
+    __device__ __forceinline__ void read(uint32_t slot)
+    {
+        if constexpr (kWords == 2) {
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(slot) : "memory");
+        } else {
+#pragma unroll
+            for (int k = 0; k < kWords; k += 4)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[k]), "=r"(w[k + 1]), "=r"(w[k + 2]), "=r"(w[k + 3])
+                             : "r"(slot + k * 4)
+                             : "memory");
+        }
+    }
+    __device__ __forceinline__ void ldg(const void *p)
+    {
+        if constexpr (kWords == 2) {
+            const uint2 x = __ldg(static_cast<const uint2 *>(p));
+            w[0] = x.x;
+            w[1] = x.y;
+        } else {
+#pragma unroll
+            for (int k = 0; k < kWords; k += 4) {
+                const uint4 x = __ldg(static_cast<const uint4 *>(p) + k / 4);
+                w[k] = x.x;
+                w[k + 1] = x.y;
+                w[k + 2] = x.z;
+                w[k + 3] = x.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(void *p) const
+    {
+        if constexpr (kWords == 2) {
+            *static_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kWords; k += 4)
+                static_cast<uint4 *>(p)[k / 4] = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+        }
+    }
+};
+
+template <int W>
+__device__ __forceinline__ Vec<W> ldg_f32(const float *p)
+{
+    Raw<W, false> r;
+    r.ldg(p);
+    return r.vec();
+}
+template <int W>
+__device__ __forceinline__ Vec<W> ldg_bf16(const uint16_t *p)
+{
+    Raw<W, true> r;
+    r.ldg(p);
+    return r.vec();
+}
+template <int W, bool BF>
+__device__ __forceinline__ Vec<W> from_slot(uint32_t slot)
+{
+    Raw<W, BF> r;
+    r.read(slot);
+    return r.vec();
+}
+template <int W, bool BF>
+__device__ __forceinline__ void store_vec(void *base, int64_t i, const Vec<W> &v)
+{
+    Raw<W, BF> r;
+    r.set(v);
+    r.store(static_cast<char *>(base) + i * (BF ? 2 : 4));
 }
 
-// A thread's slots of one matrix in one stage: J chunks of one (bf16) or two
-// (fp32) 16-byte units, unit u of thread t at (u * T + t) * 16, so that a warp's
-// accesses are contiguous.
-template <bool BF>
-__device__ __forceinline__ void fetch8(uint32_t slot, int T, const void *row, int col)
+// Copy the unit at column `col` of a row to the thread's slot.
+template <int W, bool BF>
+__device__ __forceinline__ void fetch(uint32_t slot, const void *row, int col)
 {
     const char *src = static_cast<const char *>(row) + (int64_t)col * (BF ? 2 : 4);
-    cp_async_cg16(slot, src);
-    if constexpr (!BF)
-        cp_async_cg16(slot + T * 16, src + 16);
-}
-
-template <bool BF>
-__device__ __forceinline__ void slot8(uint32_t slot, int T, float (&v)[8])
-{
-    const uint4 a = ld_shared_v4(slot);
-    if constexpr (BF) {
-        unpack8(a, v);
-    } else {
-        const uint4 b = ld_shared_v4(slot + T * 16);
-        v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
-        v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
-    }
+    if constexpr (W * (BF ? 2 : 4) == 8)
+        cp_async_ca8(slot, src);
+    else
+        cp_async_cg16(slot, src);
 }
 
 // All but the newest stages - 1 groups of this thread's copies have landed.
@@ -95,168 +247,225 @@ __device__ __forceinline__ void wait_stage(int stages)
 }
 constexpr int kMaxStages = 4;
 
-__device__ __forceinline__ float warp_sum(float v)
+// Sum over the CTA, the same bits in every thread.  One barrier: two buffers take
+// turns, so a warp that is a sum ahead of another writes the one not being read.
+// Entries past the CTA's warps stay zero.
+__device__ __forceinline__ float cta_sum(f2 pair, float (&bufs)[2][32], int &turn)
 {
+    float v = lo2(pair) + hi2(pair);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
-}
-
-// Sum over the CTA, the same bits in every thread.  One barrier: two buffers take
-// turns, so a warp that is a sum ahead of another writes the one not being read.
-__device__ __forceinline__ float cta_sum(float v, float (&bufs)[2][32], int &turn)
-{
-    v = warp_sum(v);
-    const int lane = threadIdx.x & 31;
     float *red = bufs[turn];
     turn ^= 1;
-    if (lane == 0)
+    if ((threadIdx.x & 31) == 0)
         red[threadIdx.x >> 5] = v;
     __syncthreads();
-    return warp_sum(lane < (int)(blockDim.x >> 5) ? red[lane] : 0.0f);
+    f2 s0 = both(0.0f), s1 = s0;
+    const int vecs = (blockDim.x + 127) / 128;
+#pragma unroll 4
+    for (int i = 0; i < vecs; ++i) {
+        const ulonglong2 w = reinterpret_cast<const ulonglong2 *>(red)[i];
+        s0 = add2(s0, w.x);
+        s1 = add2(s1, w.y);
+    }
+    s0 = add2(s0, s1);
+    return lo2(s0) + hi2(s0);
 }
 
 // ---------------------------------------------------------------- forward
 
-template <int J, bool YB, bool HB>
-__global__ void __launch_bounds__(J == 1 ? 1024 : 512, J == 2 ? 2 : 1) norm_kernel(const NormArgs a, int stages)
+// First column of the thread's units; unit k is 32 W k further on.
+template <int U, int W>
+__device__ __forceinline__ int first_col()
 {
+    return ((int)(threadIdx.x & ~31u) * U + (int)(threadIdx.x & 31u)) * W;
+}
+
+// e4m3 codes of a row's units with one scale per 128 columns: a group is 128 / W
+// neighbouring lanes of one unit (N % 128 == 0, so whole groups are inside the row).
+// The U maxima are reduced together: while more than one is left, a step halves the
+// lanes' distance and each lane keeps half of them, so lane l ends with the maximum
+// of unit unit_of(l) and computes that unit's scale and reciprocal for the others.
+template <int U, int W>
+__device__ __forceinline__ void encode_units(const Vec<W> (&v)[U], uint8_t *q, float *scales, int N)
+{
+    constexpr int L = 128 / W;   // lanes of a group
+    const int lane = threadIdx.x & 31, c0 = first_col<U, W>();
+    float amax[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        amax[k] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i)
+            amax[k] = fmaxf(amax[k], fmaxf(fabsf(lo2(v[k].v[i])), fabsf(hi2(v[k].v[i]))));
+    }
+    int o = L / 2, mine = 0;
+#pragma unroll
+    for (int n = U; n > 1; n /= 2, o /= 2) {
+        const bool up = lane & o;
+        mine = mine * 2 + (up ? 1 : 0);
+#pragma unroll
+        for (int k = 0; k < n / 2; ++k) {
+            const float keep = up ? amax[n / 2 + k] : amax[k], send = up ? amax[k] : amax[n / 2 + k];
+            amax[k] = fmaxf(keep, __shfl_xor_sync(0xFFFFFFFFu, send, o));
+        }
+    }
+#pragma unroll
+    for (; o > 0; o /= 2)
+        amax[0] = fmaxf(amax[0], __shfl_xor_sync(0xFFFFFFFFu, amax[0], o));
+    const float sc = __fdiv_rn(amax[0], 448.0f);
+    const Enc e(sc);
+    // the first lane of a group with this unit writes its scale
+    const int first = c0 - (lane & (L - 1)) * W + mine * 32 * W;
+    if ((lane & (L / U - 1)) == 0 && first < N)
+        scales[first / 128] = sc;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const int col = c0 + k * 32 * W, src = (lane & ~(L - 1)) + k * (L / U);
+        const Enc enc(__shfl_sync(0xFFFFFFFFu, e.s, src), __shfl_sync(0xFFFFFFFFu, e.yl, src),
+                      __shfl_sync(0xFFFFFFFFu, e.yh, src), __shfl_sync(0xFFFFFFFFu, (int)e.fast, src) != 0);
+        if (col < N) {
+            float x[W];
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) {
+                x[2 * i] = lo2(v[k].v[i]);
+                x[2 * i + 1] = hi2(v[k].v[i]);
+            }
+            uint32_t w[W / 4];
+            enc.codes<W>(x, w);
+            if constexpr (W == 8)
+                *reinterpret_cast<uint2 *>(q + col) = make_uint2(w[0], w[1]);
+            else
+                *reinterpret_cast<uint32_t *>(q + col) = w[0];
+        }
+    }
+}
+
+// A thread holds U units of W columns of its row.  A warp takes 32 U W neighbouring
+// columns and its units lie 32 W apart, so one address per matrix and fixed
+// offsets reach them all (with units T W apart address arithmetic was a third of
+// the instructions: 71 us instead of XX at 4096 x 7168, fp32 stream, codes).
+// Two rows an SM in flight (two CTAs) hide each other's two sums.  Weights come
+// through L1, which the rings leave room for (kNormRing).
+template <int U, bool YB, bool HB>
+__global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int stages)
+{
+    constexpr int W = YB && HB ? 8 : 4;
+    constexpr int kY = Raw<W, YB>::kBytes, kH = Raw<W, HB>::kBytes, kG = Raw<W, true>::kBytes;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ float red[2][32];
+    __shared__ __align__(16) float red[2][32];
     const int T = blockDim.x, t = threadIdx.x, N = a.N;
     const bool token = a.gate != nullptr && a.gs != 0;
-    constexpr int UY = J * (YB ? 1 : 2), UH = J * (HB ? 1 : 2);
-    const uint32_t unit = T * 16;
-    const uint32_t stage_bytes = (UY + UH + (token ? J : 0)) * unit;
-    const uint32_t base = smem_u32(smem_raw) + t * 16;
+    const uint32_t off_h = U * kY * T, off_g = off_h + U * kH * T;
+    const uint32_t stage_bytes = off_g + (token ? U * kG * T : 0);
+    const uint32_t base = smem_u32(smem_raw);
     const float inv_n = 1.0f / N;
+    const int c0 = first_col<U, W>();
+    auto col_of = [&](int k) { return c0 + k * 32 * W; };
+    // a stage holds each matrix's row in the order of its columns
+    auto y_slot = [&](uint32_t st, int k) { return st + c0 * (kY / W) + k * 32 * kY; };
+    auto h_slot = [&](uint32_t st, int k) { return st + off_h + c0 * (kH / W) + k * 32 * kH; };
+    auto g_slot = [&](uint32_t st, int k) { return st + off_g + c0 * (kG / W) + k * 32 * kG; };
 
-    auto fetch = [&](int64_t m, uint32_t slot) {
+    auto fetch_row = [&](int64_t m, uint32_t st) {
         const char *y = static_cast<const char *>(a.y) + m * a.ys * (YB ? 2 : 4);
         const char *h = static_cast<const char *>(a.h) + m * a.hs * (HB ? 2 : 4);
 #pragma unroll
-        for (int c = 0; c < J; ++c) {
-            const int col = (c * T + t) * 8;
-            if (col < N) {
-                fetch8<YB>(slot + c * (UY / J) * unit, T, y, col);
-                fetch8<HB>(slot + (UY + c * (UH / J)) * unit, T, h, col);
+        for (int k = 0; k < U; ++k) {
+            if (col_of(k) < N) {
+                fetch<W, YB>(y_slot(st, k), y, col_of(k));
+                fetch<W, HB>(h_slot(st, k), h, col_of(k));
                 if (token)
-                    fetch8<true>(slot + (UY + UH + c) * unit, T, a.gate + m * a.gs, col);
+                    fetch<W, true>(g_slot(st, k), a.gate + m * a.gs, col_of(k));
             }
         }
     };
 
     int64_t ahead = blockIdx.x;   // next row to fetch
-    int put = 0, get = 0, turn = 0;
-    for (int s = 0; s < stages - 1; ++s, ahead += gridDim.x) {
+    for (int s = 0; s < stages; ++s, ahead += gridDim.x) {
         if (ahead < a.M)
-            fetch(ahead, base + put * stage_bytes);
+            fetch_row(ahead, base + s * stage_bytes);
         cp_async_commit();
-        if (++put == stages)
-            put = 0;
     }
+    for (int i = t; i < 64; i += T)
+        red[i >> 5][i & 31] = 0.0f;
+    __syncthreads();
+    int get = 0, turn = 0;
     for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, ahead += gridDim.x) {
-        // the slot of the row before this one is free: this thread has read it
-        if (ahead < a.M)
-            fetch(ahead, base + put * stage_bytes);
-        cp_async_commit();
-        if (++put == stages)
-            put = 0;
         wait_stage(stages);
-        const uint32_t slot = base + get * stage_bytes;
+        const uint32_t st = base + get * stage_bytes;
         if (++get == stages)
             get = 0;
 
-        float v[J][8];   // y, then t
+        Vec<W> v[U];   // y, then t, then x
         float r1 = 1.0f, r2 = 1.0f;
-        float ss = 0.0f;
 #pragma unroll
-        for (int c = 0; c < J; ++c) {
-            if ((c * T + t) * 8 < N) {
-                slot8<YB>(slot + c * (UY / J) * unit, T, v[c]);
-            } else {
+        for (int k = 0; k < U; ++k)
+            v[k] = col_of(k) < N ? from_slot<W, YB>(y_slot(st, k)) : all_of<W>(0.0f);
+        if (a.w1) {
+            f2 ss = both(0.0f);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[c][j] = 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                ss = fmaf(v[c][j], v[c][j], ss);
-        }
-        if (a.w1)
+            for (int k = 0; k < U; ++k)
+                ss = dot_of(v[k], v[k], ss);
             r1 = rsqrtf(cta_sum(ss, red, turn) * inv_n + a.eps);
-        ss = 0.0f;
-#pragma unroll
-        for (int c = 0; c < J; ++c) {
-            const int col = (c * T + t) * 8;
-            if (col < N) {
-                float f[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[c][j] *= r1;
-                if (a.w1) {
-                    ldg8(a.w1 + col, f);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[c][j] *= f[j];
-                }
-                if (a.gate) {
-                    if (token)
-                        slot8<true>(slot + (UY + UH + c) * unit, T, f);
-                    else
-                        ldg8(a.gate + col, f);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[c][j] *= f[j];
-                }
-                slot8<HB>(slot + (UY + c * (UH / J)) * unit, T, f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    v[c][j] = fmaf(a.alpha, f[j], a.beta * v[c][j]);
-                    ss = fmaf(v[c][j], v[c][j], ss);
-                }
-                store8<HB>(a.t, m * N + col, v[c]);
-            }
         }
-        if (a.w2)
+        const f2 br1 = both(a.beta * r1), alpha = both(a.alpha);
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            v[k] = v[k] * br1;
+        if (a.w1) {
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (col_of(k) < N)
+                    v[k] = v[k] * ldg_f32<W>(a.w1 + col_of(k));
+        }
+        if (token) {
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (col_of(k) < N)
+                    v[k] = v[k] * from_slot<W, true>(g_slot(st, k));
+        } else if (a.gate) {
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (col_of(k) < N)
+                    v[k] = v[k] * ldg_bf16<W>(a.gate + col_of(k));
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (col_of(k) < N)
+                v[k] = fma_of(from_slot<W, HB>(h_slot(st, k)), alpha, v[k]);
+        // this thread has read all of its slots: the row `stages` ahead takes them
+        if (ahead < a.M)
+            fetch_row(ahead, st);
+        cp_async_commit();
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (col_of(k) < N)
+                store_vec<W, HB>(a.t, m * N + col_of(k), v[k]);
+        if (a.w2) {
+            f2 ss = both(0.0f);
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                ss = dot_of(v[k], v[k], ss);
             r2 = rsqrtf(cta_sum(ss, red, turn) * inv_n + a.eps);
+        }
         if (a.rstd && t == 0)
             *reinterpret_cast<float2 *>(a.rstd + 2 * m) = make_float2(r1, r2);
         if (a.u == nullptr && a.q == nullptr)
             continue;
 #pragma unroll
-        for (int c = 0; c < J; ++c) {
-            const int col = (c * T + t) * 8;
-            float amax = 0.0f;
-            if (col < N) {
-                float f[8];
-                ldg8(a.w2 + col, f);
+        for (int k = 0; k < U; ++k)
+            if (col_of(k) < N)
+                v[k] = v[k] * both(r2) * ldg_f32<W>(a.w2 + col_of(k));
+        if (a.u) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    v[c][j] = v[c][j] * r2 * f[j];
-                    amax = fmaxf(amax, fabsf(v[c][j]));
-                }
-                if (a.u)
-                    store8<true>(a.u, m * N + col, v[c]);
-            }
-            if (a.q) {
-                // a group's 128 columns are 16 neighbouring lanes (N % 128 == 0)
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1)
-                    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-                if (col < N) {
-                    const float sc = __fdiv_rn(amax, 448.0f);
-                    const Enc enc(sc);
-                    uint2 w;
-                    w.x = enc(v[c][0], v[c][1], v[c][2], v[c][3]);
-                    w.y = enc(v[c][4], v[c][5], v[c][6], v[c][7]);
-                    *reinterpret_cast<uint2 *>(a.q + m * N + col) = w;
-                    if ((t & 15) == 0)
-                        a.scales[m * (N / 128) + col / 128] = sc;
-                }
-            }
+            for (int k = 0; k < U; ++k)
+                if (col_of(k) < N)
+                    store_vec<W, true>(a.u, m * N + col_of(k), v[k]);
         }
+        if (a.q)
+            encode_units<U, W>(v, a.q + m * N, a.scales + m * (N / 128), N);
     }
 }
 
@@ -266,225 +475,269 @@ __global__ void __launch_bounds__(J == 1 ? 1024 : 512, J == 2 ? 2 : 1) norm_kern
 // with dv = du w2, c = beta g w1, n = y r1, t = alpha h + c n and d = dt + r2 dv - k t,
 // k = r2^3 mean(dv t),
 //   mean(c n d) = mean(c n dt) + r2 mean(c n dv) - k mean(c n t).
-// The second pass recomputes n, t, dv from shared memory and writes dy, dh (and a
-// token's dgate).  The sums over rows, s1 = sum n d (times a token's gate) and
-// s2 = sum du t r2, stay in the thread's registers over all the CTA's rows and
-// leave as one part per CTA, summed in the CTAs' order by norm_bwd_sum_kernel.
-template <int J, bool YB, bool HB>
-__global__ void __launch_bounds__(J == 1 ? 256 : 512, J == 1 ? 3 : 1)
+// The second pass recomputes n, t and dv and writes dy, dh (and a token's dgate).
+// The sums over rows, s1 = sum n d (times a token's gate) and s2 = sum du t r2,
+// stay in the thread's registers over all the CTA's rows and leave as one part per
+// CTA, summed in the CTAs' order by norm_bwd_sum_kernel.
+// HOLD (rows up to 8192, 16 columns a thread): the row's packed values stay in
+// registers between the passes, so its slots are free for the next row before the
+// sums are exchanged; the weights sit in shared memory.  Wider rows take 32 columns
+// a thread, read the slots twice and the weights through L1.
+template <int U, bool YB, bool HB, bool TOKEN, bool HOLD>
+__global__ void __launch_bounds__(512, 1)
     norm_bwd_kernel(const NormBwdArgs a, float *__restrict__ ws, int stages, int gate_staged)
 {
+    constexpr int W = YB && HB ? 8 : 4;
+    constexpr int kY = Raw<W, YB>::kBytes, kH = Raw<W, HB>::kBytes, kB = Raw<W, true>::kBytes, kF = Raw<W, false>::kBytes;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ float4 red[2][32];
+    __shared__ float red[2][16][4];
     const int T = blockDim.x, t = threadIdx.x, lane = t & 31, N = a.N;
-    const bool token = a.gate != nullptr && a.gs != 0;
     const bool pre = a.w2 != nullptr, post = a.w1 != nullptr;
-    constexpr int UY = J * (YB ? 1 : 2), UH = J * (HB ? 1 : 2);
-    constexpr int kDu = UY + UH, kDt = kDu + J, kGate = kDt + UH;
-    const uint32_t unit = T * 16;
-    const uint32_t stage_bytes = (kGate + (gate_staged ? J : 0)) * unit;
-    const uint32_t base = smem_u32(smem_raw) + t * 16;
+    const uint32_t off_h = U * kY * T, off_dt = off_h + U * kH * T, off_du = off_dt + U * kH * T, off_g = off_du + U * kB * T;
+    const uint32_t stage_bytes = off_g + (gate_staged ? U * kB * T : 0);
+    const uint32_t base = smem_u32(smem_raw);
+    const uint32_t off_cw = stages * stage_bytes, off_w2 = off_cw + U * kF * T;   // HOLD
     const float inv_n = 1.0f / N;
-    constexpr bool kKeepWeights = J <= 2;   // more chunks would not fit the registers
+    const int c0 = first_col<U, W>();
+    auto col_of = [&](int k) { return c0 + k * 32 * W; };
+    // of a row kept at `off` in the order of its columns, unit k's `bytes`
+    auto at = [&](uint32_t off, int bytes, int k) { return off + c0 * (bytes / W) + k * 32 * bytes; };
 
-    auto fetch = [&](int64_t m, uint32_t slot) {
+    auto fetch_row = [&](int64_t m, uint32_t st) {
         const char *y = static_cast<const char *>(a.y) + m * a.ys * (YB ? 2 : 4);
         const char *h = static_cast<const char *>(a.h) + m * a.hs * (HB ? 2 : 4);
         const char *dt = static_cast<const char *>(a.dt) + m * a.dts * (HB ? 2 : 4);
 #pragma unroll
-        for (int c = 0; c < J; ++c) {
-            const int col = (c * T + t) * 8;
+        for (int k = 0; k < U; ++k) {
+            const int col = col_of(k);
             if (col < N) {
-                fetch8<YB>(slot + c * (UY / J) * unit, T, y, col);
-                fetch8<HB>(slot + (UY + c * (UH / J)) * unit, T, h, col);
-                if (pre)
-                    fetch8<true>(slot + (kDu + c) * unit, T, a.du + m * a.dus, col);
+                fetch<W, YB>(at(st, kY, k), y, col);
+                fetch<W, HB>(at(st + off_h, kH, k), h, col);
                 if (a.dt)
-                    fetch8<HB>(slot + (kDt + c * (UH / J)) * unit, T, dt, col);
+                    fetch<W, HB>(at(st + off_dt, kH, k), dt, col);
+                if (pre)
+                    fetch<W, true>(at(st + off_du, kB, k), a.du + m * a.dus, col);
                 if (gate_staged)
-                    fetch8<true>(slot + (kGate + c) * unit, T, a.gate + m * a.gs, col);
+                    fetch<W, true>(at(st + off_g, kB, k), a.gate + m * a.gs, col);
             }
         }
     };
-    // beta w1 (times the gate when it is one row), and w2
-    auto weights = [&](int col, float (&cw)[8], float (&w2)[8]) {
+    // a gradient that is absent reads as zero
+    for (int s = 0; s < stages; ++s) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            cw[j] = a.beta;
-            w2[j] = 0.0f;
+        for (int k = 0; k < U; ++k) {
+            if (!a.dt) {
+                Raw<W, HB> z;
+                z.set(all_of<W>(0.0f));
+                z.store(smem_raw + at(s * stage_bytes + off_dt, kH, k));
+            }
+            if (!pre) {
+                Raw<W, true> z;
+                z.set(all_of<W>(0.0f));
+                z.store(smem_raw + at(s * stage_bytes + off_du, kB, k));
+            }
         }
-        if (col >= N)
-            return;
-        float f[8];
-        if (post) {
-            ldg8(a.w1 + col, f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                cw[j] *= f[j];
-        }
-        if (a.gate != nullptr && !token) {
-            ldg8(a.gate + col, f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                cw[j] *= f[j];
-        }
-        if (pre)
-            ldg8(a.w2 + col, w2);
-    };
-
-    float s1[J][8], s2[J][8];
-    float kw[kKeepWeights ? J : 1][8], kw2[kKeepWeights ? J : 1][8];
-#pragma unroll
-    for (int c = 0; c < J; ++c) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            s1[c][j] = s2[c][j] = 0.0f;
-        if constexpr (kKeepWeights)
-            weights((c * T + t) * 8, kw[c], kw2[c]);
     }
-
     int64_t ahead = blockIdx.x;
-    int put = 0, get = 0, turn = 0;
-    for (int s = 0; s < stages - 1; ++s, ahead += gridDim.x) {
+    for (int s = 0; s < stages; ++s, ahead += gridDim.x) {
         if (ahead < a.M)
-            fetch(ahead, base + put * stage_bytes);
+            fetch_row(ahead, base + s * stage_bytes);
         cp_async_commit();
-        if (++put == stages)
-            put = 0;
     }
+
+    // beta w1 (times the gate when it is one row), and w2
+    auto weights = [&](int col, Vec<W> &cw, Vec<W> &w2) {
+        cw = all_of<W>(a.beta);
+        w2 = all_of<W>(0.0f);
+        if (post)
+            cw = cw * ldg_f32<W>(a.w1 + col);
+        if (a.gate != nullptr && !TOKEN)
+            cw = cw * ldg_bf16<W>(a.gate + col);
+        if (pre)
+            w2 = ldg_f32<W>(a.w2 + col);
+    };
+    if constexpr (HOLD) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (col_of(k) < N) {
+                Vec<W> cw, w2;
+                weights(col_of(k), cw, w2);
+                Raw<W, false> r;
+                r.set(cw);
+                r.store(smem_raw + at(off_cw, kF, k));
+                r.set(w2);
+                r.store(smem_raw + at(off_w2, kF, k));
+            }
+        }
+    }
+
+    Vec<W> s1[U], s2[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+        s1[k] = s2[k] = all_of<W>(0.0f);
+
+    int get = 0, turn = 0;
+    // the reciprocal norms are loaded a row ahead
+    const float2 *rstd = reinterpret_cast<const float2 *>(a.rstd);
+    float2 next = __ldg(rstd + blockIdx.x);
     for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, ahead += gridDim.x) {
-        if (ahead < a.M)
-            fetch(ahead, base + put * stage_bytes);
-        cp_async_commit();
-        if (++put == stages)
-            put = 0;
-        const float2 rs = __ldg(reinterpret_cast<const float2 *>(a.rstd) + m);
-        const float r1 = rs.x, r2 = rs.y;
+        const float r1s = next.x, r2s = next.y;
+        if (m + gridDim.x < a.M)
+            next = __ldg(rstd + m + gridDim.x);
+        const f2 r1 = both(r1s), r2 = both(r2s), alpha = both(a.alpha);
         wait_stage(stages);
-        const uint32_t slot = base + get * stage_bytes;
+        const uint32_t st = base + get * stage_bytes;
         if (++get == stages)
             get = 0;
 
-        // n, t, du, c of chunk c
-        auto load = [&](int c, float (&n)[8], float (&tt)[8], float (&du)[8], float (&cw)[8], float (&w2)[8],
-                        float (&gt)[8]) {
-            const int col = (c * T + t) * 8;
-            if constexpr (kKeepWeights) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    cw[j] = kw[c][j];
-                    w2[j] = kw2[c][j];
-                }
-            } else {
-                weights(col, cw, w2);
-            }
-            slot8<YB>(slot + c * (UY / J) * unit, T, n);
-            slot8<HB>(slot + (UY + c * (UH / J)) * unit, T, tt);
-            if (pre)
-                slot8<true>(slot + (kDu + c) * unit, T, du);
-            if (token) {
+        Raw<W, YB> ry[HOLD ? U : 1];
+        Raw<W, HB> rh[HOLD ? U : 1], rdt[HOLD ? U : 1];
+        Raw<W, true> rdu[HOLD ? U : 1], rg[HOLD ? U : 1];
+        auto read = [&](int k) {
+            const int i = HOLD ? k : 0;
+            ry[i].read(at(st, kY, k));
+            rh[i].read(at(st + off_h, kH, k));
+            rdt[i].read(at(st + off_dt, kH, k));
+            rdu[i].read(at(st + off_du, kB, k));
+            if constexpr (TOKEN) {
                 if (gate_staged)
-                    slot8<true>(slot + (kGate + c) * unit, T, gt);
+                    rg[i].read(at(st + off_g, kB, k));
                 else
-                    ldg8(a.gate + m * a.gs + col, gt);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (!pre)
-                    du[j] = 0.0f;
-                if (!token)
-                    gt[j] = 1.0f;
-                n[j] *= r1;
-                tt[j] = fmaf(a.alpha, tt[j], cw[j] * gt[j] * n[j]);
+                    rg[i].ldg(a.gate + m * a.gs + col_of(k));
             }
         };
-        auto stream_grad = [&](int c, float (&dt)[8]) {
-            if (a.dt) {
-                slot8<HB>(slot + (kDt + c * (UH / J)) * unit, T, dt);
+        // pair i of unit k: n, gcw = cw (times a token's gate), cn = gcw n, t = alpha h + cn, dv = du w2
+        struct Pair {
+            f2 n, cw, gcw, cn, t, du, dv;
+        };
+        auto form = [&](int k, int i, const Vec<W> &cws, const Vec<W> &w2s) {
+            const int r = HOLD ? k : 0;
+            Pair p;
+            p.n = mul2(ry[r].pair(i), r1);
+            p.gcw = p.cw = cws.v[i];
+            if constexpr (TOKEN)
+                p.gcw = mul2(p.cw, rg[r].pair(i));
+            p.cn = mul2(p.gcw, p.n);
+            p.t = fma2(rh[r].pair(i), alpha, p.cn);
+            p.du = rdu[r].pair(i);
+            p.dv = mul2(p.du, w2s.v[i]);
+            return p;
+        };
+        auto row_weights = [&](int k, Vec<W> &cw, Vec<W> &w2) {
+            if constexpr (HOLD) {
+                cw = from_slot<W, false>(base + at(off_cw, kF, k));
+                w2 = from_slot<W, false>(base + at(off_w2, kF, k));
             } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    dt[j] = 0.0f;
+                weights(col_of(k), cw, w2);
             }
         };
 
-        float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        f2 q0 = both(0.0f), q1 = q0, q2 = q0, q3 = q0;
 #pragma unroll
-        for (int c = 0; c < J; ++c) {
-            if ((c * T + t) * 8 < N) {
-                float n[8], tt[8], du[8], cw[8], w2[8], gt[8], dt[8];
-                load(c, n, tt, du, cw, w2, gt);
-                stream_grad(c, dt);
+        for (int k = 0; k < U; ++k) {
+            if (col_of(k) < N) {
+                read(k);
+                Vec<W> cw, w2;
+                row_weights(k, cw, w2);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float dv = du[j] * w2[j], cn = cw[j] * gt[j] * n[j];
-                    q.x = fmaf(dv, tt[j], q.x);
-                    q.y = fmaf(cn, dt[j], q.y);
-                    q.z = fmaf(cn, dv, q.z);
-                    q.w = fmaf(cn, tt[j], q.w);
+                for (int i = 0; i < W / 2; ++i) {
+                    const Pair p = form(k, i, cw, w2);
+                    q0 = fma2(p.dv, p.t, q0);
+                    q1 = fma2(p.cn, rdt[HOLD ? k : 0].pair(i), q1);
+                    q2 = fma2(p.cn, p.dv, q2);
+                    q3 = fma2(p.cn, p.t, q3);
                 }
             }
         }
-        float k = 0.0f, mean1 = 0.0f;
+        if constexpr (HOLD) {
+            if (ahead < a.M)
+                fetch_row(ahead, st);
+            cp_async_commit();
+        }
+        float kk = 0.0f, mean1 = 0.0f;
         if (pre || post) {
-            q.x = warp_sum(q.x);
-            q.y = warp_sum(q.y);
-            q.z = warp_sum(q.z);
-            q.w = warp_sum(q.w);
-            float4 *buf = red[turn];
+            // as in encode_units: lane l ends with sum l >> 3 of its warp
+            const bool up = lane & 16, up2 = lane & 8;
+            float s0 = lo2(q0) + hi2(q0), s1w = lo2(q1) + hi2(q1), s2w = lo2(q2) + hi2(q2), s3 = lo2(q3) + hi2(q3);
+            const float k0 = (up ? s2w : s0) + __shfl_xor_sync(0xFFFFFFFFu, up ? s0 : s2w, 16);
+            const float k1 = (up ? s3 : s1w) + __shfl_xor_sync(0xFFFFFFFFu, up ? s1w : s3, 16);
+            float s = (up2 ? k1 : k0) + __shfl_xor_sync(0xFFFFFFFFu, up2 ? k0 : k1, 8);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1)
+                s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+            float(*buf)[4] = red[turn];
             turn ^= 1;
-            if (lane == 0)
-                buf[t >> 5] = q;
+            if ((lane & 7) == 0)
+                buf[t >> 5][lane >> 3] = s;
             __syncthreads();
-            // lane l: sum l & 3 over the warps l >> 2, + 8, ...
-            float s = 0.0f;
-            for (int w = lane >> 2; w < (T >> 5); w += 8)
-                s += reinterpret_cast<const float *>(buf + w)[lane & 3];
+            // lane l: sum l & 3 of the warps l >> 2 and l >> 2 + 8
+            const int w0 = lane >> 2, warps = T >> 5;
+            s = (w0 < warps ? buf[w0][lane & 3] : 0.0f) + (w0 + 8 < warps ? buf[w0 + 8][lane & 3] : 0.0f);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1)
                 s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
             s *= inv_n;
-            k = pre ? r2 * r2 * r2 * __shfl_sync(0xFFFFFFFFu, s, 0) : 0.0f;
+            kk = !pre ? 0.0f : r2s * r2s * r2s * __shfl_sync(0xFFFFFFFFu, s, 0);
             const float m_dt = __shfl_sync(0xFFFFFFFFu, s, 1), m_dv = __shfl_sync(0xFFFFFFFFu, s, 2),
                         m_t = __shfl_sync(0xFFFFFFFFu, s, 3);
-            mean1 = post ? (pre ? fmaf(r2, m_dv, m_dt) - k * m_t : m_dt) : 0.0f;
+            mean1 = post ? fmaf(r2s, m_dv, m_dt) - kk * m_t : 0.0f;
         }
+        const f2 mk = both(-kk), mm = both(-r1s * mean1);
 #pragma unroll
-        for (int c = 0; c < J; ++c) {
-            const int col = (c * T + t) * 8;
+        for (int k = 0; k < U; ++k) {
+            const int col = col_of(k), r = HOLD ? k : 0;
             if (col < N) {
-                float n[8], tt[8], du[8], cw[8], w2[8], gt[8], d[8], o[8];
-                load(c, n, tt, du, cw, w2, gt);
-                stream_grad(c, d);
+                if constexpr (!HOLD)
+                    read(k);
+                Vec<W> cw, w2, d = rdt[r].vec(), dy, dg;
+                row_weights(k, cw, w2);
+                // (a norm that is absent must not bring its row's infinities in as 0 * inf)
+                if (pre) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (pre)
-                        d[j] += r2 * (du[j] * w2[j]) - k * tt[j];
-                    s1[c][j] = fmaf(n[j] * gt[j], d[j], s1[c][j]);
-                    s2[c][j] = fmaf(du[j] * r2, tt[j], s2[c][j]);
-                    o[j] = r1 * (cw[j] * gt[j] * d[j] - n[j] * mean1);
-                }
-                store8<YB>(a.dy, m * N + col, o);
-                if (token && a.dgate) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        o[j] = cw[j] * n[j] * d[j];
-                    store8<true>(a.dgate, m * N + col, o);
+                    for (int i = 0; i < W / 2; ++i) {
+                        const Pair p = form(k, i, cw, w2);
+                        d.v[i] = fma2(p.t, mk, fma2(p.dv, r2, d.v[i]));
+                        s2[k].v[i] = fma2(mul2(p.du, r2), p.t, s2[k].v[i]);
+                    }
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    d[j] *= a.alpha;
-                store8<HB>(a.dh, m * N + col, d);
+                for (int i = 0; i < W / 2; ++i) {
+                    const Pair p = form(k, i, cw, w2);
+                    if constexpr (TOKEN) {
+                        const f2 nd = mul2(p.n, d.v[i]);
+                        dg.v[i] = mul2(p.cw, nd);
+                        s1[k].v[i] = fma2(nd, rg[r].pair(i), s1[k].v[i]);
+                    } else {
+                        s1[k].v[i] = fma2(p.n, d.v[i], s1[k].v[i]);
+                    }
+                    dy.v[i] = mul2(mul2(p.gcw, d.v[i]), r1);
+                }
+                if (post) {
+#pragma unroll
+                    for (int i = 0; i < W / 2; ++i)
+                        dy.v[i] = fma2(mul2(ry[r].pair(i), r1), mm, dy.v[i]);
+                }
+                store_vec<W, YB>(a.dy, m * N + col, dy);
+                store_vec<W, HB>(a.dh, m * N + col, d * alpha);
+                if constexpr (TOKEN) {
+                    if (a.dgate)
+                        store_vec<W, true>(a.dgate, m * N + col, dg);
+                }
             }
+        }
+        if constexpr (!HOLD) {
+            if (ahead < a.M)
+                fetch_row(ahead, st);
+            cp_async_commit();
         }
     }
     float *part = ws + (int64_t)blockIdx.x * 2 * N;
 #pragma unroll
-    for (int c = 0; c < J; ++c) {
-        const int col = (c * T + t) * 8;
+    for (int k = 0; k < U; ++k) {
+        const int col = col_of(k);
         if (col < N) {
-            store8<false>(part, col, s1[c]);
-            store8<false>(part, N + col, s2[c]);
+            store_vec<W, false>(part, col, s1[k]);
+            store_vec<W, false>(part, N + col, s2[k]);
         }
     }
 }
@@ -526,88 +779,96 @@ __global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const NormBwdArgs a, 
 
 // ---------------------------------------------------------------- launches
 
-struct Shape {
-    int threads, ctas_per_sm;
-};
-
 int round32(int v) { return (v + 31) / 32 * 32; }
 
-// Chunks a thread: 1, 2 or 4, the fewest that keep a row in `most` threads.
-int chunks(int N, int most1, int most2) { return N <= 8 * most1 ? 1 : N <= 16 * most2 ? 2 : 4; }
+constexpr int kWide = 8192;            // widest row of 16 columns a thread in 512 threads
+constexpr int kNormRing = 176 * 1024;  // of an SM: the rest of its shared memory is L1 for the weights
 
-// Stages of the ring that fit a CTA's share of the SM's shared memory.
-int ring_stages(int stage_bytes, int ctas_per_sm, int64_t rows)
+struct Plan {
+    int threads, per_sm;   // CTAs an SM
+};
+
+// As many CTAs an SM as fill `most` threads.
+Plan plan_rows(int N, int cols, int most)
 {
-    int s = (kMaxSmem / ctas_per_sm - 1024) / stage_bytes;
-    if (ctas_per_sm == 1)
-        s = kMaxSmem / stage_bytes;
+    const int threads = round32((N + cols - 1) / cols);
+    const int per_sm = most / threads;
+    return {threads, per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm};
+}
+
+// Stages of a CTA's ring: what its share of `room` holds.
+int ring_stages(int64_t room, int stage_bytes, int64_t rows)
+{
+    int64_t s = room / stage_bytes;
     s = s < 1 ? 1 : s > kMaxStages ? kMaxStages : s;
-    return rows < s ? (int)rows : s;
+    return (int)(rows < s ? rows : s);
 }
 
-Shape bwd_shape(int N)
-{
-    const int J = chunks(N, 256, 512);
-    const int threads = round32((N + 8 * J - 1) / (8 * J));
-    return {threads, J == 1 ? (threads <= 64 ? 12 : 768 / threads) : 1};
-}
+Plan plan_bwd(int N) { return plan_rows(N, N <= kWide ? 16 : 32, 512); }
 
 int bwd_ctas(int64_t M, int N, int num_sms)
 {
     // at least two rows a CTA, so that the parts never need more room than the rows themselves
-    const int64_t most = (int64_t)num_sms * bwd_shape(N).ctas_per_sm, some = (M + 1) / 2;
+    const int64_t most = (int64_t)num_sms * plan_bwd(N).per_sm, some = (M + 1) / 2;
     return (int)(some < most ? some : most);
 }
 
-template <int J, bool YB, bool HB>
-cudaError_t run_norm(const NormArgs &a, int threads, int num_sms, cudaStream_t st)
+// COLS columns a thread.
+template <int COLS, bool YB, bool HB>
+cudaError_t run_norm(const NormArgs &a, int num_sms, cudaStream_t st)
 {
-    const int stage_bytes = (J * (YB ? 1 : 2) + J * (HB ? 1 : 2) + (a.gate && a.gs ? J : 0)) * threads * 16;
-    int per_sm = J == 1 ? 1024 / threads : J == 2 ? 1024 / threads : 1;
-    per_sm = per_sm > 16 ? 16 : per_sm;
-    while (per_sm > 1 && stage_bytes * 2 > kMaxSmem / per_sm - 1024)
-        --per_sm;
-    const int64_t most = (int64_t)num_sms * per_sm;
+    constexpr int W = YB && HB ? 8 : 4;
+    const Plan p = plan_rows(a.N, COLS, 1024);
+    const int stage_bytes = p.threads * COLS * ((YB ? 2 : 4) + (HB ? 2 : 4) + (a.gate && a.gs ? 2 : 0));
+    const int64_t most = (int64_t)num_sms * p.per_sm;
     const int grid = (int)(a.M < most ? a.M : most);
-    const int stages = ring_stages(stage_bytes, per_sm, (a.M + grid - 1) / grid);
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(norm_kernel<J, YB, HB>), kMaxSmem);
+    const int stages = ring_stages(kNormRing / p.per_sm, stage_bytes, (a.M + grid - 1) / grid);
+    const auto kernel = norm_kernel<COLS / W, YB, HB>;
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), kMaxSmem);
     if (e != cudaSuccess)
         return e;
-    norm_kernel<J, YB, HB><<<grid, threads, stages * stage_bytes, st>>>(a, stages);
+    kernel<<<grid, p.threads, stages * stage_bytes, st>>>(a, stages);
     return cudaGetLastError();
 }
 
-template <int J>
+template <int COLS>
 cudaError_t pick_norm(const NormArgs &a, int num_sms, cudaStream_t st)
 {
-    const int threads = round32((a.N + 8 * J - 1) / (8 * J));
     if (a.y_bf16)
-        return a.h_bf16 ? run_norm<J, true, true>(a, threads, num_sms, st) : run_norm<J, true, false>(a, threads, num_sms, st);
-    return a.h_bf16 ? run_norm<J, false, true>(a, threads, num_sms, st) : run_norm<J, false, false>(a, threads, num_sms, st);
+        return a.h_bf16 ? run_norm<COLS, true, true>(a, num_sms, st) : run_norm<COLS, true, false>(a, num_sms, st);
+    return a.h_bf16 ? run_norm<COLS, false, true>(a, num_sms, st) : run_norm<COLS, false, false>(a, num_sms, st);
 }
 
-template <int J, bool YB, bool HB>
-cudaError_t run_norm_bwd(const NormBwdArgs &a, float *ws, int grid, Shape s, cudaStream_t st)
+template <int COLS, bool YB, bool HB, bool TOKEN>
+cudaError_t run_norm_bwd(const NormBwdArgs &a, float *ws, int grid, cudaStream_t st)
 {
-    const int units = J * ((YB ? 1 : 2) + 2 * (HB ? 1 : 2) + 1);
-    // a token's gate is staged with the row unless a single stage would not fit
-    const bool token = a.gate && a.gs;
-    const int staged = token && (units + J) * s.threads * 16 <= kMaxSmem / s.ctas_per_sm ? 1 : 0;
-    const int stage_bytes = (units + (staged ? J : 0)) * s.threads * 16;
-    const int stages = ring_stages(stage_bytes, s.ctas_per_sm, (a.M + grid - 1) / grid);
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(norm_bwd_kernel<J, YB, HB>), kMaxSmem);
+    constexpr int W = YB && HB ? 8 : 4;
+    constexpr bool kHold = COLS == 16;
+    const Plan p = plan_bwd(a.N);
+    const int cols = p.threads * COLS;
+    const int weight_bytes = kHold ? 2 * cols * 4 : 0;
+    const int bytes = cols * ((YB ? 2 : 4) + 2 * (HB ? 2 : 4) + 2);
+    // a token's gate is staged with the row unless one stage would not fit
+    const int staged = TOKEN && bytes + cols * 2 + weight_bytes <= kMaxSmem ? 1 : 0;
+    const int stage_bytes = bytes + (staged ? cols * 2 : 0);
+    const int64_t room = (p.per_sm == 1 ? kMaxSmem : kMaxSmem / p.per_sm - 2048) - weight_bytes;
+    const int stages = ring_stages(room, stage_bytes, (a.M + grid - 1) / grid);
+    const auto kernel = norm_bwd_kernel<COLS / W, YB, HB, TOKEN, kHold>;
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), kMaxSmem);
     if (e != cudaSuccess)
         return e;
-    norm_bwd_kernel<J, YB, HB><<<grid, s.threads, stages * stage_bytes, st>>>(a, ws, stages, staged);
+    kernel<<<grid, p.threads, stages * stage_bytes + weight_bytes, st>>>(a, ws, stages, staged);
     return cudaGetLastError();
 }
 
-template <int J>
-cudaError_t pick_norm_bwd(const NormBwdArgs &a, float *ws, int grid, Shape s, cudaStream_t st)
+template <int COLS, bool TOKEN>
+cudaError_t pick_norm_bwd(const NormBwdArgs &a, float *ws, int grid, cudaStream_t st)
 {
     if (a.y_bf16)
-        return a.h_bf16 ? run_norm_bwd<J, true, true>(a, ws, grid, s, st) : run_norm_bwd<J, true, false>(a, ws, grid, s, st);
-    return a.h_bf16 ? run_norm_bwd<J, false, true>(a, ws, grid, s, st) : run_norm_bwd<J, false, false>(a, ws, grid, s, st);
+        return a.h_bf16 ? run_norm_bwd<COLS, true, true, TOKEN>(a, ws, grid, st)
+                        : run_norm_bwd<COLS, true, false, TOKEN>(a, ws, grid, st);
+    return a.h_bf16 ? run_norm_bwd<COLS, false, true, TOKEN>(a, ws, grid, st)
+                    : run_norm_bwd<COLS, false, false, TOKEN>(a, ws, grid, st);
 }
 
 }  // namespace
@@ -616,18 +877,17 @@ int64_t norm_bwd_ws_floats(int64_t M, int N, int num_sms) { return (int64_t)bwd_
 
 cudaError_t launch_norm(const NormArgs &a, int num_sms, cudaStream_t st)
 {
-    // one chunk a thread for narrow rows, and for the few rows of a decode step
-    const int J = a.M <= num_sms ? chunks(a.N, 1024, 0) : chunks(a.N, 512, 512);
-    return J == 1 ? pick_norm<1>(a, num_sms, st) : J == 2 ? pick_norm<2>(a, num_sms, st) : pick_norm<4>(a, num_sms, st);
+    // 16 columns a thread, two CTAs an SM; 8 for narrow rows and for the few rows of a decode step
+    return a.N <= kWide / 2 || (a.N <= kWide && a.M <= num_sms) ? pick_norm<8>(a, num_sms, st)
+                                                               : pick_norm<16>(a, num_sms, st);
 }
 
 cudaError_t launch_norm_bwd(const NormBwdArgs &a, float *ws, int num_sms, cudaStream_t st)
 {
-    const int J = chunks(a.N, 256, 512), grid = bwd_ctas(a.M, a.N, num_sms);
-    const Shape s = bwd_shape(a.N);
-    const cudaError_t e = J == 1   ? pick_norm_bwd<1>(a, ws, grid, s, st)
-                          : J == 2 ? pick_norm_bwd<2>(a, ws, grid, s, st)
-                                   : pick_norm_bwd<4>(a, ws, grid, s, st);
+    const int grid = bwd_ctas(a.M, a.N, num_sms);
+    const bool token = a.gate && a.gs;
+    const cudaError_t e = a.N <= kWide ? (token ? pick_norm_bwd<16, true>(a, ws, grid, st) : pick_norm_bwd<16, false>(a, ws, grid, st))
+                                       : (token ? pick_norm_bwd<32, true>(a, ws, grid, st) : pick_norm_bwd<32, false>(a, ws, grid, st));
     if (e != cudaSuccess || (!a.dw1 && !a.dw2 && !(a.dgate && a.gs == 0)))
         return e;
     norm_bwd_sum_kernel<<<(a.N + 31) / 32, 256, 0, st>>>(a, ws, grid);
