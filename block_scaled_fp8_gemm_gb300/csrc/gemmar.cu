@@ -747,15 +747,13 @@ GEMMAR_API int lora_apply(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, 
         return rc;
     if (!aligned16(v))
         return GEMMAR_ERR_ALIGN;
-    if (T * r + lora_ws_floats(T, r) > ctx->W_floats)
+    const LoraPlan p = lora_plan_call(T, (int)K, R, r, ctx->num_sms);
+    if (p.part_floats > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
     cudaStream_t st = as_stream(stream);
     const LoraArgs l{order, offsets, ranks, scales, T, R, r};
-    float *ws = ctx->W + (T * r + 3) / 4 * 4;
-    if (v == nullptr)
-        v = ctx->W;
-    CUDA_OK(launch_lora_down(l, x, x_stride, A, (int)K, false, v, ws, ctx->num_sms, st));
-    CUDA_OK(launch_lora_up(l, v, B, (int)N, true, y, y_stride, out, out_stride, ws, ctx->num_sms, st));
+    CUDA_OK(launch_lora_down(l, p, x, x_stride, A, (int)K, false, ctx->W, st));
+    CUDA_OK(launch_lora_up(l, p, ctx->W, B, (int)N, true, y, y_stride, out, out_stride, v, st));
     return GEMMAR_OK;
 }
 
@@ -776,15 +774,17 @@ GEMMAR_API int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stri
         return rc;
     if (!aligned16(v) || !aligned16(dA) || !aligned16(dB))
         return GEMMAR_ERR_ALIGN;
-    if (T * r + lora_ws_floats(T, r) > ctx->W_floats)
+    const LoraPlan p = lora_plan_call(T, (int)N, R, r, ctx->num_sms);
+    const int64_t w_floats = (T * r + 3) / 4 * 4;
+    if (w_floats + p.part_floats > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
     cudaStream_t st = as_stream(stream);
     const LoraArgs l{order, offsets, ranks, scales, T, R, r};
-    float *w = ctx->W, *ws = ctx->W + (T * r + 3) / 4 * 4;
-    CUDA_OK(launch_lora_down(l, dy, dy_stride, B, (int)N, true, w, ws, ctx->num_sms, st));
-    CUDA_OK(launch_lora_up(l, w, A, (int)K, false, dx0, dx0_stride, dx, dx_stride, ws, ctx->num_sms, st));
-    CUDA_OK(launch_lora_grad(l, w, x, x_stride, (int)K, false, dA, ws, ctx->num_sms, st));
-    CUDA_OK(launch_lora_grad(l, v, dy, dy_stride, (int)N, true, dB, ws, ctx->num_sms, st));
+    float *w = ctx->W, *part = ctx->W + w_floats;
+    CUDA_OK(launch_lora_down(l, p, dy, dy_stride, B, (int)N, true, part, st));
+    CUDA_OK(launch_lora_up(l, p, part, A, (int)K, false, dx0, dx0_stride, dx, dx_stride, w, st));
+    CUDA_OK(launch_lora_grad(l, w, x, x_stride, (int)K, false, dA, st));
+    CUDA_OK(launch_lora_grad(l, v, dy, dy_stride, (int)N, true, dB, st));
     return GEMMAR_OK;
 }
 

@@ -200,16 +200,22 @@ struct LoraArgs {
     int R, r;
 };
 cudaError_t launch_lora_plan(const int32_t *ids, int64_t T, int R, int32_t *order, int32_t *offsets, cudaStream_t st);
-// v[i,j] = f sum_c x[order[i],c] W[a,j,c], f = scales[a] if scaled, else 1
-int64_t lora_ws_floats(int64_t T, int r);
-cudaError_t launch_lora_down(const LoraArgs &l, const uint16_t *x, int64_t xs, const uint16_t *W, int C, bool scaled,
-                             float *v, float *ws, int num_sms, cudaStream_t st);
-// out[t,c] = base[t,c] + f sum_j v[i,j] W[a,j,c]; rows without an adapter: base
-cudaError_t launch_lora_up(const LoraArgs &l, const float *v, const uint16_t *W, int C, bool scaled,
-                           const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *ws, int num_sms,
+// How a call of T tokens is cut: the parts that the sums over C_down columns come in.
+struct LoraPlan {
+    int splits;
+    int64_t part_floats;   // splits * T * r
+};
+LoraPlan lora_plan_call(int64_t T, int C_down, int R, int r, int num_sms);
+// part[s][i][j], summed over s: f sum_c x[order[i],c] W[a,j,c], f = scales[a] if scaled, else 1
+cudaError_t launch_lora_down(const LoraArgs &l, const LoraPlan &p, const uint16_t *x, int64_t xs, const uint16_t *W,
+                             int C, bool scaled, float *part, cudaStream_t st);
+// out[t,c] = base[t,c] + f sum_j v[i,j] W[a,j,c] with v the sum of the parts, also written to v
+// (may be nullptr); rows without an adapter: base
+cudaError_t launch_lora_up(const LoraArgs &l, const LoraPlan &p, const float *part, const uint16_t *W, int C,
+                           bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *v,
                            cudaStream_t st);
 // G[a,j,c] = f sum_{tokens of a} p[i,j] x[order[i],c]
 cudaError_t launch_lora_grad(const LoraArgs &l, const float *p, const uint16_t *x, int64_t xs, int C, bool scaled,
-                             uint16_t *G, float *ws, int num_sms, cudaStream_t st);
+                             uint16_t *G, cudaStream_t st);
 
 }  // namespace gemmar

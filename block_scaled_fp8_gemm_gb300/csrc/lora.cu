@@ -7,6 +7,9 @@
 // with t = order[i], i in [offsets[a], offsets[a+1]), f = scales[a] or 1.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
+#include "gemmar.h"
 #include "kernels.h"
 
 namespace gemmar {
@@ -16,20 +19,6 @@ namespace {
 
 __device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 __device__ __forceinline__ uint16_t to_bf(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
-
-// Adapter of position i: the a with offsets[a] <= i < offsets[a+1]; R past offsets[R].
-__device__ __forceinline__ int adapter_of(const int32_t *__restrict__ offsets, int R, int64_t i)
-{
-    int lo = 0, hi = R;
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (offsets[mid + 1] > i)
-            hi = mid;
-        else
-            lo = mid + 1;
-    }
-    return lo;
-}
 
 __device__ __forceinline__ int rank_of(const LoraArgs &l, int a)
 {
@@ -112,44 +101,287 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t *__restri
     }
 }
 
-__global__ void __launch_bounds__(128) down_kernel(const LoraArgs l, const uint16_t *__restrict__ x, int64_t xs,
-                                                   const uint16_t *__restrict__ W, int C, bool scaled,
-                                                   float *__restrict__ v)
+// A CTA's share of the tokens: positions [i0, i0 + count) of adapter a (a == R:
+// tokens without one).
+struct Tile {
+    int a, i0, count;
+};
+
+// Tile number `want` when every adapter's tokens (and, with `bare`, those without
+// one) are cut into tiles of `size`; count 0 past the last.  Warp-collective: lane l
+// counts the tiles of a contiguous share of the adapters, a scan finds the lane.
+__device__ __forceinline__ Tile find_tile(const LoraArgs &l, int want, int size, bool bare)
 {
-    const int64_t i = blockIdx.x;
-    const int a = adapter_of(l.offsets, l.R, i), t = l.order[i];
-    if (a >= l.R || t < 0 || t >= l.T)
-        return;
-    const int rank = rank_of(l, a), lane = threadIdx.x & 31;
-    for (int j = threadIdx.x >> 5; j < l.r; j += 4) {
-        float s = 0.0f;
-        if (j < rank)
-            for (int c = lane; c < C; c += 32)
-                s += bf(x[t * xs + c]) * bf(W[((int64_t)a * l.r + j) * C + c]);
+    const int lane = threadIdx.x & 31, groups = l.R + (bare ? 1 : 0), T = (int)l.T;
+    const int per = (groups + 31) / 32, g0 = min(lane * per, groups), g1 = min(g0 + per, groups);
+    auto edge = [&](int g) { return g > l.R ? T : min(max(__ldg(l.offsets + g), 0), T); };
+    int tiles = 0, at = edge(g0);
+    for (int g = g0; g < g1; ++g) {
+        const int next = edge(g + 1);
+        tiles += (max(next - at, 0) + size - 1) / size;
+        at = next;
+    }
+    int before = tiles;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        if (lane == 0)
-            v[i * l.r + j] = scaled ? s * l.scales[a] : s;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xFFFFFFFFu, before, o);
+        if (lane >= o)
+            before += up;
+    }
+    before -= tiles;
+    const unsigned here = __ballot_sync(0xFFFFFFFFu, want >= before && want < before + tiles);
+    Tile t{0, 0, 0};
+    if (here == 0u)
+        return t;
+    const int owner = __ffs(here) - 1;
+    if (lane == owner) {
+        int rest = want - before;
+        at = edge(g0);
+        for (int g = g0; g < g1; ++g) {
+            const int next = edge(g + 1), n = (max(next - at, 0) + size - 1) / size;
+            if (rest < n) {
+                t.a = g;
+                t.i0 = at + rest * size;
+                t.count = min(size, next - t.i0);
+                break;
+            }
+            rest -= n;
+            at = next;
+        }
+    }
+    t.a = __shfl_sync(0xFFFFFFFFu, t.a, owner);
+    t.i0 = __shfl_sync(0xFFFFFFFFu, t.i0, owner);
+    t.count = __shfl_sync(0xFFFFFFFFu, t.count, owner);
+    return t;
+}
+
+// Most tiles of `size` that T tokens of R adapters (and the bare ones) can make.
+int64_t most_tiles(int64_t T, int R, int size, bool bare)
+{
+    const int64_t groups = R + (bare ? 1 : 0);
+    return T / size + (groups < T ? groups : T);
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ---------------------------------------------------------------- few tokens
+//
+// A decode batch: every adapter in it brings its weights for a token or a few, so
+// the weights are what is read, and latency is what counts.  Both kernels load
+// their fragments straight from memory into registers, 16 bytes a lane, no
+// staging: the contraction index of an MMA may be permuted as long as both
+// operands agree, so lane (g, q) takes eight consecutive elements of its row for
+// two MMAs.  Weights are the M operand, tokens the N operand (8 a tile).
+
+constexpr int kFewTokens = 32;   // tokens a tile: four N tiles
+constexpr int kFewWarps = 8;
+constexpr int kFewRanks = 32;    // ranks a CTA of the down kernel: two M tiles
+
+// part[s][i][j] of split s: sums over its share of the columns.  The CTA's eight
+// warps share that again, and their sums meet in shared memory in warp order.
+__global__ void __launch_bounds__(kFewWarps * 32) few_down_kernel(const LoraArgs l, const uint16_t *__restrict__ x,
+                                                                  int64_t xs, const uint16_t *__restrict__ W, int C,
+                                                                  bool scaled, float *__restrict__ part)
+{
+    __shared__ float sums[kFewWarps][kFewRanks][kFewTokens + 1];
+    const Tile tile = find_tile(l, blockIdx.y, kFewTokens, false);
+    const int rank = tile.count ? rank_of(l, tile.a) : 0, j0 = blockIdx.z * kFewRanks;
+    if (tile.count == 0)
+        return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    float acc[2][4][4] = {};
+    if (j0 < rank) {
+        const uint16_t *wr[4];   // rows j0 + g, + 8, + 16, + 24
+        bool wok[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = j0 + g + 8 * i;
+            wok[i] = j < rank;
+            wr[i] = W + ((int64_t)tile.a * l.r + (wok[i] ? j : 0)) * C + q * 8;
+        }
+        const int nt = (tile.count + 7) / 8;
+        const uint16_t *xr[4];
+        bool xok[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int i = n * 8 + g;
+            const int t = i < tile.count ? __ldg(l.order + tile.i0 + i) : -1;
+            xok[n] = t >= 0 && t < l.T;
+            xr[n] = x + (xok[n] ? t : 0) * xs + q * 8;
+        }
+        // blocks of 32 columns, dealt evenly to splits and warps
+        const int blocks = (C + 31) / 32, shares = gridDim.x * kFewWarps, share = blockIdx.x * kFewWarps + warp;
+        const int b0 = (int)((int64_t)blocks * share / shares), b1 = (int)((int64_t)blocks * (share + 1) / shares);
+        const bool wide = j0 + 16 < rank;
+#pragma unroll 4
+        for (int b = b0; b < b1; ++b) {
+            const bool in = b * 32 + q * 8 < C;
+            uint4 w[4], v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = make_uint4(0, 0, 0, 0);
+                if (in && wok[i])
+                    w[i] = __ldg(reinterpret_cast<const uint4 *>(wr[i] + b * 32));
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                v[n] = make_uint4(0, 0, 0, 0);
+                if (in && xok[n])
+                    v[n] = __ldg(reinterpret_cast<const uint4 *>(xr[n] + b * 32));
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                if (m == 1 && !wide)
+                    break;
+                const uint32_t lo[4] = {w[2 * m].x, w[2 * m + 1].x, w[2 * m].y, w[2 * m + 1].y};
+                const uint32_t hi[4] = {w[2 * m].z, w[2 * m + 1].z, w[2 * m].w, w[2 * m + 1].w};
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    if (n < nt) {
+                        mma_bf16(acc[m][n], lo, v[n].x, v[n].y);
+                        mma_bf16(acc[m][n], hi, v[n].z, v[n].w);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sums[warp][m * 16 + g + (e >> 1) * 8][n * 8 + q * 2 + (e & 1)] = acc[m][n][e];
+    __syncthreads();
+    const float f = scaled ? l.scales[tile.a] : 1.0f;
+    float *out = part + ((int64_t)blockIdx.x * l.T + tile.i0) * l.r;
+    const int nj = min(kFewRanks, l.r - j0);
+    for (int e = threadIdx.x; e < tile.count * nj; e += kFewWarps * 32) {
+        const int i = e / nj, j = e - i * nj;
+        float s = sums[0][j][i];
+#pragma unroll
+        for (int w = 1; w < kFewWarps; ++w)
+            s += sums[w][j][i];
+        out[(int64_t)i * l.r + j0 + j] = f * s;
     }
 }
 
-__global__ void __launch_bounds__(128) up_kernel(const LoraArgs l, const float *__restrict__ v,
-                                                 const uint16_t *__restrict__ W, int C, bool scaled,
-                                                 const uint16_t *base, int64_t bs, uint16_t *out, int64_t os)
+// out rows of a tile, 64 columns a warp.  The splits' parts are summed in their
+// order, and the sum enters as two bf16 parts.  D[n, token] = sum_j W[j, n] v[token, j]:
+// an MMA's two row halves are the even and odd columns of a lane's eight, so the
+// lane ends with eight consecutive columns of two tokens.
+constexpr int kFewCols = 64 * kFewWarps;
+
+__global__ void __launch_bounds__(kFewWarps * 32) few_up_kernel(const LoraArgs l, const float *__restrict__ part,
+                                                                int splits, const uint16_t *__restrict__ W, int C,
+                                                                bool scaled, const uint16_t *base, int64_t bs,
+                                                                uint16_t *out, int64_t os, float *v_out)
 {
-    const int64_t i = blockIdx.x;
-    const int a = adapter_of(l.offsets, l.R, i), t = l.order[i];
-    if (t < 0 || t >= l.T || (a >= l.R && base == out))
+    constexpr int kRow = GEMMAR_LORA_MAX_RANK / 2 + 4;   // pairs of a token, padded off the banks
+    __shared__ uint32_t hi[kFewTokens][kRow], lo[kFewTokens][kRow];
+    const Tile tile = find_tile(l, blockIdx.y, kFewTokens, base != out);
+    if (tile.count == 0)
         return;
-    const int rank = a < l.R ? rank_of(l, a) : 0;
-    const float f = scaled && a < l.R ? l.scales[a] : 1.0f;
-    for (int c = threadIdx.x; c < C; c += 128) {
-        float s = 0.0f;
-        for (int j = 0; j < rank; ++j)
-            s += v[i * l.r + j] * bf(W[((int64_t)a * l.r + j) * C + c]);
-        const float y = base ? bf(base[t * bs + c]) : 0.0f;
-        out[t * os + c] = to_bf(rank ? y + f * s : y);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int rank = tile.a < l.R ? rank_of(l, tile.a) : 0, steps = (rank + 15) / 16;
+    const int n0 = blockIdx.x * kFewCols + warp * 64 + g * 8;
+    const bool in = n0 < C;
+    const uint16_t *w0 = W + (int64_t)min(tile.a, l.R - 1) * l.r * C + n0;
+    auto load = [&](int s, uint4 (&w)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = s * 16 + q * 2 + (i & 1) + (i >> 1) * 8;
+            w[i] = make_uint4(0, 0, 0, 0);
+            if (in && j < rank)
+                w[i] = __ldg(reinterpret_cast<const uint4 *>(w0 + (int64_t)j * C));
+        }
+    };
+    uint4 w[4];
+    load(0, w);   // in flight while the parts are summed
+    const int pairs = steps * 8;
+    for (int e = threadIdx.x; e < kFewTokens * pairs; e += kFewWarps * 32) {
+        const int i = e / pairs, p = e - i * pairs;
+        float v[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int j = 2 * p + k;
+            if (i < tile.count && j < rank) {
+                const float *src = part + (int64_t)(tile.i0 + i) * l.r + j;
+                for (int s = 0; s < splits; ++s)
+                    v[k] += src[(int64_t)s * l.T * l.r];
+            }
+        }
+        const uint32_t h = bf16x2_from_f32(v[0], v[1]);
+        hi[i][p] = h;
+        lo[i][p] = bf16x2_from_f32(v[0] - __uint_as_float(h << 16), v[1] - __uint_as_float(h & 0xFFFF0000u));
+        if (v_out && blockIdx.x == 0 && i < tile.count) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (2 * p + k < l.r)
+                    v_out[(int64_t)(tile.i0 + i) * l.r + 2 * p + k] = v[k];
+        }
+    }
+    if (v_out && blockIdx.x == 0 && tile.a < l.R) {   // columns past the rank's last step
+        const int rest = l.r - pairs * 2;
+        for (int e = threadIdx.x; e < tile.count * rest; e += kFewWarps * 32)
+            v_out[(int64_t)(tile.i0 + e / rest) * l.r + pairs * 2 + e % rest] = 0.0f;
+    }
+    __syncthreads();
+    float acc[4][4][4] = {};   // column pair, token tile, fragment
+    const int nt = (tile.count + 7) / 8;
+    for (int s = 0; s < steps; ++s) {
+        uint4 next[4];
+        load(s + 1, next);
+        const uint32_t rows[4][4] = {{w[0].x, w[0].y, w[0].z, w[0].w}, {w[1].x, w[1].y, w[1].z, w[1].w},
+                                     {w[2].x, w[2].y, w[2].z, w[2].w}, {w[3].x, w[3].y, w[3].z, w[3].w}};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            if (n < nt) {
+                const int i = n * 8 + g;
+                const uint32_t h0 = hi[i][s * 8 + q], h1 = hi[i][s * 8 + 4 + q];
+                const uint32_t l0 = lo[i][s * 8 + q], l1 = lo[i][s * 8 + 4 + q];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t a[4] = {__byte_perm(rows[0][c], rows[1][c], 0x5410), __byte_perm(rows[0][c], rows[1][c], 0x7632),
+                                           __byte_perm(rows[2][c], rows[3][c], 0x5410), __byte_perm(rows[2][c], rows[3][c], 0x7632)};
+                    mma_bf16(acc[c][n], a, h0, h1);
+                    mma_bf16(acc[c][n], a, l0, l1);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = next[i];
+    }
+    if (!in)
+        return;
+    const float f = scaled && tile.a < l.R ? l.scales[tile.a] : 1.0f;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = n * 8 + q * 2 + k;
+            const int t = i < tile.count ? __ldg(l.order + tile.i0 + i) : -1;
+            if (t < 0 || t >= l.T)
+                continue;
+            uint4 y = make_uint4(0, 0, 0, 0);
+            if (base)
+                y = *reinterpret_cast<const uint4 *>(base + t * bs + n0);
+            if (rank > 0) {
+                uint32_t *yw = reinterpret_cast<uint32_t *>(&y);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    yw[c] = bf16x2_from_f32(fmaf(f, acc[c][n][k], __uint_as_float(yw[c] << 16)),
+                                            fmaf(f, acc[c][n][2 + k], __uint_as_float(yw[c] & 0xFFFF0000u)));
+            }
+            *reinterpret_cast<uint4 *>(out + t * os + n0) = y;
+        }
     }
 }
 
@@ -184,8 +416,6 @@ __global__ void __launch_bounds__(128) grad_kernel(const LoraArgs l, const float
 
 }  // namespace
 
-int64_t lora_ws_floats(int64_t, int) { return 0; }
-
 cudaError_t launch_lora_plan(const int32_t *ids, int64_t T, int R, int32_t *order, int32_t *offsets, cudaStream_t st)
 {
     const int smem = (32 * (R + 1) + 32) * (int)sizeof(int);
@@ -199,22 +429,36 @@ cudaError_t launch_lora_plan(const int32_t *ids, int64_t T, int R, int32_t *orde
     return cudaGetLastError();
 }
 
-cudaError_t launch_lora_down(const LoraArgs &l, const uint16_t *x, int64_t xs, const uint16_t *W, int C, bool scaled,
-                             float *v, float *, int, cudaStream_t st)
+LoraPlan lora_plan_call(int64_t T, int C_down, int R, int r, int num_sms)
 {
-    down_kernel<<<(unsigned)l.T, 128, 0, st>>>(l, x, xs, W, C, scaled, v);
+    LoraPlan p;
+    // two CTAs an SM, a block of 32 columns a warp at least
+    const int64_t ctas = most_tiles(T, R, kFewTokens, false) * ((r + kFewRanks - 1) / kFewRanks);
+    const int64_t want = 2 * (int64_t)num_sms / ctas, most = (C_down + 31) / 32 / kFewWarps;
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 16}));
+    p.part_floats = (int64_t)p.splits * T * r;
+    return p;
+}
+
+cudaError_t launch_lora_down(const LoraArgs &l, const LoraPlan &p, const uint16_t *x, int64_t xs, const uint16_t *W,
+                             int C, bool scaled, float *part, cudaStream_t st)
+{
+    const dim3 grid(p.splits, (unsigned)most_tiles(l.T, l.R, kFewTokens, false), (l.r + kFewRanks - 1) / kFewRanks);
+    few_down_kernel<<<grid, kFewWarps * 32, 0, st>>>(l, x, xs, W, C, scaled, part);
     return cudaGetLastError();
 }
 
-cudaError_t launch_lora_up(const LoraArgs &l, const float *v, const uint16_t *W, int C, bool scaled,
-                           const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *, int, cudaStream_t st)
+cudaError_t launch_lora_up(const LoraArgs &l, const LoraPlan &p, const float *part, const uint16_t *W, int C,
+                           bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *v,
+                           cudaStream_t st)
 {
-    up_kernel<<<(unsigned)l.T, 128, 0, st>>>(l, v, W, C, scaled, base, bs, out, os);
+    const dim3 grid((C + kFewCols - 1) / kFewCols, (unsigned)most_tiles(l.T, l.R, kFewTokens, base != out));
+    few_up_kernel<<<grid, kFewWarps * 32, 0, st>>>(l, part, p.splits, W, C, scaled, base, bs, out, os, v);
     return cudaGetLastError();
 }
 
 cudaError_t launch_lora_grad(const LoraArgs &l, const float *p, const uint16_t *x, int64_t xs, int C, bool scaled,
-                             uint16_t *G, float *, int, cudaStream_t st)
+                             uint16_t *G, cudaStream_t st)
 {
     grad_kernel<<<dim3((C + 127) / 128, l.R), 128, 0, st>>>(l, p, x, xs, C, scaled, G);
     return cudaGetLastError();
