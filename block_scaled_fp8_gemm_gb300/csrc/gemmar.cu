@@ -747,7 +747,7 @@ GEMMAR_API int lora_apply(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, 
         return rc;
     if (!aligned16(v))
         return GEMMAR_ERR_ALIGN;
-    const LoraPlan p = lora_plan_call(T, (int)K, R, r, ctx->num_sms);
+    const LoraPlan p = lora_plan_call(T, (int)K, R, r, ctx->num_sms, ctx->status, ctx->timeout_ns);
     if (p.part_floats > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
     cudaStream_t st = as_stream(stream);
@@ -774,7 +774,7 @@ GEMMAR_API int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stri
         return rc;
     if (!aligned16(v) || !aligned16(dA) || !aligned16(dB))
         return GEMMAR_ERR_ALIGN;
-    const LoraPlan p = lora_plan_call(T, (int)N, R, r, ctx->num_sms);
+    const LoraPlan p = lora_plan_call(T, (int)N, R, r, ctx->num_sms, ctx->status, ctx->timeout_ns);
     const int64_t w_floats = (T * r + 3) / 4 * 4;
     if (w_floats + p.part_floats > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;

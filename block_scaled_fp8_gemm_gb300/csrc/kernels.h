@@ -200,12 +200,24 @@ struct LoraArgs {
     int R, r;
 };
 cudaError_t launch_lora_plan(const int32_t *ids, int64_t T, int R, int32_t *order, int32_t *offsets, cudaStream_t st);
-// How a call of T tokens is cut: the parts that the sums over C_down columns come in.
+// How a call is cut: few tokens go to the kernels that load straight into registers
+// (lora.cu), many to the tiles on the tensor cores (lora_tile.cu); the sums over
+// C_down columns come in `splits` parts.
 struct LoraPlan {
+    bool tiled;
     int splits;
     int64_t part_floats;   // splits * T * r
+    int num_sms;
+    ptx::DevStatus *status;
+    uint64_t timeout_ns;
 };
-LoraPlan lora_plan_call(int64_t T, int C_down, int R, int r, int num_sms);
+LoraPlan lora_plan_call(int64_t T, int C_down, int R, int r, int num_sms, ptx::DevStatus *status, uint64_t timeout_ns);
+int lora_tile_splits(int64_t T, int C, int num_sms);
+cudaError_t launch_tile_down(const LoraArgs &l, const LoraPlan &p, const uint16_t *x, int64_t xs, const uint16_t *W,
+                             int C, bool scaled, float *part, cudaStream_t st);
+cudaError_t launch_tile_up(const LoraArgs &l, const LoraPlan &p, const float *part, const uint16_t *W, int C,
+                           bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *v,
+                           cudaStream_t st);
 // part[s][i][j], summed over s: f sum_c x[order[i],c] W[a,j,c], f = scales[a] if scaled, else 1
 cudaError_t launch_lora_down(const LoraArgs &l, const LoraPlan &p, const uint16_t *x, int64_t xs, const uint16_t *W,
                              int C, bool scaled, float *part, cudaStream_t st);

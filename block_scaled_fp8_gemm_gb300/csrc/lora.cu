@@ -10,7 +10,7 @@
 #include <algorithm>
 
 #include "gemmar.h"
-#include "kernels.h"
+#include "lora.cuh"
 
 namespace gemmar {
 using namespace ptx;
@@ -19,11 +19,6 @@ namespace {
 
 __device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 __device__ __forceinline__ uint16_t to_bf(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
-
-__device__ __forceinline__ int rank_of(const LoraArgs &l, int a)
-{
-    return l.ranks ? min(max(l.ranks[a], 0), l.r) : l.r;
-}
 
 // Counting sort by adapter in one CTA of 32 warps: a warp counts its contiguous
 // share of the tokens per adapter, the counts are summed over adapters and
@@ -101,67 +96,6 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t *__restri
     }
 }
 
-// A CTA's share of the tokens: positions [i0, i0 + count) of adapter a (a == R:
-// tokens without one).
-struct Tile {
-    int a, i0, count;
-};
-
-// Tile number `want` when every adapter's tokens (and, with `bare`, those without
-// one) are cut into tiles of `size`; count 0 past the last.  Warp-collective: lane l
-// counts the tiles of a contiguous share of the adapters, a scan finds the lane.
-__device__ __forceinline__ Tile find_tile(const LoraArgs &l, int want, int size, bool bare)
-{
-    const int lane = threadIdx.x & 31, groups = l.R + (bare ? 1 : 0), T = (int)l.T;
-    const int per = (groups + 31) / 32, g0 = min(lane * per, groups), g1 = min(g0 + per, groups);
-    auto edge = [&](int g) { return g > l.R ? T : min(max(__ldg(l.offsets + g), 0), T); };
-    int tiles = 0, at = edge(g0);
-    for (int g = g0; g < g1; ++g) {
-        const int next = edge(g + 1);
-        tiles += (max(next - at, 0) + size - 1) / size;
-        at = next;
-    }
-    int before = tiles;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xFFFFFFFFu, before, o);
-        if (lane >= o)
-            before += up;
-    }
-    before -= tiles;
-    const unsigned here = __ballot_sync(0xFFFFFFFFu, want >= before && want < before + tiles);
-    Tile t{0, 0, 0};
-    if (here == 0u)
-        return t;
-    const int owner = __ffs(here) - 1;
-    if (lane == owner) {
-        int rest = want - before;
-        at = edge(g0);
-        for (int g = g0; g < g1; ++g) {
-            const int next = edge(g + 1), n = (max(next - at, 0) + size - 1) / size;
-            if (rest < n) {
-                t.a = g;
-                t.i0 = at + rest * size;
-                t.count = min(size, next - t.i0);
-                break;
-            }
-            rest -= n;
-            at = next;
-        }
-    }
-    t.a = __shfl_sync(0xFFFFFFFFu, t.a, owner);
-    t.i0 = __shfl_sync(0xFFFFFFFFu, t.i0, owner);
-    t.count = __shfl_sync(0xFFFFFFFFu, t.count, owner);
-    return t;
-}
-
-// Most tiles of `size` that T tokens of R adapters (and the bare ones) can make.
-int64_t most_tiles(int64_t T, int R, int size, bool bare)
-{
-    const int64_t groups = R + (bare ? 1 : 0);
-    return T / size + (groups < T ? groups : T);
-}
-
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm volatile(
@@ -179,6 +113,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 // operands agree, so lane (g, q) takes eight consecutive elements of its row for
 // two MMAs.  Weights are the M operand, tokens the N operand (8 a tile).
 
+constexpr int kFewBatch = 256;   // largest batch for these kernels
 constexpr int kFewTokens = 32;   // tokens a tile: four N tiles
 constexpr int kFewWarps = 8;
 constexpr int kFewRanks = 32;    // ranks a CTA of the down kernel: two M tiles
@@ -429,9 +364,14 @@ cudaError_t launch_lora_plan(const int32_t *ids, int64_t T, int R, int32_t *orde
     return cudaGetLastError();
 }
 
-LoraPlan lora_plan_call(int64_t T, int C_down, int R, int r, int num_sms)
+LoraPlan lora_plan_call(int64_t T, int C_down, int R, int r, int num_sms, DevStatus *status, uint64_t timeout_ns)
 {
-    LoraPlan p;
+    LoraPlan p{T > kFewBatch, 1, 0, num_sms, status, timeout_ns};
+    if (p.tiled) {
+        p.splits = lora_tile_splits(T, C_down, num_sms);
+        p.part_floats = (int64_t)p.splits * T * r;
+        return p;
+    }
     // two CTAs an SM, a block of 32 columns a warp at least
     const int64_t ctas = most_tiles(T, R, kFewTokens, false) * ((r + kFewRanks - 1) / kFewRanks);
     const int64_t want = 2 * (int64_t)num_sms / ctas, most = (C_down + 31) / 32 / kFewWarps;
@@ -443,6 +383,8 @@ LoraPlan lora_plan_call(int64_t T, int C_down, int R, int r, int num_sms)
 cudaError_t launch_lora_down(const LoraArgs &l, const LoraPlan &p, const uint16_t *x, int64_t xs, const uint16_t *W,
                              int C, bool scaled, float *part, cudaStream_t st)
 {
+    if (p.tiled)
+        return launch_tile_down(l, p, x, xs, W, C, scaled, part, st);
     const dim3 grid(p.splits, (unsigned)most_tiles(l.T, l.R, kFewTokens, false), (l.r + kFewRanks - 1) / kFewRanks);
     few_down_kernel<<<grid, kFewWarps * 32, 0, st>>>(l, x, xs, W, C, scaled, part);
     return cudaGetLastError();
@@ -452,6 +394,8 @@ cudaError_t launch_lora_up(const LoraArgs &l, const LoraPlan &p, const float *pa
                            bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *v,
                            cudaStream_t st)
 {
+    if (p.tiled)
+        return launch_tile_up(l, p, part, W, C, scaled, base, bs, out, os, v, st);
     const dim3 grid((C + kFewCols - 1) / kFewCols, (unsigned)most_tiles(l.T, l.R, kFewTokens, base != out));
     few_up_kernel<<<grid, kFewWarps * 32, 0, st>>>(l, part, p.splits, W, C, scaled, base, bs, out, os, v);
     return cudaGetLastError();

@@ -1,0 +1,434 @@
+// lora_tile.cu -- the adapter products for many tokens, on the tensor cores: tiles
+// of 128 tokens of one adapter, tcgen05 MMAs (kind::f16, bf16 operands, fp32 sums in
+// TMEM).  The tokens' rows are gathered by cp.async into 128-byte-swizzled tiles;
+// every thread copies, one thread issues the MMAs.
+//
+// A rank r contraction does 2r flops for every element it reads, below the 283
+// flops a byte of the tensor peak over the copy rate even at r = 128: the tokens'
+// rows are what bounds these kernels, and the low-rank side costs little enough to
+// enter as two bf16 parts (its rounding error then is 2^-16).
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "gemmar.h"
+#include "lora.cuh"
+
+namespace gemmar {
+using namespace ptx;
+
+namespace {
+
+constexpr int kRows = 128;      // tokens a tile, rows of the accumulator
+constexpr int kSw = 1024;       // a swizzle atom: 8 rows of 128 bytes
+
+// 16-byte chunk c of row `row` in a tile of 128-byte rows under the 128-byte swizzle.
+__device__ __forceinline__ uint32_t sw128(int row, int c) { return row * 128 + ((c ^ (row & 7)) << 4); }
+
+__device__ __forceinline__ uint8_t *align_1024(uint8_t *p)
+{
+    return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+struct Waits {
+    DevStatus *status;
+    uint64_t timeout_ns;
+};
+
+// Bounded: after a wait that ran out (or another thread's) the kernel goes on to its
+// end without waiting, its result is void and the status word says so.
+__device__ __forceinline__ void wait_mma(uint64_t *bar, uint32_t parity, volatile int *abort, const Waits &w)
+{
+    mbar_wait(bar, parity, abort, w.status, w.timeout_ns, SITE_LORA_MMA);
+    tc_fence_after();
+}
+
+__host__ __device__ constexpr int tmem_cols(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : 512; }
+
+// ---------------------------------------------------------------- down
+
+// part[s][i][j] = f sum over split s's columns of x[t,c] W[a,j,c]: D[128 tokens, ranks],
+// both operands K-major, 64 columns a stage.
+constexpr int kDownThreads = 256;
+
+template <int RP>   // ranks rounded up to 16, 32, 64 or 128
+struct DownCfg {
+    static constexpr int kX = kRows * 128, kW = RP * 128, kStage = kX + kW;
+    static constexpr int kStages = RP == 128 ? 3 : 4;
+    static constexpr int kSmem = kStages * kStage + 1024;
+};
+
+template <int RP>
+__global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs l, const uint16_t *__restrict__ x,
+                                                                 int64_t xs, const uint16_t *__restrict__ W, int C,
+                                                                 bool scaled, float *__restrict__ part, int cols,
+                                                                 const Waits waits)
+{
+    using Cfg = DownCfg<RP>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t done[Cfg::kStages];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    const Tile tile = find_tile(l, blockIdx.x, kRows, false);
+    if (tile.count == 0)
+        return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint8_t *smem = align_1024(smem_raw);
+    const uint32_t base = smem_u32(smem);
+    const int rank = rank_of(l, tile.a);
+    if (tid == 0) {
+        for (int s = 0; s < Cfg::kStages; ++s)
+            mbar_init(done + s, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&tmem_slot, tmem_cols(RP));
+        tmem_relinquish();
+    }
+    // this thread's chunk of every stage: column chunk tid & 7 of rows tid / 8 + 32 i
+    const int ch = tid & 7, row0 = tid >> 3;
+    const uint16_t *xr[4];
+    bool xok[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int p = row0 + 32 * i;
+        const int t = p < tile.count ? __ldg(l.order + tile.i0 + p) : -1;
+        xok[i] = t >= 0 && t < l.T;
+        xr[i] = x + (xok[i] ? t : 0) * xs;
+    }
+    const uint16_t *w0 = W + (int64_t)tile.a * l.r * C;
+    const int c_lo = blockIdx.y * cols, c_hi = min(c_lo + cols, C);
+    const int steps = (c_hi - c_lo + 63) / 64;
+    auto fetch = [&](int s) {
+        if (s < steps) {
+            const uint32_t st = base + (s % Cfg::kStages) * Cfg::kStage;
+            const int c = c_lo + s * 64 + ch * 8;
+            const bool in = c < c_hi;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                cp_async_cg16_or_zero(st + sw128(row0 + 32 * i, ch), xr[i] + (in ? c : 0), in && xok[i]);
+#pragma unroll
+            for (int j = row0; j < RP; j += 32) {
+                const bool ok = in && j < rank;
+                cp_async_cg16_or_zero(st + Cfg::kX + sw128(j, ch), w0 + (ok ? (int64_t)j * C + c : 0), ok);
+            }
+        }
+        cp_async_commit();
+    };
+    for (int s = 0; s < Cfg::kStages - 1; ++s)
+        fetch(s);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t d = tmem_slot;
+    for (int s = 0; s < steps; ++s) {
+        cp_async_wait<Cfg::kStages - 2>();
+        fence_async_shared();
+        __syncthreads();
+        if (tid == 0) {
+            tc_fence_after();
+            const uint32_t st = base + (s % Cfg::kStages) * Cfg::kStage;
+            const uint64_t ad = desc_kmajor_sw128(st), bd = desc_kmajor_sw128(st + Cfg::kX);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_bf16_ss(d, ad + 2 * k, bd + 2 * k, idesc_bf16(kRows, RP, 0, 0), s > 0 || k > 0);
+            tc_commit(done + s % Cfg::kStages);
+        }
+        // the stage of step s - 1 takes step s + stages - 1
+        if (s > 0 && s + Cfg::kStages - 1 < steps)
+            wait_mma(done + (s - 1) % Cfg::kStages, ((s - 1) / Cfg::kStages) & 1, &abort_flag, waits);
+        fetch(s + Cfg::kStages - 1);
+    }
+    wait_mma(done + (steps - 1) % Cfg::kStages, ((steps - 1) / Cfg::kStages) & 1, &abort_flag, waits);
+    if (warp < 4) {
+        const int i = warp * 32 + lane;
+        const float f = scaled ? l.scales[tile.a] : 1.0f;
+        float *out = part + ((int64_t)blockIdx.y * l.T + tile.i0 + i) * l.r;
+#pragma unroll
+        for (int j0 = 0; j0 < RP; j0 += 16) {
+            uint32_t v[16];
+            tmem_ld_x16(d + ((uint32_t)(warp * 32) << 16) + j0, v);
+            tmem_wait_ld(v);
+            if (i < tile.count) {
+                if (l.r % 4 == 0) {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4)
+                        if (j0 + j < l.r)
+                            *reinterpret_cast<float4 *>(out + j0 + j) =
+                                make_float4(f * __uint_as_float(v[j]), f * __uint_as_float(v[j + 1]),
+                                            f * __uint_as_float(v[j + 2]), f * __uint_as_float(v[j + 3]));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j0 + j < l.r)
+                            out[j0 + j] = f * __uint_as_float(v[j]);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0)
+        tmem_dealloc(d, tmem_cols(RP));
+}
+
+// ---------------------------------------------------------------- up
+
+// out[t, c] = base[t, c] + f sum_j v[i, j] W[a, j, c]: D[128 tokens, 64 columns] for 64
+// columns a step, A the two bf16 parts of v in TMEM, B the weights' rows (N
+// contiguous).  A warp owns 32 tokens: it copies their rows of base ahead into a
+// ring of its own, adds its lanes' rows of D there and writes whole 128-byte row
+// pieces out of it.
+constexpr int kUpThreads = 128;
+
+template <int RP>
+struct UpCfg {
+    static constexpr int kRing = 4;                   // steps copied ahead
+    static constexpr int kY = kRows * 128, kW = RP * 128, kStage = kY + kW;
+    // at least 78 KB: a third CTA an SM would wait for TMEM columns
+    static constexpr int kSmem = kRing * kStage + 1024 > 78 * 1024 ? kRing * kStage + 1024 : 78 * 1024;
+    static constexpr int kA = 128;                    // TMEM: two accumulators of 64 columns, then hi, lo
+    static constexpr int kTmem = 128 + RP <= 256 ? 256 : 512;
+};
+
+template <int RP>
+__global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, const float *__restrict__ part, int splits,
+                                                             const uint16_t *__restrict__ W, int C, bool scaled,
+                                                             const uint16_t *base, int64_t bs, uint16_t *out,
+                                                             int64_t os, float *v_out, int cols, const Waits waits)
+{
+    using Cfg = UpCfg<RP>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ float vs[kRows][17];
+    __shared__ uint64_t done[2];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    const Tile tile = find_tile(l, blockIdx.x, kRows, base != out);
+    if (tile.count == 0)
+        return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t smem = smem_u32(align_1024(smem_raw));
+    const int rank = tile.a < l.R ? rank_of(l, tile.a) : 0;
+    if (tid == 0) {
+        mbar_init(done, 1);
+        mbar_init(done + 1, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&tmem_slot, Cfg::kTmem);
+        tmem_relinquish();
+    }
+    // chunk lane & 7 of the warp's rows lane / 8 + 4 i
+    const int ch = lane & 7;
+    int tok[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int p = warp * 32 + (lane >> 3) + 4 * i;
+        const int t = p < tile.count ? __ldg(l.order + tile.i0 + p) : -1;
+        tok[i] = t >= 0 && t < l.T ? t : -1;
+    }
+    const uint16_t *w0 = W + (int64_t)min(tile.a, l.R - 1) * l.r * C;
+    const int c_lo = blockIdx.y * cols, c_hi = min(c_lo + cols, C);
+    const int steps = (c_hi - c_lo + 63) / 64;
+    auto fetch = [&](int s) {
+        if (s < steps) {
+            const uint32_t st = smem + (s % Cfg::kRing) * Cfg::kStage;
+            const int c = c_lo + s * 64 + ch * 8;
+            const bool in = c < c_hi;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool ok = in && tok[i] >= 0 && base != nullptr;
+                cp_async_cg16_or_zero(st + sw128(warp * 32 + (lane >> 3) + 4 * i, ch),
+                                      ok ? base + tok[i] * bs + c : w0, ok);
+            }
+#pragma unroll
+            for (int j = tid >> 3; j < RP; j += kUpThreads / 8) {
+                const bool ok = in && j < rank;
+                cp_async_cg16_or_zero(st + Cfg::kY + sw128(j, ch), w0 + (ok ? (int64_t)j * C + c : 0), ok);
+            }
+        }
+        cp_async_commit();
+    };
+    for (int s = 0; s < Cfg::kRing; ++s)
+        fetch(s);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = tmem_slot;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    // v: the parts in their order, 16 ranks at a time through shared memory
+    const int ksteps = (rank + 15) / 16;
+    for (int k = 0; k < ksteps; ++k) {
+        const int j = k * 16 + (tid & 15);
+        float sum[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            sum[i] = 0.0f;
+        const float *src = part + (int64_t)(tile.i0 + (tid >> 4)) * l.r + j;
+        for (int s = 0; s < splits; ++s) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if ((tid >> 4) + 8 * i < tile.count && j < rank)
+                    sum[i] += src[((int64_t)s * l.T + 8 * i) * l.r];
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int p = (tid >> 4) + 8 * i;
+            vs[p][tid & 15] = sum[i];
+            if (v_out && blockIdx.y == 0 && p < tile.count && j < l.r)
+                v_out[(int64_t)(tile.i0 + p) * l.r + j] = sum[i];
+        }
+        __syncthreads();
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            const float a = vs[tid][2 * p], b = vs[tid][2 * p + 1];
+            hi[p] = bf16x2_from_f32(a, b);
+            lo[p] = bf16x2_from_f32(a - __uint_as_float(hi[p] << 16), b - __uint_as_float(hi[p] & 0xFFFF0000u));
+        }
+        tmem_st_x8(tm + lanes + Cfg::kA + k * 8, hi);
+        tmem_st_x8(tm + lanes + Cfg::kA + RP / 2 + k * 8, lo);
+        __syncthreads();
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    if (v_out && blockIdx.y == 0 && tile.a < l.R) {   // columns past the rank's last step
+        const int rest = l.r - ksteps * 16;
+        for (int e = tid; e < tile.count * rest; e += kUpThreads)
+            v_out[(int64_t)(tile.i0 + e / rest) * l.r + ksteps * 16 + e % rest] = 0.0f;
+    }
+    const float f = scaled && tile.a < l.R ? l.scales[tile.a] : 1.0f;
+    for (int s = 0; s <= steps; ++s) {
+        if (s < steps) {
+            cp_async_wait<Cfg::kRing - 2>();
+            fence_async_shared();
+            __syncthreads();
+            if (tid == 0 && ksteps > 0) {
+                tc_fence_after();
+                const uint32_t wst = smem + (s % Cfg::kRing) * Cfg::kStage + Cfg::kY;
+                for (int k = 0; k < ksteps; ++k) {
+                    const uint64_t bd = smem_desc(wst + k * 2 * kSw, kSw, kSw, 2);
+                    const uint32_t a = tm + Cfg::kA + k * 8;
+                    mma_bf16_ts(tm + (s & 1) * 64, a, bd, idesc_bf16(kRows, 64, 0, 1), k > 0);
+                    mma_bf16_ts(tm + (s & 1) * 64, a + RP / 2, bd, idesc_bf16(kRows, 64, 0, 1), 1);
+                }
+                tc_commit(done + (s & 1));
+            }
+        }
+        if (s == 0)
+            continue;
+        // step s - 1
+        const int e = s - 1, c0 = c_lo + e * 64;
+        const uint32_t st = smem + (e % Cfg::kRing) * Cfg::kStage;
+        if (ksteps > 0) {
+            wait_mma(done + (e & 1), (e >> 1) & 1, &abort_flag, waits);
+            const int row = warp * 32 + lane;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[32];
+                tmem_ld_x32(tm + lanes + (e & 1) * 64 + h * 32, v);
+                tmem_wait_ld(v);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t at = st + sw128(row, h * 4 + c);
+                    uint4 y = ld_shared_v4(at);
+                    uint32_t *w = reinterpret_cast<uint32_t *>(&y);
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        w[p] = bf16x2_from_f32(fmaf(f, __uint_as_float(v[c * 8 + 2 * p]), __uint_as_float(w[p] << 16)),
+                                               fmaf(f, __uint_as_float(v[c * 8 + 2 * p + 1]),
+                                                    __uint_as_float(w[p] & 0xFFFF0000u)));
+                    st_shared_v4(at, y);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+        }
+        const int c = c0 + ch * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint4 y = ld_shared_v4(st + sw128(warp * 32 + (lane >> 3) + 4 * i, ch));
+            if (tok[i] >= 0 && c < c_hi)
+                *reinterpret_cast<uint4 *>(out + tok[i] * os + c) = y;
+        }
+        __syncwarp();
+        fetch(e + Cfg::kRing);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0)
+        tmem_dealloc(tm, Cfg::kTmem);
+}
+
+int pad_rank(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
+
+template <int RP>
+cudaError_t run_down(const LoraArgs &l, const LoraPlan &p, const uint16_t *x, int64_t xs, const uint16_t *W, int C,
+                     bool scaled, float *part, cudaStream_t st)
+{
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(tile_down_kernel<RP>), DownCfg<RP>::kSmem);
+    if (e != cudaSuccess)
+        return e;
+    const int cols = ((C + 63) / 64 + p.splits - 1) / p.splits * 64;
+    const dim3 grid((unsigned)most_tiles(l.T, l.R, kRows, false), p.splits);
+    tile_down_kernel<RP><<<grid, kDownThreads, DownCfg<RP>::kSmem, st>>>(l, x, xs, W, C, scaled, part, cols,
+                                                                        Waits{p.status, p.timeout_ns});
+    return cudaGetLastError();
+}
+
+template <int RP>
+cudaError_t run_up(const LoraArgs &l, const LoraPlan &p, const float *part, const uint16_t *W, int C, bool scaled,
+                   const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *v, cudaStream_t st)
+{
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(tile_up_kernel<RP>), UpCfg<RP>::kSmem);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t tiles = most_tiles(l.T, l.R, kRows, base != out);
+    // ranges of columns that fill two CTAs an SM once, four steps at least
+    const int steps = (C + 63) / 64;
+    const int64_t want = 2 * (int64_t)p.num_sms / std::max<int64_t>(1, l.T / kRows + 1);
+    const int ranges = (int)std::max<int64_t>(1, std::min<int64_t>(want, steps / 4));
+    const int per = (steps + ranges - 1) / ranges;
+    const dim3 grid((unsigned)tiles, (steps + per - 1) / per);
+    tile_up_kernel<RP><<<grid, kUpThreads, UpCfg<RP>::kSmem, st>>>(l, part, p.splits, W, C, scaled, base, bs, out, os, v,
+                                                                  per * 64, Waits{p.status, p.timeout_ns});
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int lora_tile_splits(int64_t T, int C, int num_sms)
+{
+    // splits that fill two CTAs an SM once, four stages at least
+    const int64_t want = 2 * (int64_t)num_sms / std::max<int64_t>(1, T / kRows + 1);
+    int splits = (int)std::max<int64_t>(1, std::min<int64_t>({want, (C + 63) / 64 / 4, 16}));
+    const int steps = (C + 63) / 64, per = (steps + splits - 1) / splits;
+    return (steps + per - 1) / per;   // none empty
+}
+
+cudaError_t launch_tile_down(const LoraArgs &l, const LoraPlan &p, const uint16_t *x, int64_t xs, const uint16_t *W,
+                             int C, bool scaled, float *part, cudaStream_t st)
+{
+    switch (pad_rank(l.r)) {
+    case 16: return run_down<16>(l, p, x, xs, W, C, scaled, part, st);
+    case 32: return run_down<32>(l, p, x, xs, W, C, scaled, part, st);
+    case 64: return run_down<64>(l, p, x, xs, W, C, scaled, part, st);
+    default: return run_down<128>(l, p, x, xs, W, C, scaled, part, st);
+    }
+}
+
+cudaError_t launch_tile_up(const LoraArgs &l, const LoraPlan &p, const float *part, const uint16_t *W, int C,
+                           bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *v,
+                           cudaStream_t st)
+{
+    switch (pad_rank(l.r)) {
+    case 16: return run_up<16>(l, p, part, W, C, scaled, base, bs, out, os, v, st);
+    case 32: return run_up<32>(l, p, part, W, C, scaled, base, bs, out, os, v, st);
+    case 64: return run_up<64>(l, p, part, W, C, scaled, base, bs, out, os, v, st);
+    default: return run_up<128>(l, p, part, W, C, scaled, base, bs, out, os, v, st);
+    }
+}
+
+}  // namespace gemmar

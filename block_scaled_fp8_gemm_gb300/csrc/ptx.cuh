@@ -103,6 +103,7 @@ enum WaitSite : int {
     SITE_REDUCE_BAND = 7,
     SITE_PARK_FULL = 8,    // a store warp waiting for its epilogue warp's parked partial
     SITE_PARK_EMPTY = 9,   // an epilogue warp waiting for its park to be copied out
+    SITE_LORA_MMA = 10,    // an adapter kernel waiting for its MMAs
 };
 
 constexpr int kErrTimeout = 6;   // == GEMMAR_ERR_TIMEOUT
@@ -335,6 +336,30 @@ __device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t adesc, uint64
         : "memory");
 }
 
+// D(tmem) (+)= A * B, bf16 x bf16 -> f32, M and N from idesc, K=16; A in shared
+// memory, or in TMEM (lane = row, two values of K per 32-bit column).
+__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Copy a 32-row x 128-bit matrix from shared memory into TMEM columns
 // [taddr, taddr+4) of all four 32-lane quarters.
 __device__ __forceinline__ void tc_cp_32x128b_warpx4(uint32_t taddr, uint64_t sdesc)
@@ -368,6 +393,15 @@ __host__ __device__ constexpr uint32_t idesc_f8_e4m3(uint32_t M, uint32_t N)
            | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// Instruction descriptor, kind::f16: D f32, A/B bf16; mn_a, mn_b: 1 where the
+// operand's rows run along K (M or N contiguous), 0 where K is contiguous.
+__host__ __device__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N, uint32_t mn_a, uint32_t mn_b)
+{
+    return (1u << 4)                 // D format f32
+           | (1u << 7) | (1u << 10)  // A, B bf16
+           | (mn_a << 15) | (mn_b << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
 // Instruction descriptor, kind::mxf8f6f4 block-scaled: A/B e4m3, ue8m0 scales,
 // scale-factor ids (byte of the 32-bit TMEM scale word) for A and B.
 __host__ __device__ constexpr uint32_t idesc_mx_e4m3(uint32_t M, uint32_t N, uint32_t sf_id)
@@ -393,6 +427,14 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const float *v)
           "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]),
           "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
         : "memory");
+}
+
+// 8 columns.
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 // Wait until this thread's tcgen05.st have been performed.
@@ -534,6 +576,16 @@ __device__ __forceinline__ void cp_async_cg16(uint32_t dst, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+
+// The same, or 16 zero bytes where !ok (src is then not read).
+__device__ __forceinline__ void cp_async_cg16_or_zero(uint32_t dst, const void *src, bool ok)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+
+// Make this thread's shared-memory writes (cp.async included, once waited for)
+// visible to the async proxy, which the MMA reads through.
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // 8 bytes (through L1: the 8-byte form has no other).
 __device__ __forceinline__ void cp_async_ca8(uint32_t dst, const void *src)
