@@ -747,13 +747,15 @@ GEMMAR_API int lora_apply(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, 
         return rc;
     if (!aligned16(v))
         return GEMMAR_ERR_ALIGN;
-    const LoraPlan p = lora_plan_call(T, (int)K, R, r, ctx->num_sms, ctx->status, ctx->timeout_ns);
-    if (p.part_floats > ctx->W_floats)
+    if (T * r > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
+    if (v == nullptr)
+        v = ctx->W;
     cudaStream_t st = as_stream(stream);
     const LoraArgs l{order, offsets, ranks, scales, T, R, r};
-    CUDA_OK(launch_lora_down(l, p, x, x_stride, A, (int)K, false, ctx->W, st));
-    CUDA_OK(launch_lora_up(l, p, ctx->W, B, (int)N, true, y, y_stride, out, out_stride, v, st));
+    const LoraCall p{ctx->num_sms, ctx->status, ctx->timeout_ns};
+    CUDA_OK(launch_lora_down(l, p, x, x_stride, A, (int)K, false, v, st));
+    CUDA_OK(launch_lora_up(l, p, v, B, (int)N, true, y, y_stride, out, out_stride, st));
     return GEMMAR_OK;
 }
 
@@ -774,15 +776,14 @@ GEMMAR_API int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stri
         return rc;
     if (!aligned16(v) || !aligned16(dA) || !aligned16(dB))
         return GEMMAR_ERR_ALIGN;
-    const LoraPlan p = lora_plan_call(T, (int)N, R, r, ctx->num_sms, ctx->status, ctx->timeout_ns);
-    const int64_t w_floats = (T * r + 3) / 4 * 4;
-    if (w_floats + p.part_floats > ctx->W_floats)
+    if (T * r > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
     cudaStream_t st = as_stream(stream);
     const LoraArgs l{order, offsets, ranks, scales, T, R, r};
-    float *w = ctx->W, *part = ctx->W + w_floats;
-    CUDA_OK(launch_lora_down(l, p, dy, dy_stride, B, (int)N, true, part, st));
-    CUDA_OK(launch_lora_up(l, p, part, A, (int)K, false, dx0, dx0_stride, dx, dx_stride, w, st));
+    const LoraCall p{ctx->num_sms, ctx->status, ctx->timeout_ns};
+    float *w = ctx->W;
+    CUDA_OK(launch_lora_down(l, p, dy, dy_stride, B, (int)N, true, w, st));
+    CUDA_OK(launch_lora_up(l, p, w, A, (int)K, false, dx0, dx0_stride, dx, dx_stride, st));
     CUDA_OK(launch_lora_grad(l, w, x, x_stride, (int)K, false, dA, st));
     CUDA_OK(launch_lora_grad(l, v, dy, dy_stride, (int)N, true, dB, st));
     return GEMMAR_OK;

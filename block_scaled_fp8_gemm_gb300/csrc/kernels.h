@@ -200,32 +200,24 @@ struct LoraArgs {
     int R, r;
 };
 cudaError_t launch_lora_plan(const int32_t *ids, int64_t T, int R, int32_t *order, int32_t *offsets, cudaStream_t st);
-// How a call is cut: few tokens go to the kernels that load straight into registers
-// (lora.cu), many to the tiles on the tensor cores (lora_tile.cu); the sums over
-// C_down columns come in `splits` parts.
-struct LoraPlan {
-    bool tiled;
-    int splits;
-    int64_t part_floats;   // splits * T * r
+// What the launches of a call share: the device, and the tiles' bounded waits.
+struct LoraCall {
     int num_sms;
     ptx::DevStatus *status;
     uint64_t timeout_ns;
 };
-LoraPlan lora_plan_call(int64_t T, int C_down, int R, int r, int num_sms, ptx::DevStatus *status, uint64_t timeout_ns);
-int lora_tile_splits(int64_t T, int C, int num_sms);
-cudaError_t launch_tile_down(const LoraArgs &l, const LoraPlan &p, const uint16_t *x, int64_t xs, const uint16_t *W,
-                             int C, bool scaled, float *part, cudaStream_t st);
-cudaError_t launch_tile_up(const LoraArgs &l, const LoraPlan &p, const float *part, const uint16_t *W, int C,
-                           bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *v,
-                           cudaStream_t st);
-// part[s][i][j], summed over s: f sum_c x[order[i],c] W[a,j,c], f = scales[a] if scaled, else 1
-cudaError_t launch_lora_down(const LoraArgs &l, const LoraPlan &p, const uint16_t *x, int64_t xs, const uint16_t *W,
-                             int C, bool scaled, float *part, cudaStream_t st);
-// out[t,c] = base[t,c] + f sum_j v[i,j] W[a,j,c] with v the sum of the parts, also written to v
-// (may be nullptr); rows without an adapter: base
-cudaError_t launch_lora_up(const LoraArgs &l, const LoraPlan &p, const float *part, const uint16_t *W, int C,
-                           bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *v,
-                           cudaStream_t st);
+// v[i,j] = f sum_c x[order[i],c] W[a,j,c], f = scales[a] if scaled, else 1; 0 for j past the rank
+cudaError_t launch_lora_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *W,
+                             int C, bool scaled, float *v, cudaStream_t st);
+// out[t,c] = base[t,c] + f sum_j v[i,j] W[a,j,c]; rows without an adapter: base
+cudaError_t launch_lora_up(const LoraArgs &l, const LoraCall &p, const float *v, const uint16_t *W, int C,
+                           bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st);
+// Few tokens go to the kernels that load straight into registers (lora.cu), many to
+// the tiles on the tensor cores (lora_tile.cu).
+cudaError_t launch_tile_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *W,
+                             int C, bool scaled, float *v, cudaStream_t st);
+cudaError_t launch_tile_up(const LoraArgs &l, const LoraCall &p, const float *v, const uint16_t *W, int C,
+                           bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st);
 // G[a,j,c] = f sum_{tokens of a} p[i,j] x[order[i],c]
 cudaError_t launch_lora_grad(const LoraArgs &l, const float *p, const uint16_t *x, int64_t xs, int C, bool scaled,
                              uint16_t *G, cudaStream_t st);

@@ -118,14 +118,14 @@ constexpr int kFewTokens = 32;   // tokens a tile: four N tiles
 constexpr int kFewWarps = 8;
 constexpr int kFewRanks = 32;    // ranks a CTA of the down kernel: two M tiles
 
-// part[s][i][j] of split s: sums over its share of the columns.  The CTA's eight
-// warps share that again, and their sums meet in shared memory in warp order.
+// v[i][j] of a tile: the CTAs of a cluster share the columns (blockIdx.y) and so do a
+// CTA's eight warps; their sums are added in warp and in rank order.
 __global__ void __launch_bounds__(kFewWarps * 32) few_down_kernel(const LoraArgs l, const uint16_t *__restrict__ x,
                                                                   int64_t xs, const uint16_t *__restrict__ W, int C,
-                                                                  bool scaled, float *__restrict__ part)
+                                                                  bool scaled, float *__restrict__ v)
 {
     __shared__ float sums[kFewWarps][kFewRanks][kFewTokens + 1];
-    const Tile tile = find_tile(l, blockIdx.y, kFewTokens, false);
+    const Tile tile = find_tile(l, blockIdx.x, kFewTokens, false);
     const int rank = tile.count ? rank_of(l, tile.a) : 0, j0 = blockIdx.z * kFewRanks;
     if (tile.count == 0)
         return;
@@ -151,13 +151,13 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_down_kernel(const LoraArgs
             xr[n] = x + (xok[n] ? t : 0) * xs + q * 8;
         }
         // blocks of 32 columns, dealt evenly to splits and warps
-        const int blocks = (C + 31) / 32, shares = gridDim.x * kFewWarps, share = blockIdx.x * kFewWarps + warp;
+        const int blocks = (C + 31) / 32, shares = gridDim.y * kFewWarps, share = blockIdx.y * kFewWarps + warp;
         const int b0 = (int)((int64_t)blocks * share / shares), b1 = (int)((int64_t)blocks * (share + 1) / shares);
         const bool wide = j0 + 16 < rank;
 #pragma unroll 4
         for (int b = b0; b < b1; ++b) {
             const bool in = b * 32 + q * 8 < C;
-            uint4 w[4], v[4];
+            uint4 w[4], xv[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 w[i] = make_uint4(0, 0, 0, 0);
@@ -166,9 +166,9 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_down_kernel(const LoraArgs
             }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                v[n] = make_uint4(0, 0, 0, 0);
+                xv[n] = make_uint4(0, 0, 0, 0);
                 if (in && xok[n])
-                    v[n] = __ldg(reinterpret_cast<const uint4 *>(xr[n] + b * 32));
+                    xv[n] = __ldg(reinterpret_cast<const uint4 *>(xr[n] + b * 32));
             }
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_down_kernel(const LoraArgs
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     if (n < nt) {
-                        mma_bf16(acc[m][n], lo, v[n].x, v[n].y);
-                        mma_bf16(acc[m][n], hi, v[n].z, v[n].w);
+                        mma_bf16(acc[m][n], lo, xv[n].x, xv[n].y);
+                        mma_bf16(acc[m][n], hi, xv[n].z, xv[n].w);
                     }
                 }
             }
@@ -194,29 +194,29 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_down_kernel(const LoraArgs
             for (int e = 0; e < 4; ++e)
                 sums[warp][m * 16 + g + (e >> 1) * 8][n * 8 + q * 2 + (e & 1)] = acc[m][n][e];
     __syncthreads();
-    const float f = scaled ? l.scales[tile.a] : 1.0f;
-    float *out = part + ((int64_t)blockIdx.x * l.T + tile.i0) * l.r;
-    const int nj = min(kFewRanks, l.r - j0);
-    for (int e = threadIdx.x; e < tile.count * nj; e += kFewWarps * 32) {
-        const int i = e / nj, j = e - i * nj;
-        float s = sums[0][j][i];
+    for (int e = threadIdx.x; e < kFewRanks * kFewTokens; e += kFewWarps * 32) {
+        float *at = &sums[0][e / kFewTokens][e % kFewTokens];
+        float s = *at;
 #pragma unroll
         for (int w = 1; w < kFewWarps; ++w)
-            s += sums[w][j][i];
-        out[(int64_t)i * l.r + j0 + j] = f * s;
+            s += sums[w][e / kFewTokens][e % kFewTokens];
+        *at = s;
     }
+    const float f = scaled ? l.scales[tile.a] : 1.0f;
+    float *out = v + (int64_t)tile.i0 * l.r + j0;
+    cluster_sum(smem_u32(sums), min(kFewRanks, l.r - j0), tile.count, kFewTokens + 1, gridDim.y,
+                [&](int j, int i, float s) { out[(int64_t)i * l.r + j] = f * s; });
 }
 
-// out rows of a tile, 64 columns a warp.  The splits' parts are summed in their
-// order, and the sum enters as two bf16 parts.  D[n, token] = sum_j W[j, n] v[token, j]:
+// out rows of a tile, 64 columns a warp; v enters as two bf16 parts.  D[n, token] = sum_j W[j, n] v[token, j]:
 // an MMA's two row halves are the even and odd columns of a lane's eight, so the
 // lane ends with eight consecutive columns of two tokens.
 constexpr int kFewCols = 64 * kFewWarps;
 
-__global__ void __launch_bounds__(kFewWarps * 32) few_up_kernel(const LoraArgs l, const float *__restrict__ part,
-                                                                int splits, const uint16_t *__restrict__ W, int C,
-                                                                bool scaled, const uint16_t *base, int64_t bs,
-                                                                uint16_t *out, int64_t os, float *v_out)
+__global__ void __launch_bounds__(kFewWarps * 32) few_up_kernel(const LoraArgs l, const float *__restrict__ v,
+                                                                const uint16_t *__restrict__ W, int C, bool scaled,
+                                                                const uint16_t *base, int64_t bs, uint16_t *out,
+                                                                int64_t os)
 {
     constexpr int kRow = GEMMAR_LORA_MAX_RANK / 2 + 4;   // pairs of a token, padded off the banks
     __shared__ uint32_t hi[kFewTokens][kRow], lo[kFewTokens][kRow];
@@ -238,34 +238,16 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_up_kernel(const LoraArgs l
         }
     };
     uint4 w[4];
-    load(0, w);   // in flight while the parts are summed
+    load(0, w);   // in flight while v is read
     const int pairs = steps * 8;
     for (int e = threadIdx.x; e < kFewTokens * pairs; e += kFewWarps * 32) {
         const int i = e / pairs, p = e - i * pairs;
-        float v[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int j = 2 * p + k;
-            if (i < tile.count && j < rank) {
-                const float *src = part + (int64_t)(tile.i0 + i) * l.r + j;
-                for (int s = 0; s < splits; ++s)
-                    v[k] += src[(int64_t)s * l.T * l.r];
-            }
-        }
-        const uint32_t h = bf16x2_from_f32(v[0], v[1]);
+        const float *src = v + (int64_t)(tile.i0 + i) * l.r + 2 * p;
+        const float v0 = i < tile.count && 2 * p < rank ? __ldg(src) : 0.0f;
+        const float v1 = i < tile.count && 2 * p + 1 < rank ? __ldg(src + 1) : 0.0f;
+        const uint32_t h = bf16x2_from_f32(v0, v1);
         hi[i][p] = h;
-        lo[i][p] = bf16x2_from_f32(v[0] - __uint_as_float(h << 16), v[1] - __uint_as_float(h & 0xFFFF0000u));
-        if (v_out && blockIdx.x == 0 && i < tile.count) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (2 * p + k < l.r)
-                    v_out[(int64_t)(tile.i0 + i) * l.r + 2 * p + k] = v[k];
-        }
-    }
-    if (v_out && blockIdx.x == 0 && tile.a < l.R) {   // columns past the rank's last step
-        const int rest = l.r - pairs * 2;
-        for (int e = threadIdx.x; e < tile.count * rest; e += kFewWarps * 32)
-            v_out[(int64_t)(tile.i0 + e / rest) * l.r + pairs * 2 + e % rest] = 0.0f;
+        lo[i][p] = bf16x2_from_f32(v0 - __uint_as_float(h << 16), v1 - __uint_as_float(h & 0xFFFF0000u));
     }
     __syncthreads();
     float acc[4][4][4] = {};   // column pair, token tile, fragment
@@ -364,40 +346,27 @@ cudaError_t launch_lora_plan(const int32_t *ids, int64_t T, int R, int32_t *orde
     return cudaGetLastError();
 }
 
-LoraPlan lora_plan_call(int64_t T, int C_down, int R, int r, int num_sms, DevStatus *status, uint64_t timeout_ns)
+cudaError_t launch_lora_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *W,
+                             int C, bool scaled, float *v, cudaStream_t st)
 {
-    LoraPlan p{T > kFewBatch, 1, 0, num_sms, status, timeout_ns};
-    if (p.tiled) {
-        p.splits = lora_tile_splits(T, C_down, num_sms);
-        p.part_floats = (int64_t)p.splits * T * r;
-        return p;
-    }
+    if (l.T > kFewBatch)
+        return launch_tile_down(l, p, x, xs, W, C, scaled, v, st);
     // two CTAs an SM, a block of 32 columns a warp at least
-    const int64_t ctas = most_tiles(T, R, kFewTokens, false) * ((r + kFewRanks - 1) / kFewRanks);
-    const int64_t want = 2 * (int64_t)num_sms / ctas, most = (C_down + 31) / 32 / kFewWarps;
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 16}));
-    p.part_floats = (int64_t)p.splits * T * r;
-    return p;
+    const int64_t tiles = most_tiles(l.T, l.R, kFewTokens, false);
+    const int rank_blocks = (l.r + kFewRanks - 1) / kFewRanks;
+    const int64_t want = std::min<int64_t>({2 * (int64_t)p.num_sms / (tiles * rank_blocks), (C + 31) / 32 / kFewWarps, kMaxSplits});
+    const int splits = (int)std::max<int64_t>(1, want);
+    return launch_split(few_down_kernel, dim3((unsigned)tiles, splits, rank_blocks), kFewWarps * 32, 0, splits, st, l, x, xs,
+                        W, C, scaled, v);
 }
 
-cudaError_t launch_lora_down(const LoraArgs &l, const LoraPlan &p, const uint16_t *x, int64_t xs, const uint16_t *W,
-                             int C, bool scaled, float *part, cudaStream_t st)
+cudaError_t launch_lora_up(const LoraArgs &l, const LoraCall &p, const float *v, const uint16_t *W, int C,
+                           bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st)
 {
-    if (p.tiled)
-        return launch_tile_down(l, p, x, xs, W, C, scaled, part, st);
-    const dim3 grid(p.splits, (unsigned)most_tiles(l.T, l.R, kFewTokens, false), (l.r + kFewRanks - 1) / kFewRanks);
-    few_down_kernel<<<grid, kFewWarps * 32, 0, st>>>(l, x, xs, W, C, scaled, part);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_lora_up(const LoraArgs &l, const LoraPlan &p, const float *part, const uint16_t *W, int C,
-                           bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *v,
-                           cudaStream_t st)
-{
-    if (p.tiled)
-        return launch_tile_up(l, p, part, W, C, scaled, base, bs, out, os, v, st);
+    if (l.T > kFewBatch)
+        return launch_tile_up(l, p, v, W, C, scaled, base, bs, out, os, st);
     const dim3 grid((C + kFewCols - 1) / kFewCols, (unsigned)most_tiles(l.T, l.R, kFewTokens, base != out));
-    few_up_kernel<<<grid, kFewWarps * 32, 0, st>>>(l, part, p.splits, W, C, scaled, base, bs, out, os, v);
+    few_up_kernel<<<grid, kFewWarps * 32, 0, st>>>(l, v, W, C, scaled, base, bs, out, os);
     return cudaGetLastError();
 }
 

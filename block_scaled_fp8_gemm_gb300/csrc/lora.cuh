@@ -64,6 +64,53 @@ __device__ __forceinline__ Tile find_tile(const LoraArgs &l, int want, int size,
     return t;
 }
 
+// Sum over the CTAs of the cluster, in the order of their ranks, of the fp32 array
+// [rows][cols] that each has at the same shared-memory address, rows `pitch` floats
+// apart; put(row, col, sum) is called for each element by one thread of one of
+// them.  The whole cluster calls it, after its threads have written the array.
+template <typename Put>
+__device__ __forceinline__ void cluster_sum(uint32_t array, int rows, int cols, int pitch, int ctas, Put put)
+{
+    if (ctas == 1)
+        __syncthreads();
+    else
+        ptx::cluster_sync();
+    const int me = ctas == 1 ? 0 : (int)ptx::cluster_ctarank(), share = (rows + ctas - 1) / ctas;
+    const int lo = me * share, n = max(0, min(share, rows - lo)) * cols;
+    for (int e = threadIdx.x; e < n; e += blockDim.x) {
+        const int row = lo + e / cols, col = e % cols;
+        const uint32_t at = array + (row * pitch + col) * 4;
+        float s = ptx::ld_shared_cluster_f32(ptx::mapa_shared(at, ctas == 1 ? me : 0));
+        for (int p = 1; p < ctas; ++p)
+            s += ptx::ld_shared_cluster_f32(ptx::mapa_shared(at, p));
+        put(row, col, s);
+    }
+    if (ctas > 1)
+        ptx::cluster_sync();   // no CTA leaves while another reads its array
+}
+
+constexpr int kMaxSplits = 8;   // CTAs of a cluster
+
+// Launch with a cluster of `splits` along y.
+template <typename... Params, typename... Args>
+cudaError_t launch_split(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int splits, cudaStream_t st,
+                         Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1;
+    attr.val.clusterDim.y = (unsigned)splits;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Most tiles of `size` that T tokens of R adapters (and the bare ones) can make.
 inline int64_t most_tiles(int64_t T, int R, int size, bool bare)
 {

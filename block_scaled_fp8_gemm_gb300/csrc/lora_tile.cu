@@ -47,8 +47,9 @@ __host__ __device__ constexpr int tmem_cols(int n) { return n <= 32 ? 32 : n <= 
 
 // ---------------------------------------------------------------- down
 
-// part[s][i][j] = f sum over split s's columns of x[t,c] W[a,j,c]: D[128 tokens, ranks],
-// both operands K-major, 64 columns a stage.
+// v[i][j] = f sum_c x[t,c] W[a,j,c]: D[128 tokens, ranks], both operands K-major, 64
+// columns a stage.  The CTAs of a cluster share the columns of a tile (blockIdx.y) and
+// add their sums in rank order through distributed shared memory.
 constexpr int kDownThreads = 256;
 
 template <int RP>   // ranks rounded up to 16, 32, 64 or 128
@@ -61,7 +62,7 @@ struct DownCfg {
 template <int RP>
 __global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs l, const uint16_t *__restrict__ x,
                                                                  int64_t xs, const uint16_t *__restrict__ W, int C,
-                                                                 bool scaled, float *__restrict__ part, int cols,
+                                                                 bool scaled, float *__restrict__ v, int cols,
                                                                  const Waits waits)
 {
     using Cfg = DownCfg<RP>;
@@ -141,32 +142,25 @@ __global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs 
         fetch(s + Cfg::kStages - 1);
     }
     wait_mma(done + (steps - 1) % Cfg::kStages, ((steps - 1) / Cfg::kStages) & 1, &abort_flag, waits);
+    // the stages are free: D goes there for the cluster's sum
+    constexpr int kPitch = RP + 1;
+    static_assert(kRows * kPitch * 4 <= Cfg::kStages * Cfg::kStage, "D fits the stages");
     if (warp < 4) {
-        const int i = warp * 32 + lane;
-        const float f = scaled ? l.scales[tile.a] : 1.0f;
-        float *out = part + ((int64_t)blockIdx.y * l.T + tile.i0 + i) * l.r;
+        float *mine = reinterpret_cast<float *>(smem) + (warp * 32 + lane) * kPitch;
 #pragma unroll
         for (int j0 = 0; j0 < RP; j0 += 16) {
-            uint32_t v[16];
-            tmem_ld_x16(d + ((uint32_t)(warp * 32) << 16) + j0, v);
-            tmem_wait_ld(v);
-            if (i < tile.count) {
-                if (l.r % 4 == 0) {
+            uint32_t r[16];
+            tmem_ld_x16(d + ((uint32_t)(warp * 32) << 16) + j0, r);
+            tmem_wait_ld(r);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4)
-                        if (j0 + j < l.r)
-                            *reinterpret_cast<float4 *>(out + j0 + j) =
-                                make_float4(f * __uint_as_float(v[j]), f * __uint_as_float(v[j + 1]),
-                                            f * __uint_as_float(v[j + 2]), f * __uint_as_float(v[j + 3]));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (j0 + j < l.r)
-                            out[j0 + j] = f * __uint_as_float(v[j]);
-                }
-            }
+            for (int j = 0; j < 16; ++j)
+                mine[j0 + j] = __uint_as_float(r[j]);
         }
     }
+    const float f = scaled ? l.scales[tile.a] : 1.0f;
+    float *out = v + (int64_t)tile.i0 * l.r;
+    cluster_sum(base, tile.count, l.r, kPitch, gridDim.y,
+                [&](int i, int j, float sum) { out[(int64_t)i * l.r + j] = f * sum; });
     tc_fence_before();
     __syncthreads();
     if (warp == 0)
@@ -193,10 +187,10 @@ struct UpCfg {
 };
 
 template <int RP>
-__global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, const float *__restrict__ part, int splits,
+__global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, const float *__restrict__ v,
                                                              const uint16_t *__restrict__ W, int C, bool scaled,
                                                              const uint16_t *base, int64_t bs, uint16_t *out,
-                                                             int64_t os, float *v_out, int cols, const Waits waits)
+                                                             int64_t os, int cols, const Waits waits)
 {
     using Cfg = UpCfg<RP>;
     extern __shared__ uint8_t smem_raw[];
@@ -258,28 +252,18 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
     tc_fence_after();
     const uint32_t tm = tmem_slot;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    // v: the parts in their order, 16 ranks at a time through shared memory
+    // v in two bf16 parts, 16 ranks at a time through shared memory
     const int ksteps = (rank + 15) / 16;
     for (int k = 0; k < ksteps; ++k) {
         const int j = k * 16 + (tid & 15);
-        float sum[16];
+        const float *src = v + (int64_t)(tile.i0 + (tid >> 4)) * l.r + j;
+        float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            sum[i] = 0.0f;
-        const float *src = part + (int64_t)(tile.i0 + (tid >> 4)) * l.r + j;
-        for (int s = 0; s < splits; ++s) {
+            x[i] = (tid >> 4) + 8 * i < tile.count && j < rank ? __ldg(src + (int64_t)8 * i * l.r) : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if ((tid >> 4) + 8 * i < tile.count && j < rank)
-                    sum[i] += src[((int64_t)s * l.T + 8 * i) * l.r];
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int p = (tid >> 4) + 8 * i;
-            vs[p][tid & 15] = sum[i];
-            if (v_out && blockIdx.y == 0 && p < tile.count && j < l.r)
-                v_out[(int64_t)(tile.i0 + p) * l.r + j] = sum[i];
-        }
+        for (int i = 0; i < 16; ++i)
+            vs[(tid >> 4) + 8 * i][tid & 15] = x[i];
         __syncthreads();
         uint32_t hi[8], lo[8];
 #pragma unroll
@@ -294,11 +278,6 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
     }
     tmem_wait_st();
     tc_fence_before();
-    if (v_out && blockIdx.y == 0 && tile.a < l.R) {   // columns past the rank's last step
-        const int rest = l.r - ksteps * 16;
-        for (int e = tid; e < tile.count * rest; e += kUpThreads)
-            v_out[(int64_t)(tile.i0 + e / rest) * l.r + ksteps * 16 + e % rest] = 0.0f;
-    }
     const float f = scaled && tile.a < l.R ? l.scales[tile.a] : 1.0f;
     for (int s = 0; s <= steps; ++s) {
         if (s < steps) {
@@ -327,9 +306,9 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
             const int row = warp * 32 + lane;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint32_t v[32];
-                tmem_ld_x32(tm + lanes + (e & 1) * 64 + h * 32, v);
-                tmem_wait_ld(v);
+                uint32_t r[32];
+                tmem_ld_x32(tm + lanes + (e & 1) * 64 + h * 32, r);
+                tmem_wait_ld(r);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const uint32_t at = st + sw128(row, h * 4 + c);
@@ -337,8 +316,8 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
                     uint32_t *w = reinterpret_cast<uint32_t *>(&y);
 #pragma unroll
                     for (int p = 0; p < 4; ++p)
-                        w[p] = bf16x2_from_f32(fmaf(f, __uint_as_float(v[c * 8 + 2 * p]), __uint_as_float(w[p] << 16)),
-                                               fmaf(f, __uint_as_float(v[c * 8 + 2 * p + 1]),
+                        w[p] = bf16x2_from_f32(fmaf(f, __uint_as_float(r[c * 8 + 2 * p]), __uint_as_float(w[p] << 16)),
+                                               fmaf(f, __uint_as_float(r[c * 8 + 2 * p + 1]),
                                                     __uint_as_float(w[p] & 0xFFFF0000u)));
                     st_shared_v4(at, y);
                 }
@@ -364,70 +343,63 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
 
 int pad_rank(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 
+// How many ways to share `steps` of 64 columns so that the tiles fill two CTAs an SM
+// once, four steps a share at least.
+int shares(const LoraArgs &l, int steps, int num_sms, int most)
+{
+    const int64_t want = std::min<int64_t>(2 * (int64_t)num_sms / (l.T / kRows + 1), most);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(want, steps / 4));
+}
+
 template <int RP>
-cudaError_t run_down(const LoraArgs &l, const LoraPlan &p, const uint16_t *x, int64_t xs, const uint16_t *W, int C,
-                     bool scaled, float *part, cudaStream_t st)
+cudaError_t run_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *W, int C,
+                     bool scaled, float *v, cudaStream_t st)
 {
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(tile_down_kernel<RP>), DownCfg<RP>::kSmem);
     if (e != cudaSuccess)
         return e;
-    const int cols = ((C + 63) / 64 + p.splits - 1) / p.splits * 64;
-    const dim3 grid((unsigned)most_tiles(l.T, l.R, kRows, false), p.splits);
-    tile_down_kernel<RP><<<grid, kDownThreads, DownCfg<RP>::kSmem, st>>>(l, x, xs, W, C, scaled, part, cols,
-                                                                        Waits{p.status, p.timeout_ns});
-    return cudaGetLastError();
+    const int steps = (C + 63) / 64, want = shares(l, steps, p.num_sms, kMaxSplits), per = (steps + want - 1) / want;
+    const int splits = (steps + per - 1) / per;   // none empty
+    const dim3 grid((unsigned)most_tiles(l.T, l.R, kRows, false), splits);
+    return launch_split(tile_down_kernel<RP>, grid, kDownThreads, DownCfg<RP>::kSmem, splits, st, l, x, xs, W, C, scaled,
+                        v, per * 64, Waits{p.status, p.timeout_ns});
 }
 
 template <int RP>
-cudaError_t run_up(const LoraArgs &l, const LoraPlan &p, const float *part, const uint16_t *W, int C, bool scaled,
-                   const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *v, cudaStream_t st)
+cudaError_t run_up(const LoraArgs &l, const LoraCall &p, const float *v, const uint16_t *W, int C, bool scaled,
+                   const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st)
 {
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(tile_up_kernel<RP>), UpCfg<RP>::kSmem);
     if (e != cudaSuccess)
         return e;
-    const int64_t tiles = most_tiles(l.T, l.R, kRows, base != out);
-    // ranges of columns that fill two CTAs an SM once, four steps at least
-    const int steps = (C + 63) / 64;
-    const int64_t want = 2 * (int64_t)p.num_sms / std::max<int64_t>(1, l.T / kRows + 1);
-    const int ranges = (int)std::max<int64_t>(1, std::min<int64_t>(want, steps / 4));
-    const int per = (steps + ranges - 1) / ranges;
-    const dim3 grid((unsigned)tiles, (steps + per - 1) / per);
-    tile_up_kernel<RP><<<grid, kUpThreads, UpCfg<RP>::kSmem, st>>>(l, part, p.splits, W, C, scaled, base, bs, out, os, v,
-                                                                  per * 64, Waits{p.status, p.timeout_ns});
+    const int steps = (C + 63) / 64, ranges = shares(l, steps, p.num_sms, steps), per = (steps + ranges - 1) / ranges;
+    const dim3 grid((unsigned)most_tiles(l.T, l.R, kRows, base != out), (steps + per - 1) / per);
+    tile_up_kernel<RP><<<grid, kUpThreads, UpCfg<RP>::kSmem, st>>>(l, v, W, C, scaled, base, bs, out, os, per * 64,
+                                                                  Waits{p.status, p.timeout_ns});
     return cudaGetLastError();
 }
 
 }  // namespace
 
-int lora_tile_splits(int64_t T, int C, int num_sms)
-{
-    // splits that fill two CTAs an SM once, four stages at least
-    const int64_t want = 2 * (int64_t)num_sms / std::max<int64_t>(1, T / kRows + 1);
-    int splits = (int)std::max<int64_t>(1, std::min<int64_t>({want, (C + 63) / 64 / 4, 16}));
-    const int steps = (C + 63) / 64, per = (steps + splits - 1) / splits;
-    return (steps + per - 1) / per;   // none empty
-}
-
-cudaError_t launch_tile_down(const LoraArgs &l, const LoraPlan &p, const uint16_t *x, int64_t xs, const uint16_t *W,
-                             int C, bool scaled, float *part, cudaStream_t st)
+cudaError_t launch_tile_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *W,
+                             int C, bool scaled, float *v, cudaStream_t st)
 {
     switch (pad_rank(l.r)) {
-    case 16: return run_down<16>(l, p, x, xs, W, C, scaled, part, st);
-    case 32: return run_down<32>(l, p, x, xs, W, C, scaled, part, st);
-    case 64: return run_down<64>(l, p, x, xs, W, C, scaled, part, st);
-    default: return run_down<128>(l, p, x, xs, W, C, scaled, part, st);
+    case 16: return run_down<16>(l, p, x, xs, W, C, scaled, v, st);
+    case 32: return run_down<32>(l, p, x, xs, W, C, scaled, v, st);
+    case 64: return run_down<64>(l, p, x, xs, W, C, scaled, v, st);
+    default: return run_down<128>(l, p, x, xs, W, C, scaled, v, st);
     }
 }
 
-cudaError_t launch_tile_up(const LoraArgs &l, const LoraPlan &p, const float *part, const uint16_t *W, int C,
-                           bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *v,
-                           cudaStream_t st)
+cudaError_t launch_tile_up(const LoraArgs &l, const LoraCall &p, const float *v, const uint16_t *W, int C,
+                           bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st)
 {
     switch (pad_rank(l.r)) {
-    case 16: return run_up<16>(l, p, part, W, C, scaled, base, bs, out, os, v, st);
-    case 32: return run_up<32>(l, p, part, W, C, scaled, base, bs, out, os, v, st);
-    case 64: return run_up<64>(l, p, part, W, C, scaled, base, bs, out, os, v, st);
-    default: return run_up<128>(l, p, part, W, C, scaled, base, bs, out, os, v, st);
+    case 16: return run_up<16>(l, p, v, W, C, scaled, base, bs, out, os, st);
+    case 32: return run_up<32>(l, p, v, W, C, scaled, base, bs, out, os, st);
+    case 64: return run_up<64>(l, p, v, W, C, scaled, base, bs, out, os, st);
+    default: return run_up<128>(l, p, v, W, C, scaled, base, bs, out, os, st);
     }
 }
 
