@@ -776,7 +776,8 @@ GEMMAR_API int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stri
         return rc;
     if (!aligned16(v) || !aligned16(dA) || !aligned16(dB))
         return GEMMAR_ERR_ALIGN;
-    if (T * r > ctx->W_floats)
+    const int64_t w_floats = (T * r + 3) / 4 * 4;
+    if (w_floats + lora_grad_floats(T, r, (int)K, (int)N) > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
     cudaStream_t st = as_stream(stream);
     const LoraArgs l{order, offsets, ranks, scales, T, R, r};
@@ -784,8 +785,8 @@ GEMMAR_API int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stri
     float *w = ctx->W;
     CUDA_OK(launch_lora_down(l, p, dy, dy_stride, B, (int)N, true, w, st));
     CUDA_OK(launch_lora_up(l, p, w, A, (int)K, false, dx0, dx0_stride, dx, dx_stride, st));
-    CUDA_OK(launch_lora_grad(l, w, x, x_stride, (int)K, false, dA, st));
-    CUDA_OK(launch_lora_grad(l, v, dy, dy_stride, (int)N, true, dB, st));
+    CUDA_OK(launch_lora_grad(l, p, w, x, x_stride, (int)K, dA, v, dy, dy_stride, (int)N, dB, ctx->W + w_floats,
+                             ctx->W_floats - w_floats, st));
     return GEMMAR_OK;
 }
 

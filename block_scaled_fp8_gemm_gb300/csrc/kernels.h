@@ -218,8 +218,11 @@ cudaError_t launch_tile_down(const LoraArgs &l, const LoraCall &p, const uint16_
                              int C, bool scaled, float *v, cudaStream_t st);
 cudaError_t launch_tile_up(const LoraArgs &l, const LoraCall &p, const float *v, const uint16_t *W, int C,
                            bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st);
-// G[a,j,c] = f sum_{tokens of a} p[i,j] x[order[i],c]
-cudaError_t launch_lora_grad(const LoraArgs &l, const float *p, const uint16_t *x, int64_t xs, int C, bool scaled,
-                             uint16_t *G, cudaStream_t st);
+// dA[a,j,c] = sum_{tokens of a} w[i,j] x[order[i],c] and dB[a,j,c] = scales[a] sum v[i,j] dy[order[i],c];
+// ws: lora_grad_floats at least, more lets the tokens of a large adapter be shared out
+int64_t lora_grad_floats(int64_t T, int r, int K, int N);
+cudaError_t launch_lora_grad(const LoraArgs &l, const LoraCall &p, const float *w, const uint16_t *x, int64_t xs, int K,
+                             uint16_t *dA, const float *v, const uint16_t *dy, int64_t ys, int N, uint16_t *dB, float *ws,
+                             int64_t ws_floats, cudaStream_t st);
 
 }  // namespace gemmar

@@ -17,9 +17,6 @@ using namespace ptx;
 
 namespace {
 
-__device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-__device__ __forceinline__ uint16_t to_bf(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
-
 // Counting sort by adapter in one CTA of 32 warps: a warp counts its contiguous
 // share of the tokens per adapter, the counts are summed over adapters and
 // warps, and the warp then places its tokens in order.  Stable, so the sums
@@ -126,8 +123,8 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_down_kernel(const LoraArgs
 {
     __shared__ float sums[kFewWarps][kFewRanks][kFewTokens + 1];
     const Tile tile = find_tile(l, blockIdx.x, kFewTokens, false);
-    const int rank = tile.count ? rank_of(l, tile.a) : 0, j0 = blockIdx.z * kFewRanks;
-    if (tile.count == 0)
+    const int rank = tile.of ? rank_of(l, tile.a) : 0, j0 = blockIdx.z * kFewRanks;
+    if (tile.of == 0)
         return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     float acc[2][4][4] = {};
@@ -221,7 +218,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_up_kernel(const LoraArgs l
     constexpr int kRow = GEMMAR_LORA_MAX_RANK / 2 + 4;   // pairs of a token, padded off the banks
     __shared__ uint32_t hi[kFewTokens][kRow], lo[kFewTokens][kRow];
     const Tile tile = find_tile(l, blockIdx.y, kFewTokens, base != out);
-    if (tile.count == 0)
+    if (tile.of == 0)
         return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int rank = tile.a < l.R ? rank_of(l, tile.a) : 0, steps = (rank + 15) / 16;
@@ -302,35 +299,6 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_up_kernel(const LoraArgs l
     }
 }
 
-__global__ void __launch_bounds__(128) grad_kernel(const LoraArgs l, const float *__restrict__ p,
-                                                   const uint16_t *__restrict__ x, int64_t xs, int C, bool scaled,
-                                                   uint16_t *__restrict__ G)
-{
-    const int a = blockIdx.y, c = blockIdx.x * 128 + threadIdx.x;
-    if (c >= C)
-        return;
-    const int rank = rank_of(l, a);
-    const int64_t lo = max(l.offsets[a], 0), hi = min((int64_t)l.offsets[a + 1], l.T);
-    const float f = scaled ? l.scales[a] : 1.0f;
-    for (int j0 = 0; j0 < l.r; j0 += 16) {
-        float s[16] = {};
-        for (int64_t i = lo; i < hi; ++i) {
-            const int t = l.order[i];
-            if (t < 0 || t >= l.T)
-                continue;
-            const float xv = bf(x[t * xs + c]);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (j0 + j < rank)
-                    s[j] += p[i * l.r + j0 + j] * xv;
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j0 + j < l.r)
-                G[((int64_t)a * l.r + j0 + j) * C + c] = to_bf(f * s[j]);
-    }
-}
-
 }  // namespace
 
 cudaError_t launch_lora_plan(const int32_t *ids, int64_t T, int R, int32_t *order, int32_t *offsets, cudaStream_t st)
@@ -367,13 +335,6 @@ cudaError_t launch_lora_up(const LoraArgs &l, const LoraCall &p, const float *v,
         return launch_tile_up(l, p, v, W, C, scaled, base, bs, out, os, st);
     const dim3 grid((C + kFewCols - 1) / kFewCols, (unsigned)most_tiles(l.T, l.R, kFewTokens, base != out));
     few_up_kernel<<<grid, kFewWarps * 32, 0, st>>>(l, v, W, C, scaled, base, bs, out, os);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_lora_grad(const LoraArgs &l, const float *p, const uint16_t *x, int64_t xs, int C, bool scaled,
-                             uint16_t *G, cudaStream_t st)
-{
-    grad_kernel<<<dim3((C + 127) / 128, l.R), 128, 0, st>>>(l, p, x, xs, C, scaled, G);
     return cudaGetLastError();
 }
 

@@ -11,23 +11,31 @@ __device__ __forceinline__ int rank_of(const LoraArgs &l, int a)
 }
 
 // A CTA's share of the tokens: positions [i0, i0 + count) of adapter a (a == R:
-// tokens without one).
+// tokens without one), its tile `index` of `of`.
 struct Tile {
-    int a, i0, count;
+    int a, i0, count, index, of;
 };
 
-// Tile number `want` when every adapter's tokens (and, with `bare`, those without
-// one) are cut into tiles of `size`; count 0 past the last.  Warp-collective: lane l
-// counts the tiles of a contiguous share of the adapters, a scan finds the lane.
-__device__ __forceinline__ Tile find_tile(const LoraArgs &l, int want, int size, bool bare)
+// Where group g's positions begin (g == R: the tokens without an adapter; R + 1: T).
+__device__ __forceinline__ int group_begin(const LoraArgs &l, int g)
 {
-    const int lane = threadIdx.x & 31, groups = l.R + (bare ? 1 : 0), T = (int)l.T;
+    const int T = (int)l.T;
+    return g > l.R ? T : min(max(__ldg(l.offsets + g), 0), T);
+}
+
+// Tile number `want` when every adapter's tokens (and, with `bare`, those without
+// one) are cut into tiles of `size`, an adapter without tokens into `least` (0 or 1)
+// empty ones; of == 0 past the last.  Warp-collective: lane l counts the tiles of a
+// contiguous share of the adapters, a scan finds the lane.
+__device__ __forceinline__ Tile find_tile(const LoraArgs &l, int want, int size, bool bare, int least = 0)
+{
+    const int lane = threadIdx.x & 31, groups = l.R + (bare ? 1 : 0);
     const int per = (groups + 31) / 32, g0 = min(lane * per, groups), g1 = min(g0 + per, groups);
-    auto edge = [&](int g) { return g > l.R ? T : min(max(__ldg(l.offsets + g), 0), T); };
-    int tiles = 0, at = edge(g0);
+    auto cut = [&](int n) { return max(least, (max(n, 0) + size - 1) / size); };
+    int tiles = 0, at = group_begin(l, g0);
     for (int g = g0; g < g1; ++g) {
-        const int next = edge(g + 1);
-        tiles += (max(next - at, 0) + size - 1) / size;
+        const int next = group_begin(l, g + 1);
+        tiles += cut(next - at);
         at = next;
     }
     int before = tiles;
@@ -39,19 +47,17 @@ __device__ __forceinline__ Tile find_tile(const LoraArgs &l, int want, int size,
     }
     before -= tiles;
     const unsigned here = __ballot_sync(0xFFFFFFFFu, want >= before && want < before + tiles);
-    Tile t{0, 0, 0};
+    Tile t{0, 0, 0, 0, 0};
     if (here == 0u)
         return t;
     const int owner = __ffs(here) - 1;
     if (lane == owner) {
         int rest = want - before;
-        at = edge(g0);
+        at = group_begin(l, g0);
         for (int g = g0; g < g1; ++g) {
-            const int next = edge(g + 1), n = (max(next - at, 0) + size - 1) / size;
+            const int next = group_begin(l, g + 1), n = cut(next - at);
             if (rest < n) {
-                t.a = g;
-                t.i0 = at + rest * size;
-                t.count = min(size, next - t.i0);
+                t = Tile{g, at + rest * size, min(size, max(next - at, 0) - rest * size), rest, n};
                 break;
             }
             rest -= n;
@@ -61,7 +67,20 @@ __device__ __forceinline__ Tile find_tile(const LoraArgs &l, int want, int size,
     t.a = __shfl_sync(0xFFFFFFFFu, t.a, owner);
     t.i0 = __shfl_sync(0xFFFFFFFFu, t.i0, owner);
     t.count = __shfl_sync(0xFFFFFFFFu, t.count, owner);
+    t.index = __shfl_sync(0xFFFFFFFFu, t.index, owner);
+    t.of = __shfl_sync(0xFFFFFFFFu, t.of, owner);
     return t;
+}
+
+// Tiles of `size` that the adapters before `a` with more than one tile have (warp-collective).
+__device__ __forceinline__ int split_tiles_before(const LoraArgs &l, int a, int size)
+{
+    int n = 0;
+    for (int g = threadIdx.x & 31; g < a; g += 32) {
+        const int c = (max(group_begin(l, g + 1) - group_begin(l, g), 0) + size - 1) / size;
+        n += c > 1 ? c : 0;
+    }
+    return __reduce_add_sync(0xFFFFFFFFu, n);
 }
 
 // Sum over the CTAs of the cluster, in the order of their ranks, of the fp32 array

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs 
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const Tile tile = find_tile(l, blockIdx.x, kRows, false);
-    if (tile.count == 0)
+    if (tile.of == 0)
         return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t *smem = align_1024(smem_raw);
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const Tile tile = find_tile(l, blockIdx.x, kRows, base != out);
-    if (tile.count == 0)
+    if (tile.of == 0)
         return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem = smem_u32(align_1024(smem_raw));
@@ -341,6 +341,196 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
         tmem_dealloc(tm, Cfg::kTmem);
 }
 
+// ---------------------------------------------------------------- grad
+
+// G[a,j,c] = f sum_i p[i,j] x[t,c] over an adapter's tokens: D[128 columns, ranks] with
+// the tokens as the contracted index, both operands in rows that run along M and N, 64
+// tokens a stage.  p comes as two bf16 parts side by side (p2), so an MMA of twice
+// the ranks gives both products, and the halves are added at the end.  Both gradients
+// of a call are one launch: blockIdx.y counts first dA's and then dB's column tiles.
+constexpr int kGradThreads = 256;
+constexpr int kGradTokens = 64;   // a stage
+constexpr int kGradCols = 128;
+
+template <int RP>
+struct GradCfg {
+    static constexpr int kAtoms = RP <= 32 ? 1 : 2 * RP / 64;   // 64-wide tiles of p2
+    static constexpr int kTile = kGradTokens * 128, kX = 2 * kTile, kStage = kX + kAtoms * kTile;
+    static constexpr int kStages = RP <= 32 ? 4 : RP == 64 ? 3 : 4;
+    static constexpr int kSmem = kStages * kStage + 1024;
+};
+
+struct GradSide {
+    const uint16_t *x;    // tokens' rows
+    int64_t xs;
+    int C, scaled;
+    const uint16_t *p2;   // [T][2 RP]
+    uint16_t *G;
+    float *part;          // [split tile][r][C]
+};
+
+template <int RP>
+__global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs l, const GradSide A, const GradSide B,
+                                                                 int size, const Waits waits)
+{
+    using Cfg = GradCfg<RP>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t done[Cfg::kStages];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    const Tile tile = find_tile(l, blockIdx.x, size, false, 1);
+    if (tile.of == 0)
+        return;
+    const int a_tiles = (A.C + kGradCols - 1) / kGradCols;
+    const bool second = (int)blockIdx.y >= a_tiles;
+    const GradSide &S = second ? B : A;
+    const int c0 = ((int)blockIdx.y - (second ? a_tiles : 0)) * kGradCols;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = smem_u32(align_1024(smem_raw));
+    const int rank = rank_of(l, tile.a);
+    if (tid == 0) {
+        for (int s = 0; s < Cfg::kStages; ++s)
+            mbar_init(done + s, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&tmem_slot, 2 * RP);
+        tmem_relinquish();
+    }
+    const int steps = (tile.count + kGradTokens - 1) / kGradTokens;
+    // x: 16 chunks a token, tokens tid / 16 + 16 i; p2: RP / 4 chunks a token
+    const int ch = tid & 15;
+    const bool in = c0 + ch * 8 < S.C;
+    auto token = [&](int s, int row) {
+        const int i = s * kGradTokens + row;
+        const int t = i < tile.count ? __ldg(l.order + tile.i0 + i) : -1;
+        return t >= 0 && t < l.T ? t : -1;
+    };
+    int next[4];
+    auto look_up = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            next[i] = token(s, (tid >> 4) + 16 * i);
+    };
+    look_up(0);
+    auto fetch = [&](int s) {
+        if (s < steps) {
+            const uint32_t st = base + (s % Cfg::kStages) * Cfg::kStage;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool ok = in && next[i] >= 0;
+                cp_async_cg16_or_zero(st + (ch >> 3) * Cfg::kTile + sw128((tid >> 4) + 16 * i, ch & 7),
+                                      S.x + (ok ? next[i] * S.xs + c0 + ch * 8 : 0), ok);
+            }
+#pragma unroll
+            for (int e = tid; e < kGradTokens * (RP / 4); e += kGradThreads) {
+                const int row = e / (RP / 4), pc = e % (RP / 4), i = s * kGradTokens + row;
+                const bool ok = i < tile.count;
+                cp_async_cg16_or_zero(st + Cfg::kX + (pc >> 3) * Cfg::kTile + sw128(row, pc & 7),
+                                      S.p2 + (ok ? (int64_t)(tile.i0 + i) * (2 * RP) + pc * 8 : 0), ok);
+            }
+            look_up(s + 1);
+        }
+        cp_async_commit();
+    };
+    for (int s = 0; s < Cfg::kStages - 1; ++s)
+        fetch(s);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t d = tmem_slot;
+    for (int s = 0; s < steps; ++s) {
+        cp_async_wait<Cfg::kStages - 2>();
+        fence_async_shared();
+        __syncthreads();
+        if (tid == 0) {
+            tc_fence_after();
+            const uint32_t st = base + (s % Cfg::kStages) * Cfg::kStage;
+#pragma unroll
+            for (int k = 0; k < kGradTokens / 16; ++k)
+                mma_bf16_ss(d, smem_desc(st + k * 2 * kSw, Cfg::kTile, kSw, 2),
+                            smem_desc(st + Cfg::kX + k * 2 * kSw, Cfg::kTile, kSw, 2),
+                            idesc_bf16(kGradCols, 2 * RP, 1, 1), s > 0 || k > 0);
+            tc_commit(done + s % Cfg::kStages);
+        }
+        if (s > 0 && s + Cfg::kStages - 1 < steps)
+            wait_mma(done + (s - 1) % Cfg::kStages, ((s - 1) / Cfg::kStages) & 1, &abort_flag, waits);
+        fetch(s + Cfg::kStages - 1);
+    }
+    if (steps > 0)
+        wait_mma(done + (steps - 1) % Cfg::kStages, ((steps - 1) / Cfg::kStages) & 1, &abort_flag, waits);
+    // lane: a column; the two warps of a lane quarter take half of the ranks each
+    const int c = c0 + (warp & 3) * 32 + lane;
+    const float f = S.scaled ? l.scales[tile.a] : 1.0f;
+    const int slot = tile.of > 1 ? split_tiles_before(l, tile.a, size) + tile.index : 0;
+#pragma unroll
+    for (int j0 = (warp >> 2) * 8; j0 < RP; j0 += 16) {
+        uint32_t hi[8], lo[8];
+        if (steps > 0) {
+            tmem_ld_x8(d + ((uint32_t)((warp & 3) * 32) << 16) + j0, hi);
+            tmem_ld_x8(d + ((uint32_t)((warp & 3) * 32) << 16) + RP + j0, lo);
+            tmem_wait_ld(hi, lo);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int j = j0 + k;
+            const float g = steps > 0 && j < rank ? f * (__uint_as_float(hi[k]) + __uint_as_float(lo[k])) : 0.0f;
+            if (j < l.r && c < S.C) {
+                if (tile.of > 1)
+                    S.part[((int64_t)slot * l.r + j) * S.C + c] = g;
+                else
+                    S.G[((int64_t)tile.a * l.r + j) * S.C + c] = __bfloat16_as_ushort(__float2bfloat16_rn(g));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0)
+        tmem_dealloc(d, 2 * RP);
+}
+
+// The gradients of adapters whose tokens were cut: their tiles' parts in order.
+__global__ void __launch_bounds__(256) grad_join_kernel(const LoraArgs l, const GradSide A, const GradSide B, int size)
+{
+    const int a = blockIdx.x;
+    const int n = (max(group_begin(l, a + 1) - group_begin(l, a), 0) + size - 1) / size;
+    if (n <= 1)
+        return;
+    const GradSide &S = blockIdx.z ? B : A;
+    const int64_t elems = (int64_t)l.r * S.C;
+    const float *part = S.part + (int64_t)split_tiles_before(l, a, size) * elems;
+    for (int64_t e = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4; e < elems; e += (int64_t)gridDim.y * 1024) {
+        float4 s = *reinterpret_cast<const float4 *>(part + e);
+        for (int k = 1; k < n; ++k) {
+            const float4 p = *reinterpret_cast<const float4 *>(part + k * elems + e);
+            s.x += p.x; s.y += p.y; s.z += p.z; s.w += p.w;
+        }
+        uint2 o;
+        o.x = bf16x2_from_f32(s.x, s.y);
+        o.y = bf16x2_from_f32(s.z, s.w);
+        *reinterpret_cast<uint2 *>(S.G + a * elems + e) = o;
+    }
+}
+
+// Two bf16 parts of w and of v (blockIdx.y), [T][RP hi, RP lo], 0 past r.
+__global__ void __launch_bounds__(256) halves_kernel(const float *__restrict__ w, uint32_t *__restrict__ w2,
+                                                     const float *__restrict__ v, uint32_t *__restrict__ v2, int64_t T,
+                                                     int r, int RP)
+{
+    const float *src = blockIdx.y ? v : w;
+    uint32_t *dst = blockIdx.y ? v2 : w2;
+    const int pairs = RP / 2;
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < T * pairs; e += (int64_t)gridDim.x * 256) {
+        const int64_t i = e / pairs;
+        const int p = (int)(e - i * pairs);
+        const float x0 = 2 * p < r ? src[i * r + 2 * p] : 0.0f, x1 = 2 * p + 1 < r ? src[i * r + 2 * p + 1] : 0.0f;
+        const uint32_t h = bf16x2_from_f32(x0, x1);
+        dst[i * RP + p] = h;
+        dst[i * RP + pairs + p] = bf16x2_from_f32(x0 - __uint_as_float(h << 16), x1 - __uint_as_float(h & 0xFFFF0000u));
+    }
+}
+
 int pad_rank(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 
 // How many ways to share `steps` of 64 columns so that the tiles fill two CTAs an SM
@@ -379,6 +569,26 @@ cudaError_t run_up(const LoraArgs &l, const LoraCall &p, const float *v, const u
     return cudaGetLastError();
 }
 
+template <int RP>
+cudaError_t run_grad(const LoraArgs &l, const LoraCall &p, const GradSide &A, const GradSide &B, int size, cudaStream_t st)
+{
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(tile_grad_kernel<RP>), GradCfg<RP>::kSmem);
+    if (e != cudaSuccess)
+        return e;
+    const int tiles = (A.C + kGradCols - 1) / kGradCols + (B.C + kGradCols - 1) / kGradCols;
+    const dim3 grid((unsigned)(l.T / size + l.R), tiles);
+    tile_grad_kernel<RP><<<grid, kGradThreads, GradCfg<RP>::kSmem, st>>>(l, A, B, size, Waits{p.status, p.timeout_ns});
+    return cudaGetLastError();
+}
+
+// Floats of scratch when the tokens are cut into tiles of `size`: the two halves of w
+// and v, and a part of both gradients for every tile of an adapter that has several.
+int64_t grad_floats(int64_t T, int r, int K, int N, int64_t size)
+{
+    const int64_t parts = size < T ? 2 * (T / size) : 0;
+    return 2 * T * pad_rank(r) + parts * r * ((int64_t)K + N);
+}
+
 }  // namespace
 
 cudaError_t launch_tile_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *W,
@@ -401,6 +611,46 @@ cudaError_t launch_tile_up(const LoraArgs &l, const LoraCall &p, const float *v,
     case 64: return run_up<64>(l, p, v, W, C, scaled, base, bs, out, os, st);
     default: return run_up<128>(l, p, v, W, C, scaled, base, bs, out, os, st);
     }
+}
+
+int64_t lora_grad_floats(int64_t T, int r, int K, int N) { return grad_floats(T, r, K, N, T); }
+
+cudaError_t launch_lora_grad(const LoraArgs &l, const LoraCall &p, const float *w, const uint16_t *x, int64_t xs, int K,
+                             uint16_t *dA, const float *v, const uint16_t *dy, int64_t ys, int N, uint16_t *dB, float *ws,
+                             int64_t ws_floats, cudaStream_t st)
+{
+    const int RP = pad_rank(l.r);
+    // cut an adapter's tokens so that one adapter alone would fill the SMs four times,
+    // into tiles of 256 at least, and no finer than the scratch allows
+    const int tiles = (K + kGradCols - 1) / kGradCols + (N + kGradCols - 1) / kGradCols;
+    const int64_t ways = (4 * p.num_sms + tiles - 1) / tiles;
+    int64_t size = std::max<int64_t>(256, ((l.T + ways - 1) / ways + 63) / 64 * 64);
+    while (size < l.T && grad_floats(l.T, l.r, K, N, size) > ws_floats)
+        size *= 2;
+    size = std::min<int64_t>(size, (l.T + 63) / 64 * 64);
+    uint32_t *w2 = reinterpret_cast<uint32_t *>(ws), *v2 = w2 + l.T * RP;
+    float *part = ws + 2 * l.T * RP;
+    const int64_t slots = size < l.T ? 2 * (l.T / size) : 0;
+    const GradSide A{x, xs, K, 0, reinterpret_cast<uint16_t *>(w2), dA, part};
+    const GradSide B{dy, ys, N, 1, reinterpret_cast<uint16_t *>(v2), dB, part + slots * l.r * K};
+    const int64_t pairs = l.T * (RP / 2);
+    const int blocks = (int)std::min<int64_t>((pairs + 255) / 256, 8 * p.num_sms);
+    halves_kernel<<<dim3(blocks, 2), 256, 0, st>>>(w, w2, v, v2, l.T, l.r, RP);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    switch (RP) {
+    case 16: e = run_grad<16>(l, p, A, B, (int)size, st); break;
+    case 32: e = run_grad<32>(l, p, A, B, (int)size, st); break;
+    case 64: e = run_grad<64>(l, p, A, B, (int)size, st); break;
+    default: e = run_grad<128>(l, p, A, B, (int)size, st); break;
+    }
+    if (e != cudaSuccess || size >= l.T)
+        return e;
+    const int64_t most = (int64_t)l.r * std::max(K, N);
+    const int join = (int)std::min<int64_t>((most + 1023) / 1024, std::max(1, 8 * p.num_sms / l.R));
+    grad_join_kernel<<<dim3(l.R, join, 2), 256, 0, st>>>(l, A, B, (int)size);
+    return cudaGetLastError();
 }
 
 }  // namespace gemmar
