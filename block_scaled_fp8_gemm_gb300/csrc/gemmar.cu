@@ -749,13 +749,11 @@ GEMMAR_API int lora_apply(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, 
         return GEMMAR_ERR_ALIGN;
     if (T * r > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
-    if (v == nullptr)
-        v = ctx->W;
     cudaStream_t st = as_stream(stream);
     const LoraArgs l{order, offsets, ranks, scales, T, R, r};
     const LoraCall p{ctx->num_sms, ctx->status, ctx->timeout_ns};
-    CUDA_OK(launch_lora_down(l, p, x, x_stride, A, (int)K, false, v, st));
-    CUDA_OK(launch_lora_up(l, p, v, B, (int)N, true, y, y_stride, out, out_stride, st));
+    CUDA_OK(launch_lora_products(l, p, x, x_stride, A, (int)K, false, v ? v : ctx->W, v != nullptr, B, (int)N, true, y,
+                                 y_stride, out, out_stride, st));
     return GEMMAR_OK;
 }
 
@@ -783,8 +781,8 @@ GEMMAR_API int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stri
     const LoraArgs l{order, offsets, ranks, scales, T, R, r};
     const LoraCall p{ctx->num_sms, ctx->status, ctx->timeout_ns};
     float *w = ctx->W;
-    CUDA_OK(launch_lora_down(l, p, dy, dy_stride, B, (int)N, true, w, st));
-    CUDA_OK(launch_lora_up(l, p, w, A, (int)K, false, dx0, dx0_stride, dx, dx_stride, st));
+    CUDA_OK(launch_lora_products(l, p, dy, dy_stride, B, (int)N, true, w, true, A, (int)K, false, dx0, dx0_stride, dx,
+                                 dx_stride, st));
     CUDA_OK(launch_lora_grad(l, p, w, x, x_stride, (int)K, dA, v, dy, dy_stride, (int)N, dB, ctx->W + w_floats,
                              ctx->W_floats - w_floats, st));
     return GEMMAR_OK;

@@ -206,14 +206,15 @@ struct LoraCall {
     ptx::DevStatus *status;
     uint64_t timeout_ns;
 };
-// v[i,j] = f sum_c x[order[i],c] W[a,j,c], f = scales[a] if scaled, else 1; 0 for j past the rank
-cudaError_t launch_lora_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *W,
-                             int C, bool scaled, float *v, cudaStream_t st);
-// out[t,c] = base[t,c] + f sum_j v[i,j] W[a,j,c]; rows without an adapter: base
-cudaError_t launch_lora_up(const LoraArgs &l, const LoraCall &p, const float *v, const uint16_t *W, int C,
-                           bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st);
-// Few tokens go to the kernels that load straight into registers (lora.cu), many to
-// the tiles on the tensor cores (lora_tile.cu).
+// Both products of a call:
+//   v[i,j] = f sum_c x[order[i],c] Wd[a,j,c]            (0 for j past the rank; in memory if v_asked)
+//   out[t,c] = base[t,c] + f sum_j v[i,j] Wu[a,j,c]     (rows without an adapter: base)
+// with f = scales[a] where scaled, else 1.  Few tokens go to one kernel that loads
+// straight into registers (lora.cu), many to tiles on the tensor cores (lora_tile.cu),
+// which pass v on through memory.
+cudaError_t launch_lora_products(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *Wd,
+                                 int Cd, bool scaled_d, float *v, bool v_asked, const uint16_t *Wu, int Cu, bool scaled_u,
+                                 const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st);
 cudaError_t launch_tile_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *W,
                              int C, bool scaled, float *v, cudaStream_t st);
 cudaError_t launch_tile_up(const LoraArgs &l, const LoraCall &p, const float *v, const uint16_t *W, int C,

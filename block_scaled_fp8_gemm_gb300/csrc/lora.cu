@@ -104,199 +104,271 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 // ---------------------------------------------------------------- few tokens
 //
 // A decode batch: every adapter in it brings its weights for a token or a few, so
-// the weights are what is read, and latency is what counts.  Both kernels load
-// their fragments straight from memory into registers, 16 bytes a lane, no
+// the weights are what is read, and latency is what counts.  One launch does both
+// products: a cluster takes 32 tokens of one adapter, its CTAs share the columns of
+// the first product, exchange v through distributed shared memory, and share the
+// columns of the second, whose weights they have meanwhile asked into L2.
+//
+// Fragments are loaded straight from memory into registers, 16 bytes a lane, no
 // staging: the contraction index of an MMA may be permuted as long as both
 // operands agree, so lane (g, q) takes eight consecutive elements of its row for
 // two MMAs.  Weights are the M operand, tokens the N operand (8 a tile).
 
-constexpr int kFewBatch = 256;   // largest batch for these kernels
+constexpr int kFewBatch = 256;   // largest batch for this kernel
 constexpr int kFewTokens = 32;   // tokens a tile: four N tiles
 constexpr int kFewWarps = 8;
-constexpr int kFewRanks = 32;    // ranks a CTA of the down kernel: two M tiles
+constexpr int kFewRanks = 32;    // ranks at a time in the first product: two M tiles
+constexpr int kPairRow = GEMMAR_LORA_MAX_RANK / 2 + 4;   // rank pairs of a token, padded off the banks
 
-// v[i][j] of a tile: the CTAs of a cluster share the columns (blockIdx.y) and so do a
-// CTA's eight warps; their sums are added in warp and in rank order.
-__global__ void __launch_bounds__(kFewWarps * 32) few_down_kernel(const LoraArgs l, const uint16_t *__restrict__ x,
-                                                                  int64_t xs, const uint16_t *__restrict__ W, int C,
-                                                                  bool scaled, float *__restrict__ v)
+struct FewSmem {
+    float part[GEMMAR_LORA_MAX_RANK][kFewTokens + 1];   // this CTA's sums
+    union {
+        float sums[kFewWarps][kFewRanks][kFewTokens + 1];
+        struct {
+            uint32_t hi[kFewTokens][kPairRow], lo[kFewTokens][kPairRow];
+        } v;
+    };
+};
+
+// One product's weights [R, r, C], and what its result is scaled by.
+struct Factor {
+    const uint16_t *W;
+    int C;
+    bool scaled;
+};
+
+// Sums of 16 MT ranks from j0 over the warp's share of the columns, for 8 NT tokens,
+// into sums[rank][token].
+template <int MT, int NT>
+__device__ __forceinline__ void few_down(const LoraArgs &l, const Tile &tile, int rank, int j0, const Factor &f,
+                                         const uint16_t *__restrict__ x, int64_t xs, float (&sums)[kFewRanks][kFewTokens + 1])
 {
-    __shared__ float sums[kFewWarps][kFewRanks][kFewTokens + 1];
-    const Tile tile = find_tile(l, blockIdx.x, kFewTokens, false);
-    const int rank = tile.of ? rank_of(l, tile.a) : 0, j0 = blockIdx.z * kFewRanks;
-    if (tile.of == 0)
-        return;
+    constexpr int kUnroll = 2 * MT + NT <= 3 ? 8 : 2 * MT + NT <= 6 ? 4 : 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    float acc[2][4][4] = {};
-    if (j0 < rank) {
-        const uint16_t *wr[4];   // rows j0 + g, + 8, + 16, + 24
-        bool wok[4];
+    const uint16_t *wr[2 * MT];   // rows j0 + g, + 8, ...
+    bool wok[2 * MT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = j0 + g + 8 * i;
-            wok[i] = j < rank;
-            wr[i] = W + ((int64_t)tile.a * l.r + (wok[i] ? j : 0)) * C + q * 8;
-        }
-        const int nt = (tile.count + 7) / 8;
-        const uint16_t *xr[4];
-        bool xok[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int i = n * 8 + g;
-            const int t = i < tile.count ? __ldg(l.order + tile.i0 + i) : -1;
-            xok[n] = t >= 0 && t < l.T;
-            xr[n] = x + (xok[n] ? t : 0) * xs + q * 8;
-        }
-        // blocks of 32 columns, dealt evenly to splits and warps
-        const int blocks = (C + 31) / 32, shares = gridDim.y * kFewWarps, share = blockIdx.y * kFewWarps + warp;
-        const int b0 = (int)((int64_t)blocks * share / shares), b1 = (int)((int64_t)blocks * (share + 1) / shares);
-        const bool wide = j0 + 16 < rank;
-#pragma unroll 4
-        for (int b = b0; b < b1; ++b) {
-            const bool in = b * 32 + q * 8 < C;
-            uint4 w[4], xv[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[i] = make_uint4(0, 0, 0, 0);
-                if (in && wok[i])
-                    w[i] = __ldg(reinterpret_cast<const uint4 *>(wr[i] + b * 32));
-            }
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                xv[n] = make_uint4(0, 0, 0, 0);
-                if (in && xok[n])
-                    xv[n] = __ldg(reinterpret_cast<const uint4 *>(xr[n] + b * 32));
-            }
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                if (m == 1 && !wide)
-                    break;
-                const uint32_t lo[4] = {w[2 * m].x, w[2 * m + 1].x, w[2 * m].y, w[2 * m + 1].y};
-                const uint32_t hi[4] = {w[2 * m].z, w[2 * m + 1].z, w[2 * m].w, w[2 * m + 1].w};
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    if (n < nt) {
-                        mma_bf16(acc[m][n], lo, xv[n].x, xv[n].y);
-                        mma_bf16(acc[m][n], hi, xv[n].z, xv[n].w);
-                    }
-                }
-            }
-        }
+    for (int i = 0; i < 2 * MT; ++i) {
+        const int j = j0 + g + 8 * i;
+        wok[i] = j < rank;
+        wr[i] = f.W + ((int64_t)tile.a * l.r + (wok[i] ? j : 0)) * f.C + q * 8;
     }
+    const uint16_t *xr[NT];
+    bool xok[NT];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                sums[warp][m * 16 + g + (e >> 1) * 8][n * 8 + q * 2 + (e & 1)] = acc[m][n][e];
-    __syncthreads();
-    for (int e = threadIdx.x; e < kFewRanks * kFewTokens; e += kFewWarps * 32) {
-        float *at = &sums[0][e / kFewTokens][e % kFewTokens];
-        float s = *at;
-#pragma unroll
-        for (int w = 1; w < kFewWarps; ++w)
-            s += sums[w][e / kFewTokens][e % kFewTokens];
-        *at = s;
+    for (int n = 0; n < NT; ++n) {
+        const int i = n * 8 + g;
+        const int t = i < tile.count ? __ldg(l.order + tile.i0 + i) : -1;
+        xok[n] = t >= 0 && t < l.T;
+        xr[n] = x + (xok[n] ? t : 0) * xs + q * 8;
     }
-    const float f = scaled ? l.scales[tile.a] : 1.0f;
-    float *out = v + (int64_t)tile.i0 * l.r + j0;
-    cluster_sum(smem_u32(sums), min(kFewRanks, l.r - j0), tile.count, kFewTokens + 1, gridDim.y,
-                [&](int j, int i, float s) { out[(int64_t)i * l.r + j] = f * s; });
-}
-
-// out rows of a tile, 64 columns a warp; v enters as two bf16 parts.  D[n, token] = sum_j W[j, n] v[token, j]:
-// an MMA's two row halves are the even and odd columns of a lane's eight, so the
-// lane ends with eight consecutive columns of two tokens.
-constexpr int kFewCols = 64 * kFewWarps;
-
-__global__ void __launch_bounds__(kFewWarps * 32) few_up_kernel(const LoraArgs l, const float *__restrict__ v,
-                                                                const uint16_t *__restrict__ W, int C, bool scaled,
-                                                                const uint16_t *base, int64_t bs, uint16_t *out,
-                                                                int64_t os)
-{
-    constexpr int kRow = GEMMAR_LORA_MAX_RANK / 2 + 4;   // pairs of a token, padded off the banks
-    __shared__ uint32_t hi[kFewTokens][kRow], lo[kFewTokens][kRow];
-    const Tile tile = find_tile(l, blockIdx.y, kFewTokens, base != out);
-    if (tile.of == 0)
-        return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int rank = tile.a < l.R ? rank_of(l, tile.a) : 0, steps = (rank + 15) / 16;
-    const int n0 = blockIdx.x * kFewCols + warp * 64 + g * 8;
-    const bool in = n0 < C;
-    const uint16_t *w0 = W + (int64_t)min(tile.a, l.R - 1) * l.r * C + n0;
-    auto load = [&](int s, uint4 (&w)[4]) {
+    // blocks of 32 columns, dealt evenly to the cluster's warps
+    const int blocks = (f.C + 31) / 32, shares = gridDim.y * kFewWarps, share = blockIdx.y * kFewWarps + warp;
+    const int b0 = (int)((int64_t)blocks * share / shares), b1 = (int)((int64_t)blocks * (share + 1) / shares);
+    float acc[MT][NT][4] = {};
+    auto block = [&](int b, bool in) {
+        uint4 w[2 * MT], xv[NT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = s * 16 + q * 2 + (i & 1) + (i >> 1) * 8;
-            w[i] = make_uint4(0, 0, 0, 0);
-            if (in && j < rank)
-                w[i] = __ldg(reinterpret_cast<const uint4 *>(w0 + (int64_t)j * C));
+        for (int i = 0; i < 2 * MT; ++i)
+            w[i] = in && wok[i] ? __ldg(reinterpret_cast<const uint4 *>(wr[i] + b * 32)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            xv[n] = in && xok[n] ? __ldg(reinterpret_cast<const uint4 *>(xr[n] + b * 32)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const uint32_t lo[4] = {w[2 * m].x, w[2 * m + 1].x, w[2 * m].y, w[2 * m + 1].y};
+            const uint32_t hi[4] = {w[2 * m].z, w[2 * m + 1].z, w[2 * m].w, w[2 * m + 1].w};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma_bf16(acc[m][n], lo, xv[n].x, xv[n].y);
+                mma_bf16(acc[m][n], hi, xv[n].z, xv[n].w);
+            }
         }
     };
-    uint4 w[4];
-    load(0, w);   // in flight while v is read
-    const int pairs = steps * 8;
-    for (int e = threadIdx.x; e < kFewTokens * pairs; e += kFewWarps * 32) {
-        const int i = e / pairs, p = e - i * pairs;
-        const float *src = v + (int64_t)(tile.i0 + i) * l.r + 2 * p;
-        const float v0 = i < tile.count && 2 * p < rank ? __ldg(src) : 0.0f;
-        const float v1 = i < tile.count && 2 * p + 1 < rank ? __ldg(src + 1) : 0.0f;
-        const uint32_t h = bf16x2_from_f32(v0, v1);
-        hi[i][p] = h;
-        lo[i][p] = bf16x2_from_f32(v0 - __uint_as_float(h << 16), v1 - __uint_as_float(h & 0xFFFF0000u));
-    }
-    __syncthreads();
-    float acc[4][4][4] = {};   // column pair, token tile, fragment
-    const int nt = (tile.count + 7) / 8;
-    for (int s = 0; s < steps; ++s) {
-        uint4 next[4];
-        load(s + 1, next);
-        const uint32_t rows[4][4] = {{w[0].x, w[0].y, w[0].z, w[0].w}, {w[1].x, w[1].y, w[1].z, w[1].w},
-                                     {w[2].x, w[2].y, w[2].z, w[2].w}, {w[3].x, w[3].y, w[3].z, w[3].w}};
+    int b = b0;
+    for (; b + kUnroll <= b1 && (b + kUnroll) * 32 <= f.C; b += kUnroll) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            if (n < nt) {
+        for (int k = 0; k < kUnroll; ++k)
+            block(b + k, true);
+    }
+    for (; b < b1; ++b)
+        block(b, b * 32 + q * 8 < f.C);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sums[m * 16 + g + (e >> 1) * 8][n * 8 + q * 2 + (e & 1)] = acc[m][n][e];
+}
+
+// out rows of a tile of 8 NT tokens, 64 columns a warp at a time; v enters as two bf16
+// parts.  D[n, token] = sum_j W[j, n] v[token, j]: an MMA's two row halves are the even
+// and odd columns of a lane's eight, so the lane ends with eight consecutive columns of
+// two tokens.
+template <int NT>
+__device__ __forceinline__ void few_up(const LoraArgs &l, const Tile &tile, int rank, const Factor &f, const FewSmem &sm,
+                                       const uint16_t *base, int64_t bs, uint16_t *out, int64_t os)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int steps = (rank + 15) / 16;
+    const float scale = f.scaled && tile.a < l.R ? l.scales[tile.a] : 1.0f;
+    int tok[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = n * 8 + q * 2 + k, t = i < tile.count ? __ldg(l.order + tile.i0 + i) : -1;
+            tok[n][k] = t >= 0 && t < l.T ? t : -1;
+        }
+    for (int b = blockIdx.y * kFewWarps + warp; b * 64 < f.C; b += gridDim.y * kFewWarps) {
+        const int n0 = b * 64 + g * 8;
+        const bool in = n0 < f.C;
+        const uint16_t *w0 = f.W + (int64_t)min(tile.a, l.R - 1) * l.r * f.C + n0;
+        auto load = [&](int s, uint4 (&w)[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = s * 16 + q * 2 + (i & 1) + (i >> 1) * 8;
+                w[i] = in && j < rank ? __ldg(reinterpret_cast<const uint4 *>(w0 + (int64_t)j * f.C)) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        uint4 w[4], y[NT][2];
+        load(0, w);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                y[n][k] = base && in && tok[n][k] >= 0 ? *reinterpret_cast<const uint4 *>(base + tok[n][k] * bs + n0)
+                                                       : make_uint4(0, 0, 0, 0);
+        float acc[4][NT][4] = {};   // column pair, token tile, fragment
+        for (int s = 0; s < steps; ++s) {
+            uint4 next[4];
+            load(s + 1, next);
+            const uint32_t rows[4][4] = {{w[0].x, w[0].y, w[0].z, w[0].w}, {w[1].x, w[1].y, w[1].z, w[1].w},
+                                         {w[2].x, w[2].y, w[2].z, w[2].w}, {w[3].x, w[3].y, w[3].z, w[3].w}};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
                 const int i = n * 8 + g;
-                const uint32_t h0 = hi[i][s * 8 + q], h1 = hi[i][s * 8 + 4 + q];
-                const uint32_t l0 = lo[i][s * 8 + q], l1 = lo[i][s * 8 + 4 + q];
+                const uint32_t h0 = sm.v.hi[i][s * 8 + q], h1 = sm.v.hi[i][s * 8 + 4 + q];
+                const uint32_t l0 = sm.v.lo[i][s * 8 + q], l1 = sm.v.lo[i][s * 8 + 4 + q];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const uint32_t a[4] = {__byte_perm(rows[0][c], rows[1][c], 0x5410), __byte_perm(rows[0][c], rows[1][c], 0x7632),
-                                           __byte_perm(rows[2][c], rows[3][c], 0x5410), __byte_perm(rows[2][c], rows[3][c], 0x7632)};
+                    const uint32_t a[4] = {
+                        __byte_perm(rows[0][c], rows[1][c], 0x5410), __byte_perm(rows[0][c], rows[1][c], 0x7632),
+                        __byte_perm(rows[2][c], rows[3][c], 0x5410), __byte_perm(rows[2][c], rows[3][c], 0x7632)};
                     mma_bf16(acc[c][n], a, h0, h1);
                     mma_bf16(acc[c][n], a, l0, l1);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = next[i];
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = next[i];
-    }
-    if (!in)
-        return;
-    const float f = scaled && tile.a < l.R ? l.scales[tile.a] : 1.0f;
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
+            for (int k = 0; k < 2; ++k) {
+                if (!in || tok[n][k] < 0)
+                    continue;
+                uint32_t yw[4] = {y[n][k].x, y[n][k].y, y[n][k].z, y[n][k].w};
+                if (rank > 0) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int i = n * 8 + q * 2 + k;
-            const int t = i < tile.count ? __ldg(l.order + tile.i0 + i) : -1;
-            if (t < 0 || t >= l.T)
-                continue;
-            uint4 y = make_uint4(0, 0, 0, 0);
-            if (base)
-                y = *reinterpret_cast<const uint4 *>(base + t * bs + n0);
-            if (rank > 0) {
-                uint32_t *yw = reinterpret_cast<uint32_t *>(&y);
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    yw[c] = bf16x2_from_f32(fmaf(f, acc[c][n][k], __uint_as_float(yw[c] << 16)),
-                                            fmaf(f, acc[c][n][2 + k], __uint_as_float(yw[c] & 0xFFFF0000u)));
+                    for (int c = 0; c < 4; ++c)
+                        yw[c] = bf16x2_from_f32(fmaf(scale, acc[c][n][k], __uint_as_float(yw[c] << 16)),
+                                                fmaf(scale, acc[c][n][2 + k], __uint_as_float(yw[c] & 0xFFFF0000u)));
+                }
+                *reinterpret_cast<uint4 *>(out + tok[n][k] * os + n0) = make_uint4(yw[0], yw[1], yw[2], yw[3]);
             }
-            *reinterpret_cast<uint4 *>(out + t * os + n0) = y;
         }
     }
+}
+
+__global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const LoraArgs l, const uint16_t *__restrict__ x, int64_t xs,
+                                                              const Factor down, const Factor up, const uint16_t *base,
+                                                              int64_t bs, uint16_t *out, int64_t os, float *v_out)
+{
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    FewSmem &sm = *reinterpret_cast<FewSmem *>(smem_raw);
+    const Tile tile = find_tile(l, blockIdx.x, kFewTokens, base != out);
+    if (tile.of == 0)
+        return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = tile.a < l.R ? rank_of(l, tile.a) : 0, ctas = gridDim.y;
+    const int pairs = (rank + 15) / 16 * 8;
+    // the 128-byte pieces of the second product's operands that this warp will read
+    for (int b = blockIdx.y * kFewWarps + warp; b * 64 < up.C; b += ctas * kFewWarps) {
+        for (int j = lane; j < rank; j += 32)
+            prefetch_l2(up.W + ((int64_t)tile.a * l.r + j) * up.C + b * 64);
+        if (base && lane < tile.count) {
+            const int t = __ldg(l.order + tile.i0 + lane);
+            if (t >= 0 && t < l.T)
+                prefetch_l2(base + t * bs + b * 64);
+        }
+    }
+    for (int j0 = 0; j0 < rank; j0 += kFewRanks) {
+        const bool wide = rank - j0 > 16;
+        if (tile.count <= 8) {
+            if (wide)
+                few_down<2, 1>(l, tile, rank, j0, down, x, xs, sm.sums[warp]);
+            else
+                few_down<1, 1>(l, tile, rank, j0, down, x, xs, sm.sums[warp]);
+        } else if (wide) {
+            few_down<2, 4>(l, tile, rank, j0, down, x, xs, sm.sums[warp]);
+        } else {
+            few_down<1, 4>(l, tile, rank, j0, down, x, xs, sm.sums[warp]);
+        }
+        __syncthreads();
+        const int nj = min(kFewRanks, rank - j0);
+        for (int e = tid; e < nj * tile.count; e += kFewWarps * 32) {
+            const int j = e / tile.count, i = e - j * tile.count;
+            float s = sm.sums[0][j][i];
+#pragma unroll
+            for (int w = 1; w < kFewWarps; ++w)
+                s += sm.sums[w][j][i];
+            sm.part[j0 + j][i] = s;
+        }
+        __syncthreads();
+    }
+    if (rank > 0) {
+        if (ctas > 1)
+            cluster_sync();
+        // v, in rank order, by every CTA for itself
+        const float f = down.scaled ? l.scales[tile.a] : 1.0f;
+        const int rows = tile.count <= 8 ? 8 : kFewTokens;
+        for (int e = tid; e < rows * pairs; e += kFewWarps * 32) {
+            const int i = e / pairs, p = e - i * pairs;
+            float v[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int j = 2 * p + k;
+                if (i < tile.count && j < rank) {
+                    const uint32_t at = smem_u32(&sm.part[j][i]);
+                    for (int c = 0; c < ctas; ++c)
+                        v[k] += ctas > 1 ? ld_shared_cluster_f32(mapa_shared(at, c)) : sm.part[j][i];
+                    v[k] *= f;
+                }
+                if (v_out && blockIdx.y == 0 && i < tile.count && j < l.r)
+                    v_out[(int64_t)(tile.i0 + i) * l.r + j] = v[k];
+            }
+            const uint32_t h = bf16x2_from_f32(v[0], v[1]);
+            sm.v.hi[i][p] = h;
+            sm.v.lo[i][p] = bf16x2_from_f32(v[0] - __uint_as_float(h << 16), v[1] - __uint_as_float(h & 0xFFFF0000u));
+        }
+        if (ctas > 1)
+            cluster_arrive();   // its sums have been read
+    }
+    if (v_out && blockIdx.y == 0 && tile.a < l.R) {   // columns past the rank's last step
+        const int rest = l.r - 2 * pairs;
+        for (int e = tid; e < tile.count * rest; e += kFewWarps * 32)
+            v_out[(int64_t)(tile.i0 + e / rest) * l.r + 2 * pairs + e % rest] = 0.0f;
+    }
+    __syncthreads();
+    if (tile.count <= 8)
+        few_up<1>(l, tile, rank, up, sm, base, bs, out, os);
+    else
+        few_up<4>(l, tile, rank, up, sm, base, bs, out, os);
+    if (rank > 0 && ctas > 1)
+        cluster_wait();   // no CTA leaves while another reads its sums
 }
 
 }  // namespace
@@ -314,28 +386,24 @@ cudaError_t launch_lora_plan(const int32_t *ids, int64_t T, int R, int32_t *orde
     return cudaGetLastError();
 }
 
-cudaError_t launch_lora_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *W,
-                             int C, bool scaled, float *v, cudaStream_t st)
+cudaError_t launch_lora_products(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *Wd,
+                                 int Cd, bool scaled_d, float *v, bool v_asked, const uint16_t *Wu, int Cu, bool scaled_u,
+                                 const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st)
 {
-    if (l.T > kFewBatch)
-        return launch_tile_down(l, p, x, xs, W, C, scaled, v, st);
-    // two CTAs an SM, a block of 32 columns a warp at least
-    const int64_t tiles = most_tiles(l.T, l.R, kFewTokens, false);
-    const int rank_blocks = (l.r + kFewRanks - 1) / kFewRanks;
-    const int64_t want = std::min<int64_t>({2 * (int64_t)p.num_sms / (tiles * rank_blocks), (C + 31) / 32 / kFewWarps, kMaxSplits});
-    const int splits = (int)std::max<int64_t>(1, want);
-    return launch_split(few_down_kernel, dim3((unsigned)tiles, splits, rank_blocks), kFewWarps * 32, 0, splits, st, l, x, xs,
-                        W, C, scaled, v);
-}
-
-cudaError_t launch_lora_up(const LoraArgs &l, const LoraCall &p, const float *v, const uint16_t *W, int C,
-                           bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st)
-{
-    if (l.T > kFewBatch)
-        return launch_tile_up(l, p, v, W, C, scaled, base, bs, out, os, st);
-    const dim3 grid((C + kFewCols - 1) / kFewCols, (unsigned)most_tiles(l.T, l.R, kFewTokens, base != out));
-    few_up_kernel<<<grid, kFewWarps * 32, 0, st>>>(l, v, W, C, scaled, base, bs, out, os);
-    return cudaGetLastError();
+    if (l.T > kFewBatch) {
+        const cudaError_t e = launch_tile_down(l, p, x, xs, Wd, Cd, scaled_d, v, st);
+        return e != cudaSuccess ? e : launch_tile_up(l, p, v, Wu, Cu, scaled_u, base, bs, out, os, st);
+    }
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(few_kernel), sizeof(FewSmem));
+    if (e != cudaSuccess)
+        return e;
+    // clusters as large as fill the SMs twice
+    const int64_t tiles = most_tiles(l.T, l.R, kFewTokens, base != out);
+    int ctas = kMaxSplits;
+    while (ctas > 1 && tiles * ctas > 2 * p.num_sms)
+        ctas /= 2;
+    return launch_split(few_kernel, dim3((unsigned)tiles, ctas), kFewWarps * 32, sizeof(FewSmem), ctas, st, l, x, xs,
+                        Factor{Wd, Cd, scaled_d}, Factor{Wu, Cu, scaled_u}, base, bs, out, os, v_asked ? v : nullptr);
 }
 
 }  // namespace gemmar
