@@ -149,7 +149,8 @@ def _bf16(t: torch.Tensor, name: str) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle: building a torch.cuda.Stream for it takes 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -363,34 +364,37 @@ def fused_gemm_reduce_noalloc_status():
 
 # ---- the residual stream after wo_b, and adapters beside it --------------------------
 
-def _shaped(t: torch.Tensor, shape, name: str) -> None:
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+# A decode step is a few microseconds of device time, so the checks of these entry
+# points read a tensor's type, shape and layout once and explain a refusal apart.
 
-
-def _rows(t: torch.Tensor, shape, name: str, dtype=None):
-    """(pointer, row stride) of a [rows, cols] matrix with contiguous rows, which may be a view."""
+def _refuse(t, shape, name: str, dtype, rows: bool):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    _shaped(t, shape, name)
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have contiguous rows" if rows else f"{name} must be contiguous")
 
 
 def _dense(t, shape, name: str, dtype):
     """Pointer of a contiguous tensor of that shape and type; None stays None."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    p = _ptr(t, name)
-    _shaped(t, shape, name)
-    return p
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, shape, name, dtype, False)
+
+
+def _rows(t, shape, name: str, dtype=None):
+    """(pointer, row stride) of a [rows, cols] matrix with contiguous rows, which may be a view."""
+    if isinstance(t, torch.Tensor) and (dtype is None or t.dtype is dtype) and t.shape == shape and t.is_cuda:
+        row, col = t.stride()
+        if col == 1 or shape[1] == 1:
+            return t.data_ptr(), row if shape[0] > 1 else shape[1]
+    _refuse(t, shape, name, dtype, True)
 
 
 def _gate(gate, M: int, N: int):
@@ -405,6 +409,12 @@ def _gate(gate, M: int, N: int):
     return ptr, stride
 
 
+def _codes(q, shape, name: str):
+    if q is None:
+        return None
+    return _dense(q, shape, name, torch.uint8 if q.dtype is torch.uint8 else torch.float8_e4m3fn)
+
+
 def norm_gate_residual(ctx: Context, y, h, w_pre, t, w_post=None, gate=None, alpha: float = 1.0, beta: float = 1.0,
                        eps: float = 1e-6, u=None, q=None, scales=None, rstd=None, stream=None) -> None:
     """t = alpha*h + beta*gate*norm(y)*w_post and the next block's input norm(t)*w_pre, as bf16 rows u
@@ -415,12 +425,10 @@ def norm_gate_residual(ctx: Context, y, h, w_pre, t, w_post=None, gate=None, alp
     hp, hs = _rows(h, (M, N), "h")
     gp, gs = _gate(gate, M, N)
     f32, bf16 = torch.float32, torch.bfloat16
-    if q is not None:
-        _shaped(q, (M, N), "q")
     _check(_lib.norm_gate_residual(ctx.handle, yp, _xdtype(y), ys, hp, _xdtype(h), hs,
                                    _dense(w_post, (N,), "w_post", f32), _dense(w_pre, (N,), "w_pre", f32), gp, gs,
                                    alpha, beta, eps, M, N, _dense(t, (M, N), "t", h.dtype),
-                                   _dense(u, (M, N), "u", bf16), None if q is None else _u8(q, "q"),
+                                   _dense(u, (M, N), "u", bf16), _codes(q, (M, N), "q"),
                                    _dense(scales, (M, N // 128), "scales", f32), _dense(rstd, (M, 2), "rstd", f32),
                                    _stream(stream)),
            "norm_gate_residual")
