@@ -16,6 +16,7 @@
 
 #include "gemmar.h"
 #include "kernels.h"
+#include "lora.cuh"
 
 #define GEMMAR_API extern "C" __attribute__((visibility("default")))
 
@@ -752,7 +753,7 @@ GEMMAR_API int lora_apply(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, 
     cudaStream_t st = as_stream(stream);
     const LoraArgs l{order, offsets, ranks, scales, T, R, r};
     const LoraCall p{ctx->num_sms, ctx->status, ctx->timeout_ns};
-    CUDA_OK(launch_lora_products(l, p, x, x_stride, A, (int)K, false, v ? v : ctx->W, v != nullptr, B, (int)N, true, y,
+    CUDA_OK(launch_lora_products(l, p, x, x_stride, A, (int)K, false, v ? v : ctx->W, v != nullptr, Halves{}, B, (int)N, true, y,
                                  y_stride, out, out_stride, st));
     return GEMMAR_OK;
 }
@@ -780,10 +781,11 @@ GEMMAR_API int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stri
     cudaStream_t st = as_stream(stream);
     const LoraArgs l{order, offsets, ranks, scales, T, R, r};
     const LoraCall p{ctx->num_sms, ctx->status, ctx->timeout_ns};
-    float *w = ctx->W;
-    CUDA_OK(launch_lora_products(l, p, dy, dy_stride, B, (int)N, true, w, true, A, (int)K, false, dx0, dx0_stride, dx,
+    float *w = ctx->W, *ws = ctx->W + w_floats;
+    const Halves halves = lora_halves(v, T, r, ws);
+    CUDA_OK(launch_lora_products(l, p, dy, dy_stride, B, (int)N, true, w, true, halves, A, (int)K, false, dx0, dx0_stride, dx,
                                  dx_stride, st));
-    CUDA_OK(launch_lora_grad(l, p, w, x, x_stride, (int)K, dA, v, dy, dy_stride, (int)N, dB, ctx->W + w_floats,
+    CUDA_OK(launch_lora_grad(l, p, halves, x, x_stride, (int)K, dA, dy, dy_stride, (int)N, dB, ws,
                              ctx->W_floats - w_floats, st));
     return GEMMAR_OK;
 }

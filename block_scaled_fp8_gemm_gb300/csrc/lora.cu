@@ -285,13 +285,14 @@ __device__ __forceinline__ void few_up(const LoraArgs &l, const Tile &tile, int 
 
 __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const LoraArgs l, const uint16_t *__restrict__ x, int64_t xs,
                                                               const Factor down, const Factor up, const uint16_t *base,
-                                                              int64_t bs, uint16_t *out, int64_t os, float *v_out)
+                                                              int64_t bs, uint16_t *out, int64_t os, float *v_out, const Halves halves)
 {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     FewSmem &sm = *reinterpret_cast<FewSmem *>(smem_raw);
     const Tile tile = find_tile(l, blockIdx.x, kFewTokens, base != out);
     if (tile.of == 0)
         return;
+    grid_launch_next();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = tile.a < l.R ? rank_of(l, tile.a) : 0, ctas = gridDim.y;
     const int pairs = (rank + 15) / 16 * 8;
@@ -347,8 +348,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const LoraArgs l
                         v[k] += ctas > 1 ? ld_shared_cluster_f32(mapa_shared(at, c)) : sm.part[j][i];
                     v[k] *= f;
                 }
-                if (v_out && blockIdx.y == 0 && i < tile.count && j < l.r)
-                    v_out[(int64_t)(tile.i0 + i) * l.r + j] = v[k];
+                if (v_out && blockIdx.y == 0 && i < tile.count) {
+                    if (j < l.r)
+                        v_out[(int64_t)(tile.i0 + i) * l.r + j] = v[k];
+                    put_pair(halves, tile.i0 + i, j, l.r, v[k]);
+                }
             }
             const uint32_t h = bf16x2_from_f32(v[0], v[1]);
             sm.v.hi[i][p] = h;
@@ -358,9 +362,13 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const LoraArgs l
             cluster_arrive();   // its sums have been read
     }
     if (v_out && blockIdx.y == 0 && tile.a < l.R) {   // columns past the rank's last step
-        const int rest = l.r - 2 * pairs;
-        for (int e = tid; e < tile.count * rest; e += kFewWarps * 32)
-            v_out[(int64_t)(tile.i0 + e / rest) * l.r + 2 * pairs + e % rest] = 0.0f;
+        const int rest = pad_rank(l.r) - 2 * pairs;
+        for (int e = tid; e < tile.count * rest; e += kFewWarps * 32) {
+            const int i = tile.i0 + e / rest, j = 2 * pairs + e % rest;
+            if (j < l.r)
+                v_out[(int64_t)i * l.r + j] = 0.0f;
+            put_pair(halves, i, j, l.r, 0.0f);
+        }
     }
     __syncthreads();
     if (tile.count <= 8)
@@ -387,11 +395,11 @@ cudaError_t launch_lora_plan(const int32_t *ids, int64_t T, int R, int32_t *orde
 }
 
 cudaError_t launch_lora_products(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *Wd,
-                                 int Cd, bool scaled_d, float *v, bool v_asked, const uint16_t *Wu, int Cu, bool scaled_u,
+                                 int Cd, bool scaled_d, float *v, bool v_asked, const Halves &halves, const uint16_t *Wu, int Cu, bool scaled_u,
                                  const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st)
 {
     if (l.T > kFewBatch) {
-        const cudaError_t e = launch_tile_down(l, p, x, xs, Wd, Cd, scaled_d, v, st);
+        const cudaError_t e = launch_tile_down(l, p, x, xs, Wd, Cd, scaled_d, v, halves, st);
         return e != cudaSuccess ? e : launch_tile_up(l, p, v, Wu, Cu, scaled_u, base, bs, out, os, st);
     }
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(few_kernel), sizeof(FewSmem));
@@ -402,8 +410,8 @@ cudaError_t launch_lora_products(const LoraArgs &l, const LoraCall &p, const uin
     int ctas = kMaxSplits;
     while (ctas > 1 && tiles * ctas > 2 * p.num_sms)
         ctas /= 2;
-    return launch_split(few_kernel, dim3((unsigned)tiles, ctas), kFewWarps * 32, sizeof(FewSmem), ctas, st, l, x, xs,
-                        Factor{Wd, Cd, scaled_d}, Factor{Wu, Cu, scaled_u}, base, bs, out, os, v_asked ? v : nullptr);
+    return launch(few_kernel, dim3((unsigned)tiles, ctas), kFewWarps * 32, sizeof(FewSmem), ctas, false, st, l, x, xs,
+                        Factor{Wd, Cd, scaled_d}, Factor{Wu, Cu, scaled_u}, base, bs, out, os, v_asked ? v : nullptr, halves);
 }
 
 }  // namespace gemmar

@@ -110,25 +110,59 @@ __device__ __forceinline__ void cluster_sum(uint32_t array, int rows, int cols, 
 
 constexpr int kMaxSplits = 8;   // CTAs of a cluster
 
-// Launch with a cluster of `splits` along y.
+// Launch with a cluster of `splits` along y; with `early` the kernel may start while the
+// one before it in the stream still runs (it calls grid_wait before it reads that one's
+// results, and every CTA does before it ends).
 template <typename... Params, typename... Args>
-cudaError_t launch_split(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int splits, cudaStream_t st,
-                         Args... args)
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int splits, bool early,
+                   cudaStream_t st, Args... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 1;
-    attr.val.clusterDim.y = (unsigned)splits;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = splits > 1 ? 1 : 0;
+    cudaLaunchAttribute attrs[2];
+    cfg.attrs = attrs;
+    if (splits > 1) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attrs[cfg.numAttrs].val.clusterDim.x = 1;
+        attrs[cfg.numAttrs].val.clusterDim.y = (unsigned)splits;
+        attrs[cfg.numAttrs++].val.clusterDim.z = 1;
+    }
+    if (early) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+
+// What the backward pass keeps of w and v for the weight gradients: [T][RP hi, RP lo] in
+// bf16, x = hi + lo to 2^-16 of x, RP the padded rank; nullptr: nothing.
+struct Halves {
+    const float *v;       // the forward pass's v [T, r]
+    uint16_t *w2, *v2;
+    int RP;
+};
+
+__device__ __forceinline__ void put_halves(uint16_t *row, int RP, int j, float x)
+{
+    const uint32_t p = ptx::bf16x2_from_f32(x, x) & 0xFFFFu;
+    const float h = __uint_as_float(p << 16);
+    row[j] = (uint16_t)p;
+    row[RP + j] = (uint16_t)(ptx::bf16x2_from_f32(x - h, 0.0f) & 0xFFFFu);
+}
+
+// Element (i, j) of both, i a position, w its value; j runs over the padded rank.
+__device__ __forceinline__ void put_pair(const Halves &h, int64_t i, int j, int r, float w)
+{
+    if (h.w2 == nullptr)
+        return;
+    put_halves(h.w2 + i * 2 * h.RP, h.RP, j, w);
+    put_halves(h.v2 + i * 2 * h.RP, h.RP, j, j < r ? __ldg(h.v + i * r + j) : 0.0f);
+}
+
+__host__ __device__ constexpr int pad_rank(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 
 // Most tiles of `size` that T tokens of R adapters (and the bare ones) can make.
 inline int64_t most_tiles(int64_t T, int R, int size, bool bare)

@@ -55,15 +55,14 @@ constexpr int kDownThreads = 256;
 template <int RP>   // ranks rounded up to 16, 32, 64 or 128
 struct DownCfg {
     static constexpr int kX = kRows * 128, kW = RP * 128, kStage = kX + kW;
-    static constexpr int kStages = RP == 128 ? 3 : 4;
+    static constexpr int kStages = RP == 16 ? 6 : RP == 32 ? 5 : RP == 64 ? 4 : 3;   // two CTAs an SM
     static constexpr int kSmem = kStages * kStage + 1024;
 };
 
 template <int RP>
 __global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs l, const uint16_t *__restrict__ x,
                                                                  int64_t xs, const uint16_t *__restrict__ W, int C,
-                                                                 bool scaled, float *__restrict__ v, int cols,
-                                                                 const Waits waits)
+                                                                 bool scaled, float *__restrict__ v, const Halves halves, int cols, const Waits waits)
 {
     using Cfg = DownCfg<RP>;
     extern __shared__ uint8_t smem_raw[];
@@ -71,6 +70,7 @@ __global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs 
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const Tile tile = find_tile(l, blockIdx.x, kRows, false);
+    grid_launch_next();
     if (tile.of == 0)
         return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -159,8 +159,11 @@ __global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs 
     }
     const float f = scaled ? l.scales[tile.a] : 1.0f;
     float *out = v + (int64_t)tile.i0 * l.r;
-    cluster_sum(base, tile.count, l.r, kPitch, gridDim.y,
-                [&](int i, int j, float sum) { out[(int64_t)i * l.r + j] = f * sum; });
+    cluster_sum(base, tile.count, RP, kPitch, gridDim.y, [&](int i, int j, float sum) {
+        if (j < l.r)
+            out[(int64_t)i * l.r + j] = f * sum;
+        put_pair(halves, tile.i0 + i, j, l.r, f * sum);
+    });
     tc_fence_before();
     __syncthreads();
     if (warp == 0)
@@ -199,8 +202,10 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const Tile tile = find_tile(l, blockIdx.x, kRows, base != out);
-    if (tile.of == 0)
+    if (tile.of == 0) {
+        grid_wait();
         return;
+    }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem = smem_u32(align_1024(smem_raw));
     const int rank = tile.a < l.R ? rank_of(l, tile.a) : 0;
@@ -252,6 +257,8 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
     tc_fence_after();
     const uint32_t tm = tmem_slot;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    grid_wait();   // v
+    grid_launch_next();
     // v in two bf16 parts, 16 ranks at a time through shared memory
     const int ksteps = (rank + 15) / 16;
     for (int k = 0; k < ksteps; ++k) {
@@ -349,15 +356,16 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
 // the ranks gives both products, and the halves are added at the end.  Both gradients
 // of a call are one launch: blockIdx.y counts first dA's and then dB's column tiles.
 constexpr int kGradThreads = 256;
-constexpr int kGradTokens = 64;   // a stage
-constexpr int kGradCols = 128;
+constexpr int kGradTokens = 32;   // a stage
+constexpr int kGradCols = 256;    // two accumulators
 
 template <int RP>
 struct GradCfg {
     static constexpr int kAtoms = RP <= 32 ? 1 : 2 * RP / 64;   // 64-wide tiles of p2
-    static constexpr int kTile = kGradTokens * 128, kX = 2 * kTile, kStage = kX + kAtoms * kTile;
-    static constexpr int kStages = RP <= 32 ? 4 : RP == 64 ? 3 : 4;
+    static constexpr int kTile = kGradTokens * 128, kX = 4 * kTile, kStage = kX + kAtoms * kTile;
+    static constexpr int kStages = RP <= 32 ? 5 : RP == 64 ? 4 : 6;   // two CTAs an SM (RP 128: one, it takes all of TMEM)
     static constexpr int kSmem = kStages * kStage + 1024;
+    static constexpr int kTmem = 4 * RP;   // 64 to 512
 };
 
 struct GradSide {
@@ -379,8 +387,10 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const Tile tile = find_tile(l, blockIdx.x, size, false, 1);
-    if (tile.of == 0)
+    if (tile.of == 0) {
+        grid_wait();
         return;
+    }
     const int a_tiles = (A.C + kGradCols - 1) / kGradCols;
     const bool second = (int)blockIdx.y >= a_tiles;
     const GradSide &S = second ? B : A;
@@ -395,12 +405,12 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
         fence_mbar_init();
     }
     if (warp == 0) {
-        tmem_alloc(&tmem_slot, 2 * RP);
+        tmem_alloc(&tmem_slot, Cfg::kTmem);
         tmem_relinquish();
     }
     const int steps = (tile.count + kGradTokens - 1) / kGradTokens;
-    // x: 16 chunks a token, tokens tid / 16 + 16 i; p2: RP / 4 chunks a token
-    const int ch = tid & 15;
+    // x: 32 chunks a token, tokens tid / 32 + 8 i; p2: RP / 4 chunks a token
+    const int ch = tid & 31;
     const bool in = c0 + ch * 8 < S.C;
     auto token = [&](int s, int row) {
         const int i = s * kGradTokens + row;
@@ -411,7 +421,7 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
     auto look_up = [&](int s) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            next[i] = token(s, (tid >> 4) + 16 * i);
+            next[i] = token(s, (tid >> 5) + 8 * i);
     };
     look_up(0);
     auto fetch = [&](int s) {
@@ -420,7 +430,7 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const bool ok = in && next[i] >= 0;
-                cp_async_cg16_or_zero(st + (ch >> 3) * Cfg::kTile + sw128((tid >> 4) + 16 * i, ch & 7),
+                cp_async_cg16_or_zero(st + (ch >> 3) * Cfg::kTile + sw128((tid >> 5) + 8 * i, ch & 7),
                                       S.x + (ok ? next[i] * S.xs + c0 + ch * 8 : 0), ok);
             }
 #pragma unroll
@@ -434,6 +444,8 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
         }
         cp_async_commit();
     };
+    grid_wait();   // the two parts of w and v
+    grid_launch_next();
     for (int s = 0; s < Cfg::kStages - 1; ++s)
         fetch(s);
     tc_fence_before();
@@ -448,10 +460,13 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
             tc_fence_after();
             const uint32_t st = base + (s % Cfg::kStages) * Cfg::kStage;
 #pragma unroll
-            for (int k = 0; k < kGradTokens / 16; ++k)
-                mma_bf16_ss(d, smem_desc(st + k * 2 * kSw, Cfg::kTile, kSw, 2),
-                            smem_desc(st + Cfg::kX + k * 2 * kSw, Cfg::kTile, kSw, 2),
-                            idesc_bf16(kGradCols, 2 * RP, 1, 1), s > 0 || k > 0);
+            for (int k = 0; k < kGradTokens / 16; ++k) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)   // 128 columns each
+                    mma_bf16_ss(d + h * 2 * RP, smem_desc(st + h * 2 * Cfg::kTile + k * 2 * kSw, Cfg::kTile, kSw, 2),
+                                smem_desc(st + Cfg::kX + k * 2 * kSw, Cfg::kTile, kSw, 2),
+                                idesc_bf16(128, 2 * RP, 1, 1), s > 0 || k > 0);
+            }
             tc_commit(done + s % Cfg::kStages);
         }
         if (s > 0 && s + Cfg::kStages - 1 < steps)
@@ -460,16 +475,17 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
     }
     if (steps > 0)
         wait_mma(done + (steps - 1) % Cfg::kStages, ((steps - 1) / Cfg::kStages) & 1, &abort_flag, waits);
-    // lane: a column; the two warps of a lane quarter take half of the ranks each
-    const int c = c0 + (warp & 3) * 32 + lane;
+    // lane: a column, warps 4 to 7 the second accumulator's
+    const int c = c0 + warp * 32 + lane;
+    const uint32_t dw = d + (warp >> 2) * 2 * RP + ((uint32_t)((warp & 3) * 32) << 16);
     const float f = S.scaled ? l.scales[tile.a] : 1.0f;
     const int slot = tile.of > 1 ? split_tiles_before(l, tile.a, size) + tile.index : 0;
 #pragma unroll
-    for (int j0 = (warp >> 2) * 8; j0 < RP; j0 += 16) {
+    for (int j0 = 0; j0 < RP; j0 += 8) {
         uint32_t hi[8], lo[8];
         if (steps > 0) {
-            tmem_ld_x8(d + ((uint32_t)((warp & 3) * 32) << 16) + j0, hi);
-            tmem_ld_x8(d + ((uint32_t)((warp & 3) * 32) << 16) + RP + j0, lo);
+            tmem_ld_x8(dw + j0, hi);
+            tmem_ld_x8(dw + RP + j0, lo);
             tmem_wait_ld(hi, lo);
         }
 #pragma unroll
@@ -487,13 +503,14 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
     tc_fence_before();
     __syncthreads();
     if (warp == 0)
-        tmem_dealloc(d, 2 * RP);
+        tmem_dealloc(d, Cfg::kTmem);
 }
 
 // The gradients of adapters whose tokens were cut: their tiles' parts in order.
 __global__ void __launch_bounds__(256) grad_join_kernel(const LoraArgs l, const GradSide A, const GradSide B, int size)
 {
     const int a = blockIdx.x;
+    grid_wait();
     const int n = (max(group_begin(l, a + 1) - group_begin(l, a), 0) + size - 1) / size;
     if (n <= 1)
         return;
@@ -513,26 +530,6 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const LoraArgs l, const 
     }
 }
 
-// Two bf16 parts of w and of v (blockIdx.y), [T][RP hi, RP lo], 0 past r.
-__global__ void __launch_bounds__(256) halves_kernel(const float *__restrict__ w, uint32_t *__restrict__ w2,
-                                                     const float *__restrict__ v, uint32_t *__restrict__ v2, int64_t T,
-                                                     int r, int RP)
-{
-    const float *src = blockIdx.y ? v : w;
-    uint32_t *dst = blockIdx.y ? v2 : w2;
-    const int pairs = RP / 2;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < T * pairs; e += (int64_t)gridDim.x * 256) {
-        const int64_t i = e / pairs;
-        const int p = (int)(e - i * pairs);
-        const float x0 = 2 * p < r ? src[i * r + 2 * p] : 0.0f, x1 = 2 * p + 1 < r ? src[i * r + 2 * p + 1] : 0.0f;
-        const uint32_t h = bf16x2_from_f32(x0, x1);
-        dst[i * RP + p] = h;
-        dst[i * RP + pairs + p] = bf16x2_from_f32(x0 - __uint_as_float(h << 16), x1 - __uint_as_float(h & 0xFFFF0000u));
-    }
-}
-
-int pad_rank(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
-
 // How many ways to share `steps` of 64 columns so that the tiles fill two CTAs an SM
 // once, four steps a share at least.
 int shares(const LoraArgs &l, int steps, int num_sms, int most)
@@ -543,7 +540,7 @@ int shares(const LoraArgs &l, int steps, int num_sms, int most)
 
 template <int RP>
 cudaError_t run_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *W, int C,
-                     bool scaled, float *v, cudaStream_t st)
+                     bool scaled, float *v, const Halves &halves, cudaStream_t st)
 {
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(tile_down_kernel<RP>), DownCfg<RP>::kSmem);
     if (e != cudaSuccess)
@@ -551,8 +548,8 @@ cudaError_t run_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, in
     const int steps = (C + 63) / 64, want = shares(l, steps, p.num_sms, kMaxSplits), per = (steps + want - 1) / want;
     const int splits = (steps + per - 1) / per;   // none empty
     const dim3 grid((unsigned)most_tiles(l.T, l.R, kRows, false), splits);
-    return launch_split(tile_down_kernel<RP>, grid, kDownThreads, DownCfg<RP>::kSmem, splits, st, l, x, xs, W, C, scaled,
-                        v, per * 64, Waits{p.status, p.timeout_ns});
+    return launch(tile_down_kernel<RP>, grid, kDownThreads, DownCfg<RP>::kSmem, splits, false, st, l, x, xs, W, C, scaled, v,
+                  halves, per * 64, Waits{p.status, p.timeout_ns});
 }
 
 template <int RP>
@@ -564,9 +561,8 @@ cudaError_t run_up(const LoraArgs &l, const LoraCall &p, const float *v, const u
         return e;
     const int steps = (C + 63) / 64, ranges = shares(l, steps, p.num_sms, steps), per = (steps + ranges - 1) / ranges;
     const dim3 grid((unsigned)most_tiles(l.T, l.R, kRows, base != out), (steps + per - 1) / per);
-    tile_up_kernel<RP><<<grid, kUpThreads, UpCfg<RP>::kSmem, st>>>(l, v, W, C, scaled, base, bs, out, os, per * 64,
-                                                                  Waits{p.status, p.timeout_ns});
-    return cudaGetLastError();
+    return launch(tile_up_kernel<RP>, grid, kUpThreads, UpCfg<RP>::kSmem, 1, true, st, l, v, W, C, scaled, base, bs, out, os,
+                  per * 64, Waits{p.status, p.timeout_ns});
 }
 
 template <int RP>
@@ -577,8 +573,8 @@ cudaError_t run_grad(const LoraArgs &l, const LoraCall &p, const GradSide &A, co
         return e;
     const int tiles = (A.C + kGradCols - 1) / kGradCols + (B.C + kGradCols - 1) / kGradCols;
     const dim3 grid((unsigned)(l.T / size + l.R), tiles);
-    tile_grad_kernel<RP><<<grid, kGradThreads, GradCfg<RP>::kSmem, st>>>(l, A, B, size, Waits{p.status, p.timeout_ns});
-    return cudaGetLastError();
+    return launch(tile_grad_kernel<RP>, grid, kGradThreads, GradCfg<RP>::kSmem, 1, true, st, l, A, B, size,
+                  Waits{p.status, p.timeout_ns});
 }
 
 // Floats of scratch when the tokens are cut into tiles of `size`: the two halves of w
@@ -592,13 +588,13 @@ int64_t grad_floats(int64_t T, int r, int K, int N, int64_t size)
 }  // namespace
 
 cudaError_t launch_tile_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *W,
-                             int C, bool scaled, float *v, cudaStream_t st)
+                             int C, bool scaled, float *v, const Halves &halves, cudaStream_t st)
 {
     switch (pad_rank(l.r)) {
-    case 16: return run_down<16>(l, p, x, xs, W, C, scaled, v, st);
-    case 32: return run_down<32>(l, p, x, xs, W, C, scaled, v, st);
-    case 64: return run_down<64>(l, p, x, xs, W, C, scaled, v, st);
-    default: return run_down<128>(l, p, x, xs, W, C, scaled, v, st);
+    case 16: return run_down<16>(l, p, x, xs, W, C, scaled, v, halves, st);
+    case 32: return run_down<32>(l, p, x, xs, W, C, scaled, v, halves, st);
+    case 64: return run_down<64>(l, p, x, xs, W, C, scaled, v, halves, st);
+    default: return run_down<128>(l, p, x, xs, W, C, scaled, v, halves, st);
     }
 }
 
@@ -615,31 +611,30 @@ cudaError_t launch_tile_up(const LoraArgs &l, const LoraCall &p, const float *v,
 
 int64_t lora_grad_floats(int64_t T, int r, int K, int N) { return grad_floats(T, r, K, N, T); }
 
-cudaError_t launch_lora_grad(const LoraArgs &l, const LoraCall &p, const float *w, const uint16_t *x, int64_t xs, int K,
-                             uint16_t *dA, const float *v, const uint16_t *dy, int64_t ys, int N, uint16_t *dB, float *ws,
+Halves lora_halves(const float *v, int64_t T, int r, float *ws)
+{
+    uint16_t *w2 = reinterpret_cast<uint16_t *>(ws);
+    return {v, w2, w2 + T * 2 * pad_rank(r), pad_rank(r)};
+}
+
+cudaError_t launch_lora_grad(const LoraArgs &l, const LoraCall &p, const Halves &h, const uint16_t *x, int64_t xs, int K,
+                             uint16_t *dA, const uint16_t *dy, int64_t ys, int N, uint16_t *dB, float *ws,
                              int64_t ws_floats, cudaStream_t st)
 {
-    const int RP = pad_rank(l.r);
-    // cut an adapter's tokens so that one adapter alone would fill the SMs four times,
-    // into tiles of 256 at least, and no finer than the scratch allows
+    // cut an adapter's tokens so that one adapter alone would fill two CTAs an SM, into
+    // tiles of 256 at least, and no finer than the scratch allows
     const int tiles = (K + kGradCols - 1) / kGradCols + (N + kGradCols - 1) / kGradCols;
-    const int64_t ways = (4 * p.num_sms + tiles - 1) / tiles;
+    const int64_t ways = (2 * p.num_sms + tiles - 1) / tiles;
     int64_t size = std::max<int64_t>(256, ((l.T + ways - 1) / ways + 63) / 64 * 64);
     while (size < l.T && grad_floats(l.T, l.r, K, N, size) > ws_floats)
         size *= 2;
     size = std::min<int64_t>(size, (l.T + 63) / 64 * 64);
-    uint32_t *w2 = reinterpret_cast<uint32_t *>(ws), *v2 = w2 + l.T * RP;
-    float *part = ws + 2 * l.T * RP;
+    float *part = ws + 2 * l.T * h.RP;
     const int64_t slots = size < l.T ? 2 * (l.T / size) : 0;
-    const GradSide A{x, xs, K, 0, reinterpret_cast<uint16_t *>(w2), dA, part};
-    const GradSide B{dy, ys, N, 1, reinterpret_cast<uint16_t *>(v2), dB, part + slots * l.r * K};
-    const int64_t pairs = l.T * (RP / 2);
-    const int blocks = (int)std::min<int64_t>((pairs + 255) / 256, 8 * p.num_sms);
-    halves_kernel<<<dim3(blocks, 2), 256, 0, st>>>(w, w2, v, v2, l.T, l.r, RP);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess)
-        return e;
-    switch (RP) {
+    const GradSide A{x, xs, K, 0, h.w2, dA, part};
+    const GradSide B{dy, ys, N, 1, h.v2, dB, part + slots * l.r * K};
+    cudaError_t e = cudaSuccess;
+    switch (h.RP) {
     case 16: e = run_grad<16>(l, p, A, B, (int)size, st); break;
     case 32: e = run_grad<32>(l, p, A, B, (int)size, st); break;
     case 64: e = run_grad<64>(l, p, A, B, (int)size, st); break;
@@ -649,8 +644,7 @@ cudaError_t launch_lora_grad(const LoraArgs &l, const LoraCall &p, const float *
         return e;
     const int64_t most = (int64_t)l.r * std::max(K, N);
     const int join = (int)std::min<int64_t>((most + 1023) / 1024, std::max(1, 8 * p.num_sms / l.R));
-    grad_join_kernel<<<dim3(l.R, join, 2), 256, 0, st>>>(l, A, B, (int)size);
-    return cudaGetLastError();
+    return launch(grad_join_kernel, dim3(l.R, join, 2), 256, 0, 1, true, st, l, A, B, (int)size);
 }
 
 }  // namespace gemmar

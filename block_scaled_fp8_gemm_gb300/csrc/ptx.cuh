@@ -167,6 +167,11 @@ __device__ __forceinline__ void cluster_arrive()
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// Programmatic dependent launch: wait until the kernel before this one (in a stream, as
+// the launch allowed) has completed and its writes are visible; let the next one start.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr)
