@@ -616,10 +616,12 @@ __device__ __forceinline__ void cp_async_cg16(uint32_t dst, const void *src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// The same, or 16 zero bytes where !ok (src is then not read).
+// The same, or 16 zero bytes where !ok (src is then not read).  The 256 bytes around src are
+// asked into L2: for rows that are read on in pieces.
 __device__ __forceinline__ void cp_async_cg16_or_zero(uint32_t dst, const void *src, bool ok)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");
 }
 
 // Make this thread's shared-memory writes (cp.async included, once waited for)
