@@ -748,12 +748,12 @@ GEMMAR_API int lora_apply(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, 
         return rc;
     if (!aligned16(v))
         return GEMMAR_ERR_ALIGN;
-    if (T * r > ctx->W_floats)
+    if (lora_half_floats(T, r) > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
     cudaStream_t st = as_stream(stream);
     const LoraArgs l{order, offsets, ranks, scales, T, R, r};
     const LoraCall p{ctx->num_sms, ctx->status, ctx->timeout_ns};
-    CUDA_OK(launch_lora_products(l, p, x, x_stride, A, (int)K, false, v ? v : ctx->W, v != nullptr, Halves{}, B, (int)N, true, y,
+    CUDA_OK(launch_lora_products(l, p, x, x_stride, A, (int)K, false, v, lora_halves(nullptr, T, r, ctx->W), B, (int)N, true, y,
                                  y_stride, out, out_stride, st));
     return GEMMAR_OK;
 }
@@ -775,18 +775,16 @@ GEMMAR_API int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stri
         return rc;
     if (!aligned16(v) || !aligned16(dA) || !aligned16(dB))
         return GEMMAR_ERR_ALIGN;
-    const int64_t w_floats = (T * r + 3) / 4 * 4;
-    if (w_floats + lora_grad_floats(T, r, (int)K, (int)N) > ctx->W_floats)
+    if (lora_grad_floats(T, r, (int)K, (int)N) > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
     cudaStream_t st = as_stream(stream);
     const LoraArgs l{order, offsets, ranks, scales, T, R, r};
     const LoraCall p{ctx->num_sms, ctx->status, ctx->timeout_ns};
-    float *w = ctx->W, *ws = ctx->W + w_floats;
-    const Halves halves = lora_halves(v, T, r, ws);
-    CUDA_OK(launch_lora_products(l, p, dy, dy_stride, B, (int)N, true, w, true, halves, A, (int)K, false, dx0, dx0_stride, dx,
+    const Halves halves = lora_halves(v, T, r, ctx->W);
+    CUDA_OK(launch_lora_products(l, p, dy, dy_stride, B, (int)N, true, nullptr, halves, A, (int)K, false, dx0, dx0_stride, dx,
                                  dx_stride, st));
-    CUDA_OK(launch_lora_grad(l, p, halves, x, x_stride, (int)K, dA, dy, dy_stride, (int)N, dB, ws,
-                             ctx->W_floats - w_floats, st));
+    CUDA_OK(launch_lora_grad(l, p, halves, x, x_stride, (int)K, dA, dy, dy_stride, (int)N, dB, ctx->W,
+                             ctx->W_floats, st));
     return GEMMAR_OK;
 }
 

@@ -348,8 +348,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const LoraArgs l
                         v[k] += ctas > 1 ? ld_shared_cluster_f32(mapa_shared(at, c)) : sm.part[j][i];
                     v[k] *= f;
                 }
-                if (v_out && blockIdx.y == 0 && i < tile.count) {
-                    if (j < l.r)
+                if (blockIdx.y == 0 && i < tile.count) {
+                    if (v_out && j < l.r)
                         v_out[(int64_t)(tile.i0 + i) * l.r + j] = v[k];
                     put_pair(halves, tile.i0 + i, j, l.r, v[k]);
                 }
@@ -361,11 +361,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const LoraArgs l
         if (ctas > 1)
             cluster_arrive();   // its sums have been read
     }
-    if (v_out && blockIdx.y == 0 && tile.a < l.R) {   // columns past the rank's last step
+    if (blockIdx.y == 0 && tile.a < l.R) {   // columns past the rank's last step
         const int rest = pad_rank(l.r) - 2 * pairs;
         for (int e = tid; e < tile.count * rest; e += kFewWarps * 32) {
             const int i = tile.i0 + e / rest, j = 2 * pairs + e % rest;
-            if (j < l.r)
+            if (v_out && j < l.r)
                 v_out[(int64_t)i * l.r + j] = 0.0f;
             put_pair(halves, i, j, l.r, 0.0f);
         }
@@ -395,12 +395,12 @@ cudaError_t launch_lora_plan(const int32_t *ids, int64_t T, int R, int32_t *orde
 }
 
 cudaError_t launch_lora_products(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *Wd,
-                                 int Cd, bool scaled_d, float *v, bool v_asked, const Halves &halves, const uint16_t *Wu, int Cu, bool scaled_u,
+                                 int Cd, bool scaled_d, float *v, const Halves &halves, const uint16_t *Wu, int Cu, bool scaled_u,
                                  const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st)
 {
     if (l.T > kFewBatch) {
         const cudaError_t e = launch_tile_down(l, p, x, xs, Wd, Cd, scaled_d, v, halves, st);
-        return e != cudaSuccess ? e : launch_tile_up(l, p, v, Wu, Cu, scaled_u, base, bs, out, os, st);
+        return e != cudaSuccess ? e : launch_tile_up(l, p, halves.w2, Wu, Cu, scaled_u, base, bs, out, os, st);
     }
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(few_kernel), sizeof(FewSmem));
     if (e != cudaSuccess)
@@ -411,7 +411,7 @@ cudaError_t launch_lora_products(const LoraArgs &l, const LoraCall &p, const uin
     while (ctas > 1 && tiles * ctas > 2 * p.num_sms)
         ctas /= 2;
     return launch(few_kernel, dim3((unsigned)tiles, ctas), kFewWarps * 32, sizeof(FewSmem), ctas, false, st, l, x, xs,
-                        Factor{Wd, Cd, scaled_d}, Factor{Wu, Cu, scaled_u}, base, bs, out, os, v_asked ? v : nullptr, halves);
+                        Factor{Wd, Cd, scaled_d}, Factor{Wu, Cu, scaled_u}, base, bs, out, os, v, halves);
 }
 
 }  // namespace gemmar

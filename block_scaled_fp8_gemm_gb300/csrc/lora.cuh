@@ -137,29 +137,30 @@ cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, size_t sme
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// What the backward pass keeps of w and v for the weight gradients: [T][RP hi, RP lo] in
-// bf16, x = hi + lo to 2^-16 of x, RP the padded rank; nullptr: nothing.
+// A product's inner factor in two bf16 parts, x = hi + lo to 2^-16 of x: [T][RP hi, RP lo]
+// with RP the padded rank, 0 past the rank.  `v` and `v2`: the backward pass has the
+// forward pass's v [T, r] split on the way; nullptr: not asked for.
 struct Halves {
-    const float *v;       // the forward pass's v [T, r]
-    uint16_t *w2, *v2;
+    uint16_t *w2;
+    const float *v;
+    uint16_t *v2;
     int RP;
 };
 
 __device__ __forceinline__ void put_halves(uint16_t *row, int RP, int j, float x)
 {
     const uint32_t p = ptx::bf16x2_from_f32(x, x) & 0xFFFFu;
-    const float h = __uint_as_float(p << 16);
     row[j] = (uint16_t)p;
-    row[RP + j] = (uint16_t)(ptx::bf16x2_from_f32(x - h, 0.0f) & 0xFFFFu);
+    row[RP + j] = (uint16_t)(ptx::bf16x2_from_f32(x - __uint_as_float(p << 16), 0.0f) & 0xFFFFu);
 }
 
 // Element (i, j) of both, i a position, w its value; j runs over the padded rank.
 __device__ __forceinline__ void put_pair(const Halves &h, int64_t i, int j, int r, float w)
 {
-    if (h.w2 == nullptr)
-        return;
-    put_halves(h.w2 + i * 2 * h.RP, h.RP, j, w);
-    put_halves(h.v2 + i * 2 * h.RP, h.RP, j, j < r ? __ldg(h.v + i * r + j) : 0.0f);
+    if (h.w2)
+        put_halves(h.w2 + i * 2 * h.RP, h.RP, j, w);
+    if (h.v2)
+        put_halves(h.v2 + i * 2 * h.RP, h.RP, j, j < r ? __ldg(h.v + i * r + j) : 0.0f);
 }
 
 __host__ __device__ constexpr int pad_rank(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }

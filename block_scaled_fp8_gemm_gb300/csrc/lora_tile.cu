@@ -158,9 +158,9 @@ __global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs 
         }
     }
     const float f = scaled ? l.scales[tile.a] : 1.0f;
-    float *out = v + (int64_t)tile.i0 * l.r;
+    float *out = v ? v + (int64_t)tile.i0 * l.r : nullptr;
     cluster_sum(base, tile.count, RP, kPitch, gridDim.y, [&](int i, int j, float sum) {
-        if (j < l.r)
+        if (v && j < l.r)
             out[(int64_t)i * l.r + j] = f * sum;
         put_pair(halves, tile.i0 + i, j, l.r, f * sum);
     });
@@ -176,29 +176,32 @@ __global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs 
 // columns a step, A the two bf16 parts of v in TMEM, B the weights' rows (N
 // contiguous).  A warp owns 32 tokens: it copies their rows of base ahead into a
 // ring of its own, adds its lanes' rows of D there and writes whole 128-byte row
-// pieces out of it.
+// pieces out of it.  A step is a chain (barrier, MMA, TMEM read, transposition,
+// stores) that its own CTA does not overlap; three or four CTAs an SM do, so the
+// accumulator is single and the ring short.
 constexpr int kUpThreads = 128;
 
 template <int RP>
 struct UpCfg {
-    static constexpr int kRing = 4;                   // steps copied ahead
+    static constexpr int kCtas = RP == 16 ? 4 : RP <= 64 ? 3 : 2;   // an SM
+    static constexpr int kRing = 3;                   // steps copied ahead
     static constexpr int kY = kRows * 128, kW = RP * 128, kStage = kY + kW;
-    // at least 78 KB: a third CTA an SM would wait for TMEM columns
-    static constexpr int kSmem = kRing * kStage + 1024 > 78 * 1024 ? kRing * kStage + 1024 : 78 * 1024;
-    static constexpr int kA = 128;                    // TMEM: two accumulators of 64 columns, then hi, lo
-    static constexpr int kTmem = 128 + RP <= 256 ? 256 : 512;
+    static constexpr int kSmem = kRing * kStage + 1024;
+    static constexpr int kA = 64;                     // TMEM: the accumulator, then hi, lo
+    static constexpr int kTmem = 64 + RP <= 128 ? 128 : 256;
+    static_assert(kCtas * kTmem <= 512, "the CTAs of an SM share its TMEM");
+    static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "and its shared memory");
 };
 
 template <int RP>
-__global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, const float *__restrict__ v,
+__global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, const uint16_t *__restrict__ v2,
                                                              const uint16_t *__restrict__ W, int C, bool scaled,
                                                              const uint16_t *base, int64_t bs, uint16_t *out,
                                                              int64_t os, int cols, const Waits waits)
 {
     using Cfg = UpCfg<RP>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ float vs[kRows][17];
-    __shared__ uint64_t done[2];
+    __shared__ uint64_t done;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const Tile tile = find_tile(l, blockIdx.x, kRows, base != out);
@@ -210,8 +213,7 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
     const uint32_t smem = smem_u32(align_1024(smem_raw));
     const int rank = tile.a < l.R ? rank_of(l, tile.a) : 0;
     if (tid == 0) {
-        mbar_init(done, 1);
-        mbar_init(done + 1, 1);
+        mbar_init(&done, 1);
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -220,11 +222,12 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
         tmem_relinquish();
     }
     // chunk lane & 7 of the warp's rows lane / 8 + 4 i
-    const int ch = lane & 7;
+    const int ch = lane & 7, row0 = warp * 32 + (lane >> 3);
+    const uint32_t piece[2] = {sw128(row0, ch), sw128(row0 + 4, ch)};   // + 1024 every second i
     int tok[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int p = warp * 32 + (lane >> 3) + 4 * i;
+        const int p = row0 + 4 * i;
         const int t = p < tile.count ? __ldg(l.order + tile.i0 + p) : -1;
         tok[i] = t >= 0 && t < l.T ? t : -1;
     }
@@ -236,11 +239,11 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
             const uint32_t st = smem + (s % Cfg::kRing) * Cfg::kStage;
             const int c = c_lo + s * 64 + ch * 8;
             const bool in = c < c_hi;
+            if (base) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const bool ok = in && tok[i] >= 0 && base != nullptr;
-                cp_async_cg16_or_zero(st + sw128(warp * 32 + (lane >> 3) + 4 * i, ch),
-                                      ok ? base + tok[i] * bs + c : w0, ok);
+                for (int i = 0; i < 8; ++i)
+                    if (in && tok[i] >= 0)
+                        cp_async_cg16(st + piece[i & 1] + (i >> 1) * kSw, base + tok[i] * bs + c);
             }
 #pragma unroll
             for (int j = tid >> 3; j < RP; j += kUpThreads / 8) {
@@ -250,6 +253,12 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
         }
         cp_async_commit();
     };
+    if (!base) {   // a base that is absent reads as zero
+        for (int s = 0; s < Cfg::kRing; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                st_shared_v4(smem + s * Cfg::kStage + piece[i & 1] + (i >> 1) * kSw, make_uint4(0, 0, 0, 0));
+    }
     for (int s = 0; s < Cfg::kRing; ++s)
         fetch(s);
     tc_fence_before();
@@ -257,90 +266,85 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
     tc_fence_after();
     const uint32_t tm = tmem_slot;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    grid_wait();   // v
-    grid_launch_next();
-    // v in two bf16 parts, 16 ranks at a time through shared memory
     const int ksteps = (rank + 15) / 16;
-    for (int k = 0; k < ksteps; ++k) {
-        const int j = k * 16 + (tid & 15);
-        const float *src = v + (int64_t)(tile.i0 + (tid >> 4)) * l.r + j;
-        float x[16];
+    grid_wait();   // v2
+    grid_launch_next();
+    {
+        // a thread's token: its row of v2 is the A operand's row, word for word
+        const bool some = tid < tile.count;
+        const uint4 *src = reinterpret_cast<const uint4 *>(v2 + (int64_t)(tile.i0 + (some ? tid : 0)) * (2 * RP));
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            x[i] = (tid >> 4) + 8 * i < tile.count && j < rank ? __ldg(src + (int64_t)8 * i * l.r) : 0.0f;
+        for (int k = 0; k < RP / 16; ++k) {
+            if (k < ksteps) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            vs[(tid >> 4) + 8 * i][tid & 15] = x[i];
-        __syncthreads();
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            const float a = vs[tid][2 * p], b = vs[tid][2 * p + 1];
-            hi[p] = bf16x2_from_f32(a, b);
-            lo[p] = bf16x2_from_f32(a - __uint_as_float(hi[p] << 16), b - __uint_as_float(hi[p] & 0xFFFF0000u));
+                for (int h = 0; h < 2; ++h) {
+                    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+                    if (some) {
+                        a = __ldg(src + h * (RP / 8) + k * 2);
+                        b = __ldg(src + h * (RP / 8) + k * 2 + 1);
+                    }
+                    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                    tmem_st_x8(tm + lanes + Cfg::kA + h * (RP / 2) + k * 8, w);
+                }
+            }
         }
-        tmem_st_x8(tm + lanes + Cfg::kA + k * 8, hi);
-        tmem_st_x8(tm + lanes + Cfg::kA + RP / 2 + k * 8, lo);
-        __syncthreads();
     }
     tmem_wait_st();
     tc_fence_before();
     const float f = scaled && tile.a < l.R ? l.scales[tile.a] : 1.0f;
-    for (int s = 0; s <= steps; ++s) {
-        if (s < steps) {
-            cp_async_wait<Cfg::kRing - 2>();
-            fence_async_shared();
-            __syncthreads();
-            if (tid == 0 && ksteps > 0) {
-                tc_fence_after();
-                const uint32_t wst = smem + (s % Cfg::kRing) * Cfg::kStage + Cfg::kY;
-                for (int k = 0; k < ksteps; ++k) {
-                    const uint64_t bd = smem_desc(wst + k * 2 * kSw, kSw, kSw, 2);
-                    const uint32_t a = tm + Cfg::kA + k * 8;
-                    mma_bf16_ts(tm + (s & 1) * 64, a, bd, idesc_bf16(kRows, 64, 0, 1), k > 0);
-                    mma_bf16_ts(tm + (s & 1) * 64, a + RP / 2, bd, idesc_bf16(kRows, 64, 0, 1), 1);
-                }
-                tc_commit(done + (s & 1));
-            }
-        }
-        if (s == 0)
-            continue;
-        // step s - 1
-        const int e = s - 1, c0 = c_lo + e * 64;
-        const uint32_t st = smem + (e % Cfg::kRing) * Cfg::kStage;
+    for (int s = 0; s < steps; ++s) {
+        cp_async_wait<Cfg::kRing - 1>();
+        const uint32_t st = smem + (s % Cfg::kRing) * Cfg::kStage;
         if (ksteps > 0) {
-            wait_mma(done + (e & 1), (e >> 1) & 1, &abort_flag, waits);
-            const int row = warp * 32 + lane;
+            fence_async_shared();
+            __syncthreads();   // the weights have landed; D has been read
+            if (tid == 0) {
+                tc_fence_after();
+                for (int k = 0; k < ksteps; ++k) {
+                    const uint64_t bd = smem_desc(st + Cfg::kY + k * 2 * kSw, kSw, kSw, 2);
+                    const uint32_t a = tm + Cfg::kA + k * 8;
+                    mma_bf16_ts(tm, a, bd, idesc_bf16(kRows, 64, 0, 1), k > 0);
+                    mma_bf16_ts(tm, a + RP / 2, bd, idesc_bf16(kRows, 64, 0, 1), 1);
+                }
+                tc_commit(&done);
+            }
+            __syncwarp();
+            wait_mma(&done, s & 1, &abort_flag, waits);
+            const uint32_t mine = st + tid * 128;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t r[32];
-                tmem_ld_x32(tm + lanes + (e & 1) * 64 + h * 32, r);
+                tmem_ld_x32(tm + lanes + h * 32, r);
                 tmem_wait_ld(r);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const uint32_t at = st + sw128(row, h * 4 + c);
-                    uint4 y = ld_shared_v4(at);
-                    uint32_t *w = reinterpret_cast<uint32_t *>(&y);
+                    const uint32_t at = mine + (((h * 4 + c) ^ (lane & 7)) << 4);
+                    const uint4 y = ld_shared_v4(at);
+                    uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                    for (int p = 0; p < 4; ++p)
-                        w[p] = bf16x2_from_f32(fmaf(f, __uint_as_float(r[c * 8 + 2 * p]), __uint_as_float(w[p] << 16)),
-                                               fmaf(f, __uint_as_float(r[c * 8 + 2 * p + 1]),
-                                                    __uint_as_float(w[p] & 0xFFFF0000u)));
-                    st_shared_v4(at, y);
+                    for (int p = 0; p < 4; ++p) {
+                        float y0 = __uint_as_float(w[p] << 16), y1 = __uint_as_float(w[p] & 0xFFFF0000u);
+                        fma2(y0, y1, f, r[c * 8 + 2 * p], r[c * 8 + 2 * p + 1]);
+                        w[p] = bf16x2_from_f32(y0, y1);
+                    }
+                    st_shared_v4(at, make_uint4(w[0], w[1], w[2], w[3]));
                 }
             }
             tc_fence_before();
             __syncwarp();
         }
-        const int c = c0 + ch * 8;
+        const int c = c_lo + s * 64 + ch * 8;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint4 y = ld_shared_v4(st + sw128(warp * 32 + (lane >> 3) + 4 * i, ch));
+            const uint32_t at = st + piece[i & 1] + (i >> 1) * kSw;
+            const uint4 y = ld_shared_v4(at);
             if (tok[i] >= 0 && c < c_hi)
                 *reinterpret_cast<uint4 *>(out + tok[i] * os + c) = y;
+            if (!base)
+                st_shared_v4(at, make_uint4(0, 0, 0, 0));
         }
         __syncwarp();
-        fetch(e + Cfg::kRing);
+        fetch(s + Cfg::kRing);
     }
     tc_fence_before();
     __syncthreads();
@@ -385,6 +389,7 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t done[Cfg::kStages];
     __shared__ uint32_t tmem_slot;
+    __shared__ __align__(16) int tok[2 * Cfg::kStages][kGradTokens];   // a ring of the steps' tokens
     __shared__ int abort_flag;
     const Tile tile = find_tile(l, blockIdx.x, size, false, 1);
     if (tile.of == 0) {
@@ -412,26 +417,22 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
     // x: 32 chunks a token, tokens tid / 32 + 8 i; p2: RP / 4 chunks a token
     const int ch = tid & 31;
     const bool in = c0 + ch * 8 < S.C;
-    auto token = [&](int s, int row) {
-        const int i = s * kGradTokens + row;
-        const int t = i < tile.count ? __ldg(l.order + tile.i0 + i) : -1;
-        return t >= 0 && t < l.T ? t : -1;
-    };
-    int next[4];
+    // the tokens of step s are asked for with the rows of step s - kStages: a load whose
+    // latency a step would otherwise have to wait for
     auto look_up = [&](int s) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            next[i] = token(s, (tid >> 5) + 8 * i);
+        if (tid < kGradTokens && s * kGradTokens + tid < tile.count)
+            cp_async_ca4(smem_u32(&tok[s % (2 * Cfg::kStages)][tid]), l.order + tile.i0 + s * kGradTokens + tid);
     };
-    look_up(0);
     auto fetch = [&](int s) {
         if (s < steps) {
             const uint32_t st = base + (s % Cfg::kStages) * Cfg::kStage;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const bool ok = in && next[i] >= 0;
+                const int row = (tid >> 5) + 8 * i;
+                const int t = s * kGradTokens + row < tile.count ? tok[s % (2 * Cfg::kStages)][row] : -1;
+                const bool ok = in && t >= 0 && t < l.T;
                 cp_async_cg16_or_zero(st + (ch >> 3) * Cfg::kTile + sw128((tid >> 5) + 8 * i, ch & 7),
-                                      S.x + (ok ? next[i] * S.xs + c0 + ch * 8 : 0), ok);
+                                      S.x + (ok ? t * S.xs + c0 + ch * 8 : 0), ok);
             }
 #pragma unroll
             for (int e = tid; e < kGradTokens * (RP / 4); e += kGradThreads) {
@@ -440,10 +441,15 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
                 cp_async_cg16_or_zero(st + Cfg::kX + (pc >> 3) * Cfg::kTile + sw128(row, pc & 7),
                                       S.p2 + (ok ? (int64_t)(tile.i0 + i) * (2 * RP) + pc * 8 : 0), ok);
             }
-            look_up(s + 1);
         }
+        look_up(s + Cfg::kStages);
         cp_async_commit();
     };
+    for (int s = 0; s < Cfg::kStages; ++s)
+        look_up(s);
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
     grid_wait();   // the two parts of w and v
     grid_launch_next();
     for (int s = 0; s < Cfg::kStages - 1; ++s)
@@ -530,11 +536,13 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const LoraArgs l, const 
     }
 }
 
-// How many ways to share `steps` of 64 columns so that the tiles fill two CTAs an SM
-// once, four steps a share at least.
-int shares(const LoraArgs &l, int steps, int num_sms, int most)
+// How many ways to share `steps` of 64 columns so that the tiles fill `slots` CTAs once,
+// four steps a share at least.  The host does not know the tiles: it takes every
+// adapter's last one for half full (one CTA too many would be a second wave).
+int shares(const LoraArgs &l, int steps, int slots, int most)
 {
-    const int64_t want = std::min<int64_t>(2 * (int64_t)num_sms / (l.T / kRows + 1), most);
+    const int64_t tiles = l.T / kRows + 1 + std::min<int64_t>(l.R, l.T) / 2;
+    const int64_t want = std::min<int64_t>(slots / tiles, most);
     return (int)std::max<int64_t>(1, std::min<int64_t>(want, steps / 4));
 }
 
@@ -545,7 +553,7 @@ cudaError_t run_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, in
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(tile_down_kernel<RP>), DownCfg<RP>::kSmem);
     if (e != cudaSuccess)
         return e;
-    const int steps = (C + 63) / 64, want = shares(l, steps, p.num_sms, kMaxSplits), per = (steps + want - 1) / want;
+    const int steps = (C + 63) / 64, want = shares(l, steps, 2 * p.num_sms, kMaxSplits), per = (steps + want - 1) / want;
     const int splits = (steps + per - 1) / per;   // none empty
     const dim3 grid((unsigned)most_tiles(l.T, l.R, kRows, false), splits);
     return launch(tile_down_kernel<RP>, grid, kDownThreads, DownCfg<RP>::kSmem, splits, false, st, l, x, xs, W, C, scaled, v,
@@ -553,15 +561,16 @@ cudaError_t run_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, in
 }
 
 template <int RP>
-cudaError_t run_up(const LoraArgs &l, const LoraCall &p, const float *v, const uint16_t *W, int C, bool scaled,
+cudaError_t run_up(const LoraArgs &l, const LoraCall &p, const uint16_t *v2, const uint16_t *W, int C, bool scaled,
                    const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st)
 {
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(tile_up_kernel<RP>), UpCfg<RP>::kSmem);
+    using Cfg = UpCfg<RP>;
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(tile_up_kernel<RP>), Cfg::kSmem);
     if (e != cudaSuccess)
         return e;
-    const int steps = (C + 63) / 64, ranges = shares(l, steps, p.num_sms, steps), per = (steps + ranges - 1) / ranges;
+    const int steps = (C + 63) / 64, ranges = shares(l, steps, Cfg::kCtas * p.num_sms, steps), per = (steps + ranges - 1) / ranges;
     const dim3 grid((unsigned)most_tiles(l.T, l.R, kRows, base != out), (steps + per - 1) / per);
-    return launch(tile_up_kernel<RP>, grid, kUpThreads, UpCfg<RP>::kSmem, 1, true, st, l, v, W, C, scaled, base, bs, out, os,
+    return launch(tile_up_kernel<RP>, grid, kUpThreads, Cfg::kSmem, 1, true, st, l, v2, W, C, scaled, base, bs, out, os,
                   per * 64, Waits{p.status, p.timeout_ns});
 }
 
@@ -598,23 +607,25 @@ cudaError_t launch_tile_down(const LoraArgs &l, const LoraCall &p, const uint16_
     }
 }
 
-cudaError_t launch_tile_up(const LoraArgs &l, const LoraCall &p, const float *v, const uint16_t *W, int C,
-                           bool scaled, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st)
+cudaError_t launch_tile_up(const LoraArgs &l, const LoraCall &p, const uint16_t *v2, const uint16_t *W, int C, bool scaled,
+                           const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st)
 {
     switch (pad_rank(l.r)) {
-    case 16: return run_up<16>(l, p, v, W, C, scaled, base, bs, out, os, st);
-    case 32: return run_up<32>(l, p, v, W, C, scaled, base, bs, out, os, st);
-    case 64: return run_up<64>(l, p, v, W, C, scaled, base, bs, out, os, st);
-    default: return run_up<128>(l, p, v, W, C, scaled, base, bs, out, os, st);
+    case 16: return run_up<16>(l, p, v2, W, C, scaled, base, bs, out, os, st);
+    case 32: return run_up<32>(l, p, v2, W, C, scaled, base, bs, out, os, st);
+    case 64: return run_up<64>(l, p, v2, W, C, scaled, base, bs, out, os, st);
+    default: return run_up<128>(l, p, v2, W, C, scaled, base, bs, out, os, st);
     }
 }
+
+int64_t lora_half_floats(int64_t T, int r) { return T * pad_rank(r); }
 
 int64_t lora_grad_floats(int64_t T, int r, int K, int N) { return grad_floats(T, r, K, N, T); }
 
 Halves lora_halves(const float *v, int64_t T, int r, float *ws)
 {
     uint16_t *w2 = reinterpret_cast<uint16_t *>(ws);
-    return {v, w2, w2 + T * 2 * pad_rank(r), pad_rank(r)};
+    return {w2, v, v ? w2 + T * 2 * pad_rank(r) : nullptr, pad_rank(r)};
 }
 
 cudaError_t launch_lora_grad(const LoraArgs &l, const LoraCall &p, const Halves &h, const uint16_t *x, int64_t xs, int K,
