@@ -98,22 +98,27 @@ __global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs 
         xok[i] = t >= 0 && t < l.T;
         xr[i] = x + (xok[i] ? t : 0) * xs;
     }
-    const uint16_t *w0 = W + (int64_t)tile.a * l.r * C;
     const int c_lo = blockIdx.y * cols, c_hi = min(c_lo + cols, C);
     const int steps = (c_hi - c_lo + 63) / 64;
+    // rows 32 apart are 4096 bytes apart in a stage and share their swizzle
+    const uint32_t at_x = sw128(row0, ch);
+    const uint16_t *wr = W + ((int64_t)tile.a * l.r + row0) * C;
+    int c = c_lo + ch * 8;   // of the next step
     auto fetch = [&](int s) {
         if (s < steps) {
-            const uint32_t st = base + (s % Cfg::kStages) * Cfg::kStage;
-            const int c = c_lo + s * 64 + ch * 8;
+            const uint32_t st = base + (s % Cfg::kStages) * Cfg::kStage + at_x;
             const bool in = c < c_hi;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                cp_async_cg16_or_zero(st + sw128(row0 + 32 * i, ch), xr[i] + (in ? c : 0), in && xok[i]);
+                cp_async_cg16_or_zero(st + i * 4096, in && xok[i] ? xr[i] + c : x, in && xok[i]);
 #pragma unroll
-            for (int j = row0; j < RP; j += 32) {
-                const bool ok = in && j < rank;
-                cp_async_cg16_or_zero(st + Cfg::kX + sw128(j, ch), w0 + (ok ? (int64_t)j * C + c : 0), ok);
+            for (int j = 0; j < RP; j += 32) {
+                if (RP >= 32 || row0 < RP) {
+                    const bool ok = in && row0 + j < rank;
+                    cp_async_cg16_or_zero(st + Cfg::kX + j * 128, ok ? wr + (int64_t)j * C + c : W, ok);
+                }
             }
+            c += 64;
         }
         cp_async_commit();
     };
@@ -224,14 +229,20 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
     // chunk lane & 7 of the warp's rows lane / 8 + 4 i
     const int ch = lane & 7, row0 = warp * 32 + (lane >> 3);
     const uint32_t piece[2] = {sw128(row0, ch), sw128(row0 + 4, ch)};   // + 1024 every second i
-    int tok[8];
+    const uint16_t *yr[8];
+    uint16_t *orow[8];
+    uint32_t tok = 0;   // bit i: row i is a token
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int p = row0 + 4 * i;
         const int t = p < tile.count ? __ldg(l.order + tile.i0 + p) : -1;
-        tok[i] = t >= 0 && t < l.T ? t : -1;
+        const bool ok = t >= 0 && t < l.T;
+        tok |= (ok ? 1u : 0u) << i;
+        yr[i] = base + (ok ? t : 0) * bs;
+        orow[i] = out + (ok ? t : 0) * os;
     }
-    const uint16_t *w0 = W + (int64_t)min(tile.a, l.R - 1) * l.r * C;
+    const uint16_t *wr = W + ((int64_t)min(tile.a, l.R - 1) * l.r + (tid >> 3)) * C;
+    const uint32_t at_w = sw128(tid >> 3, ch);
     const int c_lo = blockIdx.y * cols, c_hi = min(c_lo + cols, C);
     const int steps = (c_hi - c_lo + 63) / 64;
     auto fetch = [&](int s) {
@@ -242,13 +253,13 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
             if (base) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (in && tok[i] >= 0)
-                        cp_async_cg16(st + piece[i & 1] + (i >> 1) * kSw, base + tok[i] * bs + c);
+                    if (in && (tok >> i & 1))
+                        cp_async_cg16(st + piece[i & 1] + (i >> 1) * kSw, yr[i] + c);
             }
 #pragma unroll
-            for (int j = tid >> 3; j < RP; j += kUpThreads / 8) {
-                const bool ok = in && j < rank;
-                cp_async_cg16_or_zero(st + Cfg::kY + sw128(j, ch), w0 + (ok ? (int64_t)j * C + c : 0), ok);
+            for (int j = 0; j < RP; j += kUpThreads / 8) {   // rows 16 apart share their swizzle
+                const bool ok = in && (tid >> 3) + j < rank;
+                cp_async_cg16_or_zero(st + Cfg::kY + at_w + j * 128, ok ? wr + (int64_t)j * C + c : W, ok);
             }
         }
         cp_async_commit();
@@ -310,7 +321,7 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
             }
             __syncwarp();
             wait_mma(&done, s & 1, &abort_flag, waits);
-            const uint32_t mine = st + tid * 128;
+            const uint32_t row = st + tid * 128;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t r[32];
@@ -318,7 +329,7 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
                 tmem_wait_ld(r);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const uint32_t at = mine + (((h * 4 + c) ^ (lane & 7)) << 4);
+                    const uint32_t at = row + (((h * 4 + c) ^ (lane & 7)) << 4);
                     const uint4 y = ld_shared_v4(at);
                     uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -338,8 +349,8 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
         for (int i = 0; i < 8; ++i) {
             const uint32_t at = st + piece[i & 1] + (i >> 1) * kSw;
             const uint4 y = ld_shared_v4(at);
-            if (tok[i] >= 0 && c < c_hi)
-                *reinterpret_cast<uint4 *>(out + tok[i] * os + c) = y;
+            if ((tok >> i & 1) && c < c_hi)
+                *reinterpret_cast<uint4 *>(orow[i] + c) = y;
             if (!base)
                 st_shared_v4(at, make_uint4(0, 0, 0, 0));
         }
@@ -367,9 +378,11 @@ template <int RP>
 struct GradCfg {
     static constexpr int kAtoms = RP <= 32 ? 1 : 2 * RP / 64;   // 64-wide tiles of p2
     static constexpr int kTile = kGradTokens * 128, kX = 4 * kTile, kStage = kX + kAtoms * kTile;
-    static constexpr int kStages = RP <= 32 ? 5 : RP == 64 ? 4 : 6;   // two CTAs an SM (RP 128: one, it takes all of TMEM)
+    static constexpr int kStages = RP <= 32 ? 3 : RP == 64 ? 4 : 6;
+    static constexpr int kCtas = RP <= 32 ? 3 : RP == 64 ? 2 : 1;   // an SM (RP 128 takes all of its TMEM)
     static constexpr int kSmem = kStages * kStage + 1024;
     static constexpr int kTmem = 4 * RP;   // 64 to 512
+    static_assert(kCtas * kTmem <= 512 && kCtas * (kSmem + 2048) <= 228 * 1024, "the CTAs of an SM share it");
 };
 
 struct GradSide {
@@ -398,7 +411,7 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
     }
     const int a_tiles = (A.C + kGradCols - 1) / kGradCols;
     const bool second = (int)blockIdx.y >= a_tiles;
-    const GradSide &S = second ? B : A;
+    const GradSide S = second ? B : A;
     const int c0 = ((int)blockIdx.y - (second ? a_tiles : 0)) * kGradCols;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = smem_u32(align_1024(smem_raw));
@@ -414,9 +427,16 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
         tmem_relinquish();
     }
     const int steps = (tile.count + kGradTokens - 1) / kGradTokens;
-    // x: 32 chunks a token, tokens tid / 32 + 8 i; p2: RP / 4 chunks a token
+    // x: 32 chunks a token, tokens tid / 32 + 8 i; p2: RP / 4 chunks a token, tokens
+    // kPer apart.  Tokens 8 apart are 1024 bytes apart in a tile and share their swizzle.
     const int ch = tid & 31;
     const bool in = c0 + ch * 8 < S.C;
+    const uint16_t *xc = S.x + (in ? c0 + ch * 8 : 0);
+    const uint32_t at_x = (ch >> 3) * Cfg::kTile + sw128(tid >> 5, ch & 7);
+    constexpr int kPer = kGradThreads / (RP / 4);
+    const int prow = tid / (RP / 4), pc = tid % (RP / 4);
+    const uint32_t at_p = Cfg::kX + (pc >> 3) * Cfg::kTile + sw128(prow, pc & 7);
+    const uint16_t *pr = S.p2 + (int64_t)(tile.i0 + prow) * (2 * RP) + pc * 8;
     // the tokens of step s are asked for with the rows of step s - kStages: a load whose
     // latency a step would otherwise have to wait for
     auto look_up = [&](int s) {
@@ -426,21 +446,22 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
     auto fetch = [&](int s) {
         if (s < steps) {
             const uint32_t st = base + (s % Cfg::kStages) * Cfg::kStage;
+            const int left = tile.count - s * kGradTokens;
+            const int *row = tok[s % (2 * Cfg::kStages)] + (tid >> 5);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int row = (tid >> 5) + 8 * i;
-                const int t = s * kGradTokens + row < tile.count ? tok[s % (2 * Cfg::kStages)][row] : -1;
+                const int t = (tid >> 5) + 8 * i < left ? row[8 * i] : -1;
                 const bool ok = in && t >= 0 && t < l.T;
-                cp_async_cg16_or_zero(st + (ch >> 3) * Cfg::kTile + sw128((tid >> 5) + 8 * i, ch & 7),
-                                      S.x + (ok ? t * S.xs + c0 + ch * 8 : 0), ok);
+                cp_async_cg16_or_zero(st + at_x + i * kSw, ok ? xc + t * S.xs : xc, ok);
             }
 #pragma unroll
-            for (int e = tid; e < kGradTokens * (RP / 4); e += kGradThreads) {
-                const int row = e / (RP / 4), pc = e % (RP / 4), i = s * kGradTokens + row;
-                const bool ok = i < tile.count;
-                cp_async_cg16_or_zero(st + Cfg::kX + (pc >> 3) * Cfg::kTile + sw128(row, pc & 7),
-                                      S.p2 + (ok ? (int64_t)(tile.i0 + i) * (2 * RP) + pc * 8 : 0), ok);
+            for (int i = 0; i < kGradTokens; i += kPer) {
+                if (kPer <= kGradTokens || prow < kGradTokens) {
+                    const bool ok = prow + i < left;
+                    cp_async_cg16_or_zero(st + at_p + i * 128, ok ? pr + i * 2 * RP : S.p2, ok);
+                }
             }
+            pr += kGradTokens * 2 * RP;
         }
         look_up(s + Cfg::kStages);
         cp_async_commit();
@@ -632,10 +653,11 @@ cudaError_t launch_lora_grad(const LoraArgs &l, const LoraCall &p, const Halves 
                              uint16_t *dA, const uint16_t *dy, int64_t ys, int N, uint16_t *dB, float *ws,
                              int64_t ws_floats, cudaStream_t st)
 {
-    // cut an adapter's tokens so that one adapter alone would fill two CTAs an SM, into
+    // cut an adapter's tokens so that one adapter alone would fill the SMs once, into
     // tiles of 256 at least, and no finer than the scratch allows
     const int tiles = (K + kGradCols - 1) / kGradCols + (N + kGradCols - 1) / kGradCols;
-    const int64_t ways = (2 * p.num_sms + tiles - 1) / tiles;
+    const int ctas = h.RP <= 32 ? GradCfg<32>::kCtas : h.RP == 64 ? GradCfg<64>::kCtas : GradCfg<128>::kCtas;
+    const int64_t ways = (ctas * p.num_sms + tiles - 1) / tiles;
     int64_t size = std::max<int64_t>(256, ((l.T + ways - 1) / ways + 63) / 64 * 64);
     while (size < l.T && grad_floats(l.T, l.r, K, N, size) > ws_floats)
         size *= 2;
