@@ -16,7 +16,6 @@
 
 #include "gemmar.h"
 #include "kernels.h"
-#include "lora.cuh"
 
 #define GEMMAR_API extern "C" __attribute__((visibility("default")))
 
@@ -753,8 +752,7 @@ GEMMAR_API int lora_apply(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, 
     cudaStream_t st = as_stream(stream);
     const LoraArgs l{order, offsets, ranks, scales, T, R, r};
     const LoraCall p{ctx->num_sms, ctx->status, ctx->timeout_ns};
-    CUDA_OK(launch_lora_products(l, p, x, x_stride, A, (int)K, false, v, lora_halves(nullptr, T, r, ctx->W), B, (int)N, true, y,
-                                 y_stride, out, out_stride, st));
+    CUDA_OK(launch_lora_apply(l, p, x, x_stride, A, (int)K, B, (int)N, y, y_stride, out, out_stride, v, ctx->W, st));
     return GEMMAR_OK;
 }
 
@@ -780,11 +778,8 @@ GEMMAR_API int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stri
     cudaStream_t st = as_stream(stream);
     const LoraArgs l{order, offsets, ranks, scales, T, R, r};
     const LoraCall p{ctx->num_sms, ctx->status, ctx->timeout_ns};
-    const Halves halves = lora_halves(v, T, r, ctx->W);
-    CUDA_OK(launch_lora_products(l, p, dy, dy_stride, B, (int)N, true, nullptr, halves, A, (int)K, false, dx0, dx0_stride, dx,
-                                 dx_stride, st));
-    CUDA_OK(launch_lora_grad(l, p, halves, x, x_stride, (int)K, dA, dy, dy_stride, (int)N, dB, ctx->W,
-                             ctx->W_floats, st));
+    CUDA_OK(launch_lora_apply_bwd(l, p, x, x_stride, dy, dy_stride, A, (int)K, B, (int)N, v, dx0, dx0_stride, dx, dx_stride,
+                                  dA, dB, ctx->W, ctx->W_floats, st));
     return GEMMAR_OK;
 }
 

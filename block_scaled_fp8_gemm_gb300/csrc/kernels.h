@@ -206,28 +206,18 @@ struct LoraCall {
     ptx::DevStatus *status;
     uint64_t timeout_ns;
 };
-struct Halves;   // lora.cuh
-// Both products of a call:
-//   v[i,j] = f sum_c x[order[i],c] Wd[a,j,c]            (0 for j past the rank; in fp32 if v is given)
-//   out[t,c] = base[t,c] + f sum_j v[i,j] Wu[a,j,c]     (rows without an adapter: base)
-// with f = scales[a] where scaled, else 1.  Few tokens go to one kernel that loads
-// straight into registers (lora.cu), which writes the halves if they are wanted later;
-// many to tiles (lora_tile.cu), which pass v on as its halves (halves.w2).
-cudaError_t launch_lora_products(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *Wd,
-                                 int Cd, bool scaled_d, float *v, const Halves &halves, const uint16_t *Wu, int Cu, bool scaled_u,
-                                 const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st);
-cudaError_t launch_tile_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *W,
-                             int C, bool scaled, float *v, const Halves &halves, cudaStream_t st);
-cudaError_t launch_tile_up(const LoraArgs &l, const LoraCall &p, const uint16_t *v2, const uint16_t *W, int C, bool scaled,
-                             const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st);
-// dA[a,j,c] = sum_{tokens of a} w[i,j] x[order[i],c] and dB[a,j,c] = scales[a] sum v[i,j] dy[order[i],c],
-// from the two bf16 parts of w and v that launch_lora_products left at the start of ws; ws:
-// lora_grad_floats at least, more lets the tokens of a large adapter be shared out
+// lora_apply and lora_apply_bwd.  Few tokens go to one kernel that does both products of
+// a direction (lora.cu), many to tiles on the tensor cores (lora_tile.cu).  Scratch:
+// lora_half_floats(T, r) for the forward pass, lora_grad_floats at least for the backward
+// pass, where more lets the tokens of a large adapter be shared out.
 int64_t lora_half_floats(int64_t T, int r);
 int64_t lora_grad_floats(int64_t T, int r, int K, int N);
-Halves lora_halves(const float *v, int64_t T, int r, float *ws);
-cudaError_t launch_lora_grad(const LoraArgs &l, const LoraCall &p, const Halves &h, const uint16_t *x, int64_t xs, int K,
-                             uint16_t *dA, const uint16_t *dy, int64_t ys, int N, uint16_t *dB, float *ws,
-                             int64_t ws_floats, cudaStream_t st);
+cudaError_t launch_lora_apply(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *A, int K,
+                              const uint16_t *B, int N, const uint16_t *y, int64_t ys, uint16_t *out, int64_t os, float *v,
+                              float *ws, cudaStream_t st);
+cudaError_t launch_lora_apply_bwd(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *dy,
+                                  int64_t dys, const uint16_t *A, int K, const uint16_t *B, int N, const float *v,
+                                  const uint16_t *dx0, int64_t dx0s, uint16_t *dx, int64_t dxs, uint16_t *dA, uint16_t *dB,
+                                  float *ws, int64_t ws_floats, cudaStream_t st);
 
 }  // namespace gemmar

@@ -394,14 +394,12 @@ cudaError_t launch_lora_plan(const int32_t *ids, int64_t T, int R, int32_t *orde
     return cudaGetLastError();
 }
 
-cudaError_t launch_lora_products(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *Wd,
-                                 int Cd, bool scaled_d, float *v, const Halves &halves, const uint16_t *Wu, int Cu, bool scaled_u,
-                                 const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st)
+namespace {
+
+cudaError_t launch_few(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const Factor &down,
+                       const Factor &up, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *v,
+                       const Halves &halves, cudaStream_t st)
 {
-    if (l.T > kFewBatch) {
-        const cudaError_t e = launch_tile_down(l, p, x, xs, Wd, Cd, scaled_d, v, halves, st);
-        return e != cudaSuccess ? e : launch_tile_up(l, p, halves.w2, Wu, Cu, scaled_u, base, bs, out, os, st);
-    }
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(few_kernel), sizeof(FewSmem));
     if (e != cudaSuccess)
         return e;
@@ -410,8 +408,47 @@ cudaError_t launch_lora_products(const LoraArgs &l, const LoraCall &p, const uin
     int ctas = kMaxSplits;
     while (ctas > 1 && tiles * ctas > 2 * p.num_sms)
         ctas /= 2;
-    return launch(few_kernel, dim3((unsigned)tiles, ctas), kFewWarps * 32, sizeof(FewSmem), ctas, false, st, l, x, xs,
-                        Factor{Wd, Cd, scaled_d}, Factor{Wu, Cu, scaled_u}, base, bs, out, os, v, halves);
+    return launch(few_kernel, dim3((unsigned)tiles, ctas), kFewWarps * 32, sizeof(FewSmem), ctas, false, st, l, x, xs, down,
+                  up, base, bs, out, os, v, halves);
+}
+
+}  // namespace
+
+#define TRY(x)                           \
+    do {                                 \
+        const cudaError_t e_ = (x);      \
+        if (e_ != cudaSuccess)           \
+            return e_;                   \
+    } while (0)
+
+cudaError_t launch_lora_apply(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *A, int K,
+                              const uint16_t *B, int N, const uint16_t *y, int64_t ys, uint16_t *out, int64_t os, float *v,
+                              float *ws, cudaStream_t st)
+{
+    if (l.T <= kFewBatch)
+        return launch_few(l, p, x, xs, Factor{A, K, false}, Factor{B, N, true}, y, ys, out, os, v, Halves{}, st);
+    const Halves h = lora_halves(nullptr, l.T, l.r, ws);
+    TRY(launch_tile_down(l, p, x, xs, A, K, false, v, h, st));
+    return launch_tile_up(l, p, h.w2, B, N, true, y, ys, out, os, false, st);
+}
+
+cudaError_t launch_lora_apply_bwd(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *dy,
+                                  int64_t dys, const uint16_t *A, int K, const uint16_t *B, int N, const float *v,
+                                  const uint16_t *dx0, int64_t dx0s, uint16_t *dx, int64_t dxs, uint16_t *dA, uint16_t *dB,
+                                  float *ws, int64_t ws_floats, cudaStream_t st)
+{
+    const Halves h = lora_halves(v, l.T, l.r, ws);
+    const GradCall g = lora_grad_call(l, p, h, x, xs, K, dA, dy, dys, N, dB, ws, ws_floats);
+    if (l.T <= kFewBatch) {
+        TRY(launch_few(l, p, dy, dys, Factor{B, N, true}, Factor{A, K, false}, dx0, dx0s, dx, dxs, nullptr, h, st));
+        TRY(launch_tile_grad(l, p, g, st));
+    } else {
+        // the weight gradients and dx need only w: they run side by side
+        TRY(launch_tile_down(l, p, dy, dys, B, N, true, nullptr, h, st));
+        TRY(launch_tile_grad(l, p, g, st));
+        TRY(launch_tile_up(l, p, h.w2, A, K, false, dx0, dx0s, dx, dxs, true, st));
+    }
+    return launch_grad_join(l, p, g, st);
 }
 
 }  // namespace gemmar

@@ -172,4 +172,31 @@ inline int64_t most_tiles(int64_t T, int R, int size, bool bare)
     return T / size + (groups < T ? groups : T);
 }
 
+// One weight gradient: G[a,j,c] = f sum_i p[i,j] x[order[i],c], p from its halves.
+struct GradSide {
+    const uint16_t *x;    // tokens' rows
+    int64_t xs;
+    int C, scaled;
+    const uint16_t *p2;   // [T][2 RP]
+    uint16_t *G;
+    float *part;          // [split tile][r][C]
+};
+
+// Both of a call, and the tokens a tile.
+struct GradCall {
+    GradSide A, B;
+    int RP, size;
+};
+
+// The launches of lora_tile.cu.
+cudaError_t launch_tile_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *W,
+                             int C, bool scaled, float *v, const Halves &halves, cudaStream_t st);
+cudaError_t launch_tile_up(const LoraArgs &l, const LoraCall &p, const uint16_t *v2, const uint16_t *W, int C, bool scaled,
+                           const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, bool beside, cudaStream_t st);
+Halves lora_halves(const float *v, int64_t T, int r, float *ws);
+GradCall lora_grad_call(const LoraArgs &l, const LoraCall &p, const Halves &h, const uint16_t *x, int64_t xs, int K,
+                        uint16_t *dA, const uint16_t *dy, int64_t ys, int N, uint16_t *dB, float *ws, int64_t ws_floats);
+cudaError_t launch_tile_grad(const LoraArgs &l, const LoraCall &p, const GradCall &g, cudaStream_t st);
+cudaError_t launch_grad_join(const LoraArgs &l, const LoraCall &p, const GradCall &g, cudaStream_t st);
+
 }  // namespace gemmar

@@ -70,7 +70,6 @@ __global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs 
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const Tile tile = find_tile(l, blockIdx.x, kRows, false);
-    grid_launch_next();
     if (tile.of == 0)
         return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -128,6 +127,7 @@ __global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs 
     __syncthreads();
     tc_fence_after();
     const uint32_t d = tmem_slot;
+    grid_launch_next();   // not before this CTA has its TMEM: the next kernel's would wait holding theirs
     for (int s = 0; s < steps; ++s) {
         cp_async_wait<Cfg::kStages - 2>();
         fence_async_shared();
@@ -184,6 +184,10 @@ __global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs 
 // pieces out of it.  A step is a chain (barrier, MMA, TMEM read, transposition,
 // stores) that its own CTA does not overlap; three or four CTAs an SM do, so the
 // accumulator is single and the ring short.
+// With `beside` the kernel before this one does not produce v2 but has waited for the
+// one that does before it let this one start (tile_grad_kernel): the two then run side
+// by side, and this one waits for the other at its end, so that what follows in the
+// stream finds both complete.
 constexpr int kUpThreads = 128;
 
 template <int RP>
@@ -202,7 +206,7 @@ template <int RP>
 __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, const uint16_t *__restrict__ v2,
                                                              const uint16_t *__restrict__ W, int C, bool scaled,
                                                              const uint16_t *base, int64_t bs, uint16_t *out,
-                                                             int64_t os, int cols, const Waits waits)
+                                                             int64_t os, int cols, bool beside, const Waits waits)
 {
     using Cfg = UpCfg<RP>;
     extern __shared__ uint8_t smem_raw[];
@@ -278,7 +282,8 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
     const uint32_t tm = tmem_slot;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     const int ksteps = (rank + 15) / 16;
-    grid_wait();   // v2
+    if (!beside)
+        grid_wait();   // v2
     grid_launch_next();
     {
         // a thread's token: its row of v2 is the A operand's row, word for word
@@ -361,6 +366,8 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
     __syncthreads();
     if (warp == 0)
         tmem_dealloc(tm, Cfg::kTmem);
+    if (beside)
+        grid_wait();
 }
 
 // ---------------------------------------------------------------- grad
@@ -383,15 +390,6 @@ struct GradCfg {
     static constexpr int kSmem = kStages * kStage + 1024;
     static constexpr int kTmem = 4 * RP;   // 64 to 512
     static_assert(kCtas * kTmem <= 512 && kCtas * (kSmem + 2048) <= 228 * 1024, "the CTAs of an SM share it");
-};
-
-struct GradSide {
-    const uint16_t *x;    // tokens' rows
-    int64_t xs;
-    int C, scaled;
-    const uint16_t *p2;   // [T][2 RP]
-    uint16_t *G;
-    float *part;          // [split tile][r][C]
 };
 
 template <int RP>
@@ -583,7 +581,7 @@ cudaError_t run_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, in
 
 template <int RP>
 cudaError_t run_up(const LoraArgs &l, const LoraCall &p, const uint16_t *v2, const uint16_t *W, int C, bool scaled,
-                   const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st)
+                   const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, bool beside, cudaStream_t st)
 {
     using Cfg = UpCfg<RP>;
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(tile_up_kernel<RP>), Cfg::kSmem);
@@ -592,7 +590,7 @@ cudaError_t run_up(const LoraArgs &l, const LoraCall &p, const uint16_t *v2, con
     const int steps = (C + 63) / 64, ranges = shares(l, steps, Cfg::kCtas * p.num_sms, steps), per = (steps + ranges - 1) / ranges;
     const dim3 grid((unsigned)most_tiles(l.T, l.R, kRows, base != out), (steps + per - 1) / per);
     return launch(tile_up_kernel<RP>, grid, kUpThreads, Cfg::kSmem, 1, true, st, l, v2, W, C, scaled, base, bs, out, os,
-                  per * 64, Waits{p.status, p.timeout_ns});
+                  per * 64, beside, Waits{p.status, p.timeout_ns});
 }
 
 template <int RP>
@@ -629,13 +627,13 @@ cudaError_t launch_tile_down(const LoraArgs &l, const LoraCall &p, const uint16_
 }
 
 cudaError_t launch_tile_up(const LoraArgs &l, const LoraCall &p, const uint16_t *v2, const uint16_t *W, int C, bool scaled,
-                           const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st)
+                           const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, bool beside, cudaStream_t st)
 {
     switch (pad_rank(l.r)) {
-    case 16: return run_up<16>(l, p, v2, W, C, scaled, base, bs, out, os, st);
-    case 32: return run_up<32>(l, p, v2, W, C, scaled, base, bs, out, os, st);
-    case 64: return run_up<64>(l, p, v2, W, C, scaled, base, bs, out, os, st);
-    default: return run_up<128>(l, p, v2, W, C, scaled, base, bs, out, os, st);
+    case 16: return run_up<16>(l, p, v2, W, C, scaled, base, bs, out, os, beside, st);
+    case 32: return run_up<32>(l, p, v2, W, C, scaled, base, bs, out, os, beside, st);
+    case 64: return run_up<64>(l, p, v2, W, C, scaled, base, bs, out, os, beside, st);
+    default: return run_up<128>(l, p, v2, W, C, scaled, base, bs, out, os, beside, st);
     }
 }
 
@@ -649,9 +647,8 @@ Halves lora_halves(const float *v, int64_t T, int r, float *ws)
     return {w2, v, v ? w2 + T * 2 * pad_rank(r) : nullptr, pad_rank(r)};
 }
 
-cudaError_t launch_lora_grad(const LoraArgs &l, const LoraCall &p, const Halves &h, const uint16_t *x, int64_t xs, int K,
-                             uint16_t *dA, const uint16_t *dy, int64_t ys, int N, uint16_t *dB, float *ws,
-                             int64_t ws_floats, cudaStream_t st)
+GradCall lora_grad_call(const LoraArgs &l, const LoraCall &p, const Halves &h, const uint16_t *x, int64_t xs, int K,
+                        uint16_t *dA, const uint16_t *dy, int64_t ys, int N, uint16_t *dB, float *ws, int64_t ws_floats)
 {
     // cut an adapter's tokens so that one adapter alone would fill the SMs once, into
     // tiles of 256 at least, and no finer than the scratch allows
@@ -664,20 +661,26 @@ cudaError_t launch_lora_grad(const LoraArgs &l, const LoraCall &p, const Halves 
     size = std::min<int64_t>(size, (l.T + 63) / 64 * 64);
     float *part = ws + 2 * l.T * h.RP;
     const int64_t slots = size < l.T ? 2 * (l.T / size) : 0;
-    const GradSide A{x, xs, K, 0, h.w2, dA, part};
-    const GradSide B{dy, ys, N, 1, h.v2, dB, part + slots * l.r * K};
-    cudaError_t e = cudaSuccess;
-    switch (h.RP) {
-    case 16: e = run_grad<16>(l, p, A, B, (int)size, st); break;
-    case 32: e = run_grad<32>(l, p, A, B, (int)size, st); break;
-    case 64: e = run_grad<64>(l, p, A, B, (int)size, st); break;
-    default: e = run_grad<128>(l, p, A, B, (int)size, st); break;
+    return {{x, xs, K, 0, h.w2, dA, part}, {dy, ys, N, 1, h.v2, dB, part + slots * l.r * K}, h.RP, (int)size};
+}
+
+cudaError_t launch_tile_grad(const LoraArgs &l, const LoraCall &p, const GradCall &g, cudaStream_t st)
+{
+    switch (g.RP) {
+    case 16: return run_grad<16>(l, p, g.A, g.B, g.size, st);
+    case 32: return run_grad<32>(l, p, g.A, g.B, g.size, st);
+    case 64: return run_grad<64>(l, p, g.A, g.B, g.size, st);
+    default: return run_grad<128>(l, p, g.A, g.B, g.size, st);
     }
-    if (e != cudaSuccess || size >= l.T)
-        return e;
-    const int64_t most = (int64_t)l.r * std::max(K, N);
+}
+
+cudaError_t launch_grad_join(const LoraArgs &l, const LoraCall &p, const GradCall &g, cudaStream_t st)
+{
+    if (g.size >= l.T)
+        return cudaSuccess;   // no adapter was cut
+    const int64_t most = (int64_t)l.r * std::max(g.A.C, g.B.C);
     const int join = (int)std::min<int64_t>((most + 1023) / 1024, std::max(1, 8 * p.num_sms / l.R));
-    return launch(grad_join_kernel, dim3(l.R, join, 2), 256, 0, 1, true, st, l, A, B, (int)size);
+    return launch(grad_join_kernel, dim3(l.R, join, 2), 256, 0, 1, true, st, l, g.A, g.B, g.size);
 }
 
 }  // namespace gemmar
