@@ -13,6 +13,7 @@
 
 #include "e4m3_encode.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 
 namespace gemmar {
 using namespace ptx;
@@ -345,7 +346,7 @@ __device__ __forceinline__ void encode_units(const Vec<W> (&v)[U], uint8_t *q, f
 // A thread holds U units of W columns of its row.  A warp takes 32 U W neighbouring
 // columns and its units lie 32 W apart, so one address per matrix and fixed
 // offsets reach them all (with units T W apart address arithmetic was a third of
-// the instructions: 71 us instead of XX at 4096 x 7168, fp32 stream, codes).
+// the instructions: 71 us instead of 66 at 4096 x 7168, fp32 stream, codes).
 // Two rows an SM in flight (two CTAs) hide each other's two sums.  Weights come
 // through L1, which the rings leave room for (kNormRing).
 template <int U, bool YB, bool HB>
@@ -483,7 +484,8 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int sta
 // registers between the passes, so its slots are free for the next row before the
 // sums are exchanged; the weights sit in shared memory.  Wider rows take 32 columns
 // a thread, read the slots twice and the weights through L1.
-template <int U, bool YB, bool HB, bool TOKEN, bool HOLD>
+// BOTH: both norms are there (known when compiling, a pass of the row is one loop).
+template <int U, bool YB, bool HB, bool TOKEN, bool HOLD, bool BOTH>
 __global__ void __launch_bounds__(512, 1)
     norm_bwd_kernel(const NormBwdArgs a, float *__restrict__ ws, int stages, int gate_staged)
 {
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(512, 1)
     extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ float red[2][16][4];
     const int T = blockDim.x, t = threadIdx.x, lane = t & 31, N = a.N;
-    const bool pre = a.w2 != nullptr, post = a.w1 != nullptr;
+    const bool pre = BOTH || a.w2 != nullptr, post = BOTH || a.w1 != nullptr;
     const uint32_t off_h = U * kY * T, off_dt = off_h + U * kH * T, off_du = off_dt + U * kH * T, off_g = off_du + U * kB * T;
     const uint32_t stage_bytes = off_g + (gate_staged ? U * kB * T : 0);
     const uint32_t base = smem_u32(smem_raw);
@@ -691,31 +693,48 @@ __global__ void __launch_bounds__(512, 1)
                     read(k);
                 Vec<W> cw, w2, d = rdt[r].vec(), dy, dg;
                 row_weights(k, cw, w2);
-                // (a norm that is absent must not bring its row's infinities in as 0 * inf)
-                if (pre) {
+                if constexpr (BOTH) {
 #pragma unroll
                     for (int i = 0; i < W / 2; ++i) {
                         const Pair p = form(k, i, cw, w2);
                         d.v[i] = fma2(p.t, mk, fma2(p.dv, r2, d.v[i]));
                         s2[k].v[i] = fma2(mul2(p.du, r2), p.t, s2[k].v[i]);
+                        if constexpr (TOKEN) {
+                            const f2 nd = mul2(p.n, d.v[i]);
+                            dg.v[i] = mul2(p.cw, nd);
+                            s1[k].v[i] = fma2(nd, rg[r].pair(i), s1[k].v[i]);
+                        } else {
+                            s1[k].v[i] = fma2(p.n, d.v[i], s1[k].v[i]);
+                        }
+                        dy.v[i] = fma2(p.n, mm, mul2(mul2(p.gcw, d.v[i]), r1));
                     }
-                }
+                } else {
+                    // a norm that is absent must not bring its row's infinities in as 0 * inf
+                    if (pre) {
 #pragma unroll
-                for (int i = 0; i < W / 2; ++i) {
-                    const Pair p = form(k, i, cw, w2);
-                    if constexpr (TOKEN) {
-                        const f2 nd = mul2(p.n, d.v[i]);
-                        dg.v[i] = mul2(p.cw, nd);
-                        s1[k].v[i] = fma2(nd, rg[r].pair(i), s1[k].v[i]);
-                    } else {
-                        s1[k].v[i] = fma2(p.n, d.v[i], s1[k].v[i]);
+                        for (int i = 0; i < W / 2; ++i) {
+                            const Pair p = form(k, i, cw, w2);
+                            d.v[i] = fma2(p.t, mk, fma2(p.dv, r2, d.v[i]));
+                            s2[k].v[i] = fma2(mul2(p.du, r2), p.t, s2[k].v[i]);
+                        }
                     }
-                    dy.v[i] = mul2(mul2(p.gcw, d.v[i]), r1);
-                }
-                if (post) {
 #pragma unroll
-                    for (int i = 0; i < W / 2; ++i)
-                        dy.v[i] = fma2(mul2(ry[r].pair(i), r1), mm, dy.v[i]);
+                    for (int i = 0; i < W / 2; ++i) {
+                        const Pair p = form(k, i, cw, w2);
+                        if constexpr (TOKEN) {
+                            const f2 nd = mul2(p.n, d.v[i]);
+                            dg.v[i] = mul2(p.cw, nd);
+                            s1[k].v[i] = fma2(nd, rg[r].pair(i), s1[k].v[i]);
+                        } else {
+                            s1[k].v[i] = fma2(p.n, d.v[i], s1[k].v[i]);
+                        }
+                        dy.v[i] = mul2(mul2(p.gcw, d.v[i]), r1);
+                    }
+                    if (post) {
+#pragma unroll
+                        for (int i = 0; i < W / 2; ++i)
+                            dy.v[i] = fma2(mul2(ry[r].pair(i), r1), mm, dy.v[i]);
+                    }
                 }
                 store_vec<W, YB>(a.dy, m * N + col, dy);
                 store_vec<W, HB>(a.dh, m * N + col, d * alpha);
@@ -731,6 +750,7 @@ __global__ void __launch_bounds__(512, 1)
             cp_async_commit();
         }
     }
+    grid_launch_next();
     float *part = ws + (int64_t)blockIdx.x * 2 * N;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
@@ -742,32 +762,37 @@ __global__ void __launch_bounds__(512, 1)
     }
 }
 
-// The CTAs' parts in the order of the CTAs: eight threads a column, each a
-// contiguous eighth of the parts.  s1 = sum n d (times a token's gate):
-// dw1 = beta g s1 and dgate = beta w1 s1 for a gate row g.
-__global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const NormBwdArgs a, const float *__restrict__ ws, int parts)
+// The sums of the CTAs' parts, in an order that their number fixes: 32 columns a CTA,
+// warp p takes every part p + 32 k, and a warp a column then adds the 32 sums.
+// s1 = sum n d (times a token's gate): dw1 = beta g s1 and dgate = beta w1 s1 for a gate
+// row g.
+__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const NormBwdArgs a, const float *__restrict__ ws, int parts)
 {
-    __shared__ float sums[2][8][32];
-    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
-    const int n = blockIdx.x * 32 + lane;
-    const int share = (parts + 7) / 8, lo = part * share, hi = min(lo + share, parts);
+    __shared__ float sums[2][32][33];
+    grid_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float s1 = 0.0f, s2 = 0.0f;
-    if (n < a.N) {
+    if (blockIdx.x * 32 + lane < a.N) {
+        const float *src = ws + blockIdx.x * 32 + lane;
 #pragma unroll 8
-        for (int p = lo; p < hi; ++p) {
-            s1 += ws[(int64_t)p * 2 * a.N + n];
-            s2 += ws[(int64_t)p * 2 * a.N + a.N + n];
+        for (int p = warp; p < parts; p += 32) {
+            s1 += src[(int64_t)p * 2 * a.N];
+            s2 += src[(int64_t)p * 2 * a.N + a.N];
         }
     }
-    sums[0][part][lane] = s1;
-    sums[1][part][lane] = s2;
+    sums[0][warp][lane] = s1;
+    sums[1][warp][lane] = s2;
     __syncthreads();
-    if (part != 0 || n >= a.N)
-        return;
-    for (int p = 1; p < 8; ++p) {
-        s1 += sums[0][p][lane];
-        s2 += sums[1][p][lane];
+    s1 = sums[0][lane][warp];
+    s2 = sums[1][lane][warp];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
+        s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
     }
+    const int n = blockIdx.x * 32 + warp;
+    if (lane != 0 || n >= a.N)
+        return;
     const bool row = a.gate && a.gs == 0;
     if (a.dw1)
         a.dw1[n] = a.beta * (row ? bf16_lo(a.gate[n]) : 1.0f) * s1;
@@ -853,7 +878,8 @@ cudaError_t run_norm_bwd(const NormBwdArgs &a, float *ws, int grid, cudaStream_t
     const int stage_bytes = bytes + (staged ? cols * 2 : 0);
     const int64_t room = (p.per_sm == 1 ? kMaxSmem : kMaxSmem / p.per_sm - 2048) - weight_bytes;
     const int stages = ring_stages(room, stage_bytes, (a.M + grid - 1) / grid);
-    const auto kernel = norm_bwd_kernel<COLS / W, YB, HB, TOKEN, kHold>;
+    const auto kernel = a.w1 && a.w2 ? norm_bwd_kernel<COLS / W, YB, HB, TOKEN, kHold, true>
+                                     : norm_bwd_kernel<COLS / W, YB, HB, TOKEN, kHold, false>;
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), kMaxSmem);
     if (e != cudaSuccess)
         return e;
@@ -890,8 +916,7 @@ cudaError_t launch_norm_bwd(const NormBwdArgs &a, float *ws, int num_sms, cudaSt
                                        : (token ? pick_norm_bwd<32, true>(a, ws, grid, st) : pick_norm_bwd<32, false>(a, ws, grid, st));
     if (e != cudaSuccess || (!a.dw1 && !a.dw2 && !(a.dgate && a.gs == 0)))
         return e;
-    norm_bwd_sum_kernel<<<(a.N + 31) / 32, 256, 0, st>>>(a, ws, grid);
-    return cudaGetLastError();
+    return launch(norm_bwd_sum_kernel, dim3((a.N + 31) / 32), 1024, 0, 1, true, st, a, static_cast<const float *>(ws), grid);
 }
 
 }  // namespace gemmar
