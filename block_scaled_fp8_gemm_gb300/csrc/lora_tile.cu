@@ -55,7 +55,8 @@ constexpr int kDownThreads = 256;
 template <int RP>   // ranks rounded up to 16, 32, 64 or 128
 struct DownCfg {
     static constexpr int kX = kRows * 128, kW = RP * 128, kStage = kX + kW;
-    static constexpr int kStages = RP == 16 ? 6 : RP == 32 ? 5 : RP == 64 ? 4 : 3;   // two CTAs an SM
+    static constexpr int kCtas = RP <= 64 ? 3 : 2;   // an SM
+    static constexpr int kStages = RP == 16 ? 4 : 3;
     static constexpr int kSmem = kStages * kStage + 1024;
 };
 
@@ -572,7 +573,7 @@ cudaError_t run_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, in
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(tile_down_kernel<RP>), DownCfg<RP>::kSmem);
     if (e != cudaSuccess)
         return e;
-    const int steps = (C + 63) / 64, want = shares(l, steps, 2 * p.num_sms, kMaxSplits), per = (steps + want - 1) / want;
+    const int steps = (C + 63) / 64, want = shares(l, steps, DownCfg<RP>::kCtas * p.num_sms, kMaxSplits), per = (steps + want - 1) / want;
     const int splits = (steps + per - 1) / per;   // none empty
     const dim3 grid((unsigned)most_tiles(l.T, l.R, kRows, false), splits);
     return launch(tile_down_kernel<RP>, grid, kDownThreads, DownCfg<RP>::kSmem, splits, false, st, l, x, xs, W, C, scaled, v,
