@@ -740,7 +740,7 @@ GEMMAR_API int lora_apply(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, 
     int rc = check_ctx(ctx);
     if (rc)
         return rc;
-    if (!x || !out)
+    if (!x || !out || (y == out && y_stride != out_stride))
         return GEMMAR_ERR_ARG;
     if ((rc = check_lora(order, offsets, A, B, scales, ranks, T, K, N, R, r)) || (rc = check_rows(x, x_stride, K, 2)) ||
         (y && (rc = check_rows(y, y_stride, N, 2))) || (rc = check_rows(out, out_stride, N, 2, true)))
@@ -765,7 +765,7 @@ GEMMAR_API int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stri
     int rc = check_ctx(ctx);
     if (rc)
         return rc;
-    if (!x || !dy || !v || !dx || !dA || !dB)
+    if (!x || !dy || !v || !dx || !dA || !dB || (dx0 == dx && dx0_stride != dx_stride))
         return GEMMAR_ERR_ARG;
     if ((rc = check_lora(order, offsets, A, B, scales, ranks, T, K, N, R, r)) || (rc = check_rows(x, x_stride, K, 2)) ||
         (rc = check_rows(dy, dy_stride, N, 2)) || (dx0 && (rc = check_rows(dx0, dx0_stride, K, 2))) ||

@@ -156,10 +156,11 @@ struct GradSide {
     float *part;          // [split tile][r][C]
 };
 
-// Both of a call, and the tokens a tile.
+// Both of a call, the tokens a tile, and the split tiles that the scratch has room for:
+// enough for any plan, which offsets that are none could still exceed.
 struct GradCall {
     GradSide A, B;
-    int RP, size;
+    int RP, size, slots;
 };
 
 // The launches of lora_tile.cu.

@@ -395,7 +395,7 @@ struct GradCfg {
 
 template <int RP>
 __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs l, const GradSide A, const GradSide B,
-                                                                 int size, const Waits waits)
+                                                                 int size, int slots, const Waits waits)
 {
     using Cfg = GradCfg<RP>;
     extern __shared__ uint8_t smem_raw[];
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
     const int c = c0 + warp * 32 + lane;
     const uint32_t dw = d + (warp >> 2) * 2 * RP + ((uint32_t)((warp & 3) * 32) << 16);
     const float f = S.scaled ? l.scales[tile.a] : 1.0f;
-    const int slot = tile.of > 1 ? split_tiles_before(l, tile.a, size) + tile.index : 0;
+    const int slot = tile.of > 1 ? split_tiles_before(l, tile.a, size) + tile.index : -1;
 #pragma unroll
     for (int j0 = 0; j0 < RP; j0 += 8) {
         uint32_t hi[8], lo[8];
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
         for (int k = 0; k < 8; ++k) {
             const int j = j0 + k;
             const float g = steps > 0 && j < rank ? f * (__uint_as_float(hi[k]) + __uint_as_float(lo[k])) : 0.0f;
-            if (j < l.r && c < S.C) {
+            if (j < l.r && c < S.C && slot < slots) {
                 if (tile.of > 1)
                     S.part[((int64_t)slot * l.r + j) * S.C + c] = g;
                 else
@@ -533,7 +533,8 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
 }
 
 // The gradients of adapters whose tokens were cut: their tiles' parts in order.
-__global__ void __launch_bounds__(256) grad_join_kernel(const LoraArgs l, const GradSide A, const GradSide B, int size)
+__global__ void __launch_bounds__(256) grad_join_kernel(const LoraArgs l, const GradSide A, const GradSide B, int size,
+                                                        int slots)
 {
     const int a = blockIdx.x;
     grid_wait();
@@ -542,7 +543,10 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const LoraArgs l, const 
         return;
     const GradSide &S = blockIdx.z ? B : A;
     const int64_t elems = (int64_t)l.r * S.C;
-    const float *part = S.part + (int64_t)split_tiles_before(l, a, size) * elems;
+    const int first = split_tiles_before(l, a, size);
+    if (first + n > slots)
+        return;
+    const float *part = S.part + first * elems;
     for (int64_t e = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4; e < elems; e += (int64_t)gridDim.y * 1024) {
         float4 s = *reinterpret_cast<const float4 *>(part + e);
         for (int k = 1; k < n; ++k) {
@@ -595,14 +599,14 @@ cudaError_t run_up(const LoraArgs &l, const LoraCall &p, const uint16_t *v2, con
 }
 
 template <int RP>
-cudaError_t run_grad(const LoraArgs &l, const LoraCall &p, const GradSide &A, const GradSide &B, int size, cudaStream_t st)
+cudaError_t run_grad(const LoraArgs &l, const LoraCall &p, const GradCall &g, cudaStream_t st)
 {
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(tile_grad_kernel<RP>), GradCfg<RP>::kSmem);
     if (e != cudaSuccess)
         return e;
-    const int tiles = (A.C + kGradCols - 1) / kGradCols + (B.C + kGradCols - 1) / kGradCols;
-    const dim3 grid((unsigned)(l.T / size + l.R), tiles);
-    return launch(tile_grad_kernel<RP>, grid, kGradThreads, GradCfg<RP>::kSmem, 1, true, st, l, A, B, size,
+    const int tiles = (g.A.C + kGradCols - 1) / kGradCols + (g.B.C + kGradCols - 1) / kGradCols;
+    const dim3 grid((unsigned)(l.T / g.size + l.R), tiles);
+    return launch(tile_grad_kernel<RP>, grid, kGradThreads, GradCfg<RP>::kSmem, 1, true, st, l, g.A, g.B, g.size, g.slots,
                   Waits{p.status, p.timeout_ns});
 }
 
@@ -662,16 +666,16 @@ GradCall lora_grad_call(const LoraArgs &l, const LoraCall &p, const Halves &h, c
     size = std::min<int64_t>(size, (l.T + 63) / 64 * 64);
     float *part = ws + 2 * l.T * h.RP;
     const int64_t slots = size < l.T ? 2 * (l.T / size) : 0;
-    return {{x, xs, K, 0, h.w2, dA, part}, {dy, ys, N, 1, h.v2, dB, part + slots * l.r * K}, h.RP, (int)size};
+    return {{x, xs, K, 0, h.w2, dA, part}, {dy, ys, N, 1, h.v2, dB, part + slots * l.r * K}, h.RP, (int)size, (int)slots};
 }
 
 cudaError_t launch_tile_grad(const LoraArgs &l, const LoraCall &p, const GradCall &g, cudaStream_t st)
 {
     switch (g.RP) {
-    case 16: return run_grad<16>(l, p, g.A, g.B, g.size, st);
-    case 32: return run_grad<32>(l, p, g.A, g.B, g.size, st);
-    case 64: return run_grad<64>(l, p, g.A, g.B, g.size, st);
-    default: return run_grad<128>(l, p, g.A, g.B, g.size, st);
+    case 16: return run_grad<16>(l, p, g, st);
+    case 32: return run_grad<32>(l, p, g, st);
+    case 64: return run_grad<64>(l, p, g, st);
+    default: return run_grad<128>(l, p, g, st);
     }
 }
 
@@ -681,7 +685,7 @@ cudaError_t launch_grad_join(const LoraArgs &l, const LoraCall &p, const GradCal
         return cudaSuccess;   // no adapter was cut
     const int64_t most = (int64_t)l.r * std::max(g.A.C, g.B.C);
     const int join = (int)std::min<int64_t>((most + 1023) / 1024, std::max(1, 8 * p.num_sms / l.R));
-    return launch(grad_join_kernel, dim3(l.R, join, 2), 256, 0, 1, true, st, l, g.A, g.B, g.size);
+    return launch(grad_join_kernel, dim3(l.R, join, 2), 256, 0, 1, true, st, l, g.A, g.B, g.size, g.slots);
 }
 
 }  // namespace gemmar

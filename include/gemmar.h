@@ -494,7 +494,7 @@ int lora_plan(gemmar_ctx *ctx, const int32_t *adapter_ids, int64_t T, int R, int
  * rows on 16 bytes.  v is fp32 and enters the second product as two bf16 parts
  * (its rounding error is below 2^-16); out is rounded once.
  *   x bf16 [T,K], y bf16 [T,N] (NULL: 0) and out bf16 [T,N] with row strides; y may
- *   be out itself.  order, offsets: lora_plan's form (entries outside [0,T) are
+ *   be out itself, at the same stride.  order, offsets: lora_plan's form (entries outside [0,T) are
  *   skipped).  A bf16 [R,r,K], B bf16 [R,r,N], scales fp32 [R], ranks int32 [R] (NULL:
  *   r for all; rows beyond ranks[a] are not used).  v: NULL, or fp32 [T,r] for the
  *   backward pass: row i belongs to token order[i]; rows past offsets[R] are left

@@ -310,3 +310,23 @@ def test_refusals(g, ctx):
     finally:
         small.close()
     assert g.gemmar_status(ctx)[0] == 0
+
+
+def test_offsets_that_are_no_plan_stay_in_bounds(g, ctx):
+    """Offsets that go back and forth name every token for every adapter: the result means nothing, but
+    nothing outside the outputs is written, and the next call is right."""
+    T, R, r, K, N = 900, 6, 16, 256, 384
+    d = make(g, ctx, mixed_ids(T, R, 3), R, r, K, N, seed=5, ranks=None)
+    out, v = apply(g, ctx, d)
+    grads = apply_bwd(g, ctx, d, v)
+    bad = dict(d, offsets=torch.tensor([0, T, 0, T, -7, 1 << 30, 0], dtype=torch.int32, device="cuda"))
+    fenced = torch.full((T + 8, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    apply(g, ctx, bad, out=fenced[4:T + 4])
+    assert (fenced[:4] == 3).all() and (fenced[T + 4:] == 3).all()
+    fence = {k: torch.full((n + 64,), 3.0, dtype=torch.bfloat16, device="cuda") for k, n in (("dx", T * K), ("dA", R * r * K), ("dB", R * r * N))}
+    inner = [fence[k][32:-32].view(s) for k, s in (("dx", (T, K)), ("dA", (R, r, K)), ("dB", (R, r, N)))]
+    g.lora_apply_bwd(ctx, d["x"], d["dy"], d["order"], bad["offsets"], d["A"], d["B"], d["scales"], d["ranks"], v, *inner, dx0=d["dx0"])
+    assert all((f[:32] == 3).all() and (f[-32:] == 3).all() for f in fence.values())
+    assert torch.equal(apply(g, ctx, d)[0], out)
+    assert all(torch.equal(a, b) for a, b in zip(apply_bwd(g, ctx, d, v), grads))
+    assert g.gemmar_status(ctx)[0] == 0
