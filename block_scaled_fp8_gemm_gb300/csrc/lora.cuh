@@ -86,7 +86,7 @@ __device__ __forceinline__ int split_tiles_before(const LoraArgs &l, int a, int 
 
 // Sum over the CTAs of the cluster, in the order of their ranks, of the fp32 array
 // [rows][cols] that each has at the same shared-memory address, rows `pitch` floats
-// apart; put(row, col, sum) is called for each element by one thread of one of
+// apart; put(row, col, sum) is called for every four columns by one thread of one of
 // them.  The whole cluster calls it, after its threads have written the array.
 template <typename Put>
 __device__ __forceinline__ void cluster_sum(uint32_t array, int rows, int cols, int pitch, int ctas, Put put)
@@ -95,14 +95,16 @@ __device__ __forceinline__ void cluster_sum(uint32_t array, int rows, int cols, 
         __syncthreads();
     else
         ptx::cluster_sync();
-    const int me = ctas == 1 ? 0 : (int)ptx::cluster_ctarank(), share = (rows + ctas - 1) / ctas;
-    const int lo = me * share, n = max(0, min(share, rows - lo)) * cols;
+    const int me = ctas == 1 ? 0 : (int)ptx::cluster_ctarank(), share = (rows + ctas - 1) / ctas, quads = cols / 4;
+    const int lo = me * share, n = max(0, min(share, rows - lo)) * quads;
     for (int e = threadIdx.x; e < n; e += blockDim.x) {
-        const int row = lo + e / cols, col = e % cols;
+        const int row = lo + e / quads, col = e % quads * 4;
         const uint32_t at = array + (row * pitch + col) * 4;
-        float s = ptx::ld_shared_cluster_f32(ptx::mapa_shared(at, ctas == 1 ? me : 0));
-        for (int p = 1; p < ctas; ++p)
-            s += ptx::ld_shared_cluster_f32(ptx::mapa_shared(at, p));
+        float4 s = ptx::ld_shared_cluster_f32x4(ptx::mapa_shared(at, ctas == 1 ? ptx::cluster_ctarank() : 0));
+        for (int p = 1; p < ctas; ++p) {
+            const float4 a = ptx::ld_shared_cluster_f32x4(ptx::mapa_shared(at, p));
+            s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
+        }
         put(row, col, s);
     }
     if (ctas > 1)
@@ -135,6 +137,28 @@ __device__ __forceinline__ void put_pair(const Halves &h, int64_t i, int j, int 
         put_halves(h.w2 + i * 2 * h.RP, h.RP, j, w);
     if (h.v2)
         put_halves(h.v2 + i * 2 * h.RP, h.RP, j, j < r ? __ldg(h.v + i * r + j) : 0.0f);
+}
+
+__device__ __forceinline__ void put_halves4(uint16_t *row, int RP, int j, const float4 &x)
+{
+    const uint32_t a = ptx::bf16x2_from_f32(x.x, x.y), b = ptx::bf16x2_from_f32(x.z, x.w);
+    *reinterpret_cast<uint2 *>(row + j) = make_uint2(a, b);
+    *reinterpret_cast<uint2 *>(row + RP + j) =
+        make_uint2(ptx::bf16x2_from_f32(x.x - __uint_as_float(a << 16), x.y - __uint_as_float(a & 0xFFFF0000u)),
+                   ptx::bf16x2_from_f32(x.z - __uint_as_float(b << 16), x.w - __uint_as_float(b & 0xFFFF0000u)));
+}
+
+// The same for j .. j + 3, j a multiple of four.
+__device__ __forceinline__ void put_pair4(const Halves &h, int64_t i, int j, int r, const float4 &w)
+{
+    if (h.w2)
+        put_halves4(h.w2 + i * 2 * h.RP, h.RP, j, w);
+    if (h.v2) {
+        const float *v = h.v + i * r + j;
+        put_halves4(h.v2 + i * 2 * h.RP, h.RP, j,
+                    make_float4(j < r ? __ldg(v) : 0.0f, j + 1 < r ? __ldg(v + 1) : 0.0f, j + 2 < r ? __ldg(v + 2) : 0.0f,
+                                j + 3 < r ? __ldg(v + 3) : 0.0f));
+    }
 }
 
 __host__ __device__ constexpr int pad_rank(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }

@@ -149,26 +149,33 @@ __global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs 
     }
     wait_mma(done + (steps - 1) % Cfg::kStages, ((steps - 1) / Cfg::kStages) & 1, &abort_flag, waits);
     // the stages are free: D goes there for the cluster's sum
-    constexpr int kPitch = RP + 1;
+    constexpr int kPitch = RP + 4;   // whole 16-byte pieces, a row's off the banks of the next
     static_assert(kRows * kPitch * 4 <= Cfg::kStages * Cfg::kStage, "D fits the stages");
     if (warp < 4) {
-        float *mine = reinterpret_cast<float *>(smem) + (warp * 32 + lane) * kPitch;
+        const uint32_t mine = base + (warp * 32 + lane) * kPitch * 4;
 #pragma unroll
         for (int j0 = 0; j0 < RP; j0 += 16) {
             uint32_t r[16];
             tmem_ld_x16(d + ((uint32_t)(warp * 32) << 16) + j0, r);
             tmem_wait_ld(r);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                mine[j0 + j] = __uint_as_float(r[j]);
+            for (int j = 0; j < 16; j += 4)
+                st_shared_v4(mine + (j0 + j) * 4, make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]));
         }
     }
     const float f = scaled ? l.scales[tile.a] : 1.0f;
     float *out = v ? v + (int64_t)tile.i0 * l.r : nullptr;
-    cluster_sum(base, tile.count, RP, kPitch, gridDim.y, [&](int i, int j, float sum) {
-        if (v && j < l.r)
-            out[(int64_t)i * l.r + j] = f * sum;
-        put_pair(halves, tile.i0 + i, j, l.r, f * sum);
+    cluster_sum(base, tile.count, RP, kPitch, gridDim.y, [&](int i, int j, float4 s) {
+        s = make_float4(f * s.x, f * s.y, f * s.z, f * s.w);
+        if (v) {
+            float *o = out + (int64_t)i * l.r + j;
+            const float e[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (j + k < l.r)
+                    o[k] = e[k];
+        }
+        put_pair4(halves, tile.i0 + i, j, l.r, s);
     });
     tc_fence_before();
     __syncthreads();

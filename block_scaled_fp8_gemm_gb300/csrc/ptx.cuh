@@ -181,6 +181,16 @@ __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr)
     return v;
 }
 
+__device__ __forceinline__ float4 ld_shared_cluster_f32x4(uint32_t cluster_addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
+    return v;
+}
+
 // Arrive on an mbarrier of another CTA of the cluster.  Default (CTA-scope)
 // release: a cluster-scope release would first wait for every memory access
 // this thread has in flight (scale prefetches, streamed partial stores) to be
