@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t done[Cfg::kStages];
     __shared__ uint32_t tmem_slot;
-    __shared__ __align__(16) int tok[2 * Cfg::kStages][kGradTokens];   // a ring of the steps' tokens
+    __shared__ const uint16_t *rows[2 * Cfg::kStages][kGradTokens];   // a ring of the steps' rows
     __shared__ int abort_flag;
     const Tile tile = find_tile(l, blockIdx.x, size, false, 1);
     if (tile.of == 0) {
@@ -437,45 +437,55 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
     // kPer apart.  Tokens 8 apart are 1024 bytes apart in a tile and share their swizzle.
     const int ch = tid & 31;
     const bool in = c0 + ch * 8 < S.C;
-    const uint16_t *xc = S.x + (in ? c0 + ch * 8 : 0);
+    const int col = c0 + ch * 8;
     const uint32_t at_x = (ch >> 3) * Cfg::kTile + sw128(tid >> 5, ch & 7);
     constexpr int kPer = kGradThreads / (RP / 4);
     const int prow = tid / (RP / 4), pc = tid % (RP / 4);
     const uint32_t at_p = Cfg::kX + (pc >> 3) * Cfg::kTile + sw128(prow, pc & 7);
     const uint16_t *pr = S.p2 + (int64_t)(tile.i0 + prow) * (2 * RP) + pc * 8;
-    // the tokens of step s are asked for with the rows of step s - kStages: a load whose
-    // latency a step would otherwise have to wait for
-    auto look_up = [&](int s) {
-        if (tid < kGradTokens && s * kGradTokens + tid < tile.count)
-            cp_async_ca4(smem_u32(&tok[s % (2 * Cfg::kStages)][tid]), l.order + tile.i0 + s * kGradTokens + tid);
+    // Lane t of warp 0 looks the rows up, kStages + 2 steps before their copies: a load whose
+    // latency a step would otherwise wait for, and one address for all that copy the row.
+    auto token = [&](int s) {
+        const int i = s * kGradTokens + tid;
+        return tid < kGradTokens && i < tile.count ? __ldg(l.order + tile.i0 + i) : -1;
     };
+    auto put_row = [&](int slot, int t) {
+        if (tid < kGradTokens)
+            rows[slot][tid] = t >= 0 && t < l.T ? S.x + t * S.xs : nullptr;
+    };
+    for (int s = 0; s < Cfg::kStages; ++s)
+        put_row(s, token(s));
+    int t0 = token(Cfg::kStages), t1 = token(Cfg::kStages + 1);
+    int put = 0, row_put = Cfg::kStages, row_get = 0;   // stage of the next copies; row slots
+    int left = tile.count - prow;
     auto fetch = [&](int s) {
         if (s < steps) {
-            const uint32_t st = base + (s % Cfg::kStages) * Cfg::kStage;
-            const int left = tile.count - s * kGradTokens;
-            const int *row = tok[s % (2 * Cfg::kStages)] + (tid >> 5);
+            const uint32_t st = base + put * Cfg::kStage;
+            const uint16_t *const *row = rows[row_get] + (tid >> 5);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int t = (tid >> 5) + 8 * i < left ? row[8 * i] : -1;
-                const bool ok = in && t >= 0 && t < l.T;
-                cp_async_cg16_or_zero(st + at_x + i * kSw, ok ? xc + t * S.xs : xc, ok);
+                const uint16_t *r = row[8 * i];
+                const bool ok = in && r != nullptr;
+                cp_async_cg16_or_zero(st + at_x + i * kSw, ok ? r + col : S.x, ok);
             }
 #pragma unroll
             for (int i = 0; i < kGradTokens; i += kPer) {
                 if (kPer <= kGradTokens || prow < kGradTokens) {
-                    const bool ok = prow + i < left;
+                    const bool ok = i < left;
                     cp_async_cg16_or_zero(st + at_p + i * 128, ok ? pr + i * 2 * RP : S.p2, ok);
                 }
             }
             pr += kGradTokens * 2 * RP;
+            left -= kGradTokens;
+            put_row(row_put, t0);
+            t0 = t1;
+            t1 = token(s + Cfg::kStages + 2);
+            put = put + 1 == Cfg::kStages ? 0 : put + 1;
+            row_put = row_put + 1 == 2 * Cfg::kStages ? 0 : row_put + 1;
+            row_get = row_get + 1 == 2 * Cfg::kStages ? 0 : row_get + 1;
         }
-        look_up(s + Cfg::kStages);
         cp_async_commit();
     };
-    for (int s = 0; s < Cfg::kStages; ++s)
-        look_up(s);
-    cp_async_commit();
-    cp_async_wait<0>();
     __syncthreads();
     grid_wait();   // the two parts of w and v
     grid_launch_next();
