@@ -165,7 +165,7 @@ class Context:
 
     @property
     def handle(self) -> ctypes.c_void_p:
-        if not self._h:
+        if self._h.value is None:
             raise ValueError("context already destroyed")
         return self._h
 
@@ -279,9 +279,9 @@ def band_reduce(ctx: Context, W, P: int, M: int, N: int, bands: int, out, stream
 
 
 def _xdtype(x) -> int:
-    if x.dtype == torch.bfloat16:
+    if x.dtype is torch.bfloat16:
         return GEMMAR_DTYPE_BF16
-    if x.dtype == torch.float32:
+    if x.dtype is torch.float32:
         return GEMMAR_DTYPE_F32
     raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")
 
@@ -383,17 +383,23 @@ def _dense(t, shape, name: str, dtype):
     """Pointer of a contiguous tensor of that shape and type; None stays None."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _refuse(t, shape, name, dtype, False)
 
 
 def _rows(t, shape, name: str, dtype=None):
     """(pointer, row stride) of a [rows, cols] matrix with contiguous rows, which may be a view."""
-    if isinstance(t, torch.Tensor) and (dtype is None or t.dtype is dtype) and t.shape == shape and t.is_cuda:
-        row, col = t.stride()
-        if col == 1 or shape[1] == 1:
-            return t.data_ptr(), row if shape[0] > 1 else shape[1]
+    try:
+        if (dtype is None or t.dtype is dtype) and t.shape == shape and t.is_cuda:
+            row, col = t.stride()
+            if col == 1 or shape[1] == 1:
+                return t.data_ptr(), row if shape[0] > 1 else shape[1]
+    except AttributeError:
+        pass
     _refuse(t, shape, name, dtype, True)
 
 
@@ -401,7 +407,7 @@ def _gate(gate, M: int, N: int):
     """(pointer, row stride) of a gate: [N] (stride 0) or [M, N]."""
     if gate is None:
         return None, 0
-    if isinstance(gate, torch.Tensor) and gate.dim() == 1:
+    if getattr(gate, "ndim", 2) == 1:
         return _dense(gate, (N,), "gate", torch.bfloat16), 0
     ptr, stride = _rows(gate, (M, N), "gate", torch.bfloat16)
     if stride == 0:
@@ -420,15 +426,15 @@ def norm_gate_residual(ctx: Context, y, h, w_pre, t, w_post=None, gate=None, alp
     """t = alpha*h + beta*gate*norm(y)*w_post and the next block's input norm(t)*w_pre, as bf16 rows u
     and/or e4m3 codes q with fp32 scales per 1x128 (gemm_blockscale_fp8's A operand).  w_post None: no
     post norm; w_pre None: t only; gate bf16 [N] or [M, N]; rstd fp32 [M, 2] for the backward pass."""
-    M, N = y.shape
-    yp, ys = _rows(y, (M, N), "y")
-    hp, hs = _rows(h, (M, N), "h")
+    shape = M, N = y.shape
+    width, f32, bf16 = (N,), torch.float32, torch.bfloat16
+    yp, ys = _rows(y, shape, "y")
+    hp, hs = _rows(h, shape, "h")
     gp, gs = _gate(gate, M, N)
-    f32, bf16 = torch.float32, torch.bfloat16
     _check(_lib.norm_gate_residual(ctx.handle, yp, _xdtype(y), ys, hp, _xdtype(h), hs,
-                                   _dense(w_post, (N,), "w_post", f32), _dense(w_pre, (N,), "w_pre", f32), gp, gs,
-                                   alpha, beta, eps, M, N, _dense(t, (M, N), "t", h.dtype),
-                                   _dense(u, (M, N), "u", bf16), _codes(q, (M, N), "q"),
+                                   _dense(w_post, width, "w_post", f32), _dense(w_pre, width, "w_pre", f32), gp, gs,
+                                   alpha, beta, eps, M, N, _dense(t, shape, "t", h.dtype),
+                                   _dense(u, shape, "u", bf16), _codes(q, shape, "q"),
                                    _dense(scales, (M, N // 128), "scales", f32), _dense(rstd, (M, 2), "rstd", f32),
                                    _stream(stream)),
            "norm_gate_residual")
