@@ -112,10 +112,9 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 // Fragments are loaded straight from memory into registers, 16 bytes a lane, no
 // staging: the contraction index of an MMA may be permuted as long as both
 // operands agree, so lane (g, q) takes eight consecutive elements of its row for
-// two MMAs.  Weights are the M operand, tokens the N operand (8 a tile).
+// two MMAs.  Weights are the M operand, tokens the N operand.
 
-constexpr int kFewBatch = 256;   // largest batch for this kernel
-constexpr int kFewTokens = 32;   // tokens a tile: four N tiles
+constexpr int kFewTokens = 8;    // tokens a tile: one N tile
 constexpr int kFewWarps = 8;
 constexpr int kFewRanks = 32;    // ranks at a time in the first product: two M tiles
 constexpr int kPairRow = GEMMAR_LORA_MAX_RANK / 2 + 4;   // rank pairs of a token, padded off the banks
@@ -137,13 +136,12 @@ struct Factor {
     bool scaled;
 };
 
-// Sums of 16 MT ranks from j0 over the warp's share of the columns, for 8 NT tokens,
-// into sums[rank][token].
-template <int MT, int NT>
+// Sums of 16 MT ranks from j0 over the warp's share of the columns into sums[rank][token].
+template <int MT>
 __device__ __forceinline__ void few_down(const LoraArgs &l, const Tile &tile, int rank, int j0, const Factor &f,
                                          const uint16_t *__restrict__ x, int64_t xs, float (&sums)[kFewRanks][kFewTokens + 1])
 {
-    constexpr int kUnroll = 2 * MT + NT <= 3 ? 8 : 2 * MT + NT <= 6 ? 4 : 2;
+    constexpr int kUnroll = MT == 1 ? 8 : 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const uint16_t *wr[2 * MT];   // rows j0 + g, + 8, ...
     bool wok[2 * MT];
@@ -153,36 +151,25 @@ __device__ __forceinline__ void few_down(const LoraArgs &l, const Tile &tile, in
         wok[i] = j < rank;
         wr[i] = f.W + ((int64_t)tile.a * l.r + (wok[i] ? j : 0)) * f.C + q * 8;
     }
-    const uint16_t *xr[NT];
-    bool xok[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int i = n * 8 + g;
-        const int t = i < tile.count ? __ldg(l.order + tile.i0 + i) : -1;
-        xok[n] = t >= 0 && t < l.T;
-        xr[n] = x + (xok[n] ? t : 0) * xs + q * 8;
-    }
+    const int t = g < tile.count ? __ldg(l.order + tile.i0 + g) : -1;
+    const bool xok = t >= 0 && t < l.T;
+    const uint16_t *xr = x + (xok ? t : 0) * xs + q * 8;
     // blocks of 32 columns, dealt evenly to the cluster's warps
     const int blocks = (f.C + 31) / 32, shares = gridDim.y * kFewWarps, share = blockIdx.y * kFewWarps + warp;
     const int b0 = (int)((int64_t)blocks * share / shares), b1 = (int)((int64_t)blocks * (share + 1) / shares);
-    float acc[MT][NT][4] = {};
+    float acc[MT][4] = {};
     auto block = [&](int b, bool in) {
-        uint4 w[2 * MT], xv[NT];
+        uint4 w[2 * MT];
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i)
             w[i] = in && wok[i] ? __ldg(reinterpret_cast<const uint4 *>(wr[i] + b * 32)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            xv[n] = in && xok[n] ? __ldg(reinterpret_cast<const uint4 *>(xr[n] + b * 32)) : make_uint4(0, 0, 0, 0);
+        const uint4 xv = in && xok ? __ldg(reinterpret_cast<const uint4 *>(xr + b * 32)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const uint32_t lo[4] = {w[2 * m].x, w[2 * m + 1].x, w[2 * m].y, w[2 * m + 1].y};
             const uint32_t hi[4] = {w[2 * m].z, w[2 * m + 1].z, w[2 * m].w, w[2 * m + 1].w};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                mma_bf16(acc[m][n], lo, xv[n].x, xv[n].y);
-                mma_bf16(acc[m][n], hi, xv[n].z, xv[n].w);
-            }
+            mma_bf16(acc[m], lo, xv.x, xv.y);
+            mma_bf16(acc[m], hi, xv.z, xv.w);
         }
     };
     int b = b0;
@@ -196,31 +183,26 @@ __device__ __forceinline__ void few_down(const LoraArgs &l, const Tile &tile, in
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                sums[m * 16 + g + (e >> 1) * 8][n * 8 + q * 2 + (e & 1)] = acc[m][n][e];
+        for (int e = 0; e < 4; ++e)
+            sums[m * 16 + g + (e >> 1) * 8][q * 2 + (e & 1)] = acc[m][e];
 }
 
-// out rows of a tile of 8 NT tokens, 64 columns a warp at a time; v enters as two bf16
-// parts.  D[n, token] = sum_j W[j, n] v[token, j]: an MMA's two row halves are the even
-// and odd columns of a lane's eight, so the lane ends with eight consecutive columns of
-// two tokens.
-template <int NT>
+// out rows of a tile, 64 columns a warp at a time; v enters as two bf16 parts.
+// D[n, token] = sum_j W[j, n] v[token, j]: an MMA's two row halves are the even and odd
+// columns of a lane's eight, so the lane ends with eight consecutive columns of two
+// tokens.
 __device__ __forceinline__ void few_up(const LoraArgs &l, const Tile &tile, int rank, const Factor &f, const FewSmem &sm,
                                        const uint16_t *base, int64_t bs, uint16_t *out, int64_t os)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int steps = (rank + 15) / 16;
     const float scale = f.scaled && tile.a < l.R ? l.scales[tile.a] : 1.0f;
-    int tok[NT][2];
+    int tok[2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int i = n * 8 + q * 2 + k, t = i < tile.count ? __ldg(l.order + tile.i0 + i) : -1;
-            tok[n][k] = t >= 0 && t < l.T ? t : -1;
-        }
+    for (int k = 0; k < 2; ++k) {
+        const int i = q * 2 + k, t = i < tile.count ? __ldg(l.order + tile.i0 + i) : -1;
+        tok[k] = t >= 0 && t < l.T ? t : -1;
+    }
     for (int b = blockIdx.y * kFewWarps + warp; b * 64 < f.C; b += gridDim.y * kFewWarps) {
         const int n0 = b * 64 + g * 8;
         const bool in = n0 < f.C;
@@ -232,63 +214,52 @@ __device__ __forceinline__ void few_up(const LoraArgs &l, const Tile &tile, int 
                 w[i] = in && j < rank ? __ldg(reinterpret_cast<const uint4 *>(w0 + (int64_t)j * f.C)) : make_uint4(0, 0, 0, 0);
             }
         };
-        uint4 w[4], y[NT][2];
+        uint4 w[4], y[2];
         load(0, w);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                y[n][k] = base && in && tok[n][k] >= 0 ? *reinterpret_cast<const uint4 *>(base + tok[n][k] * bs + n0)
-                                                       : make_uint4(0, 0, 0, 0);
-        float acc[4][NT][4] = {};   // column pair, token tile, fragment
+        for (int k = 0; k < 2; ++k)
+            y[k] = base && in && tok[k] >= 0 ? *reinterpret_cast<const uint4 *>(base + tok[k] * bs + n0) : make_uint4(0, 0, 0, 0);
+        float acc[4][4] = {};   // column pair, fragment
         for (int s = 0; s < steps; ++s) {
             uint4 next[4];
             load(s + 1, next);
             const uint32_t rows[4][4] = {{w[0].x, w[0].y, w[0].z, w[0].w}, {w[1].x, w[1].y, w[1].z, w[1].w},
                                          {w[2].x, w[2].y, w[2].z, w[2].w}, {w[3].x, w[3].y, w[3].z, w[3].w}};
+            const uint32_t h0 = sm.v.hi[g][s * 8 + q], h1 = sm.v.hi[g][s * 8 + 4 + q];
+            const uint32_t l0 = sm.v.lo[g][s * 8 + q], l1 = sm.v.lo[g][s * 8 + 4 + q];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int i = n * 8 + g;
-                const uint32_t h0 = sm.v.hi[i][s * 8 + q], h1 = sm.v.hi[i][s * 8 + 4 + q];
-                const uint32_t l0 = sm.v.lo[i][s * 8 + q], l1 = sm.v.lo[i][s * 8 + 4 + q];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t a[4] = {
-                        __byte_perm(rows[0][c], rows[1][c], 0x5410), __byte_perm(rows[0][c], rows[1][c], 0x7632),
-                        __byte_perm(rows[2][c], rows[3][c], 0x5410), __byte_perm(rows[2][c], rows[3][c], 0x7632)};
-                    mma_bf16(acc[c][n], a, h0, h1);
-                    mma_bf16(acc[c][n], a, l0, l1);
-                }
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t a[4] = {
+                    __byte_perm(rows[0][c], rows[1][c], 0x5410), __byte_perm(rows[0][c], rows[1][c], 0x7632),
+                    __byte_perm(rows[2][c], rows[3][c], 0x5410), __byte_perm(rows[2][c], rows[3][c], 0x7632)};
+                mma_bf16(acc[c], a, h0, h1);
+                mma_bf16(acc[c], a, l0, l1);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 w[i] = next[i];
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int k = 0; k < 2; ++k) {
+            if (!in || tok[k] < 0)
+                continue;
+            uint32_t yw[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+            if (rank > 0) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                if (!in || tok[n][k] < 0)
-                    continue;
-                uint32_t yw[4] = {y[n][k].x, y[n][k].y, y[n][k].z, y[n][k].w};
-                if (rank > 0) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        yw[c] = bf16x2_from_f32(fmaf(scale, acc[c][n][k], __uint_as_float(yw[c] << 16)),
-                                                fmaf(scale, acc[c][n][2 + k], __uint_as_float(yw[c] & 0xFFFF0000u)));
-                }
-                *reinterpret_cast<uint4 *>(out + tok[n][k] * os + n0) = make_uint4(yw[0], yw[1], yw[2], yw[3]);
+                for (int c = 0; c < 4; ++c)
+                    yw[c] = bf16x2_from_f32(fmaf(scale, acc[c][k], __uint_as_float(yw[c] << 16)),
+                                            fmaf(scale, acc[c][2 + k], __uint_as_float(yw[c] & 0xFFFF0000u)));
             }
+            *reinterpret_cast<uint4 *>(out + tok[k] * os + n0) = make_uint4(yw[0], yw[1], yw[2], yw[3]);
         }
     }
 }
 
-__global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const LoraArgs l, const uint16_t *__restrict__ x, int64_t xs,
+__global__ void __launch_bounds__(kFewWarps * 32, 3) few_kernel(const LoraArgs l, const uint16_t *__restrict__ x, int64_t xs,
                                                               const Factor down, const Factor up, const uint16_t *base,
                                                               int64_t bs, uint16_t *out, int64_t os, float *v_out, const Halves halves)
 {
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    FewSmem &sm = *reinterpret_cast<FewSmem *>(smem_raw);
+    __shared__ FewSmem sm;
     const Tile tile = find_tile(l, blockIdx.x, kFewTokens, base != out);
     if (tile.of == 0)
         return;
@@ -307,17 +278,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const LoraArgs l
         }
     }
     for (int j0 = 0; j0 < rank; j0 += kFewRanks) {
-        const bool wide = rank - j0 > 16;
-        if (tile.count <= 8) {
-            if (wide)
-                few_down<2, 1>(l, tile, rank, j0, down, x, xs, sm.sums[warp]);
-            else
-                few_down<1, 1>(l, tile, rank, j0, down, x, xs, sm.sums[warp]);
-        } else if (wide) {
-            few_down<2, 4>(l, tile, rank, j0, down, x, xs, sm.sums[warp]);
-        } else {
-            few_down<1, 4>(l, tile, rank, j0, down, x, xs, sm.sums[warp]);
-        }
+        if (rank - j0 > 16)
+            few_down<2>(l, tile, rank, j0, down, x, xs, sm.sums[warp]);
+        else
+            few_down<1>(l, tile, rank, j0, down, x, xs, sm.sums[warp]);
         __syncthreads();
         const int nj = min(kFewRanks, rank - j0);
         for (int e = tid; e < nj * tile.count; e += kFewWarps * 32) {
@@ -335,8 +299,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const LoraArgs l
             cluster_sync();
         // v, in rank order, by every CTA for itself
         const float f = down.scaled ? l.scales[tile.a] : 1.0f;
-        const int rows = tile.count <= 8 ? 8 : kFewTokens;
-        for (int e = tid; e < rows * pairs; e += kFewWarps * 32) {
+        for (int e = tid; e < kFewTokens * pairs; e += kFewWarps * 32) {
             const int i = e / pairs, p = e - i * pairs;
             float v[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -371,10 +334,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const LoraArgs l
         }
     }
     __syncthreads();
-    if (tile.count <= 8)
-        few_up<1>(l, tile, rank, up, sm, base, bs, out, os);
-    else
-        few_up<4>(l, tile, rank, up, sm, base, bs, out, os);
+    few_up(l, tile, rank, up, sm, base, bs, out, os);
     if (rank > 0 && ctas > 1)
         cluster_wait();   // no CTA leaves while another reads its sums
 }
@@ -396,20 +356,24 @@ cudaError_t launch_lora_plan(const int32_t *ids, int64_t T, int R, int32_t *orde
 
 namespace {
 
+// Few tokens an adapter: its weights are read again for every eight of them, from L2 after
+// the first, which costs T r and beats the tensor-core tiles up to here (K = 2048 or 16384,
+// N = 7168; this kernel against the tiles): T = 64 of 16 adapters, r = 16, 9 us against 16;
+// 512 of 64, 31 against 68; 1024 of 32, 22 against 28; 256 of 8, r = 64, 26 against 16.
+bool few(const LoraArgs &l) { return l.T <= 4096 && l.T * l.r <= 1024 * (int64_t)l.R; }
+
 cudaError_t launch_few(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const Factor &down,
                        const Factor &up, const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, float *v,
                        const Halves &halves, cudaStream_t st)
 {
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(few_kernel), sizeof(FewSmem));
-    if (e != cudaSuccess)
-        return e;
-    // clusters as large as fill the SMs twice
+    // clusters as large as fill the SMs, of which three CTAs each, were all tiles there are
+    // to be half of the most there can be
     const int64_t tiles = most_tiles(l.T, l.R, kFewTokens, base != out);
     int ctas = kMaxSplits;
-    while (ctas > 1 && tiles * ctas > 2 * p.num_sms)
+    while (ctas > 1 && tiles * ctas > 4 * p.num_sms)
         ctas /= 2;
-    return launch(few_kernel, dim3((unsigned)tiles, ctas), kFewWarps * 32, sizeof(FewSmem), ctas, false, st, l, x, xs, down,
-                  up, base, bs, out, os, v, halves);
+    return launch(few_kernel, dim3((unsigned)tiles, ctas), kFewWarps * 32, 0, ctas, false, st, l, x, xs, down, up, base, bs,
+                  out, os, v, halves);
 }
 
 }  // namespace
@@ -425,7 +389,7 @@ cudaError_t launch_lora_apply(const LoraArgs &l, const LoraCall &p, const uint16
                               const uint16_t *B, int N, const uint16_t *y, int64_t ys, uint16_t *out, int64_t os, float *v,
                               float *ws, cudaStream_t st)
 {
-    if (l.T <= kFewBatch)
+    if (few(l))
         return launch_few(l, p, x, xs, Factor{A, K, false}, Factor{B, N, true}, y, ys, out, os, v, Halves{}, st);
     const Halves h = lora_halves(nullptr, l.T, l.r, ws);
     TRY(launch_tile_down(l, p, x, xs, A, K, false, v, h, st));
@@ -439,7 +403,7 @@ cudaError_t launch_lora_apply_bwd(const LoraArgs &l, const LoraCall &p, const ui
 {
     const Halves h = lora_halves(v, l.T, l.r, ws);
     const GradCall g = lora_grad_call(l, p, h, x, xs, K, dA, dy, dys, N, dB, ws, ws_floats);
-    if (l.T <= kFewBatch) {
+    if (few(l)) {
         TRY(launch_few(l, p, dy, dys, Factor{B, N, true}, Factor{A, K, false}, dx0, dx0s, dx, dxs, nullptr, h, st));
         TRY(launch_tile_grad(l, p, g, st));
     } else {
