@@ -50,9 +50,10 @@ __device__ __forceinline__ uint32_t enc2_guarded(float a, float b, float s, floa
 struct Enc {
     float s, yl, yh;
     bool fast;
-    __device__ __forceinline__ explicit Enc(float sc) : s(sc)
+    __device__ __forceinline__ static float reciprocal(float sc) { return sc > 0.0f ? __frcp_rn(sc) : 0.0f; }
+    __device__ __forceinline__ explicit Enc(float sc) : Enc(sc, reciprocal(sc)) {}
+    __device__ __forceinline__ Enc(float sc, float y) : s(sc)
     {
-        const float y = sc > 0.0f ? __frcp_rn(sc) : 0.0f;
         yl = __fmul_rn(y, 1.0f - 0x1p-21f);
         yh = __fmul_rn(y, 1.0f + 0x1p-21f);
         fast = sc >= 0x1p-125f;   // 1/s <= 2^125: finite, and y (1 + 2^-21) cannot overflow

@@ -223,6 +223,18 @@ __device__ __forceinline__ void store_vec(void *base, int64_t i, const Vec<W> &v
     r.store(static_cast<char *>(base) + i * (BF ? 2 : 4));
 }
 
+template <int BYTES>
+__device__ __forceinline__ void zero_slot(uint32_t slot)
+{
+    if constexpr (BYTES == 8) {
+        asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(slot), "r"(0u) : "memory");
+    } else {
+#pragma unroll
+        for (int k = 0; k < BYTES; k += 16)
+            st_shared_v4(slot + k, make_uint4(0, 0, 0, 0));
+    }
+}
+
 // Copy the unit at column `col` of a row to the thread's slot.
 template <int W, bool BF>
 __device__ __forceinline__ void fetch(uint32_t slot, const void *row, int col)
@@ -262,13 +274,11 @@ __device__ __forceinline__ float cta_sum(f2 pair, float (&bufs)[2][32], int &tur
     if ((threadIdx.x & 31) == 0)
         red[threadIdx.x >> 5] = v;
     __syncthreads();
-    f2 s0 = both(0.0f), s1 = s0;
-    const int vecs = (blockDim.x + 127) / 128;
-#pragma unroll 4
-    for (int i = 0; i < vecs; ++i) {
-        const ulonglong2 w = reinterpret_cast<const ulonglong2 *>(red)[i];
-        s0 = add2(s0, w.x);
-        s1 = add2(s1, w.y);
+    const ulonglong2 *w = reinterpret_cast<const ulonglong2 *>(red);   // the sums of four warps
+    f2 s0 = add2(add2(w[0].x, w[1].x), add2(w[2].x, w[3].x)), s1 = add2(add2(w[0].y, w[1].y), add2(w[2].y, w[3].y));
+    if (blockDim.x > 512) {
+        s0 = add2(s0, add2(add2(w[4].x, w[5].x), add2(w[6].x, w[7].x)));
+        s1 = add2(s1, add2(add2(w[4].y, w[5].y), add2(w[6].y, w[7].y)));
     }
     s0 = add2(s0, s1);
     return lo2(s0) + hi2(s0);
@@ -316,7 +326,7 @@ __device__ __forceinline__ void encode_units(const Vec<W> (&v)[U], uint8_t *q, f
     for (; o > 0; o /= 2)
         amax[0] = fmaxf(amax[0], __shfl_xor_sync(0xFFFFFFFFu, amax[0], o));
     const float sc = __fdiv_rn(amax[0], 448.0f);
-    const Enc e(sc);
+    const float y = Enc::reciprocal(sc);
     // the first lane of a group with this unit writes its scale
     const int first = c0 - (lane & (L - 1)) * W + mine * 32 * W;
     if ((lane & (L / U - 1)) == 0 && first < N)
@@ -324,8 +334,7 @@ __device__ __forceinline__ void encode_units(const Vec<W> (&v)[U], uint8_t *q, f
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         const int col = c0 + k * 32 * W, src = (lane & ~(L - 1)) + k * (L / U);
-        const Enc enc(__shfl_sync(0xFFFFFFFFu, e.s, src), __shfl_sync(0xFFFFFFFFu, e.yl, src),
-                      __shfl_sync(0xFFFFFFFFu, e.yh, src), __shfl_sync(0xFFFFFFFFu, (int)e.fast, src) != 0);
+        const Enc enc(__shfl_sync(0xFFFFFFFFu, sc, src), __shfl_sync(0xFFFFFFFFu, y, src));
         if (col < N) {
             float x[W];
 #pragma unroll
@@ -383,6 +392,24 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int sta
         }
     };
 
+    // Units past the row's end read as zero and add nothing; their weights are column 0's.
+    // Only their copies and stores are left out, so the row's passes have no branches.
+    bool ok[U];
+    int wcol[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        ok[k] = col_of(k) < N;
+        wcol[k] = ok[k] ? col_of(k) : 0;
+        if (!ok[k]) {
+            for (int s = 0; s < stages; ++s) {
+                const uint32_t st = base + s * stage_bytes;
+                zero_slot<kY>(y_slot(st, k));
+                zero_slot<kH>(h_slot(st, k));
+                if (token)
+                    zero_slot<kG>(g_slot(st, k));
+            }
+        }
+    }
     int64_t ahead = blockIdx.x;   // next row to fetch
     for (int s = 0; s < stages; ++s, ahead += gridDim.x) {
         if (ahead < a.M)
@@ -403,7 +430,7 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int sta
         float r1 = 1.0f, r2 = 1.0f;
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            v[k] = col_of(k) < N ? from_slot<W, YB>(y_slot(st, k)) : all_of<W>(0.0f);
+            v[k] = from_slot<W, YB>(y_slot(st, k));
         if (a.w1) {
             f2 ss = both(0.0f);
 #pragma unroll
@@ -418,31 +445,27 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int sta
         if (a.w1) {
 #pragma unroll
             for (int k = 0; k < U; ++k)
-                if (col_of(k) < N)
-                    v[k] = v[k] * ldg_f32<W>(a.w1 + col_of(k));
+                v[k] = v[k] * ldg_f32<W>(a.w1 + wcol[k]);
         }
         if (token) {
 #pragma unroll
             for (int k = 0; k < U; ++k)
-                if (col_of(k) < N)
-                    v[k] = v[k] * from_slot<W, true>(g_slot(st, k));
+                v[k] = v[k] * from_slot<W, true>(g_slot(st, k));
         } else if (a.gate) {
 #pragma unroll
             for (int k = 0; k < U; ++k)
-                if (col_of(k) < N)
-                    v[k] = v[k] * ldg_bf16<W>(a.gate + col_of(k));
+                v[k] = v[k] * ldg_bf16<W>(a.gate + wcol[k]);
         }
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            if (col_of(k) < N)
-                v[k] = fma_of(from_slot<W, HB>(h_slot(st, k)), alpha, v[k]);
+            v[k] = fma_of(from_slot<W, HB>(h_slot(st, k)), alpha, v[k]);
         // this thread has read all of its slots: the row `stages` ahead takes them
         if (ahead < a.M)
             fetch_row(ahead, st);
         cp_async_commit();
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            if (col_of(k) < N)
+            if (ok[k])
                 store_vec<W, HB>(a.t, m * N + col_of(k), v[k]);
         if (a.w2) {
             f2 ss = both(0.0f);
@@ -457,12 +480,11 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int sta
             continue;
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            if (col_of(k) < N)
-                v[k] = v[k] * both(r2) * ldg_f32<W>(a.w2 + col_of(k));
+            v[k] = v[k] * both(r2) * ldg_f32<W>(a.w2 + wcol[k]);
         if (a.u) {
 #pragma unroll
             for (int k = 0; k < U; ++k)
-                if (col_of(k) < N)
+                if (ok[k])
                     store_vec<W, true>(a.u, m * N + col_of(k), v[k]);
         }
         if (a.q)
