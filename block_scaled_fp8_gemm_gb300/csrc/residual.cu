@@ -527,6 +527,26 @@ __global__ void __launch_bounds__(512, 1)
     // of a row kept at `off` in the order of its columns, unit k's `bytes`
     auto at = [&](uint32_t off, int bytes, int k) { return off + c0 * (bytes / W) + k * 32 * bytes; };
 
+    // fp32 weights in planes of 16 bytes a unit: a lane's 32 bytes side by side would put
+    // two lanes on every bank
+    auto plane = [&](uint32_t off, int k, int p) { return off + p * (U * 16 * T) + (c0 / W + k * 32) * 16; };
+    auto put_weights = [&](uint32_t off, int k, const Raw<W, false> &r) {
+#pragma unroll
+        for (int p = 0; p < W / 4; ++p)
+            st_shared_v4(base + plane(off, k, p), make_uint4(r.w[4 * p], r.w[4 * p + 1], r.w[4 * p + 2], r.w[4 * p + 3]));
+    };
+    auto get_weights = [&](uint32_t off, int k) {
+        Raw<W, false> r;
+#pragma unroll
+        for (int p = 0; p < W / 4; ++p) {
+            const uint4 x = ld_shared_v4(base + plane(off, k, p));
+            r.w[4 * p] = x.x;
+            r.w[4 * p + 1] = x.y;
+            r.w[4 * p + 2] = x.z;
+            r.w[4 * p + 3] = x.w;
+        }
+        return r.vec();
+    };
     auto fetch_row = [&](int64_t m, uint32_t st) {
         const char *y = static_cast<const char *>(a.y) + m * a.ys * (YB ? 2 : 4);
         const char *h = static_cast<const char *>(a.h) + m * a.hs * (HB ? 2 : 4);
@@ -588,9 +608,9 @@ __global__ void __launch_bounds__(512, 1)
                 weights(col_of(k), cw, w2);
                 Raw<W, false> r;
                 r.set(cw);
-                r.store(smem_raw + at(off_cw, kF, k));
+                put_weights(off_cw, k, r);
                 r.set(w2);
-                r.store(smem_raw + at(off_w2, kF, k));
+                put_weights(off_w2, k, r);
             }
         }
     }
@@ -649,8 +669,8 @@ __global__ void __launch_bounds__(512, 1)
         };
         auto row_weights = [&](int k, Vec<W> &cw, Vec<W> &w2) {
             if constexpr (HOLD) {
-                cw = from_slot<W, false>(base + at(off_cw, kF, k));
-                w2 = from_slot<W, false>(base + at(off_w2, kF, k));
+                cw = get_weights(off_cw, k);
+                w2 = get_weights(off_w2, k);
             } else {
                 weights(col_of(k), cw, w2);
             }
