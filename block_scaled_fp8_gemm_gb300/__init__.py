@@ -29,6 +29,8 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
+from . import _operators  # noqa: E402  (built with the library; needs torch loaded)
+
 # ---- constants (mirror include/gemmar.h) -------------------------------------
 GEMMAR_OK = 0
 GEMMAR_ERR_ARG = 1
@@ -105,6 +107,9 @@ for _name, (_res, _args) in _SIGS.items():
     _fn.argtypes = _args
 
 EXPORTED = tuple(_SIGS)
+
+_operators.bind(*(ctypes.cast(getattr(_lib, n), _P).value for n in
+                  ("norm_gate_residual", "norm_gate_residual_bwd", "lora_apply", "lora_apply_bwd")))
 
 
 class GemmarError(RuntimeError):
@@ -364,8 +369,9 @@ def fused_gemm_reduce_noalloc_status():
 
 # ---- the residual stream after wo_b, and adapters beside it --------------------------
 
-# A decode step is a few microseconds of device time, so the checks of these entry
-# points read a tensor's type, shape and layout once and explain a refusal apart.
+# A decode step is a few microseconds of device time, so csrc/binding.cpp reads the tensors
+# of these entry points and calls the library.  Where it finds one that does not fit, it
+# answers -1 and the checks here say which and why.
 
 def _refuse(t, shape, name: str, dtype, rows: bool):
     if not isinstance(t, torch.Tensor):
@@ -421,23 +427,83 @@ def _codes(q, shape, name: str):
     return _dense(q, shape, name, torch.uint8 if q.dtype is torch.uint8 else torch.float8_e4m3fn)
 
 
+def _explain_norm_gate_residual(y, h, w_pre, t, w_post, gate, u, q, scales, rstd):
+    shape = M, N = y.shape
+    f32, bf16 = torch.float32, torch.bfloat16
+    _xdtype(y), _xdtype(h)
+    _rows(y, shape, "y")
+    _rows(h, shape, "h")
+    _gate(gate, M, N)
+    for x, s, name, dtype in ((w_post, (N,), "w_post", f32), (w_pre, (N,), "w_pre", f32), (t, shape, "t", h.dtype),
+                              (u, shape, "u", bf16), (scales, (M, N // 128), "scales", f32), (rstd, (M, 2), "rstd", f32)):
+        _dense(x, s, name, dtype)
+    _codes(q, shape, "q")
+
+
+def _explain_norm_gate_residual_bwd(y, h, rstd, dt, dy, dh, w_post, w_pre, gate, du, dw_post, dw_pre, dgate):
+    shape = M, N = y.shape
+    f32, bf16 = torch.float32, torch.bfloat16
+    _xdtype(y), _xdtype(h)
+    _rows(y, shape, "y")
+    _rows(h, shape, "h")
+    row = _gate(gate, M, N)[1] == 0
+    if dt is not None:
+        _rows(dt, shape, "dt", h.dtype)
+    if du is not None:
+        _rows(du, shape, "du", bf16)
+    for x, s, name, dtype in ((rstd, (M, 2), "rstd", f32), (dy, shape, "dy", y.dtype), (dh, shape, "dh", h.dtype),
+                              (w_post, (N,), "w_post", f32), (w_pre, (N,), "w_pre", f32), (dw_post, (N,), "dw_post", f32),
+                              (dw_pre, (N,), "dw_pre", f32), (dgate, (N,) if row else shape, "dgate", f32 if row else bf16)):
+        _dense(x, s, name, dtype)
+
+
+def _explain_lora_operands(x, order, offsets, A, B, scales, ranks):
+    for name, t, dim in (("x", x, 2), ("A", A, 3), ("B", B, 3)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != dim:
+            raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
+    T, K = x.shape
+    R, r, _ = A.shape
+    N = B.shape[2]
+    i32, bf16 = torch.int32, torch.bfloat16
+    _rows(x, (T, K), "x", bf16)
+    for t, s, name, dtype in ((order, (T,), "order", i32), (offsets, (R + 1,), "offsets", i32), (A, (R, r, K), "A", bf16),
+                              (B, (R, r, N), "B", bf16), (scales, (R,), "scales", torch.float32), (ranks, (R,), "ranks", i32)):
+        _dense(t, s, name, dtype)
+    return T, K, N, R, r
+
+
+def _explain_lora_apply(x, order, offsets, A, B, scales, ranks, out, y, v):
+    T, K, N, R, r = _explain_lora_operands(x, order, offsets, A, B, scales, ranks)
+    _rows(out, (T, N), "out", torch.bfloat16)
+    if y is not None:
+        _rows(y, (T, N), "y", torch.bfloat16)
+    _dense(v, (T, r), "v", torch.float32)
+
+
+def _explain_lora_apply_bwd(x, order, offsets, A, B, scales, ranks, dy, v, dx, dA, dB, dx0):
+    T, K, N, R, r = _explain_lora_operands(x, order, offsets, A, B, scales, ranks)
+    bf16 = torch.bfloat16
+    _rows(dy, (T, N), "dy", bf16)
+    _rows(dx, (T, K), "dx", bf16)
+    if dx0 is not None:
+        _rows(dx0, (T, K), "dx0", bf16)
+    for t, s, name, dtype in ((v, (T, r), "v", torch.float32), (dA, (R, r, K), "dA", bf16), (dB, (R, r, N), "dB", bf16)):
+        _dense(t, s, name, dtype)
+
+
 def norm_gate_residual(ctx: Context, y, h, w_pre, t, w_post=None, gate=None, alpha: float = 1.0, beta: float = 1.0,
                        eps: float = 1e-6, u=None, q=None, scales=None, rstd=None, stream=None) -> None:
     """t = alpha*h + beta*gate*norm(y)*w_post and the next block's input norm(t)*w_pre, as bf16 rows u
     and/or e4m3 codes q with fp32 scales per 1x128 (gemm_blockscale_fp8's A operand).  w_post None: no
     post norm; w_pre None: t only; gate bf16 [N] or [M, N]; rstd fp32 [M, 2] for the backward pass."""
-    shape = M, N = y.shape
-    width, f32, bf16 = (N,), torch.float32, torch.bfloat16
-    yp, ys = _rows(y, shape, "y")
-    hp, hs = _rows(h, shape, "h")
-    gp, gs = _gate(gate, M, N)
-    _check(_lib.norm_gate_residual(ctx.handle, yp, _xdtype(y), ys, hp, _xdtype(h), hs,
-                                   _dense(w_post, width, "w_post", f32), _dense(w_pre, width, "w_pre", f32), gp, gs,
-                                   alpha, beta, eps, M, N, _dense(t, shape, "t", h.dtype),
-                                   _dense(u, shape, "u", bf16), _codes(q, shape, "q"),
-                                   _dense(scales, (M, N // 128), "scales", f32), _dense(rstd, (M, 2), "rstd", f32),
-                                   _stream(stream)),
-           "norm_gate_residual")
+    rc = _operators.norm_gate_residual(ctx.handle.value, y, h, w_pre, t, w_post, gate, alpha, beta, eps, u, q,
+                                       scales, rstd, _stream(stream))
+    if rc < 0:
+        _explain_norm_gate_residual(y, h, w_pre, t, w_post, gate, u, q, scales, rstd)
+    if rc:
+        _check(rc, "norm_gate_residual")
 
 
 def norm_gate_residual_bwd(ctx: Context, y, h, rstd, dt, dy, dh, w_post=None, w_pre=None, gate=None,
@@ -445,21 +511,12 @@ def norm_gate_residual_bwd(ctx: Context, y, h, rstd, dt, dy, dh, w_post=None, w_
                            stream=None) -> None:
     """Gradients of norm_gate_residual from dt (of t; None: zero) and du (of the normed rows), given its
     inputs and rstd.  dw_post, dw_pre fp32 [N]; dgate fp32 [N] for a gate row, bf16 [M, N] per token."""
-    M, N = y.shape
-    yp, ys = _rows(y, (M, N), "y")
-    hp, hs = _rows(h, (M, N), "h")
-    gp, gs = _gate(gate, M, N)
-    tp, ts = (None, 0) if dt is None else _rows(dt, (M, N), "dt", h.dtype)
-    up, us = (None, 0) if du is None else _rows(du, (M, N), "du", torch.bfloat16)
-    f32 = torch.float32
-    dg = _dense(dgate, (N,), "dgate", f32) if gs == 0 else _dense(dgate, (M, N), "dgate", torch.bfloat16)
-    _check(_lib.norm_gate_residual_bwd(ctx.handle, yp, _xdtype(y), ys, hp, _xdtype(h), hs,
-                                       _dense(rstd, (M, 2), "rstd", f32), _dense(w_post, (N,), "w_post", f32),
-                                       _dense(w_pre, (N,), "w_pre", f32), gp, gs, alpha, beta, M, N, tp, ts, up, us,
-                                       _dense(dy, (M, N), "dy", y.dtype), _dense(dh, (M, N), "dh", h.dtype),
-                                       _dense(dw_post, (N,), "dw_post", f32), _dense(dw_pre, (N,), "dw_pre", f32), dg,
-                                       _stream(stream)),
-           "norm_gate_residual_bwd")
+    rc = _operators.norm_gate_residual_bwd(ctx.handle.value, y, h, rstd, dt, dy, dh, w_post, w_pre, gate, alpha, beta, du,
+                                           dw_post, dw_pre, dgate, _stream(stream))
+    if rc < 0:
+        _explain_norm_gate_residual_bwd(y, h, rstd, dt, dy, dh, w_post, w_pre, gate, du, dw_post, dw_pre, dgate)
+    if rc:
+        _check(rc, "norm_gate_residual_bwd")
 
 
 def lora_plan(ctx: Context, adapter_ids, order, offsets, stream=None) -> None:
@@ -473,40 +530,23 @@ def lora_plan(ctx: Context, adapter_ids, order, offsets, stream=None) -> None:
            "lora_plan")
 
 
-def _lora_operands(x, order, offsets, A, B, scales, ranks):
-    T, K = x.shape
-    R, r, _ = A.shape
-    N = B.shape[2]
-    i32, bf16 = torch.int32, torch.bfloat16
-    return (T, K, N, R, r), (_dense(order, (T,), "order", i32), _dense(offsets, (R + 1,), "offsets", i32),
-                             _dense(A, (R, r, K), "A", bf16), _dense(B, (R, r, N), "B", bf16),
-                             _dense(scales, (R,), "scales", torch.float32), _dense(ranks, (R,), "ranks", i32))
-
-
 def lora_apply(ctx: Context, x, order, offsets, A, B, scales, ranks, out, y=None, v=None, stream=None) -> None:
     """out = y + the tokens' adapters applied to x: scales[a] * (x[t] A[a]^T) B[a], A [R, r, K] and B [R, r, N]
     bf16, ranks int32 [R] or None.  y None: zero; y may be out.  v fp32 [T, r]: kept for the backward pass."""
-    (T, K, N, R, r), ptrs = _lora_operands(x, order, offsets, A, B, scales, ranks)
-    bf16 = torch.bfloat16
-    xp, xs = _rows(x, (T, K), "x", bf16)
-    yp, ys = (None, 0) if y is None else _rows(y, (T, N), "y", bf16)
-    op, os_ = _rows(out, (T, N), "out", bf16)
-    _check(_lib.lora_apply(ctx.handle, xp, xs, *ptrs, T, K, N, R, r, yp, ys, op, os_,
-                           _dense(v, (T, r), "v", torch.float32), _stream(stream)),
-           "lora_apply")
+    rc = _operators.lora_apply(ctx.handle.value, x, order, offsets, A, B, scales, ranks, out, y, v, _stream(stream))
+    if rc < 0:
+        _explain_lora_apply(x, order, offsets, A, B, scales, ranks, out, y, v)
+    if rc:
+        _check(rc, "lora_apply")
 
 
 def lora_apply_bwd(ctx: Context, x, dy, order, offsets, A, B, scales, ranks, v, dx, dA, dB, dx0=None,
                    stream=None) -> None:
     """Gradients of lora_apply: dx = dx0 + the adapters' part (dx0 None: zero; may be dx), dA and dB of A's
     and B's shapes, from dy, the forward pass's x and its v."""
-    (T, K, N, R, r), ptrs = _lora_operands(x, order, offsets, A, B, scales, ranks)
-    bf16 = torch.bfloat16
-    xp, xs = _rows(x, (T, K), "x", bf16)
-    yp, ys = _rows(dy, (T, N), "dy", bf16)
-    bp, bs = (None, 0) if dx0 is None else _rows(dx0, (T, K), "dx0", bf16)
-    dp, ds = _rows(dx, (T, K), "dx", bf16)
-    _check(_lib.lora_apply_bwd(ctx.handle, xp, xs, yp, ys, *ptrs, _dense(v, (T, r), "v", torch.float32),
-                               T, K, N, R, r, bp, bs, dp, ds, _dense(dA, (R, r, K), "dA", bf16),
-                               _dense(dB, (R, r, N), "dB", bf16), _stream(stream)),
-           "lora_apply_bwd")
+    rc = _operators.lora_apply_bwd(ctx.handle.value, x, order, offsets, A, B, scales, ranks, dy, v, dx, dA, dB, dx0,
+                                   _stream(stream))
+    if rc < 0:
+        _explain_lora_apply_bwd(x, order, offsets, A, B, scales, ranks, dy, v, dx, dA, dB, dx0)
+    if rc:
+        _check(rc, "lora_apply_bwd")

@@ -1,4 +1,4 @@
-"""Compile libgemmar.so in-tree for sm_103a (nvcc, one -gencode, parallel TUs)."""
+"""Compile libgemmar.so (nvcc, sm_103a, one -gencode, parallel TUs) and the binding's _operators.so (g++) in-tree."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -6,12 +6,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libgemmar.so")
+BINDING_PATH = os.path.join(PKG, "_operators.so")
 SOURCES = ["gemm_blockscale.cu", "gemm_blockscale_2sm.cu", "gemm_mx.cu", "streaming.cu", "gemmar.cu", "noalloc.cu",
            "residual.cu", "lora.cu", "lora_tile.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -29,6 +31,25 @@ def _flags():
                    "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 
 
+def build_binding() -> str:
+    """The tensor marshalling of the decode-step entry points, against the installed torch's headers."""
+    import torch
+    home = os.path.dirname(torch.__file__)
+    lib = os.path.join(home, "lib")
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", lib, "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the binding did not compile:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -42,8 +63,10 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, (r.stdout + r.stderr)
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(build_binding)
         results = list(ex.map(compile_one, SOURCES))
+        binding.result()
     if verbose or ptxas_info:
         for _, log in results:
             if log.strip():
