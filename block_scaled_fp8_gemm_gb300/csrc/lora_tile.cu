@@ -50,6 +50,10 @@ __host__ __device__ constexpr int tmem_cols(int n) { return n <= 32 ? 32 : n <= 
 // v[i][j] = f sum_c x[t,c] W[a,j,c]: D[128 tokens, ranks], both operands K-major, 64
 // columns a stage.  The CTAs of a cluster share the columns of a tile (blockIdx.y) and
 // add their sums in rank order through distributed shared memory.
+// Bound by the reads of x: 88 us for the 483 MB of 14746 tokens, K = 16384, r = 64, 5.5 TB/s;
+// of that 19 us do not depend on K (launch, first stages, the cluster's sum), the rest
+// runs at 6.8 TB/s.  A TMA gather of four rows a copy takes 155 us (128 bytes of a row at
+// a time leave it at 20 bytes a ns and SM), TMA boxes of neighbouring rows 86.
 constexpr int kDownThreads = 256;
 
 template <int RP>   // ranks rounded up to 16, 32, 64 or 128
@@ -192,6 +196,10 @@ __global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs 
 // pieces out of it.  A step is a chain (barrier, MMA, TMEM read, transposition,
 // stores) that its own CTA does not overlap; three or four CTAs an SM do, so the
 // accumulator is single and the ring short.
+// 88 us for the 470 MB of 16384 tokens, N = 7168, r = 64, 5.3 TB/s.  A version of 97 us took 82
+// without MMAs and sums, 85 without stores and 60 without either: reads, the chain of a
+// step and writes share the time.  mma.sync fragments instead of tcgen05 took 149 where this
+// took 95, eight warps a CTA 102 against 96.
 // With `beside` the kernel before this one does not produce v2 but has waited for the
 // one that does before it let this one start (tile_grad_kernel): the two then run side
 // by side, and this one waits for the other at its end, so that what follows in the
@@ -381,10 +389,14 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
 // ---------------------------------------------------------------- grad
 
 // G[a,j,c] = f sum_i p[i,j] x[t,c] over an adapter's tokens: D[128 columns, ranks] with
-// the tokens as the contracted index, both operands in rows that run along M and N, 64
+// the tokens as the contracted index, both operands in rows that run along M and N, 32
 // tokens a stage.  p comes as two bf16 parts side by side (p2), so an MMA of twice
 // the ranks gives both products, and the halves are added at the end.  Both gradients
 // of a call are one launch: blockIdx.y counts first dA's and then dB's column tiles.
+// 90 us for the 385 MB of 8191 tokens of 9 adapters, K = 16384, N = 7168, r = 64, 4.3 TB/s:
+// with neither loads nor MMAs the steps' chain (rows' numbers, barrier, issue, commit)
+// takes 52 of them.  A ring with mbarriers and copying warps of their own took 136 where
+// this took 116, a TMA gather of four rows a copy 165 against 90.
 constexpr int kGradThreads = 256;
 constexpr int kGradTokens = 32;   // a stage
 constexpr int kGradCols = 256;    // two accumulators

@@ -638,12 +638,6 @@ __device__ __forceinline__ void cp_async_cg16_or_zero(uint32_t dst, const void *
 // visible to the async proxy, which the MMA reads through.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// 4 and 8 bytes (through L1: these forms have no other).
-__device__ __forceinline__ void cp_async_ca4(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-
 __device__ __forceinline__ void cp_async_ca8(uint32_t dst, const void *src)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");

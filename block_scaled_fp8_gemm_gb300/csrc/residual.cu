@@ -4,8 +4,8 @@
 //
 // Both are HBM-bound: about 14 and 36 flops per element against 6 to 16 bytes, each
 // input read and each output written once.  A persistent CTA takes a row at a
-// time, a thread keeping the same 8-column chunks (16 bytes of bf16) of every
-// row, so that what a row needs from another thread is only its sums.  Rows
+// time, a thread keeping the same units of 8 or 4 columns of every row, so that
+// what a row needs from another thread is only its sums.  Rows
 // ahead are copied to shared memory with cp.async into slots that only the
 // copying thread reads: no barrier guards them, and a thread waits for nothing
 // but its own copies.
@@ -358,6 +358,9 @@ __device__ __forceinline__ void encode_units(const Vec<W> (&v)[U], uint8_t *q, f
 // the instructions: 71 us instead of 66 at 4096 x 7168, fp32 stream, codes).
 // Two rows an SM in flight (two CTAs) hide each other's two sums.  Weights come
 // through L1, which the rings leave room for (kNormRing).
+// 16384 x 7168 with a gate per token, bf16: 180 us, 6.5 TB/s, the rate of a copy but
+// for 4%.  4096 x 7168 with an fp32 stream and codes: 64 us, 5.0 TB/s: the start (the rings'
+// first fill) and the encoder's latency, which two rows an SM do not hide, are the rest.
 template <int U, bool YB, bool HB>
 __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int stages)
 {
@@ -507,6 +510,13 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int sta
 // sums are exchanged; the weights sit in shared memory.  Wider rows take 32 columns
 // a thread, read the slots twice and the weights through L1.
 // BOTH: both norms are there (known when compiling, a pass of the row is one loop).
+// 4096 x 7168 bf16: 78 us, 4.5 TB/s; 16384 rows 265, 5.3.  Not bound by HBM (56% busy) nor
+// by one pipe (issue slots 44%): 14 warps of 122 registers, whose two sums over the rows
+// leave no room for a second CTA, do not hide the latencies of shared memory and of the
+// arithmetic.  Running a row's first pass before the second of the row before it, so
+// that the exchange of sums is off the path, is no faster (78 and 268 us), nor is twice
+// the threads with 8 columns each (95).  Rows wider than 8192 have one CTA's ring for a
+// single row: 4096 x 16384 211 us, 3.8 TB/s.
 template <int U, bool YB, bool HB, bool TOKEN, bool HOLD, bool BOTH>
 __global__ void __launch_bounds__(512, 1)
     norm_bwd_kernel(const NormBwdArgs a, float *__restrict__ ws, int stages, int gate_staged)
@@ -808,8 +818,9 @@ __global__ void __launch_bounds__(512, 1)
 // columns (a 32-byte sector of a part), its groups of eight lanes take the parts in
 // turn, and a warp a column then adds the groups' sums.  Wide rows have few parts and
 // many columns, narrow ones the opposite: 32 groups or 128 (the whole backward pass of
-// 4096 x 7168 80 us against 84, of 16384 x 1024 54 against 42).  s1 = sum n d (times a token's gate): dw1 = beta g s1 and
-// dgate = beta w1 s1 for a gate row g.
+// 4096 x 7168 80 us with 32 groups, 84 with 128; of 16384 x 1024 54 and 42).
+// s1 = sum n d (times a token's gate): dw1 = beta g s1 and dgate = beta w1 s1 for a gate
+// row g.
 constexpr int kSumGroups = 128;   // at most
 
 __global__ void __launch_bounds__(kSumGroups * 8) norm_bwd_sum_kernel(const NormBwdArgs a, const float *__restrict__ ws,
