@@ -11,6 +11,8 @@
 // but its own copies.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "e4m3_encode.cuh"
 #include "kernels.h"
 #include "launch.cuh"
@@ -246,19 +248,14 @@ __device__ __forceinline__ void fetch(uint32_t slot, const void *row, int col)
         cp_async_cg16(slot, src);
 }
 
-// All but the newest stages - 1 groups of this thread's copies have landed.
+// This thread's oldest row of one or two under way has landed.
 __device__ __forceinline__ void wait_stage(int stages)
 {
     if (stages == 1)
         cp_async_wait<0>();
-    else if (stages == 2)
-        cp_async_wait<1>();
-    else if (stages == 3)
-        cp_async_wait<2>();
     else
-        cp_async_wait<3>();
+        cp_async_wait<1>();
 }
-constexpr int kMaxStages = 4;
 
 // Sum over the CTA, the same bits in every thread.  One barrier: two buffers take
 // turns, so a warp that is a sum ahead of another writes the one not being read.
@@ -291,6 +288,37 @@ template <int U, int W>
 __device__ __forceinline__ int first_col()
 {
     return ((int)(threadIdx.x & ~31u) * U + (int)(threadIdx.x & 31u)) * W;
+}
+
+// Unit k of an fp32 row kept in shared memory, in planes of 16 bytes a unit: a lane's 32
+// bytes side by side would put two lanes on every bank.
+template <int U, int W>
+__device__ __forceinline__ uint32_t plane_of(uint32_t at, int k, int p)
+{
+    return at + p * (U * 16 * blockDim.x) + (first_col<U, W>() / W + k * 32) * 16;
+}
+template <int U, int W>
+__device__ __forceinline__ void put_plane(uint32_t at, int k, const Vec<W> &v)
+{
+    Raw<W, false> r;
+    r.set(v);
+#pragma unroll
+    for (int p = 0; p < W / 4; ++p)
+        st_shared_v4(plane_of<U, W>(at, k, p), make_uint4(r.w[4 * p], r.w[4 * p + 1], r.w[4 * p + 2], r.w[4 * p + 3]));
+}
+template <int U, int W>
+__device__ __forceinline__ Vec<W> get_plane(uint32_t at, int k)
+{
+    Raw<W, false> r;
+#pragma unroll
+    for (int p = 0; p < W / 4; ++p) {
+        const uint4 x = ld_shared_v4(plane_of<U, W>(at, k, p));
+        r.w[4 * p] = x.x;
+        r.w[4 * p + 1] = x.y;
+        r.w[4 * p + 2] = x.z;
+        r.w[4 * p + 3] = x.w;
+    }
+    return r.vec();
 }
 
 // e4m3 codes of a row's units with one scale per 128 columns: a group is 128 / W
@@ -352,16 +380,21 @@ __device__ __forceinline__ void encode_units(const Vec<W> (&v)[U], uint8_t *q, f
     }
 }
 
+// STAGED (CTAs of several rows): the weights are kept in shared memory, w_post times a gate row
+// as one, since 72 KB of them do not stay in L1 beside the rows: 16384 x 7168 bf16 with codes
+// 147 us, 183 through L1.  With fp32 rows w_pre stays in L1, which then has room for it:
+// 4096 x 7168 57 us, 61 with both, 61 with none.
+__host__ __device__ constexpr bool stage_pre(int W) { return W == 8; }
+
 // A thread holds U units of W columns of its row.  A warp takes 32 U W neighbouring
 // columns and its units lie 32 W apart, so one address per matrix and fixed
 // offsets reach them all (with units T W apart address arithmetic was a third of
 // the instructions: 71 us instead of 66 at 4096 x 7168, fp32 stream, codes).
-// Two rows an SM in flight (two CTAs) hide each other's two sums.  Weights come
-// through L1, which the rings leave room for (kNormRing).
-// 16384 x 7168 with a gate per token, bf16: 180 us, 6.5 TB/s, the rate of a copy but
-// for 4%.  4096 x 7168 with an fp32 stream and codes: 64 us, 5.0 TB/s: the start (the rings'
-// first fill) and the encoder's latency, which two rows an SM do not hide, are the rest.
-template <int U, bool YB, bool HB>
+// Two rows an SM in flight (two CTAs) hide each other's two sums.
+// 16384 x 7168 with a gate per token, bf16: 174 us, 6.7 TB/s, the rate of a copy.  4096 x
+// 7168 with an fp32 stream and codes: 57 us, 5.7 TB/s (16384 rows 202 us, 6.4): the first
+// rows' copies and 14 turns for 13.5 rows a CTA are the rest.
+template <int U, bool YB, bool HB, bool STAGED>
 __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int stages)
 {
     constexpr int W = YB && HB ? 8 : 4;
@@ -373,6 +406,7 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int sta
     const uint32_t off_h = U * kY * T, off_g = off_h + U * kH * T;
     const uint32_t stage_bytes = off_g + (token ? U * kG * T : 0);
     const uint32_t base = smem_u32(smem_raw);
+    const uint32_t at_cw = base + stages * stage_bytes;   // STAGED
     const float inv_n = 1.0f / N;
     const int c0 = first_col<U, W>();
     auto col_of = [&](int k) { return c0 + k * 32 * W; };
@@ -419,6 +453,28 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int sta
             fetch_row(ahead, base + s * stage_bytes);
         cp_async_commit();
     }
+    // w_post times a gate that is one row, and w_pre
+    const bool scaled = a.w1 != nullptr || (a.gate != nullptr && !token);
+    const bool normed = a.u != nullptr || a.q != nullptr;
+    auto scale = [&](int k) {
+        Vec<W> cw = all_of<W>(1.0f);
+        if (a.w1)
+            cw = ldg_f32<W>(a.w1 + wcol[k]);
+        if (a.gate && !token)
+            cw = cw * ldg_bf16<W>(a.gate + wcol[k]);
+        return cw;
+    };
+    constexpr bool kStageW2 = STAGED && stage_pre(W);
+    const uint32_t at_w2 = at_cw + (scaled ? U * W * 4 * T : 0);
+    if constexpr (STAGED) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (scaled)
+                put_plane<U, W>(at_cw, k, scale(k));
+            if (kStageW2 && normed)
+                put_plane<U, W>(at_w2, k, ldg_f32<W>(a.w2 + wcol[k]));
+        }
+    }
     for (int i = t; i < 64; i += T)
         red[i >> 5][i & 31] = 0.0f;
     __syncthreads();
@@ -445,19 +501,19 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int sta
 #pragma unroll
         for (int k = 0; k < U; ++k)
             v[k] = v[k] * br1;
-        if (a.w1) {
+        if (scaled) {
 #pragma unroll
-            for (int k = 0; k < U; ++k)
-                v[k] = v[k] * ldg_f32<W>(a.w1 + wcol[k]);
+            for (int k = 0; k < U; ++k) {
+                if constexpr (STAGED)
+                    v[k] = v[k] * get_plane<U, W>(at_cw, k);
+                else
+                    v[k] = v[k] * scale(k);
+            }
         }
         if (token) {
 #pragma unroll
             for (int k = 0; k < U; ++k)
                 v[k] = v[k] * from_slot<W, true>(g_slot(st, k));
-        } else if (a.gate) {
-#pragma unroll
-            for (int k = 0; k < U; ++k)
-                v[k] = v[k] * ldg_bf16<W>(a.gate + wcol[k]);
         }
 #pragma unroll
         for (int k = 0; k < U; ++k)
@@ -479,11 +535,15 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int sta
         }
         if (a.rstd && t == 0)
             *reinterpret_cast<float2 *>(a.rstd + 2 * m) = make_float2(r1, r2);
-        if (a.u == nullptr && a.q == nullptr)
+        if (!normed)
             continue;
 #pragma unroll
-        for (int k = 0; k < U; ++k)
-            v[k] = v[k] * both(r2) * ldg_f32<W>(a.w2 + wcol[k]);
+        for (int k = 0; k < U; ++k) {
+            if constexpr (kStageW2)
+                v[k] = v[k] * both(r2) * get_plane<U, W>(at_w2, k);
+            else
+                v[k] = v[k] * both(r2) * ldg_f32<W>(a.w2 + wcol[k]);
+        }
         if (a.u) {
 #pragma unroll
             for (int k = 0; k < U; ++k)
@@ -510,7 +570,7 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int sta
 // sums are exchanged; the weights sit in shared memory.  Wider rows take 32 columns
 // a thread, read the slots twice and the weights through L1.
 // BOTH: both norms are there (known when compiling, a pass of the row is one loop).
-// 4096 x 7168 bf16: 78 us, 4.5 TB/s; 16384 rows 265, 5.3.  Not bound by HBM (56% busy) nor
+// 4096 x 7168 bf16: 76 us, 4.7 TB/s; 16384 rows 265, 5.3.  Not bound by HBM (56% busy) nor
 // by one pipe (issue slots 44%): 14 warps of 122 registers, whose two sums over the rows
 // leave no room for a second CTA, do not hide the latencies of shared memory and of the
 // arithmetic.  Running a row's first pass before the second of the row before it, so
@@ -537,26 +597,6 @@ __global__ void __launch_bounds__(512, 1)
     // of a row kept at `off` in the order of its columns, unit k's `bytes`
     auto at = [&](uint32_t off, int bytes, int k) { return off + c0 * (bytes / W) + k * 32 * bytes; };
 
-    // fp32 weights in planes of 16 bytes a unit: a lane's 32 bytes side by side would put
-    // two lanes on every bank
-    auto plane = [&](uint32_t off, int k, int p) { return off + p * (U * 16 * T) + (c0 / W + k * 32) * 16; };
-    auto put_weights = [&](uint32_t off, int k, const Raw<W, false> &r) {
-#pragma unroll
-        for (int p = 0; p < W / 4; ++p)
-            st_shared_v4(base + plane(off, k, p), make_uint4(r.w[4 * p], r.w[4 * p + 1], r.w[4 * p + 2], r.w[4 * p + 3]));
-    };
-    auto get_weights = [&](uint32_t off, int k) {
-        Raw<W, false> r;
-#pragma unroll
-        for (int p = 0; p < W / 4; ++p) {
-            const uint4 x = ld_shared_v4(base + plane(off, k, p));
-            r.w[4 * p] = x.x;
-            r.w[4 * p + 1] = x.y;
-            r.w[4 * p + 2] = x.z;
-            r.w[4 * p + 3] = x.w;
-        }
-        return r.vec();
-    };
     auto fetch_row = [&](int64_t m, uint32_t st) {
         const char *y = static_cast<const char *>(a.y) + m * a.ys * (YB ? 2 : 4);
         const char *h = static_cast<const char *>(a.h) + m * a.hs * (HB ? 2 : 4);
@@ -616,11 +656,8 @@ __global__ void __launch_bounds__(512, 1)
             if (col_of(k) < N) {
                 Vec<W> cw, w2;
                 weights(col_of(k), cw, w2);
-                Raw<W, false> r;
-                r.set(cw);
-                put_weights(off_cw, k, r);
-                r.set(w2);
-                put_weights(off_w2, k, r);
+                put_plane<U, W>(base + off_cw, k, cw);
+                put_plane<U, W>(base + off_w2, k, w2);
             }
         }
     }
@@ -679,8 +716,8 @@ __global__ void __launch_bounds__(512, 1)
         };
         auto row_weights = [&](int k, Vec<W> &cw, Vec<W> &w2) {
             if constexpr (HOLD) {
-                cw = get_weights(off_cw, k);
-                w2 = get_weights(off_w2, k);
+                cw = get_plane<U, W>(base + off_cw, k);
+                w2 = get_plane<U, W>(base + off_w2, k);
             } else {
                 weights(col_of(k), cw, w2);
             }
@@ -869,7 +906,8 @@ __global__ void __launch_bounds__(kSumGroups * 8) norm_bwd_sum_kernel(const Norm
 int round32(int v) { return (v + 31) / 32 * 32; }
 
 constexpr int kWide = 8192;            // widest row of 16 columns a thread in 512 threads
-constexpr int kNormRing = 176 * 1024;  // of an SM: the rest of its shared memory is L1 for the weights
+constexpr int kSmSmem = 228 * 1024, kCtaSmem = 2048;   // an SM's, and a CTA's besides the dynamic part
+constexpr int kStageRows = 3;   // of a CTA, from which staged weights pay (3 of 7168 bf16 columns: 13.9 us, 15.9 without)
 
 struct Plan {
     int threads, per_sm;   // CTAs an SM
@@ -883,13 +921,8 @@ Plan plan_rows(int N, int cols, int most)
     return {threads, per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm};
 }
 
-// Stages of a CTA's ring: what its share of `room` holds.
-int ring_stages(int64_t room, int stage_bytes, int64_t rows)
-{
-    int64_t s = room / stage_bytes;
-    s = s < 1 ? 1 : s > kMaxStages ? kMaxStages : s;
-    return (int)(rows < s ? rows : s);
-}
+// Rows of a CTA under way: two if they fit, one if it has no second.
+int ring_stages(int64_t room, int stage_bytes, int64_t rows) { return rows >= 2 && room >= 2 * stage_bytes ? 2 : 1; }
 
 Plan plan_bwd(int N) { return plan_rows(N, N <= kWide ? 16 : 32, 512); }
 
@@ -909,12 +942,20 @@ cudaError_t run_norm(const NormArgs &a, int num_sms, cudaStream_t st)
     const int stage_bytes = p.threads * COLS * ((YB ? 2 : 4) + (HB ? 2 : 4) + (a.gate && a.gs ? 2 : 0));
     const int64_t most = (int64_t)num_sms * p.per_sm;
     const int grid = (int)(a.M < most ? a.M : most);
-    const int stages = ring_stages(kNormRing / p.per_sm, stage_bytes, (a.M + grid - 1) / grid);
-    const auto kernel = norm_kernel<COLS / W, YB, HB>;
+    const int64_t rows = (a.M + grid - 1) / grid;
+    const int kept = (a.w1 || (a.gate && a.gs == 0) ? 1 : 0) + (stage_pre(W) && (a.u || a.q) ? 1 : 0);
+    const int weight_bytes = kept * p.threads * COLS * 4;
+    const int64_t room = kSmSmem / p.per_sm - kCtaSmem - weight_bytes;
+    const bool staged = rows >= kStageRows && room >= stage_bytes;
+    // One row: a second takes its shared memory from L1 (16384 x 7168 bf16 147 us, 168 with
+    // two), but narrow rows with a gate each have too few bytes under way (3584 columns
+    // 108 us, 94 with two).
+    const int stages = COLS == 8 && a.gate && a.gs ? ring_stages(room, stage_bytes, rows) : 1;
+    const auto kernel = staged ? norm_kernel<COLS / W, YB, HB, true> : norm_kernel<COLS / W, YB, HB, false>;
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), kMaxSmem);
     if (e != cudaSuccess)
         return e;
-    kernel<<<grid, p.threads, stages * stage_bytes, st>>>(a, stages);
+    kernel<<<grid, p.threads, stages * stage_bytes + (staged ? weight_bytes : 0), st>>>(a, stages);
     return cudaGetLastError();
 }
 
@@ -939,6 +980,7 @@ cudaError_t run_norm_bwd(const NormBwdArgs &a, float *ws, int grid, cudaStream_t
     const int staged = TOKEN && bytes + cols * 2 + weight_bytes <= kMaxSmem ? 1 : 0;
     const int stage_bytes = bytes + (staged ? cols * 2 : 0);
     const int64_t room = (p.per_sm == 1 ? kMaxSmem : kMaxSmem / p.per_sm - 2048) - weight_bytes;
+    // a third row would slow the first one down: 608 x 7168 23 us, 21 with two, 4096 rows 77.4 and 75.6
     const int stages = ring_stages(room, stage_bytes, (a.M + grid - 1) / grid);
     const auto kernel = a.w1 && a.w2 ? norm_bwd_kernel<COLS / W, YB, HB, TOKEN, kHold, true>
                                      : norm_bwd_kernel<COLS / W, YB, HB, TOKEN, kHold, false>;
