@@ -219,7 +219,7 @@ struct UpCfg {
 };
 
 template <int RP>
-__global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, const uint16_t *__restrict__ v2,
+__global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, const uint16_t *v2,
                                                              const uint16_t *__restrict__ W, int C, bool scaled,
                                                              const uint16_t *base, int64_t bs, uint16_t *out,
                                                              int64_t os, int cols, bool beside, const Waits waits)
@@ -306,17 +306,26 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
         const bool some = tid < tile.count;
         const uint4 *src = reinterpret_cast<const uint4 *>(v2 + (int64_t)(tile.i0 + (some ? tid : 0)) * (2 * RP));
 #pragma unroll
-        for (int k = 0; k < RP / 16; ++k) {
-            if (k < ksteps) {
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-                    if (some) {
-                        a = __ldg(src + h * (RP / 8) + k * 2);
-                        b = __ldg(src + h * (RP / 8) + k * 2 + 1);
+            for (int k0 = 0; k0 < RP / 16; k0 += 2) {
+                constexpr int kBatch = RP == 16 ? 1 : 2;   // 16 ranks each, loads before stores
+                uint4 w[kBatch][2];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    w[k][0] = w[k][1] = make_uint4(0, 0, 0, 0);
+                    if (some && k0 + k < ksteps) {
+                        w[k][0] = ld_after_v4(src + h * (RP / 8) + (k0 + k) * 2);
+                        w[k][1] = ld_after_v4(src + h * (RP / 8) + (k0 + k) * 2 + 1);
                     }
-                    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                    tmem_st_x8(tm + lanes + Cfg::kA + h * (RP / 2) + k * 8, w);
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    if (k0 + k < ksteps) {
+                        const uint4 a = w[k][0], b = w[k][1];
+                        const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                        tmem_st_x8(tm + lanes + Cfg::kA + h * (RP / 2) + (k0 + k) * 8, x);
+                    }
                 }
             }
         }
@@ -577,9 +586,10 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const LoraArgs l, const 
         return;
     const float *part = S.part + first * elems;
     for (int64_t e = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4; e < elems; e += (int64_t)gridDim.y * 1024) {
-        float4 s = *reinterpret_cast<const float4 *>(part + e);
+        float4 s = ld_after_f32x4(part + e);
+#pragma unroll 4
         for (int k = 1; k < n; ++k) {
-            const float4 p = *reinterpret_cast<const float4 *>(part + k * elems + e);
+            const float4 p = ld_after_f32x4(part + k * elems + e);
             s.x += p.x; s.y += p.y; s.z += p.z; s.w += p.w;
         }
         uint2 o;

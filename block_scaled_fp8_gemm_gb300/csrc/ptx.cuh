@@ -170,6 +170,25 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // Programmatic dependent launch: wait until the kernel before this one (in a stream, as
 // the launch allowed) has completed and its writes are visible; let the next one start.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// What the kernel before this one wrote is read with these after the wait: a load through
+// the read-only path could be moved above it.
+__device__ __forceinline__ uint4 ld_after_v4(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_after_f32x4(const float *p)
+{
+    const uint4 v = ld_after_v4(p);
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ float ld_after_f32(const float *p)
+{
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
 __device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }

@@ -860,7 +860,7 @@ __global__ void __launch_bounds__(512, 1)
 // row g.
 constexpr int kSumGroups = 128;   // at most
 
-__global__ void __launch_bounds__(kSumGroups * 8) norm_bwd_sum_kernel(const NormBwdArgs a, const float *__restrict__ ws,
+__global__ void __launch_bounds__(kSumGroups * 8) norm_bwd_sum_kernel(const NormBwdArgs a, const float *ws,
                                                                       int parts)
 {
     __shared__ float sums[2][8][kSumGroups + 1];
@@ -871,8 +871,8 @@ __global__ void __launch_bounds__(kSumGroups * 8) norm_bwd_sum_kernel(const Norm
     const float *src = ws + blockIdx.x * 8 + col;   // N is a multiple of eight
 #pragma unroll 4
     for (int p = group; p < parts; p += groups) {
-        s1 += src[(int64_t)p * 2 * a.N];
-        s2 += src[(int64_t)p * 2 * a.N + a.N];
+        s1 += ld_after_f32(src + (int64_t)p * 2 * a.N);
+        s2 += ld_after_f32(src + (int64_t)p * 2 * a.N + a.N);
     }
     sums[0][col][group] = s1;
     sums[1][col][group] = s2;
