@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, c
 // G[a,j,c] = f sum_i p[i,j] x[t,c] over an adapter's tokens: D[128 columns, ranks] with
 // the tokens as the contracted index, both operands in rows that run along M and N, 32
 // tokens a stage.  p comes as two bf16 parts side by side (p2), so an MMA of twice
-// the ranks gives both products, and the halves are added at the end.  Both gradients
+// the ranks gives both products, and the halves are added at the end (GradCfg::kJoint).  Both gradients
 // of a call are one launch: blockIdx.y counts first dA's and then dB's column tiles.
 // 90 us for the 385 MB of 8191 tokens of 9 adapters, K = 16384, N = 7168, r = 64, 4.3 TB/s:
 // with neither loads nor MMAs the steps' chain (rows' numbers, barrier, issue, commit)
@@ -414,10 +414,14 @@ template <int RP>
 struct GradCfg {
     static constexpr int kAtoms = RP <= 32 ? 1 : 2 * RP / 64;   // 64-wide tiles of p2
     static constexpr int kTile = kGradTokens * 128, kX = 4 * kTile, kStage = kX + kAtoms * kTile;
-    static constexpr int kStages = RP <= 32 ? 3 : RP == 64 ? 4 : 6;
-    static constexpr int kCtas = RP <= 32 ? 3 : RP == 64 ? 2 : 1;   // an SM (RP 128 takes all of its TMEM)
+    static constexpr int kStages = RP == 64 ? 4 : 3;
+    static constexpr int kCtas = RP <= 32 ? 3 : 2;   // an SM
     static constexpr int kSmem = kStages * kStage + 1024;
-    static constexpr int kTmem = 4 * RP;   // 64 to 512
+    // one MMA for both parts of p, or two into one accumulator: at 128 ranks the TMEM of a
+    // second CTA (8191 tokens, K = 16384: the backward pass 319 us, 350 with one)
+    static constexpr bool kJoint = RP <= 64;
+    static constexpr int kAcc = kJoint ? 2 * RP : RP;   // TMEM columns of an accumulator
+    static constexpr int kTmem = 2 * kAcc;   // 64 to 256
     static_assert(kCtas * kTmem <= 512 && kCtas * (kSmem + 2048) <= 228 * 1024, "the CTAs of an SM share it");
 };
 
@@ -526,10 +530,13 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
 #pragma unroll
             for (int k = 0; k < kGradTokens / 16; ++k) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)   // 128 columns each
-                    mma_bf16_ss(d + h * 2 * RP, smem_desc(st + h * 2 * Cfg::kTile + k * 2 * kSw, Cfg::kTile, kSw, 2),
-                                smem_desc(st + Cfg::kX + k * 2 * kSw, Cfg::kTile, kSw, 2),
-                                idesc_bf16(128, 2 * RP, 1, 1), s > 0 || k > 0);
+                for (int h = 0; h < 2; ++h) {   // 128 columns each
+                    const uint64_t xd = smem_desc(st + h * 2 * Cfg::kTile + k * 2 * kSw, Cfg::kTile, kSw, 2);
+                    const uint32_t p = st + Cfg::kX + k * 2 * kSw, id = idesc_bf16(128, Cfg::kAcc, 1, 1);
+                    mma_bf16_ss(d + h * Cfg::kAcc, xd, smem_desc(p, Cfg::kTile, kSw, 2), id, s > 0 || k > 0);
+                    if constexpr (!Cfg::kJoint)
+                        mma_bf16_ss(d + h * Cfg::kAcc, xd, smem_desc(p + Cfg::kAtoms / 2 * Cfg::kTile, Cfg::kTile, kSw, 2), id, 1);
+                }
             }
             tc_commit(done + s % Cfg::kStages);
         }
@@ -541,15 +548,16 @@ __global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs 
         wait_mma(done + (steps - 1) % Cfg::kStages, ((steps - 1) / Cfg::kStages) & 1, &abort_flag, waits);
     // lane: a column, warps 4 to 7 the second accumulator's
     const int c = c0 + warp * 32 + lane;
-    const uint32_t dw = d + (warp >> 2) * 2 * RP + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t dw = d + (warp >> 2) * Cfg::kAcc + ((uint32_t)((warp & 3) * 32) << 16);
     const float f = S.scaled ? l.scales[tile.a] : 1.0f;
     const int slot = tile.of > 1 ? split_tiles_before(l, tile.a, size) + tile.index : -1;
 #pragma unroll
     for (int j0 = 0; j0 < RP; j0 += 8) {
-        uint32_t hi[8], lo[8];
+        uint32_t hi[8], lo[8] = {};
         if (steps > 0) {
             tmem_ld_x8(dw + j0, hi);
-            tmem_ld_x8(dw + RP + j0, lo);
+            if constexpr (Cfg::kJoint)
+                tmem_ld_x8(dw + RP + j0, lo);
             tmem_wait_ld(hi, lo);
         }
 #pragma unroll
@@ -700,7 +708,7 @@ GradCall lora_grad_call(const LoraArgs &l, const LoraCall &p, const Halves &h, c
     // tokens take 78 us, with it 73, at half as large again 74; 4 of rank 64 over 16384: 163,
     // 156, 162.  At least 256 tokens instead of 384: 45 against 44 us for 4096 tokens.
     const int tiles = (K + kGradCols - 1) / kGradCols + (N + kGradCols - 1) / kGradCols;
-    const int ctas = h.RP <= 32 ? GradCfg<32>::kCtas : h.RP == 64 ? GradCfg<64>::kCtas : GradCfg<128>::kCtas;
+    const int ctas = h.RP <= 32 ? 3 : h.RP == 64 ? 2 : 1;   // an SM; 128 ranks have the largest parts to join
     const int64_t ways = (ctas * p.num_sms + tiles - 1) / tiles;
     int64_t size = std::max<int64_t>(384, (5 * l.T / (4 * ways) + 63) / 64 * 64);
     while (size < l.T && grad_floats(l.T, l.r, K, N, size) > ws_floats)
