@@ -139,10 +139,12 @@ struct Factor {
     bool scaled;
 };
 
-// Sums of 16 MT ranks from j0 over the warp's share of the columns into sums[rank][token].
+// Sums of 16 MT ranks from j0 over the warp's share of the columns into sums[rank][token];
+// t: the token of lane >> 2, or -1.
 template <int MT>
 __device__ __forceinline__ void few_down(const LoraArgs &l, const Tile &tile, int rank, int j0, const Factor &f,
-                                         const uint16_t *__restrict__ x, int64_t xs, float (&sums)[kFewRanks][kFewTokens + 1])
+                                         const uint16_t *__restrict__ x, int64_t xs, int t,
+                                         float (&sums)[kFewRanks][kFewTokens + 1])
 {
     constexpr int kUnroll = MT == 1 ? 8 : 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -154,8 +156,7 @@ __device__ __forceinline__ void few_down(const LoraArgs &l, const Tile &tile, in
         wok[i] = j < rank;
         wr[i] = f.W + ((int64_t)tile.a * l.r + (wok[i] ? j : 0)) * f.C + q * 8;
     }
-    const int t = g < tile.count ? __ldg(l.order + tile.i0 + g) : -1;
-    const bool xok = t >= 0 && t < l.T;
+    const bool xok = t >= 0;
     const uint16_t *xr = x + (xok ? t : 0) * xs + q * 8;
     // blocks of 32 columns, dealt evenly to the cluster's warps
     const int blocks = (f.C + 31) / 32, shares = gridDim.y * kFewWarps, share = blockIdx.y * kFewWarps + warp;
@@ -270,21 +271,20 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3) few_kernel(const LoraArgs l
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = tile.a < l.R ? rank_of(l, tile.a) : 0, ctas = gridDim.y;
     const int pairs = (rank + 15) / 16 * 8;
+    int t = (lane >> 2) < tile.count ? __ldg(l.order + tile.i0 + (lane >> 2)) : -1;
+    t = t < l.T ? t : -1;
     // the 128-byte pieces of the second product's operands that this warp will read
     for (int b = blockIdx.y * kFewWarps + warp; b * 64 < up.C; b += ctas * kFewWarps) {
         for (int j = lane; j < rank; j += 32)
             prefetch_l2(up.W + ((int64_t)tile.a * l.r + j) * up.C + b * 64);
-        if (base && lane < tile.count) {
-            const int t = __ldg(l.order + tile.i0 + lane);
-            if (t >= 0 && t < l.T)
-                prefetch_l2(base + t * bs + b * 64);
-        }
+        if (base && (lane & 3) == 0 && t >= 0)
+            prefetch_l2(base + t * bs + b * 64);
     }
     for (int j0 = 0; j0 < rank; j0 += kFewRanks) {
         if (rank - j0 > 16)
-            few_down<2>(l, tile, rank, j0, down, x, xs, sm.sums[warp]);
+            few_down<2>(l, tile, rank, j0, down, x, xs, t, sm.sums[warp]);
         else
-            few_down<1>(l, tile, rank, j0, down, x, xs, sm.sums[warp]);
+            few_down<1>(l, tile, rank, j0, down, x, xs, t, sm.sums[warp]);
         __syncthreads();
         const int nj = min(kFewRanks, rank - j0);
         for (int e = tid; e < nj * tile.count; e += kFewWarps * 32) {
@@ -304,16 +304,21 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3) few_kernel(const LoraArgs l
         const float f = down.scaled ? l.scales[tile.a] : 1.0f;
         for (int e = tid; e < kFewTokens * pairs; e += kFewWarps * 32) {
             const int i = e / pairs, p = e - i * pairs;
-            float v[2] = {0.0f, 0.0f};
+            float v[2] = {0.0f, 0.0f}, part[2][kMaxSplits];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {   // all on their way before the first is added
+                const uint32_t at = smem_u32(&sm.part[2 * p + k][i]);
+#pragma unroll
+                for (int c = 0; c < kMaxSplits; ++c)
+                    part[k][c] = c < ctas && i < tile.count && 2 * p + k < rank ? ld_shared_cluster_f32(mapa_shared(at, c)) : 0.0f;
+            }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int j = 2 * p + k;
-                if (i < tile.count && j < rank) {
-                    const uint32_t at = smem_u32(&sm.part[j][i]);
-                    for (int c = 0; c < ctas; ++c)
-                        v[k] += ctas > 1 ? ld_shared_cluster_f32(mapa_shared(at, c)) : sm.part[j][i];
-                    v[k] *= f;
-                }
+#pragma unroll
+                for (int c = 0; c < kMaxSplits; ++c)
+                    v[k] += part[k][c];
+                v[k] *= f;
                 if (blockIdx.y == 0 && i < tile.count) {
                     if (v_out && j < l.r)
                         v_out[(int64_t)(tile.i0 + i) * l.r + j] = v[k];
