@@ -427,8 +427,17 @@ def _codes(q, shape, name: str):
     return _dense(q, shape, name, torch.uint8 if q.dtype is torch.uint8 else torch.float8_e4m3fn)
 
 
+def _dims(t, name: str, dim: int):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
+    return t.shape
+
+
 def _explain_norm_gate_residual(y, h, w_pre, t, w_post, gate, u, q, scales, rstd):
-    shape = M, N = y.shape
+    shape = M, N = _dims(y, "y", 2)
+    _dims(h, "h", 2)
     f32, bf16 = torch.float32, torch.bfloat16
     _xdtype(y), _xdtype(h)
     _rows(y, shape, "y")
@@ -441,7 +450,8 @@ def _explain_norm_gate_residual(y, h, w_pre, t, w_post, gate, u, q, scales, rstd
 
 
 def _explain_norm_gate_residual_bwd(y, h, rstd, dt, dy, dh, w_post, w_pre, gate, du, dw_post, dw_pre, dgate):
-    shape = M, N = y.shape
+    shape = M, N = _dims(y, "y", 2)
+    _dims(h, "h", 2)
     f32, bf16 = torch.float32, torch.bfloat16
     _xdtype(y), _xdtype(h)
     _rows(y, shape, "y")
@@ -458,14 +468,9 @@ def _explain_norm_gate_residual_bwd(y, h, rstd, dt, dy, dh, w_post, w_pre, gate,
 
 
 def _explain_lora_operands(x, order, offsets, A, B, scales, ranks):
-    for name, t, dim in (("x", x, 2), ("A", A, 3), ("B", B, 3)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dim() != dim:
-            raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
-    T, K = x.shape
-    R, r, _ = A.shape
-    N = B.shape[2]
+    T, K = _dims(x, "x", 2)
+    R, r, _ = _dims(A, "A", 3)
+    N = _dims(B, "B", 3)[2]
     i32, bf16 = torch.int32, torch.bfloat16
     _rows(x, (T, K), "x", bf16)
     for t, s, name, dtype in ((order, (T,), "order", i32), (offsets, (R + 1,), "offsets", i32), (A, (R, r, K), "A", bf16),
