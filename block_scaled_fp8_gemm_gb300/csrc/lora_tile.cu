@@ -65,7 +65,7 @@ struct DownCfg {
 };
 
 template <int RP>
-__global__ void __launch_bounds__(kDownThreads) tile_down_kernel(const LoraArgs l, const uint16_t *__restrict__ x,
+__global__ void __launch_bounds__(kDownThreads, DownCfg<RP>::kCtas) tile_down_kernel(const LoraArgs l, const uint16_t *__restrict__ x,
                                                                  int64_t xs, const uint16_t *__restrict__ W, int C,
                                                                  bool scaled, float *__restrict__ v, const Halves halves, int cols, const Waits waits)
 {
@@ -219,7 +219,7 @@ struct UpCfg {
 };
 
 template <int RP>
-__global__ void __launch_bounds__(kUpThreads) tile_up_kernel(const LoraArgs l, const uint16_t *v2,
+__global__ void __launch_bounds__(kUpThreads, UpCfg<RP>::kCtas) tile_up_kernel(const LoraArgs l, const uint16_t *v2,
                                                              const uint16_t *__restrict__ W, int C, bool scaled,
                                                              const uint16_t *base, int64_t bs, uint16_t *out,
                                                              int64_t os, int cols, bool beside, const Waits waits)
@@ -426,7 +426,7 @@ struct GradCfg {
 };
 
 template <int RP>
-__global__ void __launch_bounds__(kGradThreads) tile_grad_kernel(const LoraArgs l, const GradSide A, const GradSide B,
+__global__ void __launch_bounds__(kGradThreads, GradCfg<RP>::kCtas) tile_grad_kernel(const LoraArgs l, const GradSide A, const GradSide B,
                                                                  int size, int slots, const Waits waits)
 {
     using Cfg = GradCfg<RP>;
