@@ -84,6 +84,8 @@ __device__ __forceinline__ int split_tiles_before(const LoraArgs &l, int a, int 
     return __reduce_add_sync(0xFFFFFFFFu, n);
 }
 
+constexpr int kMaxSplits = 8;   // CTAs of a cluster
+
 // Sum over the CTAs of the cluster, in the order of their ranks, of the fp32 array
 // [rows][cols] that each has at the same shared-memory address, rows `pitch` floats
 // apart; put(row, col, sum) is called for every four columns by one thread of one of
@@ -100,10 +102,15 @@ __device__ __forceinline__ void cluster_sum(uint32_t array, int rows, int cols, 
     for (int e = threadIdx.x; e < n; e += blockDim.x) {
         const int row = lo + e / quads, col = e % quads * 4;
         const uint32_t at = array + (row * pitch + col) * 4;
-        float4 s = ptx::ld_shared_cluster_f32x4(ptx::mapa_shared(at, ctas == 1 ? ptx::cluster_ctarank() : 0));
-        for (int p = 1; p < ctas; ++p) {
-            const float4 a = ptx::ld_shared_cluster_f32x4(ptx::mapa_shared(at, p));
-            s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
+        // all on their way before the first is added
+        float4 a[kMaxSplits];
+#pragma unroll
+        for (int p = 0; p < kMaxSplits; ++p)
+            a[p] = p < ctas ? ptx::ld_shared_cluster_f32x4(ptx::mapa_shared(at, p)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float4 s = a[0];
+#pragma unroll
+        for (int p = 1; p < kMaxSplits; ++p) {
+            s.x += a[p].x; s.y += a[p].y; s.z += a[p].z; s.w += a[p].w;
         }
         put(row, col, s);
     }
@@ -111,7 +118,6 @@ __device__ __forceinline__ void cluster_sum(uint32_t array, int rows, int cols, 
         ptx::cluster_sync();   // no CTA leaves while another reads its array
 }
 
-constexpr int kMaxSplits = 8;   // CTAs of a cluster
 
 // A product's inner factor in two bf16 parts, x = hi + lo to 2^-16 of x: [T][RP hi, RP lo]
 // with RP the padded rank, 0 past the rank.  `v` and `v2`: the backward pass has the
