@@ -402,6 +402,8 @@ __global__ void __launch_bounds__(kUpThreads, UpCfg<RP>::kCtas) tile_up_kernel(c
 // tokens a stage.  p comes as two bf16 parts side by side (p2), so an MMA of twice
 // the ranks gives both products, and the halves are added at the end (GradCfg::kJoint).  Both gradients
 // of a call are one launch: blockIdx.y counts first dA's and then dB's column tiles.
+// Three accumulators (384 columns a tile, a third less of p2) gain 3 us of 224 there and lose
+// as much or more elsewhere (adapters of 1024 tokens, rank 64: 66 against 62).
 // 90 us for the 385 MB of 8191 tokens of 9 adapters, K = 16384, N = 7168, r = 64, 4.3 TB/s:
 // with neither loads nor MMAs the steps' chain (rows' numbers, barrier, issue, commit)
 // takes 52 of them.  A ring with mbarriers and copying warps of their own took 136 where
@@ -413,12 +415,12 @@ constexpr int kGradCols = 256;    // two accumulators
 template <int RP>
 struct GradCfg {
     static constexpr int kAtoms = RP <= 32 ? 1 : 2 * RP / 64;   // 64-wide tiles of p2
-    static constexpr int kTile = kGradTokens * 128, kX = 4 * kTile, kStage = kX + kAtoms * kTile;
+    static constexpr int kTile = kGradTokens * 128, kX = kGradCols / 64 * kTile, kStage = kX + kAtoms * kTile;
     static constexpr int kStages = RP == 64 ? 4 : 3;
     static constexpr int kCtas = RP <= 32 ? 3 : 2;   // an SM
     static constexpr int kSmem = kStages * kStage + 1024;
     // one MMA for both parts of p, or two into one accumulator: at 128 ranks the TMEM of a
-    // second CTA (8191 tokens, K = 16384: the backward pass 319 us, 350 with one)
+    // second CTA (8191 tokens, K = 16384: the backward pass 316 us, 350 with one)
     static constexpr bool kJoint = RP <= 64;
     static constexpr int kAcc = kJoint ? 2 * RP : RP;   // TMEM columns of an accumulator
     static constexpr int kTmem = 2 * kAcc;   // 64 to 256
@@ -458,12 +460,11 @@ __global__ void __launch_bounds__(kGradThreads, GradCfg<RP>::kCtas) tile_grad_ke
         tmem_relinquish();
     }
     const int steps = (tile.count + kGradTokens - 1) / kGradTokens;
-    // x: 32 chunks a token, tokens tid / 32 + 8 i; p2: RP / 4 chunks a token, tokens
+    // x: chunk tid & 7 of every 64 columns of token tid / 8; p2: RP / 4 chunks a token, tokens
     // kPer apart.  Tokens 8 apart are 1024 bytes apart in a tile and share their swizzle.
-    const int ch = tid & 31;
-    const bool in = c0 + ch * 8 < S.C;
-    const int col = c0 + ch * 8;
-    const uint32_t at_x = (ch >> 3) * Cfg::kTile + sw128(tid >> 5, ch & 7);
+    const int col = c0 + (tid & 7) * 8;
+    const uint32_t at_x = sw128(tid >> 3, tid & 7);
+    static_assert(kGradThreads == 8 * kGradTokens, "a thread copies of one token");
     constexpr int kPer = kGradThreads / (RP / 4);
     const int prow = tid / (RP / 4), pc = tid % (RP / 4);
     const uint32_t at_p = Cfg::kX + (pc >> 3) * Cfg::kTile + sw128(prow, pc & 7);
@@ -486,12 +487,11 @@ __global__ void __launch_bounds__(kGradThreads, GradCfg<RP>::kCtas) tile_grad_ke
     auto fetch = [&](int s) {
         if (s < steps) {
             const uint32_t st = base + put * Cfg::kStage;
-            const uint16_t *const *row = rows[row_get] + (tid >> 5);
+            const uint16_t *row = rows[row_get][tid >> 3];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint16_t *r = row[8 * i];
-                const bool ok = in && r != nullptr;
-                cp_async_cg16_or_zero(st + at_x + i * kSw, ok ? r + col : S.x, ok);
+            for (int i = 0; i < kGradCols / 64; ++i) {
+                const bool ok = row != nullptr && col + i * 64 < S.C;
+                cp_async_cg16_or_zero(st + at_x + i * Cfg::kTile, ok ? row + col + i * 64 : S.x, ok);
             }
 #pragma unroll
             for (int i = 0; i < kGradTokens; i += kPer) {
