@@ -404,9 +404,9 @@ __global__ void __launch_bounds__(kUpThreads, UpCfg<RP>::kCtas) tile_up_kernel(c
 // of a call are one launch: blockIdx.y counts first dA's and then dB's column tiles.
 // Three accumulators (384 columns a tile, a third less of p2) gain 3 us of 224 there and lose
 // as much or more elsewhere (adapters of 1024 tokens, rank 64: 66 against 62).
-// 90 us for the 385 MB of 8191 tokens of 9 adapters, K = 16384, N = 7168, r = 64, 4.3 TB/s:
-// with neither loads nor MMAs the steps' chain (rows' numbers, barrier, issue, commit)
-// takes 52 of them.  A ring with mbarriers and copying warps of their own took 136 where
+// 87 us for the 385 MB of 8191 tokens of 9 adapters, K = 16384, N = 7168, r = 64, 4.4 TB/s:
+// a version of 90 us took 52 with neither loads nor MMAs, the chain of its steps (rows'
+// numbers, barrier, issue, commit).  A ring with mbarriers and copying warps of their own took 136 where
 // this took 116, a TMA gather of four rows a copy 165 against 90.
 constexpr int kGradThreads = 256;
 constexpr int kGradTokens = 32;   // a stage
@@ -435,7 +435,6 @@ __global__ void __launch_bounds__(kGradThreads, GradCfg<RP>::kCtas) tile_grad_ke
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t done[Cfg::kStages];
     __shared__ uint32_t tmem_slot;
-    __shared__ const uint16_t *rows[2 * Cfg::kStages][kGradTokens];   // a ring of the steps' rows
     __shared__ int abort_flag;
     const Tile tile = find_tile(l, blockIdx.x, size, false, 1);
     if (tile.of == 0) {
@@ -469,29 +468,21 @@ __global__ void __launch_bounds__(kGradThreads, GradCfg<RP>::kCtas) tile_grad_ke
     const int prow = tid / (RP / 4), pc = tid % (RP / 4);
     const uint32_t at_p = Cfg::kX + (pc >> 3) * Cfg::kTile + sw128(prow, pc & 7);
     const uint16_t *pr = S.p2 + (int64_t)(tile.i0 + prow) * (2 * RP) + pc * 8;
-    // Lane t of warp 0 looks the rows up, kStages + 2 steps before their copies: a load whose
-    // latency a step would otherwise wait for, and one address for all that copy the row.
+    // the token of this thread's copies, looked up two steps ahead
     auto token = [&](int s) {
-        const int i = s * kGradTokens + tid;
-        return tid < kGradTokens && i < tile.count ? __ldg(l.order + tile.i0 + i) : -1;
+        const int i = s * kGradTokens + (tid >> 3), t = i < tile.count ? __ldg(l.order + tile.i0 + i) : -1;
+        return t < l.T ? t : -1;
     };
-    auto put_row = [&](int slot, int t) {
-        if (tid < kGradTokens)
-            rows[slot][tid] = t >= 0 && t < l.T ? S.x + t * S.xs : nullptr;
-    };
-    for (int s = 0; s < Cfg::kStages; ++s)
-        put_row(s, token(s));
-    int t0 = token(Cfg::kStages), t1 = token(Cfg::kStages + 1);
-    int put = 0, row_put = Cfg::kStages, row_get = 0;   // stage of the next copies; row slots
+    int t0 = token(0), t1 = token(1), put = 0;   // put: stage of the next copies
     int left = tile.count - prow;
     auto fetch = [&](int s) {
         if (s < steps) {
             const uint32_t st = base + put * Cfg::kStage;
-            const uint16_t *row = rows[row_get][tid >> 3];
+            const uint16_t *row = S.x + (t0 >= 0 ? t0 : 0) * S.xs + col;
 #pragma unroll
             for (int i = 0; i < kGradCols / 64; ++i) {
-                const bool ok = row != nullptr && col + i * 64 < S.C;
-                cp_async_cg16_or_zero(st + at_x + i * Cfg::kTile, ok ? row + col + i * 64 : S.x, ok);
+                const bool ok = t0 >= 0 && col + i * 64 < S.C;
+                cp_async_cg16_or_zero(st + at_x + i * Cfg::kTile, ok ? row + i * 64 : S.x, ok);
             }
 #pragma unroll
             for (int i = 0; i < kGradTokens; i += kPer) {
@@ -502,12 +493,9 @@ __global__ void __launch_bounds__(kGradThreads, GradCfg<RP>::kCtas) tile_grad_ke
             }
             pr += kGradTokens * 2 * RP;
             left -= kGradTokens;
-            put_row(row_put, t0);
             t0 = t1;
-            t1 = token(s + Cfg::kStages + 2);
+            t1 = token(s + 2);
             put = put + 1 == Cfg::kStages ? 0 : put + 1;
-            row_put = row_put + 1 == 2 * Cfg::kStages ? 0 : row_put + 1;
-            row_get = row_get + 1 == 2 * Cfg::kStages ? 0 : row_get + 1;
         }
         cp_async_commit();
     };
