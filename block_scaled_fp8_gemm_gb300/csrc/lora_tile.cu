@@ -206,10 +206,10 @@ __global__ void __launch_bounds__(kDownThreads, DownCfg<RP>::kCtas) tile_down_ke
 // stream finds both complete.
 constexpr int kUpThreads = 128;
 
-template <int RP>
+template <int RP, int RING>   // RING: steps copied ahead
 struct UpCfg {
-    static constexpr int kCtas = RP == 16 ? 4 : RP <= 64 ? 3 : 2;   // an SM
-    static constexpr int kRing = 3;                   // steps copied ahead
+    static constexpr int kCtas = RP == 16 || RING == 2 ? 4 : RP <= 64 ? 3 : 2;   // an SM
+    static constexpr int kRing = RING;
     static constexpr int kY = kRows * 128, kW = RP * 128, kStage = kY + kW;
     static constexpr int kSmem = kRing * kStage + 1024;
     static constexpr int kA = 64;                     // TMEM: the accumulator, then hi, lo
@@ -218,13 +218,13 @@ struct UpCfg {
     static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "and its shared memory");
 };
 
-template <int RP>
-__global__ void __launch_bounds__(kUpThreads, UpCfg<RP>::kCtas) tile_up_kernel(const LoraArgs l, const uint16_t *v2,
+template <int RP, int RING>
+__global__ void __launch_bounds__(kUpThreads, UpCfg<RP, RING>::kCtas) tile_up_kernel(const LoraArgs l, const uint16_t *v2,
                                                              const uint16_t *__restrict__ W, int C, bool scaled,
                                                              const uint16_t *base, int64_t bs, uint16_t *out,
                                                              int64_t os, int cols, bool beside, const Waits waits)
 {
-    using Cfg = UpCfg<RP>;
+    using Cfg = UpCfg<RP, RING>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t done;
     __shared__ uint32_t tmem_slot;
@@ -595,13 +595,14 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const LoraArgs l, const 
     }
 }
 
-// How many ways to share `steps` of 64 columns so that the tiles fill `slots` CTAs once,
-// four steps a share at least.  The host does not know the tiles: it takes every
-// adapter's last one for half full (one CTA too many would be a second wave).
+// The tiles of 128 tokens, which the host does not know: every adapter's last one counts for half.
+int64_t host_tiles(const LoraArgs &l) { return l.T / kRows + 1 + std::min<int64_t>(l.R, l.T) / 2; }
+
+// How many ways to share `steps` of 64 columns so that the tiles fill `slots` CTAs once (one
+// CTA too many would be a second wave), four steps a share at least.
 int shares(const LoraArgs &l, int steps, int slots, int most)
 {
-    const int64_t tiles = l.T / kRows + 1 + std::min<int64_t>(l.R, l.T) / 2;
-    const int64_t want = std::min<int64_t>(slots / tiles, most);
+    const int64_t want = std::min<int64_t>(slots / host_tiles(l), most);
     return (int)std::max<int64_t>(1, std::min<int64_t>(want, steps / 4));
 }
 
@@ -619,17 +620,23 @@ cudaError_t run_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, in
                   halves, per * 64, Waits{p.status, p.timeout_ns});
 }
 
-template <int RP>
+template <int RP, int RING>
 cudaError_t run_up(const LoraArgs &l, const LoraCall &p, const uint16_t *v2, const uint16_t *W, int C, bool scaled,
                    const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, bool beside, cudaStream_t st)
 {
-    using Cfg = UpCfg<RP>;
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(tile_up_kernel<RP>), Cfg::kSmem);
+    using Cfg = UpCfg<RP, RING>;
+    const int steps = (C + 63) / 64, slots = Cfg::kCtas * p.num_sms, ranges = shares(l, steps, slots, steps);
+    // A shorter ring lets a fourth CTA in: 4096 tokens of rank 32 34.3 us, 35.3 without, 16384 104.6
+    // and 105.7; where there are not that many, a longer one is better: 1024 tokens 21.5 and 20.1.
+    if constexpr (RING == 3 && (RP == 32 || RP == 64))
+        if (host_tiles(l) * (steps / 4) >= UpCfg<RP, 2>::kCtas * p.num_sms)
+            return run_up<RP, 2>(l, p, v2, W, C, scaled, base, bs, out, os, beside, st);
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(tile_up_kernel<RP, RING>), Cfg::kSmem);
     if (e != cudaSuccess)
         return e;
-    const int steps = (C + 63) / 64, ranges = shares(l, steps, Cfg::kCtas * p.num_sms, steps), per = (steps + ranges - 1) / ranges;
+    const int per = (steps + ranges - 1) / ranges;
     const dim3 grid((unsigned)most_tiles(l.T, l.R, kRows, base != out), (steps + per - 1) / per);
-    return launch(tile_up_kernel<RP>, grid, kUpThreads, Cfg::kSmem, 1, true, st, l, v2, W, C, scaled, base, bs, out, os,
+    return launch(tile_up_kernel<RP, RING>, grid, kUpThreads, Cfg::kSmem, 1, true, st, l, v2, W, C, scaled, base, bs, out, os,
                   per * 64, beside, Waits{p.status, p.timeout_ns});
 }
 
@@ -670,10 +677,10 @@ cudaError_t launch_tile_up(const LoraArgs &l, const LoraCall &p, const uint16_t 
                            const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, bool beside, cudaStream_t st)
 {
     switch (pad_rank(l.r)) {
-    case 16: return run_up<16>(l, p, v2, W, C, scaled, base, bs, out, os, beside, st);
-    case 32: return run_up<32>(l, p, v2, W, C, scaled, base, bs, out, os, beside, st);
-    case 64: return run_up<64>(l, p, v2, W, C, scaled, base, bs, out, os, beside, st);
-    default: return run_up<128>(l, p, v2, W, C, scaled, base, bs, out, os, beside, st);
+    case 16: return run_up<16, 3>(l, p, v2, W, C, scaled, base, bs, out, os, beside, st);
+    case 32: return run_up<32, 3>(l, p, v2, W, C, scaled, base, bs, out, os, beside, st);
+    case 64: return run_up<64, 3>(l, p, v2, W, C, scaled, base, bs, out, os, beside, st);
+    default: return run_up<128, 3>(l, p, v2, W, C, scaled, base, bs, out, os, beside, st);
     }
 }
 

@@ -330,3 +330,15 @@ def test_offsets_that_are_no_plan_stay_in_bounds(g, ctx):
     assert torch.equal(apply(g, ctx, d)[0], out)
     assert all(torch.equal(a, b) for a, b in zip(apply_bwd(g, ctx, d, v), grads))
     assert g.gemmar_status(ctx)[0] == 0
+
+
+@pytest.mark.parametrize("T,r", [(2900, 20), (2750, 64)])
+def test_tiles_and_columns_for_four_ctas_an_sm(g, ctx, T, r):
+    """The second product's shorter ring, taken where its CTAs are many; a last step of part of its columns."""
+    ids = mixed_ids(T, 4, seed=T)
+    d = make(g, ctx, ids, 4, r, 136, 7160, seed=T)
+    out, v = apply(g, ctx, d)
+    check_apply(d, out, v)
+    d = make(g, ctx, ids, 4, r, 7160, 136, seed=T + 1)
+    _, v = apply(g, ctx, d)
+    check_bwd(d, v, *apply_bwd(g, ctx, d, v))
