@@ -2,9 +2,10 @@
 // 4 to 12 us on the device, and reading the ten tensors' types, shapes and layouts
 // through Python attributes and ctypes took 9 us a call before the library's own 4.
 // Read here, a pass of norm_gate_residual over one token, outputs allocated, is 18 us
-// instead of 28, and lora_apply's 9 instead of 20; the call itself takes 3.  Each function checks its tensors
-// and calls the C ABI; it returns the library's status, or -1 when a tensor is not what
-// the entry point takes: the Python wrapper then says which one and why.
+// instead of 28, and lora_apply's 9 instead of 20; the call itself takes 3.
+// Each function checks its tensors and calls the C ABI; it returns the library's status, or
+// -1 when a tensor is not what the entry point takes: the Python wrapper then says which
+// one and why.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>

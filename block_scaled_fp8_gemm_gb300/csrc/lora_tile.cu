@@ -400,13 +400,14 @@ __global__ void __launch_bounds__(kUpThreads, UpCfg<RP, RING>::kCtas) tile_up_ke
 // G[a,j,c] = f sum_i p[i,j] x[t,c] over an adapter's tokens: D[128 columns, ranks] with
 // the tokens as the contracted index, both operands in rows that run along M and N, 32
 // tokens a stage.  p comes as two bf16 parts side by side (p2), so an MMA of twice
-// the ranks gives both products, and the halves are added at the end (GradCfg::kJoint).  Both gradients
-// of a call are one launch: blockIdx.y counts first dA's and then dB's column tiles.
-// Three accumulators (384 columns a tile, a third less of p2) gain 3 us of 224 there and lose
-// as much or more elsewhere (adapters of 1024 tokens, rank 64: 66 against 62).
+// the ranks gives both products, and the halves are added at the end (GradCfg::kJoint).
+// Both gradients of a call are one launch: blockIdx.y counts first dA's and then dB's
+// column tiles.
 // 87 us for the 385 MB of 8191 tokens of 9 adapters, K = 16384, N = 7168, r = 64, 4.4 TB/s:
 // a version of 90 us took 52 with neither loads nor MMAs, the chain of its steps (rows'
-// numbers, barrier, issue, commit).  A ring with mbarriers and copying warps of their own took 136 where
+// numbers, barrier, issue, commit).  Three accumulators (384 columns a tile, a third less
+// of p2) gain 3 us there and lose more elsewhere (4 adapters of 1024 tokens, K = 2048, the
+// whole backward pass: 66 against 62).  A ring with mbarriers and copying warps of their own took 136 where
 // this took 116, a TMA gather of four rows a copy 165 against 90.
 constexpr int kGradThreads = 256;
 constexpr int kGradTokens = 32;   // a stage
