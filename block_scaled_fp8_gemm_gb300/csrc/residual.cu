@@ -771,7 +771,8 @@ __global__ void __launch_bounds__(512, 1)
             kk = !pre ? 0.0f : r2s * r2s * r2s * __shfl_sync(0xFFFFFFFFu, s, 0);
             const float m_dt = __shfl_sync(0xFFFFFFFFu, s, 1), m_dv = __shfl_sync(0xFFFFFFFFu, s, 2),
                         m_t = __shfl_sync(0xFFFFFFFFu, s, 3);
-            mean1 = post ? fmaf(r2s, m_dv, m_dt) - kk * m_t : 0.0f;
+            // h is in m_t alone: without a pre norm it must not come in as 0 * inf
+            mean1 = !post ? 0.0f : pre ? fmaf(r2s, m_dv, m_dt) - kk * m_t : m_dt;
         }
         const f2 mk = both(-kk), mm = both(-r1s * mean1);
 #pragma unroll

@@ -1,0 +1,48 @@
+"""norm_gate_residual and its backward pass on non-finite values and extreme magnitudes.  Formulas, inputs
+and tolerances are those of the operators' own test file."""
+import importlib.util
+import os
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def load(name):
+    spec = importlib.util.spec_from_file_location(name, os.path.join(os.path.dirname(os.path.abspath(__file__)), name + ".py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+res = load("test_gpu_residual")
+
+
+@pytest.fixture(scope="module")
+def g():
+    import block_scaled_fp8_gemm_gb300 as g
+    return g
+
+
+@pytest.fixture(scope="module")
+def ctx(g):
+    torch.cuda.set_device(0)
+    c = g.gemmar_create(0, 4096, 16384, 128, 1, flags=g.GEMMAR_NO_SELF_TEST, wait_timeout_ns=500_000_000)
+    yield c
+    c.close()
+
+
+@pytest.mark.parametrize("M,N", [(5, 1032), (700, 256), (3, 16384)])
+@pytest.mark.parametrize("gate", ["none", "row", "token"])
+def test_without_a_pre_norm_no_gradient_depends_on_the_stream(g, ctx, M, N, gate):
+    """d = dt then, so h's infinities, NaN and sums that overflow must not reach any gradient."""
+    d = res.make(M, N, True, False, gate, True, seed=M)
+    o = res.forward(g, ctx, d)
+    clean = res.backward(g, ctx, d, o["rstd"])
+    res.check_backward(d, o["rstd"], clean, 1.0, 1.0)
+    for row, value in ((0, float("inf")), (1, float("nan")), (2, 3e38)):
+        d["h"][row, 1::2] = value
+    sick = res.backward(g, ctx, d, o["rstd"])
+    for k in clean:
+        assert torch.equal(sick[k], clean[k]), k
