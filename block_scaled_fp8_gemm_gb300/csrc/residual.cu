@@ -558,9 +558,11 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int sta
 // ---------------------------------------------------------------- backward
 
 // One pass over the row forms four sums, from which both projections follow:
-// with dv = du w2, c = beta g w1, n = y r1, t = alpha h + c n and d = dt + r2 dv - k t,
-// k = r2^3 mean(dv t),
-//   mean(c n d) = mean(c n dt) + r2 mean(c n dv) - k mean(c n t).
+// with dv = du w2, c = beta g w1, n = y r1, t = alpha h + c n and d = dt + r2 (dv - k t),
+// k = r2 (r2 mean(dv t)) (`proj`),
+//   mean(c n d) = mean(c n dt) + r2 (mean(c n dv) - k mean(c n t)).
+// k t is of dv's size whatever the row's; r2^3, where it appears by itself, leaves the fp32 range
+// for rows of rms above 1e12 or below 1e-12.
 // The second pass recomputes n, t and dv and writes dy, dh (and a token's dgate).
 // The sums over rows, s1 = sum n d (times a token's gate) and s2 = sum du t r2,
 // stay in the thread's registers over all the CTA's rows and leave as one part per
@@ -745,7 +747,7 @@ __global__ void __launch_bounds__(512, 1)
                 fetch_row(ahead, st);
             cp_async_commit();
         }
-        float kk = 0.0f, mean1 = 0.0f;
+        float proj = 0.0f, mean1 = 0.0f;
         if (pre || post) {
             // as in encode_units: lane l ends with sum l >> 3 of its warp
             const bool up = lane & 16, up2 = lane & 8;
@@ -768,13 +770,13 @@ __global__ void __launch_bounds__(512, 1)
             for (int o = 4; o < 32; o <<= 1)
                 s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
             s *= inv_n;
-            kk = !pre ? 0.0f : r2s * r2s * r2s * __shfl_sync(0xFFFFFFFFu, s, 0);
+            proj = r2s * (r2s * __shfl_sync(0xFFFFFFFFu, s, 0));   // used with a pre norm alone
             const float m_dt = __shfl_sync(0xFFFFFFFFu, s, 1), m_dv = __shfl_sync(0xFFFFFFFFu, s, 2),
                         m_t = __shfl_sync(0xFFFFFFFFu, s, 3);
             // h is in m_t alone: without a pre norm it must not come in as 0 * inf
-            mean1 = !post ? 0.0f : pre ? fmaf(r2s, m_dv, m_dt) - kk * m_t : m_dt;
+            mean1 = !post ? 0.0f : pre ? fmaf(r2s, fmaf(-proj, m_t, m_dv), m_dt) : m_dt;
         }
-        const f2 mk = both(-kk), mm = both(-r1s * mean1);
+        const f2 mk = both(-proj), mm = both(-r1s * mean1);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int col = col_of(k), r = HOLD ? k : 0;
@@ -787,7 +789,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
                     for (int i = 0; i < W / 2; ++i) {
                         const Pair p = form(k, i, cw, w2);
-                        d.v[i] = fma2(p.t, mk, fma2(p.dv, r2, d.v[i]));
+                        d.v[i] = fma2(fma2(p.t, mk, p.dv), r2, d.v[i]);
                         s2[k].v[i] = fma2(mul2(p.du, r2), p.t, s2[k].v[i]);
                         if constexpr (TOKEN) {
                             const f2 nd = mul2(p.n, d.v[i]);
@@ -804,7 +806,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
                         for (int i = 0; i < W / 2; ++i) {
                             const Pair p = form(k, i, cw, w2);
-                            d.v[i] = fma2(p.t, mk, fma2(p.dv, r2, d.v[i]));
+                            d.v[i] = fma2(fma2(p.t, mk, p.dv), r2, d.v[i]);
                             s2[k].v[i] = fma2(mul2(p.du, r2), p.t, s2[k].v[i]);
                         }
                     }

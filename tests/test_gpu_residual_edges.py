@@ -46,3 +46,20 @@ def test_without_a_pre_norm_no_gradient_depends_on_the_stream(g, ctx, M, N, gate
     sick = res.backward(g, ctx, d, o["rstd"])
     for k in clean:
         assert torch.equal(sick[k], clean[k]), k
+
+
+@pytest.mark.parametrize("N", [512, 8200])
+@pytest.mark.parametrize("post,gate", [(False, "none"), (True, "row"), (True, "token")])
+@pytest.mark.parametrize("size", [1e16, 1e15, 1e13, 1e-12, 1e-14])
+def test_gradients_of_rows_of_any_size(g, ctx, N, post, gate, size):
+    """The pre norm takes a row's size out, so its gradient's terms stay comparable whatever it is."""
+    d = res.make(6, N, post, True, gate, True, y32=True, seed=7)
+    beta = size if post else 1.0   # a post norm takes y's size out
+    d["h"] *= size
+    if not post:
+        d["y"] *= size
+    d["dt"] /= size                # of du's gradient's size, which goes with 1 / size
+    o = res.forward(g, ctx, d, 0.75, beta, 0.0)
+    res.check_forward(d, o, 0.75, beta, 0.0)
+    b = res.backward(g, ctx, d, o["rstd"], 0.75, beta)
+    res.check_backward(d, o["rstd"], b, 0.75, beta)
