@@ -63,3 +63,25 @@ def test_gradients_of_rows_of_any_size(g, ctx, N, post, gate, size):
     res.check_forward(d, o, 0.75, beta, 0.0)
     b = res.backward(g, ctx, d, o["rstd"], 0.75, beta)
     res.check_backward(d, o["rstd"], b, 0.75, beta)
+
+
+@pytest.mark.parametrize("M,N", [(3, 1032), (3000, 1032), (3, 4104), (1000, 4104)])
+@pytest.mark.parametrize("h32", [False, True])
+@pytest.mark.parametrize("which", ["w_post", "gate", "w_pre"])
+def test_an_infinite_weight_stays_in_its_column(g, ctx, M, N, h32, which):
+    """Of the first column, whose weight is also at hand where a row's last threads have no column: t is infinite
+    there alone, its square makes r2 zero, and 0 is what the other columns' x is.  An infinite w_pre makes only
+    its own column of x infinite."""
+    d = res.make(M, N, which == "w_post", True, "row" if which == "gate" else "none", h32, seed=M)
+    d["y"][:, 0] = 1.0
+    clean = res.forward(g, ctx, d)
+    d[which][0] = float("inf")
+    o = res.forward(g, ctx, d)
+    assert torch.equal(o["t"][:, 1:], clean["t"][:, 1:]) and torch.equal(o["rstd"][:, 0], clean["rstd"][:, 0])
+    if which == "w_pre":
+        assert torch.equal(o["rstd"], clean["rstd"]) and torch.equal(o["u"][:, 1:], clean["u"][:, 1:])
+        zero = d["h"][:, 0] + d["y"][:, 0] == 0   # 0 * inf
+        assert torch.equal(o["u"][:, 0].isnan(), zero) and torch.equal(o["u"][:, 0].isinf(), ~zero)
+    else:
+        assert o["t"][:, 0].isinf().all() and (o["rstd"][:, 1] == 0).all()
+        assert (o["u"][:, 1:] == 0).all() and o["u"][:, 0].isnan().all()
