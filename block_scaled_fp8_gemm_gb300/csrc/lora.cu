@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3) few_kernel(const LoraArgs l
 #pragma unroll
                 for (int c = 0; c < kMaxSplits; ++c)
                     v[k] += part[k][c];
-                v[k] *= f;
+                v[k] = j < rank ? v[k] * f : 0.0f;
                 if (blockIdx.y == 0 && i < tile.count) {
                     if (v_out && j < l.r)
                         v_out[(int64_t)(tile.i0 + i) * l.r + j] = v[k];

@@ -170,7 +170,9 @@ __global__ void __launch_bounds__(kDownThreads, DownCfg<RP>::kCtas) tile_down_ke
     const float f = scaled ? l.scales[tile.a] : 1.0f;
     float *out = v ? v + (int64_t)tile.i0 * l.r : nullptr;
     cluster_sum(base, tile.count, RP, kPitch, gridDim.y, [&](int i, int j, float4 s) {
-        s = make_float4(f * s.x, f * s.y, f * s.z, f * s.w);
+        // past the rank the product was with zeros, which a NaN or an infinity makes NaN
+        s = make_float4(j < rank ? f * s.x : 0.0f, j + 1 < rank ? f * s.y : 0.0f, j + 2 < rank ? f * s.z : 0.0f,
+                        j + 3 < rank ? f * s.w : 0.0f);
         if (v) {
             float *o = out + (int64_t)i * l.r + j;
             const float e[4] = {s.x, s.y, s.z, s.w};
