@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3) few_kernel(const LoraArgs l
                     put_pair(halves, tile.i0 + i, j, l.r, v[k]);
                 }
             }
-            const uint32_t h = bf16x2_from_f32(v[0], v[1]);
+            const uint32_t h = high_halves(v[0], v[1]);
             sm.v.hi[i][p] = h;
             sm.v.lo[i][p] = bf16x2_from_f32(v[0] - __uint_as_float(h << 16), v[1] - __uint_as_float(h & 0xFFFF0000u));
         }

@@ -120,7 +120,8 @@ __device__ __forceinline__ void cluster_sum(uint32_t array, int rows, int cols, 
 
 
 // A product's inner factor in two bf16 parts, x = hi + lo to 2^-16 of x: [T][RP hi, RP lo]
-// with RP the padded rank, 0 past the rank.  `v` and `v2`: the backward pass has the
+// with RP the padded rank, 0 past the rank.  hi stays finite: rounded to infinity it would
+// leave lo = x - hi the opposite one, or NaN; so lo alone is infinite where x is.  `v` and `v2`: the backward pass has the
 // forward pass's v [T, r] split on the way; nullptr: not asked for.
 struct Halves {
     uint16_t *w2;
@@ -129,9 +130,18 @@ struct Halves {
     int RP;
 };
 
+__device__ __forceinline__ float finite_bf16(float x)
+{
+    constexpr float kMost = 0x1.FEp127f;
+    return fminf(fmaxf(x, -kMost), kMost);
+}
+
+// hi of two values
+__device__ __forceinline__ uint32_t high_halves(float a, float b) { return ptx::bf16x2_from_f32(finite_bf16(a), finite_bf16(b)); }
+
 __device__ __forceinline__ void put_halves(uint16_t *row, int RP, int j, float x)
 {
-    const uint32_t p = ptx::bf16x2_from_f32(x, x) & 0xFFFFu;
+    const uint32_t p = high_halves(x, x) & 0xFFFFu;
     row[j] = (uint16_t)p;
     row[RP + j] = (uint16_t)(ptx::bf16x2_from_f32(x - __uint_as_float(p << 16), 0.0f) & 0xFFFFu);
 }
@@ -147,7 +157,7 @@ __device__ __forceinline__ void put_pair(const Halves &h, int64_t i, int j, int 
 
 __device__ __forceinline__ void put_halves4(uint16_t *row, int RP, int j, const float4 &x)
 {
-    const uint32_t a = ptx::bf16x2_from_f32(x.x, x.y), b = ptx::bf16x2_from_f32(x.z, x.w);
+    const uint32_t a = high_halves(x.x, x.y), b = high_halves(x.z, x.w);
     *reinterpret_cast<uint2 *>(row + j) = make_uint2(a, b);
     *reinterpret_cast<uint2 *>(row + RP + j) =
         make_uint2(ptx::bf16x2_from_f32(x.x - __uint_as_float(a << 16), x.y - __uint_as_float(a & 0xFFFF0000u)),

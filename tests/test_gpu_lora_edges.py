@@ -3,6 +3,7 @@ tolerances are those of the operators' own test file."""
 import importlib.util
 import os
 
+import numpy as np
 import pytest
 import torch
 
@@ -45,3 +46,67 @@ def test_columns_of_v_past_a_rank_are_zero_for_any_token(g, ctx, T, r):
         k = int(d["ranks"][a])
         assert (v[at[a]:at[a + 1], k:] == 0).all(), a
         assert k == 0 or not torch.isfinite(v[at[a]:at[a + 1], :k]).all()
+
+
+@pytest.mark.parametrize("T,r", [(24, 16), (900, 32), (700, 100)])
+def test_an_infinite_scale_reaches_the_ranks_alone(g, ctx, T, r):
+    """w is infinite at an adapter's ranks; past them, where zeros stand for its rows, it must not be 0 * inf."""
+    d = lora.make(g, ctx, lora.mixed_ids(T, 4, 6), 4, r, 256, 384, seed=6)
+    for k in ("A", "B", "dy"):
+        d[k] = d[k].abs() + 0.01
+    d["scales"][1:3] = float("inf")
+    dx, _, _ = lora.apply_bwd(g, ctx, d, torch.zeros(T, r, device="cuda"))
+    sick = (d["ids"] == 1) | (d["ids"] == 2)
+    assert torch.isfinite(dx[~sick].float()).all() and (dx[sick] == float("inf")).all()
+
+
+def alike(got, ref):
+    """Infinities and NaN at the same places, the infinities of the same sign."""
+    got, bad = got.double(), ~torch.isfinite(ref)
+    return torch.equal(~torch.isfinite(got), bad) and torch.equal(got[bad].nan_to_num(0.0), ref[bad].nan_to_num(0.0))
+
+
+@pytest.mark.parametrize("T,r", [(24, 16), (900, 32), (700, 128)])
+def test_infinite_sums_stay_infinite(g, ctx, T, r):
+    """An infinity of x makes v infinite, and out = y + s v B is infinite of v B's sign (factors of one sign, so no
+    sum has infinities of both); one of dy does the same to w, dx and dA."""
+    d = lora.make(g, ctx, lora.mixed_ids(T, 4, 6), 4, r, 256, 384, seed=6, ranks=None)
+    d["A"], d["B"] = d["A"].abs() + 0.01, d["B"].abs() + 0.01
+    d["x"][::5, 7] = float("inf")
+    d["x"][1::5, 9] = -float("inf")
+    d["dy"][:, 11] = d["dy"][:, 11].abs()
+    out, v = lora.apply(g, ctx, d)
+    at = d["offsets"].tolist()
+    ref = d["y"].double()
+    for a in range(4):
+        rows = d["order"][at[a]:at[a + 1]].long()
+        vr = d["x"][rows].double() @ d["A"][a].double().T
+        assert alike(v[at[a]:at[a + 1]], vr)
+        ref[rows] += float(d["scales"][a]) * vr @ d["B"][a].double()
+    assert alike(out, ref) and ref.isinf().any() and not ref.isnan().any()
+    d = lora.make(g, ctx, lora.mixed_ids(T, 4, 6), 4, r, 256, 384, seed=6, ranks=None)
+    d["A"], d["B"], d["x"] = d["A"].abs() + 0.01, d["B"].abs() + 0.01, d["x"].abs() + 0.01
+    _, v = lora.apply(g, ctx, d)
+    d["dy"][::5, 7] = float("inf")
+    dx, dA, _ = lora.apply_bwd(g, ctx, d, v)
+    ref = d["dx0"].double()
+    for a in range(4):
+        rows = d["order"][at[a]:at[a + 1]].long()
+        w = float(d["scales"][a]) * d["dy"][rows].double() @ d["B"][a].double().T
+        ref[rows] += w @ d["A"][a].double()
+        assert alike(dA[a], w.T @ d["x"][rows].double())
+    assert alike(dx, ref) and ref.isinf().any() and not ref.isnan().any()
+
+
+@pytest.mark.parametrize("T,r", [(24, 16), (900, 32)])
+def test_v_above_the_largest_bf16(g, ctx, T, r):
+    """v = 0x7F7F (the largest bf16) + 2^119 is finite in fp32 and rounds to infinity in bf16."""
+    d = lora.make(g, ctx, np.zeros(T, np.int32), 1, r, 64, 128, seed=2, ranks=None)
+    big = torch.tensor(0x7F7F, dtype=torch.int16).view(torch.bfloat16).item()
+    d["A"].zero_()
+    d["A"][0, :, :2] = 1.0
+    d["x"].zero_()
+    d["x"][:, 0], d["x"][:, 1] = big, 2.0 ** 119
+    d["B"] *= 2.0 ** -12
+    out, v = lora.apply(g, ctx, d)
+    lora.check_apply(d, out, v)
