@@ -402,7 +402,7 @@ cudaError_t launch_lora_apply(const LoraArgs &l, const LoraCall &p, const uint16
         return launch_few(l, p, x, xs, Factor{A, K, false}, Factor{B, N, true}, y, ys, out, os, v, Halves{}, st);
     const Halves h = lora_halves(nullptr, l.T, l.r, ws);
     TRY(launch_tile_down(l, p, x, xs, A, K, false, v, h, st));
-    return launch_tile_up(l, p, h.w2, B, N, true, y, ys, out, os, false, st);
+    return launch_tile_up(l, p, h.w2, B, N, true, y, ys, out, os, st);
 }
 
 cudaError_t launch_lora_apply_bwd(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *dy,
@@ -416,10 +416,10 @@ cudaError_t launch_lora_apply_bwd(const LoraArgs &l, const LoraCall &p, const ui
         TRY(launch_few(l, p, dy, dys, Factor{B, N, true}, Factor{A, K, false}, dx0, dx0s, dx, dxs, nullptr, h, st));
         TRY(launch_tile_grad(l, p, g, st));
     } else {
-        // the weight gradients and dx need only w: they run side by side
+        // the weight gradients and dx need only w, but each launch waits for the one before it
         TRY(launch_tile_down(l, p, dy, dys, B, N, true, nullptr, h, st));
         TRY(launch_tile_grad(l, p, g, st));
-        TRY(launch_tile_up(l, p, h.w2, A, K, false, dx0, dx0s, dx, dxs, true, st));
+        TRY(launch_tile_up(l, p, h.w2, A, K, false, dx0, dx0s, dx, dxs, st));
     }
     return launch_grad_join(l, p, g, st);
 }

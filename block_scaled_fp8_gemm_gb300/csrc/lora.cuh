@@ -207,7 +207,7 @@ struct GradCall {
 cudaError_t launch_tile_down(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *W,
                              int C, bool scaled, float *v, const Halves &halves, cudaStream_t st);
 cudaError_t launch_tile_up(const LoraArgs &l, const LoraCall &p, const uint16_t *v2, const uint16_t *W, int C, bool scaled,
-                           const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, bool beside, cudaStream_t st);
+                           const uint16_t *base, int64_t bs, uint16_t *out, int64_t os, cudaStream_t st);
 Halves lora_halves(const float *v, int64_t T, int r, float *ws);
 GradCall lora_grad_call(const LoraArgs &l, const LoraCall &p, const Halves &h, const uint16_t *x, int64_t xs, int K,
                         uint16_t *dA, const uint16_t *dy, int64_t ys, int N, uint16_t *dB, float *ws, int64_t ws_floats);

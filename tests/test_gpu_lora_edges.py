@@ -110,3 +110,19 @@ def test_v_above_the_largest_bf16(g, ctx, T, r):
     d["B"] *= 2.0 ** -12
     out, v = lora.apply(g, ctx, d)
     lora.check_apply(d, out, v)
+
+
+@pytest.mark.parametrize("T,r,K,N", [(2000, 16, 2048, 512), (3000, 64, 512, 2048), (900, 128, 256, 7168)])
+def test_dx_reads_the_v_of_its_own_call(g, ctx, T, r, K, N):
+    """Two batches in turn through one context's scratch, nothing between the calls: dx, whose launch overlaps the
+    end of the weight gradients', must not see the other batch's w."""
+    batches = [lora.make(g, ctx, lora.mixed_ids(T, 5, s), 5, r, K, N, seed=s) for s in (1, 2)]
+    kept = [lora.apply(g, ctx, d)[1] for d in batches]
+    want = []
+    for d, v in zip(batches, kept):
+        want.append(lora.apply_bwd(g, ctx, d, v))
+        lora.check_bwd(d, v, *want[-1])
+    for _ in range(20):
+        got = [lora.apply_bwd(g, ctx, d, v) for d, v in zip(batches, kept)]
+        assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
+    assert g.gemmar_status(ctx)[0] == 0
