@@ -629,6 +629,22 @@ int check_rows(const void *p, int64_t stride, int64_t cols, int elem_bytes, bool
     return GEMMAR_OK;
 }
 
+// Do two bf16 matrices of T rows share elements?  Rows at one stride may lie between one
+// another (columns of a wider matrix); at two strides only the same start counts.
+bool rows_meet(const uint16_t *a, int64_t a_stride, int64_t a_cols, const uint16_t *b, int64_t b_stride, int64_t b_cols,
+               int64_t T)
+{
+    if (a == b)
+        return true;
+    if (a_stride != b_stride && T > 1)
+        return false;
+    const int64_t d = ((intptr_t)b - (intptr_t)a) / 2, last = (T - 1) * a_stride;
+    if (d >= last + a_cols || -d >= last + b_cols)
+        return false;
+    const int64_t off = a_stride > 0 && T > 1 ? ((d % a_stride) + a_stride) % a_stride : d;
+    return T == 1 || a_stride == 0 || off < a_cols || a_stride - off < b_cols;
+}
+
 int norm_shape(int64_t M, int64_t N)
 {
     if (M < 1 || N < 1)
@@ -773,6 +789,11 @@ GEMMAR_API int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stri
         return rc;
     if (!aligned16(v) || !aligned16(dA) || !aligned16(dB))
         return GEMMAR_ERR_ALIGN;
+    const int64_t na = (int64_t)R * r * K, nb = (int64_t)R * r * N;
+    auto meet = [](const uint16_t *p, int64_t n, const uint16_t *q, int64_t m) { return rows_meet(p, n, n, q, m, m, 1); };
+    if (rows_meet(dx, dx_stride, K, x, x_stride, K, T) || rows_meet(dx, dx_stride, K, dy, dy_stride, N, T) ||
+        meet(dA, na, A, na) || meet(dA, na, B, nb) || meet(dB, nb, A, na) || meet(dB, nb, B, nb) || meet(dA, na, dB, nb))
+        return GEMMAR_ERR_ARG;
     if (lora_grad_floats(T, r, (int)K, (int)N) > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
     cudaStream_t st = as_stream(stream);

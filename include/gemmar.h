@@ -513,9 +513,12 @@ int lora_apply(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, const int32
  *   dx[t,k]   = dx0[t,k] + sum_{j < ranks[a]} w[t,j] A[a,j,k]   (dx0[t] for a token without one)
  *   dA[a,j,k] = sum_{t of a} w[t,j] x[t,k],   dB[a,j,n] = scales[a] sum_{t of a} v[t,j] dy[t,n]
  * (the gradient of y is dy itself).  dx0 bf16 [T,K] (NULL: 0; may be dx itself) and
- * dx bf16 [T,K] with row strides, apart from x, dy, A and B; dA, dB bf16, of A's and B's shapes, overwritten:
+ * dx bf16 [T,K] with row strides; dA, dB bf16, of A's and B's shapes, overwritten:
  * 0 for an adapter without tokens and for rows past ranks[a].  Sums are fp32 in a
- * fixed order, rounded once.  Other arguments and limits as lora_apply.
+ * fixed order, rounded once.  dx lies apart from x, dy, A and B, and dA and dB apart from
+ * each other and from A and B: one is written while others are read.  GEMMAR_ERR_ARG where
+ * dA or dB does not, or dx starts where x or dy does or, at the same stride, shares elements.
+ * Other arguments and limits as lora_apply.
  */
 int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, const uint16_t *dy, int64_t dy_stride,
                    const int32_t *order, const int32_t *offsets, const uint16_t *A, const uint16_t *B,

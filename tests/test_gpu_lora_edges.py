@@ -126,3 +126,40 @@ def test_dx_reads_the_v_of_its_own_call(g, ctx, T, r, K, N):
         got = [lora.apply_bwd(g, ctx, d, v) for d, v in zip(batches, kept)]
         assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
     assert g.gemmar_status(ctx)[0] == 0
+
+
+def test_gradients_over_their_inputs_are_refused(g, ctx):
+    """dx is written while x and dy are read, dA and dB while A and B are."""
+    d = lora.make(g, ctx, [0, 1, -1, 0], 2, 8, 128, 128, seed=1, ranks=None)
+    d["A"], d["B"] = d["A"].contiguous(), d["B"].contiguous()
+    _, v = lora.apply(g, ctx, d)
+
+    def code(**kw):
+        a = dict(dx=torch.empty_like(d["x"]), dA=torch.empty_like(d["A"]), dB=torch.empty_like(d["B"]), dx0=d["dx0"])
+        a.update(kw)
+        before = {k: d[k].clone() for k in ("x", "dy", "A", "B")}
+        with pytest.raises(g.GemmarError) as e:
+            g.lora_apply_bwd(ctx, d["x"], d["dy"], d["order"], d["offsets"], d["A"], d["B"], d["scales"], d["ranks"], v, **a)
+        assert all(torch.equal(d[k], before[k]) for k in before)
+        return e.value.code
+    flat = torch.zeros(3 * 2 * 8 * 128, dtype=torch.bfloat16, device="cuda")
+    for kw in ({"dx": d["x"]}, {"dx": d["dy"]}, {"dA": d["A"]}, {"dB": d["B"]}, {"dA": d["B"]}, {"dB": d["A"]},
+               {"dA": flat[:2048].view(2, 8, 128), "dB": flat[1024:3072].view(2, 8, 128)}):
+        assert code(**kw) == g.GEMMAR_ERR_ARG, list(kw)
+    assert g.gemmar_status(ctx)[0] == 0
+
+
+def test_gradients_between_the_columns_of_their_inputs(g, ctx):
+    """x and dx as columns of one matrix share no element: not refused, and right."""
+    T, K, N = 300, 128, 256
+    d = lora.make(g, ctx, lora.mixed_ids(T, 3, 2), 3, 16, K, N, seed=4)
+    _, v = lora.apply(g, ctx, d)
+    want = lora.apply_bwd(g, ctx, d, v)
+    both = torch.cat([d["x"], torch.full_like(d["x"], 7.0)], 1)
+    dx, dA, dB = both[:, K:], torch.empty_like(d["A"]), torch.empty_like(d["B"])
+    g.lora_apply_bwd(ctx, both[:, :K], d["dy"], d["order"], d["offsets"], d["A"], d["B"], d["scales"], d["ranks"], v, dx, dA, dB, dx0=d["dx0"])
+    assert torch.equal(both[:, :K], d["x"]) and all(torch.equal(a, b) for a, b in zip((dx, dA, dB), want))
+    with pytest.raises(g.GemmarError) as e:
+        g.lora_apply_bwd(ctx, both[:, :K], d["dy"], d["order"], d["offsets"], d["A"], d["B"], d["scales"], d["ranks"], v,
+                         both[:, K - 8:-8], dA, dB, dx0=d["dx0"])
+    assert e.value.code == g.GEMMAR_ERR_ARG
