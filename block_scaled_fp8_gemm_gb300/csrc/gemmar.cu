@@ -28,7 +28,7 @@ struct gemmar_ctx {
     int max_P = 0;
     uint32_t flags = 0;
     uint64_t timeout_ns = 0;
-    float *W = nullptr;               // fp32 partials, max_P * (max_M + 128 * max_P) * N (tile-blocked)
+    float *W = nullptr;               // fp32 partials, max_P * (max_M + 128 * max_P) * N (tile-blocked), or 256 * max_M
     int64_t W_floats = 0;
     uint32_t *band_done = nullptr;    // kMaxBands retire counters, then as many claim counters
     ptx::DevStatus *status = nullptr;
@@ -763,10 +763,10 @@ GEMMAR_API int lora_apply(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, 
         return rc;
     if (!aligned16(v))
         return GEMMAR_ERR_ALIGN;
-    if (lora_half_floats(T, r) > ctx->W_floats)
+    const LoraArgs l{order, offsets, ranks, scales, T, R, r};
+    if (lora_apply_floats(l) > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
     cudaStream_t st = as_stream(stream);
-    const LoraArgs l{order, offsets, ranks, scales, T, R, r};
     const LoraCall p{ctx->num_sms, ctx->status, ctx->timeout_ns};
     CUDA_OK(launch_lora_apply(l, p, x, x_stride, A, (int)K, B, (int)N, y, y_stride, out, out_stride, v, ctx->W, st));
     return GEMMAR_OK;
@@ -916,6 +916,8 @@ GEMMAR_API int gemmar_create(gemmar_ctx **out, int device, int64_t max_M, int64_
     // fp32 partials in the tile-blocked layout: every band padded to whole
     // 128-row tiles, for up to max_P bands
     ctx->W_floats = (int64_t)max_P * (max_M + 128 * max_P) * N;
+    // the adapters' gradients of max_M tokens, which pass that at N = 128 and ranks past 64
+    ctx->W_floats = std::max(ctx->W_floats, lora_grad_floats(max_M, GEMMAR_LORA_MAX_RANK, 0, 0));
     // mx repack images, sized for the largest tile count any band split can give
     ctx->sfa_bytes = (int64_t)max_P * ((max_M + 127) / 128 + kMaxBands) * (K / 128) * 512;
     ctx->sfb_bytes = (int64_t)max_P * (N / 128) * (K / 128) * 1024;

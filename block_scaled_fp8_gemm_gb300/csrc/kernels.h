@@ -208,9 +208,9 @@ struct LoraCall {
 };
 // lora_apply and lora_apply_bwd.  Few tokens go to one kernel that does both products of
 // a direction (lora.cu), many to tiles on the tensor cores (lora_tile.cu).  Scratch:
-// lora_half_floats(T, r) for the forward pass, lora_grad_floats at least for the backward
+// lora_apply_floats for the forward pass, lora_grad_floats at least for the backward
 // pass, where more lets the tokens of a large adapter be shared out.
-int64_t lora_half_floats(int64_t T, int r);
+int64_t lora_apply_floats(const LoraArgs &l);
 int64_t lora_grad_floats(int64_t T, int r, int K, int N);
 cudaError_t launch_lora_apply(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *A, int K,
                               const uint16_t *B, int N, const uint16_t *y, int64_t ys, uint16_t *out, int64_t os, float *v,

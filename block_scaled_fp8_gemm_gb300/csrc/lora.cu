@@ -394,6 +394,8 @@ cudaError_t launch_few(const LoraArgs &l, const LoraCall &p, const uint16_t *x, 
             return e_;                   \
     } while (0)
 
+int64_t lora_apply_floats(const LoraArgs &l) { return few(l) ? 0 : l.T * pad_rank(l.r); }
+
 cudaError_t launch_lora_apply(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const uint16_t *A, int K,
                               const uint16_t *B, int N, const uint16_t *y, int64_t ys, uint16_t *out, int64_t os, float *v,
                               float *ws, cudaStream_t st)

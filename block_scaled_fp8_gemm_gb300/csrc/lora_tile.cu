@@ -685,8 +685,6 @@ cudaError_t launch_tile_up(const LoraArgs &l, const LoraCall &p, const uint16_t 
     }
 }
 
-int64_t lora_half_floats(int64_t T, int r) { return T * pad_rank(r); }
-
 int64_t lora_grad_floats(int64_t T, int r, int K, int N) { return grad_floats(T, r, K, N, T); }
 
 Halves lora_halves(const float *v, int64_t T, int r, float *ws)

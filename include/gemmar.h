@@ -119,8 +119,8 @@ int gemmar_supports(int P, int64_t M, int64_t N, int64_t K, int bands, int scale
  * gemmar_create -- make a context on `device` (which must be current) whose
  * workspace serves fused_gemm_reduce calls with P <= max_P, M <= max_M and the
  * given N and K: fp32 partials of max_P*(max_M + 128*max_P)*N floats (a tile-
- * blocked layout; each band's rows are rounded up to whole 128-row tiles),
- * band counters, the
+ * blocked layout; each band's rows are rounded up to whole 128-row tiles; at
+ * least 256*max_M, the scratch of max_M tokens' adapters), band counters, the
  * mxfp8 scale repack area and the fp8-wire staging.  Like the pages' window
  * it is sized once and never grows (sglang pull request #40757, "Worth a
  * reviewer's attention": the window is sized from the chunked-prefill
@@ -411,8 +411,13 @@ int fused_gemm_reduce_noalloc_status(int *detail);
  * that has one, stride * element size a multiple of 16 bytes (else
  * GEMMAR_ERR_ALIGN), 0 for one row read for all rows.  Everything else is
  * contiguous.  They use the context's partial-sum workspace as scratch
- * (GEMMAR_ERR_WORKSPACE when it is too small; a context made for the layer's
- * max_M and N is large enough), so the rule on stream order above holds.
+ * (GEMMAR_ERR_WORKSPACE when it is too small), so the rule on stream order above
+ * holds.  Calls of at most max_M rows or tokens always fit (norms: rows of at most
+ * N columns).  For more, in floats: norm_gate_residual none, its gradients at most
+ * (M + 1) N; lora_apply T r', or none where it takes one launch; lora_apply_bwd
+ * 2 T r', r' being r rounded up to 16, 32, 64 or 128.  lora_apply_bwd shares out the
+ * tokens of a large adapter as finely as what is left allows: a context of few
+ * columns makes it slower.
  */
 
 /* Widest row and smallest column granule of norm_gate_residual. */

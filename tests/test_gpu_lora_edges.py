@@ -163,3 +163,27 @@ def test_gradients_between_the_columns_of_their_inputs(g, ctx):
         g.lora_apply_bwd(ctx, both[:, :K], d["dy"], d["order"], d["offsets"], d["A"], d["B"], d["scales"], d["ranks"], v,
                          both[:, K - 8:-8], dA, dB, dx0=d["dx0"])
     assert e.value.code == g.GEMMAR_ERR_ARG
+
+
+@pytest.mark.parametrize("N,r,T", [(128, 128, 1024), (128, 65, 1024), (256, 128, 777), (128, 128, 1)])
+def test_a_context_of_the_layer_s_rows_is_large_enough(g, N, r, T):
+    c = g.gemmar_create(0, T, N, 128, 1, flags=g.GEMMAR_NO_SELF_TEST)
+    try:
+        d = lora.make(g, c, lora.mixed_ids(T, 3, 5), 3, r, 512, N, seed=3)
+        out, v = lora.apply(g, c, d)
+        lora.check_apply(d, out, v)
+        lora.check_bwd(d, v, *lora.apply_bwd(g, c, d, v))
+        assert g.gemmar_status(c)[0] == 0
+    finally:
+        c.close()
+
+
+def test_few_tokens_an_adapter_need_no_scratch(g, ctx):
+    """The forward pass in one launch: any context serves it."""
+    d = lora.make(g, ctx, lora.mixed_ids(3000, 64, 5), 64, 16, 128, 256, seed=3)
+    c = g.gemmar_create(0, 1, 128, 128, 1, flags=g.GEMMAR_NO_SELF_TEST)
+    try:
+        out, v = lora.apply(g, c, d)
+        lora.check_apply(d, out, v)
+    finally:
+        c.close()
