@@ -507,7 +507,7 @@ GEMMAR_API int fused_gemm_reduce(gemmar_ctx *ctx, int P, const uint8_t *const *A
     const bool slices = onchip || ((flags & GEMMAR_FUSE_SLICES) != 0 && !(flags & GEMMAR_FUSE_ONCHIP));
     if (!slices && blocked_partial_floats(P, M, bands, N) > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
-    if ((flags & GEMMAR_FP8_WIRE) && M * N > ctx->max_M * ctx->N)
+    if ((flags & GEMMAR_FP8_WIRE) && (M > ctx->max_M || M * N > ctx->max_M * ctx->N))   // row scales, codes
         return GEMMAR_ERR_WORKSPACE;
     cudaStream_t st = as_stream(stream);
     ctx->ov_bands = 0;
