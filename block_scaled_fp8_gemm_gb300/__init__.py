@@ -29,7 +29,34 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-from . import _operators  # noqa: E402  (built with the library; needs torch loaded)
+
+class _NoBinding:
+    """Stands for the operators' binding where it cannot be used: the GEMMs and codecs work without it, its own
+    entry points say why not."""
+
+    def __init__(self, why: str):
+        self._why = why
+
+    def __getattr__(self, name: str):
+        raise ImportError(f"{name}: {self._why}; build it with block_scaled_fp8_gemm_gb300.build.build() (there is no fallback path)")
+
+
+def _binding():
+    path = os.path.join(_HERE, "_operators.so")
+    if not os.path.exists(path):
+        return _NoBinding(f"_operators.so not found at {path}")
+    try:
+        from . import _operators   # needs torch loaded
+    except ImportError as e:
+        return _NoBinding(f"{path} does not load ({e})")
+    # it reads tensors through torch's own layout of them
+    built = getattr(_operators, "torch_version", "of another version")
+    if built != str(torch.__version__):
+        return _NoBinding(f"{path} was built against torch {built}, this is {torch.__version__}")
+    return _operators
+
+
+_operators = _binding()
 
 # ---- constants (mirror include/gemmar.h) -------------------------------------
 GEMMAR_OK = 0
@@ -108,8 +135,9 @@ for _name, (_res, _args) in _SIGS.items():
 
 EXPORTED = tuple(_SIGS)
 
-_operators.bind(*(ctypes.cast(getattr(_lib, n), _P).value for n in
-                  ("norm_gate_residual", "norm_gate_residual_bwd", "lora_apply", "lora_apply_bwd")))
+if not isinstance(_operators, _NoBinding):
+    _operators.bind(*(ctypes.cast(getattr(_lib, n), _P).value for n in
+                      ("norm_gate_residual", "norm_gate_residual_bwd", "lora_apply", "lora_apply_bwd")))
 
 
 class GemmarError(RuntimeError):

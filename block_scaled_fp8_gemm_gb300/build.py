@@ -38,7 +38,7 @@ def build_binding() -> str:
     lib = os.path.join(home, "lib")
     tmp = BINDING_PATH + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DGEMMAR_TORCH_VERSION="{torch.__version__}"',
            "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(home, "include"),
            "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),

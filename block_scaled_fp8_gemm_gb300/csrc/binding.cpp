@@ -291,4 +291,12 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_operators", nullptr, -1, g_meth
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__operators() { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__operators()
+{
+    PyObject *m = PyModule_Create(&g_module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", GEMMAR_TORCH_VERSION) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
