@@ -311,12 +311,12 @@ def band_reduce(ctx: Context, W, P: int, M: int, N: int, bands: int, out, stream
            "band_reduce")
 
 
-def _xdtype(x) -> int:
+def _xdtype(x, name: str = "x") -> int:
     if x.dtype is torch.bfloat16:
         return GEMMAR_DTYPE_BF16
     if x.dtype is torch.float32:
         return GEMMAR_DTYPE_F32
-    raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")
+    raise TypeError(f"{name} must be bfloat16 or float32, got {x.dtype}")
 
 
 def rowquant_e4m3(ctx: Context, x, q, row_scale, stream=None) -> None:
@@ -452,7 +452,7 @@ def _gate(gate, M: int, N: int):
 def _codes(q, shape, name: str):
     if q is None:
         return None
-    return _dense(q, shape, name, torch.uint8 if q.dtype is torch.uint8 else torch.float8_e4m3fn)
+    return _dense(q, shape, name, torch.uint8 if getattr(q, "dtype", None) is torch.uint8 else torch.float8_e4m3fn)
 
 
 def _dims(t, name: str, dim: int):
@@ -467,7 +467,7 @@ def _explain_norm_gate_residual(y, h, w_pre, t, w_post, gate, u, q, scales, rstd
     shape = M, N = _dims(y, "y", 2)
     _dims(h, "h", 2)
     f32, bf16 = torch.float32, torch.bfloat16
-    _xdtype(y), _xdtype(h)
+    _xdtype(y, "y"), _xdtype(h, "h")
     _rows(y, shape, "y")
     _rows(h, shape, "h")
     _gate(gate, M, N)
@@ -481,7 +481,7 @@ def _explain_norm_gate_residual_bwd(y, h, rstd, dt, dy, dh, w_post, w_pre, gate,
     shape = M, N = _dims(y, "y", 2)
     _dims(h, "h", 2)
     f32, bf16 = torch.float32, torch.bfloat16
-    _xdtype(y), _xdtype(h)
+    _xdtype(y, "y"), _xdtype(h, "h")
     _rows(y, shape, "y")
     _rows(h, shape, "h")
     row = _gate(gate, M, N)[1] == 0
@@ -535,6 +535,7 @@ def norm_gate_residual(ctx: Context, y, h, w_pre, t, w_post=None, gate=None, alp
                                        scales, rstd, _stream(stream))
     if rc < 0:
         _explain_norm_gate_residual(y, h, w_pre, t, w_post, gate, u, q, scales, rstd)
+        raise ValueError("norm_gate_residual: an argument does not fit")
     if rc:
         _check(rc, "norm_gate_residual")
 
@@ -548,6 +549,7 @@ def norm_gate_residual_bwd(ctx: Context, y, h, rstd, dt, dy, dh, w_post=None, w_
                                            dw_post, dw_pre, dgate, _stream(stream))
     if rc < 0:
         _explain_norm_gate_residual_bwd(y, h, rstd, dt, dy, dh, w_post, w_pre, gate, du, dw_post, dw_pre, dgate)
+        raise ValueError("norm_gate_residual_bwd: an argument does not fit")
     if rc:
         _check(rc, "norm_gate_residual_bwd")
 
@@ -555,7 +557,7 @@ def norm_gate_residual_bwd(ctx: Context, y, h, rstd, dt, dy, dh, w_post=None, w_
 def lora_plan(ctx: Context, adapter_ids, order, offsets, stream=None) -> None:
     """Sort a batch's tokens by adapter: order int32 [T] and offsets int32 [R+1] from adapter_ids int32 [T]
     (an id outside [0, R) is a token without one).  One plan serves every layer of the batch."""
-    T, R = adapter_ids.numel(), offsets.numel() - 1
+    T, R = _dims(adapter_ids, "adapter_ids", 1)[0], _dims(offsets, "offsets", 1)[0] - 1
     i32 = torch.int32
     _check(_lib.lora_plan(ctx.handle, _dense(adapter_ids, (T,), "adapter_ids", i32), T, R,
                           _dense(order, (T,), "order", i32), _dense(offsets, (R + 1,), "offsets", i32),
@@ -569,6 +571,7 @@ def lora_apply(ctx: Context, x, order, offsets, A, B, scales, ranks, out, y=None
     rc = _operators.lora_apply(ctx.handle.value, x, order, offsets, A, B, scales, ranks, out, y, v, _stream(stream))
     if rc < 0:
         _explain_lora_apply(x, order, offsets, A, B, scales, ranks, out, y, v)
+        raise ValueError("lora_apply: an argument does not fit")
     if rc:
         _check(rc, "lora_apply")
 
@@ -581,5 +584,6 @@ def lora_apply_bwd(ctx: Context, x, dy, order, offsets, A, B, scales, ranks, v, 
                                    _stream(stream))
     if rc < 0:
         _explain_lora_apply_bwd(x, order, offsets, A, B, scales, ranks, dy, v, dx, dA, dB, dx0)
+        raise ValueError("lora_apply_bwd: an argument does not fit")
     if rc:
         _check(rc, "lora_apply_bwd")
