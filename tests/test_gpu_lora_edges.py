@@ -187,3 +187,32 @@ def test_few_tokens_an_adapter_need_no_scratch(g, ctx):
         lora.check_apply(d, out, v)
     finally:
         c.close()
+
+
+def few_of_many(T, R, active, seed):
+    """Tokens of a few adapters, far apart among many resident ones, in runs."""
+    rng = np.random.default_rng(seed)
+    which = rng.choice(R, active, replace=False)
+    ids = np.repeat(which[rng.integers(0, active, T // 50 + 1)], 50)[:T]
+    ids[rng.random(T) < 0.05] = -1
+    return ids.astype(np.int32)
+
+
+@pytest.mark.parametrize("T,R,active,r", [(1, 1024, 1, 16), (40, 1024, 3, 64), (2048, 1024, 4, 16), (3000, 1024, 4, 64), (4096, 256, 1, 33),
+                                          (4097, 1024, 4, 64), (6000, 1000, 2, 128)])
+def test_few_active_adapters_of_many(g, ctx, T, R, active, r):
+    d = lora.make(g, ctx, few_of_many(T, R, active, T), R, r, 256, 384, seed=T, ranks=None)
+    out, v = lora.apply(g, ctx, d)
+    lora.check_apply(d, out, v)
+    lora.check_bwd(d, v, *lora.apply_bwd(g, ctx, d, v))
+    assert g.gemmar_status(ctx)[0] == 0
+
+
+@pytest.mark.parametrize("T,R,r,K,N", [(8191, 9, 64, 2048, 1032), (16384, 3, 16, 512, 776), (5000, 2, 128, 1024, 512)])
+def test_many_tokens(g, ctx, T, R, r, K, N):
+    """Adapters cut into several tiles each, of which the parts are joined, and tiles in several waves."""
+    d = lora.make(g, ctx, lora.mixed_ids(T, R, T), R, r, K, N, seed=T)
+    out, v = lora.apply(g, ctx, d)
+    lora.check_apply(d, out, v)
+    lora.check_bwd(d, v, *lora.apply_bwd(g, ctx, d, v))
+    assert g.gemmar_status(ctx)[0] == 0
