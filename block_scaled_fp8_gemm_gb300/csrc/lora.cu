@@ -108,8 +108,8 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 // products: a cluster takes 8 tokens of one adapter (the N of one MMA), its CTAs share
 // the columns of the first product, exchange v through distributed shared memory, and
 // share the columns of the second, whose weights they have meanwhile asked into L2.
-// r = 16, N = 7168: one token, K = 2048, 6.6 us; 96 tokens of 48 adapters, K = 16384, 12.3 us
-// for 42 MB, 3.4 TB/s.  What bounds it is the chain of trips to memory: the plan, the
+// r = 16, N = 7168: one token, K = 2048, 6.8 us; 96 tokens of 48 adapters, K = 16384, 12.6 us
+// for 42 MB, 3.3 TB/s.  What bounds it is the chain of trips to memory: the plan, the
 // first weights, the exchange, the second weights, the stores.
 //
 // Fragments are loaded straight from memory into registers, 16 bytes a lane, no
@@ -368,7 +368,10 @@ namespace {
 // the first, which costs T r and beats the tensor-core tiles up to here (K = 2048 or 16384,
 // N = 7168; this kernel against the tiles): T = 64 of 16 adapters, r = 16, 8 us against 16;
 // 512 of 64, 25 against 68; 1024 of 32, 22 against 28; 2048 of 256, 45 against 106; and past
-// the rule, 256 of 8 with r = 64, 26 against 16.
+// the rule, 256 of 8 with r = 64, 26 against 16.  All for tokens spread evenly over the R
+// adapters: how many of them have tokens is known on the device alone, and a few of many
+// take this kernel past where it pays (2048 tokens of 4 adapters, r = 64, K = 2048: 29 us
+// with R = 4, 98 with R = 1024).
 bool few(const LoraArgs &l) { return l.T <= 4096 && l.T * l.r <= 1024 * (int64_t)l.R; }
 
 cudaError_t launch_few(const LoraArgs &l, const LoraCall &p, const uint16_t *x, int64_t xs, const Factor &down,

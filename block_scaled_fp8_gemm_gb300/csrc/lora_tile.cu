@@ -6,7 +6,9 @@
 // A rank r contraction does 2r flops for every element it reads, below the 283
 // flops a byte of the tensor peak over the copy rate even at r = 128: the tokens'
 // rows are what bounds these kernels, and the low-rank side costs little enough to
-// enter as two bf16 parts (its rounding error then is 2^-16).
+// enter as two bf16 parts (its rounding error then is 2^-16; the result's own, one
+// bf16 rounding, is 2^-8, and its distance from the 64-bit value is that of the same
+// formula in fp32).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -50,7 +52,7 @@ __host__ __device__ constexpr int tmem_cols(int n) { return n <= 32 ? 32 : n <= 
 // v[i][j] = f sum_c x[t,c] W[a,j,c]: D[128 tokens, ranks], both operands K-major, 64
 // columns a stage.  The CTAs of a cluster share the columns of a tile (blockIdx.y) and
 // add their sums in rank order through distributed shared memory.
-// Bound by the reads of x: 88 us for the 483 MB of 14746 tokens, K = 16384, r = 64, 5.5 TB/s;
+// Bound by the reads of x: 87 us for the 483 MB of 14746 tokens, K = 16384, r = 64, 5.6 TB/s;
 // of that 19 us do not depend on K (launch, first stages, the cluster's sum), the rest
 // runs at 6.8 TB/s.  A TMA gather of four rows a copy takes 155 us (128 bytes of a row at
 // a time leave it at 20 bytes a ns and SM), TMA boxes of neighbouring rows 86.
@@ -198,15 +200,15 @@ __global__ void __launch_bounds__(kDownThreads, DownCfg<RP>::kCtas) tile_down_ke
 // pieces out of it.  A step is a chain (barrier, MMA, TMEM read, transposition,
 // stores) that its own CTA does not overlap; three or four CTAs an SM do, so the
 // accumulator is single and the ring short.
-// 88 us for the 470 MB of 16384 tokens, N = 7168, r = 64, 5.3 TB/s.  A version of 97 us took 82
+// 89 us for the 470 MB of 16384 tokens, N = 7168, r = 64, 5.3 TB/s.  A version of 97 us took 82
 // without MMAs and sums, 85 without stores and 60 without either: reads, the chain of a
 // step and writes share the time.  mma.sync fragments instead of tcgen05 took 149 where this
 // took 95, eight warps a CTA 102 against 96.
 // In the backward pass the kernel before this one is tile_grad_kernel, whose results it does
 // not read; v2 comes from the one before that.  It waits all the same: its writes are
 // promised to be seen only through that wait, which follows the gradient kernel's own.
-// Reading v2 at once, beside the gradients, took 45.0 us instead of 47.1 for 4096 tokens of
-// rank 16 and 223 instead of 230 for 8191 of rank 64 (the whole pass).
+// Reading v2 at once, beside the gradients, took 42 us instead of 44 for 4096 tokens of rank
+// 16, 61 instead of 66 at rank 64, 221 instead of 225 for 8191 (the whole backward pass).
 constexpr int kUpThreads = 128;
 
 template <int RP, int RING>   // RING: steps copied ahead
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(kUpThreads, UpCfg<RP, RING>::kCtas) tile_up_ke
 // the ranks gives both products, and the halves are added at the end (GradCfg::kJoint).
 // Both gradients of a call are one launch: blockIdx.y counts first dA's and then dB's
 // column tiles.
-// 87 us for the 385 MB of 8191 tokens of 9 adapters, K = 16384, N = 7168, r = 64, 4.4 TB/s:
+// 89 us for the 385 MB of 8191 tokens of 9 adapters, K = 16384, N = 7168, r = 64, 4.3 TB/s:
 // a version of 90 us took 52 with neither loads nor MMAs, the chain of its steps (rows'
 // numbers, barrier, issue, commit).  Three accumulators (384 columns a tile, a third less
 // of p2) gain 3 us there and lose more elsewhere (4 adapters of 1024 tokens, K = 2048, the
@@ -421,7 +423,7 @@ struct GradCfg {
     static constexpr int kCtas = RP <= 32 ? 3 : 2;   // an SM
     static constexpr int kSmem = kStages * kStage + 1024;
     // one MMA for both parts of p, or two into one accumulator: at 128 ranks the TMEM of a
-    // second CTA (8191 tokens, K = 16384: the backward pass 316 us, 350 with one)
+    // second CTA (8191 tokens, K = 16384: the backward pass 316 us, 350 with one; 288 since)
     static constexpr bool kJoint = RP <= 64;
     static constexpr int kAcc = kJoint ? 2 * RP : RP;   // TMEM columns of an accumulator
     static constexpr int kTmem = 2 * kAcc;   // 64 to 256
@@ -699,8 +701,9 @@ GradCall lora_grad_call(const LoraArgs &l, const LoraCall &p, const Halves &h, c
     // Cut an adapter's tokens so that one adapter alone would fill the SMs once, a quarter
     // larger than that since several adapters end inside a tile each, 384 at least, and no
     // finer than the scratch allows.  Without the quarter 4 adapters of rank 16 over 8192
-    // tokens take 78 us, with it 73, at half as large again 74; 4 of rank 64 over 16384: 163,
-    // 156, 162.  At least 256 tokens instead of 384: 45 against 44 us for 4096 tokens.
+    // tokens take 77 us, with it 71, at half as large again 72; 4 of rank 64 over 16384: 167,
+    // 159, 155; rank 16 over 4096: 44.1, 44.2, 44.8.  At least 256 tokens instead of 384 change
+    // none of these.
     const int tiles = (K + kGradCols - 1) / kGradCols + (N + kGradCols - 1) / kGradCols;
     const int ctas = h.RP <= 32 ? 3 : h.RP == 64 ? 2 : 1;   // an SM; 128 ranks have the largest parts to join
     const int64_t ways = (ctas * p.num_sms + tiles - 1) / tiles;

@@ -391,8 +391,8 @@ __host__ __device__ constexpr bool stage_pre(int W) { return W == 8; }
 // offsets reach them all (with units T W apart address arithmetic was a third of
 // the instructions: 71 us instead of 66 at 4096 x 7168, fp32 stream, codes).
 // Two rows an SM in flight (two CTAs) hide each other's two sums.
-// 16384 x 7168 with a gate per token, bf16: 174 us, 6.7 TB/s, the rate of a copy.  4096 x
-// 7168 with an fp32 stream and codes: 57 us, 5.7 TB/s (16384 rows 202 us, 6.4): the first
+// 16384 x 7168 with a gate per token, bf16: 175 us, 6.7 TB/s, the rate of a copy.  4096 x
+// 7168 with an fp32 stream and codes: 56 us, 5.8 TB/s (16384 rows 202 us, 6.4): the first
 // rows' copies and 14 turns for 13.5 rows a CTA are the rest.
 template <int U, bool YB, bool HB, bool STAGED>
 __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int stages)
@@ -478,7 +478,8 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int sta
                 put_plane<U, W>(at_w2, k, ldg_f32<W>(a.w2 + wcol[k]));
         }
     }
-    if constexpr (STAGED) {   // the zeros by themselves: 4096 x 7168 57.8 us, 59.4 as a choice at the store above
+    // The zeros by themselves: 4096 x 7168, fp32 stream 57.8 us a pass, 59.4 as a choice at the store above.
+    if constexpr (STAGED) {
 #pragma unroll
         for (int k = 0; k < U; ++k)
             if (scaled && !ok[k])
@@ -581,13 +582,13 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a, int sta
 // sums are exchanged; the weights sit in shared memory.  Wider rows take 32 columns
 // a thread, read the slots twice and the weights through L1.
 // BOTH: both norms are there (known when compiling, a pass of the row is one loop).
-// 4096 x 7168 bf16: 76 us, 4.7 TB/s; 16384 rows 265, 5.3.  Not bound by HBM (56% busy) nor
+// 4096 x 7168 bf16: 74 us, 4.8 TB/s; 16384 rows 255, 5.5.  Not bound by HBM (56% busy) nor
 // by one pipe (issue slots 44%): 14 warps of 122 registers, whose two sums over the rows
 // leave no room for a second CTA, do not hide the latencies of shared memory and of the
 // arithmetic.  Running a row's first pass before the second of the row before it, so
-// that the exchange of sums is off the path, is no faster (78 and 268 us), nor is twice
-// the threads with 8 columns each (95).  Rows wider than 8192 have one CTA's ring for a
-// single row: 4096 x 16384 211 us, 3.8 TB/s.
+// that the exchange of sums is off the path, was no faster (78 and 268 us against 78 and 265),
+// nor twice the threads with 8 columns each (95 against 81).  Rows wider than 8192 have one CTA's ring for a
+// single row: 4096 x 16384 210 us, 3.8 TB/s.
 template <int U, bool YB, bool HB, bool TOKEN, bool HOLD, bool BOTH>
 __global__ void __launch_bounds__(512, 1)
     norm_bwd_kernel(const NormBwdArgs a, float *__restrict__ ws, int stages, int gate_staged)

@@ -435,8 +435,9 @@ int fused_gemm_reduce_noalloc_status(int *detail);
  * of quant_blockscale_e4m3 applied to the fp32 x (not to its bf16 rounding).
  * All arithmetic is fp32 and every output is rounded once; x is formed from the
  * fp32 t, not from its rounding to h's type.  Rows are independent: a row with a
- * NaN or an infinity leaves the others alone.  |y| or |t| above 1.8e19 overflows
- * its sum of squares.
+ * NaN or an infinity leaves the others alone.  Where a row's sum of squares passes
+ * fp32's range (a root mean square above 1.8e19 / sqrt(N)) its r is 0; squares below
+ * 1e-38 lose digits and vanish.
  *   y [M,N] of y_dtype, h [M,N] of h_dtype (GEMMAR_DTYPE_F32 or _BF16), row
  *   strides y_stride, h_stride; w_post, w_pre fp32 [N] or NULL; gate bf16:
  *   gate_stride 0 is one row [N] for every row, else [M,N].
@@ -497,7 +498,9 @@ int lora_plan(gemmar_ctx *ctx, const int32_t *adapter_ids, int64_t T, int R, int
  * and out[t] = y[t] for a token without one.  Both factors are stored rank-major
  * (B is the transpose of an [N, r] up-projection), so a rank of any size keeps its
  * rows on 16 bytes.  v is fp32 and enters the second product as two bf16 parts
- * (its rounding error is below 2^-16); out is rounded once.
+ * (its rounding error is below 2^-16; an infinite v keeps its sign); out is rounded
+ * once.  An infinite element of B makes its column of out NaN or infinite: its
+ * products with the two parts may cancel.
  *   x bf16 [T,K], y bf16 [T,N] (NULL: 0) and out bf16 [T,N] with row strides; y may
  *   be out itself, at the same stride.  order, offsets: lora_plan's form (entries outside [0,T) are
  *   skipped).  A bf16 [R,r,K], B bf16 [R,r,N], scales fp32 [R], ranks int32 [R] (NULL:
@@ -520,7 +523,8 @@ int lora_apply(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, const int32
  * (the gradient of y is dy itself).  dx0 bf16 [T,K] (NULL: 0; may be dx itself) and
  * dx bf16 [T,K] with row strides; dA, dB bf16, of A's and B's shapes, overwritten:
  * 0 for an adapter without tokens and for rows past ranks[a].  Sums are fp32 in a
- * fixed order, rounded once.  dx lies apart from x, dy, A and B, and dA and dB apart from
+ * fixed order, rounded once.  w and v enter the second products as v does in
+ * lora_apply.  dx lies apart from x, dy, A and B, and dA and dB apart from
  * each other and from A and B: one is written while others are read.  GEMMAR_ERR_ARG where
  * dA or dB does not, or dx starts where x or dy does or, at the same stride, shares elements.
  * Other arguments and limits as lora_apply.
