@@ -90,6 +90,16 @@ GEMMAR_NOALLOC_MAX_PARTIALS = 8 * 1024 * 1024
 GEMMAR_NORM_MAX_N = 16384
 GEMMAR_LORA_MAX_ADAPTERS = 1024
 GEMMAR_LORA_MAX_RANK = 128
+GEMMAR_ACT_NONE = 0
+GEMMAR_ACT_RELU = 1
+GEMMAR_ACT_SILU = 2
+GEMMAR_ACT_GELU = 3
+GEMMAR_ACT_GELU_TANH = 4
+GEMMAR_SCORE_SOFTMAX = 0
+GEMMAR_SCORE_SIGMOID = 1
+GEMMAR_MOE_MAX_TOKENS = 128
+GEMMAR_MOE_MAX_EXPERTS = 1024
+GEMMAR_MOE_MAX_CHOSEN = 16
 
 # ---- signatures ----------------------------------------------------------------
 _P = ctypes.c_void_p
@@ -127,6 +137,10 @@ _SIGS = {
     "lora_apply": (_I, [_P, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _P, _I64, _P, _I64, _P, _P]),
     "lora_apply_bwd": (_I, [_P, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I,
                             _P, _I64, _P, _I64, _P, _P, _P]),
+    "gemm_blockscale_act": (_I, [_P, _P, _P, _P, _P, _I, _I, _P, _P, _I, _I64, _I64, _I64, _I64, _P, _I, _I64, _P, _P, _P, _P]),
+    "gemm_blockscale_act_bwd": (_I, [_P, _P, _I, _I64, _P, _I, _I, _I64, _I64, _P, _P, _P, _P, _P]),
+    "moe_route": (_I, [_P, _P, _I64, _P, _I, _P, _I64, _I64, _I, _I, _I, _I, _F, _P, _P, _P]),
+    "moe_apply": (_I, [_P, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I, _I, _P, _I64, _P, _I64, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -137,7 +151,8 @@ EXPORTED = tuple(_SIGS)
 
 if not isinstance(_operators, _NoBinding):
     _operators.bind(*(ctypes.cast(getattr(_lib, n), _P).value for n in
-                      ("norm_gate_residual", "norm_gate_residual_bwd", "lora_apply", "lora_apply_bwd")))
+                      ("norm_gate_residual", "norm_gate_residual_bwd", "lora_apply", "lora_apply_bwd", "gemm_blockscale_act",
+                       "gemm_blockscale_act_bwd", "moe_route", "moe_apply")))
 
 
 class GemmarError(RuntimeError):
@@ -526,6 +541,64 @@ def _explain_lora_apply_bwd(x, order, offsets, A, B, scales, ranks, dy, v, dx, d
         _dense(t, s, name, dtype)
 
 
+def _explain_gemm_blockscale_act(A, sa, B, sb, C, act, gated, bias, residual, q, scales, z):
+    M, K = _dims(A, "A", 2)
+    P = _dims(B, "B", 2)[0]
+    if gated and P % 2:
+        raise ValueError("B must have an even number of rows where the activation is gated")
+    N = P // 2 if gated else P
+    f32 = torch.float32
+    for t, s, name in ((A, (M, K), "A"), (B, (P, K), "B"), (q, (M, N), "q")):
+        _codes(t, s, name)
+    for t, s, name, dtype in ((sa, (M, K // 128), "sa", f32), (sb, (P // 128, K // 128), "sb", f32), (bias, (P,), "bias", f32),
+                              (scales, (M, N // 128), "scales", f32), (z, (M, P), "z", torch.bfloat16)):
+        _dense(t, s, name, dtype)
+    for t, name in ((C, "C"), (residual, "residual")):
+        if t is not None:
+            _dims(t, name, 2)
+            _xdtype(t, name)
+            _rows(t, (M, N), name)
+
+
+def _explain_gemm_blockscale_act_bwd(dout, z, dz, act, gated, dbias, q, scales):
+    M, N = _dims(dout, "dout", 2)
+    P = 2 * N if gated else N
+    _xdtype(dout, "dout")
+    _rows(dout, (M, N), "dout")
+    for t, s, name, dtype in ((z, (M, P), "z", torch.bfloat16), (dz, (M, P), "dz", torch.bfloat16), (dbias, (P,), "dbias", torch.float32),
+                              (scales, (M, P // 128), "scales", torch.float32)):
+        _dense(t, s, name, dtype)
+    _codes(q, (M, P), "q")
+
+
+def _explain_moe_route(x, router, ids, weights, bias):
+    T, H = _dims(x, "x", 2)
+    E = _dims(router, "router", 2)[0]
+    k = _dims(ids, "ids", 2)[1]
+    _xdtype(router, "router")
+    _rows(x, (T, H), "x", torch.bfloat16)
+    for t, s, name, dtype in ((router, (E, H), "router", router.dtype), (ids, (T, k), "ids", torch.int32), (weights, (T, k), "weights", torch.float32),
+                              (bias, (E,), "bias", torch.float32)):
+        _dense(t, s, name, dtype)
+
+
+def _explain_moe_apply(q, sx, ids, weights, w13, s13, w2, s2, out, place, y):
+    T, H = _dims(q, "q", 2)
+    k = _dims(ids, "ids", 2)[1]
+    E, _, inner = _dims(w2, "w2", 3)
+    f32, i32 = torch.float32, torch.int32
+    for t, s, name in ((q, (T, H), "q"), (w13, (E, 2 * inner, H), "w13"), (w2, (E, H, inner), "w2")):
+        _codes(t, s, name)
+    for t, s, name, dtype in ((sx, (T, H // 128), "sx", f32), (ids, (T, k), "ids", i32), (weights, (T, k), "weights", f32),
+                              (s13, (E, 2 * inner // 128, H // 128), "s13", f32), (s2, (E, H // 128, inner // 128), "s2", f32)):
+        _dense(t, s, name, dtype)
+    if place is not None:
+        _dense(place, _dims(place, "place", 1), "place", i32)
+    _rows(out, (T, H), "out", torch.bfloat16)
+    if y is not None:
+        _rows(y, (T, H), "y", torch.bfloat16)
+
+
 def norm_gate_residual(ctx: Context, y, h, w_pre, t, w_post=None, gate=None, alpha: float = 1.0, beta: float = 1.0,
                        eps: float = 1e-6, u=None, q=None, scales=None, rstd=None, stream=None) -> None:
     """t = alpha*h + beta*gate*norm(y)*w_post and the next block's input norm(t)*w_pre, as bf16 rows u
@@ -587,3 +660,57 @@ def lora_apply_bwd(ctx: Context, x, dy, order, offsets, A, B, scales, ranks, v, 
         raise ValueError("lora_apply_bwd: an argument does not fit")
     if rc:
         _check(rc, "lora_apply_bwd")
+
+
+# ---- the feed-forward half -------------------------------------------------------------
+
+def gemm_blockscale_act(ctx: Context, A, sa, B, sb, C, act: int = GEMMAR_ACT_NONE, gated: bool = False, bias=None,
+                        residual=None, q=None, scales=None, z=None, stream=None) -> None:
+    """out = residual + act(z), z = A B^T + bias of block-scaled e4m3 codes; gated: B holds 2N rows and out =
+    residual + act(z[:, :N]) * z[:, N:].  out goes to C (bf16 or fp32, may be a view, may be residual itself;
+    None: left out) and/or to e4m3 codes q with scales [M, N/128]; z bf16 is kept for the backward pass."""
+    rc = _operators.gemm_blockscale_act(ctx.handle.value, A, sa, B, sb, C, act, gated, bias, residual, q, scales, z,
+                                        _stream(stream))
+    if rc < 0:
+        _explain_gemm_blockscale_act(A, sa, B, sb, C, act, gated, bias, residual, q, scales, z)
+        raise ValueError("gemm_blockscale_act: an argument does not fit")
+    if rc:
+        _check(rc, "gemm_blockscale_act")
+
+
+def gemm_blockscale_act_bwd(ctx: Context, dout, z, dz, act: int = GEMMAR_ACT_NONE, gated: bool = False, dbias=None,
+                            q=None, scales=None, stream=None) -> None:
+    """dz = the gradient of z from dout, as bf16 rows (None: left out) and/or e4m3 codes q with 1x128 scales;
+    dbias fp32 [N or 2N] its sums over the rows.  A's gradient is gemm_blockscale_fp8 of those codes with B's
+    codes and scales transposed; residual's is dout."""
+    rc = _operators.gemm_blockscale_act_bwd(ctx.handle.value, dout, z, dz, act, gated, dbias, q, scales, _stream(stream))
+    if rc < 0:
+        _explain_gemm_blockscale_act_bwd(dout, z, dz, act, gated, dbias, q, scales)
+        raise ValueError("gemm_blockscale_act_bwd: an argument does not fit")
+    if rc:
+        _check(rc, "gemm_blockscale_act_bwd")
+
+
+def moe_route(ctx: Context, x, router, ids, weights, bias=None, score: int = GEMMAR_SCORE_SOFTMAX, renorm: bool = True,
+              factor: float = 1.0, stream=None) -> None:
+    """Each token's k experts: ids int32 [T, k] of the largest softmax or sigmoid scores of x router^T (+ bias, for
+    the choice alone) and their weights fp32 [T, k], over their sum where renorm, times factor."""
+    rc = _operators.moe_route(ctx.handle.value, x, router, ids, weights, bias, score, renorm, factor, _stream(stream))
+    if rc < 0:
+        _explain_moe_route(x, router, ids, weights, bias)
+        raise ValueError("moe_route: an argument does not fit")
+    if rc:
+        _check(rc, "moe_route")
+
+
+def moe_apply(ctx: Context, q, sx, ids, weights, w13, s13, w2, s2, out, act: int = GEMMAR_ACT_SILU, place=None, y=None,
+              stream=None) -> None:
+    """out = y + each token's experts applied to its codes q, sx: weights * w2[e] (act(gate) * up) with gate and up the
+    halves of w13[e].  ids outside the experts add nothing; place int32 maps the router's numbers to rows of w13 and
+    w2 (-1: held elsewhere).  y None: zero; y may be out."""
+    rc = _operators.moe_apply(ctx.handle.value, q, sx, ids, weights, w13, s13, w2, s2, out, act, place, y, _stream(stream))
+    if rc < 0:
+        _explain_moe_apply(q, sx, ids, weights, w13, s13, w2, s2, out, place, y)
+        raise ValueError("moe_apply: an argument does not fit")
+    if rc:
+        _check(rc, "moe_apply")

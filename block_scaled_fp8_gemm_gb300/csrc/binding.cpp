@@ -18,6 +18,10 @@ decltype(&norm_gate_residual) p_norm = nullptr;
 decltype(&norm_gate_residual_bwd) p_norm_bwd = nullptr;
 decltype(&lora_apply) p_lora = nullptr;
 decltype(&lora_apply_bwd) p_lora_bwd = nullptr;
+decltype(&gemm_blockscale_act) p_act = nullptr;
+decltype(&gemm_blockscale_act_bwd) p_act_bwd = nullptr;
+decltype(&moe_route) p_route = nullptr;
+decltype(&moe_apply) p_moe = nullptr;
 
 constexpr at::ScalarType kF32 = at::ScalarType::Float, kBf16 = at::ScalarType::BFloat16, kI32 = at::ScalarType::Int,
                          kU8 = at::ScalarType::Byte, kE4m3 = at::ScalarType::Float8_e4m3fn;
@@ -36,6 +40,13 @@ struct Args {
         return &THPVariable_Unpack(o);
     }
     void *pointer(PyObject *o) { return o == Py_None ? nullptr : PyLong_AsVoidPtr(o); }
+    int whole(PyObject *o)
+    {
+        const long v = PyLong_AsLong(o);
+        ok = ok && v >= INT32_MIN && v <= INT32_MAX;
+        return (int)v;
+    }
+    bool truth(PyObject *o) { return PyObject_IsTrue(o) > 0; }
     float real(PyObject *o)
     {
         const double v = PyFloat_AsDouble(o);
@@ -251,11 +262,143 @@ PyObject *lora_bwd(PyObject *, PyObject *const *v, Py_ssize_t n)
     });
 }
 
+// handle, A, sa, B, sb, C, act, gated, bias, residual, q, scales, z, stream
+PyObject *gemm_act(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    if (!count(n, 14))
+        return nullptr;
+    Args a{v};
+    int64_t M = 0, K = 0, P = 0, K2 = 0, rs = 0, cs = 0;
+    const int act = a.whole(v[6]);
+    const bool gated = a.truth(v[7]);
+    if (!a.shape2(v[1], M, K) || !a.shape2(v[3], P, K2) || (gated && P % 2 != 0))
+        return refused();
+    const int64_t N = gated ? P / 2 : P;
+    const uint8_t *A = a.dense<uint8_t>(v[1], {M, K}, kU8, kE4m3), *B = a.dense<uint8_t>(v[3], {P, K}, kU8, kE4m3);
+    const float *sa = a.dense<float>(v[2], {M, K / 128}, kF32), *sb = a.dense<float>(v[4], {P / 128, K / 128}, kF32);
+    at::ScalarType ct = kF32, rt = kF32;
+    void *C = nullptr, *res = nullptr;
+    if (v[5] != Py_None) {
+        ct = a.real_type(v[5]);
+        C = a.rows<void>(v[5], M, N, ct, cs);
+    }
+    if (v[9] != Py_None) {
+        rt = a.real_type(v[9]);
+        res = a.rows<void>(v[9], M, N, rt, rs);
+    }
+    const float *bias = a.dense<float>(v[8], {P}, kF32);
+    uint8_t *q = a.dense<uint8_t>(v[10], {M, N}, kU8, kE4m3);
+    float *scales = a.dense<float>(v[11], {M, N / 128}, kF32);
+    uint16_t *z = a.dense<uint16_t>(v[12], {M, P}, kBf16);
+    void *ctx = a.pointer(v[0]), *stream = a.pointer(v[13]);
+    if (!a.ok || PyErr_Occurred())
+        return refused();
+    return status([&] {
+        return p_act(static_cast<gemmar_ctx *>(ctx), A, sa, B, sb, act, gated, bias, res, code(rt), rs, M, N, K, C, code(ct),
+                     cs, q, scales, z, stream);
+    });
+}
+
+// handle, dout, z, dz, act, gated, dbias, q, scales, stream
+PyObject *gemm_act_bwd(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    if (!count(n, 10))
+        return nullptr;
+    Args a{v};
+    int64_t M = 0, N = 0, ds = 0;
+    const int act = a.whole(v[4]);
+    const bool gated = a.truth(v[5]);
+    if (!a.shape2(v[1], M, N))
+        return refused();
+    const int64_t P = gated ? 2 * N : N;
+    const at::ScalarType dt = a.real_type(v[1]);
+    const void *dout = a.rows<void>(v[1], M, N, dt, ds);
+    const uint16_t *z = a.dense<uint16_t>(v[2], {M, P}, kBf16);
+    uint16_t *dz = a.dense<uint16_t>(v[3], {M, P}, kBf16);
+    float *dbias = a.dense<float>(v[6], {P}, kF32), *scales = a.dense<float>(v[8], {M, P / 128}, kF32);
+    uint8_t *q = a.dense<uint8_t>(v[7], {M, P}, kU8, kE4m3);
+    void *ctx = a.pointer(v[0]), *stream = a.pointer(v[9]);
+    if (!a.ok || PyErr_Occurred())
+        return refused();
+    return status([&] {
+        return p_act_bwd(static_cast<gemmar_ctx *>(ctx), dout, code(dt), ds, z, act, gated, M, N, dz, dbias, q, scales,
+                         stream);
+    });
+}
+
+// handle, x, router, ids, weights, bias, score, renorm, factor, stream
+PyObject *route(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    if (!count(n, 10))
+        return nullptr;
+    Args a{v};
+    int64_t T = 0, H = 0, E = 0, H2 = 0, T2 = 0, k = 0, xs = 0;
+    const int score = a.whole(v[6]);
+    const bool renorm = a.truth(v[7]);
+    if (!a.shape2(v[1], T, H) || !a.shape2(v[2], E, H2) || !a.shape2(v[3], T2, k) || E > INT32_MAX || k > INT32_MAX)
+        return refused();
+    const uint16_t *x = a.rows<uint16_t>(v[1], T, H, kBf16, xs);
+    const at::ScalarType wt = a.real_type(v[2]);
+    const void *w = a.dense<void>(v[2], {E, H}, wt);
+    int32_t *ids = a.dense<int32_t>(v[3], {T, k}, kI32);
+    float *weights = a.dense<float>(v[4], {T, k}, kF32);
+    const float *bias = a.dense<float>(v[5], {E}, kF32);
+    const float factor = a.real(v[8]);
+    void *ctx = a.pointer(v[0]), *stream = a.pointer(v[9]);
+    if (!a.ok || PyErr_Occurred())
+        return refused();
+    return status([&] {
+        return p_route(static_cast<gemmar_ctx *>(ctx), x, xs, w, code(wt), bias, T, H, (int)E, (int)k, score, renorm, factor,
+                       ids, weights, stream);
+    });
+}
+
+// handle, q, sx, ids, weights, w13, s13, w2, s2, out, act, place, y, stream
+PyObject *moe(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    if (!count(n, 14))
+        return nullptr;
+    Args a{v};
+    int64_t T = 0, H = 0, T2 = 0, k = 0, os = 0, ys = 0, places = 0;
+    const int act = a.whole(v[10]);
+    const at::Tensor *t2 = a.tensor(v[7]);
+    if (!a.shape2(v[1], T, H) || !a.shape2(v[3], T2, k) || !t2 || t2->dim() != 3 || k > INT32_MAX ||
+        t2->size(0) > INT32_MAX)
+        return refused();
+    const int64_t E = t2->size(0), I = t2->size(2);
+    const uint8_t *q = a.dense<uint8_t>(v[1], {T, H}, kU8, kE4m3);
+    const float *sx = a.dense<float>(v[2], {T, H / 128}, kF32);
+    const int32_t *ids = a.dense<int32_t>(v[3], {T, k}, kI32);
+    const float *weights = a.dense<float>(v[4], {T, k}, kF32);
+    const uint8_t *w13 = a.dense<uint8_t>(v[5], {E, 2 * I, H}, kU8, kE4m3), *w2 = a.dense<uint8_t>(v[7], {E, H, I}, kU8, kE4m3);
+    const float *s13 = a.dense<float>(v[6], {E, 2 * I / 128, H / 128}, kF32);
+    const float *s2 = a.dense<float>(v[8], {E, H / 128, I / 128}, kF32);
+    uint16_t *out = a.rows<uint16_t>(v[9], T, H, kBf16, os);
+    const int32_t *place = nullptr;
+    if (v[11] != Py_None) {
+        const at::Tensor *p = a.tensor(v[11]);
+        places = p && p->dim() == 1 ? p->size(0) : 0;
+        place = a.dense<int32_t>(v[11], {places}, kI32);
+    }
+    const uint16_t *y = v[12] == Py_None ? nullptr : a.rows<uint16_t>(v[12], T, H, kBf16, ys);
+    void *ctx = a.pointer(v[0]), *stream = a.pointer(v[13]);
+    if (!a.ok || PyErr_Occurred())
+        return refused();
+    return status([&] {
+        return p_moe(static_cast<gemmar_ctx *>(ctx), q, sx, ids, weights, place, places, w13, s13, w2, s2, act, T, H, I,
+                     (int)E, (int)k, y, ys, out, os, stream);
+    });
+}
+
 // The addresses of the library's entry points, in this order.
 PyObject *bind(PyObject *, PyObject *const *v, Py_ssize_t n)
 {
-    if (!count(n, 4))
+    if (!count(n, 8))
         return nullptr;
+    p_act = reinterpret_cast<decltype(p_act)>(PyLong_AsVoidPtr(v[4]));
+    p_act_bwd = reinterpret_cast<decltype(p_act_bwd)>(PyLong_AsVoidPtr(v[5]));
+    p_route = reinterpret_cast<decltype(p_route)>(PyLong_AsVoidPtr(v[6]));
+    p_moe = reinterpret_cast<decltype(p_moe)>(PyLong_AsVoidPtr(v[7]));
     p_norm = reinterpret_cast<decltype(p_norm)>(PyLong_AsVoidPtr(v[0]));
     p_norm_bwd = reinterpret_cast<decltype(p_norm_bwd)>(PyLong_AsVoidPtr(v[1]));
     p_lora = reinterpret_cast<decltype(p_lora)>(PyLong_AsVoidPtr(v[2]));
@@ -284,7 +427,9 @@ PyMethodDef method(const char *name)
 }
 
 PyMethodDef g_methods[] = {method<norm>("norm_gate_residual"), method<norm_bwd>("norm_gate_residual_bwd"),
-                           method<lora>("lora_apply"), method<lora_bwd>("lora_apply_bwd"), method<bind>("bind"),
+                           method<lora>("lora_apply"), method<lora_bwd>("lora_apply_bwd"),
+                           method<gemm_act>("gemm_blockscale_act"), method<gemm_act_bwd>("gemm_blockscale_act_bwd"),
+                           method<route>("moe_route"), method<moe>("moe_apply"), method<bind>("bind"),
                            {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_operators", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -38,6 +38,7 @@ struct gemmar_ctx {
     int64_t sfb_bytes = 0;
     uint8_t *wire_q = nullptr;        // fp8-wire codes, max_M * N
     float *wire_s = nullptr;          // fp8-wire row scales, max_M
+    uint32_t *counters = nullptr;     // kCounters arrival counters, zero between calls
     int disabled = 0;
     int64_t total_bytes = 0;
     // the last fused band-path call, for gemmar_overlap_stats
@@ -74,6 +75,7 @@ cudaError_t ensure_dynamic_smem(const void *kernel, int bytes)
 namespace {
 
 constexpr int kMaxTimedCalls = 65536;
+constexpr int kCounters = 1024;
 constexpr int kEventsPerCall = GEMMAR_NUM_PHASES + 1;
 
 // Event marking the start of phase `ph` (ph == GEMMAR_NUM_PHASES: the end) of
@@ -364,6 +366,7 @@ GEMMAR_API int gemmar_destroy(gemmar_ctx *ctx)
     cudaFree(ctx->sfb);
     cudaFree(ctx->wire_q);
     cudaFree(ctx->wire_s);
+    cudaFree(ctx->counters);
     for (cudaEvent_t e : ctx->events)
         cudaEventDestroy(e);
     if (prev >= 0)
@@ -804,6 +807,133 @@ GEMMAR_API int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stri
     return GEMMAR_OK;
 }
 
+// ---------------------------------------------------------------- feed-forward half
+
+namespace {
+
+bool known_act(int act) { return act >= GEMMAR_ACT_NONE && act <= GEMMAR_ACT_GELU_TANH; }
+
+int elem_bytes(int dtype) { return dtype == GEMMAR_DTYPE_BF16 ? 2 : 4; }
+
+}  // namespace
+
+GEMMAR_API int gemm_blockscale_act(gemmar_ctx *ctx, const uint8_t *A, const float *sa, const uint8_t *B, const float *sb,
+                                   int act, int gated, const float *bias, const void *residual, int r_dtype,
+                                   int64_t r_stride, int64_t M, int64_t N, int64_t K, void *C, int c_dtype,
+                                   int64_t c_stride, uint8_t *q, float *scales, uint16_t *z, void *stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc)
+        return rc;
+    if (!A || !sa || !B || !sb || (!C && !q) || (!q) != (!scales) || !known_act(act) || (gated != 0 && gated != 1) ||
+        (residual && !known_dtype(r_dtype)) || (C && !known_dtype(c_dtype)) ||
+        (C && residual == C && (r_dtype != c_dtype || r_stride != c_stride)))
+        return GEMMAR_ERR_ARG;
+    if (N > 65536 || (rc = shape_rules(1, M, gated ? 2 * N : N, K, 1, GEMMAR_SCALE_BLOCK128)))
+        return N > 65536 ? GEMMAR_ERR_SHAPE : rc;
+    if (N % 128 != 0)
+        return GEMMAR_ERR_SHAPE;
+    if ((residual && (rc = check_rows(residual, r_stride, N, elem_bytes(r_dtype)))) ||
+        (C && (rc = check_rows(C, c_stride, N, elem_bytes(c_dtype), true))))
+        return rc;
+    if (!aligned16(A) || !aligned16(B) || !aligned16(sa) || !aligned16(sb) || !aligned16(bias) || !aligned16(q) ||
+        !aligned16(scales) || !aligned16(z))
+        return GEMMAR_ERR_ALIGN;
+    if (!load_encode())
+        return GEMMAR_ERR_CUDA;
+    if (!gemm_act_split_ok())
+        return GEMMAR_ERR_DEVICE;
+    ActParams p;
+    std::memset(&p, 0, sizeof(p));
+    if (!make_tmap_u8(&p.tmA, A, M, K, 128) || !make_tmap_u8(&p.tmB, B, gated ? 2 * N : N, K, 128))
+        return GEMMAR_ERR_CUDA;
+    p.sa = sa;
+    p.sb = sb;
+    p.e = ActEpilogue{act, gated, (int)M, (int)N, (int)K, bias, residual, r_dtype == GEMMAR_DTYPE_BF16, r_stride,
+                      C, c_dtype == GEMMAR_DTYPE_BF16, c_stride, q, scales, z};
+    p.status = ctx->status;
+    p.timeout_ns = ctx->timeout_ns;
+    CUDA_OK(launch_gemm_act(p, ctx->num_sms, as_stream(stream)));
+    return GEMMAR_OK;
+}
+
+GEMMAR_API int gemm_blockscale_act_bwd(gemmar_ctx *ctx, const void *dout, int d_dtype, int64_t d_stride,
+                                       const uint16_t *z, int act, int gated, int64_t M, int64_t N, uint16_t *dz,
+                                       float *dbias, uint8_t *q, float *scales, void *stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc)
+        return rc;
+    if (!dout || !z || (!dz && !q) || (!q) != (!scales) || !known_act(act) || (gated != 0 && gated != 1) ||
+        !known_dtype(d_dtype) ||
+        (dz && dz == dout && (gated || d_dtype != GEMMAR_DTYPE_BF16 || d_stride != N)))
+        return GEMMAR_ERR_ARG;
+    if (M < 1 || N < 1)
+        return GEMMAR_ERR_ARG;
+    if (N % 128 != 0 || N > (gated ? 32768 : 65536) || M > (int64_t(1) << 24))
+        return GEMMAR_ERR_SHAPE;
+    if ((rc = check_rows(dout, d_stride, N, elem_bytes(d_dtype))))
+        return rc;
+    if (!aligned16(z) || !aligned16(dz) || !aligned16(dbias) || !aligned16(q) || !aligned16(scales))
+        return GEMMAR_ERR_ALIGN;
+    if (dbias && act_bwd_ws_floats(M, (int)N, gated, ctx->num_sms) > ctx->W_floats)
+        return GEMMAR_ERR_WORKSPACE;
+    const ActBwdArgs a{dout, d_dtype == GEMMAR_DTYPE_BF16, d_stride, z, act, gated, M, (int)N, dz, dbias, q, scales};
+    CUDA_OK(launch_act_bwd(a, ctx->W, ctx->num_sms, as_stream(stream)));
+    return GEMMAR_OK;
+}
+
+GEMMAR_API int moe_route(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, const void *w, int w_dtype,
+                         const float *bias, int64_t T, int64_t H, int E, int k, int score, int renorm, float factor,
+                         int32_t *ids, float *weights, void *stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc)
+        return rc;
+    if (!x || !w || !ids || !weights || !known_dtype(w_dtype) || T < 1 || H < 1 || E < 1 || k < 1 || k > E ||
+        (score != GEMMAR_SCORE_SOFTMAX && score != GEMMAR_SCORE_SIGMOID) || !std::isfinite(factor))
+        return GEMMAR_ERR_ARG;
+    if (T > GEMMAR_MOE_MAX_TOKENS || E > GEMMAR_MOE_MAX_EXPERTS || k > GEMMAR_MOE_MAX_CHOSEN || H % 8 != 0 || H > 65536)
+        return GEMMAR_ERR_SHAPE;
+    if ((rc = check_rows(x, x_stride, H, 2)))
+        return rc;
+    if (!aligned16(w) || !aligned16(bias) || !aligned16(ids) || !aligned16(weights))
+        return GEMMAR_ERR_ALIGN;
+    const RouteArgs a{x, x_stride, w, w_dtype == GEMMAR_DTYPE_BF16, bias, (int)T, (int)H, E, k, score, renorm != 0, factor,
+                      ids, weights};
+    if (route_ws_floats(a) > ctx->W_floats)
+        return GEMMAR_ERR_WORKSPACE;
+    CUDA_OK(launch_route(a, ctx->W, ctx->counters, as_stream(stream)));
+    return GEMMAR_OK;
+}
+
+GEMMAR_API int moe_apply(gemmar_ctx *ctx, const uint8_t *xq, const float *xs, const int32_t *ids, const float *weights,
+                         const int32_t *place, int64_t places, const uint8_t *w13, const float *s13, const uint8_t *w2,
+                         const float *s2, int act, int64_t T, int64_t H, int64_t I, int E, int k, const uint16_t *y,
+                         int64_t y_stride, uint16_t *out, int64_t out_stride, void *stream)
+{
+    int rc = check_ctx(ctx);
+    if (rc)
+        return rc;
+    if (!xq || !xs || !ids || !weights || !w13 || !s13 || !w2 || !s2 || !out || !known_act(act) || T < 1 || H < 1 ||
+        I < 1 || E < 1 || k < 1 || (place && (places < 1 || places > INT32_MAX)) || (y == out && y_stride != out_stride))
+        return GEMMAR_ERR_ARG;
+    if (T > GEMMAR_MOE_MAX_TOKENS || E > GEMMAR_MOE_MAX_EXPERTS || k > GEMMAR_MOE_MAX_CHOSEN || H % 128 != 0 ||
+        I % 128 != 0 || H > 65536 || I > 32768)
+        return GEMMAR_ERR_SHAPE;
+    if ((y && (rc = check_rows(y, y_stride, H, 2))) || (rc = check_rows(out, out_stride, H, 2, true)))
+        return rc;
+    if (!aligned16(xq) || !aligned16(xs) || !aligned16(ids) || !aligned16(weights) || !aligned16(place) ||
+        !aligned16(w13) || !aligned16(s13) || !aligned16(w2) || !aligned16(s2))
+        return GEMMAR_ERR_ALIGN;
+    const MoeArgs a{xq, xs, ids, place, (int)(place ? places : 0), weights, w13, w2, s13, s2, (int)T, (int)H, (int)I, E, k,
+                    act, y, y_stride, out, out_stride};
+    if (moe_ws_floats(a) > ctx->W_floats)
+        return GEMMAR_ERR_WORKSPACE;
+    CUDA_OK(launch_moe(a, ctx->W, as_stream(stream)));
+    return GEMMAR_OK;
+}
+
 // ---------------------------------------------------------------- create + self-test
 
 namespace {
@@ -935,7 +1065,9 @@ GEMMAR_API int gemmar_create(gemmar_ctx **out, int device, int64_t max_M, int64_
     alloc(reinterpret_cast<void **>(&ctx->sfb), (size_t)ctx->sfb_bytes);
     alloc(reinterpret_cast<void **>(&ctx->wire_q), (size_t)(max_M * N));
     alloc(reinterpret_cast<void **>(&ctx->wire_s), sizeof(float) * (size_t)max_M);
-    if (rc == GEMMAR_OK && cudaMemset(ctx->status, 0, sizeof(ptx::DevStatus)) != cudaSuccess)
+    alloc(reinterpret_cast<void **>(&ctx->counters), sizeof(uint32_t) * kCounters);
+    if (rc == GEMMAR_OK && (cudaMemset(ctx->status, 0, sizeof(ptx::DevStatus)) != cudaSuccess ||
+                            cudaMemset(ctx->counters, 0, sizeof(uint32_t) * kCounters) != cudaSuccess))
         rc = GEMMAR_ERR_CUDA;
     if (rc == GEMMAR_OK && !register_split_ok(256))
         rc = GEMMAR_ERR_DEVICE;

@@ -220,4 +220,80 @@ cudaError_t launch_lora_apply_bwd(const LoraArgs &l, const LoraCall &p, const ui
                                   const uint16_t *dx0, int64_t dx0s, uint16_t *dx, int64_t dxs, uint16_t *dA, uint16_t *dB,
                                   float *ws, int64_t ws_floats, cudaStream_t st);
 
+// What follows a block-scaled product (gemm_blockscale_act): N output columns, of 2 N of
+// the product where it is gated.  Strides in elements.
+struct ActEpilogue {
+    int act, gated;
+    int M, N, K;
+    const float *bias;         // [N or 2N], nullptr: none
+    const void *res;           // [M,N], nullptr: none
+    int r_bf16;
+    int64_t rs;
+    void *C;                   // [M,N], nullptr: codes only
+    int c_bf16;
+    int64_t cs;
+    uint8_t *q;                // [M,N] with scales [M,N/128], nullptr: none
+    float *scales;
+    uint16_t *z;               // bf16 [M, N or 2N], nullptr: not kept
+};
+struct ActParams {
+    CUtensorMap tmA;           // dims {K, M}, box {128, 128}
+    CUtensorMap tmB;           // dims {K, N or 2N}, box {128, 128}
+    const float *sa, *sb;
+    ActEpilogue e;
+    ptx::DevStatus *status;
+    uint64_t timeout_ns;
+};
+bool gemm_act_split_ok();
+cudaError_t launch_gemm_act(const ActParams &p, int num_sms, cudaStream_t st);
+
+// Its backward pass (act_bwd.cu): dz from dout, with codes and column sums.
+struct ActBwdArgs {
+    const void *dout;
+    int d_bf16;
+    int64_t ds;
+    const uint16_t *z;
+    int act, gated;
+    int64_t M;
+    int N;
+    uint16_t *dz;              // bf16 [M, N or 2N], nullptr: codes only
+    float *dbias;
+    uint8_t *q;
+    float *scales;
+};
+int64_t act_bwd_ws_floats(int64_t M, int N, int gated, int num_sms);
+cudaError_t launch_act_bwd(const ActBwdArgs &a, float *ws, int num_sms, cudaStream_t st);
+
+// The experts' layer of a few tokens (moe.cu).
+struct RouteArgs {
+    const uint16_t *x;
+    int64_t xs;
+    const void *w;             // [E,H]
+    int w_bf16;
+    const float *bias;
+    int T, H, E, k;
+    int score, renorm;
+    float factor;
+    int32_t *ids;
+    float *weights;
+};
+struct MoeArgs {
+    const uint8_t *q;          // [T,H] with scales [T,H/128]
+    const float *sx;
+    const int32_t *ids, *place;
+    int places;
+    const float *weights;
+    const uint8_t *w13, *w2;   // [E,2I,H], [E,H,I]
+    const float *s13, *s2;
+    int T, H, I, E, k, act;
+    const uint16_t *y;
+    int64_t ys;
+    uint16_t *out;
+    int64_t os;
+};
+int64_t route_ws_floats(const RouteArgs &a);
+cudaError_t launch_route(const RouteArgs &a, float *ws, uint32_t *counters, cudaStream_t st);
+int64_t moe_ws_floats(const MoeArgs &a);
+cudaError_t launch_moe(const MoeArgs &a, float *ws, cudaStream_t st);
+
 }  // namespace gemmar

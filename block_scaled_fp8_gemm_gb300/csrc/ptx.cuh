@@ -104,6 +104,7 @@ enum WaitSite : int {
     SITE_PARK_FULL = 8,    // a store warp waiting for its epilogue warp's parked partial
     SITE_PARK_EMPTY = 9,   // an epilogue warp waiting for its park to be copied out
     SITE_LORA_MMA = 10,    // an adapter kernel waiting for its MMAs
+    SITE_ROW_MAX = 11,     // the two halves of a gated row, for the maximum of its group
 };
 
 constexpr int kErrTimeout = 6;   // == GEMMAR_ERR_TIMEOUT
@@ -134,6 +135,29 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
             *abort = 1;
             report(st, kErrTimeout, site);
             return false;
+        }
+    }
+}
+
+// A CTA that is giving up lets the loads it has issued (`issued` so far, one phase of full[i % stages]
+// each) land before its shared memory is released.
+__device__ __forceinline__ void drain_loads(uint64_t *full, int stages, int issued, uint64_t timeout_ns)
+{
+    for (int j = issued > stages ? issued - stages : 0; j < issued; ++j) {
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(full + j % stages, (uint32_t)((j / stages) & 1)) && globaltimer() - t0 < timeout_ns) {
+        }
+    }
+}
+
+// The MMA warp's last wait: everything it committed has completed before TMEM is released.
+__device__ __forceinline__ void wait_teardown(uint64_t *bar, DevStatus *st, uint64_t timeout_ns)
+{
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(bar, 0)) {
+        if (globaltimer() - t0 > timeout_ns) {
+            report(st, kErrTimeout, SITE_TEARDOWN_MMA);
+            break;
         }
     }
 }

@@ -535,6 +535,107 @@ int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, const u
                    int64_t T, int64_t K, int64_t N, int R, int r, const uint16_t *dx0, int64_t dx0_stride,
                    uint16_t *dx, int64_t dx_stride, uint16_t *dA, uint16_t *dB, void *stream);
 
+/*
+ * ---- The feed-forward half ----------------------------------------------------
+ *
+ * What the residual stream's codes go through next: block-scaled products with an
+ * activation behind them, or the experts' layer.  Weights are e4m3 codes with 128x128
+ * scales as in gemm_blockscale_fp8, activations e4m3 codes with 1x128 scales as
+ * norm_gate_residual and quant_blockscale_e4m3 write them.  Strides, alignment, workspace
+ * and stream order as for the operators above.
+ */
+
+/* Activations: none, max(z, 0), z / (1 + e^-z), z Phi(z), and the latter's tanh form
+ * 0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))). */
+enum { GEMMAR_ACT_NONE = 0, GEMMAR_ACT_RELU = 1, GEMMAR_ACT_SILU = 2, GEMMAR_ACT_GELU = 3, GEMMAR_ACT_GELU_TANH = 4 };
+
+/*
+ * gemm_blockscale_act -- a block-scaled product and what follows it, in one launch:
+ *   z   = A B^T + bias                                       (bias NULL: 0)
+ *   out = residual + act(z)                                  (residual NULL: 0)
+ *   gated: B holds 2N rows, z = [z_g, z_u] of N columns each,
+ *   out = residual + act(z_g) * z_u
+ * The product accumulates as gemm_blockscale_fp8; everything after it is fp32 and each
+ * output is rounded once, from the fp32 value: out as C (bf16 or fp32), and/or as e4m3 codes
+ * q with scales [M, N/128] by the rule of quant_blockscale_e4m3 (the A operand of the next
+ * product); z as bf16 for the backward pass.  Rows are independent.
+ *   A e4m3 [M,K], sa fp32 [M,K/128]; B e4m3 [N,K] or [2N,K], sb fp32 [N/128 or 2N/128, K/128];
+ *   bias fp32 [N or 2N]; residual [M,N] of r_dtype with a row stride (0: one row for all);
+ *   C [M,N] of c_dtype with a row stride; z bf16 [M, N or 2N].  C or q may be NULL (not both),
+ *   z NULL leaves it out; q and scales go together.  residual may be C itself, at the same
+ *   type and stride; otherwise outputs lie apart from the inputs and from each other.
+ * N % 128 == 0, K % 128 == 0, N (2N where gated) and K <= 65536, M <= 2^24.
+ */
+int gemm_blockscale_act(gemmar_ctx *ctx, const uint8_t *A, const float *sa, const uint8_t *B, const float *sb,
+                        int act, int gated, const float *bias, const void *residual, int r_dtype, int64_t r_stride,
+                        int64_t M, int64_t N, int64_t K, void *C, int c_dtype, int64_t c_stride,
+                        uint8_t *q, float *scales, uint16_t *z, void *stream);
+
+/*
+ * gemm_blockscale_act_bwd -- gradients of what follows the product, from dout (of out) and the
+ * forward pass's z:
+ *   dz    = dout act'(z);   gated: dz = [dout z_u act'(z_g), dout act(z_g)]
+ *   dbias = sum_rows dz     (the gradient of residual is dout itself)
+ * The weights are codes and have no gradient.  A's is dz B, a product that
+ * gemm_blockscale_fp8 does: with dz's codes and the codes of B transposed, whose 128x128
+ * scales transpose with them.  dz also is the dy of the adapters beside the product.
+ *   dout [M,N] of d_dtype with a row stride; z bf16 [M, N or 2N]; dz bf16 of z's shape and/or
+ *   codes q with scales [M, N/128 or 2N/128] of the fp32 dz (one of the two may be NULL);
+ *   dbias fp32 [N or 2N], overwritten, or NULL.  dz may be z itself, and dout itself where it
+ *   is contiguous bf16 and not gated.  Where act has a corner (relu at 0) its slope is 0.
+ * The sums over rows run in fp32 in an order fixed by M, N and the GPU.
+ * N % 128 == 0, N (2N) <= 65536, M <= 2^24.  Scratch: (M / 16 + 1) N' floats at most (N' = N or
+ * 2N), and less than 1250 + N' / 512 rows of N' floats.
+ */
+int gemm_blockscale_act_bwd(gemmar_ctx *ctx, const void *dout, int d_dtype, int64_t d_stride, const uint16_t *z,
+                            int act, int gated, int64_t M, int64_t N, uint16_t *dz, float *dbias,
+                            uint8_t *q, float *scales, void *stream);
+
+/* Limits of the experts' layer: tokens and experts of a call, and experts of a token. */
+#define GEMMAR_MOE_MAX_TOKENS 128
+#define GEMMAR_MOE_MAX_EXPERTS 1024
+#define GEMMAR_MOE_MAX_CHOSEN 16
+
+/* Scores of the router: softmax over a token's E logits, or the sigmoid of each. */
+enum { GEMMAR_SCORE_SOFTMAX = 0, GEMMAR_SCORE_SIGMOID = 1 };
+
+/*
+ * moe_route -- the experts of each token:
+ *   l[t,e] = sum_h x[t,h] w[e,h],   p = softmax_e(l) or sigmoid(l)
+ *   ids[t,:] = the k experts with the largest p + bias, in that order; of equal ones the lowest
+ *   weights  = p of the chosen (without bias), over their sum where renorm, times factor
+ * An expert whose p + bias is NaN or -inf is not chosen (a bias of -inf takes one out); where
+ * fewer than k are left, id -1 with weight 0 fills up.  Scores are fp32; where two are too
+ * near to be told apart in fp32, the order is decided in 64 bits.
+ *   x bf16 [T,H] with a row stride; w [E,H] of w_dtype, bias fp32 [E] or NULL; ids int32 [T,k];
+ *   weights fp32 [T,k].  H % 8 == 0, H <= 65536, T, E and k within the limits above, k <= E.
+ * Scratch: T E floats.
+ */
+int moe_route(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, const void *w, int w_dtype, const float *bias,
+              int64_t T, int64_t H, int E, int k, int score, int renorm, float factor, int32_t *ids, float *weights,
+              void *stream);
+
+/*
+ * moe_apply -- the experts' layer for a few tokens:
+ *   out[t] = y[t] + sum_s weights[t,s] W2[e] (act(G[e] x[t]) * (U[e] x[t])),   e = ids[t,s]
+ * with G[e] the first I rows of w13[e] and U[e] its last I.  An id outside the experts (-1: none)
+ * adds nothing.  place, where given, maps the router's expert numbers to this GPU's rows of w13
+ * and w2 (an id outside [0, places) is none): the experts held elsewhere are -1, and y carries
+ * a shared expert's rows or zeros.  A token may name an expert twice.  The values between the
+ * two products stay fp32 up to the second product, which takes them as three e4m3 parts
+ * (their error is below 2^-11 of the largest of their 128); sums are fp32 in a fixed order
+ * and out is rounded once.
+ *   xq e4m3 [T,H], xs fp32 [T,H/128]; ids int32 [T,k], weights fp32 [T,k]; place int32 [places]
+ *   or NULL; w13 e4m3 [E,2I,H], s13 fp32 [E,2I/128,H/128]; w2 e4m3 [E,H,I], s2 fp32
+ *   [E,H/128,I/128]; y bf16 [T,H] (NULL: 0) and out bf16 [T,H] with row strides; y may be out
+ *   itself at the same stride.
+ * H % 128 == 0, I % 128 == 0, H and 2I <= 65536; T, E and k within the limits above.
+ */
+int moe_apply(gemmar_ctx *ctx, const uint8_t *xq, const float *xs, const int32_t *ids, const float *weights,
+              const int32_t *place, int64_t places, const uint8_t *w13, const float *s13, const uint8_t *w2,
+              const float *s2, int act, int64_t T, int64_t H, int64_t I, int E, int k, const uint16_t *y,
+              int64_t y_stride, uint16_t *out, int64_t out_stride, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
