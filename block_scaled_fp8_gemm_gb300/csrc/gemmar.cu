@@ -75,7 +75,8 @@ cudaError_t ensure_dynamic_smem(const void *kernel, int bytes)
 namespace {
 
 constexpr int kMaxTimedCalls = 65536;
-constexpr int kCounters = 1024;
+constexpr int kCounters = 64;      // of moe_route's groups of tokens, then of moe_apply
+constexpr int kMoeCounters = 32;
 constexpr int kEventsPerCall = GEMMAR_NUM_PHASES + 1;
 
 // Event marking the start of phase `ph` (ph == GEMMAR_NUM_PHASES: the end) of
@@ -928,9 +929,24 @@ GEMMAR_API int moe_apply(gemmar_ctx *ctx, const uint8_t *xq, const float *xs, co
         return GEMMAR_ERR_ALIGN;
     const MoeArgs a{xq, xs, ids, place, (int)(place ? places : 0), weights, w13, w2, s13, s2, (int)T, (int)H, (int)I, E, k,
                     act, y, y_stride, out, out_stride};
-    if (moe_ws_floats(a) > ctx->W_floats)
+    const MoeLayout l = moe_layout(a, ctx->num_sms);
+    if (l.floats > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
-    CUDA_OK(launch_moe(a, ctx->W, as_stream(stream)));
+    if (!load_encode())
+        return GEMMAR_ERR_CUDA;
+    MoeParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.a = a;
+    p.pieces = ctx->W;
+    p.hidden_scale = ctx->W + l.hidden_scale;
+    p.parts = reinterpret_cast<uint8_t *>(ctx->W + l.parts);
+    p.counters = ctx->counters + kMoeCounters;
+    p.status = ctx->status;
+    p.timeout_ns = ctx->timeout_ns;
+    if (!make_tmap_u8(&p.tmX, xq, T, H, moe_columns((int)T)) || !make_tmap_u8(&p.tmW13, w13, (int64_t)E * 2 * I, H, 128) ||
+        !make_tmap_u8(&p.tmW2, w2, (int64_t)E * H, I, 128) || !make_tmap_u8(&p.tmParts, p.parts, l.part_rows, I, 8))
+        return GEMMAR_ERR_CUDA;
+    CUDA_OK(launch_moe(p, ctx->num_sms, as_stream(stream)));
     return GEMMAR_OK;
 }
 

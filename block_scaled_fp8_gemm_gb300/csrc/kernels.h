@@ -293,7 +293,24 @@ struct MoeArgs {
 };
 int64_t route_ws_floats(const RouteArgs &a);
 cudaError_t launch_route(const RouteArgs &a, float *ws, uint32_t *counters, cudaStream_t st);
-int64_t moe_ws_floats(const MoeArgs &a);
-cudaError_t launch_moe(const MoeArgs &a, float *ws, cudaStream_t st);
+// Where moe_apply keeps what passes between its steps, in floats of the workspace: the
+// products' partial sums from 0, then the hidden values' scales and their three parts.
+struct MoeLayout {
+    int64_t hidden_scale, parts, part_rows, floats;
+};
+MoeLayout moe_layout(const MoeArgs &a, int num_sms);
+int moe_columns(int T);        // rows of the tokens' box
+struct MoeParams {
+    CUtensorMap tmX;           // dims {H, T}, box {128, moe_columns}
+    CUtensorMap tmW13, tmW2;   // dims {H, 2 I E} and {I, H E}, box {128, 128}
+    CUtensorMap tmParts;       // dims {I, part_rows}, box {128, 8}
+    MoeArgs a;
+    float *pieces, *hidden_scale;
+    uint8_t *parts;
+    uint32_t *counters;        // two, zero before and after
+    ptx::DevStatus *status;
+    uint64_t timeout_ns;
+};
+cudaError_t launch_moe(const MoeParams &p, int num_sms, cudaStream_t st);
 
 }  // namespace gemmar

@@ -1,116 +1,730 @@
-// moe.cu -- the experts' layer for a few tokens (moe_apply).
+// moe.cu -- the experts' layer for a few tokens (moe_apply), in one launch.
 //
 //   out[t] = y[t] + sum_s w[t,s] W2[e] (act(G[e] x[t]) * (U[e] x[t])),   e = the expert of slot s
+//
+// Bound by HBM: every expert that has a token gives up its 3 H I bytes once, for a handful of
+// tokens each.  So the weights are the MMA's M operand, 128 rows a tile, and the tokens its N:
+// a CTA streams pairs of weight tiles, 32 KB per 128 of K, and their sums cost the tensor
+// cores next to nothing.
+//
+// One persistent CTA per SM (a cooperative launch), 12 warps:
+//   warp 0     TMA of the weights, for both products without a pause
+//   warp 1     MMA issuer
+//   warp 2     TMA of the tokens' codes (first product) and of the hidden values' (second)
+//   warp 3     the grid's barriers
+//   warps 4-11 promotion: a thread keeps one weight row of one of the two tiles, for all tokens;
+//              between the products they form the hidden values, and at the end the rows of out
+// The work of a product is a line of units (expert, tile pair, 128 of K), cut into equal
+// shares, so that all SMs read the same number of bytes whatever the experts' number; a tile
+// whose K is cut leaves a partial sum per share in the workspace ("planes"), added in their
+// order.  Hidden values wait for the whole first product, at two barriers of the grid; the
+// weights of the second keep coming meanwhile, as deep as the ring is (160 to 210 KB per SM,
+// about 4 us of HBM).
+//
+// The first product takes every token as a column for every expert and keeps the columns of
+// the tokens that chose it: no gather, and the columns are free.  The second one's columns are
+// an expert's own hidden rows, in chunks of 8 GROUPS.  They enter as three e4m3 parts of one
+// fp32 value under the scale of its 128 (h / s = c0 + c1 / 16 + c2 / 512): 448 is coded to 16,
+// 16 times that remainder to 8, 32 times the next to 8, so the error is below
+// 2^-14 of the largest of the 128, where one e4m3 rounding would cost each value 2^-4.
+#include <algorithm>
+
 #include "activation.cuh"
 #include "e4m3_encode.cuh"
-#include "kernels.h"
+#include "epilogue.cuh"
 
 namespace gemmar {
 using namespace ptx;
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 384;
+constexpr int kEpiThreads = 256;
+constexpr int kTileBytes = 128 * 128;
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxSlots = 16;
+constexpr uint32_t kAbortGraceNs = 200000;   // let copies in flight land before an aborting CTA exits
+
+// NT: token columns of the first product; GROUPS: groups of 8 tokens in a chunk of the second.
+template <int NT_, int GROUPS_, int STAGES_, int BUFS_>
+struct Cfg {
+    static constexpr int NT = NT_, GROUPS = GROUPS_, kStages = STAGES_, kBufs = BUFS_;
+    static constexpr int kXRows = NT > 24 * GROUPS ? NT : 24 * GROUPS;
+    static constexpr int kStageBytes = 2 * kTileBytes + kXRows * 128;
+    static constexpr int kCols = NT > (24 * GROUPS + 15) / 16 * 16 ? NT : (24 * GROUPS + 15) / 16 * 16;   // per tile
+    static constexpr int kBufCols = kCols <= 32 ? 64 : kCols <= 64 ? 128 : 256;   // both tiles
+    static constexpr int kTmemCols = kBufCols * kBufs;
+    static constexpr int kAcc = NT > 8 * GROUPS ? NT : 8 * GROUPS;
+    static constexpr int kPairs = NT * kMaxSlots;
+    static constexpr int kActive = kPairs < kMaxExperts ? kPairs : kMaxExperts;
+    static constexpr int kChunks = kActive + kPairs / (8 * GROUPS);
+    static constexpr int kOffScale = kStages * kStageBytes;            // [8 warps][2][kAcc] token scales
+    static constexpr int kOffActive = kOffScale + 8 * 2 * kAcc * 4;    // u32 e | first pair << 10, and a last one
+    static constexpr int kOffChunk = kOffActive + (kActive + 1) * 4;   // u32 e | first pair << 10 | pairs << 22
+    static constexpr int kOffPair = kOffChunk + kChunks * 4;           // u32 token | active << 7 | chunk << 17
+    static constexpr int kOffSlot = kOffPair + kPairs * 4;             // u16 pair of a token's slot
+    static constexpr int kOffBar = (kOffSlot + kPairs * 2 + 7) / 8 * 8;
+    static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 5;
+    static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+    static constexpr int kSmemBytes = kOffMisc + 96 + 1024;
+    static_assert(kSmemBytes <= 232448, "shared memory budget");
+    static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM budget");
+    // the plan's scratch lies in the ring
+    static_assert(kStages * kStageBytes >= kMaxExperts * (16 + 4 + 4), "scratch of the plan");
+};
+
+using Few8 = Cfg<16, 1, 6, 4>;     // at most 8 tokens
+using Few32 = Cfg<32, 2, 5, 4>;
+using Few64 = Cfg<64, 3, 5, 2>;
+using Few128 = Cfg<128, 5, 4, 2>;
 
 __device__ __forceinline__ int expert_of(const MoeArgs &a, int slot)
 {
-    int e = a.ids[slot];
+    int e = __ldg(a.ids + slot);
     if (a.place != nullptr)
-        e = e >= 0 && e < a.places ? a.place[e] : -1;
+        e = e >= 0 && e < a.places ? __ldg(a.place + e) : -1;
     return e >= 0 && e < a.E ? e : -1;
 }
 
-__device__ __forceinline__ void decode16(const uint8_t *p, float (&v)[16])
-{
-    const uint4 r = __ldg(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 lo = f32x2_from_e4m3x2((uint16_t)w[i]), hi = f32x2_from_e4m3x2((uint16_t)(w[i] >> 16));
-        v[4 * i] = lo.x;
-        v[4 * i + 1] = lo.y;
-        v[4 * i + 2] = hi.x;
-        v[4 * i + 3] = hi.y;
+// A product's units in a line: item (tile pair of an expert) by item, KB each, `per` to a CTA.
+struct Line {
+    int KB, per, first, end;   // first, end: this CTA's
+    __device__ __forceinline__ Line(int items, int KB_) : KB(KB_)
+    {
+        const int units = items * KB;
+        per = max(1, (units + (int)gridDim.x - 1) / (int)gridDim.x);
+        first = min(units, (int)blockIdx.x * per);
+        end = min(units, first + per);
     }
-}
+    // the shares an item's units are in, and the place of this CTA's among them
+    __device__ __forceinline__ int planes(int item) const { return ((item + 1) * KB - 1) / per - item * KB / per + 1; }
+    __device__ __forceinline__ int plane(int item) const { return (int)blockIdx.x - item * KB / per; }
+};
 
-__device__ __forceinline__ float warp_sum(float s)
+// Who goes where, computed by every CTA for itself from the ids: experts that have tokens in
+// ascending order, each one's tokens in ascending order ("pairs"; a token that names an expert
+// twice is one pair, with both weights).
+template <class C>
+__device__ void make_plan(const MoeArgs &a, uint8_t *smem, int &active, int &chunks, int &pairs)
 {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t *mask = reinterpret_cast<uint32_t *>(smem);             // [E][4] tokens of an expert
+    uint32_t *place = mask + kMaxExperts * 4, *base = place + kMaxExperts;   // [E] first pair | active << 12; first chunk
+    uint32_t *act = reinterpret_cast<uint32_t *>(smem + C::kOffActive);
+    uint32_t *chk = reinterpret_cast<uint32_t *>(smem + C::kOffChunk);
+    uint32_t *pair = reinterpret_cast<uint32_t *>(smem + C::kOffPair);
+    uint16_t *slot = reinterpret_cast<uint16_t *>(smem + C::kOffSlot);
+    uint32_t *sums = reinterpret_cast<uint32_t *>(smem + C::kOffScale);      // [12][2] of the scan
+    const int slots = a.T * a.k;
+    for (int i = tid; i < a.E * 4; i += kThreads)
+        mask[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < slots; i += kThreads) {
+        const int e = expert_of(a, i), t = i / a.k;
+        if (e >= 0)
+            atomicOr(mask + e * 4 + (t >> 5), 1u << (t & 31));
+    }
+    __syncthreads();
+    // three experts in a row to a thread; sums of pairs, and of experts with tokens and chunks
+    constexpr int PER = (kMaxExperts + kThreads - 1) / kThreads, CH = 8 * C::GROUPS;
+    uint32_t n[PER], mine0 = 0, mine1 = 0;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        s += __shfl_xor_sync(0xffffffffu, s, d);
-    return s;
-}
-
-// hidden[slot, i]: a warp per value
-__global__ void __launch_bounds__(kThreads) moe_up_kernel(const MoeArgs a, float *hidden)
-{
-    const int i = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), slot = blockIdx.y, lane = threadIdx.x & 31;
-    const int e = expert_of(a, slot), t = slot / a.k, HB = a.H / 128;
-    if (e < 0)
-        return;
-    const int64_t row = (int64_t)e * 2 * a.I + i;
-    const uint8_t *g = a.w13 + row * a.H, *u = g + (int64_t)a.I * a.H, *x = a.q + (int64_t)t * a.H;
-    const float *sg = a.s13 + row / 128 * HB, *su = a.s13 + (row + a.I) / 128 * HB, *sx = a.sx + (int64_t)t * HB;
-    float zg = 0.0f, zu = 0.0f;
-    for (int c = lane * 16; c < a.H; c += 512) {
-        float xv[16], gv[16], uv[16], pg = 0.0f, pu = 0.0f;
-        decode16(x + c, xv);
-        decode16(g + c, gv);
-        decode16(u + c, uv);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            pg = fmaf(xv[j], gv[j], pg);
-            pu = fmaf(xv[j], uv[j], pu);
+    for (int j = 0; j < PER; ++j) {
+        const int e = tid * PER + j;
+        n[j] = 0;
+        if (e < a.E) {
+            const uint4 m = *reinterpret_cast<const uint4 *>(mask + e * 4);
+            n[j] = __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
         }
-        zg = fmaf(sx[c / 128] * sg[c / 128], pg, zg);
-        zu = fmaf(sx[c / 128] * su[c / 128], pu, zu);
+        mine0 += n[j];
+        mine1 += (n[j] > 0 ? 1u : 0u) | ((n[j] + CH - 1) / CH) << 16;
     }
-    zg = warp_sum(zg);
-    zu = warp_sum(zu);
-    if (lane == 0)
-        with_act(a.act, [&](auto act) {
-            hidden[(int64_t)slot * a.I + i] = act_value<decltype(act)::value>(zg) * zu * a.weights[slot];
-        });
-}
-
-// out[t, n]: a warp per value
-__global__ void __launch_bounds__(kThreads) moe_down_kernel(const MoeArgs a, const float *hidden)
-{
-    const int n = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), t = blockIdx.y, lane = threadIdx.x & 31;
-    float sum = 0.0f;
-    for (int j = 0; j < a.k; ++j) {
-        const int slot = t * a.k + j, e = expert_of(a, slot);
-        if (e < 0)
+    uint32_t s0 = mine0, s1 = mine1;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o0 = __shfl_up_sync(0xffffffffu, s0, d), o1 = __shfl_up_sync(0xffffffffu, s1, d);
+        if (lane >= d) {
+            s0 += o0;
+            s1 += o1;
+        }
+    }
+    if (lane == 31) {
+        sums[warp * 2] = s0;
+        sums[warp * 2 + 1] = s1;
+    }
+    __syncthreads();
+    uint32_t all0 = 0, all1 = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == warp) {
+            s0 += all0;
+            s1 += all1;
+        }
+        all0 += sums[w * 2];
+        all1 += sums[w * 2 + 1];
+    }
+    s0 -= mine0;
+    s1 -= mine1;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int e = tid * PER + j;
+        if (n[j] == 0)
             continue;
-        const int64_t row = (int64_t)e * a.H + n;
-        const float *h = hidden + (int64_t)slot * a.I, *s = a.s2 + row / 128 * (a.I / 128);
-        for (int c = lane * 16; c < a.I; c += 512) {
-            float wv[16], p = 0.0f;
-            decode16(a.w2 + row * a.I + c, wv);
+        const uint32_t ia = s1 & 0xFFFFu, ic = s1 >> 16;
+        act[ia] = (uint32_t)e | s0 << 10;
+        place[e] = s0 | ia << 12;
+        base[e] = ic;
+        for (uint32_t c = 0; c * CH < n[j]; ++c)
+            chk[ic + c] = (uint32_t)e | (s0 + c * CH) << 10 | min(n[j] - c * CH, (uint32_t)CH) << 22;
+        s0 += n[j];
+        s1 += 1u | ((n[j] + CH - 1) / CH) << 16;
+    }
+    pairs = (int)all0;
+    active = (int)(all1 & 0xFFFFu);
+    chunks = (int)(all1 >> 16);
+    if (tid == 0)
+        act[active] = all0 << 10;
+    __syncthreads();
+    for (int i = tid; i < slots; i += kThreads) {
+        const int e = expert_of(a, i), t = i / a.k;
+        bool first = e >= 0;
+        for (int j = t * a.k; j < i && first; ++j)
+            first = expert_of(a, j) != e;
+        uint32_t at = 0xFFFFu;
+        if (first) {
+            uint32_t rank = __popc(mask[e * 4 + (t >> 5)] & ((1u << (t & 31)) - 1));
+            for (int w = 0; w < (t >> 5); ++w)
+                rank += __popc(mask[e * 4 + w]);
+            at = (place[e] & 0xFFFu) + rank;
+            pair[at] = (uint32_t)t | (place[e] >> 12) << 7 | (base[e] + rank / CH) << 17;
+        }
+        slot[i] = (uint16_t)at;
+    }
+    fence_async_shared();   // the ring's first copies come after this scratch
+}
+
+// acc[j] += (value of column j) * (weight scale * token scale j) for 8 columns
+__device__ __forceinline__ void promote8(float *acc, const float (&d)[8], float sw, const float *ts)
+{
+    const float4 a = *reinterpret_cast<const float4 *>(ts), b = *reinterpret_cast<const float4 *>(ts + 4);
+    acc[0] = fmaf(d[0], sw * a.x, acc[0]);
+    acc[1] = fmaf(d[1], sw * a.y, acc[1]);
+    acc[2] = fmaf(d[2], sw * a.z, acc[2]);
+    acc[3] = fmaf(d[3], sw * a.w, acc[3]);
+    acc[4] = fmaf(d[4], sw * b.x, acc[4]);
+    acc[5] = fmaf(d[5], sw * b.y, acc[5]);
+    acc[6] = fmaf(d[6], sw * b.z, acc[6]);
+    acc[7] = fmaf(d[7], sw * b.w, acc[7]);
+}
+
+__device__ __forceinline__ float dot4(const float4 &v) { return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))); }
+
+__device__ __forceinline__ float4 add4(const float4 &a, const float4 &b)
+{
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
+// four codes of v, and what is left of it
+__device__ __forceinline__ uint32_t code4(float (&v)[4])
+{
+    const uint32_t lo = e4m3x2_from_f32(v[0], v[1]), hi = e4m3x2_from_f32(v[2], v[3]);
+    const float2 a = f32x2_from_e4m3x2((uint16_t)lo), b = f32x2_from_e4m3x2((uint16_t)hi);
+    v[0] -= a.x;
+    v[1] -= a.y;
+    v[2] -= b.x;
+    v[3] -= b.y;
+    return lo | hi << 16;
+}
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ MoeParams prm)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align1024(smem_raw);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
+    uint64_t *empty = full + C::kStages;
+    uint64_t *tfull = empty + C::kStages;
+    uint64_t *tempty = tfull + C::kBufs;
+    uint64_t *final_bar = tempty + C::kBufs;
+    uint64_t *epi_bar = final_bar + 1;     // the promotion warps have written what the grid waits for
+    uint64_t *grid_bar = epi_bar + 1;      // [3], once each: so have those of all CTAs
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
+
+    const MoeArgs &a = prm.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(full + s, 2);   // weights and tokens
+            mbar_init(empty + s, 1);
+        }
+        for (int b = 0; b < C::kBufs; ++b) {
+            mbar_init(tfull + b, 1);
+            mbar_init(tempty + b, 8);
+        }
+        mbar_init(final_bar, 1);
+        mbar_init(epi_bar, 8);
+        for (int b = 0; b < 3; ++b)
+            mbar_init(grid_bar + b, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&prm.tmX);
+        prefetch_tmap(&prm.tmW13);
+        prefetch_tmap(&prm.tmW2);
+        prefetch_tmap(&prm.tmParts);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, C::kTmemCols);
+        tmem_relinquish();
+    }
+    int active, chunks, pairs;
+    make_plan<C>(a, smem, active, chunks, pairs);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t *act = reinterpret_cast<const uint32_t *>(smem + C::kOffActive);
+    const uint32_t *chk = reinterpret_cast<const uint32_t *>(smem + C::kOffChunk);
+    const uint32_t *pair = reinterpret_cast<const uint32_t *>(smem + C::kOffPair);
+    const uint16_t *slot = reinterpret_cast<const uint16_t *>(smem + C::kOffSlot);
+
+    const int IB = a.I / 128, HB = a.H / 128, J2 = (HB + 1) / 2;
+    const Line l1(active * IB, HB);        // items (expert, 128 hidden values: their gate and up rows)
+    const Line l2(J2 * chunks, IB);        // items (256 columns of out, chunk)
+    const int n1 = (a.T + 15) / 16 * 16;   // columns of the first product
+    const int64_t rows3 = (int64_t)a.T * a.k + 8;   // hidden rows of one part
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------ weights
+        int stage = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        auto load = [&](const CUtensorMap *tm, int row0, int row1, int kb) {
+            ok = mbar_wait(empty + stage, ph ^ 1, abort_flag, prm.status, prm.timeout_ns, SITE_PRODUCER_EMPTY);
+            if (!ok)
+                return;
+            uint8_t *w = smem + stage * C::kStageBytes;
+            mbar_arrive_expect_tx(full + stage, 2 * kTileBytes);
+            tma_load_2d(w, tm, full + stage, kb * 128, row0);
+            tma_load_2d(w + kTileBytes, tm, full + stage, kb * 128, row1);
+            if (++stage == C::kStages) {
+                stage = 0;
+                ph ^= 1;
+            }
+        };
+        for (int u = l1.first; u < l1.end && ok; ++u) {
+            const int item = u / HB, e = act[item / IB] & 1023, r = e * 2 * a.I + item % IB * 128;
+            load(&prm.tmW13, r, r + a.I, u % HB);
+        }
+        for (int u = l2.first; u < l2.end && ok; ++u) {
+            // the second tile of an odd last pair holds other rows, or none: nobody reads its sums
+            const int item = u / IB, r = (int)(chk[item % chunks] & 1023) * a.H + item / chunks * 256;
+            load(&prm.tmW2, r, r + 128, u % IB);
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ------------------------------------------------ MMA issuer
+        int stage = 0, buf = 0;
+        uint32_t ph = 0, tph = 0;
+        bool ok = true;
+        auto issue = [&](int n) {
+            ok = mbar_wait(tempty + buf, tph ^ 1, abort_flag, prm.status, prm.timeout_ns, SITE_MMA_TMEM_EMPTY) &&
+                 mbar_wait(full + stage, ph, abort_flag, prm.status, prm.timeout_ns, SITE_MMA_FULL);
+            if (!ok)
+                return;
+            tc_fence_after();
+            const uint32_t idesc = idesc_f8_e4m3(128, n);
+            const uint32_t w = smem_u32(smem + stage * C::kStageBytes);
+            const uint64_t xd = desc_kmajor_sw128(w + 2 * kTileBytes);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                p = fmaf(wv[i], h[c + i], p);
-            sum = fmaf(s[c / 128], p, sum);
+            for (int tile = 0; tile < 2; ++tile) {
+                const uint64_t wd = desc_kmajor_sw128(w + tile * kTileBytes);
+                const uint32_t d = tmem_base + buf * C::kBufCols + tile * (C::kBufCols / 2);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_f8(d, wd + 2 * k, xd + 2 * k, idesc, k > 0 ? 1u : 0u);
+            }
+            tc_commit(empty + stage);
+            tc_commit(tfull + buf);
+            if (++stage == C::kStages) {
+                stage = 0;
+                ph ^= 1;
+            }
+            if (++buf == C::kBufs) {
+                buf = 0;
+                tph ^= 1;
+            }
+        };
+        for (int u = l1.first; u < l1.end && ok; ++u)
+            issue(n1);
+        for (int u = l2.first; u < l2.end && ok; ++u) {
+            const int groups = (int)((chk[u / IB % chunks] >> 22) + 7) / 8;
+            issue((24 * groups + 15) / 16 * 16);   // columns past the parts hold anything, and are not read
+        }
+        tc_commit(final_bar);
+        wait_teardown(final_bar, prm.status, prm.timeout_ns);
+    } else if (warp == 2 && lane == 0) {
+        // ------------------------------------------------ tokens
+        int stage = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        auto next = [&] {
+            if (++stage == C::kStages) {
+                stage = 0;
+                ph ^= 1;
+            }
+        };
+        for (int u = l1.first; u < l1.end && ok; ++u, next()) {
+            ok = mbar_wait(empty + stage, ph ^ 1, abort_flag, prm.status, prm.timeout_ns, SITE_PRODUCER_EMPTY);
+            if (ok) {
+                mbar_arrive_expect_tx(full + stage, n1 * 128);
+                tma_load_2d(smem + stage * C::kStageBytes + 2 * kTileBytes, &prm.tmX, full + stage, u % HB * 128, 0);
+            }
+        }
+        // the hidden values of all CTAs, written through the generic proxy
+        ok = ok && mbar_wait(grid_bar + 1, 0, abort_flag, prm.status, prm.timeout_ns, SITE_GRID);
+        fence_async_all();
+        for (int u = l2.first; u < l2.end && ok; ++u, next()) {
+            ok = mbar_wait(empty + stage, ph ^ 1, abort_flag, prm.status, prm.timeout_ns, SITE_PRODUCER_EMPTY);
+            if (ok) {
+                const uint32_t c = chk[u / IB % chunks];
+                const int groups = (int)((c >> 22) + 7) / 8, first = (int)(c >> 10 & 0xFFF);
+                uint8_t *x = smem + stage * C::kStageBytes + 2 * kTileBytes;
+                mbar_arrive_expect_tx(full + stage, 3 * groups * 1024);
+                for (int part = 0; part < 3; ++part)
+                    for (int i = 0; i < groups; ++i)
+                        tma_load_2d(x + (part * groups + i) * 1024, &prm.tmParts, full + stage, u % IB * 128,
+                                    (int)(part * rows3) + first + i * 8);
+            }
+        }
+    } else if (warp == 3 && lane == 0) {
+        // ------------------------------------------------ the grid's barriers
+        bool ok = true;
+        for (int b = 0; b < 3 && ok; ++b) {
+            ok = mbar_wait(epi_bar, b & 1, abort_flag, prm.status, prm.timeout_ns, SITE_GRID);
+            if (!ok)
+                break;
+            __threadfence();
+            red_release_add(prm.counters, 1u);
+            const uint32_t want = (uint32_t)(b + 1) * gridDim.x;
+            const uint64_t t0 = globaltimer();
+            while (ld_acquire(prm.counters) < want) {
+                if (*abort_flag || globaltimer() - t0 > prm.timeout_ns) {
+                    if (!*abort_flag) {
+                        *abort_flag = 1;
+                        report(prm.status, kErrTimeout, SITE_GRID);
+                    }
+                    ok = false;
+                    break;
+                }
+            }
+            if (ok) {
+                __threadfence();
+                mbar_arrive(grid_bar + b);
+            }
+        }
+        // the last CTA past the last barrier leaves the counters as the next call expects them
+        if (ok && atomicAdd(prm.counters + 1, 1u) == gridDim.x - 1) {
+            prm.counters[0] = 0;
+            prm.counters[1] = 0;
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------ promotion
+        const int q = warp & 3, h = (warp - 4) >> 2;   // lane quarter, tile of the pair
+        const int row = q * 32 + lane;
+        float *ts = reinterpret_cast<float *>(smem + C::kOffScale) + (warp - 4) * 2 * C::kAcc;
+        const uint32_t taddr0 = tmem_base + ((uint32_t)(q * 32) << 16) + h * (C::kBufCols / 2);
+        int buf = 0;
+        uint32_t tph = 0;
+        bool ok = true;
+        float acc[C::kAcc];
+        auto release = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(tempty + buf);
+            if (++buf == C::kBufs) {
+                buf = 0;
+                tph ^= 1;
+            }
+        };
+        auto everyone = [&](int b) {   // the b-th barrier of the grid
+            fence_async_all();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(epi_bar);
+            ok = mbar_wait(grid_bar + b, 0, abort_flag, prm.status, prm.timeout_ns, SITE_GRID);
+        };
+        // scales of the tokens at columns lane, lane + 32, ..., a unit ahead
+        constexpr int PER = (C::kAcc + 31) / 32;
+        float next_ts[PER], next_sw;
+
+        // -------- first product
+        auto fetch1 = [&](int u) {
+            const int item = u / HB, kb = u % HB;
+            const int e = act[item / IB] & 1023;
+            next_sw = __ldg(a.s13 + ((int64_t)e * 2 * IB + h * IB + item % IB) * HB + kb);
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                next_ts[i] = lane + 32 * i < a.T ? __ldg(a.sx + (int64_t)(lane + 32 * i) * HB + kb) : 0.0f;
+        };
+        if (l1.first < l1.end)
+            fetch1(l1.first);
+        for (int u = l1.first; u < l1.end; ++u) {
+            if (u == l1.first || u % HB == 0) {
+#pragma unroll
+                for (int j = 0; j < C::kAcc; ++j)
+                    acc[j] = 0.0f;
+            }
+            float *now = ts + (u & 1) * C::kAcc;
+            const float sw = next_sw;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (lane + 32 * i < C::kAcc)
+                    now[lane + 32 * i] = next_ts[i];
+            if (u + 1 < l1.end)
+                fetch1(u + 1);
+            ok = mbar_wait(tfull + buf, tph, abort_flag, prm.status, prm.timeout_ns, SITE_EPI_TMEM_FULL);
+            if (!ok)
+                break;
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t taddr = taddr0 + buf * C::kBufCols;
+#pragma unroll
+            for (int c = 0; c < C::NT; c += 16)
+                if (c < a.T) {
+                    uint32_t r[16];
+                    tmem_ld_x16(taddr + c, r);
+                    tmem_wait_ld(r);
+                    float d[8], f[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        d[j] = __uint_as_float(r[j]);
+                        f[j] = __uint_as_float(r[8 + j]);
+                    }
+                    promote8(acc + c, d, sw, now + c);
+                    promote8(acc + c + 8, f, sw, now + c + 8);
+                }
+            release();
+            if (u % HB == HB - 1 || u + 1 == l1.end) {
+                // the sums of the tokens that chose this expert
+                const int item = u / HB, ia = item / IB;
+                const int first = (int)(act[ia] >> 10), n = (int)(act[ia + 1] >> 10) - first;
+                uint32_t mask[(C::NT + 31) / 32] = {};
+                for (int i = 0; i < n; i += 32) {
+                    const uint32_t t = i + lane < n ? pair[first + i + lane] & 127 : 0xFFFFu;
+#pragma unroll
+                    for (int w = 0; w < (C::NT + 31) / 32; ++w)
+                        mask[w] |= __reduce_or_sync(0xffffffffu, t >> 5 == (uint32_t)w ? 1u << (t & 31) : 0u);
+                }
+                float *to = prm.pieces + ((int64_t)l1.plane(item) * pairs + first) * (2 * a.I) + h * a.I + item % IB * 128 + row;
+#pragma unroll
+                for (int j = 0; j < C::NT; ++j)
+                    if (mask[j >> 5] >> (j & 31) & 1) {
+                        __stcg(to, acc[j]);
+                        to += 2 * a.I;
+                    }
+            }
+        }
+        // -------- hidden values: a warp takes 128 of a pair at a time
+        if (ok)
+            everyone(0);
+        if (ok) {
+            const int groups = pairs * IB;
+            for (int i = blockIdx.x * 8 + warp - 4; i < groups; i += gridDim.x * 8) {
+                const int p = i / IB, jb = i % IB;
+                const uint32_t info = pair[p];
+                const int t = (int)(info & 127), ia = (int)(info >> 7 & 1023), e = (int)(act[ia] & 1023);
+                const int planes = l1.planes(ia * IB + jb);
+                const float *from = prm.pieces + (int64_t)p * 2 * a.I + jb * 128 + lane * 4;
+                float4 zg = make_float4(0, 0, 0, 0), zu = zg;
+                for (int pl = 0; pl < planes; ++pl, from += (int64_t)pairs * 2 * a.I) {
+                    zg = add4(zg, __ldcg(reinterpret_cast<const float4 *>(from)));
+                    zu = add4(zu, __ldcg(reinterpret_cast<const float4 *>(from + a.I)));
+                }
+                float w = 0.0f;
+                if (lane < a.k && expert_of(a, t * a.k + lane) == e)
+                    w = __ldg(a.weights + t * a.k + lane);
+#pragma unroll
+                for (int d = kMaxSlots / 2; d > 0; d >>= 1)
+                    w += __shfl_xor_sync(0xffffffffu, w, d);
+                w = __shfl_sync(0xffffffffu, w, 0);
+                float4 hv;
+                with_act(a.act, [&](auto kind) {
+                    constexpr int ACT = decltype(kind)::value;
+                    hv = make_float4(act_value<ACT>(zg.x) * zu.x * w, act_value<ACT>(zg.y) * zu.y * w,
+                                     act_value<ACT>(zg.z) * zu.z * w, act_value<ACT>(zg.w) * zu.w * w);
+                });
+                const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(dot4(hv))));
+                const float s = __fdiv_rn(m, 448.0f);
+                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (s > 0.0f) {
+                    v[0] = __fdiv_rn(hv.x, s);
+                    v[1] = __fdiv_rn(hv.y, s);
+                    v[2] = __fdiv_rn(hv.z, s);
+                    v[3] = __fdiv_rn(hv.w, s);
+                }
+                uint8_t *o = prm.parts + (int64_t)p * a.I + jb * 128 + lane * 4;
+#pragma unroll
+                for (int part = 0; part < 3; ++part) {
+                    *reinterpret_cast<uint32_t *>(o + part * rows3 * a.I) = code4(v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[j] *= part == 0 ? 16.0f : 32.0f;
+                }
+                if (lane == 0)
+                    __stcg(prm.hidden_scale + (int64_t)p * IB + jb, s);
+            }
+            everyone(1);
+        }
+        // -------- second product
+        auto fetch2 = [&](int u) {
+            const int item = u / IB, kb = u % IB;
+            const uint32_t c = chk[item % chunks];
+            const int64_t block = min(item / chunks * 2 + h, HB - 1);
+            next_sw = __ldg(a.s2 + ((int64_t)(c & 1023) * HB + block) * IB + kb);
+            const int first = (int)(c >> 10 & 0xFFF), n = (int)(c >> 22);
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                next_ts[i] = lane + 32 * i < n ? __ldcg(prm.hidden_scale + (int64_t)(first + lane + 32 * i) * IB + kb) : 0.0f;
+        };
+        if (ok && l2.first < l2.end)
+            fetch2(l2.first);
+        for (int u = l2.first; u < l2.end && ok; ++u) {
+            if (u == l2.first || u % IB == 0) {
+#pragma unroll
+                for (int j = 0; j < 8 * C::GROUPS; ++j)
+                    acc[j] = 0.0f;
+            }
+            float *now = ts + (u & 1) * C::kAcc;
+            const float sw = next_sw;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (lane + 32 * i < C::kAcc)
+                    now[lane + 32 * i] = next_ts[i];
+            if (u + 1 < l2.end)
+                fetch2(u + 1);
+            ok = mbar_wait(tfull + buf, tph, abort_flag, prm.status, prm.timeout_ns, SITE_EPI_TMEM_FULL);
+            if (!ok)
+                break;
+            __syncwarp();
+            tc_fence_after();
+            const int item = u / IB;
+            const uint32_t c = chk[item % chunks];
+            const int first = (int)(c >> 10 & 0xFFF), n = (int)(c >> 22), groups = (n + 7) / 8;
+            const uint32_t taddr = taddr0 + buf * C::kBufCols;
+#pragma unroll
+            for (int i = 0; i < C::GROUPS; ++i)
+                if (i < groups) {
+                    uint32_t r0[8], r1[8], r2[8];
+                    tmem_ld_x8(taddr + i * 8, r0);
+                    tmem_ld_x8(taddr + (groups + i) * 8, r1);
+                    tmem_ld_x8(taddr + (2 * groups + i) * 8, r2);
+                    tmem_wait_ld(r0, r1);
+                    tmem_wait_ld(r2, r2);
+                    float d[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        d[j] = fmaf(__uint_as_float(r2[j]), 0x1p-9f, fmaf(__uint_as_float(r1[j]), 0x1p-4f, __uint_as_float(r0[j])));
+                    promote8(acc + i * 8, d, sw, now + i * 8);
+                }
+            release();
+            if ((u % IB == IB - 1 || u + 1 == l2.end) && item / chunks * 2 + h < HB) {
+                float *to = prm.pieces + ((int64_t)l2.plane(item) * pairs + first) * a.H + (item / chunks * 2 + h) * 128 + row;
+#pragma unroll
+                for (int j = 0; j < 8 * C::GROUPS; ++j)
+                    if (j < n)
+                        __stcg(to + (int64_t)j * a.H, acc[j]);
+            }
+        }
+        if (ok)
+            everyone(2);
+        // -------- rows of out: four columns at a time, a token's experts in the order of its slots
+        if (ok) {
+            const int quads = a.H / 4;
+            for (int64_t i = (int64_t)blockIdx.x * kEpiThreads + threadIdx.x - 128; i < (int64_t)a.T * quads;
+                 i += (int64_t)gridDim.x * kEpiThreads) {
+                const int t = (int)(i / quads), col = (int)(i % quads) * 4;
+                float4 sum = make_float4(0, 0, 0, 0);
+                if (a.y != nullptr) {
+                    const uint2 y = *reinterpret_cast<const uint2 *>(a.y + t * a.ys + col);
+                    sum = make_float4(bf16_lo(y.x), bf16_hi(y.x), bf16_lo(y.y), bf16_hi(y.y));
+                }
+#pragma unroll 4
+                for (int s = 0; s < a.k; ++s) {
+                    const uint32_t p = slot[t * a.k + s];
+                    if (p == 0xFFFFu)
+                        continue;
+                    const int planes = l2.planes(col / 256 * chunks + (int)(pair[p] >> 17));
+                    const float *from = prm.pieces + (int64_t)p * a.H + col;
+                    for (int pl = 0; pl < planes; ++pl, from += (int64_t)pairs * a.H)
+                        sum = add4(sum, __ldcg(reinterpret_cast<const float4 *>(from)));
+                }
+                *reinterpret_cast<uint2 *>(a.out + t * a.os + col) =
+                    make_uint2(bf16x2_from_f32(sum.x, sum.y), bf16x2_from_f32(sum.z, sum.w));
+            }
         }
     }
-    sum = warp_sum(sum);
-    if (lane == 0) {
-        if (a.y != nullptr)
-            sum += bf16_lo(a.y[t * a.ys + n]);
-        a.out[t * a.os + n] = (uint16_t)bf16x2_from_f32(sum, 0.0f);
+
+    __syncwarp();
+    if (*abort_flag) {
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < kAbortGraceNs) {
+        }
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        tmem_dealloc(tmem_base, C::kTmemCols);
+}
+
+template <class C>
+cudaError_t launch_typed(const MoeParams &p, int num_sms, cudaStream_t st)
+{
+    const void *kernel = reinterpret_cast<const void *>(moe_kernel<C>);
+    const cudaError_t e = ensure_dynamic_smem(kernel, C::kSmemBytes);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;   // its CTAs wait for one another
+    attr[0].val.cooperative = 1;
+    cfg.gridDim = dim3(num_sms);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, moe_kernel<C>, p);
 }
 
 }  // namespace
 
-int64_t moe_ws_floats(const MoeArgs &a) { return (int64_t)a.T * a.k * a.I; }
-
-cudaError_t launch_moe(const MoeArgs &a, float *ws, cudaStream_t st)
+// Sums of both products: an item's units lie in at most sms / items + 2 shares, and there are
+// at least as many experts as a token's slots name, so the planes of all pairs are at most
+// T (sms / tile pairs + 2 k) rows.
+MoeLayout moe_layout(const MoeArgs &a, int num_sms)
 {
-    moe_up_kernel<<<dim3(a.I / (kThreads / 32), a.T * a.k), kThreads, 0, st>>>(a, ws);
-    moe_down_kernel<<<dim3(a.H / (kThreads / 32), a.T), kThreads, 0, st>>>(a, ws);
-    return cudaGetLastError();
+    MoeLayout l;
+    const int64_t IB = a.I / 128, J2 = (a.H / 128 + 1) / 2, slots = (int64_t)a.T * a.k;
+    l.hidden_scale = std::max(a.T * (num_sms / IB + 1 + 2 * a.k) * 2 * a.I, a.T * (num_sms / J2 + 1 + 2 * a.k) * (int64_t)a.H);
+    l.parts = l.hidden_scale + (slots * IB + 3) / 4 * 4;
+    l.part_rows = 3 * (slots + 8);
+    l.floats = l.parts + l.part_rows * a.I / 4;
+    return l;
+}
+
+int moe_columns(int T) { return (T + 15) / 16 * 16; }
+
+cudaError_t launch_moe(const MoeParams &p, int num_sms, cudaStream_t st)
+{
+    if (p.a.T <= 8)
+        return launch_typed<Few8>(p, num_sms, st);
+    if (p.a.T <= 32)
+        return launch_typed<Few32>(p, num_sms, st);
+    if (p.a.T <= 64)
+        return launch_typed<Few64>(p, num_sms, st);
+    return launch_typed<Few128>(p, num_sms, st);
 }
 
 }  // namespace gemmar

@@ -105,6 +105,7 @@ enum WaitSite : int {
     SITE_PARK_EMPTY = 9,   // an epilogue warp waiting for its park to be copied out
     SITE_LORA_MMA = 10,    // an adapter kernel waiting for its MMAs
     SITE_ROW_MAX = 11,     // the two halves of a gated row, for the maximum of its group
+    SITE_GRID = 12,        // a barrier of all CTAs of the experts' layer
 };
 
 constexpr int kErrTimeout = 6;   // == GEMMAR_ERR_TIMEOUT
@@ -680,6 +681,10 @@ __device__ __forceinline__ void cp_async_cg16_or_zero(uint32_t dst, const void *
 // Make this thread's shared-memory writes (cp.async included, once waited for)
 // visible to the async proxy, which the MMA reads through.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// The same for writes to any state space: before other SMs read them through their async proxy,
+// and there after the wait for them.
+__device__ __forceinline__ void fence_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 __device__ __forceinline__ void cp_async_ca8(uint32_t dst, const void *src)
 {
