@@ -43,6 +43,7 @@ constexpr int kEpiThreads = 256;
 constexpr int kTileBytes = 128 * 128;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxSlots = 16;
+constexpr int kSparse = 16;      // tokens of an expert up to which the first product's columns are picked
 constexpr uint32_t kAbortGraceNs = 200000;   // let copies in flight land before an aborting CTA exits
 
 // NT: token columns of the first product; GROUPS: groups of 8 tokens in a chunk of the second.
@@ -70,7 +71,7 @@ struct Cfg {
     static_assert(kSmemBytes <= 232448, "shared memory budget");
     static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM budget");
     // the plan's scratch lies in the ring
-    static_assert(kStages * kStageBytes >= kMaxExperts * (16 + 4 + 4), "scratch of the plan");
+    static_assert(kStages * kStageBytes >= kMaxExperts * (16 + 4 + 4) + kPairs * 2, "scratch of the plan");
 };
 
 using Few8 = Cfg<16, 1, 6, 4>;     // at most 8 tokens
@@ -97,7 +98,14 @@ struct Line {
         end = min(units, first + per);
     }
     // the shares an item's units are in, and the place of this CTA's among them
-    __device__ __forceinline__ int planes(int item) const { return ((item + 1) * KB - 1) / per - item * KB / per + 1; }
+    __device__ __forceinline__ int planes(int item) const
+    {
+        const uint32_t u = (uint32_t)(item * KB);
+        int n = 1;
+        for (int left = (int)(u % (uint32_t)per) + KB - 1; left >= per; left -= per)
+            ++n;
+        return n;
+    }
     __device__ __forceinline__ int plane(int item) const { return (int)blockIdx.x - item * KB / per; }
 };
 
@@ -110,6 +118,7 @@ __device__ void make_plan(const MoeArgs &a, uint8_t *smem, int &active, int &chu
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t *mask = reinterpret_cast<uint32_t *>(smem);             // [E][4] tokens of an expert
     uint32_t *place = mask + kMaxExperts * 4, *base = place + kMaxExperts;   // [E] first pair | active << 12; first chunk
+    int16_t *expert = reinterpret_cast<int16_t *>(base + kMaxExperts);       // [T k] of a slot
     uint32_t *act = reinterpret_cast<uint32_t *>(smem + C::kOffActive);
     uint32_t *chk = reinterpret_cast<uint32_t *>(smem + C::kOffChunk);
     uint32_t *pair = reinterpret_cast<uint32_t *>(smem + C::kOffPair);
@@ -121,6 +130,7 @@ __device__ void make_plan(const MoeArgs &a, uint8_t *smem, int &active, int &chu
     __syncthreads();
     for (int i = tid; i < slots; i += kThreads) {
         const int e = expert_of(a, i), t = i / a.k;
+        expert[i] = (int16_t)e;
         if (e >= 0)
             atomicOr(mask + e * 4 + (t >> 5), 1u << (t & 31));
     }
@@ -185,10 +195,10 @@ __device__ void make_plan(const MoeArgs &a, uint8_t *smem, int &active, int &chu
         act[active] = all0 << 10;
     __syncthreads();
     for (int i = tid; i < slots; i += kThreads) {
-        const int e = expert_of(a, i), t = i / a.k;
+        const int e = expert[i], t = i / a.k;
         bool first = e >= 0;
-        for (int j = t * a.k; j < i && first; ++j)
-            first = expert_of(a, j) != e;
+        for (int j = t * a.k; j < i; ++j)
+            first = first && expert[j] != e;
         uint32_t at = 0xFFFFu;
         if (first) {
             uint32_t rank = __popc(mask[e * 4 + (t >> 5)] & ((1u << (t & 31)) - 1));
@@ -203,20 +213,18 @@ __device__ void make_plan(const MoeArgs &a, uint8_t *smem, int &active, int &chu
 }
 
 // acc[j] += (value of column j) * (weight scale * token scale j) for 8 columns
-__device__ __forceinline__ void promote8(float *acc, const float (&d)[8], float sw, const float *ts)
+__device__ __forceinline__ void promote8(float *acc, const float *d, const float *ts)
 {
     const float4 a = *reinterpret_cast<const float4 *>(ts), b = *reinterpret_cast<const float4 *>(ts + 4);
-    acc[0] = fmaf(d[0], sw * a.x, acc[0]);
-    acc[1] = fmaf(d[1], sw * a.y, acc[1]);
-    acc[2] = fmaf(d[2], sw * a.z, acc[2]);
-    acc[3] = fmaf(d[3], sw * a.w, acc[3]);
-    acc[4] = fmaf(d[4], sw * b.x, acc[4]);
-    acc[5] = fmaf(d[5], sw * b.y, acc[5]);
-    acc[6] = fmaf(d[6], sw * b.z, acc[6]);
-    acc[7] = fmaf(d[7], sw * b.w, acc[7]);
+    fma2(acc[0], acc[1], d[0], d[1], a.x, a.y);
+    fma2(acc[2], acc[3], d[2], d[3], a.z, a.w);
+    fma2(acc[4], acc[5], d[4], d[5], b.x, b.y);
+    fma2(acc[6], acc[7], d[6], d[7], b.z, b.w);
 }
 
-__device__ __forceinline__ float dot4(const float4 &v) { return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))); }
+__device__ __forceinline__ float max4(const float4 &v) { return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))); }
+
+__device__ __forceinline__ float4 ld4(const float *p) { return __ldcg(reinterpret_cast<const float4 *>(p)); }
 
 __device__ __forceinline__ float4 add4(const float4 &a, const float4 &b)
 {
@@ -402,8 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             ok = mbar_wait(epi_bar, b & 1, abort_flag, prm.status, prm.timeout_ns, SITE_GRID);
             if (!ok)
                 break;
-            __threadfence();
-            red_release_add(prm.counters, 1u);
+            red_release_add(prm.counters, 1u);   // releases what the promotion warps wrote before they arrived
             const uint32_t want = (uint32_t)(b + 1) * gridDim.x;
             const uint64_t t0 = globaltimer();
             while (ld_acquire(prm.counters) < want) {
@@ -416,10 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                     break;
                 }
             }
-            if (ok) {
-                __threadfence();
+            if (ok)
                 mbar_arrive(grid_bar + b);
-            }
         }
         // the last CTA past the last barrier leaves the counters as the next call expects them
         if (ok && atomicAdd(prm.counters + 1, 1u) == gridDim.x - 1) {
@@ -447,39 +452,62 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             }
         };
         auto everyone = [&](int b) {   // the b-th barrier of the grid
-            fence_async_all();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(epi_bar);
             ok = mbar_wait(grid_bar + b, 0, abort_flag, prm.status, prm.timeout_ns, SITE_GRID);
         };
-        // scales of the tokens at columns lane, lane + 32, ..., a unit ahead
+        // scales of the tokens at columns lane, lane + 32, ..., and the weights', a unit ahead
         constexpr int PER = (C::kAcc + 31) / 32;
         float next_ts[PER], next_sw;
-
-        // -------- first product
-        auto fetch1 = [&](int u) {
-            const int item = u / HB, kb = u % HB;
-            const int e = act[item / IB] & 1023;
-            next_sw = __ldg(a.s13 + ((int64_t)e * 2 * IB + h * IB + item % IB) * HB + kb);
+        auto stage_scales = [&](int u) {
+            float *now = ts + (u & 1) * C::kAcc;   // the warp's own: read by it two units back
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                next_ts[i] = lane + 32 * i < a.T ? __ldg(a.sx + (int64_t)(lane + 32 * i) * HB + kb) : 0.0f;
+                if (lane + 32 * i < C::kAcc)
+                    now[lane + 32 * i] = next_sw * next_ts[i];
+            return now;
         };
+
+        // -------- first product.  Of an expert with few tokens only their columns are read, the
+        // j-th token's sum in acc[j]; of one with many all, a token's in acc[token].
+        int item = -1, ia = 0, first = 0, n = 0;
+        constexpr bool kAlways = C::NT <= kSparse;   // there are no more tokens than that
+        bool sparse = true;
+        int list = 0;   // the expert's token at place `lane`
+        auto enter1 = [&](int u) {
+            item = u / HB;
+            ia = item / IB;
+            first = (int)(act[ia] >> 10);
+            n = (int)(act[ia + 1] >> 10) - first;
+            sparse = kAlways || n <= kSparse;
+            list = lane < n ? (int)(pair[first + lane] & 127) : 0;
+        };
+        auto fetch1 = [&](int u) {
+            const int next_item = u / HB, kb = u % HB, e = act[next_item / IB] & 1023;
+            next_sw = __ldg(a.s13 + ((int64_t)e * 2 * IB + h * IB + next_item % IB) * HB + kb);
+            const int at = (int)(act[next_item / IB] >> 10), count = (int)(act[next_item / IB + 1] >> 10) - at;
+            if (kAlways || count <= kSparse) {
+                next_ts[0] = lane < count ? __ldg(a.sx + (int64_t)(pair[at + lane] & 127) * HB + kb) : 0.0f;
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    next_ts[i] = lane + 32 * i < a.T ? __ldg(a.sx + (int64_t)(lane + 32 * i) * HB + kb) : 0.0f;
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            next_ts[i] = 0.0f;
         if (l1.first < l1.end)
             fetch1(l1.first);
         for (int u = l1.first; u < l1.end; ++u) {
             if (u == l1.first || u % HB == 0) {
+                enter1(u);
 #pragma unroll
                 for (int j = 0; j < C::kAcc; ++j)
                     acc[j] = 0.0f;
             }
-            float *now = ts + (u & 1) * C::kAcc;
-            const float sw = next_sw;
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (lane + 32 * i < C::kAcc)
-                    now[lane + 32 * i] = next_ts[i];
+            const float *now = stage_scales(u);
             if (u + 1 < l1.end)
                 fetch1(u + 1);
             ok = mbar_wait(tfull + buf, tph, abort_flag, prm.status, prm.timeout_ns, SITE_EPI_TMEM_FULL);
@@ -488,40 +516,59 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             __syncwarp();
             tc_fence_after();
             const uint32_t taddr = taddr0 + buf * C::kBufCols;
+            if (sparse) {
 #pragma unroll
-            for (int c = 0; c < C::NT; c += 16)
-                if (c < a.T) {
-                    uint32_t r[16];
-                    tmem_ld_x16(taddr + c, r);
-                    tmem_wait_ld(r);
-                    float d[8], f[8];
+                for (int c = 0; c < kSparse; c += 8)
+                    if (c < n) {
+                        uint32_t r[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        d[j] = __uint_as_float(r[j]);
-                        f[j] = __uint_as_float(r[8 + j]);
+                        for (int j = 0; j < 8; ++j)   // past the last token: the first one's, unused
+                            tmem_ld_x1(taddr + __shfl_sync(0xffffffffu, list, c + j), r[j]);
+                        tmem_wait_ld(r);
+                        float d[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            d[j] = __uint_as_float(r[j]);
+                        promote8(acc + c, d, now + c);
                     }
-                    promote8(acc + c, d, sw, now + c);
-                    promote8(acc + c + 8, f, sw, now + c + 8);
-                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < C::NT; c += 16)
+                    if (c < a.T) {
+                        uint32_t r[16];
+                        tmem_ld_x16(taddr + c, r);
+                        tmem_wait_ld(r);
+                        float d[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            d[j] = __uint_as_float(r[j]);
+                        promote8(acc + c, d, now + c);
+                        promote8(acc + c + 8, d + 8, now + c + 8);
+                    }
+            }
             release();
             if (u % HB == HB - 1 || u + 1 == l1.end) {
-                // the sums of the tokens that chose this expert
-                const int item = u / HB, ia = item / IB;
-                const int first = (int)(act[ia] >> 10), n = (int)(act[ia + 1] >> 10) - first;
-                uint32_t mask[(C::NT + 31) / 32] = {};
-                for (int i = 0; i < n; i += 32) {
-                    const uint32_t t = i + lane < n ? pair[first + i + lane] & 127 : 0xFFFFu;
-#pragma unroll
-                    for (int w = 0; w < (C::NT + 31) / 32; ++w)
-                        mask[w] |= __reduce_or_sync(0xffffffffu, t >> 5 == (uint32_t)w ? 1u << (t & 31) : 0u);
-                }
                 float *to = prm.pieces + ((int64_t)l1.plane(item) * pairs + first) * (2 * a.I) + h * a.I + item % IB * 128 + row;
+                if (sparse) {
 #pragma unroll
-                for (int j = 0; j < C::NT; ++j)
-                    if (mask[j >> 5] >> (j & 31) & 1) {
-                        __stcg(to, acc[j]);
-                        to += 2 * a.I;
+                    for (int j = 0; j < kSparse; ++j)
+                        if (j < n)
+                            __stcg(to + (int64_t)j * 2 * a.I, acc[j]);
+                } else {
+                    uint32_t mask[(C::NT + 31) / 32] = {};
+                    for (int i = 0; i < n; i += 32) {
+                        const uint32_t t = i + lane < n ? pair[first + i + lane] & 127 : 0xFFFFu;
+#pragma unroll
+                        for (int w = 0; w < (C::NT + 31) / 32; ++w)
+                            mask[w] |= __reduce_or_sync(0xffffffffu, t >> 5 == (uint32_t)w ? 1u << (t & 31) : 0u);
                     }
+#pragma unroll
+                    for (int j = 0; j < C::NT; ++j)
+                        if (mask[j >> 5] >> (j & 31) & 1) {
+                            __stcg(to, acc[j]);
+                            to += 2 * a.I;
+                        }
+                }
             }
         }
         // -------- hidden values: a warp takes 128 of a pair at a time
@@ -535,14 +582,22 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 const int t = (int)(info & 127), ia = (int)(info >> 7 & 1023), e = (int)(act[ia] & 1023);
                 const int planes = l1.planes(ia * IB + jb);
                 const float *from = prm.pieces + (int64_t)p * 2 * a.I + jb * 128 + lane * 4;
-                float4 zg = make_float4(0, 0, 0, 0), zu = zg;
-                for (int pl = 0; pl < planes; ++pl, from += (int64_t)pairs * 2 * a.I) {
-                    zg = add4(zg, __ldcg(reinterpret_cast<const float4 *>(from)));
-                    zu = add4(zu, __ldcg(reinterpret_cast<const float4 *>(from + a.I)));
+                const int64_t plane = (int64_t)pairs * 2 * a.I;
+                float4 zg = ld4(from), zu = ld4(from + a.I);
+                if (planes > 1) {
+                    const float4 g1 = ld4(from + plane), u1 = ld4(from + plane + a.I);
+                    zg = add4(zg, g1);
+                    zu = add4(zu, u1);
+                }
+                for (int pl = 2; pl < planes; ++pl) {
+                    zg = add4(zg, ld4(from + pl * plane));
+                    zu = add4(zu, ld4(from + pl * plane + a.I));
                 }
                 float w = 0.0f;
-                if (lane < a.k && expert_of(a, t * a.k + lane) == e)
-                    w = __ldg(a.weights + t * a.k + lane);
+                if (lane < a.k) {
+                    const float v = __ldg(a.weights + t * a.k + lane);
+                    w = expert_of(a, t * a.k + lane) == e ? v : 0.0f;
+                }
 #pragma unroll
                 for (int d = kMaxSlots / 2; d > 0; d >>= 1)
                     w += __shfl_xor_sync(0xffffffffu, w, d);
@@ -553,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                     hv = make_float4(act_value<ACT>(zg.x) * zu.x * w, act_value<ACT>(zg.y) * zu.y * w,
                                      act_value<ACT>(zg.z) * zu.z * w, act_value<ACT>(zg.w) * zu.w * w);
                 });
-                const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(dot4(hv))));
+                const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(max4(hv))));
                 const float s = __fdiv_rn(m, 448.0f);
                 float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 if (s > 0.0f) {
@@ -573,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 if (lane == 0)
                     __stcg(prm.hidden_scale + (int64_t)p * IB + jb, s);
             }
+            fence_async_all();   // other SMs read the parts through their async proxy
             everyone(1);
         }
         // -------- second product
@@ -581,11 +637,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             const uint32_t c = chk[item % chunks];
             const int64_t block = min(item / chunks * 2 + h, HB - 1);
             next_sw = __ldg(a.s2 + ((int64_t)(c & 1023) * HB + block) * IB + kb);
-            const int first = (int)(c >> 10 & 0xFFF), n = (int)(c >> 22);
+            const int at = (int)(c >> 10 & 0xFFF), count = (int)(c >> 22);
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                next_ts[i] = lane + 32 * i < n ? __ldcg(prm.hidden_scale + (int64_t)(first + lane + 32 * i) * IB + kb) : 0.0f;
+                next_ts[i] = lane + 32 * i < count ? ld_after_f32(prm.hidden_scale + (int64_t)(at + lane + 32 * i) * IB + kb) : 0.0f;
         };
+        __syncwarp();
         if (ok && l2.first < l2.end)
             fetch2(l2.first);
         for (int u = l2.first; u < l2.end && ok; ++u) {
@@ -594,13 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 for (int j = 0; j < 8 * C::GROUPS; ++j)
                     acc[j] = 0.0f;
             }
-            float *now = ts + (u & 1) * C::kAcc;
-            const float sw = next_sw;
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (lane + 32 * i < C::kAcc)
-                    now[lane + 32 * i] = next_ts[i];
+            const float *now = stage_scales(u);
             if (u + 1 < l2.end)
                 fetch2(u + 1);
             ok = mbar_wait(tfull + buf, tph, abort_flag, prm.status, prm.timeout_ns, SITE_EPI_TMEM_FULL);
@@ -608,9 +659,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 break;
             __syncwarp();
             tc_fence_after();
-            const int item = u / IB;
+            item = u / IB;
             const uint32_t c = chk[item % chunks];
-            const int first = (int)(c >> 10 & 0xFFF), n = (int)(c >> 22), groups = (n + 7) / 8;
+            first = (int)(c >> 10 & 0xFFF);
+            n = (int)(c >> 22);
+            const int groups = (n + 7) / 8;
             const uint32_t taddr = taddr0 + buf * C::kBufCols;
 #pragma unroll
             for (int i = 0; i < C::GROUPS; ++i)
@@ -625,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         d[j] = fmaf(__uint_as_float(r2[j]), 0x1p-9f, fmaf(__uint_as_float(r1[j]), 0x1p-4f, __uint_as_float(r0[j])));
-                    promote8(acc + i * 8, d, sw, now + i * 8);
+                    promote8(acc + i * 8, d, now + i * 8);
                 }
             release();
             if ((u % IB == IB - 1 || u + 1 == l2.end) && item / chunks * 2 + h < HB) {
@@ -649,15 +702,29 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                     const uint2 y = *reinterpret_cast<const uint2 *>(a.y + t * a.ys + col);
                     sum = make_float4(bf16_lo(y.x), bf16_hi(y.x), bf16_lo(y.y), bf16_hi(y.y));
                 }
-#pragma unroll 4
-                for (int s = 0; s < a.k; ++s) {
-                    const uint32_t p = slot[t * a.k + s];
-                    if (p == 0xFFFFu)
-                        continue;
-                    const int planes = l2.planes(col / 256 * chunks + (int)(pair[p] >> 17));
-                    const float *from = prm.pieces + (int64_t)p * a.H + col;
-                    for (int pl = 0; pl < planes; ++pl, from += (int64_t)pairs * a.H)
-                        sum = add4(sum, __ldcg(reinterpret_cast<const float4 *>(from)));
+                // four slots' loads under way at a time
+                const int64_t plane = (int64_t)pairs * a.H;
+                for (int s0 = 0; s0 < a.k; s0 += 4) {
+                    float4 v[4], w[4];
+                    int planes[4];
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const uint32_t p = s0 + s < a.k ? slot[t * a.k + s0 + s] : 0xFFFFu;
+                        planes[s] = p == 0xFFFFu ? 0 : l2.planes(col / 256 * chunks + (int)(pair[p] >> 17));
+                        const float *from = prm.pieces + (int64_t)p * a.H + col;
+                        v[s] = planes[s] > 0 ? ld4(from) : make_float4(0, 0, 0, 0);
+                        w[s] = planes[s] > 1 ? ld4(from + plane) : make_float4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        if (planes[s] > 0)
+                            sum = add4(sum, v[s]);
+                        if (planes[s] > 1)
+                            sum = add4(sum, w[s]);
+                        const float *from = prm.pieces + (int64_t)slot[t * a.k + min(s0 + s, a.k - 1)] * a.H + col;
+                        for (int pl = 2; pl < planes[s]; ++pl)
+                            sum = add4(sum, ld4(from + pl * plane));
+                    }
                 }
                 *reinterpret_cast<uint2 *>(a.out + t * a.os + col) =
                     make_uint2(bf16x2_from_f32(sum.x, sum.y), bf16x2_from_f32(sum.z, sum.w));

@@ -518,6 +518,20 @@ __device__ __forceinline__ void tmem_wait_st()
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// 32 lanes x 32 bits, one column (see tmem_ld_x32), and the wait for eight such loads.
+__device__ __forceinline__ void tmem_ld_x1(uint32_t taddr, uint32_t &r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&a)[8])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7])
+                 :
+                 : "memory");
+}
+
 // 32 lanes x 32 bits, 8 consecutive columns (see tmem_ld_x32), and the wait for two such loads.
 __device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8])
 {
@@ -629,6 +643,17 @@ __device__ __forceinline__ void fma2(float &cx, float &cy, float a, uint32_t bx,
     const uint64_t b = ((uint64_t)by << 32) | bx;
     const uint64_t aa = ((uint64_t)__float_as_uint(a) << 32) | __float_as_uint(a);
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(aa), "l"(b));
+    cx = __uint_as_float((uint32_t)c);
+    cy = __uint_as_float((uint32_t)(c >> 32));
+}
+
+// (c.x, c.y) = (a.x * b.x + c.x, a.y * b.y + c.y), each lane exactly fmaf()
+__device__ __forceinline__ void fma2(float &cx, float &cy, float ax, float ay, float bx, float by)
+{
+    uint64_t c = ((uint64_t)__float_as_uint(cy) << 32) | __float_as_uint(cx);
+    const uint64_t a = ((uint64_t)__float_as_uint(ay) << 32) | __float_as_uint(ax);
+    const uint64_t b = ((uint64_t)__float_as_uint(by) << 32) | __float_as_uint(bx);
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
     cx = __uint_as_float((uint32_t)c);
     cy = __uint_as_float((uint32_t)(c >> 32));
 }
