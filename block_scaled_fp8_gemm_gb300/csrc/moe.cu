@@ -43,6 +43,10 @@ constexpr int kEpiThreads = 256;
 constexpr int kTileBytes = 128 * 128;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxSlots = 16;
+constexpr int kTake = 8;
+constexpr int kRegsLow = 56;     // warps 0-3 after setmaxnreg.dec
+constexpr int kRegsHigh = 224;   // promotion warps after setmaxnreg.inc
+constexpr int kRegsNeeded = 128 * kRegsLow + kEpiThreads * kRegsHigh;
 constexpr int kSparse = 16;      // tokens of an expert up to which the first product's columns are picked
 constexpr uint32_t kAbortGraceNs = 200000;   // let copies in flight land before an aborting CTA exits
 
@@ -107,6 +111,34 @@ struct Line {
         return n;
     }
     __device__ __forceinline__ int plane(int item) const { return (int)blockIdx.x - item * KB / per; }
+};
+
+// A CTA's way along its share.  step() goes on to the next item's first unit; stay() to the next unit
+// of this one, false where there is none.
+struct Walk {
+    const Line &l;
+    int u, item, kb;
+    __device__ __forceinline__ explicit Walk(const Line &line) : l(line), u(line.first), item(line.first / line.KB), kb(line.first - item * line.KB) {}
+    __device__ __forceinline__ bool last_of_item() const { return kb + 1 == l.KB || u + 1 == l.end; }
+    __device__ __forceinline__ bool stay()
+    {
+        if (last_of_item())
+            return false;
+        ++u;
+        ++kb;
+        return true;
+    }
+    __device__ __forceinline__ void step()
+    {
+        ++u;
+        ++item;
+        kb = 0;
+    }
+    __device__ __forceinline__ void advance()
+    {
+        if (!stay())
+            step();
+    }
 };
 
 // Who goes where, computed by every CTA for itself from the ids: experts that have tokens in
@@ -212,14 +244,14 @@ __device__ void make_plan(const MoeArgs &a, uint8_t *smem, int &active, int &chu
     fence_async_shared();   // the ring's first copies come after this scratch
 }
 
-// acc[j] += (value of column j) * (weight scale * token scale j) for 8 columns
-__device__ __forceinline__ void promote8(float *acc, const float *d, const float *ts)
+// acc[j] += (sum of column j) * (weight scale * token scale j) for 8 columns
+__device__ __forceinline__ void promote8(float *acc, const uint32_t (&d)[8], const float *ts)
 {
     const float4 a = *reinterpret_cast<const float4 *>(ts), b = *reinterpret_cast<const float4 *>(ts + 4);
-    fma2(acc[0], acc[1], d[0], d[1], a.x, a.y);
-    fma2(acc[2], acc[3], d[2], d[3], a.z, a.w);
-    fma2(acc[4], acc[5], d[4], d[5], b.x, b.y);
-    fma2(acc[6], acc[7], d[6], d[7], b.z, b.w);
+    fma2(acc[0], acc[1], __uint_as_float(d[0]), __uint_as_float(d[1]), a.x, a.y);
+    fma2(acc[2], acc[3], __uint_as_float(d[2]), __uint_as_float(d[3]), a.z, a.w);
+    fma2(acc[4], acc[5], __uint_as_float(d[4]), __uint_as_float(d[5]), b.x, b.y);
+    fma2(acc[6], acc[7], __uint_as_float(d[6]), __uint_as_float(d[7]), b.z, b.w);
 }
 
 __device__ __forceinline__ float max4(const float4 &v) { return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))); }
@@ -301,137 +333,148 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     const int n1 = (a.T + 15) / 16 * 16;   // columns of the first product
     const int64_t rows3 = (int64_t)a.T * a.k + 8;   // hidden rows of one part
 
-    if (warp == 0 && lane == 0) {
-        // ------------------------------------------------ weights
-        int stage = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        auto load = [&](const CUtensorMap *tm, int row0, int row1, int kb) {
-            ok = mbar_wait(empty + stage, ph ^ 1, abort_flag, prm.status, prm.timeout_ns, SITE_PRODUCER_EMPTY);
-            if (!ok)
-                return;
-            uint8_t *w = smem + stage * C::kStageBytes;
-            mbar_arrive_expect_tx(full + stage, 2 * kTileBytes);
-            tma_load_2d(w, tm, full + stage, kb * 128, row0);
-            tma_load_2d(w + kTileBytes, tm, full + stage, kb * 128, row1);
-            if (++stage == C::kStages) {
-                stage = 0;
-                ph ^= 1;
+    if (warp < 4) {
+        setmaxnreg_dec<kRegsLow>();
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------ weights
+            int stage = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            auto load = [&](const CUtensorMap *tm, int row0, int row1, int kb) {
+                ok = mbar_wait(empty + stage, ph ^ 1, abort_flag, prm.status, prm.timeout_ns, SITE_PRODUCER_EMPTY);
+                if (!ok)
+                    return;
+                uint8_t *w = smem + stage * C::kStageBytes;
+                mbar_arrive_expect_tx(full + stage, 2 * kTileBytes);
+                tma_load_2d(w, tm, full + stage, kb * 128, row0);
+                tma_load_2d(w + kTileBytes, tm, full + stage, kb * 128, row1);
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    ph ^= 1;
+                }
+            };
+            for (Walk w(l1); w.u < l1.end && ok; w.step()) {
+                const int ia = w.item / IB, r = (int)(act[ia] & 1023) * 2 * a.I + (w.item - ia * IB) * 128;
+                const int r1 = r + a.I;
+                for (bool same = true; same && ok; same = w.stay())
+                    load(&prm.tmW13, r, r1, w.kb);
             }
-        };
-        for (int u = l1.first; u < l1.end && ok; ++u) {
-            const int item = u / HB, e = act[item / IB] & 1023, r = e * 2 * a.I + item % IB * 128;
-            load(&prm.tmW13, r, r + a.I, u % HB);
-        }
-        for (int u = l2.first; u < l2.end && ok; ++u) {
-            // the second tile of an odd last pair holds other rows, or none: nobody reads its sums
-            const int item = u / IB, r = (int)(chk[item % chunks] & 1023) * a.H + item / chunks * 256;
-            load(&prm.tmW2, r, r + 128, u % IB);
-        }
-    } else if (warp == 1 && lane == 0) {
-        // ------------------------------------------------ MMA issuer
-        int stage = 0, buf = 0;
-        uint32_t ph = 0, tph = 0;
-        bool ok = true;
-        auto issue = [&](int n) {
-            ok = mbar_wait(tempty + buf, tph ^ 1, abort_flag, prm.status, prm.timeout_ns, SITE_MMA_TMEM_EMPTY) &&
-                 mbar_wait(full + stage, ph, abort_flag, prm.status, prm.timeout_ns, SITE_MMA_FULL);
-            if (!ok)
-                return;
-            tc_fence_after();
-            const uint32_t idesc = idesc_f8_e4m3(128, n);
-            const uint32_t w = smem_u32(smem + stage * C::kStageBytes);
-            const uint64_t xd = desc_kmajor_sw128(w + 2 * kTileBytes);
+            for (Walk w(l2); w.u < l2.end && ok; w.step()) {
+                // the second tile of an odd last pair holds other rows, or none: nobody reads its sums
+                const int j = w.item / chunks, r = (int)(chk[w.item - j * chunks] & 1023) * a.H + j * 256;
+                for (bool same = true; same && ok; same = w.stay())
+                    load(&prm.tmW2, r, r + 128, w.kb);
+            }
+        } else if (warp == 1 && lane == 0) {
+            // ------------------------------------------------ MMA issuer
+            int stage = 0, buf = 0;
+            uint32_t ph = 0, tph = 0;
+            bool ok = true;
+            auto issue = [&](int n) {
+                ok = mbar_wait(tempty + buf, tph ^ 1, abort_flag, prm.status, prm.timeout_ns, SITE_MMA_TMEM_EMPTY) &&
+                     mbar_wait(full + stage, ph, abort_flag, prm.status, prm.timeout_ns, SITE_MMA_FULL);
+                if (!ok)
+                    return;
+                tc_fence_after();
+                const uint32_t idesc = idesc_f8_e4m3(128, n);
+                const uint32_t w = smem_u32(smem + stage * C::kStageBytes);
+                const uint64_t xd = desc_kmajor_sw128(w + 2 * kTileBytes);
 #pragma unroll
-            for (int tile = 0; tile < 2; ++tile) {
-                const uint64_t wd = desc_kmajor_sw128(w + tile * kTileBytes);
-                const uint32_t d = tmem_base + buf * C::kBufCols + tile * (C::kBufCols / 2);
+                for (int tile = 0; tile < 2; ++tile) {
+                    const uint64_t wd = desc_kmajor_sw128(w + tile * kTileBytes);
+                    const uint32_t d = tmem_base + buf * C::kBufCols + tile * (C::kBufCols / 2);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_f8(d, wd + 2 * k, xd + 2 * k, idesc, k > 0 ? 1u : 0u);
+                    for (int k = 0; k < 4; ++k)
+                        mma_f8(d, wd + 2 * k, xd + 2 * k, idesc, k > 0 ? 1u : 0u);
+                }
+                tc_commit(empty + stage);
+                tc_commit(tfull + buf);
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    ph ^= 1;
+                }
+                if (++buf == C::kBufs) {
+                    buf = 0;
+                    tph ^= 1;
+                }
+            };
+            for (int u = l1.first; u < l1.end && ok; ++u)
+                issue(n1);
+            for (Walk w(l2); w.u < l2.end && ok; w.step()) {
+                const int groups = (int)((chk[w.item % chunks] >> 22) + 7) / 8;
+                const int n2 = (24 * groups + 15) / 16 * 16;   // columns past the parts hold anything, and are not read
+                for (bool same = true; same && ok; same = w.stay())
+                    issue(n2);
             }
-            tc_commit(empty + stage);
-            tc_commit(tfull + buf);
-            if (++stage == C::kStages) {
-                stage = 0;
-                ph ^= 1;
-            }
-            if (++buf == C::kBufs) {
-                buf = 0;
-                tph ^= 1;
-            }
-        };
-        for (int u = l1.first; u < l1.end && ok; ++u)
-            issue(n1);
-        for (int u = l2.first; u < l2.end && ok; ++u) {
-            const int groups = (int)((chk[u / IB % chunks] >> 22) + 7) / 8;
-            issue((24 * groups + 15) / 16 * 16);   // columns past the parts hold anything, and are not read
-        }
-        tc_commit(final_bar);
-        wait_teardown(final_bar, prm.status, prm.timeout_ns);
-    } else if (warp == 2 && lane == 0) {
-        // ------------------------------------------------ tokens
-        int stage = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        auto next = [&] {
-            if (++stage == C::kStages) {
-                stage = 0;
-                ph ^= 1;
-            }
-        };
-        for (int u = l1.first; u < l1.end && ok; ++u, next()) {
-            ok = mbar_wait(empty + stage, ph ^ 1, abort_flag, prm.status, prm.timeout_ns, SITE_PRODUCER_EMPTY);
-            if (ok) {
-                mbar_arrive_expect_tx(full + stage, n1 * 128);
-                tma_load_2d(smem + stage * C::kStageBytes + 2 * kTileBytes, &prm.tmX, full + stage, u % HB * 128, 0);
-            }
-        }
-        // the hidden values of all CTAs, written through the generic proxy
-        ok = ok && mbar_wait(grid_bar + 1, 0, abort_flag, prm.status, prm.timeout_ns, SITE_GRID);
-        fence_async_all();
-        for (int u = l2.first; u < l2.end && ok; ++u, next()) {
-            ok = mbar_wait(empty + stage, ph ^ 1, abort_flag, prm.status, prm.timeout_ns, SITE_PRODUCER_EMPTY);
-            if (ok) {
-                const uint32_t c = chk[u / IB % chunks];
-                const int groups = (int)((c >> 22) + 7) / 8, first = (int)(c >> 10 & 0xFFF);
-                uint8_t *x = smem + stage * C::kStageBytes + 2 * kTileBytes;
-                mbar_arrive_expect_tx(full + stage, 3 * groups * 1024);
-                for (int part = 0; part < 3; ++part)
-                    for (int i = 0; i < groups; ++i)
-                        tma_load_2d(x + (part * groups + i) * 1024, &prm.tmParts, full + stage, u % IB * 128,
-                                    (int)(part * rows3) + first + i * 8);
-            }
-        }
-    } else if (warp == 3 && lane == 0) {
-        // ------------------------------------------------ the grid's barriers
-        bool ok = true;
-        for (int b = 0; b < 3 && ok; ++b) {
-            ok = mbar_wait(epi_bar, b & 1, abort_flag, prm.status, prm.timeout_ns, SITE_GRID);
-            if (!ok)
-                break;
-            red_release_add(prm.counters, 1u);   // releases what the promotion warps wrote before they arrived
-            const uint32_t want = (uint32_t)(b + 1) * gridDim.x;
-            const uint64_t t0 = globaltimer();
-            while (ld_acquire(prm.counters) < want) {
-                if (*abort_flag || globaltimer() - t0 > prm.timeout_ns) {
-                    if (!*abort_flag) {
-                        *abort_flag = 1;
-                        report(prm.status, kErrTimeout, SITE_GRID);
-                    }
-                    ok = false;
-                    break;
+            tc_commit(final_bar);
+            wait_teardown(final_bar, prm.status, prm.timeout_ns);
+        } else if (warp == 2 && lane == 0) {
+            // ------------------------------------------------ tokens
+            int stage = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            auto next = [&] {
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    ph ^= 1;
+                }
+            };
+            for (Walk w(l1); w.u < l1.end && ok; w.advance(), next()) {
+                ok = mbar_wait(empty + stage, ph ^ 1, abort_flag, prm.status, prm.timeout_ns, SITE_PRODUCER_EMPTY);
+                if (ok) {
+                    mbar_arrive_expect_tx(full + stage, n1 * 128);
+                    tma_load_2d(smem + stage * C::kStageBytes + 2 * kTileBytes, &prm.tmX, full + stage, w.kb * 128, 0);
                 }
             }
-            if (ok)
-                mbar_arrive(grid_bar + b);
+            // the hidden values of all CTAs, written through the generic proxy
+            ok = ok && mbar_wait(grid_bar + 1, 0, abort_flag, prm.status, prm.timeout_ns, SITE_GRID);
+            fence_async_all();
+            for (Walk w(l2); w.u < l2.end && ok; w.step()) {
+                const uint32_t c = chk[w.item % chunks];
+                const int groups = (int)((c >> 22) + 7) / 8, first = (int)(c >> 10 & 0xFFF);
+                for (bool same = true; same && ok; same = w.stay(), next()) {
+                    ok = mbar_wait(empty + stage, ph ^ 1, abort_flag, prm.status, prm.timeout_ns, SITE_PRODUCER_EMPTY);
+                    if (!ok)
+                        break;
+                    uint8_t *x = smem + stage * C::kStageBytes + 2 * kTileBytes;
+                    mbar_arrive_expect_tx(full + stage, 3 * groups * 1024);
+                    for (int part = 0; part < 3; ++part)
+                        for (int i = 0; i < groups; ++i)
+                            tma_load_2d(x + (part * groups + i) * 1024, &prm.tmParts, full + stage, w.kb * 128,
+                                        (int)(part * rows3) + first + i * 8);
+                }
+            }
+        } else if (warp == 3 && lane == 0) {
+            // ------------------------------------------------ the grid's barriers
+            bool ok = true;
+            for (int b = 0; b < 3 && ok; ++b) {
+                ok = mbar_wait(epi_bar, b & 1, abort_flag, prm.status, prm.timeout_ns, SITE_GRID);
+                if (!ok)
+                    break;
+                red_release_add(prm.counters, 1u);   // releases what the promotion warps wrote before they arrived
+                const uint32_t want = (uint32_t)(b + 1) * gridDim.x;
+                const uint64_t t0 = globaltimer();
+                while (ld_acquire(prm.counters) < want) {
+                    if (*abort_flag || globaltimer() - t0 > prm.timeout_ns) {
+                        if (!*abort_flag) {
+                            *abort_flag = 1;
+                            report(prm.status, kErrTimeout, SITE_GRID);
+                        }
+                        ok = false;
+                        break;
+                    }
+                }
+                if (ok)
+                    mbar_arrive(grid_bar + b);
+            }
+            // the last CTA past the last barrier leaves the counters as the next call expects them
+            if (ok && atomicAdd(prm.counters + 1, 1u) == gridDim.x - 1) {
+                prm.counters[0] = 0;
+                prm.counters[1] = 0;
+            }
         }
-        // the last CTA past the last barrier leaves the counters as the next call expects them
-        if (ok && atomicAdd(prm.counters + 1, 1u) == gridDim.x - 1) {
-            prm.counters[0] = 0;
-            prm.counters[1] = 0;
-        }
-    } else if (warp >= 4) {
+    } else {
+        setmaxnreg_inc<kRegsHigh>();
         // ------------------------------------------------ promotion
         const int q = warp & 3, h = (warp - 4) >> 2;   // lane quarter, tile of the pair
         const int row = q * 32 + lane;
@@ -457,11 +500,26 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 mbar_arrive(epi_bar);
             ok = mbar_wait(grid_bar + b, 0, abort_flag, prm.status, prm.timeout_ns, SITE_GRID);
         };
-        // scales of the tokens at columns lane, lane + 32, ..., and the weights', a unit ahead
+        // Scales of the tokens, a unit ahead: column lane + 32 i at from + at[i] + kb, the weights' at
+        // from_sw + kb.  The product of both goes to the warp's own shared memory, from where each
+        // thread reads all of them.
         constexpr int PER = (C::kAcc + 31) / 32;
-        float next_ts[PER], next_sw;
+        const float *from = a.sx, *from_sw = nullptr;
+        int at[PER];   // -1: no token at this column
+        float next_ts[PER], next_sw = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            at[i] = -1;
+            next_ts[i] = 0.0f;
+        }
+        auto fetch = [&](int kb) {
+            next_sw = __ldg(from_sw + kb);
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                next_ts[i] = at[i] >= 0 ? ld_after_f32(from + at[i] + kb) : 0.0f;
+        };
         auto stage_scales = [&](int u) {
-            float *now = ts + (u & 1) * C::kAcc;   // the warp's own: read by it two units back
+            float *now = ts + (u & 1) * C::kAcc;   // read last two units back
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 if (lane + 32 * i < C::kAcc)
@@ -470,100 +528,117 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         };
 
         // -------- first product.  Of an expert with few tokens only their columns are read, the
-        // j-th token's sum in acc[j]; of one with many all, a token's in acc[token].
-        int item = -1, ia = 0, first = 0, n = 0;
-        constexpr bool kAlways = C::NT <= kSparse;   // there are no more tokens than that
-        bool sparse = true;
-        int list = 0;   // the expert's token at place `lane`
-        auto enter1 = [&](int u) {
-            item = u / HB;
-            ia = item / IB;
-            first = (int)(act[ia] >> 10);
-            n = (int)(act[ia + 1] >> 10) - first;
-            sparse = kAlways || n <= kSparse;
-            list = lane < n ? (int)(pair[first + lane] & 127) : 0;
-        };
-        auto fetch1 = [&](int u) {
-            const int next_item = u / HB, kb = u % HB, e = act[next_item / IB] & 1023;
-            next_sw = __ldg(a.s13 + ((int64_t)e * 2 * IB + h * IB + next_item % IB) * HB + kb);
-            const int at = (int)(act[next_item / IB] >> 10), count = (int)(act[next_item / IB + 1] >> 10) - at;
-            if (kAlways || count <= kSparse) {
-                next_ts[0] = lane < count ? __ldg(a.sx + (int64_t)(pair[at + lane] & 127) * HB + kb) : 0.0f;
+        // j-th token's sum in acc[j]; of one with more all, a token's in acc[token].  Where there
+        // are 8 tokens at most, all.
+        constexpr bool kAll = C::NT <= 16;
+        constexpr int kDense = kAll ? 8 : C::NT;
+        constexpr int kPick = kAll ? 8 : kSparse;
+        int first = 0, n = 0;
+        bool sparse = false;
+        uint32_t column[kPick];
+        auto point1 = [&](int item) {
+            const int ia = item / IB;
+            const uint32_t e = act[ia];
+            from_sw = a.s13 + ((int64_t)(e & 1023) * 2 * IB + h * IB + (item - ia * IB)) * HB;
+            const int begin = (int)(e >> 10), count = (int)(act[ia + 1] >> 10) - begin;
+            if (!kAll && count <= kSparse) {
+                at[0] = lane < count ? (int)(pair[begin + lane] & 127) * HB : -1;
+#pragma unroll
+                for (int i = 1; i < PER; ++i)
+                    at[i] = -1;
             } else {
 #pragma unroll
                 for (int i = 0; i < PER; ++i)
-                    next_ts[i] = lane + 32 * i < a.T ? __ldg(a.sx + (int64_t)(lane + 32 * i) * HB + kb) : 0.0f;
+                    at[i] = lane + 32 * i < a.T ? (lane + 32 * i) * HB : -1;
             }
         };
+        auto enter1 = [&](int item) {
+            const int ia = item / IB;
+            first = (int)(act[ia] >> 10);
+            n = (int)(act[ia + 1] >> 10) - first;
+            if (!kAll) {
+                sparse = n <= kSparse;
+                const int list = lane < n ? (int)(pair[first + lane] & 127) : 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            next_ts[i] = 0.0f;
-        if (l1.first < l1.end)
-            fetch1(l1.first);
-        for (int u = l1.first; u < l1.end; ++u) {
-            if (u == l1.first || u % HB == 0) {
-                enter1(u);
-#pragma unroll
-                for (int j = 0; j < C::kAcc; ++j)
-                    acc[j] = 0.0f;
+                for (int j = 0; j < kPick; ++j)   // past the last token: a column nobody asked for, unused
+                    column[j] = taddr0 + __shfl_sync(0xffffffffu, list, j);
             }
-            const float *now = stage_scales(u);
-            if (u + 1 < l1.end)
-                fetch1(u + 1);
+#pragma unroll
+            for (int j = 0; j < C::kAcc; ++j)
+                acc[j] = 0.0f;
+        };
+        Walk w1(l1);
+        if (w1.u < l1.end) {
+            point1(w1.item);
+            fetch(w1.kb);
+        }
+        for (bool fresh = true; w1.u < l1.end; w1.advance()) {
+            if (fresh)
+                enter1(w1.item);
+            const float *now = stage_scales(w1.u);
+            const bool last = fresh = w1.last_of_item();
+            if (!last) {
+                fetch(w1.kb + 1);
+            } else if (w1.u + 1 < l1.end) {
+                point1(w1.item + 1);
+                fetch(0);
+            }
             ok = mbar_wait(tfull + buf, tph, abort_flag, prm.status, prm.timeout_ns, SITE_EPI_TMEM_FULL);
             if (!ok)
                 break;
             __syncwarp();
             tc_fence_after();
-            const uint32_t taddr = taddr0 + buf * C::kBufCols;
             if (sparse) {
+                uint32_t r[kPick];
 #pragma unroll
-                for (int c = 0; c < kSparse; c += 8)
+                for (int c = 0; c < kPick; c += 8)
                     if (c < n) {
-                        uint32_t r[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)   // past the last token: the first one's, unused
-                            tmem_ld_x1(taddr + __shfl_sync(0xffffffffu, list, c + j), r[j]);
-                        tmem_wait_ld(r);
-                        float d[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            d[j] = __uint_as_float(r[j]);
-                        promote8(acc + c, d, now + c);
+                            tmem_ld_x1(column[c + j] + buf * C::kBufCols, r[c + j]);
                     }
+#pragma unroll
+                for (int c = 0; c < kPick; c += 8)
+                    if (c < n) {
+                        uint32_t(&v)[8] = *reinterpret_cast<uint32_t(*)[8]>(&r[c]);
+                        tmem_wait_ld(v);
+                        promote8(acc + c, v, now + c);
+                    }
+            } else if (kAll) {
+                uint32_t r[8];
+                tmem_ld_x8(taddr0 + buf * C::kBufCols, r);
+                tmem_wait_ld(r);
+                promote8(acc, r, now);
             } else {
 #pragma unroll
-                for (int c = 0; c < C::NT; c += 16)
+                for (int c = 0; c < kDense; c += 16)
                     if (c < a.T) {
                         uint32_t r[16];
-                        tmem_ld_x16(taddr + c, r);
+                        tmem_ld_x16(taddr0 + buf * C::kBufCols + c, r);
                         tmem_wait_ld(r);
-                        float d[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            d[j] = __uint_as_float(r[j]);
-                        promote8(acc + c, d, now + c);
-                        promote8(acc + c + 8, d + 8, now + c + 8);
+                        promote8(acc + c, *reinterpret_cast<uint32_t(*)[8]>(&r[0]), now + c);
+                        promote8(acc + c + 8, *reinterpret_cast<uint32_t(*)[8]>(&r[8]), now + c + 8);
                     }
             }
             release();
-            if (u % HB == HB - 1 || u + 1 == l1.end) {
-                float *to = prm.pieces + ((int64_t)l1.plane(item) * pairs + first) * (2 * a.I) + h * a.I + item % IB * 128 + row;
+            if (last) {
+                const int ia = w1.item / IB, jb = w1.item - ia * IB;
+                float *to = prm.pieces + ((int64_t)l1.plane(w1.item) * pairs + first) * (2 * a.I) + h * a.I + jb * 128 + row;
                 if (sparse) {
 #pragma unroll
-                    for (int j = 0; j < kSparse; ++j)
+                    for (int j = 0; j < kPick; ++j)
                         if (j < n)
                             __stcg(to + (int64_t)j * 2 * a.I, acc[j]);
                 } else {
-                    uint32_t mask[(C::NT + 31) / 32] = {};
+                    uint32_t mask[(kDense + 31) / 32] = {};
                     for (int i = 0; i < n; i += 32) {
                         const uint32_t t = i + lane < n ? pair[first + i + lane] & 127 : 0xFFFFu;
 #pragma unroll
-                        for (int w = 0; w < (C::NT + 31) / 32; ++w)
+                        for (int w = 0; w < (kDense + 31) / 32; ++w)
                             mask[w] |= __reduce_or_sync(0xffffffffu, t >> 5 == (uint32_t)w ? 1u << (t & 31) : 0u);
                     }
 #pragma unroll
-                    for (int j = 0; j < C::NT; ++j)
+                    for (int j = 0; j < kDense; ++j)
                         if (mask[j >> 5] >> (j & 31) & 1) {
                             __stcg(to, acc[j]);
                             to += 2 * a.I;
@@ -576,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             everyone(0);
         if (ok) {
             const int groups = pairs * IB;
-            for (int i = blockIdx.x * 8 + warp - 4; i < groups; i += gridDim.x * 8) {
+            for (int i = (warp - 4) * gridDim.x + blockIdx.x; i < groups; i += gridDim.x * 8) {
                 const int p = i / IB, jb = i % IB;
                 const uint32_t info = pair[p];
                 const int t = (int)(info & 127), ia = (int)(info >> 7 & 1023), e = (int)(act[ia] & 1023);
@@ -632,83 +707,92 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             everyone(1);
         }
         // -------- second product
-        auto fetch2 = [&](int u) {
-            const int item = u / IB, kb = u % IB;
-            const uint32_t c = chk[item % chunks];
-            const int64_t block = min(item / chunks * 2 + h, HB - 1);
-            next_sw = __ldg(a.s2 + ((int64_t)(c & 1023) * HB + block) * IB + kb);
-            const int at = (int)(c >> 10 & 0xFFF), count = (int)(c >> 22);
+        auto point2 = [&](int item) {
+            const int j = item / chunks;
+            const uint32_t c = chk[item - j * chunks];
+            from_sw = a.s2 + ((int64_t)(c & 1023) * HB + min(j * 2 + h, HB - 1)) * IB;
+            const int begin = (int)(c >> 10 & 0xFFF), count = (int)(c >> 22);
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                next_ts[i] = lane + 32 * i < count ? ld_after_f32(prm.hidden_scale + (int64_t)(at + lane + 32 * i) * IB + kb) : 0.0f;
+                at[i] = lane + 32 * i < count ? (begin + lane + 32 * i) * IB : -1;
         };
+        from = prm.hidden_scale;
         __syncwarp();
-        if (ok && l2.first < l2.end)
-            fetch2(l2.first);
-        for (int u = l2.first; u < l2.end && ok; ++u) {
-            if (u == l2.first || u % IB == 0) {
+        Walk w2(l2);
+        if (ok && w2.u < l2.end) {
+            point2(w2.item);
+            fetch(w2.kb);
+        }
+        int groups = 0;
+        for (bool fresh = true; w2.u < l2.end && ok; w2.advance()) {
+            if (fresh) {
+                const uint32_t c = chk[w2.item % chunks];
+                first = (int)(c >> 10 & 0xFFF);
+                n = (int)(c >> 22);
+                groups = (n + 7) / 8;
 #pragma unroll
                 for (int j = 0; j < 8 * C::GROUPS; ++j)
                     acc[j] = 0.0f;
             }
-            const float *now = stage_scales(u);
-            if (u + 1 < l2.end)
-                fetch2(u + 1);
+            const float *now = stage_scales(w2.u);
+            const bool last = fresh = w2.last_of_item();
+            if (!last) {
+                fetch(w2.kb + 1);
+            } else if (w2.u + 1 < l2.end) {
+                point2(w2.item + 1);
+                fetch(0);
+            }
             ok = mbar_wait(tfull + buf, tph, abort_flag, prm.status, prm.timeout_ns, SITE_EPI_TMEM_FULL);
             if (!ok)
                 break;
             __syncwarp();
             tc_fence_after();
-            item = u / IB;
-            const uint32_t c = chk[item % chunks];
-            first = (int)(c >> 10 & 0xFFF);
-            n = (int)(c >> 22);
-            const int groups = (n + 7) / 8;
             const uint32_t taddr = taddr0 + buf * C::kBufCols;
 #pragma unroll
             for (int i = 0; i < C::GROUPS; ++i)
                 if (i < groups) {
-                    uint32_t r0[8], r1[8], r2[8];
+                    uint32_t r0[8], r1[8], r2[8], d[8];
                     tmem_ld_x8(taddr + i * 8, r0);
                     tmem_ld_x8(taddr + (groups + i) * 8, r1);
                     tmem_ld_x8(taddr + (2 * groups + i) * 8, r2);
                     tmem_wait_ld(r0, r1);
-                    tmem_wait_ld(r2, r2);
-                    float d[8];
+                    tmem_wait_ld(r2);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        d[j] = fmaf(__uint_as_float(r2[j]), 0x1p-9f, fmaf(__uint_as_float(r1[j]), 0x1p-4f, __uint_as_float(r0[j])));
+                        d[j] = __float_as_uint(fmaf(__uint_as_float(r2[j]), 0x1p-9f, fmaf(__uint_as_float(r1[j]), 0x1p-4f, __uint_as_float(r0[j]))));
                     promote8(acc + i * 8, d, now + i * 8);
                 }
             release();
-            if ((u % IB == IB - 1 || u + 1 == l2.end) && item / chunks * 2 + h < HB) {
-                float *to = prm.pieces + ((int64_t)l2.plane(item) * pairs + first) * a.H + (item / chunks * 2 + h) * 128 + row;
+            const int block = w2.item / chunks * 2 + h;
+            if (last && block < HB) {
+                float *to = prm.pieces + ((int64_t)l2.plane(w2.item) * pairs + first) * a.H + block * 128 + row;
 #pragma unroll
                 for (int j = 0; j < 8 * C::GROUPS; ++j)
                     if (j < n)
                         __stcg(to + (int64_t)j * a.H, acc[j]);
             }
         }
+        const uint32_t quads = a.H / 4;   // a multiple of 32: a warp's are of one token
+        const uint32_t quad0 = ((warp - 4) * gridDim.x + blockIdx.x) * 32 + lane;
+        if (a.y != nullptr && quad0 < a.T * quads)
+            prefetch_l2(a.y + quad0 / quads * a.ys + quad0 % quads * 4);
         if (ok)
             everyone(2);
         // -------- rows of out: four columns at a time, a token's experts in the order of its slots
         if (ok) {
-            const int quads = a.H / 4;
-            for (int64_t i = (int64_t)blockIdx.x * kEpiThreads + threadIdx.x - 128; i < (int64_t)a.T * quads;
-                 i += (int64_t)gridDim.x * kEpiThreads) {
+            for (uint32_t i = quad0; i < a.T * quads; i += gridDim.x * kEpiThreads) {
                 const int t = (int)(i / quads), col = (int)(i % quads) * 4;
-                float4 sum = make_float4(0, 0, 0, 0);
-                if (a.y != nullptr) {
-                    const uint2 y = *reinterpret_cast<const uint2 *>(a.y + t * a.ys + col);
-                    sum = make_float4(bf16_lo(y.x), bf16_hi(y.x), bf16_lo(y.y), bf16_hi(y.y));
-                }
-                // four slots' loads under way at a time
+                uint2 y = make_uint2(0, 0);
+                if (a.y != nullptr)
+                    y = *reinterpret_cast<const uint2 *>(a.y + t * a.ys + col);
+                float4 sum = make_float4(bf16_lo(y.x), bf16_hi(y.x), bf16_lo(y.y), bf16_hi(y.y));
+                // kTake slots' loads under way at a time
                 const int64_t plane = (int64_t)pairs * a.H;
-                for (int s0 = 0; s0 < a.k; s0 += 4) {
-                    float4 v[4], w[4];
-                    int planes[4];
+                for (int s0 = 0; s0 < a.k; s0 += kTake) {
+                    float4 v[kTake], w[kTake];
+                    int planes[kTake];
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
+                    for (int s = 0; s < kTake; ++s) {
                         const uint32_t p = s0 + s < a.k ? slot[t * a.k + s0 + s] : 0xFFFFu;
                         planes[s] = p == 0xFFFFu ? 0 : l2.planes(col / 256 * chunks + (int)(pair[p] >> 17));
                         const float *from = prm.pieces + (int64_t)p * a.H + col;
@@ -716,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                         w[s] = planes[s] > 1 ? ld4(from + plane) : make_float4(0, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
+                    for (int s = 0; s < kTake; ++s) {
                         if (planes[s] > 0)
                             sum = add4(sum, v[s]);
                         if (planes[s] > 1)
@@ -749,6 +833,12 @@ template <class C>
 cudaError_t launch_typed(const MoeParams &p, int num_sms, cudaStream_t st)
 {
     const void *kernel = reinterpret_cast<const void *>(moe_kernel<C>);
+    static const int regs = [&] {   // of the one image there is
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (regs * kThreads < kRegsNeeded)
+        return cudaErrorInvalidConfiguration;   // setmaxnreg would wait forever
     const cudaError_t e = ensure_dynamic_smem(kernel, C::kSmemBytes);
     if (e != cudaSuccess)
         return e;
