@@ -15,7 +15,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libgemmar.so")
 BINDING_PATH = os.path.join(PKG, "_operators.so")
 SOURCES = ["gemm_blockscale.cu", "gemm_blockscale_2sm.cu", "gemm_mx.cu", "streaming.cu", "gemmar.cu", "noalloc.cu",
-           "residual.cu", "lora.cu", "lora_tile.cu", "gemm_act.cu", "act_bwd.cu", "moe_route.cu", "moe.cu"]
+           "residual.cu", "lora.cu", "lora_tile.cu", "gemm_act.cu", "gemm_act_few.cu", "act_bwd.cu", "moe_route.cu", "moe.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -842,11 +842,12 @@ GEMMAR_API int gemm_blockscale_act(gemmar_ctx *ctx, const uint8_t *A, const floa
         return GEMMAR_ERR_ALIGN;
     if (!load_encode())
         return GEMMAR_ERR_CUDA;
-    if (!gemm_act_split_ok())
+    const bool few = M <= 128;
+    if (!few && !gemm_act_split_ok())
         return GEMMAR_ERR_DEVICE;
     ActParams p;
     std::memset(&p, 0, sizeof(p));
-    if (!make_tmap_u8(&p.tmA, A, M, K, 128) || !make_tmap_u8(&p.tmB, B, gated ? 2 * N : N, K, 128))
+    if (!make_tmap_u8(&p.tmA, A, M, K, few ? gemm_act_few_rows((int)M) : 128) || !make_tmap_u8(&p.tmB, B, gated ? 2 * N : N, K, 128))
         return GEMMAR_ERR_CUDA;
     p.sa = sa;
     p.sb = sb;
@@ -854,7 +855,7 @@ GEMMAR_API int gemm_blockscale_act(gemmar_ctx *ctx, const uint8_t *A, const floa
                       C, c_dtype == GEMMAR_DTYPE_BF16, c_stride, q, scales, z};
     p.status = ctx->status;
     p.timeout_ns = ctx->timeout_ns;
-    CUDA_OK(launch_gemm_act(p, ctx->num_sms, as_stream(stream)));
+    CUDA_OK(few ? launch_gemm_act_few(p, ctx->num_sms, as_stream(stream)) : launch_gemm_act(p, ctx->num_sms, as_stream(stream)));
     return GEMMAR_OK;
 }
 

@@ -32,23 +32,16 @@
 #include "activation.cuh"
 #include "e4m3_encode.cuh"
 #include "epilogue.cuh"
+#include "few_rows.cuh"
 
 namespace gemmar {
 using namespace ptx;
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kEpiThreads = 256;
-constexpr int kTileBytes = 128 * 128;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxSlots = 16;
 constexpr int kTake = 8;
-constexpr int kRegsLow = 56;     // warps 0-3 after setmaxnreg.dec
-constexpr int kRegsHigh = 224;   // promotion warps after setmaxnreg.inc
-constexpr int kRegsNeeded = 128 * kRegsLow + kEpiThreads * kRegsHigh;
-constexpr int kSparse = 16;      // tokens of an expert up to which the first product's columns are picked
-constexpr uint32_t kAbortGraceNs = 200000;   // let copies in flight land before an aborting CTA exits
 
 // NT: token columns of the first product; GROUPS: groups of 8 tokens in a chunk of the second.
 template <int NT_, int GROUPS_, int STAGES_, int BUFS_>
@@ -59,6 +52,7 @@ struct Cfg {
     static constexpr int kCols = NT > (24 * GROUPS + 15) / 16 * 16 ? NT : (24 * GROUPS + 15) / 16 * 16;   // per tile
     static constexpr int kBufCols = kCols <= 32 ? 64 : kCols <= 64 ? 128 : 256;   // both tiles
     static constexpr int kTmemCols = kBufCols * kBufs;
+    static constexpr int kSparse = NT >= 64 ? 32 : 16;   // tokens of an expert up to which its columns are picked
     static constexpr int kAcc = NT > 8 * GROUPS ? NT : 8 * GROUPS;
     static constexpr int kPairs = NT * kMaxSlots;
     static constexpr int kActive = kPairs < kMaxExperts ? kPairs : kMaxExperts;
@@ -242,16 +236,6 @@ __device__ void make_plan(const MoeArgs &a, uint8_t *smem, int &active, int &chu
         slot[i] = (uint16_t)at;
     }
     fence_async_shared();   // the ring's first copies come after this scratch
-}
-
-// acc[j] += (sum of column j) * (weight scale * token scale j) for 8 columns
-__device__ __forceinline__ void promote8(float *acc, const uint32_t (&d)[8], const float *ts)
-{
-    const float4 a = *reinterpret_cast<const float4 *>(ts), b = *reinterpret_cast<const float4 *>(ts + 4);
-    fma2(acc[0], acc[1], __uint_as_float(d[0]), __uint_as_float(d[1]), a.x, a.y);
-    fma2(acc[2], acc[3], __uint_as_float(d[2]), __uint_as_float(d[3]), a.z, a.w);
-    fma2(acc[4], acc[5], __uint_as_float(d[4]), __uint_as_float(d[5]), b.x, b.y);
-    fma2(acc[6], acc[7], __uint_as_float(d[6]), __uint_as_float(d[7]), b.z, b.w);
 }
 
 __device__ __forceinline__ float max4(const float4 &v) { return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))); }
@@ -532,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         // are 8 tokens at most, all.
         constexpr bool kAll = C::NT <= 16;
         constexpr int kDense = kAll ? 8 : C::NT;
-        constexpr int kPick = kAll ? 8 : kSparse;
+        constexpr int kPick = kAll ? 8 : C::kSparse;
         int first = 0, n = 0;
         bool sparse = false;
         uint32_t column[kPick];
@@ -541,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             const uint32_t e = act[ia];
             from_sw = a.s13 + ((int64_t)(e & 1023) * 2 * IB + h * IB + (item - ia * IB)) * HB;
             const int begin = (int)(e >> 10), count = (int)(act[ia + 1] >> 10) - begin;
-            if (!kAll && count <= kSparse) {
+            if (!kAll && count <= C::kSparse) {
                 at[0] = lane < count ? (int)(pair[begin + lane] & 127) * HB : -1;
 #pragma unroll
                 for (int i = 1; i < PER; ++i)
@@ -557,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             first = (int)(act[ia] >> 10);
             n = (int)(act[ia + 1] >> 10) - first;
             if (!kAll) {
-                sparse = n <= kSparse;
+                sparse = n <= C::kSparse;
                 const int list = lane < n ? (int)(pair[first + lane] & 127) : 0;
 #pragma unroll
                 for (int j = 0; j < kPick; ++j)   // past the last token: a column nobody asked for, unused
@@ -833,12 +817,9 @@ template <class C>
 cudaError_t launch_typed(const MoeParams &p, int num_sms, cudaStream_t st)
 {
     const void *kernel = reinterpret_cast<const void *>(moe_kernel<C>);
-    static const int regs = [&] {   // of the one image there is
-        cudaFuncAttributes f;
-        return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
-    }();
-    if (regs * kThreads < kRegsNeeded)
-        return cudaErrorInvalidConfiguration;   // setmaxnreg would wait forever
+    static const bool split_ok = few_rows_split_ok(kernel);
+    if (!split_ok)
+        return cudaErrorInvalidConfiguration;
     const cudaError_t e = ensure_dynamic_smem(kernel, C::kSmemBytes);
     if (e != cudaSuccess)
         return e;
