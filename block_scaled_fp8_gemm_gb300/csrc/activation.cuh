@@ -16,8 +16,9 @@ enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GEL
 constexpr float kSqrt2OverPi = 0.7978845608028654f;
 constexpr float kGeluCubic = 0.044715f;
 
-// 1 / (1 + exp(-z)); the divisor is at least 1, and an infinite one gives 0
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + expf(-z)); }
+// 1 / (1 + exp(-z)); the divisor is at least 1, and an infinite one gives 0.  The fast exponential rounds
+// z / ln 2 once, which costs (2 + |z|) 2^-24 of its value: less than the sums before it.
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float z)

@@ -6,12 +6,19 @@
 //
 // Bound by the tensor cores and, before them, by the promotion: the block scales change every
 // 128 of K, so each of a tile's 128 x 256 sums is read from TMEM and multiplied-added in fp32
-// once per K-block.  The kernel is laid out for that as gemm_blockscale.cu is: one persistent
-// CTA per SM, a TMA producer warp, an MMA warp, two TMEM accumulators, and eight epilogue
-// warps whose threads keep one row and 128 columns in registers.  A gated tile holds 128
-// columns of each half, and a thread the same 64 of both, so the gate needs nothing from
-// another thread.  What follows the product never leaves the registers except as the
-// call's outputs.
+// once per K-block.  One persistent CTA per SM, 16 warps:
+//   warp 0      TMA producer: A tile 128x128 and B rows 2 x 128 per 128-K stage
+//   warp 1      MMA issuer, 128 x 256 x 32 each into one of two TMEM buffers (two MMAs of 128
+//               columns with two buffers each, for a finer overlap, ran at 0.69 of the rate)
+//   warps 4-11  promotion: a thread keeps one row and 128 columns in registers; at tile end they
+//               go back into the TMEM buffer of the last K-block (a "park").  While it is parked
+//               the next tile's K-blocks run in the other buffer, one by one, so the MMA warp
+//               takes for each the buffer that is free and leaves on record which
+//   warps 12-15 finish: one per TMEM lane quarter, a thread per row.  They take a parked tile 32
+//               columns at a time through bias, activation, gate, residual and the stores, while
+//               the next tile is promoted.  A thread reads and writes its own row in whole
+//               32-byte sectors, with no staging and nothing to wait for but the residual, which
+//               it asks for a block of columns, and into L2 a tile, ahead
 #include <algorithm>
 
 #include "activation.cuh"
@@ -23,25 +30,23 @@ using namespace ptx;
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kStages = 4;
 constexpr int kABytes = 128 * 128;
 constexpr int kBBytes = 256 * 128;
 constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kEpiWarps = 8;
+constexpr int kSteps = 4;        // K-steps whose buffer is on record: more than can be under way
 constexpr int kOffB = kStages * kABytes;
-constexpr int kOffStaging = kOffB + kStages * kBBytes;   // 4 KB per epilogue warp
-constexpr int kOffMax = kOffStaging + kEpiWarps * 4096;  // a gated row's maximum, per column half
-constexpr int kOffBar = kOffMax + 2 * 128 * 4;
-constexpr int kNumBars = 2 * kStages + 5 + 4;
+constexpr int kOffBar = kOffB + kStages * kBBytes;
+constexpr int kNumBars = 2 * kStages + kSteps + 5;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
-constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+constexpr int kSmemBytes = kOffMisc + 8 + 4 * kSteps + 8 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-constexpr int kRegsLow = 56;     // warps 0-3 after setmaxnreg.dec
-constexpr int kRegsHigh = 224;   // epilogue warps after setmaxnreg.inc
-constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsHigh;
+// setmaxnreg: warps 0-3, promotion, finish, of 128 a thread
+constexpr int kRegsLow = 40, kRegsPromote = 184, kRegsFinish = 104;
+constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsPromote + 128 * kRegsFinish;
+static_assert(kRegsNeeded <= 65536, "register split");
 constexpr int kGroupM = 16;      // row tiles that share their columns of B while they are in L2
-
 struct Tile {
     int m0, n0;
 };
@@ -55,50 +60,73 @@ __device__ __forceinline__ Tile decode(int t, int mt_total, int ntiles, int bn)
     return {(m_first + idx % gm) * 128, (idx / gm) * bn};
 }
 
-// The reverse of store_chunk: each thread gets UNITS 16-byte units of its own row, which the
-// warp reads row-contiguously.  Rows past rows_valid read as zero.
-template <int UNITS>
-__device__ __forceinline__ void load_chunk(uint32_t stage, uint4 (&v)[UNITS], const char *gsrc, int64_t row_stride_bytes,
-                                           int rows_valid)
+// 32 bytes of a row at a 16-byte boundary; `whole`: at a 32-byte one
+__device__ __forceinline__ void load32(const char *p, bool whole, uint32_t *r)
 {
-    constexpr int ROWB = UNITS * 16, RPI = 32 / UNITS;
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < UNITS; ++i) {
-        const int r = i * RPI + lane / UNITS, u = lane % UNITS;
-        const int rsw = (UNITS == 8) ? (r & 7) : ((r >> 1) & 3);
-        uint4 val = make_uint4(0, 0, 0, 0);
-        if (r < rows_valid)
-            val = *reinterpret_cast<const uint4 *>(gsrc + r * row_stride_bytes + u * 16);
-        st_shared_v4(stage + r * ROWB + ((u ^ rsw) * 16), val);
+    if (whole)
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "l"(p)
+                     : "memory");
+    else {
+        const uint4 a = ld_after_v4(p), b = ld_after_v4(p + 16);
+        r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
+        r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
     }
-    __syncwarp();
-    const int sw = (UNITS == 8) ? (lane & 7) : ((lane >> 1) & 3);
-#pragma unroll
-    for (int u = 0; u < UNITS; ++u)
-        v[u] = ld_shared_v4(stage + lane * ROWB + ((u ^ sw) * 16));
-    __syncwarp();
 }
 
-// 32 columns of a thread's row to global memory, as bf16 or fp32.
-__device__ __forceinline__ void store_cols32(uint32_t staging, const float *a, bool bf16, char *dst, int64_t stride,
-                                             int rows_valid)
+__device__ __forceinline__ void store32(char *p, bool whole, const uint32_t *r)
+{
+    if (whole)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                     "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    }
+}
+
+// 32 columns of a thread's row as bf16 or fp32
+__device__ __forceinline__ void store_cols(char *p, bool whole, bool bf16, const float *v)
 {
     if (bf16) {
-        uint4 v[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            v[u] = make_uint4(bf16x2_from_f32(a[8 * u], a[8 * u + 1]), bf16x2_from_f32(a[8 * u + 2], a[8 * u + 3]),
-                              bf16x2_from_f32(a[8 * u + 4], a[8 * u + 5]), bf16x2_from_f32(a[8 * u + 6], a[8 * u + 7]));
-        store_chunk<4>(staging, v, dst, stride * 2, rows_valid);
+        for (int i = 0; i < 2; ++i) {
+            uint32_t r[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                r[j] = bf16x2_from_f32(v[16 * i + 2 * j], v[16 * i + 2 * j + 1]);
+            store32(p + 32 * i, whole, r);
+        }
     } else {
-        uint4 v[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            v[u] = make_uint4(__float_as_uint(a[4 * u]), __float_as_uint(a[4 * u + 1]), __float_as_uint(a[4 * u + 2]),
-                              __float_as_uint(a[4 * u + 3]));
-        store_chunk<8>(staging, v, dst, stride * 4, rows_valid);
+        for (int i = 0; i < 4; ++i)
+            store32(p + 32 * i, whole, reinterpret_cast<const uint32_t *>(v + 8 * i));
     }
+}
+
+// 32 columns of the park plus the bias at `bias` (nullptr: none)
+__device__ __forceinline__ void load_park(uint32_t taddr, const float *bias, float (&v)[32])
+{
+    uint32_t(&r)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v);
+    tmem_ld_x32(taddr, r);
+    tmem_wait_ld(r);
+    if (bias != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 b = __ldg(reinterpret_cast<const float4 *>(bias) + j);
+            v[4 * j] += b.x;
+            v[4 * j + 1] += b.y;
+            v[4 * j + 2] += b.z;
+            v[4 * j + 3] += b.w;
+        }
+    }
+}
+
+__device__ __forceinline__ bool whole32(const void *p, int64_t row_bytes)
+{
+    return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)row_bytes) & 31) == 0;
 }
 
 template <bool GATED>
@@ -109,12 +137,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
     uint8_t *smem = align1024(smem_raw);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar);
     uint64_t *empty = full + kStages;
-    uint64_t *tfull = empty + kStages;   // [2]
-    uint64_t *tempty = tfull + 2;        // [2]
-    uint64_t *final_bar = tempty + 2;
-    uint64_t *max_bar = final_bar + 1;   // [4], per lane quarter: both halves' maxima written, then both read
+    uint64_t *tfull = empty + kStages;   // [kSteps], by K-step
+    uint64_t *tempty = tfull + kSteps;   // [2], by buffer
+    uint64_t *park_full = tempty + 2;    // [2], by tile: its sums are in TMEM
+    uint64_t *final_bar = park_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
+    volatile int *step_buf = abort_flag + 1;          // [kSteps] buffer of a K-step
+    volatile int *park_buf = step_buf + kSteps;       // [2] buffer of a tile's park
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const ActEpilogue &e = prm.e;
@@ -125,13 +155,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
         }
+        for (int i = 0; i < kSteps; ++i)
+            mbar_init(tfull + i, 2);   // the MMAs, and the record of their buffer
         for (int b = 0; b < 2; ++b) {
-            mbar_init(tfull + b, 1);
-            mbar_init(tempty + b, kEpiWarps);
+            mbar_init(tempty + b, 8);
+            mbar_init(park_full + b, 8);
         }
         mbar_init(final_bar, 1);
-        for (int i = 0; i < 4; ++i)
-            mbar_init(max_bar + i, 2);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&prm.tmA);
@@ -177,18 +207,36 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                 drain_loads(full, kStages, issued, prm.timeout_ns);
         } else if (warp == 1 && lane == 0) {
             // ------------------------------------------------ MMA issuer
-            const uint32_t idesc = idesc_f8_e4m3(128, 256);
-            int stage = 0;
-            uint32_t ph = 0, n = 0;
+            constexpr uint32_t idesc = idesc_f8_e4m3(128, 256);
+            int stage = 0, buf = 1;
+            uint32_t ph = 0, step = 0, use0 = 0, use1 = 0;
             bool ok = true;
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                for (int kb = 0; kb < KB; ++kb, ++n) {
-                    const uint32_t buf = n & 1, tph = (n >> 1) & 1;
-                    if (!mbar_wait(tempty + buf, tph ^ 1, abort_flag, prm.status, prm.timeout_ns, SITE_MMA_TMEM_EMPTY) ||
-                        !mbar_wait(full + stage, ph, abort_flag, prm.status, prm.timeout_ns, SITE_MMA_FULL)) {
+                for (int kb = 0; kb < KB; ++kb, ++step) {
+                    // the other buffer than the last step's, or the first of the two that is free
+                    buf ^= 1;
+                    uint64_t t0 = 0;
+                    for (uint32_t tries = 1; !mbar_test_wait(tempty + buf, ((buf ? use1 : use0) & 1) ^ 1); ++tries) {
+                        buf ^= 1;
+                        if (tries % 256 != 0)
+                            continue;
+                        const uint64_t now = globaltimer();
+                        t0 = t0 == 0 ? now : t0;
+                        if (*abort_flag || now - t0 > prm.timeout_ns) {
+                            if (!*abort_flag) {
+                                *abort_flag = 1;
+                                report(prm.status, kErrTimeout, SITE_MMA_TMEM_EMPTY);
+                            }
+                            ok = false;
+                            break;
+                        }
+                    }
+                    if (!ok || !mbar_wait(full + stage, ph, abort_flag, prm.status, prm.timeout_ns, SITE_MMA_FULL)) {
                         ok = false;
                         break;
                     }
+                    use0 += buf ? 0u : 1u;
+                    use1 += buf ? 1u : 0u;
                     tc_fence_after();
                     const uint64_t ad = desc_kmajor_sw128(smem_u32(smem + stage * kABytes));
                     const uint64_t bd = desc_kmajor_sw128(smem_u32(smem + kOffB + stage * kBBytes));
@@ -196,7 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                     for (int k = 0; k < 4; ++k)   // 4 x 32 of K = one 128-byte swizzle row
                         mma_f8(tmem_base + buf * 256, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
                     tc_commit(empty + stage);
-                    tc_commit(tfull + buf);
+                    tc_commit(tfull + step % kSteps);
+                    step_buf[step % kSteps] = buf;
+                    mbar_arrive(tfull + step % kSteps);   // for what this thread wrote
                     if (++stage == kStages) {
                         stage = 0;
                         ph ^= 1;
@@ -206,62 +256,55 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
             tc_commit(final_bar);
             wait_teardown(final_bar, prm.status, prm.timeout_ns);
         }
-    } else {
-        setmaxnreg_inc<kRegsHigh>();
-        // ---------------------------------------------------- epilogue
-        const int ew = warp - 4, q = warp & 3, h = ew >> 2;   // lane quarter, column half
+    } else if (warp < 12) {
+        setmaxnreg_inc<kRegsPromote>();
+        // ---------------------------------------------------- promotion
+        const int q = warp & 3, h = (warp - 4) >> 2;   // lane quarter, half of the accumulator's columns
         const int row = q * 32 + lane;
-        const uint32_t staging = smem_u32(smem + kOffStaging + ew * 4096);
-        float *maxima = reinterpret_cast<float *>(smem + kOffMax);   // [2][128]
-        uint32_t groups = 0;   // tiles whose maxima were exchanged
-        // the thread's two runs of 64 columns in the accumulator, and the same columns in B's rows
-        const int col0 = GATED ? h * 64 : h * 128, col1 = GATED ? 128 + h * 64 : h * 128 + 64;
-        const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
-        uint32_t n = 0;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16) + h * 128;
+        // a tile past the last column block (an odd number of them) has no scales to read
+        const int last_block = (GATED ? 2 * e.N : e.N) / 128 - 1;
+        uint32_t step = 0, tile = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++tile) {
             const Tile c = decode(t, mt, nt, BN);
-            const int64_t mrow = min(c.m0 + row, e.M - 1);
-            const float *sa_row = prm.sa + mrow * KB;
-            // a tile past the last column block (an odd number of them) has no scales to read
-            const int last_block = (GATED ? 2 * e.N : e.N) / 128 - 1;
-            const float *sb0 = prm.sb + (int64_t)min(last_block, (c.n0 + (GATED ? 0 : h * 128)) / 128) * KB;
-            const float *sb1 = GATED ? prm.sb + (int64_t)((e.N + c.n0) / 128) * KB : sb0;
+            const float *sa_row = prm.sa + (int64_t)min(c.m0 + row, e.M - 1) * KB;
+            const float *sb = prm.sb + (int64_t)min(last_block, (GATED ? h * e.N + c.n0 : c.n0 + h * 128) / 128) * KB;
             float acc[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j)
                 acc[j] = 0.0f;
-            float a_next = __ldg(sa_row), b0_next = __ldg(sb0), b1_next = __ldg(sb1);
-            for (int kb = 0; kb < KB; ++kb, ++n) {
-                const float s0 = a_next * b0_next, s1 = a_next * b1_next;
+            float a_next = __ldg(sa_row), b_next = __ldg(sb);
+            for (int kb = 0; kb < KB; ++kb, ++step) {
+                const float s = a_next * b_next;
                 if (kb + 1 < KB) {
                     a_next = __ldg(sa_row + kb + 1);
-                    b0_next = __ldg(sb0 + kb + 1);
-                    b1_next = __ldg(sb1 + kb + 1);
+                    b_next = __ldg(sb + kb + 1);
                 }
-                const uint32_t buf = n & 1, tph = (n >> 1) & 1;
-                if (!mbar_wait(tfull + buf, tph, abort_flag, prm.status, prm.timeout_ns, SITE_EPI_TMEM_FULL)) {
+                if (!mbar_wait(tfull + step % kSteps, step / kSteps & 1, abort_flag, prm.status, prm.timeout_ns, SITE_EPI_TMEM_FULL)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                const int buf = step_buf[step % kSteps];
                 const uint32_t taddr = lane_base + buf * 256;
+                const bool parks = kb == KB - 1;
                 // 16-column loads, the next one issued before the current one's promotions
                 uint32_t ra[16], rb[16];
-                tmem_ld_x16(taddr + col0, ra);
+                tmem_ld_x16(taddr, ra);
                 tmem_wait_ld(ra);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     uint32_t(&cur)[16] = (i & 1) ? rb : ra;
                     uint32_t(&nxt)[16] = (i & 1) ? ra : rb;
                     if (i + 1 < 8)
-                        tmem_ld_x16(taddr + (i + 1 < 4 ? col0 + (i + 1) * 16 : col1 + (i - 3) * 16), nxt);
+                        tmem_ld_x16(taddr + (i + 1) * 16, nxt);
 #pragma unroll
                     for (int j = 0; j < 16; j += 2)
-                        fma2(acc[i * 16 + j], acc[i * 16 + j + 1], i < 4 ? s0 : s1, cur[j], cur[j + 1]);
+                        fma2(acc[i * 16 + j], acc[i * 16 + j + 1], s, cur[j], cur[j + 1]);
                     if (i + 1 < 8) {
                         tmem_wait_ld(nxt);
-                        if (i + 2 == 8) {
+                        if (i + 2 == 8 && !parks) {
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0)
@@ -269,124 +312,134 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                         }
                     }
                 }
-            }
-            if (!ok)
-                break;
-            // -------- what follows the product
-            const int m_warp = c.m0 + q * 32;
-            const int cols0 = c.n0 + (GATED ? h * 64 : h * 128);   // the thread's first output column
-            const bool inside = cols0 < e.N;                       // warp-uniform
-            const int rows_valid = inside ? max(0, min(32, e.M - m_warp)) : 0;
-            const int P = GATED ? 2 * e.N : e.N;
-            if (e.bias != nullptr && inside) {
-                const float4 *b0 = reinterpret_cast<const float4 *>(e.bias + cols0);
-                const float4 *b1 = reinterpret_cast<const float4 *>(e.bias + (GATED ? e.N + cols0 : cols0 + 64));
+                if (parks) {
+                    // the finish warps read them from here and release the buffer
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const float4 b = __ldg(j < 16 ? b0 + j : b1 + (j - 16));
-                    acc[4 * j] += b.x;
-                    acc[4 * j + 1] += b.y;
-                    acc[4 * j + 2] += b.z;
-                    acc[4 * j + 3] += b.w;
+                    for (int i = 0; i < 4; ++i)
+                        tmem_st_x32(taddr + i * 32, &acc[i * 32]);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (warp == 4)
+                            park_buf[tile & 1] = buf;
+                        mbar_arrive(park_full + (tile & 1));
+                    }
                 }
             }
-            if (e.z != nullptr) {
-                char *z = reinterpret_cast<char *>(e.z) + ((int64_t)m_warp * P + cols0) * 2;
-                const int64_t second = GATED ? e.N : 64;
+        }
+    } else {
+        setmaxnreg_dec<kRegsFinish>();
+        // ---------------------------------------------------- finish
+        const int q = warp & 3;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
+        const int P = GATED ? 2 * e.N : e.N;
+        const int r_bytes = e.r_bf16 ? 2 : 4, c_bytes = e.c_bf16 ? 2 : 4;
+        const bool r_whole = whole32(e.res, e.rs * r_bytes), c_whole = whole32(e.C, e.cs * c_bytes);
+        const bool z_whole = whole32(e.z, 0), q_whole = whole32(e.q, 0);   // N is a multiple of 128
+        uint32_t parked = 0;
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++parked) {
+            const Tile c = decode(t, mt, nt, BN);
+            const int64_t m = c.m0 + q * 32 + lane;
+            const bool inside = m < e.M;
+            const int cols = min(BN, e.N - c.n0);   // a multiple of 128
+            // the residual's 32 columns from `col` on, a block ahead of their use
+            const char *res = static_cast<const char *>(e.res) + (m * e.rs + c.n0) * r_bytes;
+            const bool has_res = e.res != nullptr && inside;
+            uint32_t ahead[32];
+            auto fetch_residual = [&](int col) {
+                if (has_res && col < cols) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    store_cols32(staging, &acc[i * 32], true, z + (i < 2 ? i * 32 : second + (i - 2) * 32) * 2, P, rows_valid);
-            }
-            constexpr int W = GATED ? 64 : 128;   // output columns of a thread
-            with_act(e.act, [&](auto act) {
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    acc[j] = act_value<decltype(act)::value>(acc[j]);
-                    if (GATED)
-                        acc[j] *= acc[(64 + j) & 127];
+                    for (int i = 0; i < 4; ++i)
+                        if (i < r_bytes)
+                            load32(res + col * r_bytes + 32 * i, r_whole, ahead + 8 * i);
                 }
-            });
+            };
+            fetch_residual(0);
             if (e.res != nullptr) {
-                const int bytes = e.r_bf16 ? 2 : 4;
-                const char *r = static_cast<const char *>(e.res) + ((int64_t)m_warp * e.rs + cols0) * bytes;
+                // the next tile's rows of it into L2
+                const Tile d = decode(min(t + (int)gridDim.x, tiles - 1), mt, nt, BN);
+                const int64_t row = d.m0 + q * 32 + lane;
+                if (row < e.M)
+                    for (int i = 0; i < min(BN, e.N - d.n0) * r_bytes; i += 128)
+                        prefetch_l2(static_cast<const char *>(e.res) + (row * e.rs + d.n0) * r_bytes + i);
+            }
+            if (!mbar_wait(park_full + (parked & 1), parked / 2 & 1, abort_flag, prm.status, prm.timeout_ns, SITE_PARK_FULL))
+                break;
+            tc_fence_after();
+            const int buf = park_buf[parked & 1];
+            const uint32_t park = lane_base + buf * 256;
+            float top = 0.0f;
+#pragma unroll 1
+            for (int col = 0; col < cols; col += 32) {
+                const int n0 = c.n0 + col;
+                float v[32];
+                load_park(park + col, e.bias == nullptr ? nullptr : e.bias + n0, v);
+                char *z = reinterpret_cast<char *>(e.z) + (m * P + n0) * 2;
+                if (e.z != nullptr && inside)
+                    store_cols(z, z_whole, true, v);
+                with_act(e.act, [&](auto act) {
+                    if (decltype(act)::value != ACT_NONE) {
 #pragma unroll
-                for (int i = 0; i < W / 32; ++i) {
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = act_value<decltype(act)::value>(v[i]);
+                    }
+                });
+                if (GATED) {
+                    float u[32];
+                    load_park(park + 128 + col, e.bias == nullptr ? nullptr : e.bias + e.N + n0, u);
+                    if (e.z != nullptr && inside)
+                        store_cols(z + (int64_t)e.N * 2, z_whole, true, u);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] *= u[i];
+                }
+                if (has_res) {
                     if (e.r_bf16) {
-                        uint4 v[4];
-                        load_chunk<4>(staging, v, r + i * 64, e.rs * 2, rows_valid);
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                acc[i * 32 + u * 8 + 2 * j] += bf16_lo(w[j]);
-                                acc[i * 32 + u * 8 + 2 * j + 1] += bf16_hi(w[j]);
-                            }
+                        for (int i = 0; i < 16; ++i) {
+                            v[2 * i] += bf16_lo(ahead[i]);
+                            v[2 * i + 1] += bf16_hi(ahead[i]);
                         }
                     } else {
-                        uint4 v[8];
-                        load_chunk<8>(staging, v, r + i * 128, e.rs * 4, rows_valid);
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            acc[i * 32 + u * 4] += __uint_as_float(v[u].x);
-                            acc[i * 32 + u * 4 + 1] += __uint_as_float(v[u].y);
-                            acc[i * 32 + u * 4 + 2] += __uint_as_float(v[u].z);
-                            acc[i * 32 + u * 4 + 3] += __uint_as_float(v[u].w);
+                        for (int i = 0; i < 32; ++i)
+                            v[i] += __uint_as_float(ahead[i]);
+                    }
+                    fetch_residual(col + 32);
+                }
+                if (e.C != nullptr && inside)
+                    store_cols(static_cast<char *>(e.C) + (m * e.cs + n0) * c_bytes, c_whole, e.c_bf16, v);
+                if (e.q != nullptr) {
+                    // one scale per row and 128 columns: they wait in the park for it
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        top = fmaxf(top, fabsf(v[i]));   // skips NaN
+                    tmem_st_x32(park + col, v);
+                    if (col % 128 == 96) {
+                        tmem_wait_st();
+                        const float scale = __fdiv_rn(top, 448.0f);
+                        const Enc enc(scale);
+#pragma unroll 1
+                        for (int i = col - 96; i <= col; i += 32) {
+                            load_park(park + i, nullptr, v);
+                            uint32_t w[8];
+                            enc.codes(v, w);
+                            if (inside)
+                                store32(reinterpret_cast<char *>(e.q) + m * e.N + c.n0 + i, q_whole, w);
                         }
+                        if (inside)
+                            e.scales[m * (e.N / 128) + n0 / 128] = scale;
+                        top = 0.0f;
                     }
                 }
             }
-            if (e.C != nullptr) {
-                const int bytes = e.c_bf16 ? 2 : 4;
-                char *out = static_cast<char *>(e.C) + ((int64_t)m_warp * e.cs + cols0) * bytes;
-#pragma unroll
-                for (int i = 0; i < W / 32; ++i)
-                    store_cols32(staging, &acc[i * 32], e.c_bf16, out + i * 32 * bytes, e.cs, rows_valid);
-            }
-            if (e.q != nullptr) {
-                // one scale per row and 128 columns: a gated thread has half of them
-                float m = 0.0f;
-#pragma unroll
-                for (int j = 0; j < W; ++j)
-                    m = fmaxf(m, fabsf(acc[j]));   // skips NaN
-                if (GATED) {
-                    // the barrier's phases alternate: both warps have written, both have read
-                    if ((groups > 0 && !mbar_wait(max_bar + q, 1, abort_flag, prm.status, prm.timeout_ns, SITE_ROW_MAX))) {
-                        ok = false;
-                        break;
-                    }
-                    maxima[h * 128 + row] = m;
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(max_bar + q);
-                    if (!mbar_wait(max_bar + q, 0, abort_flag, prm.status, prm.timeout_ns, SITE_ROW_MAX)) {
-                        ok = false;
-                        break;
-                    }
-                    ++groups;
-                    m = fmaxf(m, maxima[(h ^ 1) * 128 + row]);
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(max_bar + q);
-                }
-                const float scale = __fdiv_rn(m, 448.0f);
-                const Enc enc(scale);
-                uint8_t *codes = e.q + (int64_t)m_warp * e.N + cols0;
-#pragma unroll
-                for (int i = 0; i < W / 64; ++i) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        float(&x)[16] = *reinterpret_cast<float(*)[16]>(&acc[i * 64 + u * 16]);
-                        uint32_t(&o)[4] = *reinterpret_cast<uint32_t(*)[4]>(&w[u * 4]);
-                        enc.codes(x, o);
-                    }
-                    const uint4 v[4] = {make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]),
-                                        make_uint4(w[8], w[9], w[10], w[11]), make_uint4(w[12], w[13], w[14], w[15])};
-                    store_chunk<4>(staging, v, reinterpret_cast<char *>(codes) + i * 64, e.N, rows_valid);
-                }
-                if (lane < rows_valid && (!GATED || h == 0))
-                    e.scales[(int64_t)(m_warp + lane) * (e.N / 128) + cols0 / 128] = scale;
+            // the park is read: the MMA may refill the buffer.  Two of the eight arrivals it waits for
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(tempty + buf);
+                mbar_arrive(tempty + buf);
             }
         }
     }

@@ -3,8 +3,8 @@
 // With one row to some tens the product is bound by HBM and, at these sizes (4 us of it), by
 // latency: a tile kernel with the rows as its M would leave most SMs without a tile and most of
 // an MMA without rows.  Here the weights are the M operand, a pair of 128-row tiles (the gate's
-// and the up-projection's rows of the same columns, or 256 columns), and the rows the N: 16, 32,
-// 64 or 128 of them, larger M in chunks of 128.  K is cut over a cluster of up to 8 CTAs, so
+// and the up-projection's rows of the same columns, or 256 columns), and the rows the N: 16, 32
+// or 64 of them, larger M in chunks of 64.  K is cut over a cluster of up to 8 CTAs, so
 // that the launch has about one CTA per SM; each streams its part of the weights through a
 // ring of TMA stages as deep as shared memory, promotes the 128-K sums by their block scales in
 // registers, and lays them in its shared memory.  The cluster's CTAs then share out the rows:
@@ -21,6 +21,8 @@ namespace gemmar {
 using namespace ptx;
 
 namespace {
+
+constexpr int kMaxSplits = 8;    // the portable cluster size
 
 // CTAS: of an SM.  Two with rings of half the depth have the same bytes under way, and clusters of
 // eight find room: of those with a whole SM per CTA only 15 fit on the GPU at a time, and the
@@ -44,8 +46,7 @@ struct Cfg {
 
 using Rows16 = Cfg<16, 3, 4, 2>;
 using Rows32 = Cfg<32, 3, 4, 2>;
-using Rows64 = Cfg<64, 2, 2, 2>;
-using Rows128 = Cfg<128, 4, 2, 1>;
+using Rows64 = Cfg<64, 5, 4, 1>;
 
 // 4 consecutive values of a row
 __device__ __forceinline__ float4 load4(const void *p, int64_t at, bool bf16)
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) gemm_act_few_kernel(const 
                 continue;   // the whole warp: an odd number of blocks of columns
             float4 z = make_float4(0, 0, 0, 0), zu = z;
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
+            for (int s = 0; s < kMaxSplits; ++s)
                 if (s < splits) {
                     const uint32_t there = mapa_shared(own, s);
                     z = add4(z, ld_shared_cluster_f32x4(there + (tile * C::NT + t) * 512));
@@ -294,58 +295,95 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) gemm_act_few_kernel(const 
         tmem_dealloc(tmem_base, C::kTmemCols);
 }
 
+// Clusters of each size that the GPU runs at a time: fewer CTAs than SMs where a GPC's are no
+// multiple of the size.
+struct Room {
+    int clusters[kMaxSplits + 1];
+};
+
 template <class C, bool GATED>
-cudaError_t launch_typed(const ActParams &p, int splits, cudaStream_t st)
+cudaLaunchConfig_t config(int splits, cudaLaunchAttribute *attrs)
 {
-    const void *kernel = reinterpret_cast<const void *>(gemm_act_few_kernel<C, GATED>);
-    static const bool split_ok = few_rows_split_ok(kernel, C::kLow, C::kHigh);
-    if (!split_ok)
-        return cudaErrorInvalidConfiguration;
-    const cudaError_t e = ensure_dynamic_smem(kernel, C::kSmemBytes);
-    if (e != cudaSuccess)
-        return e;
-    const int pairs = GATED ? p.e.N / 128 : (p.e.N + 255) / 256;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attrs[2];
     attrs[0].id = cudaLaunchAttributeClusterDimension;
     attrs[0].val.clusterDim.x = (unsigned)splits;
     attrs[0].val.clusterDim.y = 1;
     attrs[0].val.clusterDim.z = 1;
-    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(splits, pairs, (p.e.M + C::NT - 1) / C::NT);
+    cfg.gridDim = dim3(splits);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::kSmemBytes;
-    cfg.stream = st;
     cfg.attrs = attrs;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+template <class C, bool GATED>
+Room measure_room()
+{
+    Room r;
+    for (int s = 1; s <= kMaxSplits; ++s) {
+        cudaLaunchAttribute attrs[1];
+        const cudaLaunchConfig_t cfg = config<C, GATED>(s, attrs);
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, gemm_act_few_kernel<C, GATED>, &cfg) != cudaSuccess)
+            n = 0;
+        r.clusters[s] = n;
+    }
+    return r;
+}
+
+template <class C, bool GATED>
+cudaError_t launch_typed(const ActParams &p, cudaStream_t st)
+{
+    const void *kernel = reinterpret_cast<const void *>(gemm_act_few_kernel<C, GATED>);
+    const cudaError_t e = ensure_dynamic_smem(kernel, C::kSmemBytes);
+    if (e != cudaSuccess)
+        return e;
+    static const bool split_ok = few_rows_split_ok(kernel, C::kLow, C::kHigh);
+    static const Room room = measure_room<C, GATED>();
+    if (!split_ok)
+        return cudaErrorInvalidConfiguration;
+    const int KB = p.e.K / 128, pairs = GATED ? p.e.N / 128 : (p.e.N + 255) / 256, chunks = (p.e.M + C::NT - 1) / C::NT;
+    // the parts of K that end soonest: waves of clusters, each as long as a part and what
+    // starting and joining it costs (about four steps)
+    int splits = 1;
+    int64_t best = INT64_MAX;
+    for (int s = 1; s <= std::min(kMaxSplits, KB); ++s) {
+        if (room.clusters[s] < 1)
+            continue;
+        const int64_t waves = ((int64_t)pairs * chunks + room.clusters[s] - 1) / room.clusters[s];
+        const int64_t steps = waves * ((KB + s - 1) / s + 4);
+        if (steps < best) {
+            best = steps;
+            splits = s;
+        }
+    }
+    cudaLaunchAttribute attrs[2];
+    cudaLaunchConfig_t cfg = config<C, GATED>(splits, attrs);
+    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(splits, pairs, chunks);
+    cfg.stream = st;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, gemm_act_few_kernel<C, GATED>, p);
 }
 
 template <class C>
-cudaError_t launch_rows(const ActParams &p, int splits, cudaStream_t st)
+cudaError_t launch_rows(const ActParams &p, cudaStream_t st)
 {
-    return p.e.gated ? launch_typed<C, true>(p, splits, st) : launch_typed<C, false>(p, splits, st);
+    return p.e.gated ? launch_typed<C, true>(p, st) : launch_typed<C, false>(p, st);
 }
 
 }  // namespace
 
-int gemm_act_few_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+int gemm_act_few_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
-cudaError_t launch_gemm_act_few(const ActParams &p, int num_sms, cudaStream_t st)
+cudaError_t launch_gemm_act_few(const ActParams &p, cudaStream_t st)
 {
-    const int KB = p.e.K / 128, NT = gemm_act_few_rows(p.e.M);
-    const int64_t tiles = (int64_t)(p.e.gated ? p.e.N / 128 : (p.e.N + 255) / 256) * ((p.e.M + NT - 1) / NT);
-    // as many parts of K as fill the SMs, and of those counts the least with parts as short
-    const int room = num_sms * (NT == 128 ? Rows128::kCtas : Rows16::kCtas);
-    int splits = (int)std::max<int64_t>(1, std::min<int64_t>({8, KB, room / tiles}));
-    while (splits > 1 && (KB + splits - 2) / (splits - 1) == (KB + splits - 1) / splits)
-        --splits;
-    switch (NT) {
-    case 16: return launch_rows<Rows16>(p, splits, st);
-    case 32: return launch_rows<Rows32>(p, splits, st);
-    case 64: return launch_rows<Rows64>(p, splits, st);
-    default: return launch_rows<Rows128>(p, splits, st);
+    switch (gemm_act_few_rows(p.e.M)) {
+    case 16: return launch_rows<Rows16>(p, st);
+    case 32: return launch_rows<Rows32>(p, st);
+    default: return launch_rows<Rows64>(p, st);
     }
 }
 

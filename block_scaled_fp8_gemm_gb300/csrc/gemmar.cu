@@ -855,7 +855,7 @@ GEMMAR_API int gemm_blockscale_act(gemmar_ctx *ctx, const uint8_t *A, const floa
                       C, c_dtype == GEMMAR_DTYPE_BF16, c_stride, q, scales, z};
     p.status = ctx->status;
     p.timeout_ns = ctx->timeout_ns;
-    CUDA_OK(few ? launch_gemm_act_few(p, ctx->num_sms, as_stream(stream)) : launch_gemm_act(p, ctx->num_sms, as_stream(stream)));
+    CUDA_OK(few ? launch_gemm_act_few(p, as_stream(stream)) : launch_gemm_act(p, ctx->num_sms, as_stream(stream)));
     return GEMMAR_OK;
 }
 

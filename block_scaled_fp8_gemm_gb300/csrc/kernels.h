@@ -248,7 +248,7 @@ bool gemm_act_split_ok();
 cudaError_t launch_gemm_act(const ActParams &p, int num_sms, cudaStream_t st);
 // The same for few rows (gemm_act_few.cu): tmA's box is {128, gemm_act_few_rows(M)}.
 int gemm_act_few_rows(int M);
-cudaError_t launch_gemm_act_few(const ActParams &p, int num_sms, cudaStream_t st);
+cudaError_t launch_gemm_act_few(const ActParams &p, cudaStream_t st);
 
 // Its backward pass (act_bwd.cu): dz from dout, with codes and column sums.
 struct ActBwdArgs {

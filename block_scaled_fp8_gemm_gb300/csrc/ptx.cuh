@@ -104,8 +104,7 @@ enum WaitSite : int {
     SITE_PARK_FULL = 8,    // a store warp waiting for its epilogue warp's parked partial
     SITE_PARK_EMPTY = 9,   // an epilogue warp waiting for its park to be copied out
     SITE_LORA_MMA = 10,    // an adapter kernel waiting for its MMAs
-    SITE_ROW_MAX = 11,     // the two halves of a gated row, for the maximum of its group
-    SITE_GRID = 12,        // a barrier of all CTAs of the experts' layer
+    SITE_GRID = 11,        // a barrier of all CTAs of the experts' layer
 };
 
 constexpr int kErrTimeout = 6;   // == GEMMAR_ERR_TIMEOUT
