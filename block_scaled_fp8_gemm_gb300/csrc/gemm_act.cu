@@ -43,7 +43,7 @@ constexpr int kOffMisc = kOffBar + kNumBars * 8;
 constexpr int kSmemBytes = kOffMisc + 8 + 4 * kSteps + 8 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 // setmaxnreg: warps 0-3, promotion, finish, of 128 a thread
-constexpr int kRegsLow = 40, kRegsPromote = 184, kRegsFinish = 104;
+constexpr int kRegsLow = 40, kRegsPromote = 176, kRegsFinish = 120;
 constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsPromote + 128 * kRegsFinish;
 static_assert(kRegsNeeded <= 65536, "register split");
 constexpr int kGroupM = 16;      // row tiles that share their columns of B while they are in L2
@@ -106,23 +106,20 @@ __device__ __forceinline__ void store_cols(char *p, bool whole, bool bf16, const
     }
 }
 
-// 32 columns of the park plus the bias at `bias` (nullptr: none)
-__device__ __forceinline__ void load_park(uint32_t taddr, const float *bias, float (&v)[32])
+// v += the 32 values at p
+__device__ __forceinline__ void add_bias(float (&v)[32], const float *p)
 {
-    uint32_t(&r)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v);
-    tmem_ld_x32(taddr, r);
-    tmem_wait_ld(r);
-    if (bias != nullptr) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float4 b = __ldg(reinterpret_cast<const float4 *>(bias) + j);
-            v[4 * j] += b.x;
-            v[4 * j + 1] += b.y;
-            v[4 * j + 2] += b.z;
-            v[4 * j + 3] += b.w;
-        }
+    for (int j = 0; j < 8; ++j) {
+        const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + j);
+        v[4 * j] += b.x;
+        v[4 * j + 1] += b.y;
+        v[4 * j + 2] += b.z;
+        v[4 * j + 3] += b.w;
     }
 }
+
+__device__ __forceinline__ uint32_t (&bits(float (&v)[32]))[32] { return *reinterpret_cast<uint32_t(*)[32]>(&v); }
 
 __device__ __forceinline__ bool whole32(const void *p, int64_t row_bytes)
 {
@@ -343,19 +340,26 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
             const int64_t m = c.m0 + q * 32 + lane;
             const bool inside = m < e.M;
             const int cols = min(BN, e.N - c.n0);   // a multiple of 128
-            // the residual's 32 columns from `col` on, a block ahead of their use
+            // The residual's columns, 64 ahead of their use as bf16 and 32 as fp32: blocks of 32 go to
+            // the two halves of these registers in turn, or fill both.
             const char *res = static_cast<const char *>(e.res) + (m * e.rs + c.n0) * r_bytes;
             const bool has_res = e.res != nullptr && inside;
             uint32_t ahead[32];
-            auto fetch_residual = [&](int col) {
-                if (has_res && col < cols) {
+            auto fetch_residual = [&](int col, int half) {   // half is a constant where it is used
+                if (!has_res || col >= cols)
+                    return;
+                if (e.r_bf16) {
+                    load32(res + col * 2, r_whole, ahead + 16 * half);
+                    load32(res + col * 2 + 32, r_whole, ahead + 16 * half + 8);
+                } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (i < r_bytes)
-                            load32(res + col * r_bytes + 32 * i, r_whole, ahead + 8 * i);
+                        load32(res + col * 4 + 32 * i, r_whole, ahead + 8 * i);
                 }
             };
-            fetch_residual(0);
+            fetch_residual(0, 0);
+            if (e.r_bf16)
+                fetch_residual(32, 1);
             if (e.res != nullptr) {
                 // the next tile's rows of it into L2
                 const Tile d = decode(min(t + (int)gridDim.x, tiles - 1), mt, nt, BN);
@@ -370,11 +374,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
             const int buf = park_buf[parked & 1];
             const uint32_t park = lane_base + buf * 256;
             float top = 0.0f;
-#pragma unroll 1
-            for (int col = 0; col < cols; col += 32) {
+            // 32 columns of out from their sums v
+            auto block = [&](float (&v)[32], int col, int half) {
                 const int n0 = c.n0 + col;
-                float v[32];
-                load_park(park + col, e.bias == nullptr ? nullptr : e.bias + n0, v);
+                if (e.bias != nullptr)
+                    add_bias(v, e.bias + n0);
                 char *z = reinterpret_cast<char *>(e.z) + (m * P + n0) * 2;
                 if (e.z != nullptr && inside)
                     store_cols(z, z_whole, true, v);
@@ -387,7 +391,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                 });
                 if (GATED) {
                     float u[32];
-                    load_park(park + 128 + col, e.bias == nullptr ? nullptr : e.bias + e.N + n0, u);
+                    tmem_ld_x32(park + 128 + col, bits(u));
+                    tmem_wait_ld(bits(u));
+                    if (e.bias != nullptr)
+                        add_bias(u, e.bias + e.N + n0);
                     if (e.z != nullptr && inside)
                         store_cols(z + (int64_t)e.N * 2, z_whole, true, u);
 #pragma unroll
@@ -398,15 +405,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                     if (e.r_bf16) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            v[2 * i] += bf16_lo(ahead[i]);
-                            v[2 * i + 1] += bf16_hi(ahead[i]);
+                            v[2 * i] += bf16_lo(ahead[16 * half + i]);
+                            v[2 * i + 1] += bf16_hi(ahead[16 * half + i]);
                         }
+                        fetch_residual(col + 64, half);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             v[i] += __uint_as_float(ahead[i]);
+                        fetch_residual(col + 32, 0);
                     }
-                    fetch_residual(col + 32);
                 }
                 if (e.C != nullptr && inside)
                     store_cols(static_cast<char *>(e.C) + (m * e.cs + n0) * c_bytes, c_whole, e.c_bf16, v);
@@ -416,22 +424,36 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                     for (int i = 0; i < 32; ++i)
                         top = fmaxf(top, fabsf(v[i]));   // skips NaN
                     tmem_st_x32(park + col, v);
-                    if (col % 128 == 96) {
-                        tmem_wait_st();
-                        const float scale = __fdiv_rn(top, 448.0f);
-                        const Enc enc(scale);
+                }
+            };
 #pragma unroll 1
-                        for (int i = col - 96; i <= col; i += 32) {
-                            load_park(park + i, nullptr, v);
-                            uint32_t w[8];
-                            enc.codes(v, w);
-                            if (inside)
-                                store32(reinterpret_cast<char *>(e.q) + m * e.N + c.n0 + i, q_whole, w);
-                        }
+            for (int col = 0; col < cols; col += 64) {
+                float v[32], w[32];
+                tmem_ld_x32(park + col, bits(v));
+                tmem_wait_ld(bits(v));
+                if (!GATED)   // under way while the first block is taken through
+                    tmem_ld_x32(park + col + 32, bits(w));
+                block(v, col, 0);
+                if (GATED)
+                    tmem_ld_x32(park + col + 32, bits(w));
+                tmem_wait_ld(bits(w));
+                block(w, col + 32, 1);
+                if (e.q != nullptr && col % 128 == 64) {
+                    tmem_wait_st();
+                    const float scale = __fdiv_rn(top, 448.0f);
+                    const Enc enc(scale);
+#pragma unroll 1
+                    for (int i = col - 64; i < col + 64; i += 32) {
+                        tmem_ld_x32(park + i, bits(v));
+                        tmem_wait_ld(bits(v));
+                        uint32_t o[8];
+                        enc.codes(v, o);
                         if (inside)
-                            e.scales[m * (e.N / 128) + n0 / 128] = scale;
-                        top = 0.0f;
+                            store32(reinterpret_cast<char *>(e.q) + m * e.N + c.n0 + i, q_whole, o);
                     }
+                    if (inside)
+                        e.scales[m * (e.N / 128) + (c.n0 + col) / 128] = scale;
+                    top = 0.0f;
                 }
             }
             // the park is read: the MMA may refill the buffer.  Two of the eight arrivals it waits for
