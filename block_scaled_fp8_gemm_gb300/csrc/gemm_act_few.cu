@@ -320,7 +320,9 @@ cudaLaunchConfig_t config(int splits, cudaLaunchAttribute *attrs)
 template <class C, bool GATED>
 Room measure_room()
 {
-    Room r;
+    Room r{};
+    if (ensure_dynamic_smem(reinterpret_cast<const void *>(gemm_act_few_kernel<C, GATED>), C::kSmemBytes) != cudaSuccess)
+        return r;
     for (int s = 1; s <= kMaxSplits; ++s) {
         cudaLaunchAttribute attrs[1];
         const cudaLaunchConfig_t cfg = config<C, GATED>(s, attrs);
@@ -332,6 +334,35 @@ Room measure_room()
     return r;
 }
 
+template <bool GATED>
+int tile_pairs(int N) { return GATED ? N / 128 : (N + 255) / 256; }
+
+// The parts of K that end soonest, and when: a wave of clusters takes 0.54 us per 128 of K, 0.35 us
+// per turn of its warps through the rows, and 2 us besides, a launch 3 (measured: 20 us for 256
+// gated rows at N = 2048, K = 7168, 11.9 for 128 at N = 7168, K = 2048, 10.5 for 512 at 1920 x 1152).
+struct Plan {
+    int splits;
+    int64_t ns;
+};
+
+template <class C, bool GATED>
+Plan plan(int M, int N, int K)
+{
+    static const Room room = measure_room<C, GATED>();
+    const int KB = K / 128, rows = std::min(M, C::NT) * (GATED ? 1 : 2);
+    const int64_t clusters = (int64_t)tile_pairs<GATED>(N) * ((M + C::NT - 1) / C::NT);
+    Plan best{1, INT64_MAX};
+    for (int s = 1; s <= std::min(kMaxSplits, KB); ++s) {
+        if (room.clusters[s] < 1)
+            continue;
+        const int64_t waves = (clusters + room.clusters[s] - 1) / room.clusters[s];
+        const int64_t ns = waves * (540 * ((KB + s - 1) / s) + 350 * ((rows + 8 * s - 1) / (8 * s)) + 2000) + 3000;
+        if (ns < best.ns)
+            best = {s, ns};
+    }
+    return best;
+}
+
 template <class C, bool GATED>
 cudaError_t launch_typed(const ActParams &p, cudaStream_t st)
 {
@@ -340,29 +371,14 @@ cudaError_t launch_typed(const ActParams &p, cudaStream_t st)
     if (e != cudaSuccess)
         return e;
     static const bool split_ok = few_rows_split_ok(kernel, C::kLow, C::kHigh);
-    static const Room room = measure_room<C, GATED>();
     if (!split_ok)
         return cudaErrorInvalidConfiguration;
-    const int KB = p.e.K / 128, pairs = GATED ? p.e.N / 128 : (p.e.N + 255) / 256, chunks = (p.e.M + C::NT - 1) / C::NT;
-    // the parts of K that end soonest: waves of clusters, each as long as a part and what
-    // starting and joining it costs (about four steps)
-    int splits = 1;
-    int64_t best = INT64_MAX;
-    for (int s = 1; s <= std::min(kMaxSplits, KB); ++s) {
-        if (room.clusters[s] < 1)
-            continue;
-        const int64_t waves = ((int64_t)pairs * chunks + room.clusters[s] - 1) / room.clusters[s];
-        const int64_t steps = waves * ((KB + s - 1) / s + 4);
-        if (steps < best) {
-            best = steps;
-            splits = s;
-        }
-    }
+    const int splits = plan<C, GATED>(p.e.M, p.e.N, p.e.K).splits;
     cudaLaunchAttribute attrs[2];
     cudaLaunchConfig_t cfg = config<C, GATED>(splits, attrs);
     attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attrs[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(splits, pairs, chunks);
+    cfg.gridDim = dim3(splits, tile_pairs<GATED>(p.e.N), (p.e.M + C::NT - 1) / C::NT);
     cfg.stream = st;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, gemm_act_few_kernel<C, GATED>, p);
@@ -377,6 +393,15 @@ cudaError_t launch_rows(const ActParams &p, cudaStream_t st)
 }  // namespace
 
 int gemm_act_few_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
+
+int64_t gemm_act_few_ns(int M, int N, int K, bool gated)
+{
+    switch (gemm_act_few_rows(M)) {
+    case 16: return (gated ? plan<Rows16, true>(M, N, K) : plan<Rows16, false>(M, N, K)).ns;
+    case 32: return (gated ? plan<Rows32, true>(M, N, K) : plan<Rows32, false>(M, N, K)).ns;
+    default: return (gated ? plan<Rows64, true>(M, N, K) : plan<Rows64, false>(M, N, K)).ns;
+    }
+}
 
 cudaError_t launch_gemm_act_few(const ActParams &p, cudaStream_t st)
 {

@@ -842,7 +842,8 @@ GEMMAR_API int gemm_blockscale_act(gemmar_ctx *ctx, const uint8_t *A, const floa
         return GEMMAR_ERR_ALIGN;
     if (!load_encode())
         return GEMMAR_ERR_CUDA;
-    const bool few = M <= 128;
+    // 128 gated rows at N = 2048, K = 7168: 13 us as few rows, 31 as tiles; 512: 35 and 31
+    const bool few = gemm_act_few_ns((int)M, (int)N, (int)K, gated != 0) <= gemm_act_tiles_ns((int)M, (int)N, (int)K, gated != 0, ctx->num_sms);
     if (!few && !gemm_act_split_ok())
         return GEMMAR_ERR_DEVICE;
     ActParams p;

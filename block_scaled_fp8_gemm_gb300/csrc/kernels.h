@@ -248,6 +248,9 @@ bool gemm_act_split_ok();
 cudaError_t launch_gemm_act(const ActParams &p, int num_sms, cudaStream_t st);
 // The same for few rows (gemm_act_few.cu): tmA's box is {128, gemm_act_few_rows(M)}.
 int gemm_act_few_rows(int M);
+// About how long each takes: the shorter is taken.
+int64_t gemm_act_tiles_ns(int M, int N, int K, bool gated, int num_sms);
+int64_t gemm_act_few_ns(int M, int N, int K, bool gated);
 cudaError_t launch_gemm_act_few(const ActParams &p, cudaStream_t st);
 
 // Its backward pass (act_bwd.cu): dz from dout, with codes and column sums.
