@@ -12,6 +12,7 @@
 #include "activation.cuh"
 #include "e4m3_encode.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 
 namespace gemmar {
 using namespace ptx;
@@ -85,24 +86,38 @@ __global__ void __launch_bounds__(kThreads) act_bwd_kernel(const ActBwdArgs a, c
     const int P = GATED ? 2 * a.N : a.N;
     const int64_t first = (int64_t)blockIdx.y * sh.rows, end = min(first + sh.rows, a.M);
     float sum0[8] = {}, sum1[8] = {};
+    // a row ahead of its use: dout in one or two units of 16 bytes, and z
+    uint4 raw_d[BF ? 1 : 2], raw_z[GATED ? 2 : 1];
+    auto fetch = [&](int64_t base) {
+        const int64_t mm = inside && base + r0 < end ? base + r0 : first;
+        const char *dp = static_cast<const char *>(a.dout) + (mm * a.ds + col) * (BF ? 2 : 4);
+#pragma unroll
+        for (int i = 0; i < (BF ? 1 : 2); ++i)
+            raw_d[i] = __ldcs(reinterpret_cast<const uint4 *>(dp) + i);
+        const uint16_t *zp = a.z + mm * P + col;
+#pragma unroll
+        for (int i = 0; i < (GATED ? 2 : 1); ++i)
+            raw_z[i] = __ldcs(reinterpret_cast<const uint4 *>(zp + (int64_t)i * a.N));
+    };
+    fetch(first);
     // every thread of a warp makes every step: a group's lanes meet in shuffles
     for (int64_t base = first; base < end; base += kRows) {
         const int64_t m = base + r0;
         const bool live = inside && m < end;
         const int64_t mm = live ? m : first;
         float d[8], z0[8], z1[8], v0[8], v1[8];
-        if (BF) {
-            unpack8(__ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.dout) + mm * a.ds + col)), d);
+        if constexpr (BF) {
+            unpack8(raw_d[0], d);
         } else {
-            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.dout) + mm * a.ds + col);
-            const float4 lo = __ldcs(p), hi = __ldcs(p + 1);
-            d[0] = lo.x; d[1] = lo.y; d[2] = lo.z; d[3] = lo.w;
-            d[4] = hi.x; d[5] = hi.y; d[6] = hi.z; d[7] = hi.w;
+            const uint32_t w[8] = {raw_d[0].x, raw_d[0].y, raw_d[0].z, raw_d[0].w, raw_d[1].x, raw_d[1].y, raw_d[1].z, raw_d[1].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                d[i] = __uint_as_float(w[i]);
         }
-        const uint16_t *zp = a.z + mm * P + col;
-        unpack8(__ldcs(reinterpret_cast<const uint4 *>(zp)), z0);
-        if (GATED)
-            unpack8(__ldcs(reinterpret_cast<const uint4 *>(zp + a.N)), z1);
+        unpack8(raw_z[0], z0);
+        if constexpr (GATED)
+            unpack8(raw_z[1], z1);
+        fetch(base + kRows);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float value, slope;
@@ -140,6 +155,7 @@ __global__ void __launch_bounds__(kThreads) act_bwd_kernel(const ActBwdArgs a, c
     }
     if (a.dbias == nullptr)
         return;
+    grid_launch_next();
     // the CTA's rows of threads in their order, then the share's sums for the second kernel
     __shared__ float part[kRows][kRowThreads][GATED ? 16 : 8];
 #pragma unroll
@@ -167,8 +183,10 @@ __global__ void __launch_bounds__(256) act_bwd_sum_kernel(const float *ws, int s
 {
     const int c = blockIdx.x * 32 + threadIdx.x % 32, r = threadIdx.x / 32;
     float s = 0.0f;
+    grid_wait();
+#pragma unroll 4
     for (int i = r; i < shares; i += 8)
-        s += ws[(int64_t)i * P + c];
+        s += ld_after_f32(ws + (int64_t)i * P + c);
     __shared__ float part[8][32];
     part[r][threadIdx.x % 32] = s;
     __syncthreads();
@@ -210,8 +228,7 @@ cudaError_t launch_act_bwd(const ActBwdArgs &a, float *ws, int num_sms, cudaStre
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && a.dbias != nullptr && sh.shares > 1) {
         const int P = a.gated ? 2 * a.N : a.N;
-        act_bwd_sum_kernel<<<P / 32, 256, 0, st>>>(ws, sh.shares, P, a.dbias);
-        e = cudaGetLastError();
+        e = launch(act_bwd_sum_kernel, dim3(P / 32), 256, 0, 1, true, st, static_cast<const float *>(ws), (int)sh.shares, P, a.dbias);
     }
     return e;
 }

@@ -75,7 +75,7 @@ cudaError_t ensure_dynamic_smem(const void *kernel, int bytes)
 namespace {
 
 constexpr int kMaxTimedCalls = 65536;
-constexpr int kCounters = 64;      // of moe_route's groups of tokens, then of moe_apply
+constexpr int kCounters = 64;      // moe_route's, and moe_apply's in a cache line of their own
 constexpr int kMoeCounters = 32;
 constexpr int kEventsPerCall = GEMMAR_NUM_PHASES + 1;
 
@@ -904,9 +904,9 @@ GEMMAR_API int moe_route(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, c
         return GEMMAR_ERR_ALIGN;
     const RouteArgs a{x, x_stride, w, w_dtype == GEMMAR_DTYPE_BF16, bias, (int)T, (int)H, E, k, score, renorm != 0, factor,
                       ids, weights};
-    if (route_ws_floats(a) > ctx->W_floats)
+    if (route_ws_floats(a, ctx->num_sms) > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
-    CUDA_OK(launch_route(a, ctx->W, ctx->counters, as_stream(stream)));
+    CUDA_OK(launch_route(a, ctx->W, ctx->counters, ctx->num_sms, as_stream(stream)));
     return GEMMAR_OK;
 }
 

@@ -297,8 +297,8 @@ struct MoeArgs {
     uint16_t *out;
     int64_t os;
 };
-int64_t route_ws_floats(const RouteArgs &a);
-cudaError_t launch_route(const RouteArgs &a, float *ws, uint32_t *counters, cudaStream_t st);
+int64_t route_ws_floats(const RouteArgs &a, int num_sms);
+cudaError_t launch_route(const RouteArgs &a, float *ws, uint32_t *counter, int num_sms, cudaStream_t st);
 // Where moe_apply keeps what passes between its steps, in floats of the workspace: the
 // products' partial sums from 0, then the hidden values' scales and their three parts.
 struct MoeLayout {

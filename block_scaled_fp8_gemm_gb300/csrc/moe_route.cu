@@ -2,10 +2,13 @@
 //
 //   l[t,e] = sum_h x[t,h] w[e,h];   p = softmax(l) or sigmoid(l);   the k largest of p + bias
 //
-// For few tokens it reads the router once and is bound by latency and, from some tens of
-// tokens on, by fp32 FMAs.  A CTA computes the logits of a few tokens and experts with all
-// its threads along h; the CTA that finishes a group of tokens last chooses for them, a warp
-// per token, so that no second launch is needed.
+// For few tokens it reads the router once and is bound by latency, and from some tens of tokens
+// on by fp32 FMAs (the sums must tell neighbours in the order apart, so they are no tensor-core
+// sums).  Up to 8 tokens a CTA computes the logits of a few of them and of few experts with
+// all its threads along h, and the one that finishes last chooses, a warp per token.  More go by
+// tiles of 32 tokens and 32 experts, h cut into as many parts as fill the SMs (96 tokens, 256
+// experts, h = 7168: 9 000 cycles of FMAs an SM at best), and a second launch adds the parts and
+// chooses.
 //
 // The order of two experts whose scores agree to fp32's rounding would depend on how the
 // sums are split.  Such tokens are decided in 64 bits: the logits in question are summed
@@ -14,6 +17,7 @@
 
 #include "e4m3_encode.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 
 namespace gemmar {
 using namespace ptx;
@@ -22,7 +26,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTokens = 8;        // tokens of a group: one warp chooses for each
+constexpr int kTokens = 8;        // tokens of the first form: one warp chooses for each
 static_assert(kTokens == kWarps, "a warp per token");
 
 // 8 values of a row of the router
@@ -50,31 +54,14 @@ __device__ __forceinline__ const void *router_row(const RouteArgs &a, int e)
     return static_cast<const char *>(a.w) + (int64_t)e * a.H * (a.w_bf16 ? 2 : 4);
 }
 
-// a before b: the larger score, the lower number where they are equal
-__device__ __forceinline__ bool before(float sa, int ea, float sb, int eb) { return sa > sb || (sa == sb && ea < eb); }
-__device__ __forceinline__ bool before(double sa, int ea, double sb, int eb) { return sa > sb || (sa == sb && ea < eb); }
-
-// The warp's best of (score, expert); lanes without one pass expert -1.
-template <typename T>
-__device__ __forceinline__ void best_of_warp(T &s, int &e)
+// A score as an unsigned number of the same order; 0: not to be chosen (NaN, -inf).  The warp's largest
+// is then one instruction.
+__device__ __forceinline__ uint32_t key_of(float s)
 {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const T os = __shfl_xor_sync(0xffffffffu, s, d);
-        const int oe = __shfl_xor_sync(0xffffffffu, e, d);
-        if (oe >= 0 && (e < 0 || before(os, oe, s, e))) {
-            s = os;
-            e = oe;
-        }
-    }
+    const uint32_t b = __float_as_uint(s);
+    return s > -INFINITY ? (b & 0x80000000u ? ~b : b | 0x80000000u) : 0u;
 }
-
-// A score an expert can be chosen with: not NaN, not -inf.
-template <typename T>
-__device__ __forceinline__ bool eligible(T s)
-{
-    return s > -INFINITY;
-}
+__device__ __forceinline__ float score_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key); }
 
 // x[t] . w[e] in double by the whole warp
 __device__ double logit64(const RouteArgs &a, int t, int e)
@@ -100,189 +87,205 @@ __device__ double logit64(const RouteArgs &a, int t, int e)
     return s;
 }
 
-// One warp chooses token t's experts.  score: [E] in shared memory, the warp's own, holding the
-// logits; overwritten.  PER: experts of a lane (E <= 32 PER), lane + 32 i.
+// The selection score in double; p is the fp32 score without the bias.
+struct Scores64 {
+    bool soft, sums;      // sums: divided by their sum (where a bias is added)
+    double top, sum;
+    __device__ double of(double logit, double bias) const
+    {
+        if (!soft)
+            return 1.0 / (1.0 + exp(-logit)) + bias;
+        return sums ? exp(logit - top) / sum + bias : exp(logit - top);
+    }
+};
+
+// The first k in double of the experts whose fp32 score is at least `least`, for the rare token
+// where fp32 cannot tell: lane j gets the j-th.  p: fp32 scores without the bias, `scale` their
+// factor, zero: every logit of the token is exactly 0.
+__device__ __noinline__ int decide64(const RouteArgs &a, int t, const float *p, float scale, float least, int k, Scores64 s, bool zero)
+{
+    const int lane = threadIdx.x & 31;
+    int mine = -1;
+    double last = INFINITY;
+    int last_e = -1;
+    // k times the best one after the last: candidates are few, and their scores are summed anew
+    // each time rather than kept
+    for (int j = 0; j < k; ++j) {
+        double best = -INFINITY;
+        int best_e = -1;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane;
+            const float bias = e < a.E && a.bias ? __ldg(a.bias + e) : 0.0f;
+            const float f = e < a.E ? p[e] * scale + bias : -INFINITY;
+            unsigned todo = __ballot_sync(0xffffffffu, f > -INFINITY && f >= least);
+            while (todo) {
+                const int who = __ffs(todo) - 1, c = e0 + who;
+                todo &= todo - 1;
+                const double x = zero ? 0.0 : logit64(a, t, c);
+                const double b = (double)__shfl_sync(0xffffffffu, bias, who);
+                // an infinite logit's fp32 score is exact
+                const double d = x > -INFINITY && x < INFINITY ? s.of(x, b) : (double)__shfl_sync(0xffffffffu, f, who);
+                const bool after = d < last || (d == last && c > last_e);
+                if (after && (best_e < 0 || d > best)) {
+                    best = d;
+                    best_e = c;
+                }
+            }
+        }
+        if (lane == j)
+            mine = best_e;
+        last = best;
+        last_e = best_e;
+    }
+    return mine;
+}
+
+// One warp chooses token t's experts from its logits in global memory, which other CTAs wrote, in
+// `parts` to be added.  score: [E] in shared memory, the warp's own.  PER: experts of a lane
+// (E <= 32 PER), lane + 32 i.
 template <int PER>
-__device__ void choose(const RouteArgs &a, int t, float *score)
+__device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *logits, int parts, float *score)
 {
     const int lane = threadIdx.x & 31;
     const bool soft = a.score == 0;
-    float l[PER], sel[PER];
+    float v[PER], bias[PER];             // logits, then scores without the bias
     float top = -INFINITY, big = 0.0f;   // largest logit, largest size of one
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int e = lane + 32 * i;
-        l[i] = e < a.E ? score[e] : -INFINITY;
-        top = fmaxf(top, l[i]);          // skips NaN
-        if (fabsf(l[i]) < INFINITY)
-            big = fmaxf(big, fabsf(l[i]));
+        bias[i] = e < a.E && a.bias != nullptr ? __ldg(a.bias + e) : 0.0f;
+        v[i] = e < a.E ? __ldcg(logits + (int64_t)t * a.E + e) : -INFINITY;
+    }
+    // many loads under way: a lane's experts of four parts
+    const float *from = logits + (int64_t)t * a.E + lane;
+#pragma unroll(PER <= 8 ? 4 : 1)
+    for (int p = 1; p < parts; ++p) {
+        from += (int64_t)a.T * a.E;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (lane + 32 * i < a.E)
+                v[i] += __ldcg(from + 32 * i);
     }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
+    for (int i = 0; i < PER; ++i) {
+        top = fmaxf(top, v[i]);          // skips NaN
+        if (fabsf(v[i]) < INFINITY)
+            big = fmaxf(big, fabsf(v[i]));
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-    }
+    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+    // exponentials to be divided by their sum, or sigmoids
     float sum = 0.0f;
-    if (soft) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const float x = l[i] - top;   // NaN where both are infinite
-            l[i] = l[i] == top ? 1.0f : expf(x);
-            if (l[i] >= 0.0f)
-                sum += l[i];              // a NaN logit is no expert's
+    for (int i = 0; i < PER; ++i) {
+        // of the softmax's both may be infinite; a NaN logit is no expert's
+        const float x = soft && v[i] == top ? 1.0f : expf(soft ? v[i] - top : -v[i]);
+        v[i] = soft ? x : __fdividef(1.0f, 1.0f + x);
+        if (lane + 32 * i < a.E) {
+            score[lane + 32 * i] = v[i];
+            sum += v[i] >= 0.0f ? v[i] : 0.0f;
         }
+    }
+    float scale = 1.0f;
+    if (soft) {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        scale = 1.0f / sum;
     }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 32 * i;
-        const float p = soft ? l[i] / sum : 1.0f / (1.0f + expf(-l[i]));
-        sel[i] = -INFINITY;
-        if (e < a.E) {
-            sel[i] = p + (a.bias ? __ldg(a.bias + e) : 0.0f);
-            score[e] = p;                 // the weight, once chosen
-        }
-        if (!(sel[i] == sel[i]))
-            sel[i] = -INFINITY;
-    }
-    // how far fp32's rounding may move a score: the logits' sums to 2^-20 of the largest
-    // logit (twenty times the spread of such sums), the rest to a few units in the last place
-    const float peak = soft ? 1.0f / sum : 1.0f;
-    const float tol = 0x1p-20f * big * (soft ? peak : 0.25f) + 0x1p-21f * peak;
-    // the chosen, and whether neighbours in the order are too close to tell in fp32
-    int32_t *ids = a.ids + (int64_t)t * a.k;
-    float *weights = a.weights + (int64_t)t * a.k;
-    bool close = false;
-    int mine = -1;                        // lane j keeps the j-th choice (k <= 16)
-    float last = INFINITY;
-    auto pick = [&](float &s, int &e) {
-        s = -INFINITY;
-        e = -1;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (eligible(sel[i]) && (e < 0 || before(sel[i], lane + 32 * i, s, e))) {
-                s = sel[i];
-                e = lane + 32 * i;
-            }
-        best_of_warp(s, e);
-    };
-    auto take = [&](int e) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (e == lane + 32 * i)
-                sel[i] = -INFINITY;
-    };
-    float cut = -INFINITY;                // the last chosen score
-    int chosen = 0;
-    float kept[PER];
+    uint32_t key[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-        kept[i] = sel[i];
-    for (int j = 0; j <= a.k; ++j) {      // one past the last, to see how near it is
-        float s;
-        int e;
-        pick(s, e);
-        if (e < 0)
+        key[i] = lane + 32 * i < a.E ? key_of(v[i] * scale + bias[i]) : 0u;
+    // how far fp32's rounding may move a score: the logits' sums to 2^-20 of the largest
+    // logit (twenty times the spread of such sums), the rest to a few units in the last place
+    const float tol = 0x1p-20f * big * (soft ? scale : 0.25f) + 0x1p-21f * scale;
+    bool close = false;                  // whether neighbours in the order are too close to tell
+    int mine = -1, chosen = 0;           // lane j keeps the j-th choice (k <= 16)
+    float last = INFINITY, cut = -INFINITY;
+#pragma unroll 1
+    for (int j = 0; j <= a.k; ++j) {     // one past the last, to see how near it is
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            best = max(best, key[i]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        if (best == 0)
             break;
+        const float s = score_of(best);
         close = close || last - s <= tol + 0x1p-21f * fabsf(s);
         last = s;
         if (j == a.k)
             break;
-        take(e);
+        int e = INT32_MAX;               // of equal ones the lowest
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i)
+            e = key[i] == best ? lane + 32 * i : e;
+        e = __reduce_min_sync(0xffffffffu, e);
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            key[i] = e == lane + 32 * i ? 0u : key[i];
         cut = s;
         ++chosen;
         if (lane == j)
             mine = e;
     }
-    if (close && eligible(cut)) {
-        // decide in double: every expert that may be among the chosen
-        const float floor_ = cut - 2.0f * (tol + 0x1p-21f * fabsf(cut));
-        double dsum = 1.0;
+    __syncwarp();
+    if (close && chosen > 0) {
+        double sum64 = 1.0;
         if (soft && a.bias != nullptr) {
-            dsum = 0.0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (lane + 32 * i < a.E && l[i] >= 0.0f)
-                    dsum += (double)l[i];
+            sum64 = 0.0;
+            for (int e = lane; e < a.E; e += 32)
+                sum64 += score[e] >= 0.0f ? (double)score[e] : 0.0;
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1)
-                dsum += __shfl_xor_sync(0xffffffffu, dsum, d);
+                sum64 += __shfl_xor_sync(0xffffffffu, sum64, d);
         }
-        double dsel[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            dsel[i] = -INFINITY;
-            unsigned todo = __ballot_sync(0xffffffffu, eligible(kept[i]) && kept[i] >= floor_);
-            while (todo) {
-                const int who = __ffs(todo) - 1, e = who + 32 * i;
-                todo &= todo - 1;
-                const double x = big == 0.0f ? 0.0 : logit64(a, t, e);   // a padded row's logits are exact
-                if (lane == who) {
-                    const double b = a.bias ? (double)__ldg(a.bias + e) : 0.0;
-                    // an infinite logit (its score is then exact in fp32) stays as it was
-                    if (!(x > -INFINITY && x < INFINITY))
-                        dsel[i] = (double)kept[i];
-                    else if (!soft)
-                        dsel[i] = 1.0 / (1.0 + exp(-x)) + b;
-                    else
-                        dsel[i] = a.bias ? exp(x - (double)top) / dsum + b : exp(x - (double)top);
-                }
-            }
-        }
-        mine = -1;
-        for (int j = 0; j < chosen; ++j) {
-            double s = -INFINITY;
-            int e = -1;
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (eligible(dsel[i]) && (e < 0 || before(dsel[i], lane + 32 * i, s, e))) {
-                    s = dsel[i];
-                    e = lane + 32 * i;
-                }
-            best_of_warp(s, e);
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (e == lane + 32 * i)
-                    dsel[i] = -INFINITY;
-            if (lane == j)
-                mine = e;
-        }
+        mine = decide64(a, t, score, scale, cut - 2.0f * (tol + 0x1p-21f * fabsf(cut)), chosen,
+                        Scores64{soft, a.bias != nullptr, (double)top, sum64}, big == 0.0f);
     }
-    __syncwarp();
-    float w = mine >= 0 ? score[mine] : 0.0f, all = w;
+    float w = mine >= 0 ? score[mine] * scale : 0.0f, all = w;
     if (a.renorm) {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
             all += __shfl_xor_sync(0xffffffffu, all, d);
-        w = all > 0.0f ? w / all : (mine >= 0 ? w : 0.0f);
+        w = all > 0.0f ? w / all : w;
     }
     if (lane < a.k) {
-        ids[lane] = mine;
-        weights[lane] = mine >= 0 ? w * a.factor : 0.0f;
+        a.ids[(int64_t)t * a.k + lane] = mine;
+        a.weights[(int64_t)t * a.k + lane] = mine >= 0 ? w * a.factor : 0.0f;
     }
 }
 
-// grid: (experts / EB, tokens / kTokens); logits fp32 [T,E]; done: one counter per token group,
-// zero before and after.
+__device__ __forceinline__ void choose_token(const RouteArgs &a, int t, const float *logits, int parts, float *score)
+{
+    if (a.E <= 64)
+        choose<2>(a, t, logits, parts, score);
+    else if (a.E <= 256)
+        choose<8>(a, t, logits, parts, score);
+    else
+        choose<32>(a, t, logits, parts, score);
+}
+
+// At most kTokens tokens.  grid: experts / EB; logits fp32 [T,E]; done: zero before and after.
 template <int TB, int EB, bool BF>
 __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a, float *logits, uint32_t *done)
 {
     __shared__ float part[kWarps][TB * EB];
-    extern __shared__ float scores[];   // [kWarps][E]
+    extern __shared__ __align__(16) uint8_t smem[];
+    float *scores = reinterpret_cast<float *>(smem);   // [kWarps][E]
     __shared__ bool chooses;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e0 = blockIdx.x * EB;
-    const int group0 = blockIdx.y * kTokens, group1 = min(group0 + kTokens, a.T);
-    for (int t0 = group0; t0 < group1; t0 += TB) {
+    for (int t0 = 0; t0 < a.T; t0 += TB) {
         float acc[TB * EB] = {};
         for (int h = threadIdx.x * 8; h < a.H; h += kThreads * 8) {
             float x[TB][8];
 #pragma unroll
             for (int i = 0; i < TB; ++i)
-                load8<true>(a.x + (int64_t)min(t0 + i, group1 - 1) * a.xs, h, x[i]);
+                load8<true>(a.x + (int64_t)min(t0 + i, a.T - 1) * a.xs, h, x[i]);
 #pragma unroll
             for (int j = 0; j < EB; ++j) {
                 float w[8];
@@ -309,54 +312,208 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a, floa
             for (int w = 1; w < kWarps; ++w)
                 s += part[w][i];
             const int t = t0 + i / EB, e = e0 + i % EB;
-            if (t < group1 && e < a.E)
+            if (t < a.T && e < a.E)
                 __stcg(logits + (int64_t)t * a.E + e, s);
         }
         __syncthreads();
     }
     if (threadIdx.x == 0) {
-        __threadfence();
-        chooses = atomicAdd(done + blockIdx.y, 1u) == gridDim.x - 1;
-        if (chooses) {
-            __threadfence();
-            done[blockIdx.y] = 0;
-        }
+        chooses = add_acq_rel(done, 1u) == gridDim.x - 1;   // then all CTAs' logits are visible
+        if (chooses)
+            *done = 0;
     }
     __syncthreads();
-    if (!chooses)
-        return;
-    const int t = group0 + warp;
-    if (t >= a.T)
-        return;
-    float *score = scores + warp * a.E;
-    for (int e = lane; e < a.E; e += 32)
-        score[e] = __ldcg(logits + (int64_t)t * a.E + e);
-    __syncwarp();
-    if (a.E <= 64)
-        choose<2>(a, t, score);
-    else if (a.E <= 256)
-        choose<8>(a, t, score);
-    else
-        choose<32>(a, t, score);
+    if (chooses && warp < a.T)
+        choose_token(a, warp, logits, 1, scores + warp * a.E);
+}
+
+// ---- tiles of 32 tokens x 32 experts
+
+constexpr int kTile = 32, kChunk = 256, kStages = 4, kMaxParts = 16;   // kChunk: columns of a stage
+
+// Rows of the two operands in shared memory, a 16-byte unit longer than a chunk: the rows that
+// the lanes of a warp read at a time then lie in different banks.
+template <bool BF>
+struct TileSmem {
+    static constexpr int kXRow = kChunk * 2 + 16, kWRow = kChunk * (BF ? 2 : 4) + 16;
+    static constexpr int kStage = kTile * (kXRow + kWRow);
+    static constexpr int kBytes = kStages * kStage;
+    static_assert(kBytes >= kWarps * kTile * kTile * 4, "the warps' sums lie in the stages");
+    static_assert(kBytes <= 232448, "shared memory budget");
+};
+
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
+
+// four bf16 as two pairs of fp32
+__device__ __forceinline__ void widen4(uint2 v, uint64_t (&p)[2])
+{
+    p[0] = pair_of(v.x << 16, v.x & 0xFFFF0000u);
+    p[1] = pair_of(v.y << 16, v.y & 0xFFFF0000u);
+}
+
+__device__ __forceinline__ void fma_pair(uint64_t &c, uint64_t a, uint64_t b)
+{
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+
+// grid: (parts of h, experts / 32, tokens / 32); out fp32 [part][T][E].  A warp computes the whole
+// tile over every eighth run of 32 columns, a lane 4 tokens x 8 experts of it.
+template <bool BF>
+__global__ void __launch_bounds__(kThreads, 1) route_tile_kernel(const RouteArgs a, float *out)
+{
+    using S = TileSmem<BF>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int e0 = blockIdx.y * kTile, t0 = blockIdx.z * kTile;
+    const int part = (a.H + 8 * (int)gridDim.x - 1) / (8 * (int)gridDim.x) * 8;
+    const int h0 = min((int)blockIdx.x * part, a.H), h1 = min(h0 + part, a.H);
+    const int chunks = (h1 - h0 + kChunk - 1) / kChunk;
+    grid_launch_next();   // it waits for this grid's end before it reads
+    // a thread copies the same 16 bytes of columns of every 8th row (of w's fp32 rows two such)
+    constexpr int PER = BF ? 8 : 4, WU = kChunk / PER / 32;   // columns of 16 bytes of w; units of a thread
+    const int u = lane, r0 = warp;
+    const uint16_t *xp = a.x + h0 + u * 8;
+    const char *wp = static_cast<const char *>(a.w) + (int64_t)(h0 + u * PER) * (16 / PER);
+    int64_t xrow[kTile / 8], wrow[kTile / 8];
+#pragma unroll
+    for (int i = 0; i < kTile / 8; ++i) {
+        xrow[i] = (int64_t)min(t0 + r0 + 8 * i, a.T - 1) * a.xs;
+        wrow[i] = (int64_t)min(e0 + r0 + 8 * i, a.E - 1) * a.H * (16 / PER);
+    }
+    auto copy = [&](int c) {
+        if (c < chunks) {
+            const uint32_t st = smem_u32(smem + c % kStages * S::kStage) + u * 16;
+            const uint32_t x = st + r0 * S::kXRow, w = st + kTile * S::kXRow + r0 * S::kWRow;
+            const int left = h1 - h0 - c * kChunk;   // columns of the part from this chunk on
+            const bool ok = u * 8 < left;
+#pragma unroll
+            for (int i = 0; i < kTile / 8; ++i)
+                cp_async_cg16_or_zero(x + 8 * i * S::kXRow, ok ? xp + xrow[i] + c * kChunk : a.x, ok);
+#pragma unroll
+            for (int j = 0; j < WU; ++j) {
+                const bool in = (u + 32 * j) * PER < left;
+#pragma unroll
+                for (int i = 0; i < kTile / 8; ++i)
+                    cp_async_cg16_or_zero(w + 8 * i * S::kWRow + 512 * j,
+                                          in ? wp + wrow[i] + (c * kChunk + 32 * j * PER) * (16 / PER) : static_cast<const char *>(a.w), in);
+            }
+        }
+        cp_async_commit();
+    };
+    for (int c = 0; c < kStages - 1; ++c)
+        copy(c);
+    // tokens ti + 8 i, experts ei + 4 j
+    const int ti = lane >> 2, ei = lane & 3;
+    uint64_t acc[4][8] = {};   // sums over the even and the odd columns
+    for (int c = 0; c < chunks; ++c) {
+        cp_async_wait<kStages - 2>();
+        __syncthreads();   // everyone's copies of chunk c are there, and chunk c - 1 is read
+        copy(c + kStages - 1);
+        const uint32_t x = smem_u32(smem + c % kStages * S::kStage) + ti * S::kXRow;
+        const uint32_t w = smem_u32(smem + c % kStages * S::kStage) + kTile * S::kXRow + ei * S::kWRow;
+#pragma unroll 4
+        for (int col = warp * 32; col < warp * 32 + 32; col += 4) {
+            uint64_t xv[4][2], wv[2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                widen4(ld_shared_v2(x + 8 * i * S::kXRow + col * 2), xv[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (BF) {
+                    widen4(ld_shared_v2(w + 4 * j * S::kWRow + col * 2), wv);
+                } else {
+                    const uint4 r = ld_shared_v4(w + 4 * j * S::kWRow + col * 4);
+                    wv[0] = pair_of(r.x, r.y);
+                    wv[1] = pair_of(r.z, r.w);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    fma_pair(acc[i][j], xv[i][0], wv[0]);
+                    fma_pair(acc[i][j], xv[i][1], wv[1]);
+                }
+            }
+        }
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    float *sums = reinterpret_cast<float *>(smem);   // [warp][token][expert]
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            sums[(warp * kTile + ti + 8 * i) * kTile + ei + 4 * j] =
+                __uint_as_float((uint32_t)acc[i][j]) + __uint_as_float((uint32_t)(acc[i][j] >> 32));
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTile * kTile; i += kThreads) {
+        float s = sums[i];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w)
+            s += sums[w * kTile * kTile + i];
+        const int t = t0 + i / kTile, e = e0 + i % kTile;
+        if (t < a.T && e < a.E)
+            __stcg(out + ((int64_t)blockIdx.x * a.T + t) * a.E + e, s);
+    }
+}
+
+// a warp per token
+__global__ void __launch_bounds__(128) route_choose_kernel(const RouteArgs a, const float *logits, int parts)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
+    grid_wait();
+    if (t < a.T)
+        choose_token(a, t, logits, parts, reinterpret_cast<float *>(smem) + (threadIdx.x >> 5) * a.E);
+}
+
+// The number of parts that ends soonest: waves of CTAs, each as long as a part and two chunks
+// more (its first copies, and adding the sums).
+int tile_parts(const RouteArgs &a, int num_sms)
+{
+    const int tiles = ((a.E + kTile - 1) / kTile) * ((a.T + kTile - 1) / kTile);
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int p = 1; p <= std::min(kMaxParts, (a.H + kChunk - 1) / kChunk); ++p) {
+        const int64_t cost = (int64_t)((tiles * p + num_sms - 1) / num_sms) * ((a.H + p - 1) / p + 2 * kChunk);
+        if (cost < least) {
+            least = cost;
+            best = p;
+        }
+    }
+    return best;
 }
 
 template <int TB, int EB, bool BF>
-cudaError_t launch_typed(const RouteArgs &a, float *ws, uint32_t *counters, cudaStream_t st)
+cudaError_t launch_typed(const RouteArgs &a, float *ws, uint32_t *counter, cudaStream_t st)
 {
-    const dim3 grid((a.E + EB - 1) / EB, (a.T + kTokens - 1) / kTokens);
-    route_kernel<TB, EB, BF><<<grid, kThreads, sizeof(float) * kWarps * a.E, st>>>(a, ws, counters);
+    route_kernel<TB, EB, BF><<<(a.E + EB - 1) / EB, kThreads, kWarps * a.E * 4, st>>>(a, ws, counter);
     return cudaGetLastError();
+}
+
+template <bool BF>
+cudaError_t launch_tiles(const RouteArgs &a, float *ws, int num_sms, cudaStream_t st)
+{
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(route_tile_kernel<BF>), TileSmem<BF>::kBytes);
+    if (e != cudaSuccess)
+        return e;
+    const int parts = tile_parts(a, num_sms);
+    route_tile_kernel<BF><<<dim3(parts, (a.E + kTile - 1) / kTile, (a.T + kTile - 1) / kTile), kThreads, TileSmem<BF>::kBytes, st>>>(a, ws);
+    return launch(route_choose_kernel, dim3((a.T + 3) / 4), 128, (size_t)4 * a.E * 4, 1, true, st, a, static_cast<const float *>(ws), parts);
 }
 
 }  // namespace
 
-int64_t route_ws_floats(const RouteArgs &a) { return (int64_t)a.T * a.E; }
+int64_t route_ws_floats(const RouteArgs &a, int num_sms)
+{
+    return (int64_t)a.T * a.E * (a.T <= kTokens ? 1 : tile_parts(a, num_sms));
+}
 
-cudaError_t launch_route(const RouteArgs &a, float *ws, uint32_t *counters, cudaStream_t st)
+cudaError_t launch_route(const RouteArgs &a, float *ws, uint32_t *counter, int num_sms, cudaStream_t st)
 {
     if (a.T == 1)
-        return a.w_bf16 ? launch_typed<1, 1, true>(a, ws, counters, st) : launch_typed<1, 1, false>(a, ws, counters, st);
-    return a.w_bf16 ? launch_typed<4, 4, true>(a, ws, counters, st) : launch_typed<4, 4, false>(a, ws, counters, st);
+        return a.w_bf16 ? launch_typed<1, 1, true>(a, ws, counter, st) : launch_typed<1, 1, false>(a, ws, counter, st);
+    if (a.T <= kTokens)
+        return a.w_bf16 ? launch_typed<4, 4, true>(a, ws, counter, st) : launch_typed<4, 4, false>(a, ws, counter, st);
+    return a.w_bf16 ? launch_tiles<true>(a, ws, num_sms, st) : launch_tiles<false>(a, ws, num_sms, st);
 }
 
 }  // namespace gemmar

@@ -687,6 +687,13 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
 // 16-byte global -> shared copy that bypasses L1 (cp.async, generic proxy):
 // the executing thread sees the data after a cp.async.wait_group that covers it.
 __device__ __forceinline__ void cp_async_cg16(uint32_t dst, const void *src)
@@ -727,6 +734,15 @@ __device__ __forceinline__ void cp_async_wait()
 __device__ __forceinline__ void red_release_add(uint32_t *p, uint32_t v)
 {
     asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// Adds and returns what was there: a release of what came before (of the CTA's other threads too, after
+// a barrier) and an acquire of what the earlier adders released.
+__device__ __forceinline__ uint32_t add_acq_rel(uint32_t *p, uint32_t v)
+{
+    uint32_t old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
 }
 
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t *p)

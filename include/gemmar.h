@@ -609,7 +609,7 @@ enum { GEMMAR_SCORE_SOFTMAX = 0, GEMMAR_SCORE_SIGMOID = 1 };
  * near to be told apart in fp32, the order is decided in 64 bits.
  *   x bf16 [T,H] with a row stride; w [E,H] of w_dtype, bias fp32 [E] or NULL; ids int32 [T,k];
  *   weights fp32 [T,k].  H % 8 == 0, H <= 65536, T, E and k within the limits above, k <= E.
- * Scratch: T E floats.
+ * Scratch: 16 T E floats at most (T E for 8 tokens and fewer).
  */
 int moe_route(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, const void *w, int w_dtype, const float *bias,
               int64_t T, int64_t H, int E, int k, int score, int renorm, float factor, int32_t *ids, float *weights,
