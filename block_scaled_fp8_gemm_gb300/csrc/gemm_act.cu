@@ -37,15 +37,19 @@ constexpr int kBBytes = 256 * 128;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kSteps = 4;        // K-steps whose buffer is on record: more than can be under way
 constexpr int kOffB = kStages * kABytes;
-constexpr int kOffBar = kOffB + kStages * kBBytes;
+constexpr int kOffBias = kOffB + kStages * kBBytes;      // [4 finish warps][256] of the tile's columns
+constexpr int kOffBar = kOffBias + 4 * 1024;
 constexpr int kNumBars = 2 * kStages + kSteps + 5;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
 constexpr int kSmemBytes = kOffMisc + 8 + 4 * kSteps + 8 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-// setmaxnreg: warps 0-3, promotion, finish, of 128 a thread
-constexpr int kRegsLow = 40, kRegsPromote = 176, kRegsFinish = 120;
-constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsPromote + 128 * kRegsFinish;
-static_assert(kRegsNeeded <= 65536, "register split");
+// setmaxnreg: warps 0-3, promotion, finish, of 128 a thread.  An ungated finish has the next block of
+// sums under way.
+constexpr int kRegsLow = 40;
+template <bool GATED> constexpr int kRegsPromote = GATED ? 184 : 176;
+template <bool GATED> constexpr int kRegsFinish = GATED ? 104 : 120;
+constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsPromote<true> + 128 * kRegsFinish<true>;
+static_assert(kRegsNeeded <= 65536 && 128 * kRegsLow + 256 * kRegsPromote<false> + 128 * kRegsFinish<false> == kRegsNeeded, "register split");
 constexpr int kGroupM = 16;      // row tiles that share their columns of B while they are in L2
 struct Tile {
     int m0, n0;
@@ -87,18 +91,22 @@ __device__ __forceinline__ void store32(char *p, bool whole, const uint32_t *r)
     }
 }
 
-// 32 columns of a thread's row as bf16 or fp32
+// 16 columns of a thread's row as bf16
+__device__ __forceinline__ void store_bf16x16(char *p, bool whole, const float *v)
+{
+    uint32_t r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        r[j] = bf16x2_from_f32(v[2 * j], v[2 * j + 1]);
+    store32(p, whole, r);
+}
+
+// 32 columns as bf16 or fp32
 __device__ __forceinline__ void store_cols(char *p, bool whole, bool bf16, const float *v)
 {
     if (bf16) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t r[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                r[j] = bf16x2_from_f32(v[16 * i + 2 * j], v[16 * i + 2 * j + 1]);
-            store32(p + 32 * i, whole, r);
-        }
+        store_bf16x16(p, whole, v);
+        store_bf16x16(p + 32, whole, v + 16);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -106,16 +114,17 @@ __device__ __forceinline__ void store_cols(char *p, bool whole, bool bf16, const
     }
 }
 
-// v += the 32 values at p
-__device__ __forceinline__ void add_bias(float (&v)[32], const float *p)
+// v += the W values at p in shared memory
+template <int W>
+__device__ __forceinline__ void add_bias(float (&v)[W], uint32_t p)
 {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + j);
-        v[4 * j] += b.x;
-        v[4 * j + 1] += b.y;
-        v[4 * j + 2] += b.z;
-        v[4 * j + 3] += b.w;
+    for (int j = 0; j < W / 4; ++j) {
+        const uint4 b = ld_shared_v4(p + j * 16);
+        v[4 * j] += __uint_as_float(b.x);
+        v[4 * j + 1] += __uint_as_float(b.y);
+        v[4 * j + 2] += __uint_as_float(b.z);
+        v[4 * j + 3] += __uint_as_float(b.w);
     }
 }
 
@@ -254,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
             wait_teardown(final_bar, prm.status, prm.timeout_ns);
         }
     } else if (warp < 12) {
-        setmaxnreg_inc<kRegsPromote>();
+        setmaxnreg_inc<kRegsPromote<GATED>>();
         // ---------------------------------------------------- promotion
         const int q = warp & 3, h = (warp - 4) >> 2;   // lane quarter, half of the accumulator's columns
         const int row = q * 32 + lane;
@@ -326,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
             }
         }
     } else {
-        setmaxnreg_dec<kRegsFinish>();
+        setmaxnreg_dec<kRegsFinish<GATED>>();
         // ---------------------------------------------------- finish
         const int q = warp & 3;
         const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
@@ -334,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
         const int r_bytes = e.r_bf16 ? 2 : 4, c_bytes = e.c_bf16 ? 2 : 4;
         const bool r_whole = whole32(e.res, e.rs * r_bytes), c_whole = whole32(e.C, e.cs * c_bytes);
         const bool z_whole = whole32(e.z, 0), q_whole = whole32(e.q, 0);   // N is a multiple of 128
+        const uint32_t bias = smem_u32(smem + kOffBias + q * 1024);   // the warp's own copy
         uint32_t parked = 0;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++parked) {
             const Tile c = decode(t, mt, nt, BN);
@@ -360,6 +370,19 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
             fetch_residual(0, 0);
             if (e.r_bf16)
                 fetch_residual(32, 1);
+            if (e.bias != nullptr) {
+                // 256 sums' bias: a tile's columns, or 128 of both halves
+                __syncwarp();   // every lane is through with the last tile's
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int k = lane + 32 * i, n = c.n0 + (GATED ? k % 32 : k) * 4;   // four columns
+                    float4 b = make_float4(0, 0, 0, 0);
+                    if (n < e.N)
+                        b = __ldg(reinterpret_cast<const float4 *>(e.bias + (GATED && i ? e.N : 0) + n));
+                    st_shared_v4(bias + k * 16, make_uint4(__float_as_uint(b.x), __float_as_uint(b.y), __float_as_uint(b.z), __float_as_uint(b.w)));
+                }
+                __syncwarp();
+            }
             if (e.res != nullptr) {
                 // the next tile's rows of it into L2
                 const Tile d = decode(min(t + (int)gridDim.x, tiles - 1), mt, nt, BN);
@@ -378,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
             auto block = [&](float (&v)[32], int col, int half) {
                 const int n0 = c.n0 + col;
                 if (e.bias != nullptr)
-                    add_bias(v, e.bias + n0);
+                    add_bias(v, bias + col * 4);
                 char *z = reinterpret_cast<char *>(e.z) + (m * P + n0) * 2;
                 if (e.z != nullptr && inside)
                     store_cols(z, z_whole, true, v);
@@ -390,16 +413,20 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                     }
                 });
                 if (GATED) {
-                    float u[32];
-                    tmem_ld_x32(park + 128 + col, bits(u));
-                    tmem_wait_ld(bits(u));
-                    if (e.bias != nullptr)
-                        add_bias(u, e.bias + e.N + n0);
-                    if (e.z != nullptr && inside)
-                        store_cols(z + (int64_t)e.N * 2, z_whole, true, u);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] *= u[i];
+                    for (int i = 0; i < 32; i += 16) {
+                        float u[16];
+                        uint32_t(&r)[16] = *reinterpret_cast<uint32_t(*)[16]>(&u);
+                        tmem_ld_x16(park + 128 + col + i, r);
+                        tmem_wait_ld(r);
+                        if (e.bias != nullptr)
+                            add_bias(u, bias + 512 + (col + i) * 4);
+                        if (e.z != nullptr && inside)
+                            store_bf16x16(z + ((int64_t)e.N + i) * 2, z_whole, u);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            v[i + j] *= u[j];
+                    }
                 }
                 if (has_res) {
                     if (e.r_bf16) {
