@@ -12,7 +12,8 @@
 //
 // The order of two experts whose scores agree to fp32's rounding would depend on how the
 // sums are split.  Such tokens are decided in 64 bits: the logits in question are summed
-// again in double (a few microseconds, for about one token in a thousand).
+// again with what their roundings lost (a few microseconds, for about one token in a thousand).
+// Without a bias the order is the logits' own, which neither saturates nor underflows.
 #include <algorithm>
 
 #include "e4m3_encode.cuh"
@@ -28,6 +29,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokens = 8;        // tokens of the first form: one warp chooses for each
 static_assert(kTokens == kWarps, "a warp per token");
+constexpr int kMaxExperts = 1024;
 
 // 8 values of a row of the router
 template <bool BF>
@@ -54,22 +56,24 @@ __device__ __forceinline__ const void *router_row(const RouteArgs &a, int e)
     return static_cast<const char *>(a.w) + (int64_t)e * a.H * (a.w_bf16 ? 2 : 4);
 }
 
-// A score as an unsigned number of the same order; 0: not to be chosen (NaN, -inf).  The warp's largest
-// is then one instruction.
+// A number as an unsigned one of the same order, never 0 but for a NaN.  The warp's largest is then
+// one instruction, and 0 what is not to be chosen.
 __device__ __forceinline__ uint32_t key_of(float s)
 {
     const uint32_t b = __float_as_uint(s);
-    return s > -INFINITY ? (b & 0x80000000u ? ~b : b | 0x80000000u) : 0u;
+    return s == s ? (b & 0x80000000u ? ~b : b | 0x80000000u) : 0u;
 }
 __device__ __forceinline__ float score_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key); }
 
-// x[t] . w[e] in double by the whole warp
+// x[t] . w[e] by the whole warp, every product and sum with its rounding error carried along
+// (error-free sums and products by the published methods of Knuth and Dekker): about 2^-45 of the
+// terms' sizes, on the fp32 units, as those for fp64 are few.
 __device__ double logit64(const RouteArgs &a, int t, int e)
 {
     const int lane = threadIdx.x & 31;
     const uint16_t *x = a.x + (int64_t)t * a.xs;
     const void *w = router_row(a, e);
-    double s = 0.0;
+    float hi = 0.0f, lo = 0.0f;
     for (int h = lane * 8; h < a.H; h += 256) {
         float xv[8], wv[8];
         load8<true>(x, h, xv);
@@ -78,76 +82,73 @@ __device__ double logit64(const RouteArgs &a, int t, int e)
         else
             load8<false>(w, h, wv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            s = fma((double)xv[i], (double)wv[i], s);
+        for (int i = 0; i < 8; ++i) {
+            const float p = __fmul_rn(xv[i], wv[i]), pe = __fmaf_rn(xv[i], wv[i], -p);
+            const float s = __fadd_rn(hi, p), b = __fsub_rn(s, hi);
+            lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(p, b)), pe));
+            hi = s;
+        }
     }
+    double s = (double)hi + (double)lo;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
         s += __shfl_xor_sync(0xffffffffu, s, d);
     return s;
 }
 
-// The selection score in double; p is the fp32 score without the bias.
-struct Scores64 {
-    bool soft, sums;      // sums: divided by their sum (where a bias is added)
-    double top, sum;
+// What orders the experts, in double: the logit, or the score with its bias.
+struct Order64 {
+    bool soft, biased;
+    double top, sum;      // of the softmax
     __device__ double of(double logit, double bias) const
     {
-        if (!soft)
-            return 1.0 / (1.0 + exp(-logit)) + bias;
-        return sums ? exp(logit - top) / sum + bias : exp(logit - top);
+        if (!biased)
+            return logit;
+        return (soft ? exp(logit - top) / sum : 1.0 / (1.0 + exp(-logit))) + bias;
     }
 };
 
-// The first k in double of the experts whose fp32 score is at least `least`, for the rare token
-// where fp32 cannot tell: lane j gets the j-th.  p: fp32 scores without the bias, `scale` their
-// factor, zero: every logit of the token is exactly 0.
-__device__ __noinline__ int decide64(const RouteArgs &a, int t, const float *p, float scale, float least, int k, Scores64 s, bool zero)
+// The first k in double of the experts whose fp32 order value is at least `least`, for the rare
+// token where fp32 cannot tell: lane j gets the j-th.  value: the fp32 order values, in shared
+// memory; zero: every logit of the token is exactly 0.
+__device__ __noinline__ int decide64(const RouteArgs &a, int t, const float *value, float least, int k, Order64 o, bool zero)
 {
     const int lane = threadIdx.x & 31;
-    int mine = -1;
-    double last = INFINITY;
-    int last_e = -1;
-    // k times the best one after the last: candidates are few, and their scores are summed anew
-    // each time rather than kept
-    for (int j = 0; j < k; ++j) {
-        double best = -INFINITY;
-        int best_e = -1;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane;
-            const float bias = e < a.E && a.bias ? __ldg(a.bias + e) : 0.0f;
-            const float f = e < a.E ? p[e] * scale + bias : -INFINITY;
-            unsigned todo = __ballot_sync(0xffffffffu, f > -INFINITY && f >= least);
-            while (todo) {
-                const int who = __ffs(todo) - 1, c = e0 + who;
-                todo &= todo - 1;
-                const double x = zero ? 0.0 : logit64(a, t, c);
-                const double b = (double)__shfl_sync(0xffffffffu, bias, who);
-                // an infinite logit's fp32 score is exact
-                const double d = x > -INFINITY && x < INFINITY ? s.of(x, b) : (double)__shfl_sync(0xffffffffu, f, who);
-                const bool after = d < last || (d == last && c > last_e);
-                if (after && (best_e < 0 || d > best)) {
-                    best = d;
-                    best_e = c;
-                }
+    double mine = -INFINITY;   // lane j: the j-th best so far, and whose
+    int mine_e = -1, count = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+        const float f = e0 + lane < a.E ? value[e0 + lane] : -INFINITY;
+        unsigned todo = __ballot_sync(0xffffffffu, f >= least && e0 + lane < a.E);
+        while (todo) {
+            const int who = __ffs(todo) - 1, e = e0 + who;
+            todo &= todo - 1;
+            const double x = zero ? 0.0 : logit64(a, t, e);
+            // an infinite logit's fp32 value is exact
+            const double d = x > -INFINITY && x < INFINITY ? o.of(x, o.biased ? (double)__ldg(a.bias + e) : 0.0)
+                                                           : (double)__shfl_sync(0xffffffffu, f, who);
+            // its place behind the ones that are not smaller (equal ones have lower numbers)
+            const int place = __popc(__ballot_sync(0xffffffffu, lane < count && mine >= d));
+            const double up = __shfl_up_sync(0xffffffffu, mine, 1);
+            const int up_e = __shfl_up_sync(0xffffffffu, mine_e, 1);
+            if (lane >= place) {
+                mine = lane == place ? d : up;
+                mine_e = lane == place ? e : up_e;
             }
+            count = min(count + 1, 32);
         }
-        if (lane == j)
-            mine = best_e;
-        last = best;
-        last_e = best_e;
     }
-    return mine;
+    return lane < k ? mine_e : -1;
 }
 
 // One warp chooses token t's experts from its logits in global memory, which other CTAs wrote, in
-// `parts` to be added.  score: [E] in shared memory, the warp's own.  PER: experts of a lane
+// `parts` to be added.  score: [2 E] in shared memory, the warp's own.  PER: experts of a lane
 // (E <= 32 PER), lane + 32 i.
 template <int PER>
 __device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *logits, int parts, float *score)
 {
     const int lane = threadIdx.x & 31;
     const bool soft = a.score == 0;
+    float *order = score + a.E;
     float v[PER], bias[PER];             // logits, then scores without the bias
     float top = -INFINITY, big = 0.0f;   // largest logit, largest size of one
 #pragma unroll
@@ -177,16 +178,21 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *l
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
     // exponentials to be divided by their sum, or sigmoids
+    const bool biased = a.bias != nullptr;
+    uint32_t key[PER];
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
+        key[i] = lane + 32 * i < a.E ? key_of(v[i]) : 0u;   // the order without a bias
         // of the softmax's both may be infinite; a NaN logit is no expert's
         const float x = soft && v[i] == top ? 1.0f : expf(soft ? v[i] - top : -v[i]);
-        v[i] = soft ? x : __fdividef(1.0f, 1.0f + x);
+        const float p = soft ? x : __fdividef(1.0f, 1.0f + x);
         if (lane + 32 * i < a.E) {
-            score[lane + 32 * i] = v[i];
-            sum += v[i] >= 0.0f ? v[i] : 0.0f;
+            score[lane + 32 * i] = p;
+            order[lane + 32 * i] = v[i];
+            sum += p >= 0.0f ? p : 0.0f;
         }
+        v[i] = p;
     }
     float scale = 1.0f;
     if (soft) {
@@ -195,13 +201,20 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *l
             sum += __shfl_xor_sync(0xffffffffu, sum, d);
         scale = 1.0f / sum;
     }
-    uint32_t key[PER];
+    // how far fp32's rounding may move what orders: the logits' sums to 2^-20 of the largest
+    // logit (twenty times the spread of such sums), scores besides by a few units in the last place
+    float tol = 0x1p-20f * big;
+    if (biased) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        key[i] = lane + 32 * i < a.E ? key_of(v[i] * scale + bias[i]) : 0u;
-    // how far fp32's rounding may move a score: the logits' sums to 2^-20 of the largest
-    // logit (twenty times the spread of such sums), the rest to a few units in the last place
-    const float tol = 0x1p-20f * big * (soft ? scale : 0.25f) + 0x1p-21f * scale;
+        for (int i = 0; i < PER; ++i) {
+            const float s = v[i] * scale + bias[i];
+            if (lane + 32 * i < a.E) {
+                key[i] = s > -INFINITY ? key_of(s) : 0u;
+                order[lane + 32 * i] = s;
+            }
+        }
+        tol = tol * (soft ? scale : 0.25f) + 0x1p-21f * scale;
+    }
     bool close = false;                  // whether neighbours in the order are too close to tell
     int mine = -1, chosen = 0;           // lane j keeps the j-th choice (k <= 16)
     float last = INFINITY, cut = -INFINITY;
@@ -215,7 +228,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *l
         if (best == 0)
             break;
         const float s = score_of(best);
-        close = close || last - s <= tol + 0x1p-21f * fabsf(s);
+        close = close || last - s <= tol + (biased ? 0x1p-21f * fabsf(s) : 0.0f);   // no two infinities
         last = s;
         if (j == a.k)
             break;
@@ -235,7 +248,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *l
     __syncwarp();
     if (close && chosen > 0) {
         double sum64 = 1.0;
-        if (soft && a.bias != nullptr) {
+        if (soft && biased) {
             sum64 = 0.0;
             for (int e = lane; e < a.E; e += 32)
                 sum64 += score[e] >= 0.0f ? (double)score[e] : 0.0;
@@ -243,8 +256,8 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *l
             for (int d = 16; d > 0; d >>= 1)
                 sum64 += __shfl_xor_sync(0xffffffffu, sum64, d);
         }
-        mine = decide64(a, t, score, scale, cut - 2.0f * (tol + 0x1p-21f * fabsf(cut)), chosen,
-                        Scores64{soft, a.bias != nullptr, (double)top, sum64}, big == 0.0f);
+        const float near = 2.0f * (tol + (biased ? 0x1p-21f * fabsf(cut) : 0.0f));
+        mine = decide64(a, t, order, near > 0.0f ? cut - near : cut, chosen, Order64{soft, biased, (double)top, sum64}, big == 0.0f);
     }
     float w = mine >= 0 ? score[mine] * scale : 0.0f, all = w;
     if (a.renorm) {
@@ -275,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a, floa
 {
     __shared__ float part[kWarps][TB * EB];
     extern __shared__ __align__(16) uint8_t smem[];
-    float *scores = reinterpret_cast<float *>(smem);   // [kWarps][E]
+    float *scores = reinterpret_cast<float *>(smem);   // [kWarps][2 E]
     __shared__ bool chooses;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e0 = blockIdx.x * EB;
@@ -324,7 +337,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a, floa
     }
     __syncthreads();
     if (chooses && warp < a.T)
-        choose_token(a, warp, logits, 1, scores + warp * a.E);
+        choose_token(a, warp, logits, 1, scores + warp * 2 * a.E);
 }
 
 // ---- tiles of 32 tokens x 32 experts
@@ -462,7 +475,7 @@ __global__ void __launch_bounds__(128) route_choose_kernel(const RouteArgs a, co
     const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
     grid_wait();
     if (t < a.T)
-        choose_token(a, t, logits, parts, reinterpret_cast<float *>(smem) + (threadIdx.x >> 5) * a.E);
+        choose_token(a, t, logits, parts, reinterpret_cast<float *>(smem) + (threadIdx.x >> 5) * 2 * a.E);
 }
 
 // The number of parts that ends soonest: waves of CTAs, each as long as a part and two chunks
@@ -485,7 +498,10 @@ int tile_parts(const RouteArgs &a, int num_sms)
 template <int TB, int EB, bool BF>
 cudaError_t launch_typed(const RouteArgs &a, float *ws, uint32_t *counter, cudaStream_t st)
 {
-    route_kernel<TB, EB, BF><<<(a.E + EB - 1) / EB, kThreads, kWarps * a.E * 4, st>>>(a, ws, counter);
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(route_kernel<TB, EB, BF>), kWarps * kMaxExperts * 8);
+    if (e != cudaSuccess)
+        return e;
+    route_kernel<TB, EB, BF><<<(a.E + EB - 1) / EB, kThreads, a.T * a.E * 8, st>>>(a, ws, counter);
     return cudaGetLastError();
 }
 
@@ -497,7 +513,7 @@ cudaError_t launch_tiles(const RouteArgs &a, float *ws, int num_sms, cudaStream_
         return e;
     const int parts = tile_parts(a, num_sms);
     route_tile_kernel<BF><<<dim3(parts, (a.E + kTile - 1) / kTile, (a.T + kTile - 1) / kTile), kThreads, TileSmem<BF>::kBytes, st>>>(a, ws);
-    return launch(route_choose_kernel, dim3((a.T + 3) / 4), 128, (size_t)4 * a.E * 4, 1, true, st, a, static_cast<const float *>(ws), parts);
+    return launch(route_choose_kernel, dim3((a.T + 3) / 4), 128, (size_t)4 * a.E * 8, 1, true, st, a, static_cast<const float *>(ws), parts);
 }
 
 }  // namespace

@@ -606,7 +606,8 @@ enum { GEMMAR_SCORE_SOFTMAX = 0, GEMMAR_SCORE_SIGMOID = 1 };
  *   weights  = p of the chosen (without bias), over their sum where renorm, times factor
  * An expert whose p + bias is NaN or -inf is not chosen (a bias of -inf takes one out); where
  * fewer than k are left, id -1 with weight 0 fills up.  Scores are fp32; where two are too
- * near to be told apart in fp32, the order is decided in 64 bits.
+ * near to be told apart in fp32, the order is decided in 64 bits.  Without a bias it is the
+ * logits' order, also where the scores saturate.
  *   x bf16 [T,H] with a row stride; w [E,H] of w_dtype, bias fp32 [E] or NULL; ids int32 [T,k];
  *   weights fp32 [T,k].  H % 8 == 0, H <= 65536, T, E and k within the limits above, k <= E.
  * Scratch: 16 T E floats at most (T E for 8 tokens and fewer).

@@ -103,6 +103,28 @@ def test_route_scores_that_fp32_cannot_tell_apart(g, ctx, score, biased):
 
 
 @pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("T", [1, 40])
+def test_route_saturated_scores(g, ctx, score, T):
+    """Logits of many tens: most scores are 0 or 1 to fp32, the order is still the logits', and no slower."""
+    x, w, _ = router(T, 1024, 64, 16)
+    w = (w.float() * 80).bfloat16()
+    ids, weights = route(g, ctx, x, w, 8, score=score)
+    l = x.double() @ w.double().T
+    assert torch.equal(ids, torch.sort(l, dim=1, descending=True, stable=True).indices[:, :8].int())
+    p = torch.softmax(l, 1) if score == 0 else torch.sigmoid(l)
+    p = p.gather(1, ids.long())
+    el = 64 * 2.0 ** -24 * (x.double().abs() @ w.double().abs().T).amax(1, keepdim=True)
+    ff.within(weights, p / p.sum(1, keepdim=True), 4 * el + 2.0 ** -20)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    for _ in range(10):
+        g.moe_route(ctx, x, w, ids, weights, score=score)
+    end.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(end) < 10   # ms; a token that is decided in 64 bits takes some microseconds
+
+
+@pytest.mark.parametrize("score", [0, 1])
 def test_route_equal_scores_take_the_lowest(g, ctx, score):
     x, w, _ = router(20, 256, 48, 8)
     x[4] = 0                                   # a padded row: every logit is 0
