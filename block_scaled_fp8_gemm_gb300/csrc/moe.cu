@@ -41,7 +41,6 @@ namespace {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxSlots = 16;
-constexpr int kTake = 8;
 
 // NT: token columns of the first product; GROUPS: groups of 8 tokens in a chunk of the second.
 template <int NT_, int GROUPS_, int STAGES_, int BUFS_>
@@ -320,7 +319,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     if (warp < 4) {
         setmaxnreg_dec<kRegsLow>();
         if (warp == 0 && lane == 0) {
-            // ------------------------------------------------ weights
+            // ------------------------------------------------ weights: they pass through L2 without
+            // pushing out what the launch comes back to, its later steps' code among it
+            const uint64_t once = l2_evict_first();
             int stage = 0;
             uint32_t ph = 0;
             bool ok = true;
@@ -330,8 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                     return;
                 uint8_t *w = smem + stage * C::kStageBytes;
                 mbar_arrive_expect_tx(full + stage, 2 * kTileBytes);
-                tma_load_2d(w, tm, full + stage, kb * 128, row0);
-                tma_load_2d(w + kTileBytes, tm, full + stage, kb * 128, row1);
+                tma_load_2d(w, tm, full + stage, kb * 128, row0, once);
+                tma_load_2d(w + kTileBytes, tm, full + stage, kb * 128, row1, once);
                 if (++stage == C::kStages) {
                     stage = 0;
                     ph ^= 1;
@@ -668,14 +669,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                                      act_value<ACT>(zg.z) * zu.z * w, act_value<ACT>(zg.w) * zu.w * w);
                 });
                 const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(max4(hv))));
-                const float s = __fdiv_rn(m, 448.0f);
-                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (s > 0.0f) {
-                    v[0] = __fdiv_rn(hv.x, s);
-                    v[1] = __fdiv_rn(hv.y, s);
-                    v[2] = __fdiv_rn(hv.z, s);
-                    v[3] = __fdiv_rn(hv.w, s);
-                }
+                // s times the parts is h to 2^-22, whichever way the two quotients round
+                const float s = m * (1.0f / 448.0f), inv = s > 0.0f ? __fdividef(448.0f, m) : 0.0f;
+                float v[4] = {hv.x * inv, hv.y * inv, hv.z * inv, hv.w * inv};
                 uint8_t *o = prm.parts + (int64_t)p * a.I + jb * 128 + lane * 4;
 #pragma unroll
                 for (int part = 0; part < 3; ++part) {
@@ -756,46 +752,42 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                         __stcg(to + (int64_t)j * a.H, acc[j]);
             }
         }
-        const uint32_t quads = a.H / 4;   // a multiple of 32: a warp's are of one token
-        const uint32_t quad0 = ((warp - 4) * gridDim.x + blockIdx.x) * 32 + lane;
-        if (a.y != nullptr && quad0 < a.T * quads)
-            prefetch_l2(a.y + quad0 / quads * a.ys + quad0 % quads * 4);
+        // rows of out: a lane takes four columns and every fourth of the token's slots, eight lanes in a
+        // row 32 columns.  A tight loop: its code is fetched while the weights fill the memory's queues
+        const uint32_t octs = a.H / 32, oct0 = (warp - 4) * gridDim.x + blockIdx.x;
+        const int oct_lane = lane & 7, share = lane >> 3;
+        if (a.y != nullptr && oct0 < a.T * octs && share == 0)
+            prefetch_l2(a.y + oct0 / octs * a.ys + (oct0 % octs * 32 + oct_lane * 4));
         if (ok)
             everyone(2);
-        // -------- rows of out: four columns at a time, a token's experts in the order of its slots
         if (ok) {
-            for (uint32_t i = quad0; i < a.T * quads; i += gridDim.x * kEpiThreads) {
-                const int t = (int)(i / quads), col = (int)(i % quads) * 4;
-                uint2 y = make_uint2(0, 0);
-                if (a.y != nullptr)
-                    y = *reinterpret_cast<const uint2 *>(a.y + t * a.ys + col);
-                float4 sum = make_float4(bf16_lo(y.x), bf16_hi(y.x), bf16_lo(y.y), bf16_hi(y.y));
-                // kTake slots' loads under way at a time
-                const int64_t plane = (int64_t)pairs * a.H;
-                for (int s0 = 0; s0 < a.k; s0 += kTake) {
-                    float4 v[kTake], w[kTake];
-                    int planes[kTake];
-#pragma unroll
-                    for (int s = 0; s < kTake; ++s) {
-                        const uint32_t p = s0 + s < a.k ? slot[t * a.k + s0 + s] : 0xFFFFu;
-                        planes[s] = p == 0xFFFFu ? 0 : l2.planes(col / 256 * chunks + (int)(pair[p] >> 17));
-                        const float *from = prm.pieces + (int64_t)p * a.H + col;
-                        v[s] = planes[s] > 0 ? ld4(from) : make_float4(0, 0, 0, 0);
-                        w[s] = planes[s] > 1 ? ld4(from + plane) : make_float4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int s = 0; s < kTake; ++s) {
-                        if (planes[s] > 0)
-                            sum = add4(sum, v[s]);
-                        if (planes[s] > 1)
-                            sum = add4(sum, w[s]);
-                        const float *from = prm.pieces + (int64_t)slot[t * a.k + min(s0 + s, a.k - 1)] * a.H + col;
-                        for (int pl = 2; pl < planes[s]; ++pl)
-                            sum = add4(sum, ld4(from + pl * plane));
-                    }
+            const int64_t plane = (int64_t)pairs * a.H;
+#pragma unroll 1
+            for (uint32_t i = oct0; i < a.T * octs; i += gridDim.x * 8) {
+                const int t = (int)(i / octs), col = (int)(i - t * octs) * 32 + oct_lane * 4;
+                float4 sum = make_float4(0, 0, 0, 0);
+                if (share == 0 && a.y != nullptr) {
+                    const uint2 y = *reinterpret_cast<const uint2 *>(a.y + t * a.ys + col);
+                    sum = make_float4(bf16_lo(y.x), bf16_hi(y.x), bf16_lo(y.y), bf16_hi(y.y));
                 }
-                *reinterpret_cast<uint2 *>(a.out + t * a.os + col) =
-                    make_uint2(bf16x2_from_f32(sum.x, sum.y), bf16x2_from_f32(sum.z, sum.w));
+#pragma unroll 1
+                for (int s = share; s < a.k; s += 4) {
+                    const uint32_t p = slot[t * a.k + s];
+                    if (p == 0xFFFFu)
+                        continue;
+                    const float *from = prm.pieces + (int64_t)p * a.H + col;
+#pragma unroll 1
+                    for (int planes = l2.planes(col / 256 * chunks + (int)(pair[p] >> 17)); planes > 0; --planes, from += plane)
+                        sum = add4(sum, ld4(from));
+                }
+                __syncwarp();
+#pragma unroll
+                for (int d = 8; d < 32; d *= 2)
+                    sum = add4(sum, make_float4(__shfl_xor_sync(0xffffffffu, sum.x, d), __shfl_xor_sync(0xffffffffu, sum.y, d),
+                                                __shfl_xor_sync(0xffffffffu, sum.z, d), __shfl_xor_sync(0xffffffffu, sum.w, d)));
+                if (share == 0)
+                    *reinterpret_cast<uint2 *>(a.out + t * a.os + col) =
+                        make_uint2(bf16x2_from_f32(sum.x, sum.y), bf16x2_from_f32(sum.z, sum.w));
             }
         }
     }

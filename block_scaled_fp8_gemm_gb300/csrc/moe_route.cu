@@ -498,7 +498,7 @@ int tile_parts(const RouteArgs &a, int num_sms)
 template <int TB, int EB, bool BF>
 cudaError_t launch_typed(const RouteArgs &a, float *ws, uint32_t *counter, cudaStream_t st)
 {
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(route_kernel<TB, EB, BF>), kWarps * kMaxExperts * 8);
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(route_kernel<TB, EB, BF>), kWarps * kMaxExperts * 8, true);
     if (e != cudaSuccess)
         return e;
     route_kernel<TB, EB, BF><<<(a.E + EB - 1) / EB, kThreads, a.T * a.E * 8, st>>>(a, ws, counter);
@@ -511,6 +511,9 @@ cudaError_t launch_tiles(const RouteArgs &a, float *ws, int num_sms, cudaStream_
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(route_tile_kernel<BF>), TileSmem<BF>::kBytes);
     if (e != cudaSuccess)
         return e;
+    const cudaError_t c = ensure_dynamic_smem(reinterpret_cast<const void *>(route_choose_kernel), 4 * kMaxExperts * 8, true);
+    if (c != cudaSuccess)
+        return c;
     const int parts = tile_parts(a, num_sms);
     route_tile_kernel<BF><<<dim3(parts, (a.E + kTile - 1) / kTile, (a.T + kTile - 1) / kTile), kThreads, TileSmem<BF>::kBytes, st>>>(a, ws);
     return launch(route_choose_kernel, dim3((a.T + 3) / 4), 128, (size_t)4 * a.E * 8, 1, true, st, a, static_cast<const float *>(ws), parts);
