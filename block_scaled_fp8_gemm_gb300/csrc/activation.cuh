@@ -1,8 +1,8 @@
 // activation.cuh -- the activations of the feed-forward layers and their slopes, in fp32.
 //
-// Each is written as z times a factor in [0, 1] (its tail stays accurate where 1 + erf or
-// 1 + tanh would cancel), and where that factor or its slope has vanished the limit is
-// returned instead of a product with an infinity.
+// Each is written as z times a factor in [0, 1]: its tail stays accurate where 1 + erf or
+// 1 + tanh would cancel.  z enters that product no lower than -FLT_MAX and the factor's slope within
+// +-1e6 (where it has long vanished), so that no infinity meets a zero; a NaN stays one.
 #pragma once
 
 #include <cstdint>
@@ -20,21 +20,34 @@ constexpr float kGeluCubic = 0.044715f;
 // z / ln 2 once, which costs (2 + |z|) 2^-24 of its value: less than the sums before it.
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b)
+{
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+constexpr float kLowest = -3.402823466e38f;
+
+// The argument of the tanh form's sigmoid ((1 + tanh u) / 2 = sigmoid(2 u))
+__device__ __forceinline__ float tanh_arg(float z) { return 2.0f * kSqrt2OverPi * z * fmaf(kGeluCubic * z, z, 1.0f); }
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float z)
 {
     if constexpr (ACT == ACT_RELU)
-        return z < 0.0f ? 0.0f : z;   // a NaN stays one
-    if constexpr (ACT == ACT_SILU || ACT == ACT_GELU_TANH || ACT == ACT_GELU) {
-        float s;
-        if constexpr (ACT == ACT_SILU)
-            s = sigmoid(z);
-        else if constexpr (ACT == ACT_GELU_TANH)   // (1 + tanh u) / 2 = sigmoid(2 u)
-            s = sigmoid(2.0f * kSqrt2OverPi * (z + kGeluCubic * z * z * z));
-        else
-            s = 0.5f * erfcf(-0.70710678f * z);
-        return s == 0.0f ? 0.0f : z * s;
-    }
+        return max_nan(z, 0.0f);
+    if constexpr (ACT == ACT_SILU)
+        return max_nan(z, kLowest) * sigmoid(z);
+    if constexpr (ACT == ACT_GELU_TANH)
+        return max_nan(z, kLowest) * sigmoid(tanh_arg(z));
+    if constexpr (ACT == ACT_GELU)
+        return max_nan(z, kLowest) * (0.5f * erfcf(-0.70710678f * z));
     return z;
 }
 
@@ -45,25 +58,24 @@ __device__ __forceinline__ void act_slope(float z, float &value, float &slope)
     value = z;
     slope = 1.0f;
     if constexpr (ACT == ACT_RELU) {
-        value = z < 0.0f ? 0.0f : z;
-        slope = z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+        value = max_nan(z, 0.0f);
+        slope = z > 0.0f ? 1.0f : min_nan(value, 0.0f);   // 0, or the NaN
     }
-    if constexpr (ACT == ACT_SILU || ACT == ACT_GELU_TANH) {
-        // value = z s(v), slope = s + z s (1 - s) v'
-        float v = z, dv = 1.0f;
-        if constexpr (ACT == ACT_GELU_TANH) {
-            const float z2 = z * z;
-            v = 2.0f * kSqrt2OverPi * (z + kGeluCubic * z2 * z);
-            dv = 2.0f * kSqrt2OverPi * (1.0f + 3.0f * kGeluCubic * z2);
+    if constexpr (ACT == ACT_SILU || ACT == ACT_GELU_TANH || ACT == ACT_GELU) {
+        const float c = max_nan(min_nan(z, 1e6f), -1e6f);
+        float s, d;   // the factor, and its slope
+        if constexpr (ACT == ACT_SILU) {
+            s = sigmoid(z);
+            d = fmaf(-s, s, s);
+        } else if constexpr (ACT == ACT_GELU_TANH) {
+            s = sigmoid(tanh_arg(z));
+            d = fmaf(-s, s, s) * (2.0f * kSqrt2OverPi * fmaf(3.0f * kGeluCubic * c, c, 1.0f));
+        } else {
+            s = 0.5f * erfcf(-0.70710678f * z);
+            d = 0.3989422804f * __expf(-0.5f * c * c);
         }
-        const float s = sigmoid(v), t = s * (1.0f - s);
-        value = s == 0.0f ? 0.0f : z * s;
-        slope = t == 0.0f ? s : s + z * t * dv;
-    }
-    if constexpr (ACT == ACT_GELU) {
-        const float s = 0.5f * erfcf(-0.70710678f * z), d = 0.3989422804f * expf(-0.5f * z * z);
-        value = s == 0.0f ? 0.0f : z * s;
-        slope = d == 0.0f ? s : s + z * d;
+        value = max_nan(z, kLowest) * s;
+        slope = fmaf(c, d, s);
     }
 }
 

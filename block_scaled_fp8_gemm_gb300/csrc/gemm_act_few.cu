@@ -396,6 +396,8 @@ int gemm_act_few_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
 int64_t gemm_act_few_ns(int M, int N, int K, bool gated)
 {
+    if ((M + 63) / 64 > 65535)
+        return INT64_MAX;   // more chunks than a grid's third dimension has
     switch (gemm_act_few_rows(M)) {
     case 16: return (gated ? plan<Rows16, true>(M, N, K) : plan<Rows16, false>(M, N, K)).ns;
     case 32: return (gated ? plan<Rows32, true>(M, N, K) : plan<Rows32, false>(M, N, K)).ns;

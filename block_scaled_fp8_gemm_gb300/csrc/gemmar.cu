@@ -635,21 +635,31 @@ int check_rows(const void *p, int64_t stride, int64_t cols, int elem_bytes, bool
     return GEMMAR_OK;
 }
 
-// Do two bf16 matrices of T rows share elements?  Rows at one stride may lie between one
-// another (columns of a wider matrix); at two strides only the same start counts.
-bool rows_meet(const uint16_t *a, int64_t a_stride, int64_t a_cols, const uint16_t *b, int64_t b_stride, int64_t b_cols,
-               int64_t T)
+// Do two matrices of T rows share bytes?  Rows at one stride may lie between one another (columns of a
+// wider matrix); at two strides only the same start counts.  All in bytes.
+bool bytes_meet(const void *a, int64_t a_stride, int64_t a_row, const void *b, int64_t b_stride, int64_t b_row, int64_t T)
 {
+    if (a == nullptr || b == nullptr)
+        return false;
     if (a == b)
         return true;
     if (a_stride != b_stride && T > 1)
         return false;
-    const int64_t d = ((intptr_t)b - (intptr_t)a) / 2, last = (T - 1) * a_stride;
-    if (d >= last + a_cols || -d >= last + b_cols)
+    const int64_t d = (intptr_t)b - (intptr_t)a, last = (T - 1) * a_stride;
+    if (d >= last + a_row || -d >= last + b_row)
         return false;
     const int64_t off = a_stride > 0 && T > 1 ? ((d % a_stride) + a_stride) % a_stride : d;
-    return T == 1 || a_stride == 0 || off < a_cols || a_stride - off < b_cols;
+    return T == 1 || a_stride == 0 || off < a_row || a_stride - off < b_row;
 }
+
+bool rows_meet(const uint16_t *a, int64_t a_stride, int64_t a_cols, const uint16_t *b, int64_t b_stride, int64_t b_cols,
+               int64_t T)
+{
+    return bytes_meet(a, 2 * a_stride, 2 * a_cols, b, 2 * b_stride, 2 * b_cols, T);
+}
+
+// Do n contiguous bytes at a and m at b?
+bool ranges_meet(const void *a, int64_t n, const void *b, int64_t m) { return bytes_meet(a, n, n, b, m, m, 1); }
 
 int norm_shape(int64_t M, int64_t N)
 {
@@ -842,6 +852,16 @@ GEMMAR_API int gemm_blockscale_act(gemmar_ctx *ctx, const uint8_t *A, const floa
     if (!aligned16(A) || !aligned16(B) || !aligned16(sa) || !aligned16(sb) || !aligned16(bias) || !aligned16(q) ||
         !aligned16(scales) || !aligned16(z))
         return GEMMAR_ERR_ALIGN;
+    // an output over what is still being read; residual may be C itself
+    const int64_t P = gated ? 2 * N : N;
+    const int rb = elem_bytes(r_dtype), cb = elem_bytes(c_dtype);
+    if ((C != residual && bytes_meet(C, c_stride * cb, N * cb, residual, r_stride * rb, N * rb, M)) ||
+        ranges_meet(q, M * N, A, M * K) || ranges_meet(q, M * N, B, P * K) || ranges_meet(z, 2 * M * P, A, M * K) ||
+        ranges_meet(z, 2 * M * P, B, P * K) || ranges_meet(q, M * N, z, 2 * M * P) ||
+        (c_stride == N && (ranges_meet(C, M * N * cb, A, M * K) || ranges_meet(C, M * N * cb, B, P * K) ||
+                           ranges_meet(C, M * N * cb, q, M * N) || ranges_meet(C, M * N * cb, z, 2 * M * P))) ||
+        (residual && r_stride == N && (ranges_meet(residual, M * N * rb, q, M * N) || ranges_meet(residual, M * N * rb, z, 2 * M * P))))
+        return GEMMAR_ERR_ARG;
     if (!load_encode())
         return GEMMAR_ERR_CUDA;
     // 128 gated rows at N = 2048, K = 7168: 13 us as few rows, 31 as tiles; 512: 35 and 31
@@ -881,6 +901,11 @@ GEMMAR_API int gemm_blockscale_act_bwd(gemmar_ctx *ctx, const void *dout, int d_
         return rc;
     if (!aligned16(z) || !aligned16(dz) || !aligned16(dbias) || !aligned16(q) || !aligned16(scales))
         return GEMMAR_ERR_ALIGN;
+    const int64_t P = gated ? 2 * N : N, db = elem_bytes(d_dtype);
+    if ((dz && dz != z && ranges_meet(dz, 2 * M * P, z, 2 * M * P)) ||
+        (d_stride == N && ((dz && dz != dout && ranges_meet(dz, 2 * M * P, dout, M * N * db)) || ranges_meet(q, M * P, dout, M * N * db))) ||
+        ranges_meet(q, M * P, z, 2 * M * P) || ranges_meet(q, M * P, dz, 2 * M * P))
+        return GEMMAR_ERR_ARG;
     if (dbias && act_bwd_ws_floats(M, (int)N, gated, ctx->num_sms) > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
     const ActBwdArgs a{dout, d_dtype == GEMMAR_DTYPE_BF16, d_stride, z, act, gated, M, (int)N, dz, dbias, q, scales};
@@ -931,6 +956,9 @@ GEMMAR_API int moe_apply(gemmar_ctx *ctx, const uint8_t *xq, const float *xs, co
     if (!aligned16(xq) || !aligned16(xs) || !aligned16(ids) || !aligned16(weights) || !aligned16(place) ||
         !aligned16(w13) || !aligned16(s13) || !aligned16(w2) || !aligned16(s2))
         return GEMMAR_ERR_ALIGN;
+    if ((y != out && rows_meet(out, out_stride, H, y, y_stride, H, T)) ||
+        (out_stride == H && (ranges_meet(out, 2 * T * H, xq, T * H) || ranges_meet(out, 2 * T * H, ids, 4 * T * k))))
+        return GEMMAR_ERR_ARG;
     const MoeArgs a{xq, xs, ids, place, (int)(place ? places : 0), weights, w13, w2, s13, s2, (int)T, (int)H, (int)I, E, k,
                     act, y, y_stride, out, out_stride};
     const MoeLayout l = moe_layout(a, ctx->num_sms);

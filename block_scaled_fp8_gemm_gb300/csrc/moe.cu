@@ -90,7 +90,7 @@ struct Line {
     __device__ __forceinline__ Line(int items, int KB_) : KB(KB_)
     {
         const int units = items * KB;
-        per = max(1, (units + (int)gridDim.x - 1) / (int)gridDim.x);
+        per = max((units + (int)gridDim.x - 1) / (int)gridDim.x, (KB + 7) / 8);   // no item in more than 9 shares
         first = min(units, (int)blockIdx.x * per);
         end = min(units, first + per);
     }
@@ -830,14 +830,15 @@ cudaError_t launch_typed(const MoeParams &p, int num_sms, cudaStream_t st)
 
 }  // namespace
 
-// Sums of both products: an item's units lie in at most sms / items + 2 shares, and there are
-// at least as many experts as a token's slots name, so the planes of all pairs are at most
-// T (sms / tile pairs + 2 k) rows.
+// Sums of both products: an item's units lie in at most 9 shares and at most sms / items + 2, and
+// there are at least as many experts as a token's slots name, so the planes of all pairs are at
+// most T (sms / tile pairs + 2 k) rows, and 9 T k.
 MoeLayout moe_layout(const MoeArgs &a, int num_sms)
 {
     MoeLayout l;
     const int64_t IB = a.I / 128, J2 = (a.H / 128 + 1) / 2, slots = (int64_t)a.T * a.k;
-    l.hidden_scale = std::max(a.T * (num_sms / IB + 1 + 2 * a.k) * 2 * a.I, a.T * (num_sms / J2 + 1 + 2 * a.k) * (int64_t)a.H);
+    const int64_t rows1 = std::min<int64_t>(9 * a.k, num_sms / IB + 1 + 2 * a.k), rows2 = std::min<int64_t>(9 * a.k, num_sms / J2 + 1 + 2 * a.k);
+    l.hidden_scale = a.T * std::max(rows1 * 2 * a.I, rows2 * a.H);
     l.parts = l.hidden_scale + (slots * IB + 3) / 4 * 4;
     l.part_rows = 3 * (slots + 8);
     l.floats = l.parts + l.part_rows * a.I / 4;

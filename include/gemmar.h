@@ -563,7 +563,8 @@ enum { GEMMAR_ACT_NONE = 0, GEMMAR_ACT_RELU = 1, GEMMAR_ACT_SILU = 2, GEMMAR_ACT
  *   bias fp32 [N or 2N]; residual [M,N] of r_dtype with a row stride (0: one row for all);
  *   C [M,N] of c_dtype with a row stride; z bf16 [M, N or 2N].  C or q may be NULL (not both),
  *   z NULL leaves it out; q and scales go together.  residual may be C itself, at the same
- *   type and stride; otherwise outputs lie apart from the inputs and from each other.
+ *   type and stride; otherwise outputs lie apart from the inputs and from each other (GEMMAR_ERR_ARG
+ *   where contiguous ones, or C and residual, do not).
  * N % 128 == 0, K % 128 == 0, N (2N where gated) and K <= 65536, M <= 2^24.
  */
 int gemm_blockscale_act(gemmar_ctx *ctx, const uint8_t *A, const float *sa, const uint8_t *B, const float *sb,
@@ -631,6 +632,7 @@ int moe_route(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, const void *
  *   [E,H/128,I/128]; y bf16 [T,H] (NULL: 0) and out bf16 [T,H] with row strides; y may be out
  *   itself at the same stride.
  * H % 128 == 0, I % 128 == 0, H and 2I <= 65536; T, E and k within the limits above.
+ * Scratch: T k (9 max(2I, H) + I) + 8 I floats at most.
  */
 int moe_apply(gemmar_ctx *ctx, const uint8_t *xq, const float *xs, const int32_t *ids, const float *weights,
               const int32_t *place, int64_t places, const uint8_t *w13, const float *s13, const uint8_t *w2,
