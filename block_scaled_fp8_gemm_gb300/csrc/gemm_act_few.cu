@@ -15,7 +15,6 @@
 #include "e4m3_encode.cuh"
 #include "epilogue.cuh"
 #include "few_rows.cuh"
-#include "launch.cuh"
 
 namespace gemmar {
 using namespace ptx;
@@ -113,8 +112,6 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) gemm_act_few_kernel(const 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    grid_wait();   // nothing of global memory is touched before
-
     if (warp < 4) {
         setmaxnreg_dec<C::kLow>();
         if (warp == 0 && lane == 0) {
@@ -374,13 +371,10 @@ cudaError_t launch_typed(const ActParams &p, cudaStream_t st)
     if (!split_ok)
         return cudaErrorInvalidConfiguration;
     const int splits = plan<C, GATED>(p.e.M, p.e.N, p.e.K).splits;
-    cudaLaunchAttribute attrs[2];
+    cudaLaunchAttribute attrs[1];
     cudaLaunchConfig_t cfg = config<C, GATED>(splits, attrs);
-    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(splits, tile_pairs<GATED>(p.e.N), (p.e.M + C::NT - 1) / C::NT);
     cfg.stream = st;
-    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, gemm_act_few_kernel<C, GATED>, p);
 }
 
