@@ -26,7 +26,7 @@
 // an expert's own hidden rows, in chunks of 8 GROUPS.  They enter as three e4m3 parts of one
 // fp32 value under the scale of its 128 (h / s = c0 + c1 / 16 + c2 / 512): 448 is coded to 16,
 // 16 times that remainder to 8, 32 times the next to 8, so the error is below
-// 2^-14 of the largest of the 128, where one e4m3 rounding would cost each value 2^-4.
+// 2^-14 of the largest of the 128 (or of 2^-100), where one e4m3 rounding would cost each value 2^-4.
 #include <algorithm>
 
 #include "activation.cuh"
@@ -668,9 +668,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                     hv = make_float4(act_value<ACT>(zg.x) * zu.x * w, act_value<ACT>(zg.y) * zu.y * w,
                                      act_value<ACT>(zg.z) * zu.z * w, act_value<ACT>(zg.w) * zu.w * w);
                 });
-                const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(max4(hv))));
-                // s times the parts is h to 2^-22, whichever way the two quotients round
-                const float s = m * (1.0f / 448.0f), inv = s > 0.0f ? __fdividef(448.0f, m) : 0.0f;
+                // not below 2^-100, so that a scale's reciprocal stays in range
+                const float m = fmaxf(0x1p-100f, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(max4(hv)))));
+                // s times the parts is h to 2^-21, whichever way the two quotients round; no s comes near
+                // 2^126, from where __fdividef gives 0
+                const float s = m * (1.0f / 448.0f), inv = __fdividef(1.0f, s);
                 float v[4] = {hv.x * inv, hv.y * inv, hv.z * inv, hv.w * inv};
                 uint8_t *o = prm.parts + (int64_t)p * a.I + jb * 128 + lane * 4;
 #pragma unroll

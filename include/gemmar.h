@@ -607,8 +607,9 @@ enum { GEMMAR_SCORE_SOFTMAX = 0, GEMMAR_SCORE_SIGMOID = 1 };
  *   weights  = p of the chosen (without bias), over their sum where renorm, times factor
  * An expert whose p + bias is NaN or -inf is not chosen (a bias of -inf takes one out); where
  * fewer than k are left, id -1 with weight 0 fills up.  Scores are fp32; where two are too
- * near to be told apart in fp32, the order is decided in 64 bits.  Without a bias it is the
- * logits' order, also where the scores saturate.
+ * near to be told apart in fp32, the order is decided in 64 bits (of a softmax with a bias over
+ * the sum of the fp32 exponentials).  Without a bias it is the logits' order, also where the
+ * scores saturate.
  *   x bf16 [T,H] with a row stride; w [E,H] of w_dtype, bias fp32 [E] or NULL; ids int32 [T,k];
  *   weights fp32 [T,k].  H % 8 == 0, H <= 65536, T, E and k within the limits above, k <= E.
  * Scratch: 16 T E floats at most (T E for 8 tokens and fewer).
@@ -625,8 +626,8 @@ int moe_route(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, const void *
  * and w2 (an id outside [0, places) is none): the experts held elsewhere are -1, and y carries
  * a shared expert's rows or zeros.  A token may name an expert twice.  The values between the
  * two products stay fp32 up to the second product, which takes them as three e4m3 parts
- * (their error is below 2^-11 of the largest of their 128); sums are fp32 in a fixed order
- * and out is rounded once.
+ * (their error is below 2^-14 of the largest of their 128, or of 2^-100; where one of the 128 is
+ * infinite, all count as NaN); sums are fp32 in a fixed order and out is rounded once.
  *   xq e4m3 [T,H], xs fp32 [T,H/128]; ids int32 [T,k], weights fp32 [T,k]; place int32 [places]
  *   or NULL; w13 e4m3 [E,2I,H], s13 fp32 [E,2I/128,H/128]; w2 e4m3 [E,H,I], s2 fp32
  *   [E,H/128,I/128]; y bf16 [T,H] (NULL: 0) and out bf16 [T,H] with row strides; y may be out

@@ -300,6 +300,30 @@ def test_large_and_small_hidden_values(g, ctx):
     check_layer(apply(g, ctx, s, ids, weights, y=False), s, ids, weights, y=False)
 
 
+@pytest.mark.parametrize("act", ["relu", "silu"])
+@pytest.mark.parametrize("tiny", [1e-30, 1e-36, 1e-38, 1e-40, 1e-45])
+def test_weights_next_to_nothing(g, ctx, act, tiny):
+    """A softmax gives such weights to the experts behind a clear first: they add next to nothing."""
+    s, rnd, gen = layer(12, 256, 512, 4, 10)
+    ids, weights = picks(12, 3, 4, gen)
+    weights[:, 1] *= tiny
+    weights[6:, 2] = 0
+    check_layer(apply(g, ctx, s, ids, weights, act, y=False), s, ids, weights, act, y=False)
+    ids, weights = ids[:, 1:].contiguous(), weights[:, 1:].contiguous()
+    check_layer(apply(g, ctx, s, ids, weights, act), s, ids, weights, act)
+
+
+def test_hidden_values_near_the_largest(g, ctx):
+    s, rnd, gen = layer(12, 256, 512, 4, 11)
+    ids, weights = picks(12, 1, 4, gen)
+    for t in range(12):
+        e = int(ids[t, 0])
+        h = ff.act_reference(s["q"][t:t + 1], s["sx"][t:t + 1], s["w13"][e], s["s13"][e], "silu", True)[0]
+        weights[t] = 2e38 / float(h.abs().max())
+    s["s2"] = s["s2"] * 1e-30
+    check_layer(apply(g, ctx, s, ids, weights, y=False), s, ids, weights, y=False)
+
+
 def test_the_same_bits_twice(g, ctx):
     for T in (1, 37, 128):
         s, rnd, gen = layer(T, 1024, 512, 16, T)
