@@ -53,7 +53,7 @@ struct gemmar_ctx {
 
 namespace gemmar {
 
-cudaError_t ensure_dynamic_smem(const void *kernel, int bytes, bool all_shared)
+cudaError_t ensure_dynamic_smem(const void *kernel, int bytes)
 {
     static std::mutex mu;
     static std::set<std::pair<const void *, int>> done;
@@ -65,8 +65,6 @@ cudaError_t ensure_dynamic_smem(const void *kernel, int bytes, bool all_shared)
     if (done.count({kernel, dev}))
         return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && all_shared)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess)
         done.insert({kernel, dev});
     return e;

@@ -76,10 +76,8 @@ struct MxParams {
 
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) for the current device, done
 // once per (kernel, device): the attribute belongs to the kernel's instance on
-// each device, so a process that drives several GPUs sets it on each.  all_shared: the kernel
-// leaves an SM split as the tile kernels have it (all but a little of L1 shared memory), so that the
-// one after it need not wait for the SMs to empty and split anew.
-cudaError_t ensure_dynamic_smem(const void *kernel, int bytes, bool all_shared = false);
+// each device, so a process that drives several GPUs sets it on each.
+cudaError_t ensure_dynamic_smem(const void *kernel, int bytes);
 
 // GEMM launchers (bn: 256 or 128 for blockscale; 224 or 128 for mx).
 cudaError_t launch_gemm_blockscale(const BsParams &p, int bn, int grid, cudaStream_t s);

@@ -498,7 +498,7 @@ int tile_parts(const RouteArgs &a, int num_sms)
 template <int TB, int EB, bool BF>
 cudaError_t launch_typed(const RouteArgs &a, float *ws, uint32_t *counter, cudaStream_t st)
 {
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(route_kernel<TB, EB, BF>), kWarps * kMaxExperts * 8, true);
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(route_kernel<TB, EB, BF>), kWarps * kMaxExperts * 8);
     if (e != cudaSuccess)
         return e;
     route_kernel<TB, EB, BF><<<(a.E + EB - 1) / EB, kThreads, a.T * a.E * 8, st>>>(a, ws, counter);
@@ -511,7 +511,7 @@ cudaError_t launch_tiles(const RouteArgs &a, float *ws, int num_sms, cudaStream_
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(route_tile_kernel<BF>), TileSmem<BF>::kBytes);
     if (e != cudaSuccess)
         return e;
-    const cudaError_t c = ensure_dynamic_smem(reinterpret_cast<const void *>(route_choose_kernel), 4 * kMaxExperts * 8, true);
+    const cudaError_t c = ensure_dynamic_smem(reinterpret_cast<const void *>(route_choose_kernel), 4 * kMaxExperts * 8);
     if (c != cudaSuccess)
         return c;
     const int parts = tile_parts(a, num_sms);
