@@ -656,6 +656,17 @@ bool rows_meet(const uint16_t *a, int64_t a_stride, int64_t a_cols, const uint16
     return bytes_meet(a, 2 * a_stride, 2 * a_cols, b, 2 * b_stride, 2 * b_cols, T);
 }
 
+// Do T rows at a share bytes with the one row at b?
+bool rows_meet_one(const void *a, int64_t a_stride, int64_t a_row, int64_t T, const void *b, int64_t b_row)
+{
+    if (a == nullptr || b == nullptr)
+        return false;
+    const int64_t d = (intptr_t)b - (intptr_t)a;
+    if (d >= (T - 1) * a_stride + a_row || -d >= b_row)
+        return false;
+    return d < 0 || T == 1 || d % a_stride < a_row || a_stride - d % a_stride < b_row;
+}
+
 // Do n contiguous bytes at a and m at b?
 bool ranges_meet(const void *a, int64_t n, const void *b, int64_t m) { return bytes_meet(a, n, n, b, m, m, 1); }
 
@@ -854,6 +865,7 @@ GEMMAR_API int gemm_blockscale_act(gemmar_ctx *ctx, const uint8_t *A, const floa
     const int64_t P = gated ? 2 * N : N;
     const int rb = elem_bytes(r_dtype), cb = elem_bytes(c_dtype);
     if ((C != residual && bytes_meet(C, c_stride * cb, N * cb, residual, r_stride * rb, N * rb, M)) ||
+        (r_stride == 0 && C != residual && rows_meet_one(C, c_stride * cb, N * cb, M, residual, N * rb)) ||
         ranges_meet(q, M * N, A, M * K) || ranges_meet(q, M * N, B, P * K) || ranges_meet(z, 2 * M * P, A, M * K) ||
         ranges_meet(z, 2 * M * P, B, P * K) || ranges_meet(q, M * N, z, 2 * M * P) ||
         (c_stride == N && (ranges_meet(C, M * N * cb, A, M * K) || ranges_meet(C, M * N * cb, B, P * K) ||

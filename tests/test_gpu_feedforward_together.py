@@ -252,6 +252,12 @@ def test_refusals(g):
         refused(g.GEMMAR_ERR_ALIGN, act, *ops(), e(M, N + 4, dtype=bf)[:, :N])         # rows off 16 bytes
         wide = e(M + 1, N)
         refused(g.GEMMAR_ERR_ARG, act, *ops(), wide[1:], residual=wide[:M])            # a row below what it reads
+        below = e(M + 1, 2 * N)
+        for at, row in ((0, 2), (0, M - 1), (8, 1)):                                   # one row for all, among C's
+            refused(g.GEMMAR_ERR_ARG, act, *ops(), below[:M, :N], residual=below[row:row + 1, at:at + N].expand(M, N))
+        for at, row in ((N, 2), (0, M)):                                               # beside and below them is fine
+            act(ctx, *ops(), below[:M, :N], residual=below[row:row + 1, at:at + N].expand(M, N))
+        act(ctx, *ops(), below[1:, N:], residual=below[:1, N:].expand(M, N))           # and above
         o = ops()
         refused(g.GEMMAR_ERR_ARG, act, *o, C, q=o[0], scales=s)                        # codes over A
         refused(g.GEMMAR_ERR_ARG, act, *o, C, q=o[2][:M], scales=s)                    # over B
