@@ -140,6 +140,29 @@ __device__ __noinline__ int decide64(const RouteArgs &a, int t, const float *val
     return lane < k ? mine_e : -1;
 }
 
+// Weights over their sum where the scores of all chosen are too small for fp32 (a bias that takes
+// out the experts before them; a sigmoid of logits far below 0): both scores are then e^l but for a factor
+// that the sum takes out.  Lane j < chosen has the j-th expert and gets its weight.
+__device__ __noinline__ float tiny_weights(const RouteArgs &a, int t, int mine, int chosen)
+{
+    const int lane = threadIdx.x & 31;
+    double logit = -INFINITY;
+    for (int j = 0; j < chosen; ++j) {
+        const double x = logit64(a, t, __shfl_sync(0xffffffffu, mine, j));
+        logit = lane == j ? x : logit;
+    }
+    double top = logit;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        top = fmax(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const double w = logit > -INFINITY ? exp(logit - top) : 0.0;
+    double all = w;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        all += __shfl_xor_sync(0xffffffffu, all, d);
+    return all > 0.0 ? (float)(w / all) : 0.0f;
+}
+
 // One warp chooses token t's experts from its logits in global memory, which other CTAs wrote, in
 // `parts` to be added.  score: [2 E] in shared memory, the warp's own.  PER: experts of a lane
 // (E <= 32 PER), lane + 32 i.
@@ -264,7 +287,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *l
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
             all += __shfl_xor_sync(0xffffffffu, all, d);
-        w = all > 0.0f ? w / all : w;
+        w = all < 0x1p-100f && chosen > 0 ? tiny_weights(a, t, mine, chosen) : w / all;
     }
     if (lane < a.k) {
         a.ids[(int64_t)t * a.k + lane] = mine;

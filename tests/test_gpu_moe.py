@@ -125,6 +125,20 @@ def test_route_saturated_scores(g, ctx, score, T):
 
 
 @pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("T", [1, 40])
+def test_route_chosen_scores_too_small_for_fp32(g, ctx, score, T):
+    """The bias takes out the experts that have all of the softmax, or all logits are far below 0."""
+    x, w, bias = router(T, 1024, 64, 17)
+    x[:, 0], w[:, 0] = 1, -150
+    w[:32, 0] = 50
+    bias[:] = 0
+    bias[:32] = -float("inf")
+    for kw in (dict(bias=bias, score=score), dict(bias=bias, score=score, factor=2.5, renorm=False)):
+        check_route(route(g, ctx, x, w, 6, **kw), route_reference(x, w, 6, **kw))
+    check_route(route(g, ctx, x, w[32:], 6, score=score), route_reference(x, w[32:], 6, score=score))
+
+
+@pytest.mark.parametrize("score", [0, 1])
 def test_route_equal_scores_take_the_lowest(g, ctx, score):
     x, w, _ = router(20, 256, 48, 8)
     x[4] = 0                                   # a padded row: every logit is 0
