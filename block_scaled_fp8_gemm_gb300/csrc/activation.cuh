@@ -37,6 +37,28 @@ constexpr float kLowest = -3.402823466e38f;
 // The argument of the tanh form's sigmoid ((1 + tanh u) / 2 = sigmoid(2 u))
 __device__ __forceinline__ float tanh_arg(float z) { return 2.0f * kSqrt2OverPi * z * fmaf(kGeluCubic * z, z, 1.0f); }
 
+// Phi(z), and e = exp(-z^2 / 2).  Phi(-a) = e t P(t) for a >= 0 with t = 1 / (1 + 0.3 a), in which the
+// rest is smooth down to t = 0, and P of degree 9, fitted here to a relative 4e-9 for a up to 15 (weighted
+// least squares in 40 digits, reweighted towards equal errors).  The whole is off by (3 + z^2 / 2) 2^-23 of
+// its value (the exponential's argument is rounded twice), in either tail.
+__device__ __forceinline__ float normal_cdf(float z, float &e)
+{
+    const float a = fabsf(z);
+    e = __expf(-0.5f * a * a);
+    const float t = __fdividef(1.0f, fmaf(0.3f, a, 1.0f));   // 0 for the largest a, as is e
+    float p = fmaf(-2.062856220e-02f, t, 1.124642864e-01f);
+    p = fmaf(p, t, -2.282836586e-01f);
+    p = fmaf(p, t, 1.918818653e-01f);
+    p = fmaf(p, t, -7.950805128e-02f);
+    p = fmaf(p, t, 9.620437026e-02f);
+    p = fmaf(p, t, 7.837239653e-02f);
+    p = fmaf(p, t, 1.102393121e-01f);
+    p = fmaf(p, t, 1.195713207e-01f);
+    p = fmaf(p, t, 1.196867153e-01f);
+    const float tail = p * t * e;
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float z)
 {
@@ -46,8 +68,10 @@ __device__ __forceinline__ float act_value(float z)
         return max_nan(z, kLowest) * sigmoid(z);
     if constexpr (ACT == ACT_GELU_TANH)
         return max_nan(z, kLowest) * sigmoid(tanh_arg(z));
-    if constexpr (ACT == ACT_GELU)
-        return max_nan(z, kLowest) * (0.5f * erfcf(-0.70710678f * z));
+    if constexpr (ACT == ACT_GELU) {
+        float e;
+        return max_nan(z, kLowest) * normal_cdf(z, e);
+    }
     return z;
 }
 
@@ -71,8 +95,8 @@ __device__ __forceinline__ void act_slope(float z, float &value, float &slope)
             s = sigmoid(tanh_arg(z));
             d = fmaf(-s, s, s) * (2.0f * kSqrt2OverPi * fmaf(3.0f * kGeluCubic * c, c, 1.0f));
         } else {
-            s = 0.5f * erfcf(-0.70710678f * z);
-            d = 0.3989422804f * __expf(-0.5f * c * c);
+            s = normal_cdf(z, d);
+            d *= 0.3989422804f;
         }
         value = max_nan(z, kLowest) * s;
         slope = fmaf(c, d, s);

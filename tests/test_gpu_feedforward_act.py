@@ -163,3 +163,18 @@ def test_the_same_bits_twice(g, ctx):
         res = rnd(M, 512)
         a, b = (run(g, ctx, ops, 512, "silu", True, ("C32", "q", "z"), residual=res) for _ in range(2))
         assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+@pytest.mark.parametrize("M", [1, 140])
+@pytest.mark.parametrize("act", ff.ACTS)
+def test_values_over_the_whole_range(g, ctx, act, M):
+    """Without a product z is the bias, exactly: the activation's own error from one tail to the other."""
+    N = 8192
+    ops, rnd = operands(M, N, 128, 1)
+    ops[0].zero_()
+    z = torch.linspace(-12, 12, N, device="cuda")
+    ref, exact = ff.value(act, z.double()), torch.zeros(N, device="cuda", dtype=torch.float64)
+    # act is z times a factor in [0, 1], and a factor below 2^-126 may be 0 (the sigmoid's divisor is past
+    # 2^126, from where the fast division gives 0): off by at most 2^-126 |z|
+    bound = ff.value_error(act, z.double(), exact) + 2.0 ** -24 * ref.abs() + 2.0 ** -126 * z.double().abs().clamp(min=1)
+    ff.within(run(g, ctx, ops, N, act, False, bias=z)["C"], ref.expand(M, N), bound)
