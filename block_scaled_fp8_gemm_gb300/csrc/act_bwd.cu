@@ -68,9 +68,10 @@ inline Share share_out(int64_t M, int N, int num_sms)
 {
     Share s;
     s.strips = (N / 128 + kGroups - 1) / kGroups;
-    // one wave of eight CTAs per SM, which its registers hold, and at least 16 rows to a CTA (4096 x
-    // 2048 gated: 17.4 us; four CTAs of twice the rows at a time 20.9, two waves of those 19.8)
-    const int64_t want = std::max<int64_t>(1, (int64_t)num_sms * 8 / s.strips);
+    // one wave of seven CTAs per SM, which its registers hold, and at least 16 rows to a CTA (gated, N =
+    // 2048: 4096 rows, where the 16 count, 17.4 us, four CTAs of twice the rows at a time 20.9, two waves of
+    // those 19.8; 16384 rows 67 us, with eight CTAs, the eighth in a wave of its own, 83)
+    const int64_t want = std::max<int64_t>(1, (int64_t)num_sms * 7 / s.strips);
     s.rows = (M + want - 1) / want;
     s.rows = s.rows < 16 ? 16 : (s.rows + kRows - 1) / kRows * kRows;
     s.shares = (int)((M + s.rows - 1) / s.rows);
@@ -78,7 +79,7 @@ inline Share share_out(int64_t M, int N, int num_sms)
 }
 
 template <int ACT, bool GATED, bool BF>
-__global__ void __launch_bounds__(kThreads) act_bwd_kernel(const ActBwdArgs a, const Share sh, float *ws)
+__global__ void __launch_bounds__(kThreads, 7) act_bwd_kernel(const ActBwdArgs a, const Share sh, float *ws)
 {
     const int lane = threadIdx.x % kLanes, group = (threadIdx.x / kLanes) % kGroups, r0 = threadIdx.x / kRowThreads;
     const int g = blockIdx.x * kGroups + group;
