@@ -43,13 +43,11 @@ constexpr int kNumBars = 2 * kStages + kSteps + 5;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
 constexpr int kSmemBytes = kOffMisc + 8 + 4 * kSteps + 8 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-// setmaxnreg: warps 0-3, promotion, finish, of 128 a thread.  An ungated finish has the next block of
-// sums under way.
-constexpr int kRegsLow = 40;
-template <bool GATED> constexpr int kRegsPromote = GATED ? 184 : 176;
-template <bool GATED> constexpr int kRegsFinish = GATED ? 104 : 120;
-constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsPromote<true> + 128 * kRegsFinish<true>;
-static_assert(kRegsNeeded <= 65536 && 128 * kRegsLow + 256 * kRegsPromote<false> + 128 * kRegsFinish<false> == kRegsNeeded, "register split");
+// setmaxnreg: warps 0-3, promotion, finish, of 128 a thread
+constexpr int kRegsLow = 40, kRegsPromote = 176, kRegsFinish = 120;
+constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsPromote + 128 * kRegsFinish;
+static_assert(kRegsNeeded <= 65536, "register split");
+static_assert(kRegsPromote >= 128 && kRegsFinish <= 128, "raised and lowered from 128");
 constexpr int kGroupM = 16;      // row tiles that share their columns of B while they are in L2
 struct Tile {
     int m0, n0;
@@ -263,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
             wait_teardown(final_bar, prm.status, prm.timeout_ns);
         }
     } else if (warp < 12) {
-        setmaxnreg_inc<kRegsPromote<GATED>>();
+        setmaxnreg_inc<kRegsPromote>();
         // ---------------------------------------------------- promotion
         const int q = warp & 3, h = (warp - 4) >> 2;   // lane quarter, half of the accumulator's columns
         const int row = q * 32 + lane;
@@ -335,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
             }
         }
     } else {
-        setmaxnreg_dec<kRegsFinish<GATED>>();
+        setmaxnreg_dec<kRegsFinish>();
         // ---------------------------------------------------- finish
         const int q = warp & 3;
         const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
