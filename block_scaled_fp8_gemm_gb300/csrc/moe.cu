@@ -27,6 +27,10 @@
 // fp32 value under the scale of its 128 (h / s = c0 + c1 / 16 + c2 / 512): 448 is coded to 16,
 // 16 times that remainder to 8, 32 times the next to 8, so the error is below
 // 2^-14 of the largest of the 128 (or of 2^-100), where one e4m3 rounding would cost each value 2^-4.
+//
+// Experts of 7168 x 2048, bytes of the weights that are needed: one token of 8 experts 70.5 us (5.0
+// TB/s; of 16 123 us, so what streams does at 6.7), 64 tokens that meet 64 experts 454 us (6.2), 96 that
+// meet 128 879 us (6.4).  Up to 18 us are launch, plan, hidden values and rows of out.
 #include <algorithm>
 
 #include "activation.cuh"
