@@ -8,7 +8,7 @@
 // 128 of K, so each of a tile's 128 x 256 sums is read from TMEM and multiplied-added in fp32
 // once per K-block.  A K-block takes about 900 cycles, 512 of MMA, whose accumulators share TMEM's
 // bandwidth with those reads (755 in the same pipeline without them): 16384 x 7168 x 2048 to
-// bf16 in 218 us, 0.58 of the MMA's rate; with bias and residual 287 us; gated 7168 -> 2 x 2048 to
+// bf16 in 218 us, 0.58 of the MMA's rate; with bias and residual 248 us; gated 7168 -> 2 x 2048 to
 // codes and z, 4096 rows, 113 us.  One persistent CTA per SM, 16 warps:
 //   warp 0      TMA producer: A tile 128x128 and B rows 2 x 128 per 128-K stage
 //   warp 1      MMA issuer, 128 x 256 x 32 each into one of two TMEM buffers (two MMAs of 128
@@ -19,9 +19,8 @@
 //               takes for each the buffer that is free and leaves on record which
 //   warps 12-15 finish: one per TMEM lane quarter, a thread per row.  They take a parked tile 32
 //               columns at a time through bias, activation, gate, residual and the stores, while
-//               the next tile is promoted.  A thread reads and writes its own row in whole
-//               32-byte sectors, with no staging and nothing to wait for but the residual, which
-//               it asks for a block of columns, and into L2 a tile, ahead
+//               the next tile is promoted.  A thread writes its own row in whole 32-byte sectors,
+//               with no staging; the residual, which they would wait for, is asked for ahead
 #include <algorithm>
 
 #include "activation.cuh"
@@ -34,18 +33,26 @@ using namespace ptx;
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kStages = 4;
 constexpr int kABytes = 128 * 128;
 constexpr int kBBytes = 256 * 128;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kSteps = 4;        // K-steps whose buffer is on record: more than can be under way
-constexpr int kOffB = kStages * kABytes;
-constexpr int kOffBias = kOffB + kStages * kBBytes;      // [4 finish warps][256] of the tile's columns
-constexpr int kOffBar = kOffBias + 4 * 1024;
-constexpr int kNumBars = 2 * kStages + kSteps + 5;
-constexpr int kOffMisc = kOffBar + kNumBars * 8;
-constexpr int kSmemBytes = kOffMisc + 8 + 4 * kSteps + 8 + 1024;
-static_assert(kSmemBytes <= 232448, "shared memory budget");
+constexpr int kResBytes = 16 * 1024;
+// An ungated tile takes K in three stages as fast as in four, and has the room for its residual's rows on
+// their way (16384 x 7168 x 2048 with a bf16 residual 240 us, with 64 columns of it in registers 276; fp32
+// 302 and 381).  A gated one, 3% slower with three, keeps 64 columns in registers.
+template <bool GATED>
+struct Smem {
+    static constexpr int kStages = GATED ? 4 : 3;
+    static constexpr int kOffB = kStages * kABytes;
+    static constexpr int kOffBias = kOffB + kStages * kBBytes;   // [4 finish warps][256] of the tile's columns
+    static constexpr int kOffRes = kOffBias + 4 * 1024;          // [4 finish warps] rows of the residual
+    static constexpr int kOffBar = kOffRes + (GATED ? 0 : 4 * kResBytes);
+    static constexpr int kNumBars = 2 * kStages + kSteps + 5;
+    static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+    static constexpr int kBytes = kOffMisc + 8 + 4 * kSteps + 8 + 1024;
+    static_assert(kBytes <= 232448, "shared memory budget");
+};
 // setmaxnreg: warps 0-3, promotion, finish, of 128 a thread
 constexpr int kRegsLow = 40, kRegsPromote = 176, kRegsFinish = 120;
 constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsPromote + 128 * kRegsFinish;
@@ -140,16 +147,18 @@ template <bool GATED>
 __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_constant__ ActParams prm)
 {
     constexpr int BN = GATED ? 128 : 256;   // output columns of a tile
+    using S = Smem<GATED>;
+    constexpr int kStages = S::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align1024(smem_raw);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::kOffBar);
     uint64_t *empty = full + kStages;
     uint64_t *tfull = empty + kStages;   // [kSteps], by K-step
     uint64_t *tempty = tfull + kSteps;   // [2], by buffer
     uint64_t *park_full = tempty + 2;    // [2], by tile: its sums are in TMEM
     uint64_t *final_bar = park_full + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + S::kOffMisc + 4);
     volatile int *step_buf = abort_flag + 1;          // [kSteps] buffer of a K-step
     volatile int *park_buf = step_buf + kSteps;       // [2] buffer of a tile's park
 
@@ -199,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                         break;
                     }
                     mbar_arrive_expect_tx(full + stage, kStageBytes);
-                    uint8_t *b = smem + kOffB + stage * kBBytes;
+                    uint8_t *b = smem + S::kOffB + stage * kBBytes;
                     tma_load_2d(smem + stage * kABytes, &prm.tmA, full + stage, kb * 128, c.m0);
                     tma_load_2d(b, &prm.tmB, full + stage, kb * 128, c.n0);
                     tma_load_2d(b + 128 * 128, &prm.tmB, full + stage, kb * 128, nb);   // zeros past the last row
@@ -246,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                     use1 += buf ? 1u : 0u;
                     tc_fence_after();
                     const uint64_t ad = desc_kmajor_sw128(smem_u32(smem + stage * kABytes));
-                    const uint64_t bd = desc_kmajor_sw128(smem_u32(smem + kOffB + stage * kBBytes));
+                    const uint64_t bd = desc_kmajor_sw128(smem_u32(smem + S::kOffB + stage * kBBytes));
 #pragma unroll
                     for (int k = 0; k < 4; ++k)   // 4 x 32 of K = one 128-byte swizzle row
                         mma_f8(tmem_base + buf * 256, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
@@ -344,14 +353,15 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
         const int r_bytes = e.r_bf16 ? 2 : 4, c_bytes = e.c_bf16 ? 2 : 4;
         const bool r_whole = whole32(e.res, e.rs * r_bytes), c_whole = whole32(e.C, e.cs * c_bytes);
         const bool z_whole = whole32(e.z, 0), q_whole = whole32(e.q, 0);   // N is a multiple of 128
-        const uint32_t bias = smem_u32(smem + kOffBias + q * 1024);   // the warp's own copy
+        const uint32_t bias = smem_u32(smem + S::kOffBias + q * 1024);   // the warp's own copy
+        const uint32_t res_ring = smem_u32(smem + S::kOffRes + q * kResBytes);   // ungated
         uint32_t parked = 0;
         for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++parked) {
             const Tile c = decode(t, mt, nt, BN);
             const int64_t m = c.m0 + q * 32 + lane;
             const bool inside = m < e.M;
             const int cols = min(BN, e.N - c.n0);   // a multiple of 128
-            // The residual's columns, 64 ahead of their use as bf16 and 32 as fp32: blocks of 32 go to
+            // Gated: the residual's columns, 64 ahead of their use as bf16 and 32 as fp32: blocks of 32 go to
             // the two halves of these registers in turn, or fill both.
             const char *res = static_cast<const char *>(e.res) + (m * e.rs + c.n0) * r_bytes;
             const bool has_res = e.res != nullptr && inside;
@@ -368,9 +378,29 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                         load32(res + col * 4 + 32 * i, r_whole, ahead + 8 * i);
                 }
             };
-            fetch_residual(0, 0);
-            if (e.r_bf16)
-                fetch_residual(32, 1);
+            // Ungated: 64 columns at a time, in shared memory: a bf16 tile's four such blocks, or two of an fp32
+            // one's.  Unit u of row r lies at u ^ (r % 8), so that the rows that eight lanes read lie in different
+            // banks.
+            const int block_bytes = 32 * 64 * r_bytes, blocks = kResBytes / block_bytes, units = 4 * r_bytes;
+            auto stage_residual = [&](int col) {
+                if (e.res != nullptr && col < cols) {
+                    const uint32_t to = res_ring + col / 64 % blocks * block_bytes;
+                    const int u = lane % units;
+                    const char *from = static_cast<const char *>(e.res) + ((m - lane) * e.rs + c.n0 + col) * r_bytes + u * 16;
+                    for (int row = lane / units; row < 32; row += 32 / units)
+                        if (m - lane + row < e.M)
+                            cp_async_cg16(to + row * 64 * r_bytes + (u ^ row % 8) * 16, from + row * e.rs * r_bytes);
+                }
+                cp_async_commit();
+            };
+            if constexpr (GATED) {
+                fetch_residual(0, 0);
+                if (e.r_bf16)
+                    fetch_residual(32, 1);
+            } else {
+                for (int i = 0; i < blocks; ++i)
+                    stage_residual(i * 64);
+            }
             if (e.bias != nullptr) {
                 // 256 sums' bias: a tile's columns, or 128 of both halves
                 __syncwarp();   // every lane is through with the last tile's
@@ -384,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                 }
                 __syncwarp();
             }
-            if (e.res != nullptr) {
+            if (GATED && e.res != nullptr) {
                 // the next tile's rows of it into L2
                 const Tile d = decode(min(t + (int)gridDim.x, tiles - 1), mt, nt, BN);
                 const int64_t row = d.m0 + q * 32 + lane;
@@ -429,7 +459,32 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                             v[i + j] *= u[j];
                     }
                 }
-                if (has_res) {
+                if (!GATED && e.res != nullptr) {
+                    const uint32_t row = res_ring + col / 64 % blocks * block_bytes + lane * 64 * r_bytes;
+                    const int u = half * 2 * r_bytes, turn = lane % 8;
+                    if (e.r_bf16) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 a = ld_shared_v4(row + ((u + i) ^ turn) * 16);
+                            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                v[8 * i + 2 * j] += bf16_lo(w[j]);
+                                v[8 * i + 2 * j + 1] += bf16_hi(w[j]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint4 a = ld_shared_v4(row + ((u + i) ^ turn) * 16);
+                            v[4 * i] += __uint_as_float(a.x);
+                            v[4 * i + 1] += __uint_as_float(a.y);
+                            v[4 * i + 2] += __uint_as_float(a.z);
+                            v[4 * i + 3] += __uint_as_float(a.w);
+                        }
+                    }
+                }
+                if (GATED && has_res) {
                     if (e.r_bf16) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
@@ -461,11 +516,22 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                 tmem_wait_ld(bits(v));
                 if (!GATED)   // under way while the first block is taken through
                     tmem_ld_x32(park + col + 32, bits(w));
+                if (!GATED && e.res != nullptr) {
+                    if (e.r_bf16)
+                        cp_async_wait<3>();   // all but what has been asked for since
+                    else
+                        cp_async_wait<1>();
+                    __syncwarp();
+                }
                 block(v, col, 0);
                 if (GATED)
                     tmem_ld_x32(park + col + 32, bits(w));
                 tmem_wait_ld(bits(w));
                 block(w, col + 32, 1);
+                if (!GATED) {
+                    __syncwarp();   // the residual's block is read
+                    stage_residual(col + 64 * blocks);
+                }
                 if (e.q != nullptr && col % 128 == 64) {
                     tmem_wait_st();
                     const float scale = __fdiv_rn(top, 448.0f);
@@ -492,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                 mbar_arrive(tempty + buf);
             }
         }
+        cp_async_wait<0>();
     }
 
     __syncwarp();
@@ -521,22 +588,21 @@ int64_t gemm_act_tiles_ns(int M, int N, int K, bool gated, int num_sms)
     return (tiles + num_sms - 1) / num_sms * (450 * (K / 128) + 5000) + 3000;
 }
 
-cudaError_t launch_gemm_act(const ActParams &p, int num_sms, cudaStream_t st)
+template <bool GATED>
+static cudaError_t launch_typed(const ActParams &p, int num_sms, cudaStream_t st)
 {
-    const bool gated = p.e.gated;
-    const void *kernel = gated ? reinterpret_cast<const void *>(gemm_act_kernel<true>)
-                               : reinterpret_cast<const void *>(gemm_act_kernel<false>);
-    const cudaError_t e = ensure_dynamic_smem(kernel, kSmemBytes);
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(gemm_act_kernel<GATED>), Smem<GATED>::kBytes);
     if (e != cudaSuccess)
         return e;
-    const int bn = gated ? 128 : 256;
+    const int bn = GATED ? 128 : 256;
     const int64_t tiles = (int64_t)((p.e.M + 127) / 128) * ((p.e.N + bn - 1) / bn);
-    const int grid = (int)std::min<int64_t>(tiles, num_sms);
-    if (gated)
-        gemm_act_kernel<true><<<grid, kThreads, kSmemBytes, st>>>(p);
-    else
-        gemm_act_kernel<false><<<grid, kThreads, kSmemBytes, st>>>(p);
+    gemm_act_kernel<GATED><<<(int)std::min<int64_t>(tiles, num_sms), kThreads, Smem<GATED>::kBytes, st>>>(p);
     return cudaGetLastError();
+}
+
+cudaError_t launch_gemm_act(const ActParams &p, int num_sms, cudaStream_t st)
+{
+    return p.e.gated ? launch_typed<true>(p, num_sms, st) : launch_typed<false>(p, num_sms, st);
 }
 
 }  // namespace gemmar
