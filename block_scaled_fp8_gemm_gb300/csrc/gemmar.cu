@@ -837,6 +837,9 @@ bool known_act(int act) { return act >= GEMMAR_ACT_NONE && act <= GEMMAR_ACT_GEL
 
 int elem_bytes(int dtype) { return dtype == GEMMAR_DTYPE_BF16 ? 2 : 4; }
 
+// of a contiguous matrix, or of one row that stands for all (stride 0)
+int64_t row_bytes(int64_t stride, int64_t M, int64_t N, int64_t elem) { return (stride == 0 ? 1 : M) * N * elem; }
+
 }  // namespace
 
 GEMMAR_API int gemm_blockscale_act(gemmar_ctx *ctx, const uint8_t *A, const float *sa, const uint8_t *B, const float *sb,
@@ -870,7 +873,8 @@ GEMMAR_API int gemm_blockscale_act(gemmar_ctx *ctx, const uint8_t *A, const floa
         ranges_meet(z, 2 * M * P, B, P * K) || ranges_meet(q, M * N, z, 2 * M * P) ||
         (c_stride == N && (ranges_meet(C, M * N * cb, A, M * K) || ranges_meet(C, M * N * cb, B, P * K) ||
                            ranges_meet(C, M * N * cb, q, M * N) || ranges_meet(C, M * N * cb, z, 2 * M * P))) ||
-        (residual && r_stride == N && (ranges_meet(residual, M * N * rb, q, M * N) || ranges_meet(residual, M * N * rb, z, 2 * M * P))))
+        (residual && (r_stride == N || r_stride == 0) &&
+         (ranges_meet(residual, row_bytes(r_stride, M, N, rb), q, M * N) || ranges_meet(residual, row_bytes(r_stride, M, N, rb), z, 2 * M * P))))
         return GEMMAR_ERR_ARG;
     if (!load_encode())
         return GEMMAR_ERR_CUDA;
@@ -913,7 +917,9 @@ GEMMAR_API int gemm_blockscale_act_bwd(gemmar_ctx *ctx, const void *dout, int d_
         return GEMMAR_ERR_ALIGN;
     const int64_t P = gated ? 2 * N : N, db = elem_bytes(d_dtype);
     if ((dz && dz != z && ranges_meet(dz, 2 * M * P, z, 2 * M * P)) ||
-        (d_stride == N && ((dz && dz != dout && ranges_meet(dz, 2 * M * P, dout, M * N * db)) || ranges_meet(q, M * P, dout, M * N * db))) ||
+        ((d_stride == N || d_stride == 0) &&
+         ((dz && dz != dout && ranges_meet(dz, 2 * M * P, dout, row_bytes(d_stride, M, N, db))) ||
+          ranges_meet(q, M * P, dout, row_bytes(d_stride, M, N, db)))) ||
         ranges_meet(q, M * P, z, 2 * M * P) || ranges_meet(q, M * P, dz, 2 * M * P))
         return GEMMAR_ERR_ARG;
     if (dbias && act_bwd_ws_floats(M, (int)N, gated, ctx->num_sms) > ctx->W_floats)
@@ -967,6 +973,7 @@ GEMMAR_API int moe_apply(gemmar_ctx *ctx, const uint8_t *xq, const float *xs, co
         !aligned16(w13) || !aligned16(s13) || !aligned16(w2) || !aligned16(s2))
         return GEMMAR_ERR_ALIGN;
     if ((y != out && rows_meet(out, out_stride, H, y, y_stride, H, T)) ||
+        (y != out && y_stride == 0 && rows_meet_one(out, 2 * out_stride, 2 * H, T, y, 2 * H)) ||
         (out_stride == H && (ranges_meet(out, 2 * T * H, xq, T * H) || ranges_meet(out, 2 * T * H, ids, 4 * T * k))))
         return GEMMAR_ERR_ARG;
     const MoeArgs a{xq, xs, ids, place, (int)(place ? places : 0), weights, w13, w2, s13, s2, (int)T, (int)H, (int)I, E, k,

@@ -269,6 +269,9 @@ def test_refusals(g):
         zz = e(M + 1, N, dtype=bf)
         refused(g.GEMMAR_ERR_ARG, bwd, d, zz[:M], zz[1:])                              # dz a row below z
         refused(g.GEMMAR_ERR_ARG, bwd, zz[:M], z, zz[1:])
+        refused(g.GEMMAR_ERR_ARG, bwd, zz[2:3].expand(M, N), z, zz[1:])                # one row for all, among dz's
+        bwd(ctx, zz[:1].expand(M, N), z, zz[1:])                                       # above them is fine
+        refused(g.GEMMAR_ERR_ARG, act, *ops(), C, z=zz[:M], residual=zz[2:3].expand(M, N))
         H, I, E, T, k = 256, 128, 4, 3, 2
         r = lambda T=T, k=k, E=E, H=H: (e(T, H, dtype=bf), e(E, H), e(T, k, dtype=i32), e(T, k))
         refused(g.GEMMAR_ERR_ARG, g.moe_route, *r(k=5))                                # more than there are
@@ -285,6 +288,8 @@ def test_refusals(g):
         refused(g.GEMMAR_ERR_ARG, g.moe_apply, *m(), e(T, H, dtype=bf), act=9)
         rows = e(T + 1, H, dtype=bf)
         refused(g.GEMMAR_ERR_ARG, g.moe_apply, *m(), rows[1:], y=rows[:T])
+        refused(g.GEMMAR_ERR_ARG, g.moe_apply, *m(), rows[1:], y=rows[2:3].expand(T, H))
+        g.moe_apply(ctx, *m(), rows[1:], y=rows[:1].expand(T, H))
         refused(g.GEMMAR_ERR_WORKSPACE, g.moe_apply, *m(T=100, k=4), e(100, H, dtype=bf))   # a context of 128 x 256
         torch.cuda.synchronize()
         assert g.gemmar_status(ctx)[0] == 0
