@@ -12,7 +12,8 @@
 //
 // The order of two experts whose scores agree to fp32's rounding would depend on how the
 // sums are split.  Such tokens are decided in 64 bits: the logits in question are summed
-// again with what their roundings lost (a few microseconds, for about one token in a thousand).
+// again with what their roundings lost (20 us for a pair at h = 7168, for about one token in two
+// thousand).
 // Without a bias the order is the logits' own, which neither saturates nor underflows.
 #include <algorithm>
 
@@ -111,7 +112,8 @@ struct Order64 {
 // The first k in double of the experts whose fp32 order value is at least `least`, for the rare
 // token where fp32 cannot tell: lane j gets the j-th.  value: the fp32 order values, in shared
 // memory; zero: every logit of the token is exactly 0.
-__device__ __noinline__ int decide64(const RouteArgs &a, int t, const float *value, float least, int k, Order64 o, bool zero)
+// Only experts with another one twice `tol` away or nearer need it: between the others fp32 can tell.
+__device__ __noinline__ int decide64(const RouteArgs &a, int t, const float *value, float least, float tol, int k, Order64 o, bool zero)
 {
     const int lane = threadIdx.x & 31;
     double mine = -INFINITY;   // lane j: the j-th best so far, and whose
@@ -122,10 +124,16 @@ __device__ __noinline__ int decide64(const RouteArgs &a, int t, const float *val
         while (todo) {
             const int who = __ffs(todo) - 1, e = e0 + who;
             todo &= todo - 1;
-            const double x = zero ? 0.0 : logit64(a, t, e);
-            // an infinite logit's fp32 value is exact
-            const double d = x > -INFINITY && x < INFINITY ? o.of(x, o.biased ? (double)__ldg(a.bias + e) : 0.0)
-                                                           : (double)__shfl_sync(0xffffffffu, f, who);
+            const float mine32 = __shfl_sync(0xffffffffu, f, who), near = 2.0f * (tol + (o.biased ? 0x1p-21f * fabsf(mine32) : 0.0f));
+            bool alone = true;
+            for (int i = lane; i < a.E; i += 32)
+                alone = alone && (i == e || !(fabsf(value[i] - mine32) <= near));
+            double d = mine32;
+            if (!__all_sync(0xffffffffu, alone)) {
+                const double x = zero ? 0.0 : logit64(a, t, e);
+                if (x > -INFINITY && x < INFINITY)   // an infinite logit's fp32 value is exact
+                    d = o.of(x, o.biased ? (double)__ldg(a.bias + e) : 0.0);
+            }
             // its place behind the ones that are not smaller (equal ones have lower numbers)
             const int place = __popc(__ballot_sync(0xffffffffu, lane < count && mine >= d));
             const double up = __shfl_up_sync(0xffffffffu, mine, 1);
@@ -280,7 +288,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *l
                 sum64 += __shfl_xor_sync(0xffffffffu, sum64, d);
         }
         const float near = 2.0f * (tol + (biased ? 0x1p-21f * fabsf(cut) : 0.0f));
-        mine = decide64(a, t, order, near > 0.0f ? cut - near : cut, chosen, Order64{soft, biased, (double)top, sum64}, big == 0.0f);
+        mine = decide64(a, t, order, near > 0.0f ? cut - near : cut, tol, chosen, Order64{soft, biased, (double)top, sum64}, big == 0.0f);
     }
     float w = mine >= 0 ? score[mine] * scale : 0.0f, all = w;
     if (a.renorm) {

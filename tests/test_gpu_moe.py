@@ -102,6 +102,21 @@ def test_route_scores_that_fp32_cannot_tell_apart(g, ctx, score, biased):
     check_route(route(g, ctx, x, w, 8, bias=bias, score=score), route_reference(x, w, 8, bias=bias, score=score))
 
 
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_near_pairs_among_distant_ones(g, ctx, biased):
+    """Some of a token's choices are told apart in fp32 and some are not, in one order."""
+    T, H, E = 40, 7168, 256
+    x, w, bias = router(T, H, E, 18, torch.float32)
+    bias = (bias * 64).round() if biased else None
+    gen = torch.Generator("cuda").manual_seed(19)
+    pick = torch.randperm(E, generator=gen, device="cuda")
+    w[pick[:60]] = w[pick[60:120]]
+    w[pick[:60], 300] = torch.nextafter(w[pick[:60], 300], w[pick[:60], 300] - 1)
+    if biased:
+        bias[pick[:60]] = bias[pick[60:120]]
+    check_route(route(g, ctx, x, w, 16, bias=bias, score=1), route_reference(x, w, 16, bias=bias, score=1))
+
+
 @pytest.mark.parametrize("score", [0, 1])
 @pytest.mark.parametrize("T", [1, 40])
 def test_route_saturated_scores(g, ctx, score, T):
