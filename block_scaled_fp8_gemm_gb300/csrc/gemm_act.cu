@@ -8,7 +8,7 @@
 // 128 of K, so each of a tile's 128 x 256 sums is read from TMEM and multiplied-added in fp32
 // once per K-block.  A K-block takes about 900 cycles, 512 of MMA, whose accumulators share TMEM's
 // bandwidth with those reads (755 in the same pipeline without them): 16384 x 7168 x 2048 to
-// bf16 in 218 us, 0.58 of the MMA's rate; with bias and residual 248 us; gated 7168 -> 2 x 2048 to
+// bf16 in 226 us, 0.56 of the MMA's rate; with bias and residual 254 us; gated 7168 -> 2 x 2048 to
 // codes and z, 4096 rows, 113 us.  One persistent CTA per SM, 16 warps:
 //   warp 0      TMA producer: A tile 128x128 and B rows 2 x 128 per 128-K stage
 //   warp 1      MMA issuer, 128 x 256 x 32 each into one of two TMEM buffers (two MMAs of 128
@@ -143,7 +143,9 @@ __device__ __forceinline__ bool whole32(const void *p, int64_t row_bytes)
     return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)row_bytes) & 31) == 0;
 }
 
-template <bool GATED>
+// GELU: an ungated tile's activation is gelu, whose code is the longest: two copies of it, as the others have,
+// and instructions that wait for one another cost 8192 x 1920 x 1152 70 us, this form 49; the others lose 5% to it.
+template <bool GATED, bool GELU>
 __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_constant__ ActParams prm)
 {
     constexpr int BN = GATED ? 128 : 256;   // output columns of a tile
@@ -436,13 +438,18 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                 char *z = reinterpret_cast<char *>(e.z) + (m * P + n0) * 2;
                 if (e.z != nullptr && inside)
                     store_cols(z, z_whole, true, v);
-                with_act(e.act, [&](auto act) {
-                    if (decltype(act)::value != ACT_NONE) {
+                if constexpr (GELU) {
+                    gelu_values(v);
+                } else {
+                    with_act(e.act, [&](auto act) {
+                        constexpr int ACT = decltype(act)::value;
+                        if constexpr (ACT != ACT_NONE && (GATED || ACT != ACT_GELU)) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[i] = act_value<decltype(act)::value>(v[i]);
-                    }
-                });
+                            for (int i = 0; i < 32; ++i)
+                                v[i] = act_value<ACT>(v[i]);
+                        }
+                    });
+                }
                 if (GATED) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 16) {
@@ -509,45 +516,78 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                     tmem_st_x32(park + col, v);
                 }
             };
+            auto finish_codes = [&](int col0) {   // of 128 columns whose values wait in the park
+                tmem_wait_st();
+                const float scale = __fdiv_rn(top, 448.0f);
+                const Enc enc(scale);
 #pragma unroll 1
-            for (int col = 0; col < cols; col += 64) {
-                float v[32], w[32];
-                tmem_ld_x32(park + col, bits(v));
-                tmem_wait_ld(bits(v));
-                if (!GATED)   // under way while the first block is taken through
-                    tmem_ld_x32(park + col + 32, bits(w));
-                if (!GATED && e.res != nullptr) {
-                    if (e.r_bf16)
-                        cp_async_wait<3>();   // all but what has been asked for since
-                    else
-                        cp_async_wait<1>();
-                    __syncwarp();
-                }
-                block(v, col, 0);
-                if (GATED)
-                    tmem_ld_x32(park + col + 32, bits(w));
-                tmem_wait_ld(bits(w));
-                block(w, col + 32, 1);
-                if (!GATED) {
-                    __syncwarp();   // the residual's block is read
-                    stage_residual(col + 64 * blocks);
-                }
-                if (e.q != nullptr && col % 128 == 64) {
-                    tmem_wait_st();
-                    const float scale = __fdiv_rn(top, 448.0f);
-                    const Enc enc(scale);
-#pragma unroll 1
-                    for (int i = col - 64; i < col + 64; i += 32) {
-                        tmem_ld_x32(park + i, bits(v));
-                        tmem_wait_ld(bits(v));
-                        uint32_t o[8];
-                        enc.codes(v, o);
-                        if (inside)
-                            store32(reinterpret_cast<char *>(e.q) + m * e.N + c.n0 + i, q_whole, o);
-                    }
+                for (int i = col0; i < col0 + 128; i += 32) {
+                    float v[32];
+                    tmem_ld_x32(park + i, bits(v));
+                    tmem_wait_ld(bits(v));
+                    uint32_t o[8];
+                    enc.codes(v, o);
                     if (inside)
-                        e.scales[m * (e.N / 128) + (c.n0 + col) / 128] = scale;
-                    top = 0.0f;
+                        store32(reinterpret_cast<char *>(e.q) + m * e.N + c.n0 + i, q_whole, o);
+                }
+                if (inside)
+                    e.scales[m * (e.N / 128) + (c.n0 + col0) / 128] = scale;
+                top = 0.0f;
+            };
+            if constexpr (!GELU) {
+#pragma unroll 1
+                for (int col = 0; col < cols; col += 64) {
+                    float v[32], w[32];
+                    tmem_ld_x32(park + col, bits(v));
+                    tmem_wait_ld(bits(v));
+                    if (!GATED)   // under way while the first block is taken through
+                        tmem_ld_x32(park + col + 32, bits(w));
+                    if (!GATED && e.res != nullptr) {
+                        if (e.r_bf16)
+                            cp_async_wait<3>();   // all but what has been asked for since
+                        else
+                            cp_async_wait<1>();
+                        __syncwarp();
+                    }
+                    block(v, col, 0);
+                    if (GATED)
+                        tmem_ld_x32(park + col + 32, bits(w));
+                    tmem_wait_ld(bits(w));
+                    block(w, col + 32, 1);
+                    if (!GATED) {
+                        __syncwarp();   // the residual's block is read
+                        stage_residual(col + 64 * blocks);
+                    }
+                    if (e.q != nullptr && col % 128 == 64)
+                        finish_codes(col - 64);
+                }
+            } else {
+                // the next block's sums are under way in w while v is taken through
+                float v[32], w[32];
+                tmem_ld_x32(park, bits(w));
+                tmem_wait_ld(bits(w));
+#pragma unroll 1
+                for (int col = 0; col < cols; col += 32) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = w[i];
+                    if (col + 32 < cols)
+                        tmem_ld_x32(park + col + 32, bits(w));
+                    if (e.res != nullptr && col % 64 == 0) {
+                        if (e.r_bf16)
+                            cp_async_wait<3>();   // all but what has been asked for since
+                        else
+                            cp_async_wait<1>();
+                        __syncwarp();
+                    }
+                    block(v, col, col / 32 & 1);
+                    if (e.res != nullptr && col % 64 == 32) {
+                        __syncwarp();   // the residual's block is read
+                        stage_residual(col - 32 + 64 * blocks);
+                    }
+                    tmem_wait_ld(bits(w));
+                    if (e.q != nullptr && col % 128 == 96)
+                        finish_codes(col - 96);
                 }
             }
             // the park is read: the MMA may refill the buffer.  Two of the eight arrivals it waits for
@@ -573,10 +613,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
 
 bool gemm_act_split_ok()
 {
-    cudaFuncAttributes a, b;
-    return cudaFuncGetAttributes(&a, gemm_act_kernel<false>) == cudaSuccess &&
-           cudaFuncGetAttributes(&b, gemm_act_kernel<true>) == cudaSuccess &&
-           std::min(a.numRegs, b.numRegs) * kThreads >= kRegsNeeded;
+    const void *kernels[] = {reinterpret_cast<const void *>(gemm_act_kernel<false, false>), reinterpret_cast<const void *>(gemm_act_kernel<false, true>),
+                             reinterpret_cast<const void *>(gemm_act_kernel<true, false>)};
+    for (const void *k : kernels) {
+        cudaFuncAttributes a;
+        if (cudaFuncGetAttributes(&a, k) != cudaSuccess || a.numRegs * kThreads < kRegsNeeded)
+            return false;
+    }
+    return true;
 }
 
 // How long a launch takes, about: 0.45 us per 128 of K and 5 us per tile that a CTA does one after
@@ -588,21 +632,23 @@ int64_t gemm_act_tiles_ns(int M, int N, int K, bool gated, int num_sms)
     return (tiles + num_sms - 1) / num_sms * (450 * (K / 128) + 5000) + 3000;
 }
 
-template <bool GATED>
+template <bool GATED, bool GELU>
 static cudaError_t launch_typed(const ActParams &p, int num_sms, cudaStream_t st)
 {
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(gemm_act_kernel<GATED>), Smem<GATED>::kBytes);
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(gemm_act_kernel<GATED, GELU>), Smem<GATED>::kBytes);
     if (e != cudaSuccess)
         return e;
     const int bn = GATED ? 128 : 256;
     const int64_t tiles = (int64_t)((p.e.M + 127) / 128) * ((p.e.N + bn - 1) / bn);
-    gemm_act_kernel<GATED><<<(int)std::min<int64_t>(tiles, num_sms), kThreads, Smem<GATED>::kBytes, st>>>(p);
+    gemm_act_kernel<GATED, GELU><<<(int)std::min<int64_t>(tiles, num_sms), kThreads, Smem<GATED>::kBytes, st>>>(p);
     return cudaGetLastError();
 }
 
 cudaError_t launch_gemm_act(const ActParams &p, int num_sms, cudaStream_t st)
 {
-    return p.e.gated ? launch_typed<true>(p, num_sms, st) : launch_typed<false>(p, num_sms, st);
+    if (p.e.gated)
+        return launch_typed<true, false>(p, num_sms, st);
+    return p.e.act == ACT_GELU ? launch_typed<false, true>(p, num_sms, st) : launch_typed<false, false>(p, num_sms, st);
 }
 
 }  // namespace gemmar
