@@ -178,3 +178,22 @@ def test_values_over_the_whole_range(g, ctx, act, M):
     # 2^126, from where the fast division gives 0): off by at most 2^-126 |z|
     bound = ff.value_error(act, z.double(), exact) + 2.0 ** -24 * ref.abs() + 2.0 ** -126 * z.double().abs().clamp(min=1)
     ff.within(run(g, ctx, ops, N, act, False, bias=z)["C"], ref.expand(M, N), bound)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("M,N,K,gated", [(2500, 1920, 256, False), (2500, 1920, 256, True), (5000, 128, 128, False), (4097, 640, 640, False)])
+def test_many_rows_join_a_wider_stream(g, ctx, M, N, K, gated, act, dtype):
+    """Several tiles to a CTA, a ragged last one and an odd number of column blocks; the residual is columns of a
+    wider matrix, read alone, in place, and as one row for all."""
+    ops, rnd = operands(M, N * (2 if gated else 1), K, 12)
+    wide = rnd(M, N + 40).to(dtype)
+    view = wide[:, 8:8 + N]
+    before, beside = view.clone(), (wide[:, :8].clone(), wide[:, 8 + N:].clone())
+    got = run(g, ctx, ops, N, act, gated, ("C32", "q"), residual=view)
+    check(got, ops, act, gated, None, before)
+    g.gemm_blockscale_act(ctx, *ops, view, act=ff.ACTS.index(act), gated=gated, residual=view)
+    torch.cuda.synchronize()
+    assert torch.equal(view, got["C"].to(dtype)) and torch.equal(wide[:, :8], beside[0]) and torch.equal(wide[:, 8 + N:], beside[1])
+    row = before[7:8].expand(M, N)
+    check(run(g, ctx, ops, N, act, gated, ("C16",), residual=row), ops, act, gated, None, row)
