@@ -8,8 +8,8 @@
 // 128 of K, so each of a tile's 128 x 256 sums is read from TMEM and multiplied-added in fp32
 // once per K-block.  A K-block takes about 900 cycles, 512 of MMA, whose accumulators share TMEM's
 // bandwidth with those reads (755 in the same pipeline without them): 16384 x 7168 x 2048 to
-// bf16 in 223 us, 0.57 of the MMA's rate; with bias and residual 251 us; gated 7168 -> 2 x 2048 to
-// codes and z, 4096 rows, 112 us.  One persistent CTA per SM, 16 warps:
+// bf16 in 213 us, 0.59 of the MMA's rate; with bias and residual 247 us; gated 7168 -> 2 x 2048 to
+// codes and z, 4096 rows, 113 us.  One persistent CTA per SM, 16 warps:
 //   warp 0      TMA producer: A tile 128x128 and B rows 2 x 128 per 128-K stage
 //   warp 1      MMA issuer, 128 x 256 x 32 each into one of two TMEM buffers (two MMAs of 128
 //               columns with two buffers each, for a finer overlap, ran at 0.69 of the rate)
@@ -53,11 +53,15 @@ struct Smem {
     static constexpr int kBytes = kOffMisc + 8 + 4 * kSteps + 8 + 1024;
     static_assert(kBytes <= 232448, "shared memory budget");
 };
-// setmaxnreg: warps 0-3, promotion, finish, of 128 a thread
-constexpr int kRegsLow = 40, kRegsPromote = 176, kRegsFinish = 120;
-constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsPromote + 128 * kRegsFinish;
-static_assert(kRegsNeeded <= 65536, "register split");
-static_assert(kRegsPromote >= 128 && kRegsFinish <= 128, "raised and lowered from 128");
+// setmaxnreg: warps 0-3, promotion, finish, of 128 a thread.  Neither role of any form spills.  Promotion
+// with the eight more that an ungated finish without gelu leaves: 16384 x 7168 x 2048 213 us, without 224.
+constexpr int kRegsLow = 40;
+template <bool GATED, bool GELU> constexpr int kRegsPromote = GATED || GELU ? 176 : 184;
+template <bool GATED, bool GELU> constexpr int kRegsFinish = GATED || GELU ? 120 : 104;
+template <bool GATED, bool GELU> constexpr int kRegsNeeded = 128 * kRegsLow + 256 * kRegsPromote<GATED, GELU> + 128 * kRegsFinish<GATED, GELU>;
+static_assert(kRegsNeeded<true, false> <= 65536 && kRegsNeeded<false, true> <= 65536 && kRegsNeeded<false, false> <= 65536, "register split");
+static_assert(kRegsPromote<true, false> >= 128 && kRegsFinish<true, false> <= 128 && kRegsPromote<false, false> >= 128 && kRegsFinish<false, false> <= 128,
+              "raised and lowered from 128");
 constexpr int kGroupM = 16;      // row tiles that share their columns of B while they are in L2
 struct Tile {
     int m0, n0;
@@ -144,7 +148,7 @@ __device__ __forceinline__ bool whole32(const void *p, int64_t row_bytes)
 }
 
 // GELU: an ungated tile's activation is gelu, whose code is the longest: two copies of it, as the others have,
-// and instructions that wait for one another cost 8192 x 1920 x 1152 70 us, this form 49; the others lose 5% to it.
+// and instructions that wait for one another cost 8192 x 1920 x 1152 70 us, this form 49; the others lose 5% to one copy.
 template <bool GATED, bool GELU>
 __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_constant__ ActParams prm)
 {
@@ -275,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
             wait_teardown(final_bar, prm.status, prm.timeout_ns);
         }
     } else if (warp < 12) {
-        setmaxnreg_inc<kRegsPromote>();
+        setmaxnreg_inc<kRegsPromote<GATED, GELU>>();
         // ---------------------------------------------------- promotion
         const int q = warp & 3, h = (warp - 4) >> 2;   // lane quarter, half of the accumulator's columns
         const int row = q * 32 + lane;
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
             }
         }
     } else {
-        setmaxnreg_dec<kRegsFinish>();
+        setmaxnreg_dec<kRegsFinish<GATED, GELU>>();
         // ---------------------------------------------------- finish
         const int q = warp & 3;
         const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
@@ -611,17 +615,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
 
 }  // namespace
 
-bool gemm_act_split_ok()
+template <bool GATED, bool GELU>
+static bool split_ok()
 {
-    const void *kernels[] = {reinterpret_cast<const void *>(gemm_act_kernel<false, false>), reinterpret_cast<const void *>(gemm_act_kernel<false, true>),
-                             reinterpret_cast<const void *>(gemm_act_kernel<true, false>)};
-    for (const void *k : kernels) {
-        cudaFuncAttributes a;
-        if (cudaFuncGetAttributes(&a, k) != cudaSuccess || a.numRegs * kThreads < kRegsNeeded)
-            return false;
-    }
-    return true;
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, gemm_act_kernel<GATED, GELU>) == cudaSuccess && a.numRegs * kThreads >= kRegsNeeded<GATED, GELU>;
 }
+
+bool gemm_act_split_ok() { return split_ok<true, false>() && split_ok<false, true>() && split_ok<false, false>(); }
 
 // How long a launch takes, about: 0.45 us per 128 of K and 5 us per tile that a CTA does one after
 // another, and 3 us (measured: 31 us at one tile of K = 7168, 14.5 at 2048, 12.4 at 1152).
