@@ -8,12 +8,13 @@
 // all its threads along h, and the one that finishes last chooses, a warp per token.  More go by
 // tiles of 32 tokens and 32 experts, h cut into as many parts as fill the SMs (96 tokens, 256
 // experts, h = 7168: 9 000 cycles of FMAs an SM at best), and a second launch adds the parts and
-// chooses.  One token of 64 experts takes 4.7 us, 8 of 256 11 us, 96 of 256 18.8 us.
+// chooses, a CTA per token.  One token of 64 experts takes 5.6 us, 8 of 256 11 to 12 us, 96 of 256 19.5 us.
 //
-// The order of two experts whose scores agree to fp32's rounding would depend on how the
-// sums are split.  Such tokens are decided in 64 bits: the logits in question are summed
-// again with what their roundings lost (20 us for a pair at h = 7168, for about one token in two
-// thousand).
+// An fp32 sum of n roundings is off by n 2^-24 sum_h |x w| at most, and that sum is at most |x| |w| of
+// the rows' norms.  Norms are summed beside the logits; a token with two of its first k + 1 experts
+// nearer than such sums can tell is decided in 64 bits, by all warps of its CTA: the logits in question are
+// summed again with what their roundings lost.  At h = 7168 and 256 experts that is one token in 25 or so and
+// takes 5 to 7 us, of up to 8 tokens one after another: 96 tokens 25 to 26 us, 8 of them 15 on average.
 // Without a bias the order is the logits' own, which neither saturates nor underflows.
 #include <algorithm>
 
@@ -52,10 +53,37 @@ __device__ __forceinline__ void load8(const void *row, int h, float (&v)[8])
     }
 }
 
+// The warps' sums in pairs: three roundings
+template <typename F>
+__device__ __forceinline__ float sum8(F of)
+{
+    static_assert(kWarps == 8, "one each");
+    return ((of(0) + of(1)) + (of(2) + of(3))) + ((of(4) + of(5)) + (of(6) + of(7)));
+}
+
 __device__ __forceinline__ const void *router_row(const RouteArgs &a, int e)
 {
     return static_cast<const char *>(a.w) + (int64_t)e * a.H * (a.w_bf16 ? 2 : 4);
 }
+
+// What the choice starts from: `parts` sums [T,E] of logits to be added, then the parts' sums of squares of the tokens'
+// rows [parts,T], and of each tile of experts the largest sum [parts,tiles].
+struct Sums {
+    float *at;
+    int parts, tiles;
+    float slack;      // times both norms: what an fp32 logit may be off by
+    __device__ float *logit(const RouteArgs &a, int part, int t, int e) const { return at + ((int64_t)part * a.T + t) * a.E + e; }
+    __device__ float *x2(const RouteArgs &a, int part, int t) const { return logit(a, parts, 0, 0) + part * a.T + t; }
+    __device__ float *largest_w2(const RouteArgs &a, int i) const { return x2(a, parts, 0) + i; }
+    __device__ float *largest_w2(const RouteArgs &a, int part, int tile) const { return largest_w2(a, part * tiles + tile); }
+};
+
+int64_t sums_floats(int64_t T, int64_t E, int64_t parts, int64_t tiles) { return parts * (T * E + T + tiles); }
+
+// n roundings in a row, and 2% for second orders and the norms' own.
+inline float slack_of(int64_t n) { return 1.02f * 0x1p-24f * (float)n; }
+// Squares that fp32 loses, of a row of 65536: added to every sum of squares.
+constexpr float kLostSquares = 0x1p-110f;
 
 // A number as an unsigned one of the same order, never 0 but for a NaN.  The warp's largest is then
 // one instruction, and 0 what is not to be chosen.
@@ -66,86 +94,61 @@ __device__ __forceinline__ uint32_t key_of(float s)
 }
 __device__ __forceinline__ float score_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key); }
 
-// x[t] . w[e] by the whole warp, every product and sum with its rounding error carried along
-// (error-free sums and products by the published methods of Knuth and Dekker): about 2^-45 of the
-// terms' sizes, on the fp32 units, as those for fp64 are few.
-__device__ double logit64(const RouteArgs &a, int t, int e)
+// A thread's share of x . w, `threads` of them side by side, 8 columns at a time: every product and sum with its
+// rounding error carried along (error-free sums and products by the published methods of Knuth and Dekker), on
+// the fp32 units, as those for fp64 are few.  The errors of 56 terms are added in fp32 and their sums in
+// fp64: about 2^-44 of the terms' sizes is lost, and products below 2^-100 lose digits.
+template <bool BF>
+__device__ __forceinline__ double share64(const uint16_t *x, const void *w, int H, int thread, int threads)
 {
-    const int lane = threadIdx.x & 31;
-    const uint16_t *x = a.x + (int64_t)t * a.xs;
-    const void *w = router_row(a, e);
-    float hi = 0.0f, lo = 0.0f;
-    for (int h = lane * 8; h < a.H; h += 256) {
-        float xv[8], wv[8];
-        load8<true>(x, h, xv);
-        if (a.w_bf16)
-            load8<true>(w, h, wv);
-        else
-            load8<false>(w, h, wv);
+    constexpr int kAhead = 7;   // loads under way
+    float hi = 0.0f;
+    double lost = 0.0;
+    for (int h0 = thread * 8; h0 < H; h0 += kAhead * threads * 8) {
+        float xv[kAhead][8], wv[kAhead][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float p = __fmul_rn(xv[i], wv[i]), pe = __fmaf_rn(xv[i], wv[i], -p);
-            const float s = __fadd_rn(hi, p), b = __fsub_rn(s, hi);
-            lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(p, b)), pe));
-            hi = s;
+        for (int u = 0; u < kAhead; ++u) {
+            const int h = h0 + u * threads * 8;
+            if (h < H) {
+                load8<true>(x, h, xv[u]);
+                load8<BF>(w, h, wv[u]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    xv[u][i] = wv[u][i] = 0.0f;
+            }
         }
+        float lo = 0.0f;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float p = __fmul_rn(xv[u][i], wv[u][i]), pe = __fmaf_rn(xv[u][i], wv[u][i], -p);
+                const float s = __fadd_rn(hi, p), b = __fsub_rn(s, hi);
+                lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(p, b)), pe));
+                hi = s;
+            }
+        }
+        lost += (double)lo;
     }
-    double s = (double)hi + (double)lo;
+    return (double)hi + lost;
+}
+
+__device__ __forceinline__ double warp_sum(double s)
+{
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
         s += __shfl_xor_sync(0xffffffffu, s, d);
     return s;
 }
 
-// What orders the experts, in double: the logit, or the score with its bias.
-struct Order64 {
-    bool soft, biased;
-    double top, sum;      // of the softmax
-    __device__ double of(double logit, double bias) const
-    {
-        if (!biased)
-            return logit;
-        return (soft ? exp(logit - top) / sum : 1.0 / (1.0 + exp(-logit))) + bias;
-    }
-};
-
-// The first k in double of the experts whose fp32 order value is at least `least`, for the rare
-// token where fp32 cannot tell: lane j gets the j-th.  value: the fp32 order values, in shared
-// memory; zero: every logit of the token is exactly 0.
-// Only experts with another one twice `tol` away or nearer need it: between the others fp32 can tell.
-__device__ __noinline__ int decide64(const RouteArgs &a, int t, const float *value, float least, float tol, int k, Order64 o, bool zero)
+// One of `warps` warps' part of x[t] . w[e]
+__device__ __noinline__ double part64(const RouteArgs &a, int t, int e, int warp, int warps)
 {
-    const int lane = threadIdx.x & 31;
-    double mine = -INFINITY;   // lane j: the j-th best so far, and whose
-    int mine_e = -1, count = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-        const float f = e0 + lane < a.E ? value[e0 + lane] : -INFINITY;
-        unsigned todo = __ballot_sync(0xffffffffu, f >= least && e0 + lane < a.E);
-        while (todo) {
-            const int who = __ffs(todo) - 1, e = e0 + who;
-            todo &= todo - 1;
-            const float mine32 = __shfl_sync(0xffffffffu, f, who), near = 2.0f * (tol + (o.biased ? 0x1p-21f * fabsf(mine32) : 0.0f));
-            bool alone = true;
-            for (int i = lane; i < a.E; i += 32)
-                alone = alone && (i == e || !(fabsf(value[i] - mine32) <= near));
-            double d = mine32;
-            if (!__all_sync(0xffffffffu, alone)) {
-                const double x = zero ? 0.0 : logit64(a, t, e);
-                if (x > -INFINITY && x < INFINITY)   // an infinite logit's fp32 value is exact
-                    d = o.of(x, o.biased ? (double)__ldg(a.bias + e) : 0.0);
-            }
-            // its place behind the ones that are not smaller (equal ones have lower numbers)
-            const int place = __popc(__ballot_sync(0xffffffffu, lane < count && mine >= d));
-            const double up = __shfl_up_sync(0xffffffffu, mine, 1);
-            const int up_e = __shfl_up_sync(0xffffffffu, mine_e, 1);
-            if (lane >= place) {
-                mine = lane == place ? d : up;
-                mine_e = lane == place ? e : up_e;
-            }
-            count = min(count + 1, 32);
-        }
-    }
-    return lane < k ? mine_e : -1;
+    const uint16_t *x = a.x + (int64_t)t * a.xs;
+    const void *w = router_row(a, e);
+    const int thread = warp * 32 + (threadIdx.x & 31);
+    return warp_sum(a.w_bf16 ? share64<true>(x, w, a.H, thread, warps * 32) : share64<false>(x, w, a.H, thread, warps * 32));
 }
 
 // Weights over their sum where the scores of all chosen are too small for fp32 (a bias that takes
@@ -156,42 +159,77 @@ __device__ __noinline__ float tiny_weights(const RouteArgs &a, int t, int mine, 
     const int lane = threadIdx.x & 31;
     double logit = -INFINITY;
     for (int j = 0; j < chosen; ++j) {
-        const double x = logit64(a, t, __shfl_sync(0xffffffffu, mine, j));
+        const double x = part64(a, t, __shfl_sync(0xffffffffu, mine, j), 0, 1);
         logit = lane == j ? x : logit;
     }
     double top = logit;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
         top = fmax(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const double w = logit > -INFINITY ? exp(logit - top) : 0.0;
-    double all = w;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        all += __shfl_xor_sync(0xffffffffu, all, d);
+    const double w = logit > -INFINITY ? exp(logit - top) : 0.0, all = warp_sum(w);
     return all > 0.0 ? (float)(w / all) : 0.0f;
 }
 
-// One warp chooses token t's experts from its logits in global memory, which other CTAs wrote, in
-// `parts` to be added.  score: [2 E] in shared memory, the warp's own.  PER: experts of a lane
-// (E <= 32 PER), lane + 32 i.
+// Lane j has the j-th of `chosen` experts: their weights, and both outputs.
+__device__ __forceinline__ void finish(const RouteArgs &a, int t, int mine, int chosen, const float *score, float scale)
+{
+    const int lane = threadIdx.x & 31;
+    float w = mine >= 0 ? score[mine] * scale : 0.0f, all = w;
+    if (a.renorm) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            all += __shfl_xor_sync(0xffffffffu, all, d);
+        w = all < 0x1p-100f && chosen > 0 ? tiny_weights(a, t, mine, chosen) : w / all;
+    }
+    if (lane < a.k) {
+        a.ids[(int64_t)t * a.k + lane] = mine;
+        a.weights[(int64_t)t * a.k + lane] = mine >= 0 ? w * a.factor : 0.0f;
+    }
+}
+
+// What fp32 knows of a token's order.
+struct Choice {
+    bool close;       // two of the first k + 1 are too near to tell
+    int chosen;
+    float tol;        // how near that is, besides 2^-21 of a score with its bias
+    float cut;        // the last one's
+    float top, err;   // the largest logit, and what a logit may be off by
+    float scale;      // of the scores
+    bool zero;        // the token's row squares to nothing
+};
+
+__device__ __forceinline__ float nearness(const RouteArgs &a, const Choice &c, float s)
+{
+    return c.tol + (a.bias != nullptr ? 0x1p-21f * fabsf(s) : 0.0f);
+}
+
+// One warp chooses token t's experts from its logits' sums, which other CTAs wrote, and is done with
+// it unless the choice is close.  score: [2 E] in shared memory: scores without the bias, to be multiplied by
+// `scale`, then what orders.  PER: experts of a lane (E <= 32 PER), lane + 32 i.
 template <int PER>
-__device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *logits, int parts, float *score)
+__device__ __forceinline__ void choose(const RouteArgs &a, int t, const Sums &sums, float *score, Choice &out)
 {
     const int lane = threadIdx.x & 31;
     const bool soft = a.score == 0;
     float *order = score + a.E;
     float v[PER], bias[PER];             // logits, then scores without the bias
-    float top = -INFINITY, big = 0.0f;   // largest logit, largest size of one
+    float top = -INFINITY;               // largest logit
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int e = lane + 32 * i;
         bias[i] = e < a.E && a.bias != nullptr ? __ldg(a.bias + e) : 0.0f;
-        v[i] = e < a.E ? __ldcg(logits + (int64_t)t * a.E + e) : -INFINITY;
+        v[i] = e < a.E ? __ldcg(sums.logit(a, 0, t, e)) : -INFINITY;
     }
+    // of the router's rows the parts' largest, as if in one row
+    float w2 = 0.0f, x2 = lane < sums.parts ? __ldcg(sums.x2(a, lane, t)) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        w2 = fmaxf(w2, lane + 32 * i < sums.parts * sums.tiles ? __ldcg(sums.largest_w2(a, lane + 32 * i)) : 0.0f);
+    w2 *= (float)sums.parts;
     // many loads under way: a lane's experts of four parts
-    const float *from = logits + (int64_t)t * a.E + lane;
+    const float *from = sums.logit(a, 0, t, lane);
 #pragma unroll(PER <= 8 ? 4 : 1)
-    for (int p = 1; p < parts; ++p) {
+    for (int p = 1; p < sums.parts; ++p) {
         from += (int64_t)a.T * a.E;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
@@ -199,15 +237,14 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *l
                 v[i] += __ldcg(from + 32 * i);
     }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
+    for (int i = 0; i < PER; ++i)
         top = fmaxf(top, v[i]);          // skips NaN
-        if (fabsf(v[i]) < INFINITY)
-            big = fmaxf(big, fabsf(v[i]));
-    }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
+    for (int d = 16; d > 0; d >>= 1) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+        x2 += __shfl_xor_sync(0xffffffffu, x2, d);
+    }
+    w2 = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(w2)));
     // exponentials to be divided by their sum, or sigmoids
     const bool biased = a.bias != nullptr;
     uint32_t key[PER];
@@ -225,30 +262,38 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *l
         }
         v[i] = p;
     }
-    float scale = 1.0f;
+    Choice c;
+    c.top = top;
+    c.scale = 1.0f;
     if (soft) {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        scale = 1.0f / sum;
+        c.scale = 1.0f / sum;
     }
-    // how far fp32's rounding may move what orders: the logits' sums to 2^-20 of the largest
-    // logit (twenty times the spread of such sums), scores besides by a few units in the last place
-    float tol = 0x1p-20f * big;
+    // How near two values are that may stand in either order: each logit is off by err.  A sigmoid's slope is
+    // at most 1/4, and it is off by 2^-21 and one rounding besides.  Of a softmax's score the exponential and the
+    // sum are off by a factor of exp(err) each, and by two units in the last place an exponential (four roundings),
+    // PER + 5 additions, the quotient and the product.
+    c.err = sums.slack * sqrtf(x2 + kLostSquares) * sqrtf(w2 + kLostSquares);
+    c.tol = 2.0f * c.err;
     if (biased) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const float s = v[i] * scale + bias[i];
+            const float s = v[i] * c.scale + bias[i];
             if (lane + 32 * i < a.E) {
                 key[i] = s > -INFINITY ? key_of(s) : 0u;
                 order[lane + 32 * i] = s;
             }
         }
-        tol = tol * (soft ? scale : 0.25f) + 0x1p-21f * scale;
+        c.tol = soft ? 2.02f * c.scale * (expm1f(2.0f * c.err) + (PER + 16) * 0x1p-24f) : 0.5f * c.err + 0x1p-19f;
     }
-    bool close = false;                  // whether neighbours in the order are too close to tell
-    int mine = -1, chosen = 0;           // lane j keeps the j-th choice (k <= 16)
-    float last = INFINITY, cut = -INFINITY;
+    c.zero = x2 == 0.0f;
+    c.close = false;
+    c.chosen = 0;
+    c.cut = -INFINITY;
+    int mine = -1;                       // lane j keeps the j-th choice (k <= 16)
+    float last = INFINITY;
 #pragma unroll 1
     for (int j = 0; j <= a.k; ++j) {     // one past the last, to see how near it is
         uint32_t best = 0;
@@ -259,7 +304,7 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *l
         if (best == 0)
             break;
         const float s = score_of(best);
-        close = close || last - s <= tol + (biased ? 0x1p-21f * fabsf(s) : 0.0f);   // no two infinities
+        c.close = c.close || last - s <= nearness(a, c, s);   // no two infinities
         last = s;
         if (j == a.k)
             break;
@@ -271,60 +316,166 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *l
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             key[i] = e == lane + 32 * i ? 0u : key[i];
-        cut = s;
-        ++chosen;
+        c.cut = s;
+        ++c.chosen;
         if (lane == j)
             mine = e;
     }
     __syncwarp();
-    if (close && chosen > 0) {
-        double sum64 = 1.0;
-        if (soft && biased) {
-            sum64 = 0.0;
-            for (int e = lane; e < a.E; e += 32)
-                sum64 += score[e] >= 0.0f ? (double)score[e] : 0.0;
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1)
-                sum64 += __shfl_xor_sync(0xffffffffu, sum64, d);
-        }
-        const float near = 2.0f * (tol + (biased ? 0x1p-21f * fabsf(cut) : 0.0f));
-        mine = decide64(a, t, order, near > 0.0f ? cut - near : cut, tol, chosen, Order64{soft, biased, (double)top, sum64}, big == 0.0f);
-    }
-    float w = mine >= 0 ? score[mine] * scale : 0.0f, all = w;
-    if (a.renorm) {
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            all += __shfl_xor_sync(0xffffffffu, all, d);
-        w = all < 0x1p-100f && chosen > 0 ? tiny_weights(a, t, mine, chosen) : w / all;
-    }
-    if (lane < a.k) {
-        a.ids[(int64_t)t * a.k + lane] = mine;
-        a.weights[(int64_t)t * a.k + lane] = mine >= 0 ? w * a.factor : 0.0f;
-    }
+    c.close = c.close && c.chosen > 0;
+    if (!c.close)
+        finish(a, t, mine, c.chosen, score, c.scale);
+    if (lane == 0)
+        out = c;
 }
 
-__device__ __forceinline__ void choose_token(const RouteArgs &a, int t, const float *logits, int parts, float *score)
+__device__ __forceinline__ void choose_token(const RouteArgs &a, int t, const Sums &sums, float *score, Choice &out)
 {
     if (a.E <= 64)
-        choose<2>(a, t, logits, parts, score);
+        choose<2>(a, t, sums, score, out);
     else if (a.E <= 256)
-        choose<8>(a, t, logits, parts, score);
+        choose<8>(a, t, sums, score, out);
     else
-        choose<32>(a, t, logits, parts, score);
+        choose<32>(a, t, sums, score, out);
 }
 
-// At most kTokens tokens.  grid: experts / EB; logits fp32 [T,E]; done: zero before and after.
-template <int TB, int EB, bool BF>
-__global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a, float *logits, uint32_t *done)
+// Shared memory of the decisions in 64 bits: [E] doubles and two lists of experts.
+constexpr int kWideBytes = 16;   // an expert
+// Rounding may move a softmax's sum by this much before its exponentials are taken in 64 bits as well: E logits
+// instead of a few (96 tokens of 256 experts 0.6 ms).  Centred rows of 7168 with logits of a standard deviation below
+// 20 stay under it.
+constexpr float kSumSlack = 0x1p-8f;
+
+// An integer of the same order; both zeros have one.
+__device__ __forceinline__ int64_t key64(double v)
 {
-    __shared__ float part[kWarps][TB * EB];
+    const int64_t b = __double_as_longlong(v);
+    return b < 0 ? INT64_MIN - b : b;
+}
+
+// Decides a close choice in 64 bits, with all of the CTA's warps.  Only experts whose fp32 value is near
+// another's need it: twice the nearness away, fp32 can tell.  wide: [E] of shared memory and the lists behind it.
+template <int WARPS>
+__device__ __noinline__ void decide64(const RouteArgs &a, int t, const Choice &c, const float *score, double *wide)
+{
+    __shared__ int listed, candidates, best[32];
+    __shared__ double part[WARPS];
+    int *list = reinterpret_cast<int *>(wide + a.E), *candidate = list + a.E;
+    const float *order = score + a.E;
+    const int E = a.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool soft = a.score == 0, biased = a.bias != nullptr;
+    const bool whole = soft && biased && c.err > kSumSlack;
+    const float near = 2.0f * nearness(a, c, c.cut), least = c.cut < INFINITY ? c.cut - near : c.cut;
+    if (threadIdx.x == 0)
+        listed = candidates = 0;
+    bool zero = false;   // a padded row: its logits are all 0
+    if (c.zero) {
+        uint32_t some = 0;
+        const uint16_t *x = a.x + (int64_t)t * a.xs;
+        for (int h = threadIdx.x * 8; h < a.H; h += WARPS * 32 * 8) {
+            const uint4 r = __ldg(reinterpret_cast<const uint4 *>(x + h));
+            some |= (r.x | r.y | r.z | r.w) & 0x7FFF7FFFu;
+        }
+        zero = !__syncthreads_or(some != 0);
+    } else {
+        __syncthreads();
+    }
+    // which may be among the chosen, and which of them are near another
+    for (int e0 = warp * 32; e0 < E; e0 += WARPS * 32) {
+        const int e = e0 + lane;
+        const float f = e < E ? order[e] : NAN;
+        bool sum = whole && e < E && score[e] >= 0.0f;
+        unsigned todo = __ballot_sync(0xffffffffu, f >= least);
+        while (todo) {
+            const int who = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const float mine = __shfl_sync(0xffffffffu, f, who), reach = 2.0f * nearness(a, c, mine);
+            int others = 0;   // itself among them, unless it is infinite
+#pragma unroll 8
+            for (int i = lane; i < E; i += 32)
+                others += fabsf(order[i] - mine) <= reach ? 1 : 0;
+            others = __reduce_add_sync(0xffffffffu, others);
+            if (lane == who)
+                sum = sum || others > 1;
+        }
+        if (e < E)
+            wide[e] = zero && sum ? 0.0 : (double)f;
+        if (f >= least)
+            candidate[atomicAdd(&candidates, 1)] = e;
+        if (sum)
+            list[atomicAdd(&listed, 1)] = e;
+    }
+    __syncthreads();
+    // their logits: an expert by as many warps as there are for it, all by the same number
+    const int n = zero ? 0 : listed, each = max(1, WARPS / max(n, 1)), at_once = WARPS / each;
+    for (int i0 = 0; i0 < n; i0 += at_once) {
+        const int i = i0 + warp / each;
+        const bool has = warp / each < at_once && i < n;
+        const double l = has ? part64(a, t, list[i], warp % each, each) : 0.0;
+        if (lane == 0)
+            part[warp] = l;
+        if (each > 1)
+            __syncthreads();   // one round
+        if (has && warp % each == 0 && lane == 0) {
+            double all = l;
+            for (int w = 1; w < each; ++w)
+                all += part[warp + w];
+            wide[list[i]] = all;
+        }
+    }
+    __syncthreads();
+    // what orders those; where the logit is infinite, or the bias, fp32's value is exact
+    double sum = 0.0;
+    if (soft && biased) {
+        for (int e = lane; e < E; e += 32)
+            if (score[e] >= 0.0f)
+                sum += whole && fabs(wide[e]) < INFINITY ? exp(wide[e] - (double)c.top) : (double)score[e];
+        sum = warp_sum(sum);
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < listed; i += WARPS * 32) {
+        const int e = list[i];
+        const double l = wide[e];
+        if (!(fabsf(order[e]) < INFINITY && fabs(l) < INFINITY))
+            wide[e] = order[e];
+        else if (biased)
+            wide[e] = (soft ? exp(l - (double)c.top) / sum : 1.0 / (1.0 + exp(-l))) + (double)__ldg(a.bias + e);
+    }
+    __syncthreads();
+    // a candidate's place: the larger ones, and of equal ones those before it (as integers of the same order)
+    for (int i = threadIdx.x; i < candidates; i += WARPS * 32) {
+        const int e = candidate[i];
+        const int64_t mine = key64(wide[e]);
+        int place = 0;
+#pragma unroll 4
+        for (int j = 0; j < candidates; ++j) {
+            const int other = candidate[j];
+            const int64_t v = key64(wide[other]);
+            place += v > mine || (v == mine && other < e) ? 1 : 0;
+        }
+        if (place < c.chosen)
+            best[place] = e;
+    }
+    __syncthreads();
+    if (warp == 0)
+        finish(a, t, lane < c.chosen ? best[lane] : -1, c.chosen, score, c.scale);
+}
+
+// At most kTokens tokens.  grid: experts / EB; done: zero before and after.
+template <int TB, int EB, bool BF>
+__global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a, const Sums sums, uint32_t *done)
+{
+    constexpr int kSums = TB * EB + EB + TB;   // products, then the squares of the router's rows and of the tokens'
+    __shared__ float part[kWarps][kSums];
     extern __shared__ __align__(16) uint8_t smem[];
-    float *scores = reinterpret_cast<float *>(smem);   // [kWarps][2 E]
+    float *scores = reinterpret_cast<float *>(smem);   // [T][2 E]
     __shared__ bool chooses;
+    __shared__ Choice choice[kTokens];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e0 = blockIdx.x * EB;
     for (int t0 = 0; t0 < a.T; t0 += TB) {
-        float acc[TB * EB] = {};
+        const bool first = t0 == 0, squares = blockIdx.x == 0;   // once for each row
+        float acc[kSums] = {};
         for (int h = threadIdx.x * 8; h < a.H; h += kThreads * 8) {
             float x[TB][8];
 #pragma unroll
@@ -335,14 +486,29 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a, floa
                 float w[8];
                 load8<BF>(router_row(a, min(e0 + j, a.E - 1)), h, w);
 #pragma unroll
+                for (int i = 0; i < TB; ++i) {
+                    float eight = x[i][0] * w[0];   // by themselves: fewer roundings in a row
+#pragma unroll
+                    for (int c = 1; c < 8; ++c)
+                        eight = fmaf(x[i][c], w[c], eight);
+                    acc[i * EB + j] += eight;
+                }
+                if (first)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        acc[TB * EB + j] = fmaf(w[c], w[c], acc[TB * EB + j]);
+            }
+            if (squares)
+#pragma unroll
                 for (int i = 0; i < TB; ++i)
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
-                        acc[i * EB + j] = fmaf(x[i][c], w[c], acc[i * EB + j]);
-            }
+                        acc[TB * EB + EB + i] = fmaf(x[i][c], x[i][c], acc[TB * EB + EB + i]);
         }
 #pragma unroll
-        for (int i = 0; i < TB * EB; ++i) {
+        for (int i = 0; i < kSums; ++i) {
+            if (i >= TB * EB && !(i < TB * EB + EB ? first : squares))
+                continue;
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1)
                 acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], d);
@@ -350,25 +516,48 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a, floa
                 part[warp][i] = acc[i];
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < TB * EB; i += kThreads) {
-            float s = part[0][i];
+        if (threadIdx.x < kSums) {
+            const int i = threadIdx.x;
+            const float s = sum8([&](int w) { return part[w][i]; });
+            const int t = t0 + i / EB, e = e0 + i % EB, tx = t0 + i - TB * EB - EB;
+            if (i < TB * EB) {
+                if (t < a.T && e < a.E)
+                    __stcg(sums.logit(a, 0, t, e), s);
+            } else if (i < TB * EB + EB) {
+                if (first)
+                    part[0][i] = s;
+            } else if (squares && tx < a.T) {
+                __stcg(sums.x2(a, 0, tx), s);
+            }
+        }
+        if (first) {
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                float m = 0.0f;
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w)
-                s += part[w][i];
-            const int t = t0 + i / EB, e = e0 + i % EB;
-            if (t < a.T && e < a.E)
-                __stcg(logits + (int64_t)t * a.E + e, s);
+                for (int j = 0; j < EB; ++j)
+                    m = fmaxf(m, part[0][TB * EB + j]);   // skips NaN
+                __stcg(sums.largest_w2(a, 0, blockIdx.x), m);
+            }
         }
         __syncthreads();
     }
     if (threadIdx.x == 0) {
-        chooses = add_acq_rel(done, 1u) == gridDim.x - 1;   // then all CTAs' logits are visible
+        chooses = add_acq_rel(done, 1u) == gridDim.x - 1;   // then all CTAs' sums are visible
         if (chooses)
             *done = 0;
     }
     __syncthreads();
-    if (chooses && warp < a.T)
-        choose_token(a, warp, logits, 1, scores + warp * 2 * a.E);
+    if (!chooses)
+        return;
+    if (warp < a.T)
+        choose_token(a, warp, sums, scores + warp * 2 * a.E, choice[warp]);
+    __syncthreads();
+    for (int t = 0; t < a.T; ++t)
+        if (choice[t].close) {
+            decide64<kWarps>(a, t, choice[t], scores + t * 2 * a.E, reinterpret_cast<double *>(scores + a.T * 2 * a.E));
+            __syncthreads();
+        }
 }
 
 // ---- tiles of 32 tokens x 32 experts
@@ -400,10 +589,36 @@ __device__ __forceinline__ void fma_pair(uint64_t &c, uint64_t a, uint64_t b)
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
 }
 
-// grid: (parts of h, experts / 32, tokens / 32); out fp32 [part][T][E].  A warp computes the whole
-// tile over every eighth run of 32 columns, a lane 4 tokens x 8 experts of it.
+__device__ __forceinline__ void add_pair(uint64_t &c, uint64_t a) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(c) : "l"(a)); }
+
+__device__ __forceinline__ float sum_of(uint64_t v) { return __uint_as_float((uint32_t)v) + __uint_as_float((uint32_t)(v >> 32)); }
+
+// += the squares of 32 values at p in shared memory
 template <bool BF>
-__global__ void __launch_bounds__(kThreads, 1) route_tile_kernel(const RouteArgs a, float *out)
+__device__ __forceinline__ void add_squares(uint64_t &c, uint32_t p)
+{
+#pragma unroll
+    for (int i = 0; i < (BF ? 4 : 8); ++i) {
+        const uint4 r = ld_shared_v4(p + i * 16);
+        if (BF) {
+            uint64_t v[4];
+            widen4(make_uint2(r.x, r.y), *reinterpret_cast<uint64_t(*)[2]>(&v[0]));
+            widen4(make_uint2(r.z, r.w), *reinterpret_cast<uint64_t(*)[2]>(&v[2]));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                fma_pair(c, v[j], v[j]);
+        } else {
+            fma_pair(c, pair_of(r.x, r.y), pair_of(r.x, r.y));
+            fma_pair(c, pair_of(r.z, r.w), pair_of(r.z, r.w));
+        }
+    }
+}
+
+// grid: (parts of h, experts / 32, tokens / 32).  A warp computes the whole tile over every eighth run of
+// 32 columns, a lane 4 tokens x 8 experts of it.  The 16 products of a run are added up by themselves
+// before they join the other runs', which keeps a sum's roundings in a row few.
+template <bool BF>
+__global__ void __launch_bounds__(kThreads, 1) route_tile_kernel(const RouteArgs a, const Sums out)
 {
     using S = TileSmem<BF>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -448,8 +663,10 @@ __global__ void __launch_bounds__(kThreads, 1) route_tile_kernel(const RouteArgs
         copy(c);
     // tokens ti + 8 i, experts ei + 4 j
     const int ti = lane >> 2, ei = lane & 3;
-    uint64_t acc[4][8] = {};   // sums over the even and the odd columns
+    uint64_t total[4][8] = {};   // sums over the even and the odd columns
+    uint64_t x2 = 0, w2 = 0;     // squares of token t0 + lane and expert e0 + lane
     for (int c = 0; c < chunks; ++c) {
+        uint64_t acc[4][8] = {};
         cp_async_wait<kStages - 2>();
         __syncthreads();   // everyone's copies of chunk c are there, and chunk c - 1 is read
         copy(c + kStages - 1);
@@ -477,36 +694,67 @@ __global__ void __launch_bounds__(kThreads, 1) route_tile_kernel(const RouteArgs
                 }
             }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                add_pair(total[i][j], acc[i][j]);
+        // once for each row
+        const uint32_t st = smem_u32(smem + c % kStages * S::kStage);
+        if (blockIdx.y == 0)
+            add_squares<true>(x2, st + lane * S::kXRow + warp * 64);
+        if (blockIdx.z == 0)
+            add_squares<BF>(w2, st + kTile * S::kXRow + lane * S::kWRow + warp * (BF ? 64 : 128));
     }
     cp_async_wait<0>();
     __syncthreads();
+    __shared__ float squares[2][kWarps][32];
+    squares[0][warp][lane] = sum_of(x2);
+    squares[1][warp][lane] = sum_of(w2);
     float *sums = reinterpret_cast<float *>(smem);   // [warp][token][expert]
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            sums[(warp * kTile + ti + 8 * i) * kTile + ei + 4 * j] =
-                __uint_as_float((uint32_t)acc[i][j]) + __uint_as_float((uint32_t)(acc[i][j] >> 32));
+            sums[(warp * kTile + ti + 8 * i) * kTile + ei + 4 * j] = sum_of(total[i][j]);
     __syncthreads();
-    for (int i = threadIdx.x; i < kTile * kTile; i += kThreads) {
-        float s = sums[i];
+    if (warp < 2 && (warp == 0 ? blockIdx.y : blockIdx.z) == 0) {
+        float s = 0.0f;
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w)
-            s += sums[w * kTile * kTile + i];
+        for (int w = 0; w < kWarps; ++w)
+            s += squares[warp][w][lane];
+        if (warp == 0) {
+            if (t0 + lane < a.T)
+                __stcg(out.x2(a, blockIdx.x, t0 + lane), s);
+        } else {
+            s = fmaxf(0.0f, s);   // a NaN is no expert's
+            s = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(s)));
+            if (lane == 0)
+                __stcg(out.largest_w2(a, blockIdx.x, blockIdx.y), s);
+        }
+    }
+    for (int i = threadIdx.x; i < kTile * kTile; i += kThreads) {
+        const float s = sum8([&](int w) { return sums[w * kTile * kTile + i]; });
         const int t = t0 + i / kTile, e = e0 + i % kTile;
         if (t < a.T && e < a.E)
-            __stcg(out + ((int64_t)blockIdx.x * a.T + t) * a.E + e, s);
+            __stcg(out.logit(a, blockIdx.x, t, e), s);
     }
 }
 
-// a warp per token
-__global__ void __launch_bounds__(128) route_choose_kernel(const RouteArgs a, const float *logits, int parts)
+// a CTA per token: one warp chooses, the others help where it is close
+constexpr int kChooseWarps = 8;
+__global__ void __launch_bounds__(kChooseWarps * 32) route_choose_kernel(const RouteArgs a, const Sums sums)
 {
     extern __shared__ __align__(16) uint8_t smem[];
-    const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
+    __shared__ Choice choice;
+    float *score = reinterpret_cast<float *>(smem);
+    const int t = blockIdx.x;
     grid_wait();
-    if (t < a.T)
-        choose_token(a, t, logits, parts, reinterpret_cast<float *>(smem) + (threadIdx.x >> 5) * 2 * a.E);
+    if (threadIdx.x < 32)
+        choose_token(a, t, sums, score, choice);
+    __syncthreads();
+    if (choice.close)
+        decide64<kChooseWarps>(a, t, choice, score, reinterpret_cast<double *>(score + 2 * a.E));
 }
 
 // The number of parts that ends soonest: waves of CTAs, each as long as a part and two chunks
@@ -529,10 +777,13 @@ int tile_parts(const RouteArgs &a, int num_sms)
 template <int TB, int EB, bool BF>
 cudaError_t launch_typed(const RouteArgs &a, float *ws, uint32_t *counter, cudaStream_t st)
 {
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(route_kernel<TB, EB, BF>), kWarps * kMaxExperts * 8);
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(route_kernel<TB, EB, BF>), kMaxExperts * (kTokens * 8 + kWideBytes));
     if (e != cudaSuccess)
         return e;
-    route_kernel<TB, EB, BF><<<(a.E + EB - 1) / EB, kThreads, a.T * a.E * 8, st>>>(a, ws, counter);
+    const int ctas = (a.E + EB - 1) / EB;
+    // eight products, a thread's such sums, the shuffles and the warps
+    const Sums sums{ws, 1, ctas, slack_of(8 + (a.H + 8 * kThreads - 1) / (8 * kThreads) + 5 + 3)};
+    route_kernel<TB, EB, BF><<<ctas, kThreads, a.E * (a.T * 8 + kWideBytes), st>>>(a, sums, counter);
     return cudaGetLastError();
 }
 
@@ -542,19 +793,23 @@ cudaError_t launch_tiles(const RouteArgs &a, float *ws, int num_sms, cudaStream_
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(route_tile_kernel<BF>), TileSmem<BF>::kBytes);
     if (e != cudaSuccess)
         return e;
-    const cudaError_t c = ensure_dynamic_smem(reinterpret_cast<const void *>(route_choose_kernel), 4 * kMaxExperts * 8);
-    if (c != cudaSuccess)
-        return c;
-    const int parts = tile_parts(a, num_sms);
-    route_tile_kernel<BF><<<dim3(parts, (a.E + kTile - 1) / kTile, (a.T + kTile - 1) / kTile), kThreads, TileSmem<BF>::kBytes, st>>>(a, ws);
-    return launch(route_choose_kernel, dim3((a.T + 3) / 4), 128, (size_t)4 * a.E * 8, 1, true, st, a, static_cast<const float *>(ws), parts);
+    const int parts = tile_parts(a, num_sms), tiles = (a.E + kTile - 1) / kTile;
+    const int chunks = ((a.H + parts - 1) / parts + 8 + kChunk - 1) / kChunk;
+    // the products of a run, the runs, both halves, the warps and the parts
+    const Sums sums{ws, parts, tiles, slack_of(16 + chunks + 1 + 3 + parts)};
+    route_tile_kernel<BF><<<dim3(parts, tiles, (a.T + kTile - 1) / kTile), kThreads, TileSmem<BF>::kBytes, st>>>(a, sums);
+    return launch(route_choose_kernel, dim3(a.T), kChooseWarps * 32, (size_t)a.E * (8 + kWideBytes), 1, true, st, a, sums);
 }
 
 }  // namespace
 
 int64_t route_ws_floats(const RouteArgs &a, int num_sms)
 {
-    return (int64_t)a.T * a.E * (a.T <= kTokens ? 1 : tile_parts(a, num_sms));
+    if (a.T == 1)
+        return sums_floats(a.T, a.E, 1, a.E);
+    if (a.T <= kTokens)
+        return sums_floats(a.T, a.E, 1, (a.E + 3) / 4);
+    return sums_floats(a.T, a.E, tile_parts(a, num_sms), (a.E + kTile - 1) / kTile);
 }
 
 cudaError_t launch_route(const RouteArgs &a, float *ws, uint32_t *counter, int num_sms, cudaStream_t st)

@@ -606,13 +606,14 @@ enum { GEMMAR_SCORE_SOFTMAX = 0, GEMMAR_SCORE_SIGMOID = 1 };
  *   ids[t,:] = the k experts with the largest p + bias, in that order; of equal ones the lowest
  *   weights  = p of the chosen (without bias), over their sum where renorm, times factor
  * An expert whose p + bias is NaN or -inf is not chosen (a bias of -inf takes one out); where
- * fewer than k are left, id -1 with weight 0 fills up.  Scores are fp32; where two are too
- * near to be told apart in fp32, the order is decided in 64 bits (of a softmax with a bias over
- * the sum of the fp32 exponentials).  Without a bias it is the logits' order, also where the
- * scores saturate.
+ * fewer than k are left, id -1 with weight 0 fills up.  Scores are fp32; where the roundings of
+ * fp32 sums could change the order (by the norms of the rows, so also where large terms cancel) it
+ * is decided in 64 bits.  A softmax's scores are then over the sum of the fp32 exponentials if there
+ * is a bias, unless rounding could move that sum by 2^-8 of it.  Without a bias it is the logits' order,
+ * also where the scores saturate.
  *   x bf16 [T,H] with a row stride; w [E,H] of w_dtype, bias fp32 [E] or NULL; ids int32 [T,k];
  *   weights fp32 [T,k].  H % 8 == 0, H <= 65536, T, E and k within the limits above, k <= E.
- * Scratch: 16 T E floats at most (T E for 8 tokens and fewer).
+ * Scratch: 16 (T E + T + E / 32 + 1) floats at most (T E + T + E for 8 tokens and fewer).
  */
 int moe_route(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, const void *w, int w_dtype, const float *bias,
               int64_t T, int64_t H, int E, int k, int score, int renorm, float factor, int32_t *ids, float *weights,
