@@ -16,6 +16,7 @@
 
 #include "gemmar.h"
 #include "kernels.h"
+#include "spans.h"
 
 #define GEMMAR_API extern "C" __attribute__((visibility("default")))
 
@@ -633,42 +634,21 @@ int check_rows(const void *p, int64_t stride, int64_t cols, int elem_bytes, bool
     return GEMMAR_OK;
 }
 
-// Do two matrices of T rows share bytes?  Rows at one stride may lie between one another (columns of a
-// wider matrix); at two strides only the same start counts.  All in bytes.
-bool bytes_meet(const void *a, int64_t a_stride, int64_t a_row, const void *b, int64_t b_stride, int64_t b_row, int64_t T)
+// Do two bf16 matrices of T rows share elements?  Rows at one stride may lie between one
+// another (columns of a wider matrix); at two strides only the same start counts.
+bool rows_meet(const uint16_t *a, int64_t a_stride, int64_t a_cols, const uint16_t *b, int64_t b_stride, int64_t b_cols,
+               int64_t T)
 {
-    if (a == nullptr || b == nullptr)
-        return false;
     if (a == b)
         return true;
     if (a_stride != b_stride && T > 1)
         return false;
-    const int64_t d = (intptr_t)b - (intptr_t)a, last = (T - 1) * a_stride;
-    if (d >= last + a_row || -d >= last + b_row)
+    const int64_t d = ((intptr_t)b - (intptr_t)a) / 2, last = (T - 1) * a_stride;
+    if (d >= last + a_cols || -d >= last + b_cols)
         return false;
     const int64_t off = a_stride > 0 && T > 1 ? ((d % a_stride) + a_stride) % a_stride : d;
-    return T == 1 || a_stride == 0 || off < a_row || a_stride - off < b_row;
+    return T == 1 || a_stride == 0 || off < a_cols || a_stride - off < b_cols;
 }
-
-bool rows_meet(const uint16_t *a, int64_t a_stride, int64_t a_cols, const uint16_t *b, int64_t b_stride, int64_t b_cols,
-               int64_t T)
-{
-    return bytes_meet(a, 2 * a_stride, 2 * a_cols, b, 2 * b_stride, 2 * b_cols, T);
-}
-
-// Do T rows at a share bytes with the one row at b?
-bool rows_meet_one(const void *a, int64_t a_stride, int64_t a_row, int64_t T, const void *b, int64_t b_row)
-{
-    if (a == nullptr || b == nullptr)
-        return false;
-    const int64_t d = (intptr_t)b - (intptr_t)a;
-    if (d >= (T - 1) * a_stride + a_row || -d >= b_row)
-        return false;
-    return d < 0 || T == 1 || d % a_stride < a_row || a_stride - d % a_stride < b_row;
-}
-
-// Do n contiguous bytes at a and m at b?
-bool ranges_meet(const void *a, int64_t n, const void *b, int64_t m) { return bytes_meet(a, n, n, b, m, m, 1); }
 
 int norm_shape(int64_t M, int64_t N)
 {
@@ -837,9 +817,6 @@ bool known_act(int act) { return act >= GEMMAR_ACT_NONE && act <= GEMMAR_ACT_GEL
 
 int elem_bytes(int dtype) { return dtype == GEMMAR_DTYPE_BF16 ? 2 : 4; }
 
-// of a contiguous matrix, or of one row that stands for all (stride 0)
-int64_t row_bytes(int64_t stride, int64_t M, int64_t N, int64_t elem) { return (stride == 0 ? 1 : M) * N * elem; }
-
 }  // namespace
 
 GEMMAR_API int gemm_blockscale_act(gemmar_ctx *ctx, const uint8_t *A, const float *sa, const uint8_t *B, const float *sb,
@@ -867,14 +844,10 @@ GEMMAR_API int gemm_blockscale_act(gemmar_ctx *ctx, const uint8_t *A, const floa
     // an output over what is still being read; residual may be C itself
     const int64_t P = gated ? 2 * N : N;
     const int rb = elem_bytes(r_dtype), cb = elem_bytes(c_dtype);
-    if ((C != residual && bytes_meet(C, c_stride * cb, N * cb, residual, r_stride * rb, N * rb, M)) ||
-        (r_stride == 0 && C != residual && rows_meet_one(C, c_stride * cb, N * cb, M, residual, N * rb)) ||
-        ranges_meet(q, M * N, A, M * K) || ranges_meet(q, M * N, B, P * K) || ranges_meet(z, 2 * M * P, A, M * K) ||
-        ranges_meet(z, 2 * M * P, B, P * K) || ranges_meet(q, M * N, z, 2 * M * P) ||
-        (c_stride == N && (ranges_meet(C, M * N * cb, A, M * K) || ranges_meet(C, M * N * cb, B, P * K) ||
-                           ranges_meet(C, M * N * cb, q, M * N) || ranges_meet(C, M * N * cb, z, 2 * M * P))) ||
-        (residual && (r_stride == N || r_stride == 0) &&
-         (ranges_meet(residual, row_bytes(r_stride, M, N, rb), q, M * N) || ranges_meet(residual, row_bytes(r_stride, M, N, rb), z, 2 * M * P))))
+    const Span c = span_rows(C, N * cb, c_stride * cb, M), res = span_rows(residual, N * rb, r_stride * rb, M);
+    const Span qs = span(q, M * N), ss = span(scales, M * N / 32), zs = span(z, 2 * M * P);
+    if (any_meet({c, qs, ss, zs}, {span(A, M * K), span(sa, M * K / 32), span(B, P * K), span(sb, P / 128 * (K / 128) * 4), span(bias, 4 * P)}) ||
+        any_meet({qs, ss, zs}, {res}) || (C != residual && meet(c, res)))
         return GEMMAR_ERR_ARG;
     if (!load_encode())
         return GEMMAR_ERR_CUDA;
@@ -915,12 +888,11 @@ GEMMAR_API int gemm_blockscale_act_bwd(gemmar_ctx *ctx, const void *dout, int d_
         return rc;
     if (!aligned16(z) || !aligned16(dz) || !aligned16(dbias) || !aligned16(q) || !aligned16(scales))
         return GEMMAR_ERR_ALIGN;
+    // dz may be z itself, or dout
     const int64_t P = gated ? 2 * N : N, db = elem_bytes(d_dtype);
-    if ((dz && dz != z && ranges_meet(dz, 2 * M * P, z, 2 * M * P)) ||
-        ((d_stride == N || d_stride == 0) &&
-         ((dz && dz != dout && ranges_meet(dz, 2 * M * P, dout, row_bytes(d_stride, M, N, db))) ||
-          ranges_meet(q, M * P, dout, row_bytes(d_stride, M, N, db)))) ||
-        ranges_meet(q, M * P, z, 2 * M * P) || ranges_meet(q, M * P, dz, 2 * M * P))
+    const Span dzs = span(dz, 2 * M * P), bs = span(dbias, 4 * P), qs = span(q, M * P), ss = span(scales, M * P / 32);
+    const Span zs = span(z, 2 * M * P), ds = span_rows(dout, N * db, d_stride * db, M);
+    if (any_meet({dzs, bs, qs, ss}, {}) || any_meet({bs, qs, ss}, {zs, ds}) || (dz != z && meet(dzs, zs)) || (dz != dout && meet(dzs, ds)))
         return GEMMAR_ERR_ARG;
     if (dbias && act_bwd_ws_floats(M, (int)N, gated, ctx->num_sms) > ctx->W_floats)
         return GEMMAR_ERR_WORKSPACE;
@@ -945,6 +917,9 @@ GEMMAR_API int moe_route(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, c
         return rc;
     if (!aligned16(w) || !aligned16(bias) || !aligned16(ids) || !aligned16(weights))
         return GEMMAR_ERR_ALIGN;
+    if (any_meet({span(ids, 4 * T * k), span(weights, 4 * T * k)},
+                 {span_rows(x, 2 * H, 2 * x_stride, T), span(w, (int64_t)E * H * elem_bytes(w_dtype)), span(bias, 4 * (int64_t)E)}))
+        return GEMMAR_ERR_ARG;
     const RouteArgs a{x, x_stride, w, w_dtype == GEMMAR_DTYPE_BF16, bias, (int)T, (int)H, E, k, score, renorm != 0, factor,
                       ids, weights};
     if (route_ws_floats(a, ctx->num_sms) > ctx->W_floats)
@@ -972,9 +947,11 @@ GEMMAR_API int moe_apply(gemmar_ctx *ctx, const uint8_t *xq, const float *xs, co
     if (!aligned16(xq) || !aligned16(xs) || !aligned16(ids) || !aligned16(weights) || !aligned16(place) ||
         !aligned16(w13) || !aligned16(s13) || !aligned16(w2) || !aligned16(s2))
         return GEMMAR_ERR_ALIGN;
-    if ((y != out && rows_meet(out, out_stride, H, y, y_stride, H, T)) ||
-        (y != out && y_stride == 0 && rows_meet_one(out, 2 * out_stride, 2 * H, T, y, 2 * H)) ||
-        (out_stride == H && (ranges_meet(out, 2 * T * H, xq, T * H) || ranges_meet(out, 2 * T * H, ids, 4 * T * k))))
+    const Span o = span_rows(out, 2 * H, 2 * out_stride, T);
+    const int64_t w_bytes = E * H * I, s_bytes = w_bytes / (128 * 128) * 4;   // of w2; of w13 twice
+    if (any_meet({o}, {span(xq, T * H), span(xs, T * H / 32), span(ids, 4 * T * k), span(weights, 4 * T * k), span(place, 4 * places),
+                       span(w13, 2 * w_bytes), span(s13, 2 * s_bytes), span(w2, w_bytes), span(s2, s_bytes)}) ||
+        (y != out && meet(o, span_rows(y, 2 * H, 2 * y_stride, T))))
         return GEMMAR_ERR_ARG;
     const MoeArgs a{xq, xs, ids, place, (int)(place ? places : 0), weights, w13, w2, s13, s2, (int)T, (int)H, (int)I, E, k,
                     act, y, y_stride, out, out_stride};

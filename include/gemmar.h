@@ -542,7 +542,8 @@ int lora_apply_bwd(gemmar_ctx *ctx, const uint16_t *x, int64_t x_stride, const u
  * activation behind them, or the experts' layer.  Weights are e4m3 codes with 128x128
  * scales as in gemm_blockscale_fp8, activations e4m3 codes with 1x128 scales as
  * norm_gate_residual and quant_blockscale_e4m3 write them.  Strides, alignment, workspace
- * and stream order as for the operators above.
+ * and stream order as for the operators above.  An output may be an input itself where that is
+ * said; otherwise outputs share no byte with the inputs or with one another (else GEMMAR_ERR_ARG).
  */
 
 /* Activations: none, max(z, 0), z / (1 + e^-z), z Phi(z), and the latter's tanh form
@@ -563,8 +564,7 @@ enum { GEMMAR_ACT_NONE = 0, GEMMAR_ACT_RELU = 1, GEMMAR_ACT_SILU = 2, GEMMAR_ACT
  *   bias fp32 [N or 2N]; residual [M,N] of r_dtype with a row stride (0: one row for all);
  *   C [M,N] of c_dtype with a row stride; z bf16 [M, N or 2N].  C or q may be NULL (not both),
  *   z NULL leaves it out; q and scales go together.  residual may be C itself, at the same
- *   type and stride; otherwise outputs lie apart from the inputs and from each other (GEMMAR_ERR_ARG
- *   where contiguous ones, or C and residual, do not).
+ *   type and stride.
  * N % 128 == 0, K % 128 == 0, N (2N where gated) and K <= 65536, M <= 2^24.
  */
 int gemm_blockscale_act(gemmar_ctx *ctx, const uint8_t *A, const float *sa, const uint8_t *B, const float *sb,
