@@ -456,8 +456,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 if (ok)
                     mbar_arrive(grid_bar + b);
             }
-            // the last CTA past the last barrier leaves the counters as the next call expects them
-            if (ok && atomicAdd(prm.counters + 1, 1u) == gridDim.x - 1) {
+            // the last CTA that is done with the barriers, whether it passed them or gave up, leaves the counters as the
+            // next call expects them
+            if (add_acq_rel(prm.counters + 1, 1u) == gridDim.x - 1) {
                 prm.counters[0] = 0;
                 prm.counters[1] = 0;
             }
