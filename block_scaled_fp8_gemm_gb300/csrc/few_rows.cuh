@@ -3,6 +3,8 @@
 // promotion warps keep one weight row of one tile per thread, for all columns.
 #pragma once
 
+#include <atomic>
+
 #include "kernels.h"
 
 namespace gemmar {
@@ -14,11 +16,15 @@ constexpr int kRegsLow = 56;     // warps 0-3 after setmaxnreg.dec
 constexpr int kRegsHigh = 224;   // promotion warps after setmaxnreg.inc
 constexpr uint32_t kAbortGraceNs = 200000;   // let copies in flight land before an aborting CTA exits
 
-// The kernel was built with registers enough for that split (setmaxnreg would wait forever).
-inline bool few_rows_split_ok(const void *kernel, int low = kRegsLow, int high = kRegsHigh)
+// The kernel was built with registers enough for that split (setmaxnreg would wait forever).  known: that
+// it was; a query that failed is made again by the next call.
+inline bool few_rows_split_ok(std::atomic<bool> &known, const void *kernel, int low = kRegsLow, int high = kRegsHigh)
 {
-    cudaFuncAttributes f;
-    return cudaFuncGetAttributes(&f, kernel) == cudaSuccess && f.numRegs * kThreads >= 128 * low + kEpiThreads * high;
+    if (!known) {
+        cudaFuncAttributes f;
+        known = cudaFuncGetAttributes(&f, kernel) == cudaSuccess && f.numRegs * kThreads >= 128 * low + kEpiThreads * high;
+    }
+    return known;
 }
 
 // acc[j] += (sum of column j) * (weight scale * token scale j) for 8 columns

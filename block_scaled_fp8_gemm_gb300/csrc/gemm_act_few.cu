@@ -18,6 +18,7 @@
 #include "e4m3_encode.cuh"
 #include "epilogue.cuh"
 #include "few_rows.cuh"
+#include "per_device.h"
 
 namespace gemmar {
 using namespace ptx;
@@ -318,20 +319,28 @@ cudaLaunchConfig_t config(int splits, cudaLaunchAttribute *attrs)
 }
 
 template <class C, bool GATED>
-Room measure_room()
+bool measure_room(Room &r)
 {
-    Room r{};
-    if (ensure_dynamic_smem(reinterpret_cast<const void *>(gemm_act_few_kernel<C, GATED>), C::kSmemBytes) != cudaSuccess)
-        return r;
-    for (int s = 1; s <= kMaxSplits; ++s) {
+    r = Room{};
+    bool ok = ensure_dynamic_smem(reinterpret_cast<const void *>(gemm_act_few_kernel<C, GATED>), C::kSmemBytes) == cudaSuccess;
+    for (int s = 1; s <= kMaxSplits && ok; ++s) {
         cudaLaunchAttribute attrs[1];
         const cudaLaunchConfig_t cfg = config<C, GATED>(s, attrs);
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, gemm_act_few_kernel<C, GATED>, &cfg) != cudaSuccess)
-            n = 0;
-        r.clusters[s] = n;
+        ok = cudaOccupancyMaxActiveClusters(&r.clusters[s], gemm_act_few_kernel<C, GATED>, &cfg) == cudaSuccess;
     }
-    return r;
+    if (!ok)
+        cudaGetLastError();   // the call goes on without this kernel
+    return ok;
+}
+
+// The current device's; none where it cannot be told.
+template <class C, bool GATED>
+Room room_here()
+{
+    static PerDevice<Room> rooms;
+    Room r;
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && rooms.get(dev, r, measure_room<C, GATED>) ? r : Room{};
 }
 
 template <bool GATED>
@@ -348,7 +357,7 @@ struct Plan {
 template <class C, bool GATED>
 Plan plan(int M, int N, int K)
 {
-    static const Room room = measure_room<C, GATED>();
+    const Room room = room_here<C, GATED>();
     const int KB = K / 128, rows = std::min(M, C::NT) * (GATED ? 1 : 2);
     const int64_t clusters = (int64_t)tile_pairs<GATED>(N) * ((M + C::NT - 1) / C::NT);
     Plan best{1, INT64_MAX};
@@ -370,8 +379,8 @@ cudaError_t launch_typed(const ActParams &p, cudaStream_t st)
     const cudaError_t e = ensure_dynamic_smem(kernel, C::kSmemBytes);
     if (e != cudaSuccess)
         return e;
-    static const bool split_ok = few_rows_split_ok(kernel, C::kLow, C::kHigh);
-    if (!split_ok)
+    static std::atomic<bool> split_ok{false};
+    if (!few_rows_split_ok(split_ok, kernel, C::kLow, C::kHigh))
         return cudaErrorInvalidConfiguration;
     const int splits = plan<C, GATED>(p.e.M, p.e.N, p.e.K).splits;
     cudaLaunchAttribute attrs[1];

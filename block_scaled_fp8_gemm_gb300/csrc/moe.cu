@@ -816,8 +816,8 @@ template <class C>
 cudaError_t launch_typed(const MoeParams &p, int num_sms, cudaStream_t st)
 {
     const void *kernel = reinterpret_cast<const void *>(moe_kernel<C>);
-    static const bool split_ok = few_rows_split_ok(kernel);
-    if (!split_ok)
+    static std::atomic<bool> split_ok{false};
+    if (!few_rows_split_ok(split_ok, kernel))
         return cudaErrorInvalidConfiguration;
     const cudaError_t e = ensure_dynamic_smem(kernel, C::kSmemBytes);
     if (e != cudaSuccess)
