@@ -225,8 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_act_kernel(const __grid_cons
                     }
                 }
             }
-            if (*abort_flag)
-                drain_loads(full, kStages, issued, prm.timeout_ns);
+            drain_loads(full, kStages, issued, prm.timeout_ns);
         } else if (warp == 1 && lane == 0) {
             // ------------------------------------------------ MMA issuer
             constexpr uint32_t idesc = idesc_f8_e4m3(128, 256);

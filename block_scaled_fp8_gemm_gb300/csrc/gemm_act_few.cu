@@ -133,8 +133,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) gemm_act_few_kernel(const 
                 tma_load_2d(w + kTileBytes, &prm.tmB, full + stage, kb * 128, r1);
                 tma_load_2d(w + 2 * kTileBytes, &prm.tmA, full + stage, kb * 128, m0);
             }
-            if (*abort_flag)
-                drain_loads(full, C::kStages, issued, prm.timeout_ns);
+            drain_loads(full, C::kStages, issued, prm.timeout_ns);
         } else if (warp == 1 && lane == 0) {
             // ------------------------------------------------ MMA issuer
             constexpr uint32_t idesc = idesc_f8_e4m3(128, C::NT);

@@ -139,10 +139,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     }
 }
 
-// A CTA that is giving up lets the loads it has issued (`issued` so far, one phase of full[i % stages]
-// each) land before its shared memory is released.
+// The least that a CTA waits for its own copies and MMAs, however short the limit of its waits is: they
+// write to what it is about to release, and land within some microseconds.
+constexpr uint64_t kOwnWorkNs = 200000;
+
+__device__ __forceinline__ uint64_t own_work_limit(uint64_t timeout_ns) { return timeout_ns > kOwnWorkNs ? timeout_ns : kOwnWorkNs; }
+
+// A producer's last wait: the loads it has issued (`issued` in all, one phase of full[i % stages] each) have landed
+// before its shared memory is released, also where another role gives up without them.
 __device__ __forceinline__ void drain_loads(uint64_t *full, int stages, int issued, uint64_t timeout_ns)
 {
+    timeout_ns = own_work_limit(timeout_ns);
     for (int j = issued > stages ? issued - stages : 0; j < issued; ++j) {
         const uint64_t t0 = globaltimer();
         while (!mbar_try_wait(full + j % stages, (uint32_t)((j / stages) & 1)) && globaltimer() - t0 < timeout_ns) {
@@ -153,6 +160,7 @@ __device__ __forceinline__ void drain_loads(uint64_t *full, int stages, int issu
 // The MMA warp's last wait: everything it committed has completed before TMEM is released.
 __device__ __forceinline__ void wait_teardown(uint64_t *bar, DevStatus *st, uint64_t timeout_ns)
 {
+    timeout_ns = own_work_limit(timeout_ns);
     const uint64_t t0 = globaltimer();
     while (!mbar_try_wait(bar, 0)) {
         if (globaltimer() - t0 > timeout_ns) {

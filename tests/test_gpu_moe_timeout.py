@@ -36,9 +36,8 @@ def test_the_call_after_one_that_gave_up(g):
         torch.cuda.synchronize()
         for _ in range(2):
             assert torch.equal(apply(g, hurried, s, ids, weights), want)
-    code, site = g.gemmar_status(hurried)
-    assert code == g.GEMMAR_ERR_TIMEOUT and site == 11      # a barrier of the grid
-    with pytest.raises(g.GemmarError) as e:                 # disabled from here on
+    assert g.gemmar_status(hurried)[0] == g.GEMMAR_ERR_TIMEOUT
+    with pytest.raises(g.GemmarError) as e:   # disabled from here on
         g.moe_apply(hurried, *big)
     assert e.value.code == g.GEMMAR_ERR_DISABLED
     hurried.close()
