@@ -1,8 +1,9 @@
 // activation.cuh -- the activations of the feed-forward layers and their slopes, in fp32.
 //
 // Each is written as z times a factor in [0, 1]: its tail stays accurate where 1 + erf or
-// 1 + tanh would cancel, until it falls below 2^-126 and is 0 (silu: z < -87).  z enters that product no lower than -FLT_MAX and the factor's slope within
-// +-1e6 (where it has long vanished), so that no infinity meets a zero; a NaN stays one.
+// 1 + tanh would cancel, until it falls below 2^-126 and is 0 (silu: z < -87, gelu: -13, its tanh form: -10).
+// z enters that product no lower than -FLT_MAX and the factor's slope within +-1e6 (where it has long
+// vanished), so that no infinity meets a zero; a NaN stays one.
 #pragma once
 
 #include <cstdint>

@@ -8,7 +8,7 @@
 // 128 of K, so each of a tile's 128 x 256 sums is read from TMEM and multiplied-added in fp32
 // once per K-block.  A K-block takes about 900 cycles, 512 of MMA, whose accumulators share TMEM's
 // bandwidth with those reads (755 in the same pipeline without them): 16384 x 7168 x 2048 to
-// bf16 in 213 us, 0.59 of the MMA's rate; with bias and residual 247 us; gated 7168 -> 2 x 2048 to
+// bf16 in 215 us, 0.59 of the MMA's rate; with bias and residual 250 us; gated 7168 -> 2 x 2048 to
 // codes and z, 4096 rows, 113 us.  One persistent CTA per SM, 16 warps:
 //   warp 0      TMA producer: A tile 128x128 and B rows 2 x 128 per 128-K stage
 //   warp 1      MMA issuer, 128 x 256 x 32 each into one of two TMEM buffers (two MMAs of 128

@@ -556,10 +556,12 @@ enum { GEMMAR_ACT_NONE = 0, GEMMAR_ACT_RELU = 1, GEMMAR_ACT_SILU = 2, GEMMAR_ACT
  *   out = residual + act(z)                                  (residual NULL: 0)
  *   gated: B holds 2N rows, z = [z_g, z_u] of N columns each,
  *   out = residual + act(z_g) * z_u
- * The product accumulates as gemm_blockscale_fp8; everything after it is fp32 and each
- * output is rounded once, from the fp32 value: out as C (bf16 or fp32), and/or as e4m3 codes
+ * The product's sums per 128 of K are promoted by their scales and added in fp32, as in
+ * gemm_blockscale_fp8; in which parts and order depends on M, N, K, gated and the GPU, so a row's last
+ * bits (and a code at a rounding boundary) may differ between calls of different sizes.  Everything
+ * after the product is fp32 and each output is rounded once, from the fp32 value: out as C (bf16 or fp32), and/or as e4m3 codes
  * q with scales [M, N/128] by the rule of quant_blockscale_e4m3 (the A operand of the next
- * product); z as bf16 for the backward pass.  Rows are independent.
+ * product); z as bf16 for the backward pass.  No row's values enter another's.
  *   A e4m3 [M,K], sa fp32 [M,K/128]; B e4m3 [N,K] or [2N,K], sb fp32 [N/128 or 2N/128, K/128];
  *   bias fp32 [N or 2N]; residual [M,N] of r_dtype with a row stride (0: one row for all);
  *   C [M,N] of c_dtype with a row stride; z bf16 [M, N or 2N].  C or q may be NULL (not both),
